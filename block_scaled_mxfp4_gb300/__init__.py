@@ -29,6 +29,12 @@ __all__ = [
     "mxfp8_gemm_prepacked_workspace_size", "mxfp8_quantize", "mxfp8_gemm_host",
     "mxfp8_gemm_host_arena_size", "nvfp4_gemm", "nvfp4_gemm_workspace_size",
     "MXFP8_E4M3", "MXFP8_E5M2", "MXFP6_E2M3", "MXFP6_E3M2", "MXFP4_E2M1_PADDED",
+    "mxfp4_moe_route", "mxfp4_moe_route_workspace_size", "mxfp4_group_scale_size",
+    "mxfp4_group_quantize", "mxfp8_group_quantize", "mxfp4_grouped_gemm", "mxfp8_grouped_gemm",
+    "mxfp4_grouped_swiglu", "mxfp8_grouped_swiglu", "mxfp4_grouped_workspace_size",
+    "mxfp4_moe_combine", "mxfp4_moe_ffn", "mxfp4_moe_ffn_workspace_size",
+    "MXFP4_LOGITS_BF16", "MXFP4_LOGITS_FP32", "MXFP4_GATE_TOPK", "MXFP4_GATE_ALL",
+    "MXFP4_GATE_SIGMOID", "relaid_expert_scales", "moe_block",
     "gemm", "Plan",
 ]
 
@@ -40,6 +46,8 @@ _LIB_NAME = "libmxfp4_gb300.so"
 MXFP4_OK = 0
 MXFP4_FLAG_B_STATIC = 1
 MXFP8_E4M3, MXFP8_E5M2, MXFP6_E2M3, MXFP6_E3M2, MXFP4_E2M1_PADDED = 0, 1, 3, 4, 5
+MXFP4_LOGITS_BF16, MXFP4_LOGITS_FP32 = 0, 1
+MXFP4_GATE_TOPK, MXFP4_GATE_ALL, MXFP4_GATE_SIGMOID = 0, 1, 2
 STATUS_NAMES = {0: "MXFP4_OK", -1: "MXFP4_ERR_INVALID_ARG", -2: "MXFP4_ERR_UNSUPPORTED_SHAPE",
                 -3: "MXFP4_ERR_MISALIGNED", -4: "MXFP4_ERR_WORKSPACE", -5: "MXFP4_ERR_CUDA",
                 -6: "MXFP4_ERR_TIMEOUT", -7: "MXFP4_ERR_ARCH"}
@@ -114,6 +122,29 @@ def lib() -> ctypes.CDLL:
             "mxfp8_gemm_host": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, f32, f32, i32, i32, i32,
                                       i32, vp, sz, vp]),
             "mxfp8_gemm_host_arena_size": (sz, [i32, i32, i32, i32, i32]),
+            "mxfp4_moe_route": (i32, [vp, vp, vp, vp, vp, vp, i64, i32, vp, i32, i32, i32, i32, f32,
+                                      vp, sz, vp]),
+            "mxfp4_moe_route_workspace_size": (sz, [i32, i32]),
+            "mxfp4_group_scale_size": (sz, [i32, i32, i32]),
+            "mxfp4_group_quantize": (i32, [vp, i64, vp, vp, i64, i32, i32, vp, vp, i32, vp, i32, i32,
+                                           vp]),
+            "mxfp8_group_quantize": (i32, [vp, i64, vp, vp, i64, i32, i32, vp, vp, i32, vp, i32, i32,
+                                           i32, vp]),
+            "mxfp4_grouped_gemm": (i32, [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, i32, i32, i32,
+                                         i32, f32, vp, sz, vp]),
+            "mxfp8_grouped_gemm": (i32, [vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, i32, i32, i32,
+                                         i32, i32, i32, f32, vp, sz, vp]),
+            "mxfp4_grouped_swiglu": (i32, [vp, i64, vp, vp, i64, vp, vp, i64, i64, vp, vp, i32, i32,
+                                           i32, i32, f32, vp, sz, vp]),
+            "mxfp8_grouped_swiglu": (i32, [vp, i64, vp, vp, i64, vp, vp, i64, i64, vp, vp, i32, i32,
+                                           i32, i32, i32, i32, i32, f32, vp, sz, vp]),
+            "mxfp4_grouped_workspace_size": (sz, [i32, i32, i32, i32]),
+            "mxfp4_moe_combine": (i32, [vp, i64, vp, i64, vp, i64, i32, vp, vp, i32, vp, i64, vp, vp,
+                                        f32, f32, f32, i32, i32, vp]),
+            "mxfp4_moe_ffn": (i32, [vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, i32, i32, i32, i32,
+                                    i32, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp, f32, f32, f32,
+                                    vp, sz, vp]),
+            "mxfp4_moe_ffn_workspace_size": (sz, [i32, i32, i32, i32, i32]),
             "mxfp4_device_status": (i32, [ctypes.POINTER(ctypes.c_int), i32]),
             "mxfp4_wait_timeout_probe": (i32, [ctypes.c_longlong, vp]),
             "mxfp4_set_wait_limit": (None, [ctypes.c_longlong]),
@@ -333,6 +364,148 @@ def mxfp4_strerror(status) -> str:
 
 def mxfp4_version() -> int:
     return lib().mxfp4_version()
+
+
+def mxfp4_moe_route_workspace_size(T, E) -> int:
+    return lib().mxfp4_moe_route_workspace_size(T, E)
+
+
+def mxfp4_group_scale_size(rows, groups, K) -> int:
+    return lib().mxfp4_group_scale_size(rows, groups, K)
+
+
+def mxfp4_grouped_workspace_size(rows, groups, N, K) -> int:
+    return lib().mxfp4_grouped_workspace_size(rows, groups, N, K)
+
+
+def mxfp4_moe_ffn_workspace_size(T, E, k, K, F) -> int:
+    return lib().mxfp4_moe_ffn_workspace_size(T, E, k, K, F)
+
+
+def mxfp4_moe_route(ids, gates, offsets, row_token, slot_row, logits, ldl, logits_type, token_mask,
+                    T, E, k, gate_mode, gate_scale, workspace, workspace_bytes, stream=None):
+    """The k largest logits per token, their gates, and the rows' grouping by expert."""
+    return _check(lib().mxfp4_moe_route(_p(ids), _p(gates), _p(offsets), _p(row_token),
+                                        _p(slot_row), _p(logits), ldl, logits_type,
+                                        _p(token_mask), T, E, k, gate_mode, gate_scale,
+                                        _p(workspace), workspace_bytes, _stream(stream)),
+                  "mxfp4_moe_route")
+
+
+def mxfp4_group_quantize(Q, ldq, S, X, ldx, T, K, slot_row, ids, k, offsets, groups, rows,
+                         stream=None):
+    """bf16 rows -> packed E2M1 rows at their places in the grouping, grouped scales."""
+    return _check(lib().mxfp4_group_quantize(_p(Q), ldq, _p(S), _p(X), ldx, T, K, _p(slot_row),
+                                             _p(ids), k, _p(offsets), groups, rows,
+                                             _stream(stream)), "mxfp4_group_quantize")
+
+
+def mxfp8_group_quantize(Q, ldq, S, X, ldx, T, K, slot_row, ids, k, offsets, groups, rows, fmt,
+                         stream=None):
+    """mxfp4_group_quantize into E4M3 / E5M2 codes, one per byte."""
+    return _check(lib().mxfp8_group_quantize(_p(Q), ldq, _p(S), _p(X), ldx, T, K, _p(slot_row),
+                                             _p(ids), k, _p(offsets), groups, rows, fmt,
+                                             _stream(stream)), "mxfp8_group_quantize")
+
+
+def mxfp4_grouped_gemm(D, ldd, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, N, K,
+                       alpha, workspace, workspace_bytes, stream=None):
+    """D[r] = alpha * A[r] . B[e]^T for every row r of group e (bf16 out)."""
+    return _check(lib().mxfp4_grouped_gemm(_p(D), ldd, _p(A), lda, _p(SA), _p(B), ldb, stride_b,
+                                           _p(SB), _p(offsets), groups, rows, N, K, alpha,
+                                           _p(workspace), workspace_bytes, _stream(stream)),
+                  "mxfp4_grouped_gemm")
+
+
+def mxfp8_grouped_gemm(D, ldd, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, N, K,
+                       fmt_a, fmt_b, alpha, workspace, workspace_bytes, stream=None):
+    """mxfp4_grouped_gemm on the byte formats of mxfp8_gemm."""
+    return _check(lib().mxfp8_grouped_gemm(_p(D), ldd, _p(A), lda, _p(SA), _p(B), ldb, stride_b,
+                                           _p(SB), _p(offsets), groups, rows, N, K, fmt_a, fmt_b,
+                                           alpha, _p(workspace), workspace_bytes,
+                                           _stream(stream)), "mxfp8_grouped_gemm")
+
+
+def mxfp4_grouped_swiglu(H, ldh, SH, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, F, K,
+                         alpha, workspace, workspace_bytes, stream=None):
+    """H = quantise(silu(A . Bgate^T) * (A . Bup^T)) per group, packed E2M1."""
+    return _check(lib().mxfp4_grouped_swiglu(_p(H), ldh, _p(SH), _p(A), lda, _p(SA), _p(B), ldb,
+                                             stride_b, _p(SB), _p(offsets), groups, rows, F, K,
+                                             alpha, _p(workspace), workspace_bytes,
+                                             _stream(stream)), "mxfp4_grouped_swiglu")
+
+
+def mxfp8_grouped_swiglu(H, ldh, SH, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, F, K,
+                         fmt_a, fmt_b, fmt_h, alpha, workspace, workspace_bytes, stream=None):
+    """mxfp4_grouped_swiglu on byte formats, into E4M3 / E5M2 codes."""
+    return _check(lib().mxfp8_grouped_swiglu(_p(H), ldh, _p(SH), _p(A), lda, _p(SA), _p(B), ldb,
+                                             stride_b, _p(SB), _p(offsets), groups, rows, F, K,
+                                             fmt_a, fmt_b, fmt_h, alpha, _p(workspace),
+                                             workspace_bytes, _stream(stream)),
+                  "mxfp8_grouped_swiglu")
+
+
+def mxfp4_moe_combine(H, ldh, Nrm, ldn, Y, ldy, rows, slot_row, gates, k, resid, ldr, w_post,
+                      w_pre, res_scale, out_scale, eps, T, N, stream=None):
+    """Gated sum of a token's rows, its norm, the residual stream and the next block's norm."""
+    return _check(lib().mxfp4_moe_combine(_p(H), ldh, _p(Nrm), ldn, _p(Y), ldy, rows, _p(slot_row),
+                                          _p(gates), k, _p(resid), ldr, _p(w_post), _p(w_pre),
+                                          res_scale, out_scale, eps, T, N, _stream(stream)),
+                  "mxfp4_moe_combine")
+
+
+def mxfp4_moe_ffn(H, ldh, Nrm, ldn, X, ldx, ids, gates, offsets, slot_row, T, E, k, K, F, B1, ldb1,
+                  SB1, B2, ldb2, SB2, resid, ldr, w_post, w_pre, res_scale, out_scale, eps,
+                  workspace, workspace_bytes, stream=None):
+    """A routed feed-forward block on MXFP4 weights: quantise, both products, join."""
+    return _check(lib().mxfp4_moe_ffn(_p(H), ldh, _p(Nrm), ldn, _p(X), ldx, _p(ids), _p(gates),
+                                      _p(offsets), _p(slot_row), T, E, k, K, F, _p(B1), ldb1,
+                                      _p(SB1), _p(B2), ldb2, _p(SB2), _p(resid), ldr, _p(w_post),
+                                      _p(w_pre), res_scale, out_scale, eps, _p(workspace),
+                                      workspace_bytes, _stream(stream)), "mxfp4_moe_ffn")
+
+
+def relaid_expert_scales(S, K, stream=None):
+    """Row-major weight scales [..., rows, K / 32] -> one relaid buffer per
+    matrix [..., mxfp4_scale_relayout_size(rows, K)], laid out once for the
+    grouped products."""
+    import torch
+    rows = S.shape[-2]
+    flat = S.reshape(-1, rows, K // 32).contiguous()
+    size = mxfp4_scale_relayout_size(rows, K)
+    out = torch.empty((flat.shape[0], size), dtype=torch.uint8, device=S.device)
+    for i in range(flat.shape[0]):
+        mxfp4_scale_relayout(out[i], flat[i], rows, K, K // 32, stream)
+    return out.reshape(*S.shape[:-2], size)
+
+
+def moe_block(x, logits, resid, w1, s1, w2, s2, k, w_pre=None, w_post=None, token_mask=None,
+              gate_mode=MXFP4_GATE_TOPK, res_scale=1.0, out_scale=1.0, eps=1e-6, stream=None):
+    """A mixture-of-experts block on MXFP4 weights, from the router's logits on.
+
+    x bf16 [T, K] (the block's normed input), logits bf16 / fp32 [T, E], resid
+    bf16 [T, K], w1 uint8 [E, 2, F, K / 2], w2 uint8 [E, K, F / 2], s1 and s2
+    from relaid_expert_scales.  Returns (h, n): the residual stream after the
+    block and its norm, bf16 [T, K].
+    """
+    import torch
+    T, K = x.shape
+    E, F = w1.shape[0], w1.shape[2]
+    i32 = dict(dtype=torch.int32, device=x.device)
+    ids, slot_row = torch.empty((T, k), **i32), torch.empty((T, k), **i32)
+    offsets, row_token = torch.empty(E + 1, **i32), torch.empty(T * k, **i32)
+    gates = torch.empty((T, k), dtype=torch.float32, device=x.device)
+    h = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
+    n = torch.empty_like(h)
+    need = max(mxfp4_moe_route_workspace_size(T, E), mxfp4_moe_ffn_workspace_size(T, E, k, K, F))
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+    kind = MXFP4_LOGITS_FP32 if logits.dtype == torch.float32 else MXFP4_LOGITS_BF16
+    mxfp4_moe_route(ids, gates, offsets, row_token, slot_row, logits, logits.stride(0), kind,
+                    token_mask, T, E, k, gate_mode, 1.0, ws, ws.numel(), stream)
+    mxfp4_moe_ffn(h, K, n, K, x, x.stride(0), ids, gates, offsets, slot_row, T, E, k, K, F, w1, K,
+                  s1, w2, F, s2, resid, resid.stride(0), w_post, w_pre, float(res_scale),
+                  float(out_scale), float(eps), ws, ws.numel(), stream)
+    return h, n
 
 
 def gemm(A, B, SA, SB, alpha=1.0, beta=0.0, C=None, split_k=0, out=None, workspace=None,

@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/mxfp4_gemm.h"
+#include "expert.h"
 #include "internal.h"
 
 using namespace mxfp4;
@@ -499,6 +500,23 @@ int run_gemm(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A, in
 }
 
 }  // namespace
+
+// The expert-layer entry points (expert_api.cu) share these.
+namespace mxfp4 {
+
+int check_current_device(int *sms)
+{
+    *sms = device_sms_or_default();
+    return check_device();
+}
+
+long long current_wait_limit() { return g_wait_limit.load(); }
+
+uint32_t next_call_epoch() { return next_epoch(); }
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode_fn() { return tensor_map_encoder(); }
+
+}  // namespace mxfp4
 
 extern "C" {
 
@@ -1137,7 +1155,12 @@ int mxfp4_device_status(int *status, int reset)
     int st = check_device();
     if (st != MXFP4_OK)
         return st;
-    return read_device_status(status, reset) == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
+    int grouped = 0;
+    if (read_device_status(status, reset) != cudaSuccess || read_grouped_status(&grouped, reset) != cudaSuccess)
+        return MXFP4_ERR_CUDA;
+    if (*status == MXFP4_OK)
+        *status = grouped;
+    return MXFP4_OK;
 }
 
 int mxfp4_wait_timeout_probe(long long limit_cycles, void *stream)

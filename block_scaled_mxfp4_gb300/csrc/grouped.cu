@@ -1,0 +1,617 @@
+// Products grouped by expert with ragged sizes, on CTA pairs (tcgen05
+// cta_group::2, block-scaled FP4 or byte formats):
+//
+//   plain  D[r, n] = alpha * sum_k A[r, k] B[e, n, k]             (bf16)
+//   gated  h[r, f] = silu(alpha * g) * (alpha * u), g and u the products with
+//          the gate and the up rows of B[e], quantised in 1x32 blocks along f
+//          to the operand form the next product takes
+//
+// for every row r of group e, offsets[e] <= r < offsets[e + 1].
+//
+// A cluster of two CTAs computes a tile of 256 rows (of one group) x 256
+// accumulator columns, as one M = 256, N = 256 MMA: CTA `rank` holds rows
+// 128 rank .. +127 of the tile and half of B's rows in its shared memory and
+// its 128 rows of the fp32 accumulator in its tensor memory.  Plain tiles take
+// 256 columns of D.  A gated tile takes 128 columns f: accumulator columns
+// 128 h + [0, 64) are the gate products of f0 + 64 h + [0, 64) and
+// 128 h + [64, 128) the up products of the same f, so one thread of the
+// epilogue finds g and u of 64 consecutive f in its own tensor-memory lane:
+// activation, block maxima and rounding need no exchange between threads.
+// The rows of one group are the M side although decoding leaves most of the
+// 256 empty: a stage's MMAs take 512 tensor cycles whatever the rows, less
+// than the ~700 cycles that its 32 KB of weights take to stream from HBM.
+//
+// The grid is persistent: pair i takes tiles i, i + pairs, ... of a list that
+// every CTA derives from `offsets` (prefix sums of the groups' row tiles in
+// shared memory), row tiles fastest, so tiles that run together share weight
+// panels in L2.  Empty groups have no tile and their weights are not read.
+//
+// Roles per CTA (512 threads): warps 4, 6, 7 load A rows, B rows and the scale
+// atoms by TMA (a thread waits out each copy it issues, hence one thread per
+// stream); warps 12-15 move each stage's scale lines into tensor memory; warp 5
+// of the leading CTA issues the MMAs; warps 0-3 and 8-11 are the epilogue, for
+// accumulator columns [0, 128) and [128, 256).  A rows come from a 2-D map, so a
+// tile may start at any row; rows past the group's end are loaded and computed
+// but not stored, and what their scales hold reaches only their own row of the
+// accumulator.  A CTA of which no row belongs to the group loads none.
+// The atoms of A follow the grouped scale layout (expert.h).  MMAs that start
+// beyond K are not issued, so scale bytes past K / 32 rounded up to the MMA's
+// own are never used.
+#include <atomic>
+#include <cuda_bf16.h>
+
+#include "expert.h"
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace mxfp4 {
+
+namespace {
+
+__device__ int g_status = 0;
+
+__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z,
+                                            int w, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "l"(policy)
+        : "memory");
+}
+
+// Byte formats: K = 32 per instruction, one E8M0 scale per row (scale_vec::1X),
+// issued by one elected lane of a converged warp.
+__device__ __forceinline__ void mma_mxf8_pair_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                    uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&v);
+}
+
+// BYTES8: byte formats, 128 K and one scale atom per stage and 128-row block;
+// otherwise packed E2M1, 256 K and two atoms.
+template <bool BYTES8>
+struct GroupedCfg {
+    static constexpr int STAGES = 6;
+    static constexpr int G = BYTES8 ? 1 : 2;
+    static constexpr int A_BYTES = 128 * 128;
+    static constexpr int B_BYTES = 128 * 128;
+    static constexpr int SFA_BYTES = G * kSfAtomBytes;
+    static constexpr int SFB_BYTES = 2 * G * kSfAtomBytes;
+    static constexpr int STAGE_BYTES = (A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES + 1023) / 1024 * 1024;
+    static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+    static constexpr int BAR_BYTES = 512;
+    static constexpr int TABLE_BYTES = 2 * (kMaxGroups + 1) * 4;   // offsets and row-tile prefix sums
+    static constexpr int SMEM_BYTES = RING_BYTES + BAR_BYTES + TABLE_BYTES + 1024;
+    static constexpr int SF_COLS_A = 4 * G;
+    static constexpr int SF_COLS_B = 8 * G;
+    static constexpr int SF_COLS = SF_COLS_A + SF_COLS_B;
+    static constexpr int ACC_COLS = 256;
+    static constexpr int TMEM_COLS = 512;
+    static constexpr int THREADS = 512;
+    static constexpr int K_STAGE = BYTES8 ? 128 : 256;
+    static constexpr int K_MMA = BYTES8 ? 32 : 64;
+    static_assert(ACC_COLS + STAGES * SF_COLS <= TMEM_COLS, "tensor memory budget");
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
+};
+
+// The tile list: groups' offsets and row-tile prefix sums in shared memory.
+struct TileTable {
+    const int *off;     // [groups + 1], clamped to [0, rows]
+    const int *base;    // [groups + 1]: row tiles before the group
+    int groups, nt;
+
+    __device__ int tiles() const { return base[groups] * nt; }
+};
+
+struct Tile {
+    int e;              // group
+    int row0;           // first row of the tile
+    int end;            // end of the group's rows
+    int sfa;            // 128-row scale block of row0
+    int q;              // column tile
+};
+
+__device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
+{
+    // The last group whose first tile is not after i (empty groups share their
+    // successor's base and are passed over).
+    const int rt = i / t.nt;
+    int lo = 0, hi = t.groups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.base[mid] <= rt)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    Tile r;
+    const int mt = t.base[lo + 1] - t.base[lo];
+    const int local = i - t.base[lo] * t.nt;
+    const int p = local % mt;
+    r.e = lo;
+    r.q = local / mt;
+    r.row0 = t.off[lo] + p * 256;
+    r.end = t.off[lo + 1];
+    r.sfa = static_cast<int>(group_sf_block(t.off[lo], lo)) + 2 * p;
+    return r;
+}
+
+// Fill the tables: thread t takes groups 2t and 2t + 1 of up to 1024.
+__device__ __forceinline__ void build_tables(const GroupedArgs &a, int *off, int *base)
+{
+    __shared__ int warp_sum[16];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    int o[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const int e = 2 * t + i;
+        o[i] = e <= a.groups ? min(max(a.offsets[e], 0), a.rows) : 0;
+    }
+    int c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        c[i] = 2 * t + i < a.groups ? (max(o[i + 1] - o[i], 0) + 255) / 256 : 0;
+    int sum = c[0] + c[1];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d)
+            sum += v;
+    }
+    if (lane == 31)
+        warp_sum[warp] = sum;
+    __syncthreads();
+    int before = sum - c[0] - c[1];
+    for (int w = 0; w < warp; ++w)
+        before += warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int e = 2 * t + i;
+        if (e <= a.groups) {
+            off[e] = o[i];
+            base[e] = before;
+            before += c[i];
+        }
+    }
+    if (2 * t + 2 == a.groups) {       // the entry past this thread's pair
+        off[a.groups] = o[2];
+        base[a.groups] = before;
+    }
+}
+
+// OUT: -1 plain bf16, else static_cast<int>(QuantFmt) of the gated form.
+template <bool BYTES8, int OUT>
+__global__ void __launch_bounds__(512, 1)
+    grouped_pair(const __grid_constant__ GroupedArgs a, const __grid_constant__ GroupedMaps maps)
+{
+    using Cf = GroupedCfg<BYTES8>;
+    constexpr int G = Cf::G;
+    constexpr bool GATED = OUT >= 0;
+    constexpr int STAGES = Cf::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_addr(smem_raw);
+    uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cf::RING_BYTES);
+    uint64_t *empty = full + STAGES;
+    uint64_t *sf_ready = empty + STAGES;            // the leader's are used
+    uint64_t *acc_full = sf_ready + STAGES;
+    uint64_t *acc_empty = acc_full + 1;             // the leader's is used
+    uint64_t *drain = acc_empty + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *tab_off = reinterpret_cast<int *>(smem + Cf::RING_BYTES + Cf::BAR_BYTES);
+    int *tab_base = tab_off + kMaxGroups + 1;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank() & 1u;
+    const bool leader = rank == 0;
+    const int pair = blockIdx.x / 2;
+    const int pairs = gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 3);          // this CTA's three producers
+            mbar_init(&empty[s], 1);         // the pair's MMA commit
+            mbar_init(&sf_ready[s], 8);      // the scale writers of both CTAs
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 16);            // the epilogue warps of both CTAs
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 5) {
+        tmem_alloc_pair(tmem_slot, Cf::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    if (warp == 4 && lane == 0) {
+        prefetch_tensormap(&maps.A);
+        prefetch_tensormap(&maps.SA);
+        prefetch_tensormap(&maps.B);
+        prefetch_tensormap(&maps.SB);
+    }
+    // The offsets may come from the work before this grid, like everything else.
+    pdl_wait_prerequisites();
+    build_tables(a, tab_off, tab_base);
+    tc_fence_before();
+    cluster_sync();                          // barriers of both CTAs initialised
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const TileTable table{tab_off, tab_base, a.groups, a.nt};
+    const int tiles = table.tiles();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+
+    if (warp == 4 || warp == 6 || warp == 7) {
+        // ------------------------------------------------------ producers --
+        if (lane == 0) {
+            const int role = warp == 4 ? 0 : warp - 5;   // 0: A, 1: B, 2: scales
+            const uint64_t pol = l2_policy_evict_last();
+            int stage = 0;
+            uint32_t phase = 0;
+            int issued = 0;
+            bool stop = false;
+            for (int t = pair; t < tiles && !stop; t += pairs) {
+                const Tile tl = tile_at(table, t);
+                const int arow = tl.row0 + static_cast<int>(rank) * 128;
+                const bool rows_here = arow < tl.end;
+                const uint32_t unit = role == 0   ? (rows_here ? Cf::A_BYTES : 0)
+                                      : role == 1 ? Cf::B_BYTES
+                                                  : Cf::SFB_BYTES + (rows_here ? Cf::SFA_BYTES : 0);
+                for (int kt = 0; kt < a.kt; ++kt) {
+                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_limit, &g_status)) {
+                        stop = true;
+                        break;
+                    }
+                    uint8_t *st = smem + stage * Cf::STAGE_BYTES;
+                    uint8_t *sf = st + Cf::A_BYTES + Cf::B_BYTES;
+                    mbar_arrive_expect_tx(&full[stage], unit);
+                    if (role == 0) {
+                        if (rows_here)
+                            tma_load_2d(st, &maps.A, &full[stage], kt * 128, arow, pol);
+                    } else if (role == 1) {
+                        // Plain: 128 rows of B.  Gated: 64 gate rows and the
+                        // same 64 up rows (the map's third dimension).
+                        const int n = GATED ? tl.q * 128 + static_cast<int>(rank) * 64
+                                            : tl.q * 256 + static_cast<int>(rank) * 128;
+                        tma_load_4d(st + Cf::A_BYTES, &maps.B, &full[stage], kt * 128, n, 0, tl.e, pol);
+                    } else {
+                        if (rows_here)
+                            tma_load_3d(sf, &maps.SA, &full[stage], 0, G * kt, tl.sfa + static_cast<int>(rank), pol);
+                        // Plain: two 128-row blocks of the expert.  Gated: the
+                        // block of the gate rows and the block of the up rows.
+                        tma_load_4d(sf + Cf::SFA_BYTES, &maps.SB, &full[stage], 0, G * kt,
+                                    GATED ? tl.q : 2 * tl.q, GATED ? 2 * tl.e : tl.e, pol);
+                    }
+                    ++issued;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (*abort_flag) {
+                // Let the copies already issued land before the CTA exits.
+                for (int i = max(0, issued - STAGES); i < issued; ++i)
+                    mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1u, a.wait_limit);
+            }
+        }
+    } else if (warp >= 12) {
+        // -------------------------------------------- scale writers --
+        // Line `lane` of an atom: rows lane, lane + 32, lane + 64, lane + 96 of
+        // its 128-row block, a word of four scales each; the four warps write
+        // the four lane quarters' replicas.
+        const int quarter = warp & 3;
+        const uint32_t t_q = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + Cf::ACC_COLS;
+        const uint32_t lead_ready = map_to_rank(smem_addr(&sf_ready[0]), 0);
+        const int my_tiles = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
+        const int total = my_tiles * a.kt;
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int i = 0; i < total; ++i) {
+            bool ok = mbar_wait(&full[stage], phase, abort_flag, a.wait_limit, &g_status);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            const uint8_t *sf = smem + stage * Cf::STAGE_BYTES + Cf::A_BYTES + Cf::B_BYTES;
+            uint32_t wa[4 * G], wb[8 * G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(sf + g * kSfAtomBytes + 16 * lane);
+                const uint4 x = *reinterpret_cast<const uint4 *>(sf + Cf::SFA_BYTES + g * kSfAtomBytes + 16 * lane);
+                const uint4 y =
+                    *reinterpret_cast<const uint4 *>(sf + Cf::SFA_BYTES + (G + g) * kSfAtomBytes + 16 * lane);
+                wa[4 * g] = v.x;
+                wa[4 * g + 1] = v.y;
+                wa[4 * g + 2] = v.z;
+                wa[4 * g + 3] = v.w;
+                // Word j of block b of atom g -> column 8 g + 4 b + j.  Plain:
+                // blocks x, y.  Gated: the tile's first 128 rows are gate rows
+                // 0-63 and up rows 0-63 (words 0, 1 of either block).
+                uint32_t *w = wb + 8 * g;
+                w[0] = x.x;
+                w[1] = x.y;
+                w[2] = GATED ? y.x : x.z;
+                w[3] = GATED ? y.y : x.w;
+                w[4] = GATED ? x.z : y.x;
+                w[5] = GATED ? x.w : y.y;
+                w[6] = y.z;
+                w[7] = y.w;
+            }
+            const uint32_t slot = t_q + stage * Cf::SF_COLS;
+            if constexpr (G == 2) {
+                tmem_st_32x32b_x8(slot, wa);
+                tmem_st_32x32b_x16(slot + Cf::SF_COLS_A, wb);
+            } else {
+                tmem_st_32x32b_x4(slot, wa);
+                tmem_st_32x32b_x8(slot + Cf::SF_COLS_A, wb);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader)
+                    mbar_arrive(&sf_ready[stage]);
+                else
+                    mbar_arrive_cluster_relaxed(lead_ready + static_cast<uint32_t>(stage * sizeof(uint64_t)));
+            }
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (warp == 5) {
+        // ------------------------------------------------ MMA (leader) --
+        if (leader) {
+            const uint32_t idesc = BYTES8 ? a.idesc8 : idesc_mxf4(256, 256);
+            int stage = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool stop = false;
+            for (int t = pair; t < tiles && !stop; t += pairs) {
+                if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, a.wait_limit, &g_status))
+                    break;
+                tc_fence_after();
+                for (int kt = 0; kt < a.kt; ++kt) {
+                    // sf_ready completes after the scale writers of both CTAs
+                    // saw the stage's bytes land.
+                    if (!mbar_wait(&sf_ready[stage], phase, abort_flag, a.wait_limit, &g_status)) {
+                        stop = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sfa = tmem + Cf::ACC_COLS + stage * Cf::SF_COLS;
+                    const uint32_t sfb = sfa + Cf::SF_COLS_A;
+                    const uint32_t st = smem_addr(smem + stage * Cf::STAGE_BYTES);
+                    const uint64_t adesc = sdesc_kmajor_sw128(st);
+                    const uint64_t bdesc = sdesc_kmajor_sw128(st + Cf::A_BYTES);
+                    const int left = a.K - kt * Cf::K_STAGE;      // K elements of this stage
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j * Cf::K_MMA >= left)
+                            break;
+                        const uint32_t acc = (kt > 0 || j > 0) ? 1u : 0u;
+                        if constexpr (BYTES8) {
+                            mma_mxf8_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_sf_ids(idesc, j, j), sfa, sfb,
+                                                acc);
+                        } else {
+                            const uint32_t id = (j & 1) * 2;
+                            mma_mxf4_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_sf_ids(idesc, id, id),
+                                                sfa + (j >> 1) * 4, sfb + (j >> 1) * 8, acc);
+                        }
+                    }
+                    mma_commit_pair_elect(&empty[stage], static_cast<uint16_t>(3u));
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!stop)
+                    mma_commit_pair_elect(acc_full, static_cast<uint16_t>(3u));
+                acc_phase ^= 1u;
+            }
+            if (*abort_flag) {
+                mma_commit_pair_elect(drain, static_cast<uint16_t>(1u));
+                mbar_wait_drain(drain, 0, a.wait_limit);
+            }
+        }
+    } else {
+        // ------------------------------------------------------ epilogue --
+        const int quarter = warp & 3;
+        const int half = warp >> 3;
+        const int row = static_cast<int>(rank) * 128 + quarter * 32 + lane;
+        const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
+        const uint32_t lead_empty = map_to_rank(smem_addr(acc_empty), 0);
+        uint32_t acc_phase = 0;
+        for (int t = pair; t < tiles; t += pairs) {
+            const Tile tl = tile_at(table, t);
+            bool ok = mbar_wait(acc_full, acc_phase, abort_flag, a.wait_limit, &g_status);
+            if (!__all_sync(0xffffffffu, ok))
+                break;
+            acc_phase ^= 1u;
+            tc_fence_after();
+            const int r = tl.row0 + row;
+            const bool mine = r < tl.end;
+            const bool any = __any_sync(0xffffffffu, mine);
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+                uint32_t x[32], y[32];
+                __syncwarp();
+                if (any) {
+                    // Plain: columns 64 c + [0, 64).  Gated: gate and up columns 32 c + [0, 32).
+                    tmem_ld_32x32b_x32(t_lane + (GATED ? 32 * c : 64 * c), x);
+                    tmem_ld_32x32b_x32(t_lane + (GATED ? 64 + 32 * c : 64 * c + 32), y);
+                    tmem_ld_wait(x, y);
+                }
+                if (c == 1) {
+                    // The accumulator's cells are read (tcgen05.wait::ld has
+                    // returned): the next tile's MMAs may start.
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (leader)
+                            mbar_arrive(acc_empty);
+                        else
+                            mbar_arrive_cluster_relaxed(lead_empty);
+                    }
+                }
+                if (!mine)
+                    continue;
+                if constexpr (!GATED) {
+                    const int n0 = tl.q * 256 + half * 128 + 64 * c;
+                    if (n0 >= a.N)
+                        continue;
+                    uint16_t *d = a.D + static_cast<int64_t>(r) * a.ldd + n0;
+                    uint32_t out[32];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        out[j] = bf16x2(a.alpha * __uint_as_float(x[2 * j]), a.alpha * __uint_as_float(x[2 * j + 1]));
+                        out[16 + j] = bf16x2(a.alpha * __uint_as_float(y[2 * j]), a.alpha * __uint_as_float(y[2 * j + 1]));
+                    }
+                    if (a.vec32_ok && n0 + 64 <= a.N) {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 8)
+                            st_global_v8(d + 2 * j, out[j], out[j + 1], out[j + 2], out[j + 3], out[j + 4], out[j + 5],
+                                         out[j + 6], out[j + 7]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            if (a.vec_ok && n0 + 2 * j + 8 <= a.N) {
+                                *reinterpret_cast<uint4 *>(d + 2 * j) =
+                                    make_uint4(out[j], out[j + 1], out[j + 2], out[j + 3]);
+                            } else {
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    if (n0 + 2 * j + i < a.N)
+                                        d[2 * j + i] = static_cast<uint16_t>(out[j + i / 2] >> (16 * (i & 1)));
+                            }
+                        }
+                    }
+                } else {
+                    constexpr QuantFmt Q = static_cast<QuantFmt>(OUT);
+                    constexpr int W = QuantTraits<Q>::kWords;
+                    const int f0 = tl.q * 128 + half * 64 + 32 * c;
+                    uint8_t *s = a.SH + static_cast<int64_t>(tl.sfa + row / 128) *
+                                            (sf_groups(a.N) * kSfAtomBytes) + sf_byte(row & 127, f0 / 32);
+                    if (f0 >= a.N) {
+                        // The odd block's partner in the same MMA of the next
+                        // product: any finite scale serves its zero codes.
+                        if (c == 1 && f0 - 32 < a.N)
+                            *s = 0x7F;
+                        continue;
+                    }
+                    float h[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const float g = a.alpha * __uint_as_float(x[i]);
+                        const float u = a.alpha * __uint_as_float(y[i]);
+                        h[i] = __fdividef(g, 1.0f + __expf(-g)) * u;
+                    }
+                    uint32_t out[W];
+                    const uint32_t code = quantize_block<Q>(h, out);
+                    uint4 *q = reinterpret_cast<uint4 *>(a.H + static_cast<int64_t>(r) * a.ldh +
+                                                         (Q == QuantFmt::kE2M1 ? f0 / 2 : f0));
+#pragma unroll
+                    for (int w = 0; w < W; w += 4)
+                        q[w / 4] = make_uint4(out[w], out[w + 1], out[w + 2], out[w + 3]);
+                    *s = static_cast<uint8_t>(code);
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();            // no CTA leaves while its peer may still signal it
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, Cf::TMEM_COLS);
+    }
+}
+
+template <bool BYTES8, int OUT>
+cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t stream)
+{
+    using Cf = GroupedCfg<BYTES8>;
+    auto kern = grouped_pair<BYTES8, OUT>;
+    static std::atomic<int> max_clusters[64];   // per device; 0 = not yet queried
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(Cf::THREADS);
+    cfg.dynamicSmemBytes = Cf::SMEM_BYTES;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int limit = dev < 64 ? max_clusters[dev].load() : 0;
+    if (limit == 0) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES);
+        if (e != cudaSuccess)
+            return e;
+        // Persistent: every cluster must be resident at once.
+        cfg.gridDim = dim3(2);
+        e = cudaOccupancyMaxActiveClusters(&limit, kern, &cfg);
+        if (e != cudaSuccess)
+            return e;
+        if (limit <= 0)
+            return cudaErrorInvalidConfiguration;
+        if (dev < 64)
+            max_clusters[dev] = limit;
+    }
+    // The host does not know the offsets: at most this many tiles.
+    const int64_t row_tiles = static_cast<int64_t>(a.rows) / 256 + (a.groups < a.rows ? a.groups : a.rows);
+    const int64_t most = row_tiles * a.nt;
+    const int pairs = most < limit ? static_cast<int>(most) : limit;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a, m);
+}
+
+}  // namespace
+
+size_t grouped_workspace_bytes(int, int, int, int, bool, int) { return 0; }
+
+cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, int,
+                           cudaStream_t stream)
+{
+    switch (out) {
+    case -1: return bytes8 ? launch_one<true, -1>(a, m, stream) : launch_one<false, -1>(a, m, stream);
+    case 0: return bytes8 ? cudaErrorInvalidValue : launch_one<false, 0>(a, m, stream);
+    case 1: return bytes8 ? launch_one<true, 1>(a, m, stream) : cudaErrorInvalidValue;
+    case 2: return bytes8 ? launch_one<true, 2>(a, m, stream) : cudaErrorInvalidValue;
+    default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t read_grouped_status(int *status, int reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_status, sizeof(int));
+    if (e != cudaSuccess || !reset)
+        return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
+}
+
+}  // namespace mxfp4

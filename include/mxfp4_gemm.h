@@ -421,6 +421,172 @@ int mxfp4_quantize(void *Q, int64_t ldq, void *S, int64_t lds, const void *X, in
 int mxfp8_quantize(void *Q, int64_t ldq, void *S, int64_t lds, const void *X, int64_t ldx,
                    int rows, int K, int fmt, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Expert layers: routing, products grouped by expert, the gated join.
+ *
+ * Rows.  Every token t takes up to k experts; each (token, slot) is one row,
+ * and the rows are sorted by expert, tokens ascending within one: group e
+ * holds rows offsets[e] .. offsets[e + 1] - 1.  offsets (int32 [groups + 1],
+ * device memory) is the only description of the groups that the grouped
+ * entry points take, so no size travels to the host; groups may be empty, and
+ * the total offsets[groups] may be below `rows`, the capacity of the row
+ * arrays: rows past it are neither read nor written.  Offsets must ascend
+ * from 0; out of that order they give unspecified results, but no access
+ * outside the arrays.
+ *
+ * Grouped scale layout.  The scales of a grouped operand are kept in the
+ * 512-byte atoms of mxfp4_scale_relayout, group e's rows starting a 128-row
+ * block of their own: row offsets[e] + i is row i % 128 of block
+ * offsets[e] / 128 + e + i / 128 (integer divisions), a block being
+ * 2 * ceil(K / 256) atoms.  mxfp4_group_scale_size gives the bytes.  Bytes of
+ * rows and K blocks that do not exist need no value, except that a last odd
+ * 32-block of a row has a finite one beside it (the writers put 0x7F there).
+ *
+ * Weights.  B holds `groups` matrices [N, K], expert e's at e * stride_b
+ * elements, with scales relaid per matrix by mxfp4_scale_relayout and stored
+ * one after another, each mxfp4_scale_relayout_size(N, K) bytes.  The gated
+ * form's matrices are [2][F, K]: F gate rows, then F up rows, each half relaid
+ * by itself (2 * groups buffers).
+ *
+ * These entry points follow the conventions at the top of this file (caller's
+ * memory and stream, arguments checked before anything is enqueued, capture
+ * into graphs).  groups <= 1024, k <= 16.  Weights of experts without rows
+ * are not read.
+ * ------------------------------------------------------------------------ */
+
+enum { MXFP4_LOGITS_BF16 = 0, MXFP4_LOGITS_FP32 = 1 };
+/* Gates: softmax over the picked experts, softmax over all of them, or the
+ * sigmoid of each logit; gate_scale multiplies the result. */
+enum { MXFP4_GATE_TOPK = 0, MXFP4_GATE_ALL = 1, MXFP4_GATE_SIGMOID = 2 };
+
+/*
+ * Routing: the k largest logits of each token, their gates, and the rows'
+ * grouping by expert.
+ *   logits      bf16 or fp32 [T, ldl] (logits_type), ldl >= E
+ *   token_mask  uint8 [T] or NULL: 0 leaves the token without experts
+ *   ids         int32 [T, k]: experts by descending logit, the lower index
+ *               first among equal ones; -1 where the token has no more
+ *   gates       fp32 [T, k], 0 where ids is -1
+ *   offsets     int32 [E + 1]
+ *   row_token   int32 [T * k]: the token of each row, -1 past the last row
+ *   slot_row    int32 [T, k]: the row of each slot, -1 where ids is -1
+ * A logit of -inf or NaN is never picked (a token may be left with fewer than
+ * k experts, or none), and counts for nothing in a softmax.  Results do not
+ * depend on the order in which blocks run.  T >= 0, 1 <= k <= min(E, 16).
+ * workspace: mxfp4_moe_route_workspace_size(T, E) bytes (0 for few tokens),
+ * 256-byte aligned, contents arbitrary.
+ */
+int mxfp4_moe_route(int *ids, float *gates, int *offsets, int *row_token, int *slot_row,
+                    const void *logits, int64_t ldl, int logits_type, const void *token_mask,
+                    int T, int E, int k, int gate_mode, float gate_scale,
+                    void *workspace, size_t workspace_bytes, void *stream);
+size_t mxfp4_moe_route_workspace_size(int T, int E);
+
+/* Bytes of a grouped scale layout: (rows / 128 + groups) * 2 * ceil(K / 256) * 512. */
+size_t mxfp4_group_scale_size(int rows, int groups, int K);
+
+/*
+ * Grouped quantiser: bf16 rows -> the A operand of the grouped products.
+ *   X         bf16 [T, ldx], 16-byte aligned rows (ldx % 8 == 0)
+ *   slot_row  int32 [T, k] and ids int32 [T, k], as mxfp4_moe_route writes
+ *             them: row t goes to row slot_row[t, j] of group ids[t, j] for
+ *             every slot (-1: nowhere).  Both NULL (k = 1, rows = T): X is
+ *             grouped already and row t stays row t
+ *   Q         codes [rows, ldq]: packed E2M1 (ldq % 32 == 0, in elements), or
+ *             for mxfp8_group_quantize one MXFP8_E4M3 / MXFP8_E5M2 code per
+ *             byte (ldq % 16 == 0); 16-byte aligned
+ *   S         grouped scale layout for K
+ * Each row is read and rounded once, by the rules of mxfp4_quantize and
+ * mxfp8_quantize; a 32-block that holds an infinity or a NaN gets the scale
+ * 0xFF (NaN).
+ */
+int mxfp4_group_quantize(void *Q, int64_t ldq, void *S, const void *X, int64_t ldx, int T, int K,
+                         const int *slot_row, const int *ids, int k, const int *offsets,
+                         int groups, int rows, void *stream);
+int mxfp8_group_quantize(void *Q, int64_t ldq, void *S, const void *X, int64_t ldx, int T, int K,
+                         const int *slot_row, const int *ids, int k, const int *offsets,
+                         int groups, int rows, int fmt, void *stream);
+
+/*
+ * Grouped product: D[r, n] = alpha * sum_k A[r, k] * B[e, n, k] for every row
+ * r of group e, accumulated in fp32 and rounded once to bf16.
+ *   A    codes [rows, lda], SA its grouped scale layout
+ *   B    weights as above, ldb >= K, stride_b >= N * ldb, SB relaid
+ *   D    bf16 [rows, ldd], ldd >= N
+ * K % 32 == 0; A and B 16-byte aligned with rows of whole 16 bytes.
+ * mxfp8_grouped_gemm takes the byte formats of mxfp8_gemm.
+ * workspace: mxfp4_grouped_workspace_size(rows, groups, N, K) bytes, 256-byte
+ * aligned, contents arbitrary; calls that may overlap need their own.
+ */
+int mxfp4_grouped_gemm(void *D, int64_t ldd, const void *A, int64_t lda, const void *SA,
+                       const void *B, int64_t ldb, int64_t stride_b, const void *SB,
+                       const int *offsets, int groups, int rows, int N, int K, float alpha,
+                       void *workspace, size_t workspace_bytes, void *stream);
+int mxfp8_grouped_gemm(void *D, int64_t ldd, const void *A, int64_t lda, const void *SA,
+                       const void *B, int64_t ldb, int64_t stride_b, const void *SB,
+                       const int *offsets, int groups, int rows, int N, int K, int fmt_a, int fmt_b,
+                       float alpha, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gated grouped product, quantised for the next one:
+ *   g = alpha * A . Bgate^T, u = alpha * A . Bup^T (fp32),
+ *   H = quantise(g / (1 + exp(-g)) * u) in 1x32 blocks along F,
+ * by the rules of the grouped quantiser.  Nothing is rounded in between.
+ *   B    [groups][2][F, K] (gate rows, up rows), stride_b >= 2 * F * ldb
+ *   H    codes [rows, ldh]: packed E2M1 (ldh % 32 == 0), or of fmt_h, one per
+ *        byte (MXFP8_E4M3 or MXFP8_E5M2; ldh % 16 == 0); 16-byte aligned
+ *   SH   grouped scale layout for F
+ * F % 32 == 0.  Everything else as for the grouped product (N = F in the
+ * workspace size).
+ */
+int mxfp4_grouped_swiglu(void *H, int64_t ldh, void *SH, const void *A, int64_t lda,
+                         const void *SA, const void *B, int64_t ldb, int64_t stride_b,
+                         const void *SB, const int *offsets, int groups, int rows, int F, int K,
+                         float alpha, void *workspace, size_t workspace_bytes, void *stream);
+int mxfp8_grouped_swiglu(void *H, int64_t ldh, void *SH, const void *A, int64_t lda,
+                         const void *SA, const void *B, int64_t ldb, int64_t stride_b,
+                         const void *SB, const int *offsets, int groups, int rows, int F, int K,
+                         int fmt_a, int fmt_b, int fmt_h, float alpha,
+                         void *workspace, size_t workspace_bytes, void *stream);
+size_t mxfp4_grouped_workspace_size(int rows, int groups, int N, int K);
+
+/*
+ * Gated join of a token's rows, with the norms on either side of the residual
+ * stream:
+ *   b = sum_j gates[t, j] * Y[slot_row[t, j]]            (slots of -1 skipped)
+ *   b = b / sqrt(mean(b^2) + eps) * w_post               unless w_post is NULL
+ *   h = res_scale * resid[t] + out_scale * b             -> H
+ *   n = h / sqrt(mean(h^2) + eps) * w_pre                -> Nrm
+ * all in fp32, H and Nrm each rounded once (the norm is of the unrounded h).
+ *   Y bf16 [rows, ldy]; resid bf16 [T, ldr] or NULL (0); w_post, w_pre bf16
+ *   [N] or NULL (w_pre NULL: ones); H, Nrm bf16 [T, ldh / ldn], either may be
+ *   NULL; gates NULL: ones; slot_row NULL (k = 1): row t of Y.
+ * H may alias resid (with ldh == ldr).  N <= 32768.  Rows whose pointers and
+ * strides allow 16-byte accesses are faster.
+ */
+int mxfp4_moe_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *Y, int64_t ldy,
+                      int rows, const int *slot_row, const float *gates, int k, const void *resid,
+                      int64_t ldr, const void *w_post, const void *w_pre, float res_scale,
+                      float out_scale, float eps, int T, int N, void *stream);
+
+/*
+ * A routed feed-forward block on MXFP4, one call: grouped quantiser, gated
+ * product, grouped product (its bf16 rows in the workspace), gated join.
+ *   X bf16 [T, ldx] (the block's normed input); ids, gates, offsets, slot_row
+ *   as mxfp4_moe_route writes them for T tokens, E experts, k slots;
+ *   B1 [E][2][F, K] rows of ldb1 elements, B2 [E][K, F] rows of ldb2, without
+ *   gaps between matrices; SB1, SB2 their relaid scales; the rest as for
+ *   mxfp4_moe_combine with N = K.
+ * workspace: mxfp4_moe_ffn_workspace_size(T, E, k, K, F) bytes, 256-byte aligned.
+ */
+int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, int64_t ldx,
+                  const int *ids, const float *gates, const int *offsets, const int *slot_row,
+                  int T, int E, int k, int K, int F, const void *B1, int64_t ldb1, const void *SB1,
+                  const void *B2, int64_t ldb2, const void *SB2, const void *resid, int64_t ldr,
+                  const void *w_post, const void *w_pre, float res_scale, float out_scale, float eps,
+                  void *workspace, size_t workspace_bytes, void *stream);
+size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F);
+
 /* Set the in-kernel wait limit in SM clock cycles (default 2^32, ~2 s). */
 void mxfp4_set_wait_limit(long long cycles);
 
