@@ -172,8 +172,10 @@ def _p(x) -> Optional[int]:
         return None
     if isinstance(x, int):
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(x, "ctypes"):                      # numpy array
         return x.ctypes.data
     raise TypeError(f"cannot take a pointer of {type(x)}")
@@ -181,11 +183,24 @@ def _p(x) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_raw_stream = None
+
+
+def _current_stream() -> int:
+    """torch's current stream of the current device, as a handle."""
+    global _raw_stream
+    import torch
+    if _raw_stream is None:
+        # The handle alone where torch offers it: no Stream object per call.
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _check(status: int, where: str) -> int:

@@ -3,6 +3,7 @@
 // traffic at prefill sizes and by latency at decoding sizes; every kernel is a
 // programmatic dependent of the work before it on the stream and waits for that
 // work before it reads anything.
+#include <atomic>
 #include <cuda_bf16.h>
 
 #include "expert.h"
@@ -60,93 +61,158 @@ __device__ __forceinline__ float key_value(uint32_t key)
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 
-// Experts lane * V .. lane * V + V - 1 of one token's logits as keys.
-template <int V>
-__device__ __forceinline__ void load_keys(const RouteArgs &a, int t, int lane, uint32_t (&key)[V])
+// Picking.  LANES lanes share a token; each holds CH * 4 of its experts as keys
+// in shared memory, in chunks of four interleaved over the lanes (expert
+// (c * LANES + l) * 4 + i is key i of lane l's chunk c), and the chunks' maxima
+// in registers.  A pick takes the largest maximum of the lanes, and only the
+// lane that owns it looks into one chunk, drops the key and renews one maximum:
+// a handful of instructions per pick for each of the 32 / LANES tokens of a warp.
+// Ties: a lane's chunks and a chunk's keys are in index order, and where
+// several lanes hold the maximum, the lowest of their indexes counts.
+// picks: k (expert, exp or sigmoid) pairs of each of the warp's tokens.
+template <int LANES, int CH>
+__device__ __forceinline__ void route_tokens(const RouteArgs &a, int t, bool live, int bit, int lane, uint4 *keys,
+                                             float2 *picks, uint32_t *masks)
 {
-    const int64_t at = static_cast<int64_t>(t) * a.ldl + lane * V;
+    const int l = lane & (LANES - 1);
+    uint4 *mine = keys + lane;                             // chunk c at mine[32 c]: no bank conflicts
+    const bool on = live && !(a.mask && a.mask[t] == 0);
+    const int64_t row = static_cast<int64_t>(live ? t : 0) * a.ldl;
+    uint32_t top[CH];                                      // the chunks' maxima
+    // Loads first, all in flight together.
+    float x[CH][4];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = lane * V + v;
-        float x = __int_as_float(0xff800000);
-        if (e < a.E)
-            x = a.fp32 ? static_cast<const float *>(a.logits)[at + v]
-                       : bf16_lo(static_cast<const uint16_t *>(a.logits)[at + v]);
-        key[v] = order_key(x);
-    }
-}
-
-// One warp, one token: its k experts into mask bits, ids and gates.
-template <int V>
-__device__ __forceinline__ void route_token(const RouteArgs &a, int t, int bit, int lane, uint32_t *masks)
-{
-    uint32_t key[V];
-    load_keys<V>(a, t, lane, key);
-    const bool off = a.mask && a.mask[t] == 0;
-    if (off) {
+    for (int c = 0; c < CH; ++c) {
+        const int e = (c * LANES + l) * 4;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            key[v] = 0u;
-    }
-    // Lane 0 of the order has the lowest experts, so among equal keys the
-    // first lane's first register is the lowest index.
-    float sum_all = 0.0f;
-    uint32_t top = 0u;
-    uint32_t my_key = 0u;                                  // lane j: the j-th pick
-    int my_id = -1;
-    for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0u;
+        for (int i = 0; i < 4; ++i)
+            x[c][i] = __int_as_float(0xff800000);
+        if (on && e < a.E) {
+            if (a.fp32) {
+                const float *p = static_cast<const float *>(a.logits) + row + e;
+                if (a.vec && e + 4 <= a.E) {
+                    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+                    x[c][0] = v.x;
+                    x[c][1] = v.y;
+                    x[c][2] = v.z;
+                    x[c][3] = v.w;
+                } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            best = max(best, key[v]);
-        const uint32_t m = __reduce_max_sync(kFull, best);
-        if (m == 0u)
-            break;
-        if (j == 0) {
-            top = m;
-            if (a.mode == 1) {
-                const float xm = key_value(m);
+                    for (int i = 0; i < 4; ++i)
+                        if (e + i < a.E)
+                            x[c][i] = p[i];
+                }
+            } else {
+                const uint16_t *p = static_cast<const uint16_t *>(a.logits) + row + e;
+                if (a.vec && e + 4 <= a.E) {
+                    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+                    x[c][0] = bf16_lo(v.x);
+                    x[c][1] = bf16_hi(v.x);
+                    x[c][2] = bf16_lo(v.y);
+                    x[c][3] = bf16_hi(v.y);
+                } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (key[v])
-                        sum_all += key[v] == m ? 1.0f : expf(key_value(key[v]) - xm);
+                    for (int i = 0; i < 4; ++i)
+                        if (e + i < a.E)
+                            x[c][i] = bf16_lo(p[i]);
+                }
             }
         }
-        const int owner = __ffs(__ballot_sync(kFull, best == m)) - 1;
-        int at = 0;
-        if (lane == owner) {
-            bool found = false;
+    }
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (!found && key[v] == m) {
-                    found = true;
-                    at = lane * V + v;
-                    key[v] = 0u;
-                }
-        }
-        at = __shfl_sync(kFull, at, owner);
-        if (lane == j) {
-            my_key = m;
-            my_id = at;
-        }
+    for (int c = 0; c < CH; ++c) {
+        const uint4 k = make_uint4(order_key(x[c][0]), order_key(x[c][1]), order_key(x[c][2]), order_key(x[c][3]));
+        mine[32 * c] = k;
+        top[c] = max(max(k.x, k.y), max(k.z, k.w));
     }
-    const float x = key_value(my_key), xm = key_value(top);
-    float g = 0.0f;
-    if (my_id >= 0)
-        g = a.mode == 2 ? 1.0f / (1.0f + expf(-x)) : my_key == top ? 1.0f : expf(x - xm);
-    if (a.mode != 2) {
-        float sum = a.mode == 1 ? sum_all : g;
+    uint32_t best = top[0];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            sum += __shfl_xor_sync(kFull, sum, d);
-        g = my_id >= 0 ? g / sum : 0.0f;
+    for (int c = 1; c < CH; ++c)
+        best = max(best, top[c]);
+    float2 *my_picks = picks + (lane / LANES) * a.k;
+    uint32_t first = 0u;                                   // the token's largest key
+    float sum = 0.0f;                                      // of the softmax
+    int taken = 0;
+    for (; taken < a.k; ++taken) {
+        uint32_t m = best;
+#pragma unroll
+        for (int d = LANES / 2; d > 0; d >>= 1)
+            m = max(m, __shfl_xor_sync(kFull, m, d));
+        if (taken == 0) {
+            first = m;
+            if (a.mode == 1 && m != 0u) {
+                // Terms far below the largest do not matter to the sum, so the
+                // fast exponential (whose relative error grows with its
+                // argument) keeps the sum to a few 2^-24 of itself.
+                const float xm = key_value(m);
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float z = x[c][i];
+                        sum += z == xm ? 1.0f : z > __int_as_float(0xff800000) ? __expf(z - xm) : 0.0f;
+                    }
+            }
+        }
+        if (!__any_sync(kFull, m != 0u))
+            break;
+        int at = 0x7FFFFFFF, chunk = 0, in = 0;
+        uint4 k = make_uint4(0u, 0u, 0u, 0u);
+        if (m != 0u && best == m) {
+#pragma unroll
+            for (int c = CH - 1; c >= 0; --c)
+                if (top[c] == m)
+                    chunk = c;
+            k = mine[32 * chunk];
+            in = k.x == m ? 0 : k.y == m ? 1 : k.z == m ? 2 : 3;
+            at = (chunk * LANES + l) * 4 + in;
+        }
+        int low = at;
+#pragma unroll
+        for (int d = LANES / 2; d > 0; d >>= 1)
+            low = min(low, __shfl_xor_sync(kFull, low, d));
+        if (m != 0u && at == low) {
+            k.x = in == 0 ? 0u : k.x;
+            k.y = in == 1 ? 0u : k.y;
+            k.z = in == 2 ? 0u : k.z;
+            k.w = in == 3 ? 0u : k.w;
+            mine[32 * chunk] = k;
+            const uint32_t left = max(max(k.x, k.y), max(k.z, k.w));
+            best = 0u;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                top[c] = c == chunk ? left : top[c];
+                best = max(best, top[c]);
+            }
+            my_picks[taken] = make_float2(__int_as_float(at), key_value(m));
+            atomicOr(&masks[at * 4 + (bit >> 5)], 1u << (bit & 31));
+        } else if (m == 0u && l == 0) {
+            my_picks[taken] = make_float2(__int_as_float(-1), 0.0f);
+        }
     }
-    if (lane < a.k) {
-        a.ids[static_cast<int64_t>(t) * a.k + lane] = my_id;
-        a.gates[static_cast<int64_t>(t) * a.k + lane] = a.gate_scale * g;
-        if (my_id >= 0)
-            atomicOr(&masks[my_id * 4 + (bit >> 5)], 1u << (bit & 31));
-    }
+    __syncwarp();
+    // Gates: the lanes of a token share its picks.
+    const float vm = key_value(first);
+    if (a.mode == 0)
+        for (int j = l; j < taken; j += LANES) {
+            const float2 p = my_picks[j];
+            if (__float_as_int(p.x) >= 0)
+                sum += p.y == vm ? 1.0f : expf(p.y - vm);
+        }
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1)
+        sum += __shfl_xor_sync(kFull, sum, d);
+    if (live)
+        for (int j = l; j < a.k; j += LANES) {
+            const float2 p = j < taken ? my_picks[j] : make_float2(__int_as_float(-1), 0.0f);
+            const int id = __float_as_int(p.x);
+            float g = 0.0f;
+            if (id >= 0)
+                g = a.mode == 2 ? 1.0f / (1.0f + expf(-p.y)) : (p.y == vm ? 1.0f : expf(p.y - vm)) / sum;
+            a.ids[static_cast<int64_t>(t) * a.k + j] = id;
+            a.gates[static_cast<int64_t>(t) * a.k + j] = a.gate_scale * g;
+        }
+    __syncwarp();                                          // the keys and picks are used again
 }
 
 // Exclusive prefix sums of total[0 .. E) over the block, in place; returns
@@ -184,12 +250,15 @@ __device__ __forceinline__ int block_scan(int *total, int E)
     return all;
 }
 
-template <int V>
-__global__ void __launch_bounds__(kRouteThreads) route_pick_kernel(const __grid_constant__ RouteArgs a)
+template <int LANES, int CH>
+__global__ void __launch_bounds__(kRouteThreads, 2) route_pick_kernel(const __grid_constant__ RouteArgs a)
 {
-    extern __shared__ uint32_t smem_u32[];
-    uint32_t *masks = smem_u32;                            // [E][4]
-    int *run = reinterpret_cast<int *>(smem_u32 + 4 * a.E);   // [E]
+    constexpr int TPW = 32 / LANES;                        // tokens of a warp
+    extern __shared__ __align__(16) uint32_t smem_u32[];
+    uint4 *all_keys = reinterpret_cast<uint4 *>(smem_u32); // [warps][CH][32]
+    float2 *all_picks = reinterpret_cast<float2 *>(all_keys + kRouteThreads * CH);   // [warps][TPW][k]
+    uint32_t *masks = reinterpret_cast<uint32_t *>(all_picks + kRouteThreads / LANES * a.k);   // [E][4]
+    int *run = reinterpret_cast<int *>(masks + 4 * a.E);   // [E]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * a.chunk;
     const int t1 = min(a.T, t0 + a.chunk);
@@ -204,8 +273,11 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_kernel(const __grid_
             masks[i] = 0u;
         __syncthreads();
         const int s1 = min(t1, s0 + kRouteRun);
-        for (int t = s0 + warp; t < s1; t += kRouteThreads / 32)
-            route_token<V>(a, t, t - s0, lane, masks);
+        for (int q = s0 + warp * TPW; q < s1; q += kRouteThreads / 32 * TPW) {
+            const int t = q + lane / LANES;
+            route_tokens<LANES, CH>(a, t, t < s1, t - s0, lane, all_keys + warp * CH * 32, all_picks + warp * TPW * a.k,
+                                    masks);
+        }
         __syncthreads();
         // Each row's place among its expert's rows of this block.
         for (int i = threadIdx.x; i < (s1 - s0) * a.k; i += kRouteThreads) {
@@ -251,42 +323,45 @@ __global__ void __launch_bounds__(kRouteThreads) route_pick_kernel(const __grid_
 
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid_constant__ RouteArgs a)
 {
-    extern __shared__ uint32_t smem_u32[];
-    int *total = reinterpret_cast<int *>(smem_u32);        // [E rounded up to 8]
-    int *mine = total + (a.E + 7) / 8 * 8;
+    extern __shared__ __align__(16) uint32_t smem_u32[];
     const int ep = (a.E + 7) / 8 * 8, lanes = ep / 8;      // threads of one block's counts
     const int blocks = gridDim.x, me = blockIdx.x;
-    for (int i = threadIdx.x; i < 2 * ep; i += kRouteThreads)
-        total[i] = 0;
-    __syncthreads();
+    const int at_once = kRouteThreads / lanes;             // blocks whose counts are read together
+    uint32_t *part = smem_u32;                             // [at_once][2][ep]: all blocks, the blocks before
+    int *total = reinterpret_cast<int *>(part + 2 * at_once * ep);   // [ep]
+    int *mine = total + ep;                                // [ep]
     pdl_wait_prerequisites();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
-    const int rows_at_once = kRouteThreads / lanes;
-    if (static_cast<int>(threadIdx.x) < rows_at_once * lanes) {
-        const int q = threadIdx.x % lanes;
-        int all[8], before[8];
+    if (static_cast<int>(threadIdx.x) < at_once * lanes) {
+        const int q = threadIdx.x % lanes, g = threadIdx.x / lanes;
+        uint32_t all[8], before[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            all[i] = before[i] = 0;
-#pragma unroll 4
-        for (int b = threadIdx.x / lanes; b < blocks; b += rows_at_once) {
+            all[i] = before[i] = 0u;
+#pragma unroll 8
+        for (int b = g; b < blocks; b += at_once) {
             const uint4 v = *reinterpret_cast<const uint4 *>(a.counts + static_cast<int64_t>(b) * ep + 8 * q);
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int c = (w[i / 2] >> (16 * (i & 1))) & 0xFFFF;
+                const uint32_t c = (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
                 all[i] += c;
-                before[i] += b < me ? c : 0;
+                before[i] += b < me ? c : 0u;
             }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (all[i])
-                atomicAdd(&total[8 * q + i], all[i]);
-            if (before[i])
-                atomicAdd(&mine[8 * q + i], before[i]);
+            part[(2 * g) * ep + 8 * q + i] = all[i];
+            part[(2 * g + 1) * ep + 8 * q + i] = before[i];
         }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * ep; i += kRouteThreads) {
+        uint32_t s = 0u;
+        for (int g = 0; g < at_once; ++g)
+            s += part[2 * g * ep + i];
+        total[i] = static_cast<int>(s);                    // total, then mine
     }
     __syncthreads();
     const int sum = block_scan(total, a.E);
@@ -319,12 +394,24 @@ __global__ void route_empty_kernel(int *offsets, int E)
 // One thread per 1x32 block of a source row: the block is read and rounded
 // once and stored at each of the row's destinations.  The four threads of an
 // atom's word (four consecutive blocks of a row) put their scale codes
-// together and one of them stores the word.
+// together and one of them stores the word.  Blocks move in 32-byte accesses,
+// a whole sector per thread.  The destinations of four slots are looked up
+// together, so that a row costs two dependent round trips (slot, then offset)
+// and not two for each slot.
 
 constexpr int kQuantThreads = 256;
+constexpr int kQuantSlots = 4;
 
-template <QuantFmt Q>
-__global__ void __launch_bounds__(kQuantThreads) group_quantize_kernel(const __grid_constant__ GroupQuantArgs a)
+__device__ __forceinline__ void ld_global_v8(const void *p, uint32_t (&w)[8])
+{
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+
+// WIDE: X's and Q's rows allow 32-byte accesses.
+template <QuantFmt Q, bool WIDE>
+__global__ void __launch_bounds__(kQuantThreads, 3) group_quantize_kernel(const __grid_constant__ GroupQuantArgs a)
 {
     constexpr int W = QuantTraits<Q>::kWords;
     const int kb = a.K / 32;
@@ -341,38 +428,40 @@ __global__ void __launch_bounds__(kQuantThreads) group_quantize_kernel(const __g
         const int t = static_cast<int>((in ? g : total - 1) / kb4);
         const int b = static_cast<int>((in ? g : total - 1) - static_cast<int64_t>(t) * kb4);
         const bool real = in && b < kb;
-        uint32_t out[W];
-        uint32_t code = 0x7Fu;
+        uint32_t src[16];
         if (real) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.X + static_cast<int64_t>(t) * a.ldx + b * 32);
-            float x[32];
+            const uint16_t *x = a.X + static_cast<int64_t>(t) * a.ldx + b * 32;
+            if constexpr (WIDE) {
+                uint32_t lo[8], hi[8];
+                ld_global_v8(x, lo);
+                ld_global_v8(x + 16, hi);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 v = __ldcs(src + i);
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                for (int i = 0; i < 8; ++i) {
+                    src[i] = lo[i];
+                    src[8 + i] = hi[i];
+                }
+            } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[8 * i + 2 * j] = bf16_lo(w[j]);
-                    x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(x) + i);
+                    src[4 * i] = v.x;
+                    src[4 * i + 1] = v.y;
+                    src[4 * i + 2] = v.z;
+                    src[4 * i + 3] = v.w;
                 }
             }
-            code = quantize_block<Q>(x, out);
         }
-        // total and kb4 are multiples of 4, so a word's four threads are all
-        // inside or all outside.
-        uint32_t word = code << (8 * (b & 3));
-        word |= __shfl_xor_sync(kFull, word, 1);
-        word |= __shfl_xor_sync(kFull, word, 2);
-        if (!in)
-            continue;
-        for (int j = 0; j < a.k; ++j) {
-            int row = t, e;
+        uint32_t out[W];
+        uint32_t word = 0x7Fu;
+        for (int j0 = 0; j0 < a.k; j0 += kQuantSlots) {
+            int row[kQuantSlots], e[kQuantSlots], o[kQuantSlots], end[kQuantSlots];
             if (a.slot_row) {
-                const int64_t at = static_cast<int64_t>(t) * a.k + j;
-                row = a.slot_row[at];
-                e = a.ids[at];
-                if (row < 0 || row >= a.rows || e < 0 || e >= a.groups)
-                    continue;
+#pragma unroll
+                for (int i = 0; i < kQuantSlots; ++i) {
+                    const int64_t at = static_cast<int64_t>(t) * a.k + j0 + i;
+                    row[i] = j0 + i < a.k ? a.slot_row[at] : -1;
+                    e[i] = j0 + i < a.k ? a.ids[at] : -1;
+                }
             } else {
                 // The group of row t: the last whose offset is not after it.
                 int lo = 0, hi = a.groups - 1;
@@ -383,22 +472,54 @@ __global__ void __launch_bounds__(kQuantThreads) group_quantize_kernel(const __g
                     else
                         hi = mid - 1;
                 }
-                e = lo;
-            }
-            const int o = a.offsets[e];
-            if (o < 0 || row < o || row >= a.offsets[e + 1])
-                continue;
-            if (real) {
-                uint4 *q = reinterpret_cast<uint4 *>(a.Q + static_cast<int64_t>(row) * a.ldq_bytes +
-                                                     static_cast<int64_t>(b) * (4 * W));
 #pragma unroll
-                for (int w = 0; w < W; w += 4)
-                    q[w / 4] = make_uint4(out[w], out[w + 1], out[w + 2], out[w + 3]);
+                for (int i = 0; i < kQuantSlots; ++i) {
+                    row[i] = i == 0 ? t : -1;
+                    e[i] = lo;
+                }
             }
-            if ((b & 3) == 0) {
-                const int local = row - o;
-                const int64_t block = group_sf_block(o, e) + local / kSfRowBlock;
-                *reinterpret_cast<uint32_t *>(a.S + block * atoms_row + sf_byte(local % kSfRowBlock, b)) = word;
+#pragma unroll
+            for (int i = 0; i < kQuantSlots; ++i) {
+                const bool ok = in && row[i] >= 0 && row[i] < a.rows && e[i] >= 0 && e[i] < a.groups;
+                o[i] = ok ? a.offsets[e[i]] : 0;
+                end[i] = ok ? a.offsets[e[i] + 1] : 0;
+            }
+            if (j0 == 0) {
+                // Rounded after the look-ups were issued.
+                if (real) {
+                    float x[32];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        x[2 * i] = bf16_lo(src[i]);
+                        x[2 * i + 1] = bf16_hi(src[i]);
+                    }
+                    word = quantize_block<Q>(x, out);
+                }
+                // total and kb4 are multiples of 4, so a word's four threads
+                // are all inside or all outside.
+                word <<= 8 * (b & 3);
+                word |= __shfl_xor_sync(kFull, word, 1);
+                word |= __shfl_xor_sync(kFull, word, 2);
+            }
+#pragma unroll
+            for (int i = 0; i < kQuantSlots; ++i) {
+                if (o[i] < 0 || row[i] < o[i] || row[i] >= end[i])
+                    continue;
+                if (real) {
+                    uint8_t *q = a.Q + static_cast<int64_t>(row[i]) * a.ldq_bytes + static_cast<int64_t>(b) * (4 * W);
+                    if constexpr (WIDE && W == 8) {
+                        st_global_v8(q, out[0], out[1], out[2], out[3], out[4], out[5], out[6], out[7]);
+                    } else {
+#pragma unroll
+                        for (int w = 0; w < W; w += 4)
+                            reinterpret_cast<uint4 *>(q)[w / 4] = make_uint4(out[w], out[w + 1], out[w + 2], out[w + 3]);
+                    }
+                }
+                if ((b & 3) == 0) {
+                    const int local = row[i] - o[i];
+                    const int64_t block = group_sf_block(o[i], e[i]) + local / kSfRowBlock;
+                    *reinterpret_cast<uint32_t *>(a.S + block * atoms_row + sf_byte(local % kSfRowBlock, b)) = word;
+                }
             }
         }
     }
@@ -416,23 +537,6 @@ __global__ void __launch_bounds__(kQuantThreads) group_quantize_kernel(const __g
 
 constexpr int kCombineThreads = 512;
 constexpr int kCombineMaxVec = 8;                // 8-element vectors of one thread
-
-__device__ __forceinline__ void load8(const uint16_t *p, int n, int N, int vec, float (&x)[8])
-{
-    if (vec && n + 8 <= N) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p + n);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x[2 * i] = bf16_lo(w[i]);
-            x[2 * i + 1] = bf16_hi(w[i]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = n + i < N ? bf16_lo(p[n + i]) : 0.0f;
-    }
-}
 
 __device__ __forceinline__ void store8(uint16_t *p, int n, int N, int vec, const float (&x)[8])
 {
@@ -469,8 +573,28 @@ __device__ __forceinline__ float block_sum(float v, float *slot)
     return s;
 }
 
-template <int VPT>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ CombineArgs a)
+// Raw bf16 pairs of 8 elements, zeros past N.
+__device__ __forceinline__ uint4 raw8(const uint16_t *p, int n, int N, int vec)
+{
+    if (vec && n + 8 <= N)
+        return *reinterpret_cast<const uint4 *>(p + n);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (n + i < N)
+            w[i / 2] |= static_cast<uint32_t>(p[n + i]) << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float pick8(const uint4 &v, int i)
+{
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return i & 1 ? bf16_hi(w) : bf16_lo(w);
+}
+
+// VPT 8-element vectors per thread, JC slots' rows in flight together.
+template <int VPT, int JC>
+__global__ void __launch_bounds__(kCombineThreads, VPT <= 2 ? 2 : 1) combine_kernel(const __grid_constant__ CombineArgs a)
 {
     __shared__ float slots[4][kCombineThreads / 32];
     pdl_wait_prerequisites();
@@ -479,28 +603,46 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     int parity = 0;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 2) {
         float b[VPT][8];
+        uint4 res[VPT];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+        for (int v = 0; v < VPT; ++v) {
+            const int n = (v * blockDim.x + threadIdx.x) * 8;
+            res[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (VPT < 8 && a.resid && n < a.N)             // early, where registers allow
+                res[v] = raw8(a.resid + static_cast<int64_t>(t) * a.ldr, n, a.N, a.vec);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 b[v][i] = 0.0f;
-        for (int j = 0; j < a.k; ++j) {
-            const int64_t at = static_cast<int64_t>(t) * a.k + j;
-            const int row = a.slot_row ? a.slot_row[at] : t;
-            if (row < 0 || row >= a.rows)
-                continue;
-            const float g = a.gates ? a.gates[at] : 1.0f;
-            const uint16_t *y = a.Y + static_cast<int64_t>(row) * a.ldy;
+        }
+        for (int j0 = 0; j0 < a.k; j0 += JC) {
+            int row[JC];
+            float g[JC];
+            uint4 y[JC][VPT];
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int n = (v * blockDim.x + threadIdx.x) * 8;
-                if (n < a.N) {
-                    float x[8];
-                    load8(y, n, a.N, a.vec, x);
+            for (int j = 0; j < JC; ++j) {
+                const int64_t at = static_cast<int64_t>(t) * a.k + j0 + j;
+                row[j] = j0 + j < a.k ? (a.slot_row ? a.slot_row[at] : t) : -1;
+                g[j] = j0 + j < a.k && a.gates ? a.gates[at] : 1.0f;
+            }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        b[v][i] = fmaf(g, x[i], b[v][i]);
+            for (int j = 0; j < JC; ++j)
+#pragma unroll
+                for (int v = 0; v < VPT; ++v) {
+                    const int n = (v * blockDim.x + threadIdx.x) * 8;
+                    if (row[j] >= 0 && row[j] < a.rows && n < a.N)
+                        y[j][v] = raw8(a.Y + static_cast<int64_t>(row[j]) * a.ldy, n, a.N, a.vec);
                 }
+#pragma unroll
+            for (int j = 0; j < JC; ++j) {
+                if (row[j] < 0 || row[j] >= a.rows)
+                    continue;                              // block-uniform
+#pragma unroll
+                for (int v = 0; v < VPT; ++v)
+                    if ((v * blockDim.x + threadIdx.x) * 8 < a.N) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            b[v][i] = fmaf(g[j], pick8(y[j][v], i), b[v][i]);
+                    }
             }
         }
         if (a.w_post) {
@@ -516,11 +658,10 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
             for (int v = 0; v < VPT; ++v) {
                 const int n = (v * blockDim.x + threadIdx.x) * 8;
                 if (n < a.N) {
-                    float w[8];
-                    load8(a.w_post, n, a.N, a.vec, w);
+                    const uint4 w = raw8(a.w_post, n, a.N, a.vec);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        b[v][i] = b[v][i] * r * w[i];
+                        b[v][i] = b[v][i] * r * pick8(w, i);
                 }
             }
         }
@@ -529,17 +670,11 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
         for (int v = 0; v < VPT; ++v) {
             const int n = (v * blockDim.x + threadIdx.x) * 8;
             if (n < a.N) {
-                float x[8];
-                if (a.resid) {
-                    load8(a.resid + static_cast<int64_t>(t) * a.ldr, n, a.N, a.vec, x);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        x[i] = 0.0f;
-                }
+                if (VPT == 8 && a.resid)
+                    res[v] = raw8(a.resid + static_cast<int64_t>(t) * a.ldr, n, a.N, a.vec);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    b[v][i] = a.resid ? fmaf(a.out_scale, b[v][i], a.res_scale * x[i]) : a.out_scale * b[v][i];
+                    b[v][i] = a.resid ? fmaf(a.out_scale, b[v][i], a.res_scale * pick8(res[v], i)) : a.out_scale * b[v][i];
                     ss = fmaf(b[v][i], b[v][i], ss);
                 }
                 if (a.H)
@@ -553,17 +688,17 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
             for (int v = 0; v < VPT; ++v) {
                 const int n = (v * blockDim.x + threadIdx.x) * 8;
                 if (n < a.N) {
-                    float w[8], y[8];
+                    float y[8];
                     if (a.w_pre) {
-                        load8(a.w_pre, n, a.N, a.vec, w);
+                        const uint4 w = raw8(a.w_pre, n, a.N, a.vec);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = b[v][i] * r * pick8(w, i);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            w[i] = 1.0f;
+                            y[i] = b[v][i] * r;
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] = b[v][i] * r * w[i];
                     store8(a.Nrm + static_cast<int64_t>(t) * a.ldn, n, a.N, a.vec, y);
                 }
             }
@@ -571,10 +706,27 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     }
 }
 
-template <int V>
-cudaError_t launch_pick(const RouteArgs &a, size_t smem, cudaStream_t stream)
+template <int LANES, int CH>
+cudaError_t launch_pick(const RouteArgs &a, cudaStream_t stream)
 {
-    return launch_dependent(route_pick_kernel<V>, dim3(a.blocks), dim3(kRouteThreads), smem, stream, a);
+    const size_t smem = static_cast<size_t>(kRouteThreads) * CH * 16 + static_cast<size_t>(kRouteThreads / LANES) * a.k * 8 +
+                        static_cast<size_t>(5 * a.E) * 4;
+    auto kern = route_pick_kernel<LANES, CH>;
+    static std::atomic<int> configured[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
+        // The most that any E and k need of this instance.
+        const int most = kRouteThreads * CH * 16 + kRouteThreads / LANES * kMaxTopK * 8 + 5 * LANES * CH * 4 * 4;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            configured[dev].store(1, std::memory_order_relaxed);
+    }
+    return launch_dependent(kern, dim3(a.blocks), dim3(kRouteThreads), smem, stream, a);
 }
 
 }  // namespace
@@ -588,40 +740,61 @@ int route_blocks(int T, int *chunk)
     return (T + c - 1) / c;
 }
 
-cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream)
+cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream)
 {
     if (a.T == 0)
         return launch_dependent(route_empty_kernel, dim3(1), dim3(256), 0, stream, a.offsets, a.E);
-    const size_t smem = static_cast<size_t>(5 * a.E) * 4;
+    // Lanes per token: as few as hold its experts in 32 registers each, which
+    // shares a pick's instructions among the most tokens, once that still
+    // leaves every SM 16 warps; otherwise a whole warp per token, the shortest
+    // time for one.  (32768 tokens of 256 experts: 8 lanes.)
+    int lanes = 1;
+    while (lanes * 32 < a.E)
+        lanes *= 2;
     cudaError_t e;
-    if (a.E <= 32)
-        e = launch_pick<1>(a, smem, stream);
-    else if (a.E <= 64)
-        e = launch_pick<2>(a, smem, stream);
-    else if (a.E <= 128)
-        e = launch_pick<4>(a, smem, stream);
-    else if (a.E <= 256)
-        e = launch_pick<8>(a, smem, stream);
-    else if (a.E <= 512)
-        e = launch_pick<16>(a, smem, stream);
-    else
-        e = launch_pick<32>(a, smem, stream);
+    if (static_cast<int64_t>(a.T) * lanes / 32 < static_cast<int64_t>(sms) * 16) {
+        e = a.E <= 128   ? launch_pick<32, 1>(a, stream)
+            : a.E <= 256 ? launch_pick<32, 2>(a, stream)
+            : a.E <= 512 ? launch_pick<32, 4>(a, stream)
+                         : launch_pick<32, 8>(a, stream);
+    } else {
+        switch (lanes) {
+        case 1: e = launch_pick<1, 8>(a, stream); break;
+        case 2: e = launch_pick<2, 8>(a, stream); break;
+        case 4: e = launch_pick<4, 8>(a, stream); break;
+        case 8: e = launch_pick<8, 8>(a, stream); break;
+        case 16: e = launch_pick<16, 8>(a, stream); break;
+        default: e = launch_pick<32, 8>(a, stream); break;
+        }
+    }
     if (e != cudaSuccess || a.blocks == 1)
         return e;
-    const size_t smem2 = static_cast<size_t>(2 * ((a.E + 7) / 8 * 8)) * 4;
+    const int ep = (a.E + 7) / 8 * 8;
+    const size_t smem2 = static_cast<size_t>(2 * (kRouteThreads / (ep / 8)) + 2) * ep * 4;
     return launch_dependent(route_place_kernel, dim3(a.blocks), dim3(kRouteThreads), smem2, stream, a);
+}
+
+template <QuantFmt Q>
+static cudaError_t launch_quant(const GroupQuantArgs &a, dim3 grid, dim3 block, cudaStream_t stream)
+{
+    const bool wide = (reinterpret_cast<uintptr_t>(a.X) % 32) == 0 && (a.ldx % 16) == 0 &&
+                      (reinterpret_cast<uintptr_t>(a.Q) % 32) == 0 && (a.ldq_bytes % 32) == 0;
+    return wide ? launch_dependent(group_quantize_kernel<Q, true>, grid, block, 0, stream, a)
+                : launch_dependent(group_quantize_kernel<Q, false>, grid, block, 0, stream, a);
 }
 
 cudaError_t launch_group_quantize(const GroupQuantArgs &a, int sms, cudaStream_t stream)
 {
     const int64_t total = static_cast<int64_t>(a.T) * ((a.K / 32 + 3) / 4 * 4);
-    const int64_t want = (total + kQuantThreads - 1) / kQuantThreads;
+    // Few blocks of work: small CTAs, so that they spread over the SMs.
+    const int threads = total < static_cast<int64_t>(sms) * kQuantThreads ? 64 : kQuantThreads;
+    const int64_t want = (total + threads - 1) / threads;
     const int64_t most = static_cast<int64_t>(sms) * 32;
-    const dim3 grid(static_cast<unsigned>(want < most ? want : most));
+    const dim3 grid(static_cast<unsigned>(want < most ? want : most)), block(static_cast<unsigned>(threads));
     switch (a.fmt) {
-    case 0: return launch_dependent(group_quantize_kernel<QuantFmt::kE2M1>, grid, dim3(kQuantThreads), 0, stream, a);
-    case 1: return launch_dependent(group_quantize_kernel<QuantFmt::kE4M3>, grid, dim3(kQuantThreads), 0, stream, a);
-    default: return launch_dependent(group_quantize_kernel<QuantFmt::kE5M2>, grid, dim3(kQuantThreads), 0, stream, a);
+    case 0: return launch_quant<QuantFmt::kE2M1>(a, grid, block, stream);
+    case 1: return launch_quant<QuantFmt::kE4M3>(a, grid, block, stream);
+    default: return launch_quant<QuantFmt::kE5M2>(a, grid, block, stream);
     }
 }
 
@@ -633,13 +806,13 @@ cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream)
     const int most = sms * (2048 / threads);
     const dim3 grid(static_cast<unsigned>(a.T < most ? a.T : most)), block(static_cast<unsigned>(threads));
     if (per <= 1)
-        return launch_dependent(combine_kernel<1>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<1, 8>, grid, block, 0, stream, a);
     if (per <= 2)
-        return launch_dependent(combine_kernel<2>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<2, 4>, grid, block, 0, stream, a);
     if (per <= 4)
-        return launch_dependent(combine_kernel<4>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<4, 2>, grid, block, 0, stream, a);
     if (per <= kCombineMaxVec)
-        return launch_dependent(combine_kernel<8>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<8, 1>, grid, block, 0, stream, a);
     return cudaErrorInvalidValue;
 }
 

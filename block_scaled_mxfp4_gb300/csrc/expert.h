@@ -41,6 +41,7 @@ struct RouteArgs {
     const void *logits;         // bf16 or fp32 [T, ldl]
     int64_t ldl;
     int fp32;
+    int vec;                    // rows allow loads of four logits
     const uint8_t *mask;        // [T] or null; 0: the token takes no expert
     int T, E, k, mode;
     float gate_scale;
@@ -54,7 +55,7 @@ struct RouteArgs {
     int chunk;                  // tokens per block, a multiple of 32
 };
 int route_blocks(int T, int *chunk);
-cudaError_t launch_route(const RouteArgs &a, cudaStream_t stream);
+cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream);
 
 struct GroupQuantArgs {
     uint8_t *Q;
@@ -101,7 +102,8 @@ struct GroupedArgs {
     float alpha;
     uint16_t *D;                // plain form: bf16 [rows, ldd]
     int64_t ldd;
-    int vec32_ok, vec_ok;       // D allows aligned 32- / 16-byte row stores
+    int vec32_ok, vec_ok;       // D (H) allows aligned 32- / 16-byte row stores
+    int tma_ok;                 // D allows TMA stores
     uint8_t *H;                 // gated form: codes [rows, ldh bytes]
     int64_t ldh;
     uint8_t *SH;                // grouped scale layout over N
@@ -112,7 +114,8 @@ struct GroupedArgs {
     long long wait_limit;
 };
 struct GroupedMaps {
-    CUtensorMap A, SA, B, SB;
+    CUtensorMap A, A32, SA, B, SB;   // A: boxes of 128 rows, A32: of 32
+    CUtensorMap D;                   // plain form with tma_ok: boxes of 32 rows x 64 columns
 };
 // out: -1 plain (bf16), else the QuantFmt of the gated form's output.
 size_t grouped_workspace_bytes(int rows, int groups, int N, int K, bool gated, int sms);

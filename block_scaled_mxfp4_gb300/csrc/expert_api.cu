@@ -92,11 +92,13 @@ int run_product(const Product &p, int sms, cudaStream_t stream)
     const int per_stage = p.bytes8 ? 1 : 2;
     const int64_t rb = sf_row_blocks(p.N);
     GroupedMaps m;
+    std::memset(&m, 0, sizeof(m));
     {
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.K / den), static_cast<cuuint64_t>(p.rows)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.lda / den)};
-        const cuuint32_t box[2] = {128, 128};
-        if (!encode(&m.A, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        const cuuint32_t box[2] = {128, 128}, box32[2] = {128, 32};
+        if (!encode(&m.A, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.A, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !encode(&m.A32, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, p.A, dims, strides, box32, CU_TENSOR_MAP_SWIZZLE_128B))
             return MXFP4_ERR_CUDA;
     }
     {
@@ -140,11 +142,18 @@ int run_product(const Product &p, int sms, cudaStream_t stream)
         a.H = static_cast<uint8_t *>(p.D);
         a.ldh = p.out == 0 ? p.ldd / 2 : p.ldd;
         a.SH = static_cast<uint8_t *>(p.SH);
+        a.vec32_ok = aligned(p.D, 32) && (a.ldh % 32) == 0;
     } else {
         a.D = static_cast<uint16_t *>(p.D);
         a.ldd = p.ldd;
         a.vec_ok = aligned(p.D, 16) && (p.ldd % 8) == 0;
         a.vec32_ok = aligned(p.D, 32) && (p.ldd % 16) == 0;
+        a.tma_ok = a.vec_ok;
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.rows)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.ldd) * 2};
+        const cuuint32_t box[2] = {64, 32};
+        if (a.tma_ok && !encode(&m.D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.D, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+            return MXFP4_ERR_CUDA;
     }
     if (p.bytes8)
         a.idesc8 = idesc_mxf8(256, 256, static_cast<uint32_t>(p.fmt_a), static_cast<uint32_t>(p.fmt_b));
@@ -291,6 +300,7 @@ int mxfp4_moe_route(int *ids, float *gates, int *offsets, int *row_token, int *s
     a.logits = logits;
     a.ldl = ldl;
     a.fp32 = logits_type == MXFP4_LOGITS_FP32;
+    a.vec = aligned(logits, a.fp32 ? 16 : 8) && (ldl % 4) == 0;
     a.mask = static_cast<const uint8_t *>(token_mask);
     a.T = T;
     a.E = E;
@@ -303,7 +313,7 @@ int mxfp4_moe_route(int *ids, float *gates, int *offsets, int *row_token, int *s
     a.row_token = row_token;
     a.slot_row = slot_row;
     a.counts = static_cast<uint16_t *>(workspace);
-    return status_of(launch_route(a, static_cast<cudaStream_t>(stream)));
+    return status_of(launch_route(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 size_t mxfp4_group_scale_size(int rows, int groups, int K)

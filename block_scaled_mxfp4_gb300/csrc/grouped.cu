@@ -48,6 +48,8 @@ namespace mxfp4 {
 
 namespace {
 
+constexpr uint32_t kFull = 0xffffffffu;
+
 __device__ int g_status = 0;
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z,
@@ -75,6 +77,23 @@ __device__ __forceinline__ void mma_mxf8_pair_elect(uint32_t d_tmem, uint64_t ad
         : "memory");
 }
 
+// Registers move from the warpgroups that load and issue to the epilogue's,
+// which holds a warp's 128 accumulator columns at once.  Their shares, 256
+// threads each, stay within what the block was launched with (128 x 512; the
+// launcher checks it).
+constexpr int kEpilogueRegs = 192, kOtherRegs = 56;
+static_assert((kEpilogueRegs + kOtherRegs) * 256 <= 128 * 512, "register split");
+
+__device__ __forceinline__ void take_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpilogueRegs));
+}
+
+__device__ __forceinline__ void give_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+}
+
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
@@ -83,9 +102,13 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
 
 // BYTES8: byte formats, 128 K and one scale atom per stage and 128-row block;
 // otherwise packed E2M1, 256 K and two atoms.
-template <bool BYTES8>
+// The plain form gives one stage up for the epilogue's boxes.
+constexpr int kOutBoxBytes = 32 * 128;           // one epilogue warp's 32 rows x 64 bf16
+
+template <bool BYTES8, bool GATED>
 struct GroupedCfg {
-    static constexpr int STAGES = 6;
+    static constexpr int STAGES = GATED ? 6 : 5;
+    static constexpr int OUT_BYTES = GATED ? 0 : 8 * kOutBoxBytes;
     static constexpr int G = BYTES8 ? 1 : 2;
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int B_BYTES = 128 * 128;
@@ -95,7 +118,7 @@ struct GroupedCfg {
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
     static constexpr int BAR_BYTES = 512;
     static constexpr int TABLE_BYTES = 2 * (kMaxGroups + 1) * 4;   // offsets and row-tile prefix sums
-    static constexpr int SMEM_BYTES = RING_BYTES + BAR_BYTES + TABLE_BYTES + 1024;
+    static constexpr int SMEM_BYTES = RING_BYTES + OUT_BYTES + BAR_BYTES + TABLE_BYTES + 1024;
     static constexpr int SF_COLS_A = 4 * G;
     static constexpr int SF_COLS_B = 8 * G;
     static constexpr int SF_COLS = SF_COLS_A + SF_COLS_B;
@@ -123,6 +146,7 @@ struct Tile {
     int end;            // end of the group's rows
     int sfa;            // 128-row scale block of row0
     int q;              // column tile
+    bool single;        // the group has no other row tile
 };
 
 __device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
@@ -144,6 +168,7 @@ __device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
     const int p = local % mt;
     r.e = lo;
     r.q = local / mt;
+    r.single = mt == 1;
     r.row0 = t.off[lo] + p * 256;
     r.end = t.off[lo + 1];
     r.sfa = static_cast<int>(group_sf_block(t.off[lo], lo)) + 2 * p;
@@ -168,7 +193,7 @@ __device__ __forceinline__ void build_tables(const GroupedArgs &a, int *off, int
     int sum = c[0] + c[1];
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, sum, d);
+        const int v = __shfl_up_sync(kFull, sum, d);
         if (lane >= d)
             sum += v;
     }
@@ -193,19 +218,129 @@ __device__ __forceinline__ void build_tables(const GroupedArgs &a, int *off, int
     }
 }
 
+// 2-D tiled bulk-tensor store from shared memory (x innermost), in this
+// thread's current bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_addr(src)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The group's shared memory has been read / its writes are done.
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// 32 columns: alpha, one rounding, bf16 pairs.
+__device__ __forceinline__ void round_bf16(const GroupedArgs &a, const uint32_t (&x)[32], uint32_t (&out)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        out[j] = bf16x2(a.alpha * __uint_as_float(x[2 * j]), a.alpha * __uint_as_float(x[2 * j + 1]));
+}
+
+// 32 columns of row r from n0 on, by this thread alone.
+__device__ __forceinline__ void store_bf16(const GroupedArgs &a, int r, int n0, const uint32_t (&x)[32])
+{
+    if (n0 >= a.N)
+        return;
+    uint32_t out[16];
+    round_bf16(a, x, out);
+    uint16_t *d = a.D + static_cast<int64_t>(r) * a.ldd + n0;
+    if (a.vec32_ok && n0 + 32 <= a.N) {
+#pragma unroll
+        for (int j = 0; j < 16; j += 8)
+            st_global_v8(d + 2 * j, out[j], out[j + 1], out[j + 2], out[j + 3], out[j + 4], out[j + 5], out[j + 6],
+                         out[j + 7]);
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        if (a.vec_ok && n0 + 2 * j + 8 <= a.N) {
+            *reinterpret_cast<uint4 *>(d + 2 * j) = make_uint4(out[j], out[j + 1], out[j + 2], out[j + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (n0 + 2 * j + i < a.N)
+                    d[2 * j + i] = static_cast<uint16_t>(out[j + i / 2] >> (16 * (i & 1)));
+        }
+    }
+}
+
+// silu(alpha g) * (alpha u) in fp32.  The exponent's argument is rounded once,
+// so the sigmoid is good to |g| 2^-24, and the reciprocal to 1 ulp: beside the
+// products' own accumulation error.  A large negative g gives e = inf and 0.
+__device__ __forceinline__ float gated_value(float alpha, uint32_t gate, uint32_t up)
+{
+    const float g = alpha * __uint_as_float(gate);
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return g * s * (alpha * __uint_as_float(up));
+}
+
+// Columns f0 .. f0 + 63 of row r (row `local` of the 128-row scale block whose
+// atoms start at byte `block`): activation in fp32, one rounding into the
+// block's format.  gate, up: the products of columns [0, 32) and [32, 64).
+template <QuantFmt Q>
+__device__ __forceinline__ void store_gated(const GroupedArgs &a, int r, int local, int64_t block, int f0,
+                                            const uint32_t (&gate0)[32], const uint32_t (&gate1)[32],
+                                            const uint32_t (&up0)[32], const uint32_t (&up1)[32])
+{
+    constexpr int W = QuantTraits<Q>::kWords;
+    if (f0 >= a.N)
+        return;
+    float h[32];
+    uint32_t lo[W], hi[W];
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        h[i] = gated_value(a.alpha, gate0[i], up0[i]);
+    uint32_t codes = quantize_block<Q>(h, lo);
+    const bool both = f0 + 32 < a.N;
+    // An odd last block's partner in the same MMA of the next product: any
+    // finite scale serves its zero codes.
+    uint32_t second = 0x7Fu;
+    if (both) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            h[i] = gated_value(a.alpha, gate1[i], up1[i]);
+        second = quantize_block<Q>(h, hi);
+    }
+    *reinterpret_cast<uint16_t *>(a.SH + block + sf_byte(local, f0 / 32)) = static_cast<uint16_t>(codes | (second << 8));
+    uint8_t *q = a.H + static_cast<int64_t>(r) * a.ldh + (Q == QuantFmt::kE2M1 ? f0 / 2 : f0);
+    if (a.vec32_ok && both) {
+        if constexpr (W == 4) {
+            st_global_v8(q, lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]);
+        } else {
+            st_global_v8(q, lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]);
+            st_global_v8(q + 32, hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]);
+        }
+        return;
+    }
+#pragma unroll
+    for (int w = 0; w < W; w += 4) {
+        reinterpret_cast<uint4 *>(q)[w / 4] = make_uint4(lo[w], lo[w + 1], lo[w + 2], lo[w + 3]);
+        if (both)
+            reinterpret_cast<uint4 *>(q)[W / 4 + w / 4] = make_uint4(hi[w], hi[w + 1], hi[w + 2], hi[w + 3]);
+    }
+}
+
 // OUT: -1 plain bf16, else static_cast<int>(QuantFmt) of the gated form.
 template <bool BYTES8, int OUT>
 __global__ void __launch_bounds__(512, 1)
     grouped_pair(const __grid_constant__ GroupedArgs a, const __grid_constant__ GroupedMaps maps)
 {
-    using Cf = GroupedCfg<BYTES8>;
+    using Cf = GroupedCfg<BYTES8, (OUT >= 0)>;
     constexpr int G = Cf::G;
     constexpr bool GATED = OUT >= 0;
     constexpr int STAGES = Cf::STAGES;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cf::RING_BYTES);
+    uint8_t *stage_out = smem + Cf::RING_BYTES;     // the plain epilogue's boxes
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cf::RING_BYTES + Cf::OUT_BYTES);
     uint64_t *empty = full + STAGES;
     uint64_t *sf_ready = empty + STAGES;            // the leader's are used
     uint64_t *acc_full = sf_ready + STAGES;
@@ -213,7 +348,7 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t *drain = acc_empty + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *tab_off = reinterpret_cast<int *>(smem + Cf::RING_BYTES + Cf::BAR_BYTES);
+    int *tab_off = reinterpret_cast<int *>(smem + Cf::RING_BYTES + Cf::OUT_BYTES + Cf::BAR_BYTES);
     int *tab_base = tab_off + kMaxGroups + 1;
 
     const int warp = threadIdx.x >> 5;
@@ -241,6 +376,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     if (warp == 4 && lane == 0) {
         prefetch_tensormap(&maps.A);
+        prefetch_tensormap(&maps.A32);
         prefetch_tensormap(&maps.SA);
         prefetch_tensormap(&maps.B);
         prefetch_tensormap(&maps.SB);
@@ -257,178 +393,8 @@ __global__ void __launch_bounds__(512, 1)
     if (threadIdx.x == 0)
         pdl_launch_dependents();
 
-    if (warp == 4 || warp == 6 || warp == 7) {
-        // ------------------------------------------------------ producers --
-        if (lane == 0) {
-            const int role = warp == 4 ? 0 : warp - 5;   // 0: A, 1: B, 2: scales
-            const uint64_t pol = l2_policy_evict_last();
-            int stage = 0;
-            uint32_t phase = 0;
-            int issued = 0;
-            bool stop = false;
-            for (int t = pair; t < tiles && !stop; t += pairs) {
-                const Tile tl = tile_at(table, t);
-                const int arow = tl.row0 + static_cast<int>(rank) * 128;
-                const bool rows_here = arow < tl.end;
-                const uint32_t unit = role == 0   ? (rows_here ? Cf::A_BYTES : 0)
-                                      : role == 1 ? Cf::B_BYTES
-                                                  : Cf::SFB_BYTES + (rows_here ? Cf::SFA_BYTES : 0);
-                for (int kt = 0; kt < a.kt; ++kt) {
-                    if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_limit, &g_status)) {
-                        stop = true;
-                        break;
-                    }
-                    uint8_t *st = smem + stage * Cf::STAGE_BYTES;
-                    uint8_t *sf = st + Cf::A_BYTES + Cf::B_BYTES;
-                    mbar_arrive_expect_tx(&full[stage], unit);
-                    if (role == 0) {
-                        if (rows_here)
-                            tma_load_2d(st, &maps.A, &full[stage], kt * 128, arow, pol);
-                    } else if (role == 1) {
-                        // Plain: 128 rows of B.  Gated: 64 gate rows and the
-                        // same 64 up rows (the map's third dimension).
-                        const int n = GATED ? tl.q * 128 + static_cast<int>(rank) * 64
-                                            : tl.q * 256 + static_cast<int>(rank) * 128;
-                        tma_load_4d(st + Cf::A_BYTES, &maps.B, &full[stage], kt * 128, n, 0, tl.e, pol);
-                    } else {
-                        if (rows_here)
-                            tma_load_3d(sf, &maps.SA, &full[stage], 0, G * kt, tl.sfa + static_cast<int>(rank), pol);
-                        // Plain: two 128-row blocks of the expert.  Gated: the
-                        // block of the gate rows and the block of the up rows.
-                        tma_load_4d(sf + Cf::SFA_BYTES, &maps.SB, &full[stage], 0, G * kt,
-                                    GATED ? tl.q : 2 * tl.q, GATED ? 2 * tl.e : tl.e, pol);
-                    }
-                    ++issued;
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-            }
-            if (*abort_flag) {
-                // Let the copies already issued land before the CTA exits.
-                for (int i = max(0, issued - STAGES); i < issued; ++i)
-                    mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1u, a.wait_limit);
-            }
-        }
-    } else if (warp >= 12) {
-        // -------------------------------------------- scale writers --
-        // Line `lane` of an atom: rows lane, lane + 32, lane + 64, lane + 96 of
-        // its 128-row block, a word of four scales each; the four warps write
-        // the four lane quarters' replicas.
-        const int quarter = warp & 3;
-        const uint32_t t_q = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + Cf::ACC_COLS;
-        const uint32_t lead_ready = map_to_rank(smem_addr(&sf_ready[0]), 0);
-        const int my_tiles = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
-        const int total = my_tiles * a.kt;
-        int stage = 0;
-        uint32_t phase = 0;
-        for (int i = 0; i < total; ++i) {
-            bool ok = mbar_wait(&full[stage], phase, abort_flag, a.wait_limit, &g_status);
-            if (!__all_sync(0xffffffffu, ok))
-                break;
-            const uint8_t *sf = smem + stage * Cf::STAGE_BYTES + Cf::A_BYTES + Cf::B_BYTES;
-            uint32_t wa[4 * G], wb[8 * G];
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(sf + g * kSfAtomBytes + 16 * lane);
-                const uint4 x = *reinterpret_cast<const uint4 *>(sf + Cf::SFA_BYTES + g * kSfAtomBytes + 16 * lane);
-                const uint4 y =
-                    *reinterpret_cast<const uint4 *>(sf + Cf::SFA_BYTES + (G + g) * kSfAtomBytes + 16 * lane);
-                wa[4 * g] = v.x;
-                wa[4 * g + 1] = v.y;
-                wa[4 * g + 2] = v.z;
-                wa[4 * g + 3] = v.w;
-                // Word j of block b of atom g -> column 8 g + 4 b + j.  Plain:
-                // blocks x, y.  Gated: the tile's first 128 rows are gate rows
-                // 0-63 and up rows 0-63 (words 0, 1 of either block).
-                uint32_t *w = wb + 8 * g;
-                w[0] = x.x;
-                w[1] = x.y;
-                w[2] = GATED ? y.x : x.z;
-                w[3] = GATED ? y.y : x.w;
-                w[4] = GATED ? x.z : y.x;
-                w[5] = GATED ? x.w : y.y;
-                w[6] = y.z;
-                w[7] = y.w;
-            }
-            const uint32_t slot = t_q + stage * Cf::SF_COLS;
-            if constexpr (G == 2) {
-                tmem_st_32x32b_x8(slot, wa);
-                tmem_st_32x32b_x16(slot + Cf::SF_COLS_A, wb);
-            } else {
-                tmem_st_32x32b_x4(slot, wa);
-                tmem_st_32x32b_x8(slot + Cf::SF_COLS_A, wb);
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (leader)
-                    mbar_arrive(&sf_ready[stage]);
-                else
-                    mbar_arrive_cluster_relaxed(lead_ready + static_cast<uint32_t>(stage * sizeof(uint64_t)));
-            }
-            if (++stage == STAGES) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
-    } else if (warp == 5) {
-        // ------------------------------------------------ MMA (leader) --
-        if (leader) {
-            const uint32_t idesc = BYTES8 ? a.idesc8 : idesc_mxf4(256, 256);
-            int stage = 0;
-            uint32_t phase = 0, acc_phase = 0;
-            bool stop = false;
-            for (int t = pair; t < tiles && !stop; t += pairs) {
-                if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, a.wait_limit, &g_status))
-                    break;
-                tc_fence_after();
-                for (int kt = 0; kt < a.kt; ++kt) {
-                    // sf_ready completes after the scale writers of both CTAs
-                    // saw the stage's bytes land.
-                    if (!mbar_wait(&sf_ready[stage], phase, abort_flag, a.wait_limit, &g_status)) {
-                        stop = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sfa = tmem + Cf::ACC_COLS + stage * Cf::SF_COLS;
-                    const uint32_t sfb = sfa + Cf::SF_COLS_A;
-                    const uint32_t st = smem_addr(smem + stage * Cf::STAGE_BYTES);
-                    const uint64_t adesc = sdesc_kmajor_sw128(st);
-                    const uint64_t bdesc = sdesc_kmajor_sw128(st + Cf::A_BYTES);
-                    const int left = a.K - kt * Cf::K_STAGE;      // K elements of this stage
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j * Cf::K_MMA >= left)
-                            break;
-                        const uint32_t acc = (kt > 0 || j > 0) ? 1u : 0u;
-                        if constexpr (BYTES8) {
-                            mma_mxf8_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_sf_ids(idesc, j, j), sfa, sfb,
-                                                acc);
-                        } else {
-                            const uint32_t id = (j & 1) * 2;
-                            mma_mxf4_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_sf_ids(idesc, id, id),
-                                                sfa + (j >> 1) * 4, sfb + (j >> 1) * 8, acc);
-                        }
-                    }
-                    mma_commit_pair_elect(&empty[stage], static_cast<uint16_t>(3u));
-                    if (++stage == STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
-                if (!stop)
-                    mma_commit_pair_elect(acc_full, static_cast<uint16_t>(3u));
-                acc_phase ^= 1u;
-            }
-            if (*abort_flag) {
-                mma_commit_pair_elect(drain, static_cast<uint16_t>(1u));
-                mbar_wait_drain(drain, 0, a.wait_limit);
-            }
-        }
-    } else {
+    if (warp < 4 || (warp >= 8 && warp < 12)) {
+        take_registers();
         // ------------------------------------------------------ epilogue --
         const int quarter = warp & 3;
         const int half = warp >> 3;
@@ -439,95 +405,250 @@ __global__ void __launch_bounds__(512, 1)
         for (int t = pair; t < tiles; t += pairs) {
             const Tile tl = tile_at(table, t);
             bool ok = mbar_wait(acc_full, acc_phase, abort_flag, a.wait_limit, &g_status);
-            if (!__all_sync(0xffffffffu, ok))
+            if (!__all_sync(kFull, ok))
                 break;
             acc_phase ^= 1u;
             tc_fence_after();
             const int r = tl.row0 + row;
             const bool mine = r < tl.end;
-            const bool any = __any_sync(0xffffffffu, mine);
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-                uint32_t x[32], y[32];
-                __syncwarp();
-                if (any) {
-                    // Plain: columns 64 c + [0, 64).  Gated: gate and up columns 32 c + [0, 32).
-                    tmem_ld_32x32b_x32(t_lane + (GATED ? 32 * c : 64 * c), x);
-                    tmem_ld_32x32b_x32(t_lane + (GATED ? 64 + 32 * c : 64 * c + 32), y);
-                    tmem_ld_wait(x, y);
-                }
-                if (c == 1) {
-                    // The accumulator's cells are read (tcgen05.wait::ld has
-                    // returned): the next tile's MMAs may start.
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (leader)
-                            mbar_arrive(acc_empty);
-                        else
-                            mbar_arrive_cluster_relaxed(lead_empty);
-                    }
-                }
-                if (!mine)
-                    continue;
-                if constexpr (!GATED) {
-                    const int n0 = tl.q * 256 + half * 128 + 64 * c;
-                    if (n0 >= a.N)
-                        continue;
-                    uint16_t *d = a.D + static_cast<int64_t>(r) * a.ldd + n0;
-                    uint32_t out[32];
+            // All 128 columns of the lane to registers, then the accumulator is
+            // released: the next tile's MMAs wait for the reads alone.
+            uint32_t acc[4][32];
+            if (__any_sync(kFull, mine)) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        out[j] = bf16x2(a.alpha * __uint_as_float(x[2 * j]), a.alpha * __uint_as_float(x[2 * j + 1]));
-                        out[16 + j] = bf16x2(a.alpha * __uint_as_float(y[2 * j]), a.alpha * __uint_as_float(y[2 * j + 1]));
-                    }
-                    if (a.vec32_ok && n0 + 64 <= a.N) {
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld_32x32b_x32(t_lane + 32 * c, acc[c]);
+                tmem_ld_wait(acc[0], acc[1]);
+                tmem_ld_wait(acc[2], acc[3]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader)
+                    mbar_arrive(acc_empty);
+                else
+                    mbar_arrive_cluster_relaxed(lead_empty);
+            }
+            if constexpr (!GATED) {
+                const int n0 = tl.q * 256 + half * 128;
+                const int first = r - lane;
+                if (a.tma_ok && first + 32 <= tl.end) {
+                    // The warp's 32 rows are all the group's: two boxes of 32
+                    // rows x 64 columns through shared memory (128-byte
+                    // swizzle), stored by TMA.  A thread's own 32-byte stores
+                    // touch a line each, and 64 KB of them per tile hold up
+                    // the MMA warp's barrier polls in the same queue.
+                    uint8_t *buf = stage_out + (half * 4 + quarter) * kOutBoxBytes;
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            st_global_v8(d + 2 * j, out[j], out[j + 1], out[j + 2], out[j + 3], out[j + 4], out[j + 5],
-                                         out[j + 6], out[j + 7]);
-                    } else {
+                    for (int c = 0; c < 2; ++c) {
+                        if (n0 + 64 * c >= a.N)
+                            break;
+                        uint32_t out[2][16];
+                        round_bf16(a, acc[2 * c], out[0]);
+                        round_bf16(a, acc[2 * c + 1], out[1]);
+                        if (lane == 0)
+                            bulk_wait_read();
+                        __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 32; j += 4) {
-                            if (a.vec_ok && n0 + 2 * j + 8 <= a.N) {
-                                *reinterpret_cast<uint4 *>(d + 2 * j) =
-                                    make_uint4(out[j], out[j + 1], out[j + 2], out[j + 3]);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    if (n0 + 2 * j + i < a.N)
-                                        d[2 * j + i] = static_cast<uint16_t>(out[j + i / 2] >> (16 * (i & 1)));
-                            }
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                                make_uint4(out[j / 4][4 * (j % 4)], out[j / 4][4 * (j % 4) + 1],
+                                           out[j / 4][4 * (j % 4) + 2], out[j / 4][4 * (j % 4) + 3]);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store_2d(&maps.D, buf, n0 + 64 * c, first);
+                            bulk_commit();
                         }
                     }
+                } else if (mine) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        store_bf16(a, r, n0 + 32 * c, acc[c]);
+                }
+            } else if (mine) {
+                const int64_t block = static_cast<int64_t>(tl.sfa + row / 128) * (sf_groups(a.N) * kSfAtomBytes);
+                store_gated<static_cast<QuantFmt>(OUT)>(a, r, row & 127, block, tl.q * 128 + half * 64, acc[0], acc[1],
+                                                        acc[2], acc[3]);
+            }
+        }
+        if (!GATED && lane == 0)
+            bulk_wait();
+    } else {
+        give_registers();
+        if (warp == 4 || warp == 6 || warp == 7) {
+            // ------------------------------------------------------ producers --
+            if (lane == 0) {
+                const int role = warp == 4 ? 0 : warp - 5;   // 0: A, 1: B, 2: scales
+                const uint64_t keep = l2_policy_evict_last();
+                const uint64_t once = l2_policy_evict_first();
+                int stage = 0;
+                uint32_t phase = 0;
+                int issued = 0;
+                bool stop = false;
+                for (int t = pair; t < tiles && !stop; t += pairs) {
+                    const Tile tl = tile_at(table, t);
+                    const int arow = tl.row0 + static_cast<int>(rank) * 128;
+                    const bool rows_here = arow < tl.end;
+                    const bool few = tl.end - arow <= 32;
+                    // A group of one row tile reads its weights once.
+                    const uint64_t pol_b = tl.single ? once : keep;
+                    const uint32_t unit = role == 0   ? (!rows_here ? 0 : few ? 32 * 128 : Cf::A_BYTES)
+                                          : role == 1 ? Cf::B_BYTES
+                                                      : Cf::SFB_BYTES + (rows_here ? Cf::SFA_BYTES : 0);
+                    for (int kt = 0; kt < a.kt; ++kt) {
+                        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_limit, &g_status)) {
+                            stop = true;
+                            break;
+                        }
+                        uint8_t *st = smem + stage * Cf::STAGE_BYTES;
+                        uint8_t *sf = st + Cf::A_BYTES + Cf::B_BYTES;
+                        mbar_arrive_expect_tx(&full[stage], unit);
+                        if (role == 0) {
+                            if (rows_here)
+                                tma_load_2d(st, few ? &maps.A32 : &maps.A, &full[stage], kt * 128, arow, keep);
+                        } else if (role == 1) {
+                            // Plain: 128 rows of B.  Gated: 64 gate rows and the
+                            // same 64 up rows (the map's third dimension).
+                            const int n = GATED ? tl.q * 128 + static_cast<int>(rank) * 64
+                                                : tl.q * 256 + static_cast<int>(rank) * 128;
+                            tma_load_4d(st + Cf::A_BYTES, &maps.B, &full[stage], kt * 128, n, 0, tl.e, pol_b);
+                        } else {
+                            if (rows_here)
+                                tma_load_3d(sf, &maps.SA, &full[stage], 0, G * kt, tl.sfa + static_cast<int>(rank), keep);
+                            // Plain: two 128-row blocks of the expert.  Gated: the
+                            // block of the gate rows and the block of the up rows.
+                            tma_load_4d(sf + Cf::SFA_BYTES, &maps.SB, &full[stage], 0, G * kt,
+                                        GATED ? tl.q : 2 * tl.q, GATED ? 2 * tl.e : tl.e, pol_b);
+                        }
+                        ++issued;
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+                if (*abort_flag) {
+                    // Let the copies already issued land before the CTA exits.
+                    for (int i = max(0, issued - STAGES); i < issued; ++i)
+                        mbar_wait_drain(&full[i % STAGES], (i / STAGES) & 1u, a.wait_limit);
+                }
+            }
+        } else if (warp >= 12) {
+            // -------------------------------------------- scale writers --
+            // Line `lane` of an atom: rows lane, lane + 32, lane + 64, lane + 96 of
+            // its 128-row block, a word of four scales each; the four warps write
+            // the four lane quarters' replicas.
+            const int quarter = warp & 3;
+            const uint32_t t_q = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + Cf::ACC_COLS;
+            const uint32_t lead_ready = map_to_rank(smem_addr(&sf_ready[0]), 0);
+            const int my_tiles = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
+            const int total = my_tiles * a.kt;
+            int stage = 0;
+            uint32_t phase = 0;
+            for (int i = 0; i < total; ++i) {
+                bool ok = mbar_wait(&full[stage], phase, abort_flag, a.wait_limit, &g_status);
+                if (!__all_sync(kFull, ok))
+                    break;
+                const uint8_t *sf = smem + stage * Cf::STAGE_BYTES + Cf::A_BYTES + Cf::B_BYTES;
+                uint32_t wa[4 * G], wb[8 * G];
+    #pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(sf + g * kSfAtomBytes + 16 * lane);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(sf + Cf::SFA_BYTES + g * kSfAtomBytes + 16 * lane);
+                    const uint4 y =
+                        *reinterpret_cast<const uint4 *>(sf + Cf::SFA_BYTES + (G + g) * kSfAtomBytes + 16 * lane);
+                    wa[4 * g] = v.x;
+                    wa[4 * g + 1] = v.y;
+                    wa[4 * g + 2] = v.z;
+                    wa[4 * g + 3] = v.w;
+                    // Word j of block b of atom g -> column 8 g + 4 b + j.  Plain:
+                    // blocks x, y.  Gated: the tile's first 128 rows are gate rows
+                    // 0-63 and up rows 0-63 (words 0, 1 of either block).
+                    uint32_t *w = wb + 8 * g;
+                    w[0] = x.x;
+                    w[1] = x.y;
+                    w[2] = GATED ? y.x : x.z;
+                    w[3] = GATED ? y.y : x.w;
+                    w[4] = GATED ? x.z : y.x;
+                    w[5] = GATED ? x.w : y.y;
+                    w[6] = y.z;
+                    w[7] = y.w;
+                }
+                const uint32_t slot = t_q + stage * Cf::SF_COLS;
+                if constexpr (G == 2) {
+                    tmem_st_32x32b_x8(slot, wa);
+                    tmem_st_32x32b_x16(slot + Cf::SF_COLS_A, wb);
                 } else {
-                    constexpr QuantFmt Q = static_cast<QuantFmt>(OUT);
-                    constexpr int W = QuantTraits<Q>::kWords;
-                    const int f0 = tl.q * 128 + half * 64 + 32 * c;
-                    uint8_t *s = a.SH + static_cast<int64_t>(tl.sfa + row / 128) *
-                                            (sf_groups(a.N) * kSfAtomBytes) + sf_byte(row & 127, f0 / 32);
-                    if (f0 >= a.N) {
-                        // The odd block's partner in the same MMA of the next
-                        // product: any finite scale serves its zero codes.
-                        if (c == 1 && f0 - 32 < a.N)
-                            *s = 0x7F;
-                        continue;
+                    tmem_st_32x32b_x4(slot, wa);
+                    tmem_st_32x32b_x8(slot + Cf::SF_COLS_A, wb);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(&sf_ready[stage]);
+                    else
+                        mbar_arrive_cluster_relaxed(lead_ready + static_cast<uint32_t>(stage * sizeof(uint64_t)));
+                }
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        } else if (warp == 5) {
+            // ------------------------------------------------ MMA (leader) --
+            if (leader) {
+                const uint32_t idesc = BYTES8 ? a.idesc8 : idesc_mxf4(256, 256);
+                int stage = 0;
+                uint32_t phase = 0, acc_phase = 0;
+                bool stop = false;
+                for (int t = pair; t < tiles && !stop; t += pairs) {
+                    if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, a.wait_limit, &g_status))
+                        break;
+                    tc_fence_after();
+                    for (int kt = 0; kt < a.kt; ++kt) {
+                        // sf_ready completes after the scale writers of both CTAs
+                        // saw the stage's bytes land.
+                        if (!mbar_wait(&sf_ready[stage], phase, abort_flag, a.wait_limit, &g_status)) {
+                            stop = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t sfa = tmem + Cf::ACC_COLS + stage * Cf::SF_COLS;
+                        const uint32_t sfb = sfa + Cf::SF_COLS_A;
+                        const uint32_t st = smem_addr(smem + stage * Cf::STAGE_BYTES);
+                        const uint64_t adesc = sdesc_kmajor_sw128(st);
+                        const uint64_t bdesc = sdesc_kmajor_sw128(st + Cf::A_BYTES);
+                        const int left = a.K - kt * Cf::K_STAGE;      // K elements of this stage
+    #pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (j * Cf::K_MMA >= left)
+                                break;
+                            const uint32_t acc = (kt > 0 || j > 0) ? 1u : 0u;
+                            if constexpr (BYTES8) {
+                                mma_mxf8_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_sf_ids(idesc, j, j), sfa, sfb,
+                                                    acc);
+                            } else {
+                                const uint32_t id = (j & 1) * 2;
+                                mma_mxf4_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_sf_ids(idesc, id, id),
+                                                    sfa + (j >> 1) * 4, sfb + (j >> 1) * 8, acc);
+                            }
+                        }
+                        mma_commit_pair_elect(&empty[stage], static_cast<uint16_t>(3u));
+                        if (++stage == STAGES) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
                     }
-                    float h[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float g = a.alpha * __uint_as_float(x[i]);
-                        const float u = a.alpha * __uint_as_float(y[i]);
-                        h[i] = __fdividef(g, 1.0f + __expf(-g)) * u;
-                    }
-                    uint32_t out[W];
-                    const uint32_t code = quantize_block<Q>(h, out);
-                    uint4 *q = reinterpret_cast<uint4 *>(a.H + static_cast<int64_t>(r) * a.ldh +
-                                                         (Q == QuantFmt::kE2M1 ? f0 / 2 : f0));
-#pragma unroll
-                    for (int w = 0; w < W; w += 4)
-                        q[w / 4] = make_uint4(out[w], out[w + 1], out[w + 2], out[w + 3]);
-                    *s = static_cast<uint8_t>(code);
+                    if (!stop)
+                        mma_commit_pair_elect(acc_full, static_cast<uint16_t>(3u));
+                    acc_phase ^= 1u;
+                }
+                if (*abort_flag) {
+                    mma_commit_pair_elect(drain, static_cast<uint16_t>(1u));
+                    mbar_wait_drain(drain, 0, a.wait_limit);
                 }
             }
         }
@@ -545,7 +666,7 @@ __global__ void __launch_bounds__(512, 1)
 template <bool BYTES8, int OUT>
 cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t stream)
 {
-    using Cf = GroupedCfg<BYTES8>;
+    using Cf = GroupedCfg<BYTES8, (OUT >= 0)>;
     auto kern = grouped_pair<BYTES8, OUT>;
     static std::atomic<int> max_clusters[64];   // per device; 0 = not yet queried
     int dev = 0;
@@ -568,6 +689,13 @@ cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t 
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES);
         if (e != cudaSuccess)
             return e;
+        // The register split needs the registers of a 128-register launch.
+        cudaFuncAttributes attributes;
+        e = cudaFuncGetAttributes(&attributes, kern);
+        if (e != cudaSuccess)
+            return e;
+        if (attributes.numRegs <= 120)
+            return cudaErrorInvalidConfiguration;
         // Persistent: every cluster must be resident at once.
         cfg.gridDim = dim3(2);
         e = cudaOccupancyMaxActiveClusters(&limit, kern, &cfg);

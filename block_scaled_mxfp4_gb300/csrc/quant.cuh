@@ -88,18 +88,25 @@ struct QuantTraits {
     static constexpr int kWords = Q == QuantFmt::kE2M1 ? 4 : 8;   // 32-bit words of codes per block
 };
 
+// Largest magnitude of three; NaN if any is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
+{
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // One block: 32 values -> codes (element order) and the E8M0 scale code.
 template <QuantFmt Q>
 __device__ __forceinline__ uint32_t quantize_block(const float (&x)[32], uint32_t (&out)[QuantTraits<Q>::kWords])
 {
     float amax = 0.0f;
-    bool finite = true;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        const float a = fabsf(x[i]);
-        finite = finite && a <= 3.402823466e38f;     // false for NaN too, which fmaxf drops
-        amax = fmaxf(amax, a);
-    }
+    for (int i = 0; i < 32; i += 2)
+        amax = max_abs3(amax, x[i], x[i + 1]);
+    const bool finite = amax <= 3.402823466e38f;     // not for infinities and NaN
+    if (!finite)
+        amax = 0.0f;
     const int s = Q == QuantFmt::kE2M1 ? block_exponent(amax) : block_exponent8(amax, Q == QuantFmt::kE4M3 ? 8 : 15);
     const float inv = exp2_neg(s);
 #pragma unroll
