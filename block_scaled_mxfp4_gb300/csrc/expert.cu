@@ -597,9 +597,11 @@ template <int VPT, int JC>
 __global__ void __launch_bounds__(kCombineThreads, VPT <= 2 ? 2 : 1) combine_kernel(const __grid_constant__ CombineArgs a)
 {
     __shared__ float slots[4][kCombineThreads / 32];
-    pdl_wait_prerequisites();
+    if (!a.early)
+        pdl_wait_prerequisites();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
+    bool waited = !a.early;
     int parity = 0;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 2) {
         float b[VPT][8];
@@ -623,6 +625,10 @@ __global__ void __launch_bounds__(kCombineThreads, VPT <= 2 ? 2 : 1) combine_ker
                 const int64_t at = static_cast<int64_t>(t) * a.k + j0 + j;
                 row[j] = j0 + j < a.k ? (a.slot_row ? a.slot_row[at] : t) : -1;
                 g[j] = j0 + j < a.k && a.gates ? a.gates[at] : 1.0f;
+            }
+            if (!waited) {
+                pdl_wait_prerequisites();
+                waited = true;
             }
 #pragma unroll
             for (int j = 0; j < JC; ++j)

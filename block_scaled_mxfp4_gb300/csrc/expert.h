@@ -89,6 +89,7 @@ struct CombineArgs {
     float res_scale, out_scale, eps;
     int T, N;
     int vec;                    // every row takes aligned 16-byte accesses
+    int early;                  // all but Y may be read before the preceding grid ends
 };
 cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream);
 
@@ -108,6 +109,9 @@ struct GroupedArgs {
     int64_t ldh;
     uint8_t *SH;                // grouped scale layout over N
     uint32_t idesc8;            // byte formats: instruction descriptor
+    int early;                  // offsets, B and its scales may be read before the preceding
+                                // grid ends: it is a kernel of the same call, which waited
+                                // for the work before the call
     float *partials;            // workspace of split tiles
     unsigned long long *tile_count;
     uint32_t epoch;

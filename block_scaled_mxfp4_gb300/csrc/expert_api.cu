@@ -51,6 +51,7 @@ struct Product {
     int out;
     void *ws;
     size_t ws_bytes;
+    bool early;             // GroupedArgs::early
 };
 
 int check_product(const Product &p)
@@ -138,6 +139,7 @@ int run_product(const Product &p, int sms, cudaStream_t stream)
     a.kt = (p.K + stage - 1) / stage;
     a.nt = gated ? (p.N + 127) / 128 : (p.N + 255) / 256;
     a.alpha = p.alpha;
+    a.early = p.early ? 1 : 0;
     if (gated) {
         a.H = static_cast<uint8_t *>(p.D);
         a.ldh = p.out == 0 ? p.ldd / 2 : p.ldd;
@@ -218,6 +220,37 @@ int quantize_entry(void *Q, int64_t ldq, void *S, const void *X, int64_t ldx, in
     a.rows = rows;
     a.fmt = fmt;
     return status_of(launch_group_quantize(a, sms, static_cast<cudaStream_t>(stream)));
+}
+
+int run_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *Y, int64_t ldy, int rows, const int *slot_row,
+                const float *gates, int k, const void *resid, int64_t ldr, const void *w_post, const void *w_pre,
+                float res_scale, float out_scale, float eps, int T, int N, bool early, int sms, void *stream)
+{
+    CombineArgs a;
+    a.H = static_cast<uint16_t *>(H);
+    a.ldh = ldh;
+    a.Nrm = static_cast<uint16_t *>(Nrm);
+    a.ldn = ldn;
+    a.Y = static_cast<const uint16_t *>(Y);
+    a.ldy = ldy;
+    a.rows = rows;
+    a.slot_row = slot_row;
+    a.gates = gates;
+    a.k = k;
+    a.resid = static_cast<const uint16_t *>(resid);
+    a.ldr = ldr;
+    a.w_post = static_cast<const uint16_t *>(w_post);
+    a.w_pre = static_cast<const uint16_t *>(w_pre);
+    a.res_scale = res_scale;
+    a.out_scale = out_scale;
+    a.eps = eps;
+    a.T = T;
+    a.N = N;
+    auto rows_ok = [](const void *p, int64_t ld) { return !p || (aligned(p, 16) && (ld % 8) == 0); };
+    a.early = early ? 1 : 0;
+    a.vec = rows_ok(H, ldh) && rows_ok(Nrm, ldn) && rows_ok(Y, ldy) && rows_ok(resid, ldr) && rows_ok(w_post, 0) &&
+            rows_ok(w_pre, 0);
+    return status_of(launch_combine(a, sms, static_cast<cudaStream_t>(stream)));
 }
 
 // Workspace of mxfp4_moe_ffn: what each step leaves for the next.
@@ -352,7 +385,7 @@ int mxfp4_grouped_gemm(void *D, int64_t ldd, const void *A, int64_t lda, const v
                        float alpha, void *workspace, size_t workspace_bytes, void *stream)
 {
     const Product p{D, ldd, nullptr, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, N, K, alpha,
-                    false, 0, 0, -1, workspace, workspace_bytes};
+                    false, 0, 0, -1, workspace, workspace_bytes, false};
     return product_entry(p, stream);
 }
 
@@ -361,7 +394,7 @@ int mxfp8_grouped_gemm(void *D, int64_t ldd, const void *A, int64_t lda, const v
                        int fmt_a, int fmt_b, float alpha, void *workspace, size_t workspace_bytes, void *stream)
 {
     const Product p{D, ldd, nullptr, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, N, K, alpha,
-                    true, fmt_a, fmt_b, -1, workspace, workspace_bytes};
+                    true, fmt_a, fmt_b, -1, workspace, workspace_bytes, false};
     return product_entry(p, stream);
 }
 
@@ -370,7 +403,7 @@ int mxfp4_grouped_swiglu(void *H, int64_t ldh, void *SH, const void *A, int64_t 
                          int F, int K, float alpha, void *workspace, size_t workspace_bytes, void *stream)
 {
     const Product p{H, ldh, SH, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, F, K, alpha,
-                    false, 0, 0, 0, workspace, workspace_bytes};
+                    false, 0, 0, 0, workspace, workspace_bytes, false};
     return product_entry(p, stream);
 }
 
@@ -382,7 +415,7 @@ int mxfp8_grouped_swiglu(void *H, int64_t ldh, void *SH, const void *A, int64_t 
     if (fmt_h != MXFP8_E4M3 && fmt_h != MXFP8_E5M2)
         return MXFP4_ERR_INVALID_ARG;
     const Product p{H, ldh, SH, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, F, K, alpha,
-                    true, fmt_a, fmt_b, 1 + fmt_h, workspace, workspace_bytes};
+                    true, fmt_a, fmt_b, 1 + fmt_h, workspace, workspace_bytes, false};
     return product_entry(p, stream);
 }
 
@@ -406,30 +439,8 @@ int mxfp4_moe_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *
         return st;
     if (T == 0)
         return MXFP4_OK;
-    CombineArgs a;
-    a.H = static_cast<uint16_t *>(H);
-    a.ldh = ldh;
-    a.Nrm = static_cast<uint16_t *>(Nrm);
-    a.ldn = ldn;
-    a.Y = static_cast<const uint16_t *>(Y);
-    a.ldy = ldy;
-    a.rows = rows;
-    a.slot_row = slot_row;
-    a.gates = gates;
-    a.k = k;
-    a.resid = static_cast<const uint16_t *>(resid);
-    a.ldr = ldr;
-    a.w_post = static_cast<const uint16_t *>(w_post);
-    a.w_pre = static_cast<const uint16_t *>(w_pre);
-    a.res_scale = res_scale;
-    a.out_scale = out_scale;
-    a.eps = eps;
-    a.T = T;
-    a.N = N;
-    auto rows_ok = [](const void *p, int64_t ld) { return !p || (aligned(p, 16) && (ld % 8) == 0); };
-    a.vec = rows_ok(H, ldh) && rows_ok(Nrm, ldn) && rows_ok(Y, ldy) && rows_ok(resid, ldr) && rows_ok(w_post, 0) &&
-            rows_ok(w_pre, 0);
-    return status_of(launch_combine(a, sms, static_cast<cudaStream_t>(stream)));
+    return run_combine(H, ldh, Nrm, ldn, Y, ldy, rows, slot_row, gates, k, resid, ldr, w_post, w_pre, res_scale,
+                       out_scale, eps, T, N, false, sms, stream);
 }
 
 size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F)
@@ -464,9 +475,9 @@ int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, i
     const size_t ws_bytes = l.total - l.ws;
     // Every step's arguments are checked before the first one is enqueued.
     const Product up{w + l.h, F, w + l.sh, w + l.q, K, w + l.sq, B1, ldb1, 2 * static_cast<int64_t>(F) * ldb1, SB1,
-                     offsets, E, rows, F, K, 1.0f, false, 0, 0, 0, w + l.ws, ws_bytes};
+                     offsets, E, rows, F, K, 1.0f, false, 0, 0, 0, w + l.ws, ws_bytes, true};
     const Product down{w + l.y, K, nullptr, w + l.h, F, w + l.sh, B2, ldb2, static_cast<int64_t>(K) * ldb2, SB2,
-                       offsets, E, rows, K, F, 1.0f, false, 0, 0, -1, w + l.ws, ws_bytes};
+                       offsets, E, rows, K, F, 1.0f, false, 0, 0, -1, w + l.ws, ws_bytes, true};
     int st = check_product(up);
     if (st == MXFP4_OK)
         st = check_product(down);
@@ -476,14 +487,16 @@ int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, i
     st = check_current_device(&sms);
     if (st != MXFP4_OK || T == 0)
         return st;
+    // The quantiser waits for the work before the call, so that the steps after
+    // it may read the call's own inputs before their predecessor has ended.
     st = mxfp4_group_quantize(w + l.q, K, w + l.sq, X, ldx, T, K, slot_row, ids, k, offsets, E, rows, stream);
     if (st == MXFP4_OK)
         st = run_product(up, sms, static_cast<cudaStream_t>(stream));
     if (st == MXFP4_OK)
         st = run_product(down, sms, static_cast<cudaStream_t>(stream));
     if (st == MXFP4_OK)
-        st = mxfp4_moe_combine(H, ldh, Nrm, ldn, w + l.y, K, rows, slot_row, gates, k, resid, ldr, w_post, w_pre,
-                               res_scale, out_scale, eps, T, K, stream);
+        st = run_combine(H, ldh, Nrm, ldn, w + l.y, K, rows, slot_row, gates, k, resid, ldr, w_post, w_pre, res_scale,
+                         out_scale, eps, T, K, true, sms, stream);
     return st;
 }
 

@@ -26,9 +26,9 @@
 // shared memory), row tiles fastest, so tiles that run together share weight
 // panels in L2.  Empty groups have no tile and their weights are not read.
 //
-// Roles per CTA (512 threads): warps 4, 6, 7 load A rows, B rows and the scale
-// atoms by TMA (a thread waits out each copy it issues, hence one thread per
-// stream); warps 12-15 move each stage's scale lines into tensor memory; warp 5
+// Roles per CTA (512 threads): warps 4, 6, 7 load A rows with their scale atoms,
+// B rows and B's scale atoms by TMA (a thread waits out each copy it issues,
+// hence several); warps 12-15 move each stage's scale lines into tensor memory; warp 5
 // of the leading CTA issues the MMAs; warps 0-3 and 8-11 are the epilogue, for
 // accumulator columns [0, 128) and [128, 256).  A rows come from a 2-D map, so a
 // tile may start at any row; rows past the group's end are loaded and computed
@@ -381,8 +381,10 @@ __global__ void __launch_bounds__(512, 1)
         prefetch_tensormap(&maps.B);
         prefetch_tensormap(&maps.SB);
     }
-    // The offsets may come from the work before this grid, like everything else.
-    pdl_wait_prerequisites();
+    // Offsets and weights may come from the work before this grid, like
+    // everything else; with a.early only the rows and their scales do.
+    if (!a.early)
+        pdl_wait_prerequisites();
     build_tables(a, tab_off, tab_base);
     tc_fence_before();
     cluster_sync();                          // barriers of both CTAs initialised
@@ -396,6 +398,8 @@ __global__ void __launch_bounds__(512, 1)
     if (warp < 4 || (warp >= 8 && warp < 12)) {
         take_registers();
         // ------------------------------------------------------ epilogue --
+        if (a.early)
+            pdl_wait_prerequisites();
         const int quarter = warp & 3;
         const int half = warp >> 3;
         const int row = static_cast<int>(rank) * 128 + quarter * 32 + lane;
@@ -479,7 +483,9 @@ __global__ void __launch_bounds__(512, 1)
         if (warp == 4 || warp == 6 || warp == 7) {
             // ------------------------------------------------------ producers --
             if (lane == 0) {
-                const int role = warp == 4 ? 0 : warp - 5;   // 0: A, 1: B, 2: scales
+                const int role = warp == 4 ? 0 : warp - 5;   // 0: A and its scales, 1: B, 2: B's scales
+                if (role == 0 && a.early)
+                    pdl_wait_prerequisites();
                 const uint64_t keep = l2_policy_evict_last();
                 const uint64_t once = l2_policy_evict_first();
                 int stage = 0;
@@ -493,9 +499,9 @@ __global__ void __launch_bounds__(512, 1)
                     const bool few = tl.end - arow <= 32;
                     // A group of one row tile reads its weights once.
                     const uint64_t pol_b = tl.single ? once : keep;
-                    const uint32_t unit = role == 0   ? (!rows_here ? 0 : few ? 32 * 128 : Cf::A_BYTES)
+                    const uint32_t unit = role == 0   ? (!rows_here ? 0 : (few ? 32 * 128 : Cf::A_BYTES) + Cf::SFA_BYTES)
                                           : role == 1 ? Cf::B_BYTES
-                                                      : Cf::SFB_BYTES + (rows_here ? Cf::SFA_BYTES : 0);
+                                                      : Cf::SFB_BYTES;
                     for (int kt = 0; kt < a.kt; ++kt) {
                         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_limit, &g_status)) {
                             stop = true;
@@ -505,8 +511,10 @@ __global__ void __launch_bounds__(512, 1)
                         uint8_t *sf = st + Cf::A_BYTES + Cf::B_BYTES;
                         mbar_arrive_expect_tx(&full[stage], unit);
                         if (role == 0) {
-                            if (rows_here)
+                            if (rows_here) {
                                 tma_load_2d(st, few ? &maps.A32 : &maps.A, &full[stage], kt * 128, arow, keep);
+                                tma_load_3d(sf, &maps.SA, &full[stage], 0, G * kt, tl.sfa + static_cast<int>(rank), keep);
+                            }
                         } else if (role == 1) {
                             // Plain: 128 rows of B.  Gated: 64 gate rows and the
                             // same 64 up rows (the map's third dimension).
@@ -514,8 +522,6 @@ __global__ void __launch_bounds__(512, 1)
                                                 : tl.q * 256 + static_cast<int>(rank) * 128;
                             tma_load_4d(st + Cf::A_BYTES, &maps.B, &full[stage], kt * 128, n, 0, tl.e, pol_b);
                         } else {
-                            if (rows_here)
-                                tma_load_3d(sf, &maps.SA, &full[stage], 0, G * kt, tl.sfa + static_cast<int>(rank), keep);
                             // Plain: two 128-row blocks of the expert.  Gated: the
                             // block of the gate rows and the block of the up rows.
                             tma_load_4d(sf + Cf::SFA_BYTES, &maps.SB, &full[stage], 0, G * kt,
