@@ -1155,11 +1155,12 @@ int mxfp4_device_status(int *status, int reset)
     int st = check_device();
     if (st != MXFP4_OK)
         return st;
-    int grouped = 0;
-    if (read_device_status(status, reset) != cudaSuccess || read_grouped_status(&grouped, reset) != cudaSuccess)
+    int grouped = 0, expert = 0;
+    if (read_device_status(status, reset) != cudaSuccess || read_grouped_status(&grouped, reset) != cudaSuccess ||
+        read_expert_status(&expert, reset) != cudaSuccess)
         return MXFP4_ERR_CUDA;
     if (*status == MXFP4_OK)
-        *status = grouped;
+        *status = grouped != MXFP4_OK ? grouped : expert;
     return MXFP4_OK;
 }
 

@@ -89,8 +89,10 @@ struct CombineArgs {
     float res_scale, out_scale, eps;
     int T, N;
     int vec;                    // every row takes aligned 16-byte accesses
+    long long wait_limit;
     int early;                  // all but Y may be read before the preceding grid ends
 };
+cudaError_t read_expert_status(int *status, int reset);
 cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream);
 
 // Arguments of one grouped product (grouped.cu).

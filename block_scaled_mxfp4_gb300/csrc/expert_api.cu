@@ -248,6 +248,7 @@ int run_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *Y, int
     a.N = N;
     auto rows_ok = [](const void *p, int64_t ld) { return !p || (aligned(p, 16) && (ld % 8) == 0); };
     a.early = early ? 1 : 0;
+    a.wait_limit = current_wait_limit();
     a.vec = rows_ok(H, ldh) && rows_ok(Nrm, ldn) && rows_ok(Y, ldy) && rows_ok(resid, ldr) && rows_ok(w_post, 0) &&
             rows_ok(w_pre, 0);
     return status_of(launch_combine(a, sms, static_cast<cudaStream_t>(stream)));

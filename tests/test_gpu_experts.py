@@ -578,8 +578,17 @@ def test_combine_options():
     check_combine(20, 1, 768, slots=False)
 
 
-def test_combine_in_place_on_the_residual():
-    T, k, N = 50, 2, 1024
+@pytest.mark.parametrize("T,k,N,kw", [(700, 3, 2048, {}), (615, 2, 4096, dict(skip=0.4, rows=2000)),
+                                      (640, 1, 8200, dict(pad=8)), (609, 2, 2064, dict(resid=False, norm=False)),
+                                      (620, 2, 2048, dict(post=False, pre=False, h_out=False)), (611, 1, 3000, dict(slots=False))])
+def test_combine_many_long_rows(T, k, N, kw):
+    """The form that streams rows ahead of the token at work."""
+    check_combine(T, k, N, **kw)
+
+
+@pytest.mark.parametrize("T,N", [(50, 1024), (900, 2048)])
+def test_combine_in_place_on_the_residual(T, N):
+    k = 2
     rng = np.random.default_rng(1)
     Y, Yv = bf16(rng.normal(size=(T * k, N)))
     R, Rv = bf16(rng.normal(size=(T, N)))
