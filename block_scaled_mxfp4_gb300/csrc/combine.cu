@@ -1,0 +1,481 @@
+// Gated join of a token's expert rows with the norms around the residual stream.
+#include <cuda_bf16.h>
+
+#include "expert.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace mxfp4 {
+
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+
+__device__ int g_status = 0;                     // bounded waits that ran out
+
+// ------------------------------------------------------------------- join --
+//
+//   b = sum_j gates[t, j] Y[slot_row[t, j]]          (fp32, slots in order)
+//   b = b rsqrt(mean b^2 + eps) w_post               with w_post
+//   h = res_scale resid[t] + out_scale b             -> H, one rounding
+//   n = h rsqrt(mean h^2 + eps) w_pre                -> Nrm, one rounding, from the fp32 h
+//
+// One block per token (grid-stride), the row in registers between the two
+// sums, so that every input is read once.
+
+constexpr int kCombineThreads = 512;
+constexpr int kCombineMaxVec = 8;                // 8-element vectors of one thread
+
+__device__ __forceinline__ void store8(uint16_t *p, int n, int N, int vec, const float (&x)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    if (vec && n + 8 <= N) {
+        *reinterpret_cast<uint4 *>(p + n) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (n + i < N)
+                p[n + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// Sum over the block; every thread gets it.  The two slots alternate so that
+// the next call's writes do not meet this one's reads.
+__device__ __forceinline__ float block_sum(float v, float *slot)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        v += __shfl_xor_sync(kFull, v, d);
+    if ((threadIdx.x & 31) == 0)
+        slot[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float s = 0.0f;
+    const int warps = blockDim.x >> 5;
+    for (int w = 0; w < warps; ++w)
+        s += slot[w];
+    return s;
+}
+
+// Raw bf16 pairs of 8 elements, zeros past N.
+__device__ __forceinline__ uint4 raw8(const uint16_t *p, int n, int N, int vec)
+{
+    if (vec && n + 8 <= N)
+        return *reinterpret_cast<const uint4 *>(p + n);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (n + i < N)
+            w[i / 2] |= static_cast<uint32_t>(p[n + i]) << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float pick8(const uint4 &v, int i)
+{
+    const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
+    return i & 1 ? bf16_hi(w) : bf16_lo(w);
+}
+
+// VPT 8-element vectors per thread, JC slots' rows in flight together.
+template <int VPT, int JC>
+__global__ void __launch_bounds__(kCombineThreads, VPT <= 2 ? 2 : 1) combine_kernel(const __grid_constant__ CombineArgs a)
+{
+    __shared__ float slots[4][kCombineThreads / 32];
+    if (!a.early)
+        pdl_wait_prerequisites();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    bool waited = !a.early;
+    int parity = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 2) {
+        float b[VPT][8];
+        uint4 res[VPT];
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int n = (v * blockDim.x + threadIdx.x) * 8;
+            res[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (VPT < 8 && a.resid && n < a.N)             // early, where registers allow
+                res[v] = raw8(a.resid + static_cast<int64_t>(t) * a.ldr, n, a.N, a.vec);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                b[v][i] = 0.0f;
+        }
+        for (int j0 = 0; j0 < a.k; j0 += JC) {
+            int row[JC];
+            float g[JC];
+            uint4 y[JC][VPT];
+#pragma unroll
+            for (int j = 0; j < JC; ++j) {
+                const int64_t at = static_cast<int64_t>(t) * a.k + j0 + j;
+                row[j] = j0 + j < a.k ? (a.slot_row ? a.slot_row[at] : t) : -1;
+                g[j] = j0 + j < a.k && a.gates ? a.gates[at] : 1.0f;
+            }
+            if (!waited) {
+                pdl_wait_prerequisites();
+                waited = true;
+            }
+#pragma unroll
+            for (int j = 0; j < JC; ++j)
+#pragma unroll
+                for (int v = 0; v < VPT; ++v) {
+                    const int n = (v * blockDim.x + threadIdx.x) * 8;
+                    if (row[j] >= 0 && row[j] < a.rows && n < a.N)
+                        y[j][v] = raw8(a.Y + static_cast<int64_t>(row[j]) * a.ldy, n, a.N, a.vec);
+                }
+#pragma unroll
+            for (int j = 0; j < JC; ++j) {
+                if (row[j] < 0 || row[j] >= a.rows)
+                    continue;                              // block-uniform
+#pragma unroll
+                for (int v = 0; v < VPT; ++v)
+                    if ((v * blockDim.x + threadIdx.x) * 8 < a.N) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            b[v][i] = fmaf(g[j], pick8(y[j][v], i), b[v][i]);
+                    }
+            }
+        }
+        if (a.w_post) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    ss = fmaf(b[v][i], b[v][i], ss);
+            ss = block_sum(ss, slots[parity]);
+            const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int n = (v * blockDim.x + threadIdx.x) * 8;
+                if (n < a.N) {
+                    const uint4 w = raw8(a.w_post, n, a.N, a.vec);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        b[v][i] = b[v][i] * r * pick8(w, i);
+                }
+            }
+        }
+        float ss = 0.0f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int n = (v * blockDim.x + threadIdx.x) * 8;
+            if (n < a.N) {
+                if (VPT == 8 && a.resid)
+                    res[v] = raw8(a.resid + static_cast<int64_t>(t) * a.ldr, n, a.N, a.vec);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    b[v][i] = a.resid ? fmaf(a.out_scale, b[v][i], a.res_scale * pick8(res[v], i)) : a.out_scale * b[v][i];
+                    ss = fmaf(b[v][i], b[v][i], ss);
+                }
+                if (a.H)
+                    store8(a.H + static_cast<int64_t>(t) * a.ldh, n, a.N, a.vec, b[v]);
+            }
+        }
+        if (a.Nrm) {
+            ss = block_sum(ss, slots[parity + 1]);
+            const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int n = (v * blockDim.x + threadIdx.x) * 8;
+                if (n < a.N) {
+                    float y[8];
+                    if (a.w_pre) {
+                        const uint4 w = raw8(a.w_pre, n, a.N, a.vec);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = b[v][i] * r * pick8(w, i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            y[i] = b[v][i] * r;
+                    }
+                    store8(a.Nrm + static_cast<int64_t>(t) * a.ldn, n, a.N, a.vec, y);
+                }
+            }
+        }
+    }
+}
+
+// The same for long prefills, where the sums' barriers must not leave HBM
+// idle: one persistent block per SM, whose last warp streams the tokens' rows
+// (the taken rows of Y, then the residual row) into a ring of whole rows in
+// shared memory with bulk copies, as far ahead as the ring holds, while 16
+// warps work on the token at hand.  8192 tokens x 4 rows of 8192: see the
+// launcher.
+constexpr int kRingThreads = kCombineThreads + 32;
+constexpr int kRingMaxRows = 32;
+constexpr int kRingBytes = 200 * 1024;
+
+struct RingMeta {
+    uint64_t full[kRingMaxRows];
+    uint64_t empty[kRingMaxRows];
+    float gate[kRingMaxRows];
+    int last[kRingMaxRows];                      // 1: the token's last entry (its residual row, or nothing)
+    float slots[4][kCombineThreads / 32];
+    int abort_flag;
+};
+
+__device__ __forceinline__ float ring_sum(float v, float *slot)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        v += __shfl_xor_sync(kFull, v, d);
+    if ((threadIdx.x & 31) == 0)
+        slot[threadIdx.x >> 5] = v;
+    asm volatile("bar.sync 1, %0;" ::"n"(kCombineThreads) : "memory");
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kCombineThreads / 32; ++w)
+        s += slot[w];
+    return s;
+}
+
+template <int VPT>
+__global__ void __launch_bounds__(kRingThreads, 1) combine_ring_kernel(const __grid_constant__ CombineArgs a, int depth)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ RingMeta m;
+    const uint32_t row_bytes = static_cast<uint32_t>(a.N) * 2;
+    const uint32_t pitch = (row_bytes + 127u) / 128u * 128u;
+    volatile int *abort_flag = &m.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < depth; ++s) {
+            mbar_init(&m.full[s], 1);
+            mbar_init(&m.empty[s], kCombineThreads / 32);
+        }
+        m.abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait_prerequisites();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    int s = 0;
+    uint32_t phase = 0;
+    if (warp == kCombineThreads / 32) {
+        const uint64_t once = l2_policy_evict_first();
+        int issued = 0;
+        bool ok = true;
+        auto look_up = [&](int t, int &row, float &g) {
+            row = -1;
+            g = 1.0f;
+            if (t < a.T && lane < a.k) {
+                const int64_t at = static_cast<int64_t>(t) * a.k + lane;
+                row = a.slot_row ? a.slot_row[at] : t;
+                if (row >= a.rows)
+                    row = -1;
+                if (a.gates)
+                    g = a.gates[at];
+            }
+        };
+        int row, next_row;
+        float g, next_g;
+        look_up(blockIdx.x, next_row, next_g);
+        for (int t = blockIdx.x; t < a.T && ok; t += gridDim.x) {
+            row = next_row;
+            g = next_g;
+            look_up(t + gridDim.x, next_row, next_g);      // a token ahead
+            const uint32_t taken = __ballot_sync(kFull, row >= 0);
+            const int entries = __popc(taken) + 1;
+            uint32_t left = taken;
+            for (int i = 0; i < entries && ok; ++i) {
+                const bool last = left == 0u;
+                const int j = last ? 0 : __ffs(left) - 1;
+                left &= left - 1u;
+                const int r = __shfl_sync(kFull, row, j);
+                const float gate = __shfl_sync(kFull, g, j);
+                if (lane == 0) {
+                    ok = mbar_wait(&m.empty[s], phase ^ 1u, abort_flag, a.wait_limit, &g_status);
+                    if (ok) {
+                        m.gate[s] = gate;
+                        m.last[s] = last ? 1 : 0;
+                        const uint16_t *src = !last      ? a.Y + static_cast<int64_t>(r) * a.ldy
+                                              : a.resid ? a.resid + static_cast<int64_t>(t) * a.ldr
+                                                        : nullptr;
+                        mbar_arrive_expect_tx(&m.full[s], src ? row_bytes : 0u);
+                        if (src)
+                            bulk_load(ring + static_cast<size_t>(s) * pitch, src, row_bytes, &m.full[s], once);
+                    }
+                }
+                ok = __shfl_sync(kFull, ok, 0);
+                if (ok) {
+                    ++issued;
+                    if (++s == depth) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+        }
+        if (lane == 0 && *abort_flag)
+            // Let the copies already issued land before the block exits.
+            for (int i = max(0, issued - depth); i < issued; ++i)
+                mbar_wait_drain(&m.full[i % depth], (i / depth) & 1u, a.wait_limit);
+        return;
+    }
+    const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+    auto weight = [&](const uint16_t *w, int v) {
+        const int n = (v * kCombineThreads + threadIdx.x) * 8;
+        return w && n < a.N ? *reinterpret_cast<const uint4 *>(w + n) : ones;
+    };
+    constexpr bool KEEP = VPT <= 2;              // the norms' weights stay in registers
+    uint4 post[VPT], pre[VPT];
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            post[v] = weight(a.w_post, v);
+            pre[v] = weight(a.w_pre, v);
+        }
+    }
+    bool ok = true;                              // after a wait that ran out: no data, but every barrier
+    auto release = [&]() {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&m.empty[s]);
+        if (++s == depth) {
+            s = 0;
+            phase ^= 1u;
+        }
+    };
+    int parity = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 2) {
+        float b[VPT][8];
+#pragma unroll
+        for (int v = 0; v < VPT; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                b[v][i] = 0.0f;
+        for (;;) {
+            ok = __all_sync(kFull, mbar_wait(&m.full[s], phase, abort_flag, a.wait_limit, &g_status));
+            if (!ok || m.last[s])
+                break;
+            const float g = m.gate[s];
+            const uint8_t *y = ring + static_cast<size_t>(s) * pitch;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int n = (v * kCombineThreads + threadIdx.x) * 8;
+                if (n < a.N) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(y + 2 * n);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        b[v][i] = fmaf(g, pick8(x, i), b[v][i]);
+                }
+            }
+            release();
+        }
+        if (a.w_post) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int v = 0; v < VPT; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    ss = fmaf(b[v][i], b[v][i], ss);
+            ss = ring_sum(ss, m.slots[parity]);
+            const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const uint4 w = KEEP ? post[v] : weight(a.w_post, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    b[v][i] = b[v][i] * r * pick8(w, i);
+            }
+        }
+        float ss = 0.0f;
+        const uint8_t *res = ring + static_cast<size_t>(s) * pitch;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int n = (v * kCombineThreads + threadIdx.x) * 8;
+            if (n < a.N) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (a.resid)
+                    x = *reinterpret_cast<const uint4 *>(res + 2 * n);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    b[v][i] = a.resid ? fmaf(a.out_scale, b[v][i], a.res_scale * pick8(x, i)) : a.out_scale * b[v][i];
+                    ss = fmaf(b[v][i], b[v][i], ss);
+                }
+            }
+        }
+        release();
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            const int n = (v * kCombineThreads + threadIdx.x) * 8;
+            if (n < a.N && a.H && ok)
+                store8(a.H + static_cast<int64_t>(t) * a.ldh, n, a.N, 1, b[v]);
+        }
+        if (a.Nrm) {
+            ss = ring_sum(ss, m.slots[parity + 1]);
+            const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+                const int n = (v * kCombineThreads + threadIdx.x) * 8;
+                if (n < a.N && ok) {
+                    const uint4 w = KEEP ? pre[v] : weight(a.w_pre, v);
+                    float y[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        y[i] = b[v][i] * r * pick8(w, i);
+                    store8(a.Nrm + static_cast<int64_t>(t) * a.ldn, n, a.N, 1, y);
+                }
+            }
+        }
+    }
+}
+
+template <int VPT>
+cudaError_t launch_ring(const CombineArgs &a, int sms, cudaStream_t stream)
+{
+    const cudaError_t e = opt_in<combine_ring_kernel<VPT>>(kRingBytes);
+    if (e != cudaSuccess)
+        return e;
+    const int pitch = (a.N * 2 + 127) / 128 * 128;
+    const int fit = kRingBytes / pitch;
+    const int depth = fit < kRingMaxRows ? fit : kRingMaxRows;
+    return launch_dependent(combine_ring_kernel<VPT>, dim3(a.T < sms ? a.T : sms), dim3(kRingThreads),
+                            static_cast<size_t>(depth) * pitch, stream, a, depth);
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream)
+{
+    // Enough tokens for every SM to have several, and rows long enough that a
+    // ring entry's hand-over (some 200 cycles) is short beside them.
+    if (a.vec && a.N % 8 == 0 && a.N >= 2048 && a.N <= 16384 && a.T >= 4 * sms) {
+        const int per = (a.N / 8 + kCombineThreads - 1) / kCombineThreads;
+        return per <= 1   ? launch_ring<1>(a, sms, stream)
+               : per <= 2 ? launch_ring<2>(a, sms, stream)
+                          : launch_ring<4>(a, sms, stream);
+    }
+    const int vecs = (a.N + 7) / 8;
+    const int threads = vecs < kCombineThreads ? (vecs + 31) / 32 * 32 : kCombineThreads;
+    const int per = (vecs + threads - 1) / threads;
+    const int most = sms * (2048 / threads);
+    const dim3 grid(static_cast<unsigned>(a.T < most ? a.T : most)), block(static_cast<unsigned>(threads));
+    if (per <= 1)
+        return launch_dependent(combine_kernel<1, 8>, grid, block, 0, stream, a);
+    if (per <= 2)
+        return launch_dependent(combine_kernel<2, 4>, grid, block, 0, stream, a);
+    if (per <= 4)
+        return launch_dependent(combine_kernel<4, 2>, grid, block, 0, stream, a);
+    if (per <= kCombineMaxVec)
+        return launch_dependent(combine_kernel<8, 1>, grid, block, 0, stream, a);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t read_expert_status(int *status, int reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(status, g_status, sizeof(int));
+    if (e != cudaSuccess || !reset)
+        return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
+}
+
+}  // namespace mxfp4

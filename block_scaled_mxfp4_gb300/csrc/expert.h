@@ -52,7 +52,7 @@ struct RouteArgs {
     int *slot_row;              // [T, k]
     uint16_t *counts;           // workspace: [blocks][E rounded up to 8]
     int blocks;
-    int chunk;                  // tokens per block, a multiple of 32
+    int chunk;                  // tokens per block
 };
 int route_blocks(int T, int *chunk);
 cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream);

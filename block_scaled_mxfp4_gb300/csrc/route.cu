@@ -1,0 +1,730 @@
+// Routing of tokens to experts: the largest logits, their gates, and the stable
+// grouping of the rows by expert.
+#include <cuda_bf16.h>
+
+#include "expert.h"
+#include "launch.cuh"
+#include "ptx.cuh"
+#include "quant.cuh"
+
+namespace mxfp4 {
+
+namespace {
+
+constexpr uint32_t kFull = 0xffffffffu;
+
+// ------------------------------------------------------------------ routing --
+//
+// Stable counting sort of (token, slot) rows by expert.  A token picks an
+// expert at most once, so inside a run of 128 tokens an expert's rows are a
+// 128-bit mask of tokens (set with atomicOr, whose order does not matter), and
+// a row's place among them is the number of set bits before its own.  Blocks
+// write their experts' counts; the second kernel adds up the counts of the
+// blocks before its own and all of them (integers: any order, the same sum),
+// and places its tokens' rows.
+
+constexpr int kRouteThreads = 512;
+constexpr int kRouteRun = 128;                   // tokens of one mask
+constexpr int kRouteSingle = 64;                 // tokens that one block does alone
+constexpr int kRouteMaxBlocks = 456;             // of the picking kernel
+constexpr int kPlaceBlocks = 152;                // of the placing kernel
+constexpr int kPlacePer = kRouteMaxBlocks / kPlaceBlocks;   // picking blocks of one placing block
+// Its shared memory at most: two partial counts per thread's eight experts,
+// the totals, and its blocks' starts.
+constexpr int kPlaceSmem = (2 * kRouteThreads * 8 + (1 + kPlacePer) * kMaxGroups) * 4;
+static_assert(kPlacePer * kPlaceBlocks == kRouteMaxBlocks, "a placing block's share");
+
+// Float -> unsigned that orders the same way; NaN and -inf give 0, which no
+// other value does: such an expert is never picked.
+__device__ __forceinline__ uint32_t order_key(float x)
+{
+    const uint32_t b = __float_as_uint(x + 0.0f);          // -0 -> +0: equal values tie
+    const uint32_t key = b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
+    return x > __int_as_float(0xff800000) ? key : 0u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t key)
+{
+    return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+}
+
+// A token's picks (expert, logit), of which `taken` exist: gates, ids and mask
+// bits.  Its LANES lanes share the work; sum is this lane's part of the softmax
+// over all experts, top the largest logit.
+template <int LANES>
+__device__ __forceinline__ void finish_token(const RouteArgs &a, int t, bool live, int bit, int l, int taken, float top,
+                                             float sum, const float2 *picks, uint32_t *masks)
+{
+    if (a.mode == 0)
+        for (int j = l; j < taken; j += LANES) {
+            const float2 p = picks[j];
+            if (__float_as_int(p.x) >= 0)
+                sum += p.y == top ? 1.0f : expf(p.y - top);
+        }
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1)
+        sum += __shfl_xor_sync(kFull, sum, d);
+    if (live)
+        for (int j = l; j < a.k; j += LANES) {
+            const float2 p = j < taken ? picks[j] : make_float2(__int_as_float(-1), 0.0f);
+            const int id = __float_as_int(p.x);
+            float g = 0.0f;
+            if (id >= 0) {
+                g = a.mode == 2 ? 1.0f / (1.0f + expf(-p.y)) : (p.y == top ? 1.0f : expf(p.y - top)) / sum;
+                atomicOr(&masks[id * 4 + (bit >> 5)], 1u << (bit & 31));
+            }
+            a.ids[static_cast<int64_t>(t) * a.k + j] = id;
+            a.gates[static_cast<int64_t>(t) * a.k + j] = a.gate_scale * g;
+        }
+    __syncwarp();                                          // the picks are used again
+}
+
+// Picking.  LANES lanes share a token; each holds CH * 4 of its experts as keys
+// in shared memory, in chunks of four interleaved over the lanes (expert
+// (c * LANES + l) * 4 + i is key i of lane l's chunk c), and the chunks' maxima
+// in registers.  A pick takes the largest maximum of the lanes, and only the
+// lane that owns it looks into one chunk, drops the key and renews one maximum:
+// a handful of instructions per pick for each of the 32 / LANES tokens of a warp.
+// Ties: a lane's chunks and a chunk's keys are in index order, and where
+// several lanes hold the maximum, the lowest of their indexes counts.
+// picks: k (expert, exp or sigmoid) pairs of each of the warp's tokens.
+template <int LANES, int CH>
+__device__ __forceinline__ void route_tokens(const RouteArgs &a, int t, bool live, int bit, int lane, uint4 *keys,
+                                             float2 *picks, uint32_t *masks)
+{
+    const int l = lane & (LANES - 1);
+    uint4 *mine = keys + lane;                             // chunk c at mine[32 c]: no bank conflicts
+    const bool on = live && !(a.mask && a.mask[t] == 0);
+    const int64_t row = static_cast<int64_t>(live ? t : 0) * a.ldl;
+    uint32_t top[CH];                                      // the chunks' maxima
+    // Loads first, all in flight together.
+    float x[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int e = (c * LANES + l) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[c][i] = __int_as_float(0xff800000);
+        if (on && e < a.E) {
+            if (a.fp32) {
+                const float *p = static_cast<const float *>(a.logits) + row + e;
+                if (a.vec && e + 4 <= a.E) {
+                    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+                    x[c][0] = v.x;
+                    x[c][1] = v.y;
+                    x[c][2] = v.z;
+                    x[c][3] = v.w;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (e + i < a.E)
+                            x[c][i] = p[i];
+                }
+            } else {
+                const uint16_t *p = static_cast<const uint16_t *>(a.logits) + row + e;
+                if (a.vec && e + 4 <= a.E) {
+                    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+                    x[c][0] = bf16_lo(v.x);
+                    x[c][1] = bf16_hi(v.x);
+                    x[c][2] = bf16_lo(v.y);
+                    x[c][3] = bf16_hi(v.y);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (e + i < a.E)
+                            x[c][i] = bf16_lo(p[i]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const uint4 k = make_uint4(order_key(x[c][0]), order_key(x[c][1]), order_key(x[c][2]), order_key(x[c][3]));
+        mine[32 * c] = k;
+        top[c] = max(max(k.x, k.y), max(k.z, k.w));
+    }
+    uint32_t best = top[0];
+#pragma unroll
+    for (int c = 1; c < CH; ++c)
+        best = max(best, top[c]);
+    float2 *my_picks = picks + (lane / LANES) * a.k;
+    uint32_t first = 0u;                                   // the token's largest key
+    float sum = 0.0f;                                      // of the softmax
+    int taken = 0;
+    for (; taken < a.k; ++taken) {
+        uint32_t m = best;
+#pragma unroll
+        for (int d = LANES / 2; d > 0; d >>= 1)
+            m = max(m, __shfl_xor_sync(kFull, m, d));
+        if (taken == 0) {
+            first = m;
+            if (a.mode == 1 && m != 0u) {
+                // Terms far below the largest do not matter to the sum, so the
+                // fast exponential (whose relative error grows with its
+                // argument) keeps the sum to a few 2^-24 of itself.
+                const float xm = key_value(m);
+#pragma unroll
+                for (int c = 0; c < CH; ++c)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float z = x[c][i];
+                        sum += z == xm ? 1.0f : z > __int_as_float(0xff800000) ? __expf(z - xm) : 0.0f;
+                    }
+            }
+        }
+        if (!__any_sync(kFull, m != 0u))
+            break;
+        int at = 0x7FFFFFFF, chunk = 0, in = 0;
+        uint4 k = make_uint4(0u, 0u, 0u, 0u);
+        if (m != 0u && best == m) {
+#pragma unroll
+            for (int c = CH - 1; c >= 0; --c)
+                if (top[c] == m)
+                    chunk = c;
+            k = mine[32 * chunk];
+            in = k.x == m ? 0 : k.y == m ? 1 : k.z == m ? 2 : 3;
+            at = (chunk * LANES + l) * 4 + in;
+        }
+        int low = at;
+#pragma unroll
+        for (int d = LANES / 2; d > 0; d >>= 1)
+            low = min(low, __shfl_xor_sync(kFull, low, d));
+        if (m != 0u && at == low) {
+            k.x = in == 0 ? 0u : k.x;
+            k.y = in == 1 ? 0u : k.y;
+            k.z = in == 2 ? 0u : k.z;
+            k.w = in == 3 ? 0u : k.w;
+            mine[32 * chunk] = k;
+            const uint32_t left = max(max(k.x, k.y), max(k.z, k.w));
+            best = 0u;
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                top[c] = c == chunk ? left : top[c];
+                best = max(best, top[c]);
+            }
+            my_picks[taken] = make_float2(__int_as_float(at), key_value(m));
+        } else if (m == 0u && l == 0) {
+            my_picks[taken] = make_float2(__int_as_float(-1), 0.0f);
+        }
+    }
+    __syncwarp();
+    finish_token<LANES>(a, t, live, bit, l, taken, key_value(first), sum, my_picks, masks);
+}
+
+// Exclusive prefix sums of total[0 .. E) over the block, in place; returns
+// the sum of all.
+__device__ __forceinline__ int block_scan(int *total, int E)
+{
+    __shared__ int warp_sum[32];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = (E + kRouteThreads - 1) / kRouteThreads;
+    int sum = 0;
+    for (int i = 0; i < n; ++i)
+        if (t * n + i < E)
+            sum += total[t * n + i];
+    int incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d)
+            incl += v;
+    }
+    if (lane == 31)
+        warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - sum, all = 0;
+    for (int w = 0; w < kRouteThreads / 32; ++w) {
+        before += w < warp ? warp_sum[w] : 0;
+        all += warp_sum[w];
+    }
+    for (int i = 0; i < n; ++i)
+        if (t * n + i < E) {
+            const int v = total[t * n + i];
+            total[t * n + i] = before;
+            before += v;
+        }
+    __syncthreads();
+    return all;
+}
+
+// After a run of tokens [s0, s1) has been picked: each row's place among its
+// expert's rows of this block, into slot_row; the block's counts move on.
+__device__ __forceinline__ void place_in_block(const RouteArgs &a, int s0, int s1, const uint32_t *masks, int *run)
+{
+    for (int i = threadIdx.x; i < (s1 - s0) * a.k; i += blockDim.x) {
+        const int64_t at = static_cast<int64_t>(s0) * a.k + i;
+        const int e = a.ids[at];
+        int place = -1;
+        if (e >= 0) {
+            const int bit = i / a.k;
+            place = run[e];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const uint32_t m = masks[4 * e + w];
+                place += w < (bit >> 5) ? __popc(m) : w == (bit >> 5) ? __popc(m & ((1u << (bit & 31)) - 1u)) : 0;
+            }
+        }
+        a.slot_row[at] = place;
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
+        run[e] += __popc(masks[4 * e]) + __popc(masks[4 * e + 1]) + __popc(masks[4 * e + 2]) + __popc(masks[4 * e + 3]);
+    __syncthreads();
+}
+
+__device__ __forceinline__ void write_counts(const RouteArgs &a, const int *run)
+{
+    const int ep = (a.E + 7) / 8 * 8;
+    uint16_t *count = a.counts + static_cast<int64_t>(blockIdx.x) * ep;
+    for (int e = threadIdx.x; e < ep; e += blockDim.x)
+        count[e] = e < a.E ? static_cast<uint16_t>(run[e]) : uint16_t(0);
+}
+
+template <int LANES, int CH>
+__global__ void __launch_bounds__(kRouteThreads, 2) route_pick_kernel(const __grid_constant__ RouteArgs a)
+{
+    constexpr int TPW = 32 / LANES;                        // tokens of a warp
+    extern __shared__ __align__(16) uint32_t smem_u32[];
+    uint4 *all_keys = reinterpret_cast<uint4 *>(smem_u32); // [warps][CH][32]
+    float2 *all_picks = reinterpret_cast<float2 *>(all_keys + kRouteThreads * CH);   // [warps][TPW][k]
+    uint32_t *masks = reinterpret_cast<uint32_t *>(all_picks + kRouteThreads / LANES * a.k);   // [E][4]
+    int *run = reinterpret_cast<int *>(masks + 4 * a.E);   // [E]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t0 = blockIdx.x * a.chunk;
+    const int t1 = min(a.T, t0 + a.chunk);
+    const bool single = gridDim.x == 1;
+    for (int i = threadIdx.x; i < a.E; i += kRouteThreads)
+        run[i] = 0;
+    pdl_wait_prerequisites();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    for (int s0 = t0; s0 < t1; s0 += kRouteRun) {
+        for (int i = threadIdx.x; i < 4 * a.E; i += kRouteThreads)
+            masks[i] = 0u;
+        __syncthreads();
+        const int s1 = min(t1, s0 + kRouteRun);
+        for (int q = s0 + warp * TPW; q < s1; q += kRouteThreads / 32 * TPW) {
+            const int t = q + lane / LANES;
+            route_tokens<LANES, CH>(a, t, t < s1, t - s0, lane, all_keys + warp * CH * 32, all_picks + warp * TPW * a.k,
+                                    masks);
+        }
+        __syncthreads();
+        place_in_block(a, s0, s1, masks, run);
+    }
+    if (!single) {
+        write_counts(a, run);
+        return;
+    }
+    const int all = block_scan(run, a.E);
+    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads)
+        a.offsets[e] = e < a.E ? run[e] : all;
+    for (int i = threadIdx.x; i < a.T * a.k; i += kRouteThreads) {
+        const int e = a.ids[i];
+        if (e >= 0) {
+            const int row = run[e] + a.slot_row[i];
+            a.slot_row[i] = row;
+            a.row_token[row] = i / a.k;
+        }
+        if (i >= all)
+            a.row_token[i] = -1;
+    }
+}
+
+// Many tokens, k <= 8.  LANES lanes hold a token's experts, 32 each, in
+// registers.  The k-th largest of the maxima of its groups of eight experts is
+// a bound that the k-th largest logit is not below: the lanes sort their four
+// maxima and merge the lists in a butterfly.  The logits at or above the bound,
+// little more than k, are set down in shared memory, and each one's place is
+// the number of larger ones (and of equal ones with a lower index).  Where
+// more than fit are left, as among many equal logits, the warp picks its tokens
+// one expert at a time (route_tokens).  A token of 256 experts costs some 170
+// warp instructions; picking costs four times as many.
+constexpr int kManyThreads = 256;
+constexpr int kManyBlocksPerSm = 3;
+
+template <int LANES>
+constexpr int kManyCandidates = LANES == 1 ? 32 : 64;      // of one token
+
+__device__ __forceinline__ void exchange(float &hi, float &lo)
+{
+    const float a = fmaxf(hi, lo), b = fminf(hi, lo);
+    hi = a;
+    lo = b;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Bitonic sequence of eight -> descending.
+__device__ __forceinline__ void settle8(float (&v)[8])
+{
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((i & d) == 0)
+                exchange(v[i], v[i | d]);
+}
+
+template <bool FP32, int LANES>
+__global__ void __launch_bounds__(kManyThreads, kManyBlocksPerSm) route_many_kernel(const __grid_constant__ RouteArgs a)
+{
+    constexpr int TPW = 32 / LANES;                        // tokens of a warp
+    constexpr int CAP = kManyCandidates<LANES>;
+    extern __shared__ __align__(16) uint32_t smem_u32[];
+    uint4 *all_keys = reinterpret_cast<uint4 *>(smem_u32); // [warps][8][32]
+    float2 *all_picks = reinterpret_cast<float2 *>(all_keys + kManyThreads * 8);     // [warps][TPW][k]
+    float2 *all_found = all_picks + kManyThreads / LANES * a.k;                      // [warps][TPW][CAP]
+    uint32_t *masks = reinterpret_cast<uint32_t *>(all_found + kManyThreads / LANES * CAP);   // [E][4]
+    int *run = reinterpret_cast<int *>(masks + 4 * a.E);   // [E]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (LANES - 1);
+    const int t0 = blockIdx.x * a.chunk;
+    const int t1 = min(a.T, t0 + a.chunk);
+    uint4 *keys = all_keys + warp * 8 * 32;
+    float2 *picks = all_picks + warp * TPW * a.k;
+    float2 *my_picks = picks + (lane / LANES) * a.k;
+    float2 *found = all_found + (warp * TPW + lane / LANES) * CAP;
+    for (int i = threadIdx.x; i < a.E; i += kManyThreads)
+        run[i] = 0;
+    pdl_wait_prerequisites();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    const float ninf = __int_as_float(0xff800000);
+    for (int s0 = t0; s0 < t1; s0 += kRouteRun) {
+        for (int i = threadIdx.x; i < 4 * a.E; i += kManyThreads)
+            masks[i] = 0u;
+        __syncthreads();
+        const int s1 = min(t1, s0 + kRouteRun);
+        for (int q = s0 + warp * TPW; q < s1; q += kManyThreads / 32 * TPW) {
+            const int t = q + lane / LANES;
+            const bool live = t < s1;
+            const bool on = live && !(a.mask && a.mask[t] == 0);
+            const int64_t row = static_cast<int64_t>(live ? t : 0) * a.ldl;
+            float x[8][4];                                 // expert (c LANES + l) 4 + i
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const int e = (c * LANES + l) * 4;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[c][i] = ninf;
+                if (!on || e >= a.E)
+                    continue;
+                if constexpr (FP32) {
+                    const float *p = static_cast<const float *>(a.logits) + row + e;
+                    if (a.vec && e + 4 <= a.E) {
+                        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+                        x[c][0] = v.x;
+                        x[c][1] = v.y;
+                        x[c][2] = v.z;
+                        x[c][3] = v.w;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (e + i < a.E)
+                                x[c][i] = p[i];
+                    }
+                } else {
+                    const uint16_t *p = static_cast<const uint16_t *>(a.logits) + row + e;
+                    if (a.vec && e + 4 <= a.E) {
+                        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+                        x[c][0] = bf16_lo(v.x);
+                        x[c][1] = bf16_hi(v.x);
+                        x[c][2] = bf16_lo(v.y);
+                        x[c][3] = bf16_hi(v.y);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (e + i < a.E)
+                                x[c][i] = bf16_lo(p[i]);
+                    }
+                }
+            }
+            float best[8];                                 // descending
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float m = ninf;
+#pragma unroll
+                for (int c = 2 * g; c < 2 * g + 2; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        x[c][i] = fmaxf(x[c][i], ninf);    // NaN -> -inf
+                    m = max3(max3(m, x[c][0], x[c][1]), x[c][2], x[c][3]);
+                    reinterpret_cast<float4 *>(keys)[32 * c + lane] = make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
+                }
+                best[g] = m;
+                best[4 + g] = ninf;
+            }
+            exchange(best[0], best[1]);
+            exchange(best[2], best[3]);
+            exchange(best[0], best[2]);
+            exchange(best[1], best[3]);
+            exchange(best[1], best[2]);
+#pragma unroll
+            for (int d = LANES / 2; d > 0; d >>= 1) {
+                // The elementwise maxima of one list and the other reversed are
+                // the eight largest of both, as a bitonic sequence (both lanes
+                // read each other's list as it was).
+                float w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[i] = __shfl_xor_sync(kFull, best[i], d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    best[i] = fmaxf(best[i], w[7 - i]);
+                settle8(best);
+            }
+            const float top = best[0];
+            float bar = best[0];
+#pragma unroll
+            for (int j = 1; j < 8; ++j)
+                bar = j < a.k ? best[j] : bar;
+            float sum = 0.0f;
+            if (a.mode == 1 && top > ninf) {
+                // Terms far below the largest do not matter to the sum, so the
+                // fast exponential keeps it to a few 2^-24 of itself.
+                if (top < __int_as_float(0x7f800000)) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sum += __expf(x[c][i] - top);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sum += x[c][i] == top ? 1.0f : 0.0f;
+                }
+            }
+            const float low = fmaxf(bar, -3.402823466e38f);        // -inf is no candidate
+            uint32_t hits = 0u;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    hits |= x[c][i] >= low ? 1u << (4 * c + i) : 0u;
+            // This lane's place among the token's candidates, and their number.
+            const int own = __popc(hits);
+            int upto = own;
+#pragma unroll
+            for (int d = 1; d < LANES; d <<= 1) {
+                const int v = __shfl_up_sync(kFull, upto, d, LANES);
+                if (l >= d)
+                    upto += v;
+            }
+            const int n = __shfl_sync(kFull, upto, LANES - 1, LANES);
+            if (__any_sync(kFull, n > CAP)) {
+                __syncwarp();
+                route_tokens<LANES, 8>(a, t, live, t - s0, lane, keys, picks, masks);
+                continue;
+            }
+            __syncwarp();
+            for (int at = upto - own; hits; ++at) {
+                const int b = __ffs(hits) - 1;
+                hits &= hits - 1u;
+                const float z = reinterpret_cast<const float *>(keys + 32 * (b >> 2) + lane)[b & 3];
+                found[at] = make_float2(__int_as_float(((b >> 2) * LANES + l) * 4 + (b & 3)), z);
+            }
+            __syncwarp();
+            for (int i = l; i < n; i += LANES) {
+                const float2 f = found[i];
+                int place = 0;
+                for (int j = 0; j < n; ++j) {
+                    const float2 o = found[j];
+                    place += o.y > f.y || (o.y == f.y && __float_as_int(o.x) < __float_as_int(f.x)) ? 1 : 0;
+                }
+                if (place < a.k)
+                    my_picks[place] = f;
+            }
+            __syncwarp();
+            finish_token<LANES>(a, t, live, t - s0, l, min(n, a.k), top, sum, my_picks, masks);
+        }
+        __syncthreads();
+        place_in_block(a, s0, s1, masks, run);
+    }
+    write_counts(a, run);
+}
+
+// Block p takes the tokens of `per` picking blocks from p * per on: it adds up
+// all blocks' counts and those before its own, then places its rows.
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid_constant__ RouteArgs a, int per)
+{
+    extern __shared__ __align__(16) uint32_t smem_u32[];
+    const int ep = (a.E + 7) / 8 * 8, lanes = ep / 8;      // threads of one block's counts
+    const int b0 = blockIdx.x * per, b1 = min(a.blocks, b0 + per);
+    const int at_once = kRouteThreads / lanes;             // blocks whose counts are read together
+    uint32_t *part = smem_u32;                             // [at_once][2][ep]: all blocks, the blocks before
+    int *total = reinterpret_cast<int *>(part + 2 * at_once * ep);   // [ep]
+    int *mine = total + ep;                                // [per][ep]
+    pdl_wait_prerequisites();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    if (static_cast<int>(threadIdx.x) < at_once * lanes) {
+        const int q = threadIdx.x % lanes, g = threadIdx.x / lanes;
+        uint32_t all[8], before[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            all[i] = before[i] = 0u;
+#pragma unroll 8
+        for (int b = g; b < a.blocks; b += at_once) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(a.counts + static_cast<int64_t>(b) * ep + 8 * q);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t c = (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+                all[i] += c;
+                before[i] += b < b0 ? c : 0u;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            part[(2 * g) * ep + 8 * q + i] = all[i];
+            part[(2 * g + 1) * ep + 8 * q + i] = before[i];
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * ep; i += kRouteThreads) {
+        uint32_t s = 0u;
+        for (int g = 0; g < at_once; ++g)
+            s += part[2 * g * ep + i];
+        total[i] = static_cast<int>(s);                    // total, then mine[0]
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
+        int at = mine[e];
+        uint16_t c[kPlacePer];
+#pragma unroll
+        for (int i = 0; i < kPlacePer; ++i)
+            c[i] = b0 + i < b1 ? a.counts[static_cast<int64_t>(b0 + i) * ep + e] : uint16_t(0);
+#pragma unroll
+        for (int i = 0; i < kPlacePer; ++i) {
+            if (i < per)
+                mine[i * ep + e] = at;
+            at += c[i];
+        }
+    }
+    __syncthreads();
+    const int sum = block_scan(total, a.E);
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= a.E; e += kRouteThreads)
+            a.offsets[e] = e < a.E ? total[e] : sum;
+    // (T k fits an int.)
+    const int span = a.chunk * a.k;
+    const int i0 = b0 * span;
+    const int i1 = static_cast<int>(min(static_cast<int64_t>(a.T) * a.k, static_cast<int64_t>(b1) * span));
+#pragma unroll 4
+    for (int i = i0 + threadIdx.x; i < i1; i += kRouteThreads) {
+        const int e = a.ids[i], place = a.slot_row[i];
+        if (e >= 0) {
+            const int row = total[e] + mine[(i - i0) / span * ep + e] + place;
+            a.slot_row[i] = row;
+            a.row_token[row] = i / a.k;
+        }
+        if (i >= sum)
+            a.row_token[i] = -1;
+    }
+}
+
+__global__ void route_empty_kernel(int *offsets, int E)
+{
+    pdl_wait_prerequisites();
+    for (int e = threadIdx.x; e <= E; e += blockDim.x)
+        offsets[e] = 0;
+}
+
+template <int LANES, int CH>
+cudaError_t launch_pick(const RouteArgs &a, cudaStream_t stream)
+{
+    // The most that any E and k need of this instance.
+    constexpr int kMost = kRouteThreads * CH * 16 + kRouteThreads / LANES * kMaxTopK * 8 + 5 * LANES * CH * 4 * 4;
+    const size_t smem = static_cast<size_t>(kRouteThreads) * CH * 16 + static_cast<size_t>(kRouteThreads / LANES) * a.k * 8 +
+                        static_cast<size_t>(5 * a.E) * 4;
+    const cudaError_t e = opt_in<route_pick_kernel<LANES, CH>>(kMost);
+    if (e != cudaSuccess)
+        return e;
+    return launch_dependent(route_pick_kernel<LANES, CH>, dim3(a.blocks), dim3(kRouteThreads), smem, stream, a);
+}
+
+template <bool FP32, int LANES>
+cudaError_t launch_many(const RouteArgs &a, cudaStream_t stream)
+{
+    constexpr int kCap = kManyCandidates<LANES>;
+    constexpr int kMost = kManyThreads * 8 * 16 + kManyThreads / LANES * (8 + kCap) * 8 + 5 * LANES * 32 * 4;
+    const size_t smem = static_cast<size_t>(kManyThreads) * 8 * 16 +
+                        static_cast<size_t>(kManyThreads / LANES) * (a.k + kCap) * 8 +
+                        static_cast<size_t>(5 * a.E) * 4;
+    const cudaError_t e = opt_in<route_many_kernel<FP32, LANES>>(kMost);
+    if (e != cudaSuccess)
+        return e;
+    return launch_dependent(route_many_kernel<FP32, LANES>, dim3(a.blocks), dim3(kManyThreads), smem, stream, a);
+}
+
+template <bool FP32>
+cudaError_t launch_many_lanes(const RouteArgs &a, int lanes, cudaStream_t stream)
+{
+    switch (lanes) {
+    case 1: return launch_many<FP32, 1>(a, stream);
+    case 2: return launch_many<FP32, 2>(a, stream);
+    case 4: return launch_many<FP32, 4>(a, stream);
+    case 8: return launch_many<FP32, 8>(a, stream);
+    case 16: return launch_many<FP32, 16>(a, stream);
+    default: return launch_many<FP32, 32>(a, stream);
+    }
+}
+
+}  // namespace
+
+int route_blocks(int T, int *chunk)
+{
+    int c = T <= kRouteSingle ? kRouteSingle : 32;
+    if (T > 32 * kRouteMaxBlocks)
+        c = ((T + kRouteMaxBlocks - 1) / kRouteMaxBlocks + 3) / 4 * 4;      // one even wave
+    *chunk = c;
+    return (T + c - 1) / c;
+}
+
+cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream)
+{
+    if (a.T == 0)
+        return launch_dependent(route_empty_kernel, dim3(1), dim3(256), 0, stream, a.offsets, a.E);
+    // Lanes per token: as few as hold its experts in 32 registers each, which
+    // shares the instructions among the most tokens, once that still leaves
+    // every SM 16 warps; otherwise a whole warp per token, the shortest time
+    // for one.
+    int lanes = 1;
+    while (lanes * 32 < a.E)
+        lanes *= 2;
+    const bool many = static_cast<int64_t>(a.T) * lanes / 32 >= static_cast<int64_t>(sms) * 16;
+    cudaError_t e;
+    if (!many) {
+        e = a.E <= 128   ? launch_pick<32, 1>(a, stream)
+            : a.E <= 256 ? launch_pick<32, 2>(a, stream)
+            : a.E <= 512 ? launch_pick<32, 4>(a, stream)
+                         : launch_pick<32, 8>(a, stream);
+    } else if (a.k <= 8) {
+        e = a.fp32 ? launch_many_lanes<true>(a, lanes, stream) : launch_many_lanes<false>(a, lanes, stream);
+    } else {
+        switch (lanes) {
+        case 1: e = launch_pick<1, 8>(a, stream); break;
+        case 2: e = launch_pick<2, 8>(a, stream); break;
+        case 4: e = launch_pick<4, 8>(a, stream); break;
+        case 8: e = launch_pick<8, 8>(a, stream); break;
+        case 16: e = launch_pick<16, 8>(a, stream); break;
+        default: e = launch_pick<32, 8>(a, stream); break;
+        }
+    }
+    if (e != cudaSuccess || a.blocks == 1)
+        return e;
+    const int ep = (a.E + 7) / 8 * 8;
+    const int per = (a.blocks + kPlaceBlocks - 1) / kPlaceBlocks;
+    const size_t smem2 = static_cast<size_t>(2 * (kRouteThreads / (ep / 8)) + 1 + per) * ep * 4;
+    e = opt_in<route_place_kernel>(kPlaceSmem);
+    if (e != cudaSuccess)
+        return e;
+    return launch_dependent(route_place_kernel, dim3((a.blocks + per - 1) / per), dim3(kRouteThreads), smem2, stream, a, per);
+}
+
+}  // namespace mxfp4

@@ -106,6 +106,28 @@ def route(logits, k, mode, mask=None):
     return ids, gates
 
 
+def route_many(logits, k, mode, mask=None):
+    """route() and grouping() without loops over the tokens, for many of them."""
+    x = np.where(np.isnan(logits), -np.inf, logits)
+    if mask is not None:
+        x = np.where(mask[:, None] != 0, x, -np.inf)
+    order = np.argsort(-x, axis=1, kind="stable")[:, :k]
+    v = np.take_along_axis(x, order, 1)
+    fine = v > -np.inf
+    top = np.where(fine[:, :1], v[:, :1], 0)
+    with np.errstate(invalid="ignore", over="ignore"):
+        ex = lambda z: np.where(z == top, 1.0, np.where(z > -np.inf, np.exp(z - top), 0.0))
+        gates = 1 / (1 + np.exp(-v)) if mode == 2 else ex(v) / np.maximum((ex(x) if mode == 1 else ex(v)).sum(1, keepdims=True), 1)
+    ids = np.where(fine, order, -1).astype(np.int32)
+    E, flat = x.shape[1], np.where(ids < 0, x.shape[1], ids).reshape(-1)
+    by = np.argsort(flat, kind="stable")
+    offsets = np.searchsorted(flat[by], np.arange(E + 1)).astype(np.int32)
+    place = np.empty(flat.size, np.int32)
+    place[by] = np.arange(flat.size)
+    rows = np.where(np.arange(flat.size) < offsets[E], by // k, -1).astype(np.int32)
+    return ids, np.where(fine, gates, 0), offsets, rows, np.where(flat < E, place, -1).reshape(ids.shape)
+
+
 def sf_groups(K):
     return 2 * (-(-K // 256))
 

@@ -140,20 +140,43 @@ def test_route_strided_scaled_and_all_to_one():
     check_route(x, 1, 0)
 
 
-def test_route_many_tokens_against_torch():
-    """More tokens than one run per block, where the plain form is too slow."""
-    T, E, k = 40001, 64, 4
-    g = torch.Generator(device="cuda").manual_seed(1)
-    x = torch.randn((T, E), device="cuda", generator=g)
-    ids, gates, offsets, row_token, slot_row = run_route(x, k, 0)
-    want = torch.sort(x, dim=1, descending=True, stable=True).indices[:, :k].cpu().numpy()
-    np.testing.assert_array_equal(ids, want)
-    order = np.argsort(want.reshape(-1), kind="stable")
-    np.testing.assert_array_equal(row_token, order // k)
-    place = np.empty(T * k, np.int64)
-    place[order] = np.arange(T * k)
-    np.testing.assert_array_equal(slot_row.reshape(-1), place)
-    np.testing.assert_array_equal(offsets, np.concatenate([[0], np.cumsum(np.bincount(want.reshape(-1), minlength=E))]))
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,E,k,mode", [(80001, 8, 2, 0), (78000, 30, 8, 1), (40001, 64, 4, 0), (20000, 100, 8, 1),
+                                        (9985, 250, 8, 2), (5000, 512, 6, 0), (2500, 777, 7, 1), (20000, 128, 12, 0)])
+def test_route_many_tokens(T, E, k, mode, dtype):
+    """The forms for many tokens, all lane counts: random logits, then ties,
+    masked tokens, infinities and NaN among them."""
+    g = torch.Generator().manual_seed(T + E)
+    x = torch.randn((T, E), generator=g) * 2
+    x[: T // 2] = torch.round(x[: T // 2])                 # many ties
+    x[5::97] = float("-inf")
+    x[6::101, 1:] = float("-inf")
+    x[7::103, E // 2] = float("nan")
+    x[8::107, E // 3] = float("inf")
+    x[9::109, ::2] = -0.0
+    x[10::113] = -3e38
+    x = x.to(torch.bfloat16 if dtype == "bf16" else torch.float32).cuda()
+    mask = (np.random.default_rng(T).uniform(size=T) < 0.9).astype(np.uint8)
+    got = run_route(x, k, mode, dev(mask), ldl=E + 3 if mode == 1 else None)
+    want = ref.route_many(x.double().cpu().numpy(), k, mode, mask)
+    for i, what in enumerate(("ids", "gates", "offsets", "row_token", "slot_row")):
+        if what == "gates":
+            np.testing.assert_allclose(got[1], want[1], rtol=(E / 32 + 16) * 2.0 ** -23, atol=1e-37)
+        else:
+            np.testing.assert_array_equal(got[i], want[i], err_msg=what)
+
+
+def test_the_plain_forms_of_routing_agree():
+    x = np.round(np.random.default_rng(0).normal(size=(90, 17)) * 2)
+    x[3] = -np.inf
+    x[4, 5] = np.nan
+    for mode in (0, 1, 2):
+        ids, gates = ref.route(x, 6, mode)
+        many = ref.route_many(x, 6, mode)
+        np.testing.assert_array_equal(ids, many[0])
+        np.testing.assert_allclose(gates, many[1], rtol=1e-12)
+        for u, v in zip(ref.grouping(ids, 17), many[2:]):
+            np.testing.assert_array_equal(u, v)
 
 
 # ---------------------------------------------------------------- quantiser --
