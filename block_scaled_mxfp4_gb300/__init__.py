@@ -155,8 +155,24 @@ def lib() -> ctypes.CDLL:
             fn = getattr(L, name)
             fn.restype = res
             fn.argtypes = args
+        _bind_entries(L)
         _lib = L
     return _lib
+
+
+def _raise(status, where):
+    raise Mxfp4Error(status, where)
+
+
+def _bind_entries(L):
+    """Replace the calls of a decoding step by the extension module's, which
+    take the same arguments and marshal them in C."""
+    from . import _entry
+    names = [n for n in dir(_entry) if n.startswith("mxfp")]
+    _entry.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _p,
+                _current_stream, _raise)
+    for n in names:
+        globals()[n] = getattr(_entry, n)
 
 
 def header_functions(path: str = HEADER):

@@ -3,7 +3,8 @@
     python -m block_scaled_mxfp4_gb300.build [--force] [--verbose-ptxas]
 
 Each .cu under csrc/ compiles to an object in parallel, then one link makes
-libmxfp4_gb300.so next to this file.  The benchmark's streaming-read helper
+libmxfp4_gb300.so next to this file.  The Python binding's fast path
+(csrc/binding.c) compiles to the extension module _entry.so.  The benchmark's streaming-read helper
 (probe/stream_read.cu, not part of the library) links into libmxfp4_probe.so.
 Rebuilds only when a source or header is newer than its library.
 """
@@ -16,12 +17,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmxfp4_gb300.so")
+BINDING_SRC = os.path.join(CSRC, "binding.c")
+BINDING_LIB = os.path.join(PKG, "_entry.so")
 PROBE_SRC = os.path.join(PKG, "probe", "stream_read.cu")
 PROBE_LIB = os.path.join(PKG, "libmxfp4_probe.so")
 OBJDIR = os.path.join(PKG, "_build")
@@ -70,7 +74,25 @@ def build_probe(force: bool = False) -> str:
     return PROBE_LIB
 
 
+def build_binding(force: bool = False) -> str:
+    """The extension module that marshals the decoding step's calls (gcc and
+    Python's own headers; it links nothing of CUDA)."""
+    if not force and os.path.exists(BINDING_LIB) and \
+            os.path.getmtime(BINDING_SRC) <= os.path.getmtime(BINDING_LIB):
+        return BINDING_LIB
+    tmp = BINDING_LIB + ".tmp%d" % os.getpid()
+    cmd = ["gcc", "-O2", "-std=c11", "-Wall", "-shared", "-fPIC",
+           "-I" + sysconfig.get_paths()["include"], BINDING_SRC, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("gcc failed on the Python binding")
+    os.replace(tmp, BINDING_LIB)
+    return BINDING_LIB
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
+    build_binding(force)
     if not force and not verbose_ptxas and up_to_date():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)

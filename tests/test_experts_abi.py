@@ -133,3 +133,44 @@ def test_plain_quantiser_agrees_with_the_oracle(oracle_mod):
         q, s = call()[:2]
         np.testing.assert_array_equal(codes, q.reshape(codes.shape))
         np.testing.assert_array_equal(scales, s.reshape(scales.shape))
+
+
+@pytest.mark.parametrize("call,args,changes", REFUSALS, ids=lambda v: getattr(v, "__name__", ""))
+def test_refusals_through_the_bound_entries(call, args, changes):
+    """Loading the library puts the extension module's functions in place of
+    the Python ones: the same refusals, stream by place or by name."""
+    mx.lib()
+    bound = getattr(mx, call.__name__)
+    assert bound is not call and type(bound).__name__ == "builtin_function_or_method"
+    for by, want in changes:
+        assert status(bound, *change(args, **by)) == want, (call.__name__, by)
+        with pytest.raises(mx.Mxfp4Error) as e:
+            bound(*change(args, **by), 0)
+        assert want in str(e.value) and call.__name__ in str(e.value)
+
+
+def test_the_bound_entries_check_their_arguments():
+    mx.lib()
+    good = change(JOIN, _18=0)                            # refused by the library, once converted
+    with pytest.raises(TypeError):
+        mx.mxfp4_moe_combine(*good[:-1], stream=0)
+    with pytest.raises(TypeError):
+        mx.mxfp4_moe_combine(*good, flow=0)
+    with pytest.raises(TypeError):
+        mx.mxfp4_moe_combine(*change(good, _4="Y"), stream=0)
+    with pytest.raises(TypeError):
+        mx.mxfp4_moe_combine(*change(good, _14="1.0"), stream=0)
+    with pytest.raises(OverflowError):
+        mx.mxfp4_moe_combine(*change(good, _17=1 << 40), stream=0)
+    with pytest.raises(OverflowError):
+        mx.mxfp4_moe_route(*change(ROUTE, _15=-1), stream=0)
+
+    class Stream:
+        cuda_stream = 0
+
+    class Pointer:
+        def data_ptr(self):
+            return P
+
+    with pytest.raises(mx.Mxfp4Error):
+        mx.mxfp4_moe_combine(*change(good, _4=Pointer(), _0=np.zeros(8)), Stream())
