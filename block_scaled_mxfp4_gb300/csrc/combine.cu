@@ -82,10 +82,11 @@ __device__ __forceinline__ float pick8(const uint4 &v, int i)
 }
 
 // VPT 8-element vectors per thread, JC slots' rows in flight together.
-template <int VPT, int JC>
-__global__ void __launch_bounds__(kCombineThreads, VPT <= 2 ? 2 : 1) combine_kernel(const __grid_constant__ CombineArgs a)
+// Few tokens run on up to MAXT = 1024 threads each, the shortest time for one.
+template <int VPT, int JC, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == kCombineThreads && VPT <= 2 ? 2 : 1) combine_kernel(const __grid_constant__ CombineArgs a)
 {
-    __shared__ float slots[4][kCombineThreads / 32];
+    __shared__ float slots[4][MAXT / 32];
     if (!a.early)
         pdl_wait_prerequisites();
     if (threadIdx.x == 0)
@@ -454,18 +455,24 @@ cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream)
                           : launch_ring<4>(a, sms, stream);
     }
     const int vecs = (a.N + 7) / 8;
-    const int threads = vecs < kCombineThreads ? (vecs + 31) / 32 * 32 : kCombineThreads;
+    const bool few = a.T < sms && vecs <= 2048;
+    const int most_threads = few ? 1024 : kCombineThreads;
+    const int threads = vecs < most_threads ? (vecs + 31) / 32 * 32 : most_threads;
     const int per = (vecs + threads - 1) / threads;
     const int most = sms * (2048 / threads);
     const dim3 grid(static_cast<unsigned>(a.T < most ? a.T : most)), block(static_cast<unsigned>(threads));
+    if (few && per <= 1)
+        return launch_dependent(combine_kernel<1, 8, 1024>, grid, block, 0, stream, a);
+    if (few)
+        return launch_dependent(combine_kernel<2, 2, 1024>, grid, block, 0, stream, a);
     if (per <= 1)
-        return launch_dependent(combine_kernel<1, 8>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<1, 8, kCombineThreads>, grid, block, 0, stream, a);
     if (per <= 2)
-        return launch_dependent(combine_kernel<2, 4>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<2, 4, kCombineThreads>, grid, block, 0, stream, a);
     if (per <= 4)
-        return launch_dependent(combine_kernel<4, 2>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<4, 2, kCombineThreads>, grid, block, 0, stream, a);
     if (per <= kCombineMaxVec)
-        return launch_dependent(combine_kernel<8, 1>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<8, 1, kCombineThreads>, grid, block, 0, stream, a);
     return cudaErrorInvalidValue;
 }
 

@@ -26,13 +26,10 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kRouteThreads = 512;
 constexpr int kRouteRun = 128;                   // tokens of one mask
 constexpr int kRouteSingle = 64;                 // tokens that one block does alone
-constexpr int kRouteMaxBlocks = 456;             // of the picking kernel
-constexpr int kPlaceBlocks = 152;                // of the placing kernel
-constexpr int kPlacePer = kRouteMaxBlocks / kPlaceBlocks;   // picking blocks of one placing block
-// Its shared memory at most: two partial counts per thread's eight experts,
-// the totals, and its blocks' starts.
-constexpr int kPlaceSmem = (2 * kRouteThreads * 8 + (1 + kPlacePer) * kMaxGroups) * 4;
-static_assert(kPlacePer * kPlaceBlocks == kRouteMaxBlocks, "a placing block's share");
+constexpr int kRouteMaxBlocks = 152;             // a block per SM
+// Shared memory of the placing kernel at most: two partial counts per thread's
+// eight experts, their sums.
+constexpr int kPlaceSmem = (2 * kRouteThreads * 8 + 2 * kMaxGroups) * 4;
 
 // Float -> unsigned that orders the same way; NaN and -inf give 0, which no
 // other value does: such an expert is never picked.
@@ -50,10 +47,10 @@ __device__ __forceinline__ float key_value(uint32_t key)
 
 // A token's picks (expert, logit), of which `taken` exist: gates, ids and mask
 // bits.  Its LANES lanes share the work; sum is this lane's part of the softmax
-// over all experts, top the largest logit.
+// over all experts, top the largest logit.  ids: the run's, in shared memory.
 template <int LANES>
 __device__ __forceinline__ void finish_token(const RouteArgs &a, int t, bool live, int bit, int l, int taken, float top,
-                                             float sum, const float2 *picks, uint32_t *masks)
+                                             float sum, const float2 *picks, uint32_t *masks, int *ids)
 {
     if (a.mode == 0)
         for (int j = l; j < taken; j += LANES) {
@@ -73,10 +70,56 @@ __device__ __forceinline__ void finish_token(const RouteArgs &a, int t, bool liv
                 g = a.mode == 2 ? 1.0f / (1.0f + expf(-p.y)) : (p.y == top ? 1.0f : expf(p.y - top)) / sum;
                 atomicOr(&masks[id * 4 + (bit >> 5)], 1u << (bit & 31));
             }
+            ids[bit * a.k + j] = id;
             a.ids[static_cast<int64_t>(t) * a.k + j] = id;
             a.gates[static_cast<int64_t>(t) * a.k + j] = a.gate_scale * g;
         }
     __syncwarp();                                          // the picks are used again
+}
+
+// Expert (c LANES + l) 4 + i of a token -> x[c][i], -inf where there is none;
+// all loads in flight together.
+template <int LANES, int CH>
+__device__ __forceinline__ void load_logits(const RouteArgs &a, bool on, int64_t row, int l, float (&x)[CH][4])
+{
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int e = (c * LANES + l) * 4;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[c][i] = __int_as_float(0xff800000);
+        if (!on || e >= a.E)
+            continue;
+        if (a.fp32) {
+            const float *p = static_cast<const float *>(a.logits) + row + e;
+            if (a.vec && e + 4 <= a.E) {
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
+                x[c][0] = v.x;
+                x[c][1] = v.y;
+                x[c][2] = v.z;
+                x[c][3] = v.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (e + i < a.E)
+                        x[c][i] = p[i];
+            }
+        } else {
+            const uint16_t *p = static_cast<const uint16_t *>(a.logits) + row + e;
+            if (a.vec && e + 4 <= a.E) {
+                const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
+                x[c][0] = bf16_lo(v.x);
+                x[c][1] = bf16_hi(v.x);
+                x[c][2] = bf16_lo(v.y);
+                x[c][3] = bf16_hi(v.y);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (e + i < a.E)
+                        x[c][i] = bf16_lo(p[i]);
+            }
+        }
+    }
 }
 
 // Picking.  LANES lanes share a token; each holds CH * 4 of its experts as keys
@@ -90,53 +133,15 @@ __device__ __forceinline__ void finish_token(const RouteArgs &a, int t, bool liv
 // picks: k (expert, exp or sigmoid) pairs of each of the warp's tokens.
 template <int LANES, int CH>
 __device__ __forceinline__ void route_tokens(const RouteArgs &a, int t, bool live, int bit, int lane, uint4 *keys,
-                                             float2 *picks, uint32_t *masks)
+                                             float2 *picks, uint32_t *masks, int *ids)
 {
     const int l = lane & (LANES - 1);
     uint4 *mine = keys + lane;                             // chunk c at mine[32 c]: no bank conflicts
     const bool on = live && !(a.mask && a.mask[t] == 0);
     const int64_t row = static_cast<int64_t>(live ? t : 0) * a.ldl;
     uint32_t top[CH];                                      // the chunks' maxima
-    // Loads first, all in flight together.
     float x[CH][4];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-        const int e = (c * LANES + l) * 4;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            x[c][i] = __int_as_float(0xff800000);
-        if (on && e < a.E) {
-            if (a.fp32) {
-                const float *p = static_cast<const float *>(a.logits) + row + e;
-                if (a.vec && e + 4 <= a.E) {
-                    const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
-                    x[c][0] = v.x;
-                    x[c][1] = v.y;
-                    x[c][2] = v.z;
-                    x[c][3] = v.w;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (e + i < a.E)
-                            x[c][i] = p[i];
-                }
-            } else {
-                const uint16_t *p = static_cast<const uint16_t *>(a.logits) + row + e;
-                if (a.vec && e + 4 <= a.E) {
-                    const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-                    x[c][0] = bf16_lo(v.x);
-                    x[c][1] = bf16_hi(v.x);
-                    x[c][2] = bf16_lo(v.y);
-                    x[c][3] = bf16_hi(v.y);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (e + i < a.E)
-                            x[c][i] = bf16_lo(p[i]);
-                }
-            }
-        }
-    }
+    load_logits<LANES, CH>(a, on, row, l, x);
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
         const uint4 k = make_uint4(order_key(x[c][0]), order_key(x[c][1]), order_key(x[c][2]), order_key(x[c][3]));
@@ -208,7 +213,7 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, int t, bool liv
         }
     }
     __syncwarp();
-    finish_token<LANES>(a, t, live, bit, l, taken, key_value(first), sum, my_picks, masks);
+    finish_token<LANES>(a, t, live, bit, l, taken, key_value(first), sum, my_picks, masks, ids);
 }
 
 // Exclusive prefix sums of total[0 .. E) over the block, in place; returns
@@ -216,7 +221,7 @@ __device__ __forceinline__ void route_tokens(const RouteArgs &a, int t, bool liv
 __device__ __forceinline__ int block_scan(int *total, int E)
 {
     __shared__ int warp_sum[32];
-    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = (E + kRouteThreads - 1) / kRouteThreads;
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, n = (E + blockDim.x - 1) / blockDim.x;
     int sum = 0;
     for (int i = 0; i < n; ++i)
         if (t * n + i < E)
@@ -232,7 +237,7 @@ __device__ __forceinline__ int block_scan(int *total, int E)
         warp_sum[warp] = incl;
     __syncthreads();
     int before = incl - sum, all = 0;
-    for (int w = 0; w < kRouteThreads / 32; ++w) {
+    for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) {
         before += w < warp ? warp_sum[w] : 0;
         all += warp_sum[w];
     }
@@ -246,103 +251,17 @@ __device__ __forceinline__ int block_scan(int *total, int E)
     return all;
 }
 
-// After a run of tokens [s0, s1) has been picked: each row's place among its
-// expert's rows of this block, into slot_row; the block's counts move on.
-__device__ __forceinline__ void place_in_block(const RouteArgs &a, int s0, int s1, const uint32_t *masks, int *run)
-{
-    for (int i = threadIdx.x; i < (s1 - s0) * a.k; i += blockDim.x) {
-        const int64_t at = static_cast<int64_t>(s0) * a.k + i;
-        const int e = a.ids[at];
-        int place = -1;
-        if (e >= 0) {
-            const int bit = i / a.k;
-            place = run[e];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t m = masks[4 * e + w];
-                place += w < (bit >> 5) ? __popc(m) : w == (bit >> 5) ? __popc(m & ((1u << (bit & 31)) - 1u)) : 0;
-            }
-        }
-        a.slot_row[at] = place;
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x)
-        run[e] += __popc(masks[4 * e]) + __popc(masks[4 * e + 1]) + __popc(masks[4 * e + 2]) + __popc(masks[4 * e + 3]);
-    __syncthreads();
-}
-
-__device__ __forceinline__ void write_counts(const RouteArgs &a, const int *run)
-{
-    const int ep = (a.E + 7) / 8 * 8;
-    uint16_t *count = a.counts + static_cast<int64_t>(blockIdx.x) * ep;
-    for (int e = threadIdx.x; e < ep; e += blockDim.x)
-        count[e] = e < a.E ? static_cast<uint16_t>(run[e]) : uint16_t(0);
-}
-
-template <int LANES, int CH>
-__global__ void __launch_bounds__(kRouteThreads, 2) route_pick_kernel(const __grid_constant__ RouteArgs a)
-{
-    constexpr int TPW = 32 / LANES;                        // tokens of a warp
-    extern __shared__ __align__(16) uint32_t smem_u32[];
-    uint4 *all_keys = reinterpret_cast<uint4 *>(smem_u32); // [warps][CH][32]
-    float2 *all_picks = reinterpret_cast<float2 *>(all_keys + kRouteThreads * CH);   // [warps][TPW][k]
-    uint32_t *masks = reinterpret_cast<uint32_t *>(all_picks + kRouteThreads / LANES * a.k);   // [E][4]
-    int *run = reinterpret_cast<int *>(masks + 4 * a.E);   // [E]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = blockIdx.x * a.chunk;
-    const int t1 = min(a.T, t0 + a.chunk);
-    const bool single = gridDim.x == 1;
-    for (int i = threadIdx.x; i < a.E; i += kRouteThreads)
-        run[i] = 0;
-    pdl_wait_prerequisites();
-    if (threadIdx.x == 0)
-        pdl_launch_dependents();
-    for (int s0 = t0; s0 < t1; s0 += kRouteRun) {
-        for (int i = threadIdx.x; i < 4 * a.E; i += kRouteThreads)
-            masks[i] = 0u;
-        __syncthreads();
-        const int s1 = min(t1, s0 + kRouteRun);
-        for (int q = s0 + warp * TPW; q < s1; q += kRouteThreads / 32 * TPW) {
-            const int t = q + lane / LANES;
-            route_tokens<LANES, CH>(a, t, t < s1, t - s0, lane, all_keys + warp * CH * 32, all_picks + warp * TPW * a.k,
-                                    masks);
-        }
-        __syncthreads();
-        place_in_block(a, s0, s1, masks, run);
-    }
-    if (!single) {
-        write_counts(a, run);
-        return;
-    }
-    const int all = block_scan(run, a.E);
-    for (int e = threadIdx.x; e <= a.E; e += kRouteThreads)
-        a.offsets[e] = e < a.E ? run[e] : all;
-    for (int i = threadIdx.x; i < a.T * a.k; i += kRouteThreads) {
-        const int e = a.ids[i];
-        if (e >= 0) {
-            const int row = run[e] + a.slot_row[i];
-            a.slot_row[i] = row;
-            a.row_token[row] = i / a.k;
-        }
-        if (i >= all)
-            a.row_token[i] = -1;
-    }
-}
-
-// Many tokens, k <= 8.  LANES lanes hold a token's experts, 32 each, in
-// registers.  The k-th largest of the maxima of its groups of eight experts is
-// a bound that the k-th largest logit is not below: the lanes sort their four
-// maxima and merge the lists in a butterfly.  The logits at or above the bound,
-// little more than k, are set down in shared memory, and each one's place is
-// the number of larger ones (and of equal ones with a lower index).  Where
-// more than fit are left, as among many equal logits, the warp picks its tokens
-// one expert at a time (route_tokens).  A token of 256 experts costs some 170
-// warp instructions; picking costs four times as many.
-constexpr int kManyThreads = 256;
-constexpr int kManyBlocksPerSm = 3;
-
+// Bounding, k <= 8.  The k-th largest of the maxima of the token's groups of
+// experts (CH / NG chunks of four, NG groups per lane) is a bound that the k-th
+// largest logit is not below: the lanes sort their maxima and merge the lists in
+// a butterfly.  The logits at or above the bound, little more than k, are set
+// down in shared memory, and each one's place is the number of larger ones (and
+// of equal ones with a lower index).  Where more than fit are left, as among
+// many equal logits, the warp picks its tokens one expert at a time instead.
+// Against picking, a quarter of the instructions, and for a lone token five
+// exchanges in a row where picking eight experts takes eighty.
 template <int LANES>
-constexpr int kManyCandidates = LANES == 1 ? 32 : 64;      // of one token
+constexpr int kCandidates = LANES == 1 || LANES == 4 ? 32 : 64;   // of one token (what shared memory leaves)
 
 __device__ __forceinline__ void exchange(float &hi, float &lo)
 {
@@ -369,196 +288,212 @@ __device__ __forceinline__ void settle8(float (&v)[8])
                 exchange(v[i], v[i | d]);
 }
 
-template <bool FP32, int LANES>
-__global__ void __launch_bounds__(kManyThreads, kManyBlocksPerSm) route_many_kernel(const __grid_constant__ RouteArgs a)
+template <int LANES, int CH>
+__device__ __forceinline__ void bound_tokens(const RouteArgs &a, int t, bool live, int bit, int lane, uint4 *keys,
+                                             float2 *picks, float2 *found, uint32_t *masks, int *ids)
+{
+    constexpr int NG = CH < 4 ? CH : 4;
+    constexpr int CAP = kCandidates<LANES>;
+    const float ninf = __int_as_float(0xff800000);
+    const int l = lane & (LANES - 1);
+    const bool on = live && !(a.mask && a.mask[t] == 0);
+    float2 *my_picks = picks + (lane / LANES) * a.k;
+    found += (lane / LANES) * CAP;
+    float x[CH][4];
+    load_logits<LANES, CH>(a, on, static_cast<int64_t>(live ? t : 0) * a.ldl, l, x);
+    float best[8];                                         // descending
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+        best[g] = ninf;
+        if (g >= NG)
+            continue;
+#pragma unroll
+        for (int c = g * (CH / NG); c < (g + 1) * (CH / NG); ++c) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[c][i] = fmaxf(x[c][i], ninf);            // NaN -> -inf
+            best[g] = max3(max3(best[g], x[c][0], x[c][1]), x[c][2], x[c][3]);
+            reinterpret_cast<float4 *>(keys)[32 * c + lane] = make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
+        }
+    }
+    if constexpr (NG >= 2)
+        exchange(best[0], best[1]);
+    if constexpr (NG == 4) {
+        exchange(best[2], best[3]);
+        exchange(best[0], best[2]);
+        exchange(best[1], best[3]);
+        exchange(best[1], best[2]);
+    }
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d >>= 1) {
+        // The elementwise maxima of one list and the other reversed are the
+        // eight largest of both, as a bitonic sequence (both lanes read each
+        // other's list as it was).
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = __shfl_xor_sync(kFull, best[i], d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            best[i] = fmaxf(best[i], w[7 - i]);
+        settle8(best);
+    }
+    const float top = best[0];
+    float bar = best[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j)
+        bar = j < a.k ? best[j] : bar;
+    float sum = 0.0f;
+    if (a.mode == 1 && top > ninf) {
+        // Terms far below the largest do not matter to the sum, so the fast
+        // exponential keeps it to a few 2^-24 of itself.
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sum += x[c][i] == top ? 1.0f : __expf(x[c][i] - top);
+    }
+    const float low = fmaxf(bar, -3.402823466e38f);        // -inf is no candidate
+    uint32_t hits = 0u;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            hits |= x[c][i] >= low ? 1u << (4 * c + i) : 0u;
+    // This lane's place among the token's candidates, and their number.
+    const int own = __popc(hits);
+    int upto = own;
+#pragma unroll
+    for (int d = 1; d < LANES; d <<= 1) {
+        const int v = __shfl_up_sync(kFull, upto, d, LANES);
+        if (l >= d)
+            upto += v;
+    }
+    const int n = __shfl_sync(kFull, upto, LANES - 1, LANES);
+    __syncwarp();
+    if (__any_sync(kFull, n > CAP)) {
+        route_tokens<LANES, CH>(a, t, live, bit, lane, keys, picks, masks, ids);
+        return;
+    }
+    for (int at = upto - own; hits; ++at) {
+        const int b = __ffs(hits) - 1;
+        hits &= hits - 1u;
+        const float z = reinterpret_cast<const float *>(keys + 32 * (b >> 2) + lane)[b & 3];
+        found[at] = make_float2(__int_as_float(((b >> 2) * LANES + l) * 4 + (b & 3)), z);
+    }
+    __syncwarp();
+    for (int i = l; i < n; i += LANES) {
+        const float2 f = found[i];
+        int place = 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+            const float2 o = found[j];
+            place += o.y > f.y || (o.y == f.y && __float_as_int(o.x) < __float_as_int(f.x)) ? 1 : 0;
+        }
+        if (place < a.k)
+            my_picks[place] = f;
+    }
+    __syncwarp();
+    finish_token<LANES>(a, t, live, bit, l, min(n, a.k), top, sum, my_picks, masks, ids);
+}
+
+// The place of slot i of the run among its expert's rows of the run: the
+// tokens before its own in the expert's mask.
+__device__ __forceinline__ int place_in_run(const uint32_t *masks, int e, int bit)
+{
+    int place = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const uint32_t m = masks[4 * e + w];
+        place += w < (bit >> 5) ? __popc(m) : w == (bit >> 5) ? __popc(m & ((1u << (bit & 31)) - 1u)) : 0;
+    }
+    return place;
+}
+
+// BOUND: bound_tokens (k <= 8), else route_tokens.
+template <int THREADS, int BLOCKS, int LANES, int CH, bool BOUND>
+__global__ void __launch_bounds__(THREADS, BLOCKS) route_pick_kernel(const __grid_constant__ RouteArgs a)
 {
     constexpr int TPW = 32 / LANES;                        // tokens of a warp
-    constexpr int CAP = kManyCandidates<LANES>;
+    constexpr int WARPS = THREADS / 32;
     extern __shared__ __align__(16) uint32_t smem_u32[];
-    uint4 *all_keys = reinterpret_cast<uint4 *>(smem_u32); // [warps][8][32]
-    float2 *all_picks = reinterpret_cast<float2 *>(all_keys + kManyThreads * 8);     // [warps][TPW][k]
-    float2 *all_found = all_picks + kManyThreads / LANES * a.k;                      // [warps][TPW][CAP]
-    uint32_t *masks = reinterpret_cast<uint32_t *>(all_found + kManyThreads / LANES * CAP);   // [E][4]
+    uint4 *all_keys = reinterpret_cast<uint4 *>(smem_u32); // [warps][CH][32]
+    float2 *all_picks = reinterpret_cast<float2 *>(all_keys + THREADS * CH);         // [warps][TPW][k]
+    float2 *all_found = all_picks + WARPS * TPW * a.k;                               // [warps][TPW][candidates]
+    uint32_t *masks = reinterpret_cast<uint32_t *>(all_found + (BOUND ? WARPS * TPW * kCandidates<LANES> : 0));   // [E][4]
     int *run = reinterpret_cast<int *>(masks + 4 * a.E);   // [E]
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane & (LANES - 1);
+    int *ids = run + a.E;                                  // [tokens of a run][k]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * a.chunk;
     const int t1 = min(a.T, t0 + a.chunk);
-    uint4 *keys = all_keys + warp * 8 * 32;
-    float2 *picks = all_picks + warp * TPW * a.k;
-    float2 *my_picks = picks + (lane / LANES) * a.k;
-    float2 *found = all_found + (warp * TPW + lane / LANES) * CAP;
-    for (int i = threadIdx.x; i < a.E; i += kManyThreads)
-        run[i] = 0;
+    for (int i = threadIdx.x; i < 5 * a.E; i += THREADS)
+        masks[i] = 0u;                                     // run too
     pdl_wait_prerequisites();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
-    const float ninf = __int_as_float(0xff800000);
     for (int s0 = t0; s0 < t1; s0 += kRouteRun) {
-        for (int i = threadIdx.x; i < 4 * a.E; i += kManyThreads)
-            masks[i] = 0u;
         __syncthreads();
         const int s1 = min(t1, s0 + kRouteRun);
-        for (int q = s0 + warp * TPW; q < s1; q += kManyThreads / 32 * TPW) {
+        for (int q = s0 + warp * TPW; q < s1; q += WARPS * TPW) {
             const int t = q + lane / LANES;
-            const bool live = t < s1;
-            const bool on = live && !(a.mask && a.mask[t] == 0);
-            const int64_t row = static_cast<int64_t>(live ? t : 0) * a.ldl;
-            float x[8][4];                                 // expert (c LANES + l) 4 + i
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const int e = (c * LANES + l) * 4;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    x[c][i] = ninf;
-                if (!on || e >= a.E)
-                    continue;
-                if constexpr (FP32) {
-                    const float *p = static_cast<const float *>(a.logits) + row + e;
-                    if (a.vec && e + 4 <= a.E) {
-                        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p));
-                        x[c][0] = v.x;
-                        x[c][1] = v.y;
-                        x[c][2] = v.z;
-                        x[c][3] = v.w;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (e + i < a.E)
-                                x[c][i] = p[i];
-                    }
-                } else {
-                    const uint16_t *p = static_cast<const uint16_t *>(a.logits) + row + e;
-                    if (a.vec && e + 4 <= a.E) {
-                        const uint2 v = __ldcs(reinterpret_cast<const uint2 *>(p));
-                        x[c][0] = bf16_lo(v.x);
-                        x[c][1] = bf16_hi(v.x);
-                        x[c][2] = bf16_lo(v.y);
-                        x[c][3] = bf16_hi(v.y);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (e + i < a.E)
-                                x[c][i] = bf16_lo(p[i]);
-                    }
-                }
-            }
-            float best[8];                                 // descending
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                float m = ninf;
-#pragma unroll
-                for (int c = 2 * g; c < 2 * g + 2; ++c) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[c][i] = fmaxf(x[c][i], ninf);    // NaN -> -inf
-                    m = max3(max3(m, x[c][0], x[c][1]), x[c][2], x[c][3]);
-                    reinterpret_cast<float4 *>(keys)[32 * c + lane] = make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
-                }
-                best[g] = m;
-                best[4 + g] = ninf;
-            }
-            exchange(best[0], best[1]);
-            exchange(best[2], best[3]);
-            exchange(best[0], best[2]);
-            exchange(best[1], best[3]);
-            exchange(best[1], best[2]);
-#pragma unroll
-            for (int d = LANES / 2; d > 0; d >>= 1) {
-                // The elementwise maxima of one list and the other reversed are
-                // the eight largest of both, as a bitonic sequence (both lanes
-                // read each other's list as it was).
-                float w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] = __shfl_xor_sync(kFull, best[i], d);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    best[i] = fmaxf(best[i], w[7 - i]);
-                settle8(best);
-            }
-            const float top = best[0];
-            float bar = best[0];
-#pragma unroll
-            for (int j = 1; j < 8; ++j)
-                bar = j < a.k ? best[j] : bar;
-            float sum = 0.0f;
-            if (a.mode == 1 && top > ninf) {
-                // Terms far below the largest do not matter to the sum, so the
-                // fast exponential keeps it to a few 2^-24 of itself.
-                if (top < __int_as_float(0x7f800000)) {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sum += __expf(x[c][i] - top);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sum += x[c][i] == top ? 1.0f : 0.0f;
-                }
-            }
-            const float low = fmaxf(bar, -3.402823466e38f);        // -inf is no candidate
-            uint32_t hits = 0u;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    hits |= x[c][i] >= low ? 1u << (4 * c + i) : 0u;
-            // This lane's place among the token's candidates, and their number.
-            const int own = __popc(hits);
-            int upto = own;
-#pragma unroll
-            for (int d = 1; d < LANES; d <<= 1) {
-                const int v = __shfl_up_sync(kFull, upto, d, LANES);
-                if (l >= d)
-                    upto += v;
-            }
-            const int n = __shfl_sync(kFull, upto, LANES - 1, LANES);
-            if (__any_sync(kFull, n > CAP)) {
-                __syncwarp();
-                route_tokens<LANES, 8>(a, t, live, t - s0, lane, keys, picks, masks);
-                continue;
-            }
-            __syncwarp();
-            for (int at = upto - own; hits; ++at) {
-                const int b = __ffs(hits) - 1;
-                hits &= hits - 1u;
-                const float z = reinterpret_cast<const float *>(keys + 32 * (b >> 2) + lane)[b & 3];
-                found[at] = make_float2(__int_as_float(((b >> 2) * LANES + l) * 4 + (b & 3)), z);
-            }
-            __syncwarp();
-            for (int i = l; i < n; i += LANES) {
-                const float2 f = found[i];
-                int place = 0;
-                for (int j = 0; j < n; ++j) {
-                    const float2 o = found[j];
-                    place += o.y > f.y || (o.y == f.y && __float_as_int(o.x) < __float_as_int(f.x)) ? 1 : 0;
-                }
-                if (place < a.k)
-                    my_picks[place] = f;
-            }
-            __syncwarp();
-            finish_token<LANES>(a, t, live, t - s0, l, min(n, a.k), top, sum, my_picks, masks);
+            uint4 *keys = all_keys + warp * CH * 32;
+            float2 *picks = all_picks + warp * TPW * a.k;
+            if constexpr (BOUND)
+                bound_tokens<LANES, CH>(a, t, t < s1, t - s0, lane, keys, picks,
+                                        all_found + warp * TPW * kCandidates<LANES>, masks, ids);
+            else
+                route_tokens<LANES, CH>(a, t, t < s1, t - s0, lane, keys, picks, masks, ids);
         }
         __syncthreads();
-        place_in_block(a, s0, s1, masks, run);
+        if (a.blocks == 1)
+            break;                                         // one run: kRouteSingle tokens at most
+        for (int i = threadIdx.x; i < (s1 - s0) * a.k; i += THREADS) {
+            const int e = ids[i];
+            a.slot_row[static_cast<int64_t>(s0) * a.k + i] = e >= 0 ? run[e] + place_in_run(masks, e, i / a.k) : -1;
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < a.E; e += THREADS) {
+            uint4 *m = reinterpret_cast<uint4 *>(masks) + e;
+            run[e] += __popc(m->x) + __popc(m->y) + __popc(m->z) + __popc(m->w);
+            *m = make_uint4(0u, 0u, 0u, 0u);
+        }
     }
-    write_counts(a, run);
+    if (a.blocks > 1) {
+        __syncthreads();
+        const int ep = (a.E + 7) / 8 * 8;
+        uint16_t *count = a.counts + static_cast<int64_t>(blockIdx.x) * ep;
+        for (int e = threadIdx.x; e < ep; e += THREADS)
+            count[e] = e < a.E ? static_cast<uint16_t>(run[e]) : uint16_t(0);
+        return;
+    }
+    for (int e = threadIdx.x; e < a.E; e += THREADS)
+        run[e] = __popc(masks[4 * e]) + __popc(masks[4 * e + 1]) + __popc(masks[4 * e + 2]) + __popc(masks[4 * e + 3]);
+    __syncthreads();
+    const int all = block_scan(run, a.E);
+    for (int e = threadIdx.x; e <= a.E; e += THREADS)
+        a.offsets[e] = e < a.E ? run[e] : all;
+    for (int i = threadIdx.x; i < a.T * a.k; i += THREADS) {
+        const int e = ids[i], t = i / a.k;
+        const int row = e >= 0 ? run[e] + place_in_run(masks, e, t) : -1;
+        a.slot_row[i] = row;
+        if (row >= 0)
+            a.row_token[row] = t;
+        if (i >= all)
+            a.row_token[i] = -1;
+    }
 }
 
-// Block p takes the tokens of `per` picking blocks from p * per on: it adds up
-// all blocks' counts and those before its own, then places its rows.
-__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid_constant__ RouteArgs a, int per)
+// Each block adds up all picking blocks' counts and those before its own, then
+// places the rows of the tokens that picking block had.
+__global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid_constant__ RouteArgs a)
 {
     extern __shared__ __align__(16) uint32_t smem_u32[];
     const int ep = (a.E + 7) / 8 * 8, lanes = ep / 8;      // threads of one block's counts
-    const int b0 = blockIdx.x * per, b1 = min(a.blocks, b0 + per);
+    const int me = blockIdx.x;
     const int at_once = kRouteThreads / lanes;             // blocks whose counts are read together
     uint32_t *part = smem_u32;                             // [at_once][2][ep]: all blocks, the blocks before
     int *total = reinterpret_cast<int *>(part + 2 * at_once * ep);   // [ep]
-    int *mine = total + ep;                                // [per][ep]
+    int *mine = total + ep;                                // [ep]
     pdl_wait_prerequisites();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
@@ -568,58 +503,60 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             all[i] = before[i] = 0u;
+        // Two counts share a word while their sums stay below 2^16.
+        const int safe = 65535 / a.chunk * at_once;
+        for (int f = g; f < a.blocks; f += safe) {
+            uint4 s = make_uint4(0u, 0u, 0u, 0u), p = s;
 #pragma unroll 8
-        for (int b = g; b < a.blocks; b += at_once) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(a.counts + static_cast<int64_t>(b) * ep + 8 * q);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            for (int b = f; b < min(a.blocks, f + safe); b += at_once) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(a.counts + static_cast<int64_t>(b) * ep + 8 * q);
+                s.x += v.x;
+                s.y += v.y;
+                s.z += v.z;
+                s.w += v.w;
+                if (b < me) {
+                    p.x += v.x;
+                    p.y += v.y;
+                    p.z += v.z;
+                    p.w += v.w;
+                }
+            }
+            const uint32_t sw[4] = {s.x, s.y, s.z, s.w}, pw[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const uint32_t c = (w[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
-                all[i] += c;
-                before[i] += b < b0 ? c : 0u;
+                all[i] += (sw[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
+                before[i] += (pw[i / 2] >> (16 * (i & 1))) & 0xFFFFu;
             }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            part[(2 * g) * ep + 8 * q + i] = all[i];
-            part[(2 * g + 1) * ep + 8 * q + i] = before[i];
-        }
+        uint4 *mine_part = reinterpret_cast<uint4 *>(part + 2 * g * ep + 8 * q);
+        mine_part[0] = make_uint4(all[0], all[1], all[2], all[3]);
+        mine_part[1] = make_uint4(all[4], all[5], all[6], all[7]);
+        mine_part = reinterpret_cast<uint4 *>(part + (2 * g + 1) * ep + 8 * q);
+        mine_part[0] = make_uint4(before[0], before[1], before[2], before[3]);
+        mine_part[1] = make_uint4(before[4], before[5], before[6], before[7]);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * ep; i += kRouteThreads) {
         uint32_t s = 0u;
+#pragma unroll 4
         for (int g = 0; g < at_once; ++g)
             s += part[2 * g * ep + i];
-        total[i] = static_cast<int>(s);                    // total, then mine[0]
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kRouteThreads) {
-        int at = mine[e];
-        uint16_t c[kPlacePer];
-#pragma unroll
-        for (int i = 0; i < kPlacePer; ++i)
-            c[i] = b0 + i < b1 ? a.counts[static_cast<int64_t>(b0 + i) * ep + e] : uint16_t(0);
-#pragma unroll
-        for (int i = 0; i < kPlacePer; ++i) {
-            if (i < per)
-                mine[i * ep + e] = at;
-            at += c[i];
-        }
+        total[i] = static_cast<int>(s);                    // total, then mine
     }
     __syncthreads();
     const int sum = block_scan(total, a.E);
-    if (blockIdx.x == 0)
+    if (me == 0)
         for (int e = threadIdx.x; e <= a.E; e += kRouteThreads)
             a.offsets[e] = e < a.E ? total[e] : sum;
     // (T k fits an int.)
     const int span = a.chunk * a.k;
-    const int i0 = b0 * span;
-    const int i1 = static_cast<int>(min(static_cast<int64_t>(a.T) * a.k, static_cast<int64_t>(b1) * span));
+    const int i0 = me * span;
+    const int i1 = static_cast<int>(min(static_cast<int64_t>(a.T) * a.k, static_cast<int64_t>(i0) + span));
 #pragma unroll 4
     for (int i = i0 + threadIdx.x; i < i1; i += kRouteThreads) {
         const int e = a.ids[i], place = a.slot_row[i];
         if (e >= 0) {
-            const int row = total[e] + mine[(i - i0) / span * ep + e] + place;
+            const int row = total[e] + mine[e] + place;
             a.slot_row[i] = row;
             a.row_token[row] = i / a.k;
         }
@@ -635,43 +572,42 @@ __global__ void route_empty_kernel(int *offsets, int E)
         offsets[e] = 0;
 }
 
-template <int LANES, int CH>
+template <int THREADS, int BLOCKS, int LANES, int CH, bool BOUND>
 cudaError_t launch_pick(const RouteArgs &a, cudaStream_t stream)
 {
+    constexpr auto kern = route_pick_kernel<THREADS, BLOCKS, LANES, CH, BOUND>;
+    auto bytes = [](int k, int E) {
+        return THREADS * CH * 16 + THREADS / LANES * (k + (BOUND ? kCandidates<LANES> : 0)) * 8 + 5 * E * 4 +
+               kRouteRun * k * 4;
+    };
     // The most that any E and k need of this instance.
-    constexpr int kMost = kRouteThreads * CH * 16 + kRouteThreads / LANES * kMaxTopK * 8 + 5 * LANES * CH * 4 * 4;
-    const size_t smem = static_cast<size_t>(kRouteThreads) * CH * 16 + static_cast<size_t>(kRouteThreads / LANES) * a.k * 8 +
-                        static_cast<size_t>(5 * a.E) * 4;
-    const cudaError_t e = opt_in<route_pick_kernel<LANES, CH>>(kMost);
+    const cudaError_t e = opt_in<kern>(bytes(BOUND ? 8 : kMaxTopK, LANES * CH * 4));
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(route_pick_kernel<LANES, CH>, dim3(a.blocks), dim3(kRouteThreads), smem, stream, a);
+    return launch_dependent(kern, dim3(a.blocks), dim3(THREADS), static_cast<size_t>(bytes(a.k, a.E)), stream, a);
 }
 
-template <bool FP32, int LANES>
-cudaError_t launch_many(const RouteArgs &a, cudaStream_t stream)
+// A warp per token, four experts per chunk and lane.
+template <bool BOUND>
+cudaError_t launch_warps(const RouteArgs &a, cudaStream_t stream)
 {
-    constexpr int kCap = kManyCandidates<LANES>;
-    constexpr int kMost = kManyThreads * 8 * 16 + kManyThreads / LANES * (8 + kCap) * 8 + 5 * LANES * 32 * 4;
-    const size_t smem = static_cast<size_t>(kManyThreads) * 8 * 16 +
-                        static_cast<size_t>(kManyThreads / LANES) * (a.k + kCap) * 8 +
-                        static_cast<size_t>(5 * a.E) * 4;
-    const cudaError_t e = opt_in<route_many_kernel<FP32, LANES>>(kMost);
-    if (e != cudaSuccess)
-        return e;
-    return launch_dependent(route_many_kernel<FP32, LANES>, dim3(a.blocks), dim3(kManyThreads), smem, stream, a);
+    return a.E <= 128   ? launch_pick<kRouteThreads, 2, 32, 1, BOUND>(a, stream)
+           : a.E <= 256 ? launch_pick<kRouteThreads, 2, 32, 2, BOUND>(a, stream)
+           : a.E <= 512 ? launch_pick<kRouteThreads, 2, 32, 4, BOUND>(a, stream)
+                        : launch_pick<kRouteThreads, 1, 32, 8, BOUND>(a, stream);
 }
 
-template <bool FP32>
-cudaError_t launch_many_lanes(const RouteArgs &a, int lanes, cudaStream_t stream)
+// `lanes` lanes per token.
+template <bool BOUND>
+cudaError_t launch_lanes(const RouteArgs &a, int lanes, cudaStream_t stream)
 {
     switch (lanes) {
-    case 1: return launch_many<FP32, 1>(a, stream);
-    case 2: return launch_many<FP32, 2>(a, stream);
-    case 4: return launch_many<FP32, 4>(a, stream);
-    case 8: return launch_many<FP32, 8>(a, stream);
-    case 16: return launch_many<FP32, 16>(a, stream);
-    default: return launch_many<FP32, 32>(a, stream);
+    case 1: return launch_pick<384, 1, 1, 8, BOUND>(a, stream);
+    case 2: return launch_pick<512, 1, 2, 8, BOUND>(a, stream);
+    case 4: return launch_pick<1024, 1, 4, 8, BOUND>(a, stream);
+    case 8: return launch_pick<1024, 1, 8, 8, BOUND>(a, stream);
+    case 16: return launch_pick<1024, 1, 16, 8, BOUND>(a, stream);
+    default: return launch_pick<1024, 1, 32, 8, BOUND>(a, stream);
     }
 }
 
@@ -681,7 +617,7 @@ int route_blocks(int T, int *chunk)
 {
     int c = T <= kRouteSingle ? kRouteSingle : 32;
     if (T > 32 * kRouteMaxBlocks)
-        c = ((T + kRouteMaxBlocks - 1) / kRouteMaxBlocks + 3) / 4 * 4;      // one even wave
+        c = (T + kRouteMaxBlocks - 1) / kRouteMaxBlocks;
     *chunk = c;
     return (T + c - 1) / c;
 }
@@ -693,38 +629,24 @@ cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream)
     // Lanes per token: as few as hold its experts in 32 registers each, which
     // shares the instructions among the most tokens, once that still leaves
     // every SM 16 warps; otherwise a whole warp per token, the shortest time
-    // for one.
+    // for one.  One block of 32 warps per SM: with three of 8 the placing kernel
+    // has three times the counts to read (32768 tokens of 256 experts: 26.9
+    // against 31.5 us for both kernels).
     int lanes = 1;
     while (lanes * 32 < a.E)
         lanes *= 2;
     const bool many = static_cast<int64_t>(a.T) * lanes / 32 >= static_cast<int64_t>(sms) * 16;
-    cudaError_t e;
-    if (!many) {
-        e = a.E <= 128   ? launch_pick<32, 1>(a, stream)
-            : a.E <= 256 ? launch_pick<32, 2>(a, stream)
-            : a.E <= 512 ? launch_pick<32, 4>(a, stream)
-                         : launch_pick<32, 8>(a, stream);
-    } else if (a.k <= 8) {
-        e = a.fp32 ? launch_many_lanes<true>(a, lanes, stream) : launch_many_lanes<false>(a, lanes, stream);
-    } else {
-        switch (lanes) {
-        case 1: e = launch_pick<1, 8>(a, stream); break;
-        case 2: e = launch_pick<2, 8>(a, stream); break;
-        case 4: e = launch_pick<4, 8>(a, stream); break;
-        case 8: e = launch_pick<8, 8>(a, stream); break;
-        case 16: e = launch_pick<16, 8>(a, stream); break;
-        default: e = launch_pick<32, 8>(a, stream); break;
-        }
-    }
-    if (e != cudaSuccess || a.blocks == 1)
-        return e;
+    const bool bound = a.k <= 8;
+    const cudaError_t picked = many ? (bound ? launch_lanes<true>(a, lanes, stream) : launch_lanes<false>(a, lanes, stream))
+                                    : (bound ? launch_warps<true>(a, stream) : launch_warps<false>(a, stream));
+    if (picked != cudaSuccess || a.blocks == 1)
+        return picked;
     const int ep = (a.E + 7) / 8 * 8;
-    const int per = (a.blocks + kPlaceBlocks - 1) / kPlaceBlocks;
-    const size_t smem2 = static_cast<size_t>(2 * (kRouteThreads / (ep / 8)) + 1 + per) * ep * 4;
-    e = opt_in<route_place_kernel>(kPlaceSmem);
+    const size_t smem = static_cast<size_t>(2 * (kRouteThreads / (ep / 8)) + 2) * ep * 4;
+    const cudaError_t e = opt_in<route_place_kernel>(kPlaceSmem);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(route_place_kernel, dim3((a.blocks + per - 1) / per), dim3(kRouteThreads), smem2, stream, a, per);
+    return launch_dependent(route_place_kernel, dim3(a.blocks), dim3(kRouteThreads), smem, stream, a);
 }
 
 }  // namespace mxfp4

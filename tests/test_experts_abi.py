@@ -100,7 +100,7 @@ def test_sizes():
     assert mx.mxfp4_group_scale_size(256, 8, 512) == 10 * 4 * 512
     assert mx.mxfp4_group_scale_size(10, 0, 32) == mx.mxfp4_group_scale_size(10, 1, 31) == 0
     assert mx.mxfp4_moe_route_workspace_size(64, 128) == 0
-    assert mx.mxfp4_moe_route_workspace_size(10 ** 6, 128) <= 456 * 128 * 2
+    assert mx.mxfp4_moe_route_workspace_size(10 ** 6, 128) <= 152 * 128 * 2
     assert mx.mxfp4_moe_route_workspace_size(-1, 128) == 0
     whole = mx.mxfp4_moe_ffn_workspace_size(100, 8, 2, 512, 256)
     parts = 200 * (256 + 128 + 1024) + mx.mxfp4_group_scale_size(200, 8, 512) + mx.mxfp4_group_scale_size(200, 8, 256)
