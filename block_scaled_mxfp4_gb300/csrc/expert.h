@@ -121,7 +121,7 @@ struct GroupedArgs {
 };
 struct GroupedMaps {
     CUtensorMap A, A32, SA, B, SB;   // A: boxes of 128 rows, A32: of 32
-    CUtensorMap D;                   // plain form with tma_ok: boxes of 32 rows x 64 columns
+    CUtensorMap D;                   // plain form with tma_ok: boxes of 32 rows x 32 columns
 };
 // out: -1 plain (bf16), else the QuantFmt of the gated form's output.
 size_t grouped_workspace_bytes(int rows, int groups, int N, int K, bool gated, int sms);

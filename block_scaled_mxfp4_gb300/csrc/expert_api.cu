@@ -153,8 +153,8 @@ int run_product(const Product &p, int sms, cudaStream_t stream)
         a.tma_ok = a.vec_ok;
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.rows)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.ldd) * 2};
-        const cuuint32_t box[2] = {64, 32};
-        if (a.tma_ok && !encode(&m.D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.D, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        const cuuint32_t box[2] = {32, 32};
+        if (a.tma_ok && !encode(&m.D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.D, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
             return MXFP4_ERR_CUDA;
     }
     if (p.bytes8)

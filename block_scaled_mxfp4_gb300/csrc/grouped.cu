@@ -100,14 +100,16 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+constexpr int kOutBoxBytes = 32 * 64;            // one epilogue warp's 32 rows x 32 bf16
+
 // BYTES8: byte formats, 128 K and one scale atom per stage and 128-row block;
 // otherwise packed E2M1, 256 K and two atoms.
-// The plain form gives one stage up for the epilogue's boxes.
-constexpr int kOutBoxBytes = 32 * 128;           // one epilogue warp's 32 rows x 64 bf16
-
-template <bool BYTES8, bool GATED>
+// The plain form's epilogue keeps a 2 KB box per warp beside the ring.  Six
+// stages then leave little room for the tile list, so that more groups than
+// that (WIDE) run with five: 32768 rows, N = 4096, K = 2048: 107 against 113 us.
+template <bool BYTES8, bool GATED, bool WIDE>
 struct GroupedCfg {
-    static constexpr int STAGES = GATED ? 6 : 5;
+    static constexpr int STAGES = !GATED && WIDE ? 5 : 6;
     static constexpr int OUT_BYTES = GATED ? 0 : 8 * kOutBoxBytes;
     static constexpr int G = BYTES8 ? 1 : 2;
     static constexpr int A_BYTES = 128 * 128;
@@ -116,9 +118,15 @@ struct GroupedCfg {
     static constexpr int SFB_BYTES = 2 * G * kSfAtomBytes;
     static constexpr int STAGE_BYTES = (A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES + 1023) / 1024 * 1024;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
-    static constexpr int BAR_BYTES = 512;
-    static constexpr int TABLE_BYTES = 2 * (kMaxGroups + 1) * 4;   // offsets and row-tile prefix sums
-    static constexpr int SMEM_BYTES = RING_BYTES + OUT_BYTES + BAR_BYTES + TABLE_BYTES + 1024;
+    static constexpr int BAR_BYTES = 256;
+    static constexpr int MAX_GROUPS = !GATED && !WIDE ? 80 : kMaxGroups;
+    static constexpr int TABLE_BYTES = 2 * (MAX_GROUPS + 1) * 4;   // offsets and row-tile prefix sums
+    static constexpr int USED_BYTES = RING_BYTES + OUT_BYTES + BAR_BYTES + TABLE_BYTES;
+    // The ring wants 1024-byte alignment.  Dynamic shared memory starts on such
+    // a boundary in a kernel without static shared memory; where there is
+    // room, the start may still be rounded up.
+    static constexpr int SLACK = USED_BYTES + 1024 <= 227 * 1024 ? 1024 : 0;
+    static constexpr int SMEM_BYTES = USED_BYTES + SLACK;
     static constexpr int SF_COLS_A = 4 * G;
     static constexpr int SF_COLS_B = 8 * G;
     static constexpr int SF_COLS = SF_COLS_A + SF_COLS_B;
@@ -175,10 +183,10 @@ __device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
     return r;
 }
 
-// Fill the tables: thread t takes groups 2t and 2t + 1 of up to 1024.
-__device__ __forceinline__ void build_tables(const GroupedArgs &a, int *off, int *base)
+// Fill the tables: thread t takes groups 2t and 2t + 1 of up to 1024.  warp_sum:
+// 16 words of shared memory.
+__device__ __forceinline__ void build_tables(const GroupedArgs &a, int *off, int *base, int *warp_sum)
 {
-    __shared__ int warp_sum[16];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
     int o[3];
 #pragma unroll
@@ -328,16 +336,21 @@ __device__ __forceinline__ void store_gated(const GroupedArgs &a, int r, int loc
 }
 
 // OUT: -1 plain bf16, else static_cast<int>(QuantFmt) of the gated form.
-template <bool BYTES8, int OUT>
+template <bool BYTES8, int OUT, bool WIDE>
 __global__ void __launch_bounds__(512, 1)
     grouped_pair(const __grid_constant__ GroupedArgs a, const __grid_constant__ GroupedMaps maps)
 {
-    using Cf = GroupedCfg<BYTES8, (OUT >= 0)>;
+    using Cf = GroupedCfg<BYTES8, (OUT >= 0), WIDE>;
     constexpr int G = Cf::G;
     constexpr bool GATED = OUT >= 0;
     constexpr int STAGES = Cf::STAGES;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
+    if (Cf::SLACK == 0 && (raw & 1023u)) {       // (never seen; see GroupedCfg)
+        if (threadIdx.x == 0)
+            atomicExch(&g_status, -5 /* MXFP4_ERR_CUDA */);
+        return;
+    }
     uint8_t *smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
     uint8_t *stage_out = smem + Cf::RING_BYTES;     // the plain epilogue's boxes
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cf::RING_BYTES + Cf::OUT_BYTES);
@@ -348,8 +361,10 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t *drain = acc_empty + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *warp_sum = reinterpret_cast<int *>(tmem_slot + 2);
+    static_assert((3 * STAGES + 3) * 8 + 8 + 64 <= Cf::BAR_BYTES, "barriers");
     int *tab_off = reinterpret_cast<int *>(smem + Cf::RING_BYTES + Cf::OUT_BYTES + Cf::BAR_BYTES);
-    int *tab_base = tab_off + kMaxGroups + 1;
+    int *tab_base = tab_off + Cf::MAX_GROUPS + 1;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -385,7 +400,7 @@ __global__ void __launch_bounds__(512, 1)
     // everything else; with a.early only the rows and their scales do.
     if (!a.early)
         pdl_wait_prerequisites();
-    build_tables(a, tab_off, tab_base);
+    build_tables(a, tab_off, tab_base, warp_sum);
     tc_fence_before();
     cluster_sync();                          // barriers of both CTAs initialised
     tc_fence_after();
@@ -437,31 +452,29 @@ __global__ void __launch_bounds__(512, 1)
                 const int n0 = tl.q * 256 + half * 128;
                 const int first = r - lane;
                 if (a.tma_ok && first + 32 <= tl.end) {
-                    // The warp's 32 rows are all the group's: two boxes of 32
-                    // rows x 64 columns through shared memory (128-byte
+                    // The warp's 32 rows are all the group's: four boxes of 32
+                    // rows x 32 columns through shared memory (64-byte
                     // swizzle), stored by TMA.  A thread's own 32-byte stores
                     // touch a line each, and 64 KB of them per tile hold up
                     // the MMA warp's barrier polls in the same queue.
                     uint8_t *buf = stage_out + (half * 4 + quarter) * kOutBoxBytes;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (n0 + 64 * c >= a.N)
+                    for (int c = 0; c < 4; ++c) {
+                        if (n0 + 32 * c >= a.N)
                             break;
-                        uint32_t out[2][16];
-                        round_bf16(a, acc[2 * c], out[0]);
-                        round_bf16(a, acc[2 * c + 1], out[1]);
+                        uint32_t out[16];
+                        round_bf16(a, acc[c], out);
                         if (lane == 0)
                             bulk_wait_read();
                         __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
-                                make_uint4(out[j / 4][4 * (j % 4)], out[j / 4][4 * (j % 4) + 1],
-                                           out[j / 4][4 * (j % 4) + 2], out[j / 4][4 * (j % 4) + 3]);
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
+                                make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_2d(&maps.D, buf, n0 + 64 * c, first);
+                            tma_store_2d(&maps.D, buf, n0 + 32 * c, first);
                             bulk_commit();
                         }
                     }
@@ -669,11 +682,11 @@ __global__ void __launch_bounds__(512, 1)
     }
 }
 
-template <bool BYTES8, int OUT>
+template <bool BYTES8, int OUT, bool WIDE>
 cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t stream)
 {
-    using Cf = GroupedCfg<BYTES8, (OUT >= 0)>;
-    auto kern = grouped_pair<BYTES8, OUT>;
+    using Cf = GroupedCfg<BYTES8, (OUT >= 0), WIDE>;
+    auto kern = grouped_pair<BYTES8, OUT, WIDE>;
     static std::atomic<int> max_clusters[64];   // per device; 0 = not yet queried
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -730,11 +743,15 @@ size_t grouped_workspace_bytes(int, int, int, int, bool, int) { return 0; }
 cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, int,
                            cudaStream_t stream)
 {
+    const bool wide = a.groups > GroupedCfg<false, false, false>::MAX_GROUPS;
     switch (out) {
-    case -1: return bytes8 ? launch_one<true, -1>(a, m, stream) : launch_one<false, -1>(a, m, stream);
-    case 0: return bytes8 ? cudaErrorInvalidValue : launch_one<false, 0>(a, m, stream);
-    case 1: return bytes8 ? launch_one<true, 1>(a, m, stream) : cudaErrorInvalidValue;
-    case 2: return bytes8 ? launch_one<true, 2>(a, m, stream) : cudaErrorInvalidValue;
+    case -1:
+        if (wide)
+            return bytes8 ? launch_one<true, -1, true>(a, m, stream) : launch_one<false, -1, true>(a, m, stream);
+        return bytes8 ? launch_one<true, -1, false>(a, m, stream) : launch_one<false, -1, false>(a, m, stream);
+    case 0: return bytes8 ? cudaErrorInvalidValue : launch_one<false, 0, true>(a, m, stream);
+    case 1: return bytes8 ? launch_one<true, 1, true>(a, m, stream) : cudaErrorInvalidValue;
+    case 2: return bytes8 ? launch_one<true, 2, true>(a, m, stream) : cudaErrorInvalidValue;
     default: return cudaErrorInvalidValue;
     }
 }
