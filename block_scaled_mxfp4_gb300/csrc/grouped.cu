@@ -161,11 +161,10 @@ __device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
 {
     // The last group whose first tile is not after i (empty groups share their
     // successor's base and are passed over).
-    const int rt = i / t.nt;
     int lo = 0, hi = t.groups - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (t.base[mid] <= rt)
+        if (t.base[mid] * t.nt <= i)
             lo = mid;
         else
             hi = mid - 1;
@@ -173,57 +172,76 @@ __device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
     Tile r;
     const int mt = t.base[lo + 1] - t.base[lo];
     const int local = i - t.base[lo] * t.nt;
-    const int p = local % mt;
-    r.e = lo;
-    r.q = local / mt;
     r.single = mt == 1;
+    r.q = r.single ? local : local / mt;
+    const int p = r.single ? 0 : local - r.q * mt;
+    r.e = lo;
     r.row0 = t.off[lo] + p * 256;
     r.end = t.off[lo + 1];
     r.sfa = static_cast<int>(group_sf_block(t.off[lo], lo)) + 2 * p;
     return r;
 }
 
-// Fill the tables: thread t takes groups 2t and 2t + 1 of up to 1024.  warp_sum:
-// 16 words of shared memory.
-__device__ __forceinline__ void build_tables(const GroupedArgs &a, int *off, int *base, int *warp_sum)
+// Fill the tables: thread t takes groups 2t and 2t + 1 of up to 1024.  Up to 64
+// groups are one warp's work and need no exchange between warps.  warp_sum: 16
+// words of shared memory.  Ends with a block barrier.
+__device__ __forceinline__ void build_tables(const int *offsets, int groups, int rows, int *off, int *base,
+                                             int *warp_sum)
 {
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    int o[3];
+    const bool one_warp = groups <= 64;
+    if (!one_warp || warp == 0) {
+        int o[3];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const int e = 2 * t + i;
-        o[i] = e <= a.groups ? min(max(a.offsets[e], 0), a.rows) : 0;
-    }
-    int c[2];
+        for (int i = 0; i < 3; ++i) {
+            const int e = 2 * t + i;
+            o[i] = e <= groups ? min(max(offsets[e], 0), rows) : 0;
+        }
+        int c[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        c[i] = 2 * t + i < a.groups ? (max(o[i + 1] - o[i], 0) + 255) / 256 : 0;
-    int sum = c[0] + c[1];
+        for (int i = 0; i < 2; ++i)
+            c[i] = 2 * t + i < groups ? (max(o[i + 1] - o[i], 0) + 255) / 256 : 0;
+        int sum = c[0] + c[1];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(kFull, sum, d);
-        if (lane >= d)
-            sum += v;
-    }
-    if (lane == 31)
-        warp_sum[warp] = sum;
-    __syncthreads();
-    int before = sum - c[0] - c[1];
-    for (int w = 0; w < warp; ++w)
-        before += warp_sum[w];
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(kFull, sum, d);
+            if (lane >= d)
+                sum += v;
+        }
+        int before = sum - c[0] - c[1];
+        if (!one_warp) {
+            if (lane == 31)
+                warp_sum[warp] = sum;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w)
+                before += warp_sum[w];
+        }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int e = 2 * t + i;
-        if (e <= a.groups) {
-            off[e] = o[i];
-            base[e] = before;
-            before += c[i];
+        for (int i = 0; i < 2; ++i) {
+            const int e = 2 * t + i;
+            if (e <= groups) {
+                off[e] = o[i];
+                base[e] = before;
+                before += c[i];
+            }
+        }
+        if (2 * t + 2 == groups) {     // the entry past this thread's pair
+            off[groups] = o[2];
+            base[groups] = before;
         }
     }
-    if (2 * t + 2 == a.groups) {       // the entry past this thread's pair
-        off[a.groups] = o[2];
-        base[a.groups] = before;
-    }
+    __syncthreads();
+}
+
+// Cluster barrier at the end: the epilogue's stores need no ordering with the
+// peer, and waiting for them here would delay the exit by their round trip.
+__device__ __forceinline__ void cluster_leave(bool stored)
+{
+    if (stored)
+        asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    else
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // 2-D tiled bulk-tensor store from shared memory (x innermost), in this
@@ -396,16 +414,22 @@ __global__ void __launch_bounds__(512, 1)
         prefetch_tensormap(&maps.B);
         prefetch_tensormap(&maps.SB);
     }
+    tc_fence_before();
+    cluster_sync();                          // barriers of both CTAs initialised
+    tc_fence_after();
+    const uint64_t keep = l2_policy_evict_last();
+    const uint64_t once = l2_policy_evict_first();
+    // Arguments that the first steps use are fetched before the wait.
+    const int *const offsets = a.offsets;
+    const int groups = a.groups, rows = a.rows, nt = a.nt;
+    asm volatile("" ::"l"(offsets), "r"(groups), "r"(rows), "r"(nt), "r"(a.kt), "r"(a.N), "l"(a.wait_limit));
     // Offsets and weights may come from the work before this grid, like
     // everything else; with a.early only the rows and their scales do.
     if (!a.early)
         pdl_wait_prerequisites();
-    build_tables(a, tab_off, tab_base, warp_sum);
-    tc_fence_before();
-    cluster_sync();                          // barriers of both CTAs initialised
-    tc_fence_after();
+    build_tables(offsets, groups, rows, tab_off, tab_base, warp_sum);
     const uint32_t tmem = *tmem_slot;
-    const TileTable table{tab_off, tab_base, a.groups, a.nt};
+    const TileTable table{tab_off, tab_base, groups, nt};
     const int tiles = table.tiles();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
@@ -440,9 +464,11 @@ __global__ void __launch_bounds__(512, 1)
                 tmem_ld_wait(acc[0], acc[1]);
                 tmem_ld_wait(acc[2], acc[3]);
             }
+            // (Nobody waits after the last tile, and an arrive in flight must not
+            // outlive the leading CTA.)
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && t + pairs < tiles) {
                 if (leader)
                     mbar_arrive(acc_empty);
                 else
@@ -499,8 +525,6 @@ __global__ void __launch_bounds__(512, 1)
                 const int role = warp == 4 ? 0 : warp - 5;   // 0: A and its scales, 1: B, 2: B's scales
                 if (role == 0 && a.early)
                     pdl_wait_prerequisites();
-                const uint64_t keep = l2_policy_evict_last();
-                const uint64_t once = l2_policy_evict_first();
                 int stage = 0;
                 uint32_t phase = 0;
                 int issued = 0;
@@ -674,8 +698,8 @@ __global__ void __launch_bounds__(512, 1)
     }
 
     tc_fence_before();
-    __syncthreads();
-    cluster_sync();            // no CTA leaves while its peer may still signal it
+    // No CTA leaves while its peer may still signal it.
+    cluster_leave(warp < 4 || (warp >= 8 && warp < 12));
     if (warp == 5) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, Cf::TMEM_COLS);
