@@ -512,8 +512,6 @@ int check_current_device(int *sms)
 
 long long current_wait_limit() { return g_wait_limit.load(); }
 
-uint32_t next_call_epoch() { return next_epoch(); }
-
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode_fn() { return tensor_map_encoder(); }
 
 }  // namespace mxfp4

@@ -16,7 +16,6 @@ namespace mxfp4 {
 // Shared with the GEMM entry points (api.cu).
 int check_current_device(int *sms);             // MXFP4_OK, _ERR_ARCH or _ERR_CUDA
 long long current_wait_limit();
-uint32_t next_call_epoch();                     // tag of a call's counters, never 0
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encode_fn();
 
 constexpr int kMaxGroups = 1024;                // experts of one call
@@ -114,9 +113,6 @@ struct GroupedArgs {
     int early;                  // offsets, B and its scales may be read before the preceding
                                 // grid ends: it is a kernel of the same call, which waited
                                 // for the work before the call
-    float *partials;            // workspace of split tiles
-    unsigned long long *tile_count;
-    uint32_t epoch;
     long long wait_limit;
 };
 struct GroupedMaps {
@@ -124,9 +120,7 @@ struct GroupedMaps {
     CUtensorMap D;                   // plain form with tma_ok: boxes of 32 rows x 32 columns
 };
 // out: -1 plain (bf16), else the QuantFmt of the gated form's output.
-size_t grouped_workspace_bytes(int rows, int groups, int N, int K, bool gated, int sms);
-cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, int sms,
-                           cudaStream_t stream);
+cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, cudaStream_t stream);
 cudaError_t read_grouped_status(int *status, int reset);
 
 }  // namespace mxfp4

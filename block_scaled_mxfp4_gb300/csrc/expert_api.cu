@@ -49,8 +49,6 @@ struct Product {
     bool bytes8;
     int fmt_a, fmt_b;
     int out;
-    void *ws;
-    size_t ws_bytes;
     bool early;             // GroupedArgs::early
 };
 
@@ -83,7 +81,7 @@ int check_product(const Product &p)
     return MXFP4_OK;
 }
 
-int run_product(const Product &p, int sms, cudaStream_t stream)
+int run_product(const Product &p, cudaStream_t stream)
 {
     if (p.rows == 0)
         return MXFP4_OK;
@@ -159,13 +157,8 @@ int run_product(const Product &p, int sms, cudaStream_t stream)
     }
     if (p.bytes8)
         a.idesc8 = idesc_mxf8(256, 256, static_cast<uint32_t>(p.fmt_a), static_cast<uint32_t>(p.fmt_b));
-    const size_t need = grouped_workspace_bytes(p.rows, p.groups, p.N, p.K, gated, sms);
-    if (need > 0) {
-        a.tile_count = static_cast<unsigned long long *>(p.ws);
-        a.epoch = next_call_epoch();
-    }
     a.wait_limit = current_wait_limit();
-    return status_of(launch_grouped(a, m, p.bytes8, p.out, sms, stream));
+    return status_of(launch_grouped(a, m, p.bytes8, p.out, stream));
 }
 
 int product_entry(const Product &p, void *stream)
@@ -177,14 +170,7 @@ int product_entry(const Product &p, void *stream)
     st = check_current_device(&sms);
     if (st != MXFP4_OK)
         return st;
-    const size_t need = grouped_workspace_bytes(p.rows, p.groups, p.N, p.K, p.out >= 0, sms);
-    if (need > 0) {
-        if (!p.ws || p.ws_bytes < need)
-            return MXFP4_ERR_WORKSPACE;
-        if (!aligned(p.ws, kAlign))
-            return MXFP4_ERR_MISALIGNED;
-    }
-    return run_product(p, sms, static_cast<cudaStream_t>(stream));
+    return run_product(p, static_cast<cudaStream_t>(stream));
 }
 
 int quantize_entry(void *Q, int64_t ldq, void *S, const void *X, int64_t ldx, int T, int K, const int *slot_row,
@@ -256,10 +242,10 @@ int run_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *Y, int
 
 // Workspace of mxfp4_moe_ffn: what each step leaves for the next.
 struct FfnLayout {
-    size_t q, sq, h, sh, y, ws, total;
+    size_t q, sq, h, sh, y, total;
 };
 
-FfnLayout ffn_layout(int T, int E, int k, int K, int F, int sms)
+FfnLayout ffn_layout(int T, int E, int k, int K, int F)
 {
     const int rows = T * k;
     FfnLayout l;
@@ -274,9 +260,6 @@ FfnLayout ffn_layout(int T, int E, int k, int K, int F, int sms)
     l.h = take(static_cast<size_t>(rows) * (F / 2));
     l.sh = take(static_cast<size_t>(group_sf_blocks(rows, E) * sf_groups(F) * kSfAtomBytes));
     l.y = take(static_cast<size_t>(rows) * K * 2);
-    const size_t up = grouped_workspace_bytes(rows, E, F, K, true, sms);
-    const size_t down = grouped_workspace_bytes(rows, E, K, F, false, sms);
-    l.ws = take(up > down ? up : down);
     l.total = at;
     return l;
 }
@@ -285,12 +268,6 @@ bool bad_ffn_sizes(int T, int E, int k, int K, int F)
 {
     return T < 0 || bad_groups(E) || k < 1 || k > kMaxTopK || k > E || bad_k(K) || bad_k(F) ||
            static_cast<int64_t>(T) * k > 0x7FFFFFFF;
-}
-
-int sms_or_default()
-{
-    int sms = 0;
-    return check_current_device(&sms) == MXFP4_ERR_CUDA || sms <= 0 ? 152 : sms;
 }
 
 }  // namespace
@@ -371,52 +348,44 @@ int mxfp8_group_quantize(void *Q, int64_t ldq, void *S, const void *X, int64_t l
     return quantize_entry(Q, ldq, S, X, ldx, T, K, slot_row, ids, k, offsets, groups, rows, 1 + fmt, stream);
 }
 
-size_t mxfp4_grouped_workspace_size(int rows, int groups, int N, int K)
-{
-    if (rows < 0 || bad_groups(groups) || N < 1 || bad_k(K))
-        return 0;
-    const int sms = sms_or_default();
-    const size_t plain = grouped_workspace_bytes(rows, groups, N, K, false, sms);
-    const size_t gated = grouped_workspace_bytes(rows, groups, N, K, true, sms);
-    return plain > gated ? plain : gated;
-}
+// The present kernels keep everything on chip.
+size_t mxfp4_grouped_workspace_size(int, int, int, int) { return 0; }
 
 int mxfp4_grouped_gemm(void *D, int64_t ldd, const void *A, int64_t lda, const void *SA, const void *B, int64_t ldb,
                        int64_t stride_b, const void *SB, const int *offsets, int groups, int rows, int N, int K,
-                       float alpha, void *workspace, size_t workspace_bytes, void *stream)
+                       float alpha, void *, size_t, void *stream)
 {
     const Product p{D, ldd, nullptr, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, N, K, alpha,
-                    false, 0, 0, -1, workspace, workspace_bytes, false};
+                    false, 0, 0, -1, false};
     return product_entry(p, stream);
 }
 
 int mxfp8_grouped_gemm(void *D, int64_t ldd, const void *A, int64_t lda, const void *SA, const void *B, int64_t ldb,
                        int64_t stride_b, const void *SB, const int *offsets, int groups, int rows, int N, int K,
-                       int fmt_a, int fmt_b, float alpha, void *workspace, size_t workspace_bytes, void *stream)
+                       int fmt_a, int fmt_b, float alpha, void *, size_t, void *stream)
 {
     const Product p{D, ldd, nullptr, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, N, K, alpha,
-                    true, fmt_a, fmt_b, -1, workspace, workspace_bytes, false};
+                    true, fmt_a, fmt_b, -1, false};
     return product_entry(p, stream);
 }
 
 int mxfp4_grouped_swiglu(void *H, int64_t ldh, void *SH, const void *A, int64_t lda, const void *SA, const void *B,
                          int64_t ldb, int64_t stride_b, const void *SB, const int *offsets, int groups, int rows,
-                         int F, int K, float alpha, void *workspace, size_t workspace_bytes, void *stream)
+                         int F, int K, float alpha, void *, size_t, void *stream)
 {
     const Product p{H, ldh, SH, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, F, K, alpha,
-                    false, 0, 0, 0, workspace, workspace_bytes, false};
+                    false, 0, 0, 0, false};
     return product_entry(p, stream);
 }
 
 int mxfp8_grouped_swiglu(void *H, int64_t ldh, void *SH, const void *A, int64_t lda, const void *SA, const void *B,
                          int64_t ldb, int64_t stride_b, const void *SB, const int *offsets, int groups, int rows,
-                         int F, int K, int fmt_a, int fmt_b, int fmt_h, float alpha, void *workspace,
-                         size_t workspace_bytes, void *stream)
+                         int F, int K, int fmt_a, int fmt_b, int fmt_h, float alpha, void *, size_t, void *stream)
 {
     if (fmt_h != MXFP8_E4M3 && fmt_h != MXFP8_E5M2)
         return MXFP4_ERR_INVALID_ARG;
     const Product p{H, ldh, SH, A, lda, SA, B, ldb, stride_b, SB, offsets, groups, rows, F, K, alpha,
-                    true, fmt_a, fmt_b, 1 + fmt_h, workspace, workspace_bytes, false};
+                    true, fmt_a, fmt_b, 1 + fmt_h, false};
     return product_entry(p, stream);
 }
 
@@ -448,7 +417,7 @@ size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F)
 {
     if (bad_ffn_sizes(T, E, k, K, F))
         return 0;
-    return ffn_layout(T, E, k, K, F, sms_or_default()).total;
+    return ffn_layout(T, E, k, K, F).total;
 }
 
 int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, int64_t ldx, const int *ids,
@@ -467,18 +436,16 @@ int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, i
     if (T > 0 && (!aligned(H, 2) || !aligned(Nrm, 2) || !aligned(resid, 2) || !aligned(w_post, 2) ||
                   !aligned(w_pre, 2) || !aligned(X, 16) || (ldx % 8) != 0 || !aligned(workspace, kAlign)))
         return MXFP4_ERR_MISALIGNED;
-    const int sms_plan = sms_or_default();
-    const FfnLayout l = ffn_layout(T, E, k, K, F, sms_plan);
+    const FfnLayout l = ffn_layout(T, E, k, K, F);
     if (T > 0 && (!workspace || workspace_bytes < l.total))
         return MXFP4_ERR_WORKSPACE;
     uint8_t *w = static_cast<uint8_t *>(workspace);
     const int rows = T * k;
-    const size_t ws_bytes = l.total - l.ws;
     // Every step's arguments are checked before the first one is enqueued.
     const Product up{w + l.h, F, w + l.sh, w + l.q, K, w + l.sq, B1, ldb1, 2 * static_cast<int64_t>(F) * ldb1, SB1,
-                     offsets, E, rows, F, K, 1.0f, false, 0, 0, 0, w + l.ws, ws_bytes, true};
+                     offsets, E, rows, F, K, 1.0f, false, 0, 0, 0, true};
     const Product down{w + l.y, K, nullptr, w + l.h, F, w + l.sh, B2, ldb2, static_cast<int64_t>(K) * ldb2, SB2,
-                       offsets, E, rows, K, F, 1.0f, false, 0, 0, -1, w + l.ws, ws_bytes, true};
+                       offsets, E, rows, K, F, 1.0f, false, 0, 0, -1, true};
     int st = check_product(up);
     if (st == MXFP4_OK)
         st = check_product(down);
@@ -492,9 +459,9 @@ int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, i
     // it may read the call's own inputs before their predecessor has ended.
     st = mxfp4_group_quantize(w + l.q, K, w + l.sq, X, ldx, T, K, slot_row, ids, k, offsets, E, rows, stream);
     if (st == MXFP4_OK)
-        st = run_product(up, sms, static_cast<cudaStream_t>(stream));
+        st = run_product(up, static_cast<cudaStream_t>(stream));
     if (st == MXFP4_OK)
-        st = run_product(down, sms, static_cast<cudaStream_t>(stream));
+        st = run_product(down, static_cast<cudaStream_t>(stream));
     if (st == MXFP4_OK)
         st = run_combine(H, ldh, Nrm, ldn, w + l.y, K, rows, slot_row, gates, k, resid, ldr, w_post, w_pre, res_scale,
                          out_scale, eps, T, K, true, sms, stream);

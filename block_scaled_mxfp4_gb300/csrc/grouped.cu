@@ -762,10 +762,7 @@ cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t 
 
 }  // namespace
 
-size_t grouped_workspace_bytes(int, int, int, int, bool, int) { return 0; }
-
-cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, int,
-                           cudaStream_t stream)
+cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, cudaStream_t stream)
 {
     const bool wide = a.groups > GroupedCfg<false, false, false>::MAX_GROUPS;
     switch (out) {

@@ -515,8 +515,10 @@ int mxfp8_group_quantize(void *Q, int64_t ldq, void *S, const void *X, int64_t l
  *   D    bf16 [rows, ldd], ldd >= N
  * K % 32 == 0; A and B 16-byte aligned with rows of whole 16 bytes.
  * mxfp8_grouped_gemm takes the byte formats of mxfp8_gemm.
- * workspace: mxfp4_grouped_workspace_size(rows, groups, N, K) bytes, 256-byte
- * aligned, contents arbitrary; calls that may overlap need their own.
+ * workspace: mxfp4_grouped_workspace_size(rows, groups, N, K) bytes.  The
+ * present kernels need none (the size is 0, the pointer may be NULL and is not
+ * looked at); the argument is there so that a split reduction can come without
+ * a change of the interface.
  */
 int mxfp4_grouped_gemm(void *D, int64_t ldd, const void *A, int64_t lda, const void *SA,
                        const void *B, int64_t ldb, int64_t stride_b, const void *SB,
