@@ -27,7 +27,9 @@ __device__ int g_status = 0;                     // bounded waits that ran out
 constexpr int kCombineThreads = 512;
 constexpr int kCombineMaxVec = 8;                // 8-element vectors of one thread
 
-__device__ __forceinline__ void store8(uint16_t *p, int n, int N, int vec, const float (&x)[8])
+__device__ __forceinline__ uint4 raw8(const uint16_t *p, int n) { return *reinterpret_cast<const uint4 *>(p + n); }
+
+__device__ __forceinline__ void store8(uint16_t *p, int n, const float (&x)[8])
 {
     uint32_t w[4];
 #pragma unroll
@@ -35,45 +37,75 @@ __device__ __forceinline__ void store8(uint16_t *p, int n, int N, int vec, const
         const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&v);
     }
-    if (vec && n + 8 <= N) {
-        *reinterpret_cast<uint4 *>(p + n) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(p + n) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// W consecutive elements (2 W bytes, aligned) <-> floats.
+template <int W>
+__device__ __forceinline__ void load_unit(const uint16_t *p, float (&x)[W])
+{
+    if constexpr (W == 4) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        x[0] = bf16_lo(v.x);
+        x[1] = bf16_hi(v.x);
+        x[2] = bf16_lo(v.y);
+        x[3] = bf16_hi(v.y);
+    } else if constexpr (W == 2) {
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
+        x[0] = bf16_lo(v);
+        x[1] = bf16_hi(v);
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (n + i < N)
-                p[n + i] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+        x[0] = bf16_lo(*p);
     }
 }
 
-// Sum over the block; every thread gets it.  The two slots alternate so that
-// the next call's writes do not meet this one's reads.
-__device__ __forceinline__ float block_sum(float v, float *slot)
+template <int W>
+__device__ __forceinline__ void store_unit(uint16_t *p, const float (&x)[W])
+{
+    if constexpr (W == 1) {
+        const __nv_bfloat16 v = __float2bfloat16_rn(x[0]);
+        *p = *reinterpret_cast<const uint16_t *>(&v);
+    } else {
+        uint32_t w[W / 2];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        if constexpr (W == 4)
+            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(p) = w[0];
+    }
+}
+
+// Sum over the block; every thread gets it.  slot: one float per warp.  The
+// callers alternate slots so that the next call's writes do not meet this one's
+// reads.
+__device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1)
         v += __shfl_xor_sync(kFull, v, d);
-    if ((threadIdx.x & 31) == 0)
-        slot[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float s = 0.0f;
-    const int warps = blockDim.x >> 5;
-    for (int w = 0; w < warps; ++w)
-        s += slot[w];
-    return s;
+    return v;
 }
 
-// Raw bf16 pairs of 8 elements, zeros past N.
-__device__ __forceinline__ uint4 raw8(const uint16_t *p, int n, int N, int vec)
+__device__ __forceinline__ float block_sum(float v, float *slot)
 {
-    if (vec && n + 8 <= N)
-        return *reinterpret_cast<const uint4 *>(p + n);
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (n + i < N)
-            w[i / 2] |= static_cast<uint32_t>(p[n + i]) << (16 * (i & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    const int lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x) >> 5;
+    v = warp_sum(v);
+    if (lane == 0)
+        slot[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return warp_sum(lane < warps ? slot[lane] : 0.0f);
 }
+
+// 1 / sqrt(mean + eps) from the sum of squares.
+__device__ __forceinline__ float inverse_rms(const CombineArgs &a, float ss)
+{
+    return rsqrtf(ss / static_cast<float>(a.N) + a.eps);
+}
+
 
 __device__ __forceinline__ float pick8(const uint4 &v, int i)
 {
@@ -101,7 +133,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == kCombineThreads && VPT <= 2 ? 2 
             const int n = (v * blockDim.x + threadIdx.x) * 8;
             res[v] = make_uint4(0u, 0u, 0u, 0u);
             if (VPT < 8 && a.resid && n < a.N)             // early, where registers allow
-                res[v] = raw8(a.resid + static_cast<int64_t>(t) * a.ldr, n, a.N, a.vec);
+                res[v] = raw8(a.resid + static_cast<int64_t>(t) * a.ldr, n);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 b[v][i] = 0.0f;
@@ -126,7 +158,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == kCombineThreads && VPT <= 2 ? 2 
                 for (int v = 0; v < VPT; ++v) {
                     const int n = (v * blockDim.x + threadIdx.x) * 8;
                     if (row[j] >= 0 && row[j] < a.rows && n < a.N)
-                        y[j][v] = raw8(a.Y + static_cast<int64_t>(row[j]) * a.ldy, n, a.N, a.vec);
+                        y[j][v] = raw8(a.Y + static_cast<int64_t>(row[j]) * a.ldy, n);
                 }
 #pragma unroll
             for (int j = 0; j < JC; ++j) {
@@ -149,12 +181,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == kCombineThreads && VPT <= 2 ? 2 
                 for (int i = 0; i < 8; ++i)
                     ss = fmaf(b[v][i], b[v][i], ss);
             ss = block_sum(ss, slots[parity]);
-            const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+            const float r = inverse_rms(a, ss);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int n = (v * blockDim.x + threadIdx.x) * 8;
                 if (n < a.N) {
-                    const uint4 w = raw8(a.w_post, n, a.N, a.vec);
+                    const uint4 w = raw8(a.w_post, n);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         b[v][i] = b[v][i] * r * pick8(w, i);
@@ -167,26 +199,26 @@ __global__ void __launch_bounds__(MAXT, MAXT == kCombineThreads && VPT <= 2 ? 2 
             const int n = (v * blockDim.x + threadIdx.x) * 8;
             if (n < a.N) {
                 if (VPT == 8 && a.resid)
-                    res[v] = raw8(a.resid + static_cast<int64_t>(t) * a.ldr, n, a.N, a.vec);
+                    res[v] = raw8(a.resid + static_cast<int64_t>(t) * a.ldr, n);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     b[v][i] = a.resid ? fmaf(a.out_scale, b[v][i], a.res_scale * pick8(res[v], i)) : a.out_scale * b[v][i];
                     ss = fmaf(b[v][i], b[v][i], ss);
                 }
                 if (a.H)
-                    store8(a.H + static_cast<int64_t>(t) * a.ldh, n, a.N, a.vec, b[v]);
+                    store8(a.H + static_cast<int64_t>(t) * a.ldh, n, b[v]);
             }
         }
         if (a.Nrm) {
             ss = block_sum(ss, slots[parity + 1]);
-            const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+            const float r = inverse_rms(a, ss);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int n = (v * blockDim.x + threadIdx.x) * 8;
                 if (n < a.N) {
                     float y[8];
                     if (a.w_pre) {
-                        const uint4 w = raw8(a.w_pre, n, a.N, a.vec);
+                        const uint4 w = raw8(a.w_pre, n);
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             y[i] = b[v][i] * r * pick8(w, i);
@@ -195,9 +227,140 @@ __global__ void __launch_bounds__(MAXT, MAXT == kCombineThreads && VPT <= 2 ? 2 
                         for (int i = 0; i < 8; ++i)
                             y[i] = b[v][i] * r;
                     }
-                    store8(a.Nrm + static_cast<int64_t>(t) * a.ldn, n, a.N, a.vec, y);
+                    store8(a.Nrm + static_cast<int64_t>(t) * a.ldn, n, y);
                 }
             }
+        }
+    }
+}
+
+// Rows that do not allow 16-byte accesses (an odd length, stride or start): the
+// threads take units of W elements in turn, so that a warp's accesses are
+// contiguous whatever W is.  THREADS threads with E elements each (both fixed, so
+// that a row's units are one pointer and constants); JC rows in flight together.
+template <int W, int E, int JC, int THREADS, int MINB>
+__global__ void __launch_bounds__(THREADS, MINB) combine_narrow_kernel(const __grid_constant__ CombineArgs a)
+{
+    constexpr int PER = E / W;
+    __shared__ float slots[4][THREADS / 32];
+    pdl_wait_prerequisites();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    int parity = 0;
+    constexpr int step = THREADS * W;
+    const int n0 = static_cast<int>(threadIdx.x) * W;
+    // Lane j holds slot j of the token at hand, and already of the next one.
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    auto look_up = [&](int t, int &row, float &g) {
+        row = -1;
+        g = 1.0f;
+        if (t < a.T && lane < a.k) {
+            const int64_t at = static_cast<int64_t>(t) * a.k + lane;
+            row = a.slot_row ? a.slot_row[at] : t;
+            if (row >= a.rows)
+                row = -1;
+            if (a.gates)
+                g = a.gates[at];
+        }
+    };
+    int next_row;
+    float next_g;
+    look_up(blockIdx.x, next_row, next_g);
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 2) {
+        const int slot_row = next_row;
+        const float slot_g = next_g;
+        look_up(t + static_cast<int>(gridDim.x), next_row, next_g);
+        float b[PER][W];
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+#pragma unroll
+            for (int i = 0; i < W; ++i)
+                b[u][i] = 0.0f;
+        for (int j0 = 0; j0 < a.k; j0 += JC) {
+            int row[JC];
+            float g[JC];
+            float x[JC][PER][W];
+#pragma unroll
+            for (int j = 0; j < JC; ++j) {
+                row[j] = __shfl_sync(kFull, slot_row, j0 + j);
+                g[j] = __shfl_sync(kFull, slot_g, j0 + j);
+            }
+#pragma unroll
+            for (int j = 0; j < JC; ++j) {
+                if (row[j] < 0)
+                    continue;                              // block-uniform
+                const uint16_t *y = a.Y + static_cast<int64_t>(row[j]) * a.ldy + n0;
+#pragma unroll
+                for (int u = 0; u < PER; ++u)
+                    if (n0 + u * step < a.N)
+                        load_unit<W>(y + u * step, x[j][u]);
+            }
+#pragma unroll
+            for (int j = 0; j < JC; ++j) {
+                if (row[j] < 0)
+                    continue;
+#pragma unroll
+                for (int u = 0; u < PER; ++u)
+                    if (n0 + u * step < a.N) {
+#pragma unroll
+                        for (int i = 0; i < W; ++i)
+                            b[u][i] = fmaf(g[j], x[j][u][i], b[u][i]);
+                    }
+            }
+        }
+        if (a.w_post) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    ss = fmaf(b[u][i], b[u][i], ss);
+            ss = block_sum(ss, slots[parity]);
+            const float r = inverse_rms(a, ss);
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+                if (n0 + u * step < a.N) {
+                    float w[W];
+                    load_unit<W>(a.w_post + n0 + u * step, w);
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        b[u][i] = b[u][i] * r * w[i];
+                }
+        }
+        float ss = 0.0f;
+#pragma unroll
+        for (int u = 0; u < PER; ++u)
+            if (n0 + u * step < a.N) {
+                float x[W];
+                if (a.resid)
+                    load_unit<W>(a.resid + static_cast<int64_t>(t) * a.ldr + n0 + u * step, x);
+#pragma unroll
+                for (int i = 0; i < W; ++i) {
+                    b[u][i] = a.resid ? fmaf(a.out_scale, b[u][i], a.res_scale * x[i]) : a.out_scale * b[u][i];
+                    ss = fmaf(b[u][i], b[u][i], ss);
+                }
+                if (a.H)
+                    store_unit<W>(a.H + static_cast<int64_t>(t) * a.ldh + n0 + u * step, b[u]);
+            }
+        if (a.Nrm) {
+            ss = block_sum(ss, slots[parity + 1]);
+            const float r = inverse_rms(a, ss);
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+                if (n0 + u * step < a.N) {
+                    float y[W];
+#pragma unroll
+                    for (int i = 0; i < W; ++i)
+                        y[i] = b[u][i] * r;
+                    if (a.w_pre) {
+                        float w[W];
+                        load_unit<W>(a.w_pre + n0 + u * step, w);
+#pragma unroll
+                        for (int i = 0; i < W; ++i)
+                            y[i] *= w[i];
+                    }
+                    store_unit<W>(a.Nrm + static_cast<int64_t>(t) * a.ldn + n0 + u * step, y);
+                }
         }
     }
 }
@@ -223,17 +386,12 @@ struct RingMeta {
 
 __device__ __forceinline__ float ring_sum(float v, float *slot)
 {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        v += __shfl_xor_sync(kFull, v, d);
-    if ((threadIdx.x & 31) == 0)
+    const int lane = threadIdx.x & 31;
+    v = warp_sum(v);
+    if (lane == 0)
         slot[threadIdx.x >> 5] = v;
     asm volatile("bar.sync 1, %0;" ::"n"(kCombineThreads) : "memory");
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kCombineThreads / 32; ++w)
-        s += slot[w];
-    return s;
+    return warp_sum(lane < kCombineThreads / 32 ? slot[lane] : 0.0f);
 }
 
 template <int VPT>
@@ -378,7 +536,7 @@ __global__ void __launch_bounds__(kRingThreads, 1) combine_ring_kernel(const __g
                 for (int i = 0; i < 8; ++i)
                     ss = fmaf(b[v][i], b[v][i], ss);
             ss = ring_sum(ss, m.slots[parity]);
-            const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+            const float r = inverse_rms(a, ss);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const uint4 w = KEEP ? post[v] : weight(a.w_post, v);
@@ -408,11 +566,11 @@ __global__ void __launch_bounds__(kRingThreads, 1) combine_ring_kernel(const __g
         for (int v = 0; v < VPT; ++v) {
             const int n = (v * kCombineThreads + threadIdx.x) * 8;
             if (n < a.N && a.H && ok)
-                store8(a.H + static_cast<int64_t>(t) * a.ldh, n, a.N, 1, b[v]);
+                store8(a.H + static_cast<int64_t>(t) * a.ldh, n, b[v]);
         }
         if (a.Nrm) {
             ss = ring_sum(ss, m.slots[parity + 1]);
-            const float r = 1.0f / sqrtf(ss / static_cast<float>(a.N) + a.eps);
+            const float r = inverse_rms(a, ss);
 #pragma unroll
             for (int v = 0; v < VPT; ++v) {
                 const int n = (v * kCombineThreads + threadIdx.x) * 8;
@@ -422,11 +580,44 @@ __global__ void __launch_bounds__(kRingThreads, 1) combine_ring_kernel(const __g
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
                         y[i] = b[v][i] * r * pick8(w, i);
-                    store8(a.Nrm + static_cast<int64_t>(t) * a.ldn, n, a.N, 1, y);
+                    store8(a.Nrm + static_cast<int64_t>(t) * a.ldn, n, y);
                 }
             }
         }
     }
+}
+
+template <int W, int E, int JC, int THREADS, int BLOCKS>
+cudaError_t launch_narrow_as(const CombineArgs &a, int sms, cudaStream_t stream)
+{
+    const int most = sms * BLOCKS;
+    return launch_dependent(combine_narrow_kernel<W, E, JC, THREADS, BLOCKS>, dim3(a.T < most ? a.T : most), dim3(THREADS),
+                            0, stream, a);
+}
+
+// Few tokens: eight elements per thread and two rows in flight, the shortest
+// time for one (3 tokens of 2858: 3.7 against 6.0 us).  Many: sixteen elements,
+// so that the sums' share is small and more tokens fit an SM (6437 tokens of
+// 1196: 23 against 38 us).
+template <int W>
+cudaError_t launch_narrow(const CombineArgs &a, int sms, cudaStream_t stream)
+{
+    if (a.T < 2 * sms && a.N <= 8192)
+        return a.N <= 512    ? launch_narrow_as<W, 8, 2, 64, 16>(a, sms, stream)
+               : a.N <= 1024 ? launch_narrow_as<W, 8, 2, 128, 8>(a, sms, stream)
+               : a.N <= 2048 ? launch_narrow_as<W, 8, 2, 256, 4>(a, sms, stream)
+               : a.N <= 4096 ? launch_narrow_as<W, 8, 2, 512, 2>(a, sms, stream)
+                             : launch_narrow_as<W, 8, 2, 1024, 1>(a, sms, stream);
+    const int threads = (a.N + 15) / 16;
+    return threads <= 32    ? launch_narrow_as<W, 16, 1, 32, 32>(a, sms, stream)
+           : threads <= 64  ? launch_narrow_as<W, 16, 1, 64, 16>(a, sms, stream)
+           : threads <= 96  ? launch_narrow_as<W, 16, 1, 96, 12>(a, sms, stream)
+           : threads <= 128 ? launch_narrow_as<W, 16, 1, 128, 8>(a, sms, stream)
+           : threads <= 192 ? launch_narrow_as<W, 16, 1, 192, 6>(a, sms, stream)
+           : threads <= 256 ? launch_narrow_as<W, 16, 1, 256, 4>(a, sms, stream)
+           : threads <= 384 ? launch_narrow_as<W, 16, 1, 384, 3>(a, sms, stream)
+           : threads <= 512 ? launch_narrow_as<W, 16, 1, 512, 2>(a, sms, stream)
+                            : launch_narrow_as<W, 32, 1, 1024, 1>(a, sms, stream);
 }
 
 template <int VPT>
@@ -446,9 +637,13 @@ cudaError_t launch_ring(const CombineArgs &a, int sms, cudaStream_t stream)
 
 cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream)
 {
+    if (a.width < 8)
+        return a.width == 4   ? launch_narrow<4>(a, sms, stream)
+               : a.width == 2 ? launch_narrow<2>(a, sms, stream)
+                              : launch_narrow<1>(a, sms, stream);
     // Enough tokens for every SM to have several, and rows long enough that a
     // ring entry's hand-over (some 200 cycles) is short beside them.
-    if (a.vec && a.N % 8 == 0 && a.N >= 2048 && a.N <= 16384 && a.T >= 4 * sms) {
+    if (a.N >= 2048 && a.N <= 16384 && a.T >= 4 * sms) {
         const int per = (a.N / 8 + kCombineThreads - 1) / kCombineThreads;
         return per <= 1   ? launch_ring<1>(a, sms, stream)
                : per <= 2 ? launch_ring<2>(a, sms, stream)
@@ -462,11 +657,11 @@ cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream)
     const int most = sms * (2048 / threads);
     const dim3 grid(static_cast<unsigned>(a.T < most ? a.T : most)), block(static_cast<unsigned>(threads));
     if (few && per <= 1)
-        return launch_dependent(combine_kernel<1, 8, 1024>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<1, 4, 1024>, grid, block, 0, stream, a);
     if (few)
         return launch_dependent(combine_kernel<2, 2, 1024>, grid, block, 0, stream, a);
     if (per <= 1)
-        return launch_dependent(combine_kernel<1, 8, kCombineThreads>, grid, block, 0, stream, a);
+        return launch_dependent(combine_kernel<1, 4, kCombineThreads>, grid, block, 0, stream, a);
     if (per <= 2)
         return launch_dependent(combine_kernel<2, 4, kCombineThreads>, grid, block, 0, stream, a);
     if (per <= 4)

@@ -87,7 +87,7 @@ struct CombineArgs {
     const uint16_t *w_post, *w_pre;   // [N] or null
     float res_scale, out_scale, eps;
     int T, N;
-    int vec;                    // every row takes aligned 16-byte accesses
+    int width;                  // elements of the widest access that every row allows: 8, 4, 2, 1
     long long wait_limit;
     int early;                  // all but Y may be read before the preceding grid ends
 };
@@ -105,7 +105,6 @@ struct GroupedArgs {
     uint16_t *D;                // plain form: bf16 [rows, ldd]
     int64_t ldd;
     int vec32_ok, vec_ok;       // D (H) allows aligned 32- / 16-byte row stores
-    int tma_ok;                 // D allows TMA stores
     uint8_t *H;                 // gated form: codes [rows, ldh bytes]
     int64_t ldh;
     uint8_t *SH;                // grouped scale layout over N
@@ -117,7 +116,7 @@ struct GroupedArgs {
 };
 struct GroupedMaps {
     CUtensorMap A, A32, SA, B, SB;   // A: boxes of 128 rows, A32: of 32
-    CUtensorMap D;                   // plain form with tma_ok: boxes of 32 rows x 32 columns
+    CUtensorMap D;                   // plain form with vec_ok: boxes of 32 rows x 32 columns
 };
 // out: -1 plain (bf16), else the QuantFmt of the gated form's output.
 cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, cudaStream_t stream);

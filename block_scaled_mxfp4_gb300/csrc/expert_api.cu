@@ -148,11 +148,10 @@ int run_product(const Product &p, cudaStream_t stream)
         a.ldd = p.ldd;
         a.vec_ok = aligned(p.D, 16) && (p.ldd % 8) == 0;
         a.vec32_ok = aligned(p.D, 32) && (p.ldd % 16) == 0;
-        a.tma_ok = a.vec_ok;
         const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.rows)};
         const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.ldd) * 2};
         const cuuint32_t box[2] = {32, 32};
-        if (a.tma_ok && !encode(&m.D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.D, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
+        if (a.vec_ok && !encode(&m.D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.D, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
             return MXFP4_ERR_CUDA;
     }
     if (p.bytes8)
@@ -232,11 +231,21 @@ int run_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *Y, int
     a.eps = eps;
     a.T = T;
     a.N = N;
-    auto rows_ok = [](const void *p, int64_t ld) { return !p || (aligned(p, 16) && (ld % 8) == 0); };
     a.early = early ? 1 : 0;
     a.wait_limit = current_wait_limit();
-    a.vec = rows_ok(H, ldh) && rows_ok(Nrm, ldn) && rows_ok(Y, ldy) && rows_ok(resid, ldr) && rows_ok(w_post, 0) &&
-            rows_ok(w_pre, 0);
+    a.width = 8;
+    auto allow = [&a](const void *p, int64_t ld) {
+        while (p && a.width > 1 && (!aligned(p, 2 * static_cast<size_t>(a.width)) || (ld % a.width) != 0))
+            a.width /= 2;
+    };
+    allow(H, ldh);
+    allow(Nrm, ldn);
+    allow(Y, ldy);
+    allow(resid, ldr);
+    allow(w_post, N);
+    allow(w_pre, N);
+    while (N % a.width != 0)
+        a.width /= 2;
     return status_of(launch_combine(a, sms, static_cast<cudaStream_t>(stream)));
 }
 

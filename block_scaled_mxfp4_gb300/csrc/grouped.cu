@@ -267,7 +267,7 @@ __device__ __forceinline__ void round_bf16(const GroupedArgs &a, const uint32_t 
         out[j] = bf16x2(a.alpha * __uint_as_float(x[2 * j]), a.alpha * __uint_as_float(x[2 * j + 1]));
 }
 
-// 32 columns of row r from n0 on, by this thread alone.
+// 32 columns of row r from n0 on, by this thread alone (rows of whole 16 bytes).
 __device__ __forceinline__ void store_bf16(const GroupedArgs &a, int r, int n0, const uint32_t (&x)[32])
 {
     if (n0 >= a.N)
@@ -284,7 +284,7 @@ __device__ __forceinline__ void store_bf16(const GroupedArgs &a, int r, int n0, 
     }
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
-        if (a.vec_ok && n0 + 2 * j + 8 <= a.N) {
+        if (n0 + 2 * j + 8 <= a.N) {
             *reinterpret_cast<uint4 *>(d + 2 * j) = make_uint4(out[j], out[j + 1], out[j + 2], out[j + 3]);
         } else {
 #pragma unroll
@@ -293,6 +293,30 @@ __device__ __forceinline__ void store_bf16(const GroupedArgs &a, int r, int n0, 
                     d[2 * j + i] = static_cast<uint16_t>(out[j + i / 2] >> (16 * (i & 1)));
         }
     }
+}
+
+// A warp's 32 rows x 32 columns, rounded, into its 2 KB box (64-byte rows, 64-byte
+// swizzle): chunk j of 16 bytes of row i at chunk j ^ (i / 2 % 4).
+__device__ __forceinline__ void fill_box(uint8_t *box, int lane, const uint32_t (&out)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4 *>(box + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
+            make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
+}
+
+// The box's first `rows` rows to D[first ..][n0 ..] one element per lane: for
+// rows that no wider store fits (an odd ldd puts every second one off a 4-byte
+// boundary).  A row's 64 bytes leave together, where a thread that stored its
+// own row's elements would touch 32 rows at a time.
+__device__ __forceinline__ void store_box(const GroupedArgs &a, const uint8_t *box, int lane, int first, int rows, int n0)
+{
+    if (n0 + lane >= a.N)
+        return;
+    uint16_t *d = a.D + static_cast<int64_t>(first) * a.ldd + n0 + lane;
+#pragma unroll 8
+    for (int i = 0; i < rows; ++i, d += a.ldd)
+        *d = *reinterpret_cast<const uint16_t *>(box + i * 64 + (((lane >> 3) ^ ((i >> 1) & 3)) * 16) + (lane & 7) * 2);
 }
 
 // silu(alpha g) * (alpha u) in fp32.  The exponent's argument is rounded once,
@@ -477,10 +501,10 @@ __global__ void __launch_bounds__(512, 1)
             if constexpr (!GATED) {
                 const int n0 = tl.q * 256 + half * 128;
                 const int first = r - lane;
-                if (a.tma_ok && first + 32 <= tl.end) {
-                    // The warp's 32 rows are all the group's: four boxes of 32
-                    // rows x 32 columns through shared memory (64-byte
-                    // swizzle), stored by TMA.  A thread's own 32-byte stores
+                const int rows_here = min(32, tl.end - first);
+                if (rows_here > 0 && (!a.vec_ok || rows_here == 32)) {
+                    // Four boxes of 32 rows x 32 columns through shared memory.
+                    // Whole ones leave by TMA: a thread's own 32-byte stores
                     // touch a line each, and 64 KB of them per tile hold up
                     // the MMA warp's barrier polls in the same queue.
                     uint8_t *buf = stage_out + (half * 4 + quarter) * kOutBoxBytes;
@@ -493,13 +517,13 @@ __global__ void __launch_bounds__(512, 1)
                         if (lane == 0)
                             bulk_wait_read();
                         __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            *reinterpret_cast<uint4 *>(buf + lane * 64 + ((j ^ ((lane >> 1) & 3)) * 16)) =
-                                make_uint4(out[4 * j], out[4 * j + 1], out[4 * j + 2], out[4 * j + 3]);
-                        fence_proxy_async_smem();
+                        fill_box(buf, lane, out);
+                        if (a.vec_ok)
+                            fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0) {
+                        if (!a.vec_ok) {
+                            store_box(a, buf, lane, first, rows_here, n0 + 32 * c);
+                        } else if (lane == 0) {
                             tma_store_2d(&maps.D, buf, n0 + 32 * c, first);
                             bulk_commit();
                         }
