@@ -40,29 +40,12 @@ __device__ __forceinline__ void store8(uint16_t *p, int n, const float (&x)[8])
     *reinterpret_cast<uint4 *>(p + n) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// W consecutive elements (2 W bytes, aligned) <-> floats.
-template <int W>
-__device__ __forceinline__ void load_unit(const uint16_t *p, float (&x)[W])
-{
-    if constexpr (W == 4) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        x[0] = bf16_lo(v.x);
-        x[1] = bf16_hi(v.x);
-        x[2] = bf16_lo(v.y);
-        x[3] = bf16_hi(v.y);
-    } else if constexpr (W == 2) {
-        const uint32_t v = *reinterpret_cast<const uint32_t *>(p);
-        x[0] = bf16_lo(v);
-        x[1] = bf16_hi(v);
-    } else {
-        x[0] = bf16_lo(*p);
-    }
-}
-
 template <int W>
 __device__ __forceinline__ void store_unit(uint16_t *p, const float (&x)[W])
 {
-    if constexpr (W == 1) {
+    if constexpr (W == 8) {
+        store8(p, 0, x);
+    } else if constexpr (W == 1) {
         const __nv_bfloat16 v = __float2bfloat16_rn(x[0]);
         *p = *reinterpret_cast<const uint16_t *>(&v);
     } else {
@@ -79,9 +62,6 @@ __device__ __forceinline__ void store_unit(uint16_t *p, const float (&x)[W])
     }
 }
 
-// Sum over the block; every thread gets it.  slot: one float per warp.  The
-// callers alternate slots so that the next call's writes do not meet this one's
-// reads.
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -90,6 +70,9 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// Sum over the block; every thread gets it.  slot: one float per warp.  The
+// callers alternate slots so that the next call's writes do not meet this one's
+// reads.
 __device__ __forceinline__ float block_sum(float v, float *slot)
 {
     const int lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x) >> 5;
@@ -106,11 +89,42 @@ __device__ __forceinline__ float inverse_rms(const CombineArgs &a, float ss)
     return rsqrtf(ss / static_cast<float>(a.N) + a.eps);
 }
 
-
 __device__ __forceinline__ float pick8(const uint4 &v, int i)
 {
     const uint32_t w = i < 2 ? v.x : i < 4 ? v.y : i < 6 ? v.z : v.w;
     return i & 1 ? bf16_hi(w) : bf16_lo(w);
+}
+
+// W elements as they lie in memory, and element i of them.
+template <int W>
+struct UnitOf;
+template <>
+struct UnitOf<8> { using T = uint4; };
+template <>
+struct UnitOf<4> { using T = uint2; };
+template <>
+struct UnitOf<2> { using T = uint32_t; };
+template <>
+struct UnitOf<1> { using T = uint16_t; };
+
+template <int W>
+__device__ __forceinline__ float pick(const typename UnitOf<W>::T &v, int i)
+{
+    if constexpr (W == 8)
+        return pick8(v, i);
+    else if constexpr (W == 4)
+        return i & 1 ? bf16_hi(i < 2 ? v.x : v.y) : bf16_lo(i < 2 ? v.x : v.y);
+    else
+        return i & 1 ? bf16_hi(v) : bf16_lo(v);
+}
+
+template <int W>
+__device__ __forceinline__ void load_unit(const uint16_t *p, float (&x)[W])
+{
+    const typename UnitOf<W>::T v = *reinterpret_cast<const typename UnitOf<W>::T *>(p);
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+        x[i] = pick<W>(v, i);
 }
 
 // VPT 8-element vectors per thread, JC slots' rows in flight together.
@@ -366,47 +380,61 @@ __global__ void __launch_bounds__(THREADS, MINB) combine_narrow_kernel(const __g
 }
 
 // The same for long prefills, where the sums' barriers must not leave HBM
-// idle: one persistent block per SM, whose last warp streams the tokens' rows
-// (the taken rows of Y, then the residual row) into a ring of whole rows in
-// shared memory with bulk copies, as far ahead as the ring holds, while 16
-// warps work on the token at hand.  8192 tokens x 4 rows of 8192: see the
-// launcher.
-constexpr int kRingThreads = kCombineThreads + 32;
+// idle: persistent blocks, whose last warps stream the tokens' rows (the taken
+// rows of Y, then the residual row) into a ring of whole rows in shared memory
+// with bulk copies, as far ahead as the ring holds, while the others work on the
+// token at hand.  Bound by HBM: 8192 tokens x 4 rows of 8192 move 940 MB in
+// 144 us, 98 % of a plain copy's rate.
+//
+// W < 8 is for rows off 16-byte boundaries.  Such a row is copied with the rest
+// of its first and last 16 bytes, which belong to the tensor's other rows; the
+// entry notes where the row begins.  Only the tensor's first and last row may
+// have no such neighbours: there the warp sets down the elements beside the
+// whole 16-byte parts itself, so nothing outside the tensor is read.
 constexpr int kRingMaxRows = 32;
-constexpr int kRingBytes = 200 * 1024;
+constexpr int kRingBytes = 200 * 1024;           // of an SM's blocks together
 
 struct RingMeta {
     uint64_t full[kRingMaxRows];
     uint64_t empty[kRingMaxRows];
     float gate[kRingMaxRows];
     int last[kRingMaxRows];                      // 1: the token's last entry (its residual row, or nothing)
-    float slots[4][kCombineThreads / 32];
+    int shift[kRingMaxRows];                     // the row's first byte
+    float slots[4][16];
     int abort_flag;
 };
 
+__host__ __device__ constexpr uint32_t ring_pitch(int N, int W)
+{
+    return (static_cast<uint32_t>(N) * 2 + (W < 8 ? 14u : 0u) + 127u) / 128u * 128u;
+}
+
+template <int THREADS>
 __device__ __forceinline__ float ring_sum(float v, float *slot)
 {
     const int lane = threadIdx.x & 31;
     v = warp_sum(v);
     if (lane == 0)
         slot[threadIdx.x >> 5] = v;
-    asm volatile("bar.sync 1, %0;" ::"n"(kCombineThreads) : "memory");
-    return warp_sum(lane < kCombineThreads / 32 ? slot[lane] : 0.0f);
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+    return warp_sum(lane < THREADS / 32 ? slot[lane] : 0.0f);
 }
 
-template <int VPT>
-__global__ void __launch_bounds__(kRingThreads, 1) combine_ring_kernel(const __grid_constant__ CombineArgs a, int depth)
+// PER units of W elements per thread, unit u at element (u * THREADS + thread) * W.
+template <int W, int PER, int THREADS, int BLOCKS, int LOADERS>
+__global__ void __launch_bounds__(THREADS + 32 * LOADERS, BLOCKS) combine_ring_kernel(const __grid_constant__ CombineArgs a, int depth)
 {
+    using Unit = typename UnitOf<W>::T;
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ RingMeta m;
     const uint32_t row_bytes = static_cast<uint32_t>(a.N) * 2;
-    const uint32_t pitch = (row_bytes + 127u) / 128u * 128u;
+    const uint32_t pitch = ring_pitch(a.N, W);
     volatile int *abort_flag = &m.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < depth; ++s) {
             mbar_init(&m.full[s], 1);
-            mbar_init(&m.empty[s], kCombineThreads / 32);
+            mbar_init(&m.empty[s], THREADS / 32);
         }
         m.abort_flag = 0;
         fence_mbar_init();
@@ -415,11 +443,10 @@ __global__ void __launch_bounds__(kRingThreads, 1) combine_ring_kernel(const __g
     pdl_wait_prerequisites();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
-    int s = 0;
-    uint32_t phase = 0;
-    if (warp == kCombineThreads / 32) {
+    if (warp >= THREADS / 32) {
+        const int loader = warp - THREADS / 32;
         const uint64_t once = l2_policy_evict_first();
-        int issued = 0;
+        int entry = 0;                                     // of this block's, in order
         bool ok = true;
         auto look_up = [&](int t, int &row, float &g) {
             row = -1;
@@ -443,55 +470,100 @@ __global__ void __launch_bounds__(kRingThreads, 1) combine_ring_kernel(const __g
             const uint32_t taken = __ballot_sync(kFull, row >= 0);
             const int entries = __popc(taken) + 1;
             uint32_t left = taken;
-            for (int i = 0; i < entries && ok; ++i) {
+            for (int i = 0; i < entries; ++i, ++entry) {
                 const bool last = left == 0u;
                 const int j = last ? 0 : __ffs(left) - 1;
                 left &= left - 1u;
+                if (entry % LOADERS != loader)
+                    continue;
+                const int s = entry % depth;
+                const uint32_t phase = static_cast<uint32_t>(entry / depth) & 1u;
                 const int r = __shfl_sync(kFull, row, j);
                 const float gate = __shfl_sync(kFull, g, j);
+                const uint16_t *src = !last      ? a.Y + static_cast<int64_t>(r) * a.ldy
+                                      : a.resid ? a.resid + static_cast<int64_t>(t) * a.ldr
+                                                : nullptr;
+                // The 16-byte parts to copy: [from, to), the row at `shift`.
+                const uint8_t *from = reinterpret_cast<const uint8_t *>(src), *to = from + row_bytes;
+                uint32_t shift = 0, at = 0;                // at: where `from` goes
+                bool edge = false;
+                if constexpr (W < 8) {
+                    if (src) {
+                        const uint8_t *row_end = to;
+                        shift = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(from) & 15u);
+                        from -= shift;
+                        to += (16u - static_cast<uint32_t>(reinterpret_cast<uintptr_t>(to) & 15u)) & 15u;
+                        const int64_t rows = last ? a.T : a.rows, ld = last ? a.ldr : a.ldy;
+                        const uint8_t *low = reinterpret_cast<const uint8_t *>(last ? a.resid : a.Y);
+                        const uint8_t *high = low + ((rows - 1) * ld + a.N) * 2;
+                        if (from < low) {
+                            from += 16;
+                            at = 16;
+                            edge = true;
+                        }
+                        if (to > high) {
+                            to -= 16;
+                            edge = true;
+                        }
+                        if (edge) {
+                            // Lane q has the row's elements q of the first and
+                            // of the last partly covered 16 bytes.
+                            if (lane == 0)
+                                ok = mbar_wait(&m.empty[s], phase ^ 1u, abort_flag, a.wait_limit, &g_status);
+                            ok = __shfl_sync(kFull, ok, 0);
+                            if (ok) {
+                                uint8_t *to_ring = ring + static_cast<size_t>(s) * pitch + shift;
+                                const uint8_t *row0 = reinterpret_cast<const uint8_t *>(src);
+                                const uint8_t *head = row0 + 2 * lane, *tail = to + 2 * lane;
+                                if (head < from)
+                                    *reinterpret_cast<uint16_t *>(to_ring + 2 * lane) = *reinterpret_cast<const uint16_t *>(head);
+                                if (tail < row_end)
+                                    *reinterpret_cast<uint16_t *>(to_ring + (tail - row0)) = *reinterpret_cast<const uint16_t *>(tail);
+                            }
+                            __syncwarp();
+                        }
+                    }
+                }
                 if (lane == 0) {
-                    ok = mbar_wait(&m.empty[s], phase ^ 1u, abort_flag, a.wait_limit, &g_status);
+                    ok = ok && (edge || mbar_wait(&m.empty[s], phase ^ 1u, abort_flag, a.wait_limit, &g_status));
                     if (ok) {
+                        const uint32_t bytes = src ? static_cast<uint32_t>(to - from) : 0u;
                         m.gate[s] = gate;
                         m.last[s] = last ? 1 : 0;
-                        const uint16_t *src = !last      ? a.Y + static_cast<int64_t>(r) * a.ldy
-                                              : a.resid ? a.resid + static_cast<int64_t>(t) * a.ldr
-                                                        : nullptr;
-                        mbar_arrive_expect_tx(&m.full[s], src ? row_bytes : 0u);
+                        m.shift[s] = static_cast<int>(shift);
+                        mbar_arrive_expect_tx(&m.full[s], bytes);
                         if (src)
-                            bulk_load(ring + static_cast<size_t>(s) * pitch, src, row_bytes, &m.full[s], once);
+                            bulk_load(ring + static_cast<size_t>(s) * pitch + at, from, bytes, &m.full[s], once);
                     }
                 }
                 ok = __shfl_sync(kFull, ok, 0);
-                if (ok) {
-                    ++issued;
-                    if (++s == depth) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
-                }
+                if (!ok)
+                    break;
             }
         }
         if (lane == 0 && *abort_flag)
             // Let the copies already issued land before the block exits.
-            for (int i = max(0, issued - depth); i < issued; ++i)
-                mbar_wait_drain(&m.full[i % depth], (i / depth) & 1u, a.wait_limit);
+            for (int i = max(0, entry - depth); i < entry; ++i)
+                if (i % LOADERS == loader)
+                    mbar_wait_drain(&m.full[i % depth], (i / depth) & 1u, a.wait_limit);
         return;
     }
-    const uint4 ones = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-    auto weight = [&](const uint16_t *w, int v) {
-        const int n = (v * kCombineThreads + threadIdx.x) * 8;
-        return w && n < a.N ? *reinterpret_cast<const uint4 *>(w + n) : ones;
+    const int n0 = static_cast<int>(threadIdx.x) * W;
+    constexpr int step = THREADS * W;
+    auto fetch = [&](const uint16_t *w, int u) {
+        return w && n0 + u * step < a.N ? *reinterpret_cast<const Unit *>(w + n0 + u * step) : Unit{};
     };
-    constexpr bool KEEP = VPT <= 2;              // the norms' weights stay in registers
-    uint4 post[VPT], pre[VPT];
+    constexpr bool KEEP = W * PER <= 16 && THREADS * BLOCKS <= 768;        // the norms' weights stay in registers
+    Unit post[KEEP ? PER : 1], pre[KEEP ? PER : 1];
     if constexpr (KEEP) {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            post[v] = weight(a.w_post, v);
-            pre[v] = weight(a.w_pre, v);
+        for (int u = 0; u < PER; ++u) {
+            post[u] = fetch(a.w_post, u);
+            pre[u] = fetch(a.w_pre, u);
         }
     }
+    int s = 0;
+    uint32_t phase = 0;
     bool ok = true;                              // after a wait that ran out: no data, but every barrier
     auto release = [&]() {
         __syncwarp();
@@ -502,87 +574,80 @@ __global__ void __launch_bounds__(kRingThreads, 1) combine_ring_kernel(const __g
             phase ^= 1u;
         }
     };
+    auto entry = [&]() { return ring + static_cast<size_t>(s) * pitch + (W < 8 ? m.shift[s] : 0) + 2 * n0; };
     int parity = 0;
     for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 2) {
-        float b[VPT][8];
+        float b[PER][W];
 #pragma unroll
-        for (int v = 0; v < VPT; ++v)
+        for (int u = 0; u < PER; ++u)
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                b[v][i] = 0.0f;
+            for (int i = 0; i < W; ++i)
+                b[u][i] = 0.0f;
         for (;;) {
             ok = __all_sync(kFull, mbar_wait(&m.full[s], phase, abort_flag, a.wait_limit, &g_status));
             if (!ok || m.last[s])
                 break;
             const float g = m.gate[s];
-            const uint8_t *y = ring + static_cast<size_t>(s) * pitch;
+            const uint8_t *y = entry();
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int n = (v * kCombineThreads + threadIdx.x) * 8;
-                if (n < a.N) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(y + 2 * n);
+            for (int u = 0; u < PER; ++u)
+                if (n0 + u * step < a.N) {
+                    const Unit x = *reinterpret_cast<const Unit *>(y + 2 * u * step);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        b[v][i] = fmaf(g, pick8(x, i), b[v][i]);
+                    for (int i = 0; i < W; ++i)
+                        b[u][i] = fmaf(g, pick<W>(x, i), b[u][i]);
                 }
-            }
             release();
         }
         if (a.w_post) {
             float ss = 0.0f;
 #pragma unroll
-            for (int v = 0; v < VPT; ++v)
+            for (int u = 0; u < PER; ++u)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    ss = fmaf(b[v][i], b[v][i], ss);
-            ss = ring_sum(ss, m.slots[parity]);
+                for (int i = 0; i < W; ++i)
+                    ss = fmaf(b[u][i], b[u][i], ss);
+            ss = ring_sum<THREADS>(ss, m.slots[parity]);
             const float r = inverse_rms(a, ss);
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const uint4 w = KEEP ? post[v] : weight(a.w_post, v);
+            for (int u = 0; u < PER; ++u) {
+                const Unit w = KEEP ? post[KEEP ? u : 0] : fetch(a.w_post, u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    b[v][i] = b[v][i] * r * pick8(w, i);
+                for (int i = 0; i < W; ++i)
+                    b[u][i] = b[u][i] * r * pick<W>(w, i);
             }
         }
         float ss = 0.0f;
-        const uint8_t *res = ring + static_cast<size_t>(s) * pitch;
+        const uint8_t *res = entry();
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int n = (v * kCombineThreads + threadIdx.x) * 8;
-            if (n < a.N) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (a.resid)
-                    x = *reinterpret_cast<const uint4 *>(res + 2 * n);
+        for (int u = 0; u < PER; ++u)
+            if (n0 + u * step < a.N) {
+                Unit x{};
+                if (a.resid && ok)
+                    x = *reinterpret_cast<const Unit *>(res + 2 * u * step);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    b[v][i] = a.resid ? fmaf(a.out_scale, b[v][i], a.res_scale * pick8(x, i)) : a.out_scale * b[v][i];
-                    ss = fmaf(b[v][i], b[v][i], ss);
+                for (int i = 0; i < W; ++i) {
+                    b[u][i] = a.resid ? fmaf(a.out_scale, b[u][i], a.res_scale * pick<W>(x, i)) : a.out_scale * b[u][i];
+                    ss = fmaf(b[u][i], b[u][i], ss);
                 }
             }
-        }
         release();
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-            const int n = (v * kCombineThreads + threadIdx.x) * 8;
-            if (n < a.N && a.H && ok)
-                store8(a.H + static_cast<int64_t>(t) * a.ldh, n, b[v]);
-        }
+        for (int u = 0; u < PER; ++u)
+            if (n0 + u * step < a.N && a.H && ok)
+                store_unit<W>(a.H + static_cast<int64_t>(t) * a.ldh + n0 + u * step, b[u]);
         if (a.Nrm) {
-            ss = ring_sum(ss, m.slots[parity + 1]);
+            ss = ring_sum<THREADS>(ss, m.slots[parity + 1]);
             const float r = inverse_rms(a, ss);
 #pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const int n = (v * kCombineThreads + threadIdx.x) * 8;
-                if (n < a.N && ok) {
-                    const uint4 w = KEEP ? pre[v] : weight(a.w_pre, v);
-                    float y[8];
+            for (int u = 0; u < PER; ++u)
+                if (n0 + u * step < a.N && ok) {
+                    const Unit w = KEEP ? pre[KEEP ? u : 0] : fetch(a.w_pre, u);
+                    float y[W];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] = b[v][i] * r * pick8(w, i);
-                    store8(a.Nrm + static_cast<int64_t>(t) * a.ldn, n, y);
+                    for (int i = 0; i < W; ++i)
+                        y[i] = b[u][i] * r * (a.w_pre ? pick<W>(w, i) : 1.0f);
+                    store_unit<W>(a.Nrm + static_cast<int64_t>(t) * a.ldn + n0 + u * step, y);
                 }
-            }
         }
     }
 }
@@ -620,35 +685,63 @@ cudaError_t launch_narrow(const CombineArgs &a, int sms, cudaStream_t stream)
                             : launch_narrow_as<W, 32, 1, 1024, 1>(a, sms, stream);
 }
 
-template <int VPT>
-cudaError_t launch_ring(const CombineArgs &a, int sms, cudaStream_t stream)
+template <int W, int E, int THREADS, int BLOCKS, int LOADERS>
+cudaError_t launch_ring_as(const CombineArgs &a, int sms, cudaStream_t stream)
 {
-    const cudaError_t e = opt_in<combine_ring_kernel<VPT>>(kRingBytes);
+    constexpr auto kern = combine_ring_kernel<W, E / W, THREADS, BLOCKS, LOADERS>;
+    const cudaError_t e = opt_in<kern>(kRingBytes / BLOCKS);
     if (e != cudaSuccess)
         return e;
-    const int pitch = (a.N * 2 + 127) / 128 * 128;
-    const int fit = kRingBytes / pitch;
+    const int pitch = static_cast<int>(ring_pitch(a.N, W));
+    const int fit = kRingBytes / BLOCKS / pitch;
     const int depth = fit < kRingMaxRows ? fit : kRingMaxRows;
-    return launch_dependent(combine_ring_kernel<VPT>, dim3(a.T < sms ? a.T : sms), dim3(kRingThreads),
+    const int most = sms * BLOCKS;
+    return launch_dependent(kern, dim3(a.T < most ? a.T : most), dim3(THREADS + 32 * LOADERS),
                             static_cast<size_t>(depth) * pitch, stream, a, depth);
+}
+
+// Enough tokens for every SM to have several, and rows long enough that a ring
+// entry's hand-over (some 600 cycles for a block) is short beside them.
+bool ring_pays(const CombineArgs &a, int sms)
+{
+    return a.T >= 4 * sms && a.N <= 16384 && (a.N > 1280 || (a.width == 1 && a.N > 1024));
+}
+
+// Sixteen elements per thread, so that few threads share a token and an SM has
+// several tokens at hand: one's hand-overs, sums and stores hide behind another's.
+// 8192 tokens x 4 rows, both norms: N = 2048: 39 us (one block of 512 threads per
+// SM 128, no ring 50), 4096: 78 (118, 101), 8184: 148 (one loading warp 165, no
+// ring 183).
+template <int W>
+cudaError_t launch_ring(const CombineArgs &a, int sms, cudaStream_t stream)
+{
+    if (a.N <= 2048)
+        return launch_ring_as<W, 16, 128, 5, 1>(a, sms, stream);
+    if (a.N <= 4096)
+        return launch_ring_as<W, 16, 256, 3, 1>(a, sms, stream);
+    if (a.N <= 6144)
+        // Single elements take so many instructions that the weights, which only
+        // one block's threads have registers for, count more than a second block
+        // (1000 tokens x 2 rows of 5001: 20 against 28 us).
+        return launch_ring_as<W, 16, 384, W == 1 ? 1 : 2, W == 1 ? 2 : 1>(a, sms, stream);
+    if (a.N <= 8192)
+        return launch_ring_as<W, 16, 512, 1, 2>(a, sms, stream);
+    return launch_ring_as<W, 32, 512, 1, 2>(a, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream)
 {
+    if (ring_pays(a, sms))
+        return a.width == 8   ? launch_ring<8>(a, sms, stream)
+               : a.width == 4 ? launch_ring<4>(a, sms, stream)
+               : a.width == 2 ? launch_ring<2>(a, sms, stream)
+                              : launch_ring<1>(a, sms, stream);
     if (a.width < 8)
         return a.width == 4   ? launch_narrow<4>(a, sms, stream)
                : a.width == 2 ? launch_narrow<2>(a, sms, stream)
                               : launch_narrow<1>(a, sms, stream);
-    // Enough tokens for every SM to have several, and rows long enough that a
-    // ring entry's hand-over (some 200 cycles) is short beside them.
-    if (a.N >= 2048 && a.N <= 16384 && a.T >= 4 * sms) {
-        const int per = (a.N / 8 + kCombineThreads - 1) / kCombineThreads;
-        return per <= 1   ? launch_ring<1>(a, sms, stream)
-               : per <= 2 ? launch_ring<2>(a, sms, stream)
-                          : launch_ring<4>(a, sms, stream);
-    }
     const int vecs = (a.N + 7) / 8;
     const bool few = a.T < sms && vecs <= 2048;
     const int most_threads = few ? 1024 : kCombineThreads;

@@ -609,7 +609,23 @@ def test_combine_many_long_rows(T, k, N, kw):
     check_combine(T, k, N, **kw)
 
 
-@pytest.mark.parametrize("T,N", [(50, 1024), (900, 2048)])
+@pytest.mark.parametrize("T,k,N,kw", [(400, 2, 515, {}), (330, 3, 1002, dict(skip=0.3)), (310, 1, 2860, {}), (305, 2, 4097, {}),
+                                      (304, 1, 8191, dict(post=False)), (310, 2, 300, dict(offset=1, pad=7)),
+                                      (304, 2, 32, dict(pad=1)), (2, 2, 9999, {})])
+def test_combine_many_rows_off_boundaries(T, k, N, kw):
+    check_combine(T, k, N, **kw)
+
+
+@pytest.mark.parametrize("T,k,N,kw", [(620, 2, 2049, {}), (610, 1, 2050, dict(offset=1, pad=4, skip=0.3)), (609, 2, 4098, {}),
+                                      (611, 1, 4100, dict(pad=8)), (609, 1, 8191, dict(post=False)),
+                                      (608, 1, 8196, dict(resid=False)), (608, 1, 16383, dict(pre=False)),
+                                      (640, 2, 2056, dict(offset=4, pad=4)), (612, 1, 2055, dict(slots=False, norm=False))])
+def test_combine_many_long_rows_off_boundaries(T, k, N, kw):
+    """Streamed rows that begin and end inside 16 bytes, the tensors' first and last among them."""
+    check_combine(T, k, N, **kw)
+
+
+@pytest.mark.parametrize("T,N", [(50, 1024), (900, 2048), (50, 1023), (700, 2049)])
 def test_combine_in_place_on_the_residual(T, N):
     k = 2
     rng = np.random.default_rng(1)
