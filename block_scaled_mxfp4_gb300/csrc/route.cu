@@ -16,15 +16,23 @@ constexpr uint32_t kFull = 0xffffffffu;
 // ------------------------------------------------------------------ routing --
 //
 // Stable counting sort of (token, slot) rows by expert.  A token picks an
-// expert at most once, so inside a run of 128 tokens an expert's rows are a
-// 128-bit mask of tokens (set with atomicOr, whose order does not matter), and
-// a row's place among them is the number of set bits before its own.  Blocks
-// write their experts' counts; the second kernel adds up the counts of the
-// blocks before its own and all of them (integers: any order, the same sum),
-// and places its tokens' rows.
+// expert at most once, so inside a run of tokens an expert's rows are a bit mask
+// of tokens (set with atomicOr, whose order does not matter), and a row's place
+// among them is the number of set bits before its own.  Blocks write their
+// experts' counts; the second kernel adds up the counts of the blocks before its
+// own and all of them (integers: any order, the same sum), and places its tokens'
+// rows.  Up to 64 tokens one block does it all, without a second launch: 16
+// tokens of 128 experts take 4.6 us, which is latency (an empty launch is 2.3).
+// 32768 tokens of 256 fp32 logits, top 8: 26 us for 38 MB, 1.4 TB/s; the
+// instructions of picking bound it (some 300 per token and warp), then the
+// second launch (some 6 us).
 
+constexpr int kPlaceAtOnce = 32;                 // blocks whose counts are read together, at most
 constexpr int kRouteThreads = 512;
-constexpr int kRouteRun = 128;                   // tokens of one mask
+// Tokens of one mask.  A block's warps do a run without a barrier: 100000 tokens
+// of 8 experts 19.9 us with 256, 26.2 with 128; of 256 experts 24.7 against 25.4.
+constexpr int kRouteRun = 256;
+constexpr int kRunWords = kRouteRun / 32;
 constexpr int kRouteSingle = 64;                 // tokens that one block does alone
 constexpr int kRouteMaxBlocks = 152;             // a block per SM
 // Shared memory of the placing kernel at most: two partial counts per thread's
@@ -68,7 +76,7 @@ __device__ __forceinline__ void finish_token(const RouteArgs &a, int t, bool liv
             float g = 0.0f;
             if (id >= 0) {
                 g = a.mode == 2 ? 1.0f / (1.0f + expf(-p.y)) : (p.y == top ? 1.0f : expf(p.y - top)) / sum;
-                atomicOr(&masks[id * 4 + (bit >> 5)], 1u << (bit & 31));
+                atomicOr(&masks[id * kRunWords + (bit >> 5)], 1u << (bit & 31));
             }
             ids[bit * a.k + j] = id;
             a.ids[static_cast<int64_t>(t) * a.k + j] = id;
@@ -261,7 +269,7 @@ __device__ __forceinline__ int block_scan(int *total, int E)
 // Against picking, a quarter of the instructions, and for a lone token five
 // exchanges in a row where picking eight experts takes eighty.
 template <int LANES>
-constexpr int kCandidates = LANES == 1 || LANES == 4 ? 32 : 64;   // of one token (what shared memory leaves)
+constexpr int kCandidates = LANES == 4 ? 16 : 64;        // of one token (4 lanes: all of its experts)
 
 __device__ __forceinline__ void exchange(float &hi, float &lo)
 {
@@ -270,6 +278,16 @@ __device__ __forceinline__ void exchange(float &hi, float &lo)
     lo = b;
 }
 
+// exp(z) for z <= 0 as 2^(z log2 e); 0 for NaN and below the smallest normal
+// number, which is nothing beside the largest logit's 1.
+__device__ __forceinline__ float exp_below(float z)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaxf(z, -200.0f) * 1.4426950408889634f));
+    return r;
+}
+
+// NaN counts as nothing.
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
     float r;
@@ -309,9 +327,6 @@ __device__ __forceinline__ void bound_tokens(const RouteArgs &a, int t, bool liv
             continue;
 #pragma unroll
         for (int c = g * (CH / NG); c < (g + 1) * (CH / NG); ++c) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x[c][i] = fmaxf(x[c][i], ninf);            // NaN -> -inf
             best[g] = max3(max3(best[g], x[c][0], x[c][1]), x[c][2], x[c][3]);
             reinterpret_cast<float4 *>(keys)[32 * c + lane] = make_float4(x[c][0], x[c][1], x[c][2], x[c][3]);
         }
@@ -347,11 +362,19 @@ __device__ __forceinline__ void bound_tokens(const RouteArgs &a, int t, bool liv
     if (a.mode == 1 && top > ninf) {
         // Terms far below the largest do not matter to the sum, so the fast
         // exponential keeps it to a few 2^-24 of itself.
+        if (top < __int_as_float(0x7f800000)) {
 #pragma unroll
-        for (int c = 0; c < CH; ++c)
+            for (int c = 0; c < CH; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sum += x[c][i] == top ? 1.0f : __expf(x[c][i] - top);
+                for (int i = 0; i < 4; ++i)
+                    sum += exp_below(x[c][i] - top);
+        } else {
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sum += x[c][i] == top ? 1.0f : 0.0f;   // infinite logits share the whole
+        }
     }
     const float low = fmaxf(bar, -3.402823466e38f);        // -inf is no candidate
     uint32_t hits = 0u;
@@ -403,8 +426,8 @@ __device__ __forceinline__ int place_in_run(const uint32_t *masks, int e, int bi
 {
     int place = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const uint32_t m = masks[4 * e + w];
+    for (int w = 0; w < kRunWords; ++w) {
+        const uint32_t m = masks[kRunWords * e + w];
         place += w < (bit >> 5) ? __popc(m) : w == (bit >> 5) ? __popc(m & ((1u << (bit & 31)) - 1u)) : 0;
     }
     return place;
@@ -420,13 +443,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) route_pick_kernel(const __gri
     uint4 *all_keys = reinterpret_cast<uint4 *>(smem_u32); // [warps][CH][32]
     float2 *all_picks = reinterpret_cast<float2 *>(all_keys + THREADS * CH);         // [warps][TPW][k]
     float2 *all_found = all_picks + WARPS * TPW * a.k;                               // [warps][TPW][candidates]
-    uint32_t *masks = reinterpret_cast<uint32_t *>(all_found + (BOUND ? WARPS * TPW * kCandidates<LANES> : 0));   // [E][4]
-    int *run = reinterpret_cast<int *>(masks + 4 * a.E);   // [E]
+    uint32_t *masks = reinterpret_cast<uint32_t *>(all_found + (BOUND ? WARPS * TPW * kCandidates<LANES> : 0));   // [E][kRunWords]
+    int *run = reinterpret_cast<int *>(masks + kRunWords * a.E);   // [E]
     int *ids = run + a.E;                                  // [tokens of a run][k]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * a.chunk;
     const int t1 = min(a.T, t0 + a.chunk);
-    for (int i = threadIdx.x; i < 5 * a.E; i += THREADS)
+    for (int i = threadIdx.x; i < (kRunWords + 1) * a.E; i += THREADS)
         masks[i] = 0u;                                     // run too
     pdl_wait_prerequisites();
     if (threadIdx.x == 0)
@@ -436,6 +459,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) route_pick_kernel(const __gri
         const int s1 = min(t1, s0 + kRouteRun);
         for (int q = s0 + warp * TPW; q < s1; q += WARPS * TPW) {
             const int t = q + lane / LANES;
+            if (t + WARPS * TPW < t1) {                    // this warp's next logits, on their way to L2
+                const int64_t size = a.fp32 ? 4 : 2;
+                const char *next = static_cast<const char *>(a.logits) + static_cast<int64_t>(t + WARPS * TPW) * a.ldl * size;
+                for (int64_t o = 128 * (lane & (LANES - 1)); o < a.E * size; o += 128 * LANES)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(next + o));
+            }
             uint4 *keys = all_keys + warp * CH * 32;
             float2 *picks = all_picks + warp * TPW * a.k;
             if constexpr (BOUND)
@@ -453,9 +482,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) route_pick_kernel(const __gri
         }
         __syncthreads();
         for (int e = threadIdx.x; e < a.E; e += THREADS) {
-            uint4 *m = reinterpret_cast<uint4 *>(masks) + e;
-            run[e] += __popc(m->x) + __popc(m->y) + __popc(m->z) + __popc(m->w);
-            *m = make_uint4(0u, 0u, 0u, 0u);
+            int n = 0;
+#pragma unroll
+            for (int w = 0; w < kRunWords; ++w) {
+                n += __popc(masks[kRunWords * e + w]);
+                masks[kRunWords * e + w] = 0u;
+            }
+            run[e] += n;
         }
     }
     if (a.blocks > 1) {
@@ -466,8 +499,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) route_pick_kernel(const __gri
             count[e] = e < a.E ? static_cast<uint16_t>(run[e]) : uint16_t(0);
         return;
     }
-    for (int e = threadIdx.x; e < a.E; e += THREADS)
-        run[e] = __popc(masks[4 * e]) + __popc(masks[4 * e + 1]) + __popc(masks[4 * e + 2]) + __popc(masks[4 * e + 3]);
+    for (int e = threadIdx.x; e < a.E; e += THREADS) {
+        int n = 0;
+#pragma unroll
+        for (int w = 0; w < kRouteSingle / 32; ++w)        // a lone block's tokens
+            n += __popc(masks[kRunWords * e + w]);
+        run[e] = n;
+    }
     __syncthreads();
     const int all = block_scan(run, a.E);
     for (int e = threadIdx.x; e <= a.E; e += THREADS)
@@ -483,6 +521,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) route_pick_kernel(const __gri
     }
 }
 
+__host__ __device__ constexpr int place_at_once(int ep)
+{
+    return kRouteThreads / (ep / 8) < kPlaceAtOnce ? kRouteThreads / (ep / 8) : kPlaceAtOnce;
+}
+
 // Each block adds up all picking blocks' counts and those before its own, then
 // places the rows of the tokens that picking block had.
 __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid_constant__ RouteArgs a)
@@ -490,7 +533,7 @@ __global__ void __launch_bounds__(kRouteThreads) route_place_kernel(const __grid
     extern __shared__ __align__(16) uint32_t smem_u32[];
     const int ep = (a.E + 7) / 8 * 8, lanes = ep / 8;      // threads of one block's counts
     const int me = blockIdx.x;
-    const int at_once = kRouteThreads / lanes;             // blocks whose counts are read together
+    const int at_once = place_at_once(ep);                 // blocks whose counts are read together
     uint32_t *part = smem_u32;                             // [at_once][2][ep]: all blocks, the blocks before
     int *total = reinterpret_cast<int *>(part + 2 * at_once * ep);   // [ep]
     int *mine = total + ep;                                // [ep]
@@ -577,8 +620,8 @@ cudaError_t launch_pick(const RouteArgs &a, cudaStream_t stream)
 {
     constexpr auto kern = route_pick_kernel<THREADS, BLOCKS, LANES, CH, BOUND>;
     auto bytes = [](int k, int E) {
-        return THREADS * CH * 16 + THREADS / LANES * (k + (BOUND ? kCandidates<LANES> : 0)) * 8 + 5 * E * 4 +
-               kRouteRun * k * 4;
+        return THREADS * CH * 16 + THREADS / LANES * (k + (BOUND ? kCandidates<LANES> : 0)) * 8 +
+               (kRunWords + 1) * E * 4 + kRouteRun * k * 4;
     };
     // The most that any E and k need of this instance.
     const cudaError_t e = opt_in<kern>(bytes(BOUND ? 8 : kMaxTopK, LANES * CH * 4));
@@ -597,16 +640,27 @@ cudaError_t launch_warps(const RouteArgs &a, cudaStream_t stream)
                         : launch_pick<kRouteThreads, 1, 32, 8, BOUND>(a, stream);
 }
 
-// `lanes` lanes per token.
+// LANES lanes per token, `chunks` chunks of four experts per lane.  One block of
+// 32 warps per SM: with three of 8 the placing kernel has three times the counts
+// to read (32768 tokens of 256 experts: 26.9 against 31.5 us for both kernels).
+template <int LANES, bool BOUND>
+cudaError_t launch_chunks(const RouteArgs &a, int chunks, cudaStream_t stream)
+{
+    if (chunks <= 2)
+        return launch_pick<1024, 1, LANES, 2, BOUND>(a, stream);
+    if (chunks <= 4)
+        return launch_pick<1024, 1, LANES, 4, BOUND>(a, stream);
+    return launch_pick<1024, 1, LANES, 8, BOUND>(a, stream);
+}
+
 template <bool BOUND>
 cudaError_t launch_lanes(const RouteArgs &a, int lanes, cudaStream_t stream)
 {
+    const int chunks = (a.E + 4 * lanes - 1) / (4 * lanes);
     switch (lanes) {
-    case 1: return launch_pick<384, 1, 1, 8, BOUND>(a, stream);
-    case 2: return launch_pick<512, 1, 2, 8, BOUND>(a, stream);
-    case 4: return launch_pick<1024, 1, 4, 8, BOUND>(a, stream);
-    case 8: return launch_pick<1024, 1, 8, 8, BOUND>(a, stream);
-    case 16: return launch_pick<1024, 1, 16, 8, BOUND>(a, stream);
+    case 4: return launch_pick<1024, 1, 4, 2, BOUND>(a, stream);
+    case 8: return launch_chunks<8, BOUND>(a, chunks, stream);
+    case 16: return launch_chunks<16, BOUND>(a, chunks, stream);
     default: return launch_pick<1024, 1, 32, 8, BOUND>(a, stream);
     }
 }
@@ -626,23 +680,23 @@ cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream)
 {
     if (a.T == 0)
         return launch_dependent(route_empty_kernel, dim3(1), dim3(256), 0, stream, a.offsets, a.E);
-    // Lanes per token: as few as hold its experts in 32 registers each, which
-    // shares the instructions among the most tokens, once that still leaves
-    // every SM 16 warps; otherwise a whole warp per token, the shortest time
-    // for one.  One block of 32 warps per SM: with three of 8 the placing kernel
-    // has three times the counts to read (32768 tokens of 256 experts: 26.9
-    // against 31.5 us for both kernels).
-    int lanes = 1;
-    while (lanes * 32 < a.E)
+    // Lanes per token: as many as let the block's warps do its tokens (of a run
+    // of 128) in one pass, which has the latency, and at least as many as hold
+    // the experts in 32 registers each.  32768 tokens: 64 experts 14.6 us, with
+    // the fewest lanes 22; 8 experts 10.8 against 37.  5000 tokens of 256 experts:
+    // 11.8 us, with the fewest lanes 12.7, with a warp per token 14.4.  A warp per
+    // token also runs in blocks of 16 warps, for up to 16 tokens.
+    const int tokens = min(min(a.T, a.chunk), 128);
+    int lanes = 4;
+    while (lanes < 32 && (lanes * 32 < a.E || (lanes * 4 < a.E && tokens * lanes * 2 / 32 <= (lanes < 16 ? 32 : 16))))
         lanes *= 2;
-    const bool many = static_cast<int64_t>(a.T) * lanes / 32 >= static_cast<int64_t>(sms) * 16;
-    const bool bound = a.k <= 8;
+    const bool bound = a.k <= 8, many = lanes < 32 || tokens > 16;
     const cudaError_t picked = many ? (bound ? launch_lanes<true>(a, lanes, stream) : launch_lanes<false>(a, lanes, stream))
                                     : (bound ? launch_warps<true>(a, stream) : launch_warps<false>(a, stream));
     if (picked != cudaSuccess || a.blocks == 1)
         return picked;
     const int ep = (a.E + 7) / 8 * 8;
-    const size_t smem = static_cast<size_t>(2 * (kRouteThreads / (ep / 8)) + 2) * ep * 4;
+    const size_t smem = static_cast<size_t>(2 * place_at_once(ep) + 2) * ep * 4;
     const cudaError_t e = opt_in<route_place_kernel>(kPlaceSmem);
     if (e != cudaSuccess)
         return e;

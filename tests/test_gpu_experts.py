@@ -140,9 +140,20 @@ def test_route_strided_scaled_and_all_to_one():
     check_route(x, 1, 0)
 
 
+@pytest.mark.parametrize("T,E,k", [(10, 200, 8), (16, 400, 5), (13, 900, 8), (9, 100, 9), (9, 200, 10), (9, 500, 16), (9, 1000, 12),
+                                   (20, 128, 8), (56, 16, 4), (33, 600, 8)])
+def test_route_few_tokens(T, E, k):
+    g = torch.Generator().manual_seed(T + E)
+    x = torch.randn((T, E), generator=g) * 2
+    check_route(x.cuda(), k, 1)
+    check_route(x.to(torch.bfloat16).cuda(), k, 0)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("T,E,k,mode", [(80001, 8, 2, 0), (78000, 30, 8, 1), (40001, 64, 4, 0), (20000, 100, 8, 1),
-                                        (9985, 250, 8, 2), (5000, 512, 6, 0), (2500, 777, 7, 1), (20000, 128, 12, 0)])
+                                        (9985, 250, 8, 2), (5000, 512, 6, 0), (2500, 777, 7, 1), (20000, 128, 12, 0),
+                                        (5000, 251, 5, 1), (30000, 12, 10, 1), (20000, 64, 9, 0), (12000, 256, 16, 1),
+                                        (1000, 100, 9, 2), (1000, 200, 10, 0), (1000, 512, 11, 1), (500, 1024, 15, 0)])
 def test_route_many_tokens(T, E, k, mode, dtype):
     """The forms for many tokens, all lane counts: random logits, then ties,
     masked tokens, infinities and NaN among them."""
