@@ -22,7 +22,13 @@ __device__ int g_status = 0;                     // bounded waits that ran out
 //   n = h rsqrt(mean h^2 + eps) w_pre                -> Nrm, one rounding, from the fp32 h
 //
 // One block per token (grid-stride), the row in registers between the two
-// sums, so that every input is read once.
+// sums, so that every input is read once.  b, the sums and h are fp32; the sum
+// over slots keeps their order, so a result does not depend on the launch.
+//
+// Three forms.  Few tokens: as many threads per token as have eight elements
+// each, four rows in flight; the latency of two dependent loads and of the sums
+// bounds it (8 tokens x 8 rows of 7168: 3.8 us a call, an empty one's 2.9).  Rows off 16-byte boundaries: narrower units.  Many tokens with long
+// rows: a ring that streams rows ahead, bound by HBM.
 
 constexpr int kCombineThreads = 512;
 constexpr int kCombineMaxVec = 8;                // 8-element vectors of one thread
@@ -127,7 +133,8 @@ __device__ __forceinline__ void load_unit(const uint16_t *p, float (&x)[W])
         x[i] = pick<W>(v, i);
 }
 
-// VPT 8-element vectors per thread, JC slots' rows in flight together.
+// VPT 8-element vectors per thread, JC slots' rows in flight together.  8192
+// tokens x 4 rows of 1024, below the ring's sizes: 26 us, 118 MB, 4.5 TB/s.
 // Few tokens run on up to MAXT = 1024 threads each, the shortest time for one.
 template <int VPT, int JC, int MAXT>
 __global__ void __launch_bounds__(MAXT, MAXT == kCombineThreads && VPT <= 2 ? 2 : 1) combine_kernel(const __grid_constant__ CombineArgs a)
@@ -252,6 +259,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == kCombineThreads && VPT <= 2 ? 2 
 // threads take units of W elements in turn, so that a warp's accesses are
 // contiguous whatever W is.  THREADS threads with E elements each (both fixed, so
 // that a row's units are one pointer and constants); JC rows in flight together.
+// 6437 tokens x 3 rows of 1196: 22 to 25 us, 92 MB, bound by instructions.
 template <int W, int E, int JC, int THREADS, int MINB>
 __global__ void __launch_bounds__(THREADS, MINB) combine_narrow_kernel(const __grid_constant__ CombineArgs a)
 {

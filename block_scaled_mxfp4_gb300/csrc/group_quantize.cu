@@ -21,6 +21,11 @@ constexpr uint32_t kFull = 0xffffffffu;
 // a whole sector per thread.  The destinations of four slots are looked up
 // together, so that a row costs two dependent round trips (slot, then offset)
 // and not two for each slot.
+//
+// Bound by HBM when there are many rows (one read and k writes of each): 8192
+// rows of 8192, four E4M3 copies, 402 MB in 67 us, 6.0 TB/s or 90 % of a plain
+// copy's rate; with 16-byte accesses instead it takes 77 us.  Bound by the launch
+// when there are few: 64 rows of 2048, 3.0 us a call, an empty one's 2.9.
 
 constexpr int kQuantThreads = 256;
 constexpr int kQuantSlots = 4;

@@ -22,8 +22,8 @@ constexpr uint32_t kFull = 0xffffffffu;
 // experts' counts; the second kernel adds up the counts of the blocks before its
 // own and all of them (integers: any order, the same sum), and places its tokens'
 // rows.  Up to 64 tokens one block does it all, without a second launch: 16
-// tokens of 128 experts take 4.6 us, which is latency (an empty launch is 2.3).
-// 32768 tokens of 256 fp32 logits, top 8: 26 us for 38 MB, 1.4 TB/s; the
+// tokens of 128 experts take 4.7 us, which is latency (an empty call takes 2.9).
+// 32768 tokens of 256 fp32 logits, top 8: 25 us for 38 MB, 1.5 TB/s; the
 // instructions of picking bound it (some 300 per token and warp), then the
 // second launch (some 6 us).
 
