@@ -67,7 +67,7 @@ int check_product(const Product &p)
     if (p.bytes8 && (!known_fmt(p.fmt_a) || !known_fmt(p.fmt_b)))
         return MXFP4_ERR_INVALID_ARG;
     const int unit = p.bytes8 ? 16 : 32;             // elements of 16 bytes
-    if ((p.lda % unit) != 0 || (p.ldb % unit) != 0 || (p.stride_b % unit) != 0 || !aligned(p.A, 16) ||
+    if (!aligned(p.offsets, 4) || (p.lda % unit) != 0 || (p.ldb % unit) != 0 || (p.stride_b % unit) != 0 || !aligned(p.A, 16) ||
         !aligned(p.B, 16) || !aligned(p.SA, 16) || !aligned(p.SB, 16))
         return MXFP4_ERR_MISALIGNED;
     if (gated && ((p.ldd % unit) != 0 || !aligned(p.D, 16) || !aligned(p.SH, 16)))
@@ -182,6 +182,8 @@ int quantize_entry(void *Q, int64_t ldq, void *S, const void *X, int64_t ldx, in
         return MXFP4_ERR_INVALID_ARG;
     if (T > 0 && rows > 0 &&
         (!aligned(X, 16) || (ldx % 8) != 0 || !aligned(Q, 16) || (ldq % (fmt ? 16 : 32)) != 0 || !aligned(S, 16)))
+        return MXFP4_ERR_MISALIGNED;
+    if (!aligned(slot_row, 4) || !aligned(ids, 4) || !aligned(offsets, 4))
         return MXFP4_ERR_MISALIGNED;
     int sms = 0;
     const int st = check_current_device(&sms);
@@ -303,6 +305,8 @@ int mxfp4_moe_route(int *ids, float *gates, int *offsets, int *row_token, int *s
         return MXFP4_ERR_INVALID_ARG;
     if (!aligned(logits, logits_type == MXFP4_LOGITS_FP32 ? 4 : 2))
         return MXFP4_ERR_MISALIGNED;
+    if (!aligned(ids, 4) || !aligned(gates, 4) || !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(slot_row, 4))
+        return MXFP4_ERR_MISALIGNED;
     RouteArgs a;
     a.blocks = route_blocks(T, &a.chunk);
     if (static_cast<int64_t>(T) * k > 0x7FFFFFFF || a.chunk > 65504)
@@ -410,6 +414,8 @@ int mxfp4_moe_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *
     for (const void *p : {static_cast<const void *>(H), static_cast<const void *>(Nrm), Y, resid, w_post, w_pre})
         if (!aligned(p, 2))
             return MXFP4_ERR_MISALIGNED;
+    if (!aligned(slot_row, 4) || !aligned(gates, 4))
+        return MXFP4_ERR_MISALIGNED;
     if (N > 32768)
         return MXFP4_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
@@ -443,7 +449,8 @@ int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, i
     if (K > 32768)
         return MXFP4_ERR_UNSUPPORTED_SHAPE;
     if (T > 0 && (!aligned(H, 2) || !aligned(Nrm, 2) || !aligned(resid, 2) || !aligned(w_post, 2) ||
-                  !aligned(w_pre, 2) || !aligned(X, 16) || (ldx % 8) != 0 || !aligned(workspace, kAlign)))
+                  !aligned(w_pre, 2) || !aligned(X, 16) || (ldx % 8) != 0 || !aligned(ids, 4) || !aligned(gates, 4) ||
+                  !aligned(slot_row, 4) || !aligned(workspace, kAlign)))
         return MXFP4_ERR_MISALIGNED;
     const FfnLayout l = ffn_layout(T, E, k, K, F);
     if (T > 0 && (!workspace || workspace_bytes < l.total))

@@ -61,6 +61,8 @@ def values(codes, scales, fmt):
     if fmt == "e2m1":
         c = np.stack([codes & 15, codes >> 4], -1).reshape(*codes.shape[:-1], -1)
         v = E2M1[c & 7] * np.where(c & 8, -1.0, 1.0)
+    elif fmt in PADDED:
+        v = padded_values(codes, fmt)
     else:
         mag = codes & 0x7F
         grid = np.full(128, np.nan)
@@ -68,6 +70,20 @@ def values(codes, scales, fmt):
         v = grid[mag] * np.where(codes & 0x80, -1.0, 1.0)
     p = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(int) - 127))
     return v * np.repeat(p, 32, axis=-1)
+
+
+# Sub-byte formats, 16 codes packed at the start of every 16 bytes: exponent and mantissa bits.
+PADDED = {"e2m3": (2, 3), "e3m2": (3, 2), "e2m1 padded": (2, 1)}
+
+
+def padded_values(codes, fmt):
+    ebits, mbits = PADDED[fmt]
+    width, bias = 1 + ebits + mbits, 2 ** (ebits - 1) - 1
+    bits = np.unpackbits(codes.reshape(*codes.shape[:-1], -1, 16), axis=-1, bitorder="little")
+    c = (bits[..., :16 * width].reshape(*bits.shape[:-1], 16, width).astype(int) << np.arange(width)).sum(-1)
+    e, m = c >> mbits & 2 ** ebits - 1, c & 2 ** mbits - 1
+    v = np.where(e == 0, np.ldexp(1.0 * m, 1 - bias - mbits), np.ldexp(1.0 * m + 2 ** mbits, e - bias - mbits))
+    return (np.where(c >> width - 1, -1.0, 1.0) * v).reshape(codes.shape)
 
 
 def grouping(ids, E):

@@ -47,14 +47,16 @@ REFUSALS = [
                                  (dict(_12=3), "ERR_INVALID_ARG"), (dict(_5=P + 1), "ERR_MISALIGNED"),
                                  (dict(_5=P + 2, _7=1), "ERR_MISALIGNED"), (dict(_14=None), "ERR_WORKSPACE"),
                                  (dict(_15=16), "ERR_WORKSPACE"), (dict(_14=P + 16), "ERR_MISALIGNED"),
-                                 (dict(_9=1 << 30), "ERR_UNSUPPORTED_SHAPE")]),
+                                 (dict(_9=1 << 30), "ERR_UNSUPPORTED_SHAPE")]
+     + [({f"_{i}": P + 2}, "ERR_MISALIGNED") for i in range(5)]),
     (mx.mxfp4_group_quantize, QUANT, [(dict(_0=None), "ERR_INVALID_ARG"), (dict(_10=None), "ERR_INVALID_ARG"),
                                       (dict(_6=48), "ERR_INVALID_ARG"), (dict(_4=32), "ERR_INVALID_ARG"),
                                       (dict(_8=None), "ERR_INVALID_ARG"), (dict(_9=0), "ERR_INVALID_ARG"),
                                       (dict(_9=17), "ERR_INVALID_ARG"), (dict(_7=None, _8=None), "ERR_INVALID_ARG"),
                                       (dict(_7=None, _8=None, _9=1), "ERR_INVALID_ARG"),
                                       (dict(_11=0), "ERR_INVALID_ARG"), (dict(_1=80), "ERR_MISALIGNED"),
-                                      (dict(_3=P + 2), "ERR_MISALIGNED"), (dict(_2=P + 4), "ERR_MISALIGNED")]),
+                                      (dict(_3=P + 2), "ERR_MISALIGNED"), (dict(_2=P + 4), "ERR_MISALIGNED")]
+     + [({f"_{i}": P + 2}, "ERR_MISALIGNED") for i in (7, 8, 10)]),
     (mx.mxfp8_group_quantize, QUANT + [mx.MXFP8_E4M3], [(dict(_13=mx.MXFP6_E2M3), "ERR_INVALID_ARG"),
                                                         (dict(_1=72), "ERR_MISALIGNED")]),
     (mx.mxfp4_grouped_gemm, GEMM, [(dict(_0=None), "ERR_INVALID_ARG"), (dict(_9=None), "ERR_INVALID_ARG"),
@@ -64,6 +66,7 @@ REFUSALS = [
                                    (dict(_13=40), "ERR_INVALID_ARG"), (dict(_3=80), "ERR_MISALIGNED"),
                                    (dict(_2=P + 8), "ERR_MISALIGNED"), (dict(_7=64 * 64 + 16), "ERR_MISALIGNED"),
                                    (dict(_8=P + 8), "ERR_MISALIGNED"), (dict(_0=P + 1), "ERR_MISALIGNED"),
+                                   (dict(_9=P + 2), "ERR_MISALIGNED"),
                                    (dict(_11=(1 << 31) - 1, _12=1 << 30, _1=1 << 30, _7=1 << 40),
                                     "ERR_UNSUPPORTED_SHAPE")]),
     (mx.mxfp8_grouped_gemm, GEMM[:14] + [0, 1] + GEMM[14:], [(dict(_14=2), "ERR_INVALID_ARG"),
@@ -78,6 +81,7 @@ REFUSALS = [
                                   (dict(_7=None), "ERR_INVALID_ARG"), (dict(_7=None, _9=1, _6=9), "ERR_INVALID_ARG"),
                                   (dict(_9=17), "ERR_INVALID_ARG"), (dict(_16=-1.0), "ERR_INVALID_ARG"),
                                   (dict(_16=float("nan")), "ERR_INVALID_ARG"), (dict(_4=P + 1), "ERR_MISALIGNED"),
+                                  (dict(_7=P + 2), "ERR_MISALIGNED"), (dict(_8=P + 2), "ERR_MISALIGNED"),
                                   (dict(_18=40000, _1=40000, _3=40000, _5=40000, _11=40000),
                                    "ERR_UNSUPPORTED_SHAPE")]),
     (mx.mxfp4_moe_ffn, FFN, [(dict(_6=None), "ERR_INVALID_ARG"), (dict(_8=None), "ERR_INVALID_ARG"),
@@ -85,7 +89,8 @@ REFUSALS = [
                              (dict(_14=48), "ERR_INVALID_ARG"), (dict(_16=32), "ERR_INVALID_ARG"),
                              (dict(_18=None), "ERR_INVALID_ARG"), (dict(_29=1000), "ERR_WORKSPACE"),
                              (dict(_28=None), "ERR_WORKSPACE"), (dict(_28=P + 8), "ERR_MISALIGNED"),
-                             (dict(_4=P + 2), "ERR_MISALIGNED"), (dict(_13=32800, _5=32800), "ERR_INVALID_ARG")]),
+                             (dict(_4=P + 2), "ERR_MISALIGNED"),
+                             *[({f"_{i}": P + 2}, "ERR_MISALIGNED") for i in (6, 7, 8, 9)], (dict(_13=32800, _5=32800), "ERR_INVALID_ARG")]),
 ]
 
 

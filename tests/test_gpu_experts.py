@@ -278,12 +278,15 @@ def test_group_quantize_skips_rows_outside_the_arrays():
 
 # ----------------------------------------------------------------- products --
 
-FMT_CODE = {"e2m1": None, "e4m3": 0, "e5m2": 1}
+FMT_CODE = {"e2m1": None, "e4m3": 0, "e5m2": 1, "e2m3": mx.MXFP6_E2M3, "e3m2": mx.MXFP6_E3M2,
+            "e2m1 padded": mx.MXFP4_E2M1_PADDED}
 
 
 def random_operand(rng, rows, K, fmt, spread=2):
     if fmt == "e2m1":
         q = rng.integers(0, 256, size=(rows, K // 2), dtype=np.uint8)
+    elif fmt in ref.PADDED:
+        q = rng.integers(0, 256, size=(rows, K), dtype=np.uint8)   # the padding bytes too: nothing reads them
     else:
         top = {"e4m3": 0x70, "e5m2": 0x50}[fmt]
         q = (rng.integers(0x20, top, size=(rows, K)) | rng.integers(0, 2, size=(rows, K)) << 7).astype(np.uint8)
@@ -381,6 +384,14 @@ def test_grouped_gemm(name, N, K):
 @pytest.mark.parametrize("name,N,K", [("decode", 256, 256), ("tile edges", 320, 96), ("ragged", 72, 800), ("one row", 8, 32)])
 def test_grouped_gemm_bytes(fmt, fmt_b, name, N, K):
     check_gemm(Grouped(COUNTS[name], N, K, fmt, fmt_b, seed=N + K))
+
+
+@pytest.mark.parametrize("fmt,fmt_b", [("e2m3", "e2m3"), ("e3m2", "e4m3"), ("e5m2", "e2m1 padded"), ("e2m1 padded", "e3m2")])
+@pytest.mark.parametrize("name,N,K", [("decode", 72, 288), ("ragged", 256, 160)])
+def test_grouped_products_of_padded_formats(fmt, fmt_b, name, N, K):
+    check_gemm(Grouped(COUNTS[name], N, K, fmt, fmt_b, seed=N + K))
+    p = Grouped(COUNTS[name], 96, K, fmt, fmt_b, halves=2, seed=N + K)
+    check_swiglu(p, "e4m3", small(p))
 
 
 def test_grouped_gemm_strides_alpha_capacity():
