@@ -751,6 +751,8 @@ cudaError_t launch_combine(const CombineArgs &a, int sms, cudaStream_t stream)
                : a.width == 2 ? launch_narrow<2>(a, sms, stream)
                               : launch_narrow<1>(a, sms, stream);
     const int vecs = (a.N + 7) / 8;
+    // Fewer tokens than SMs: up to 1024 threads each (8 tokens x 8 rows of 7168:
+    // 3.8 us, with 512 threads 5.1).
     const bool few = a.T < sms && vecs <= 2048;
     const int most_threads = few ? 1024 : kCombineThreads;
     const int threads = vecs < most_threads ? (vecs + 31) / 32 * 32 : most_threads;

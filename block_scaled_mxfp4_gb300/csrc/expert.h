@@ -111,7 +111,8 @@ struct GroupedArgs {
     uint32_t idesc8;            // byte formats: instruction descriptor
     int early;                  // offsets, B and its scales may be read before the preceding
                                 // grid ends: it is a kernel of the same call, which waited
-                                // for the work before the call
+                                // for the work before the call (one-token block of 3 x 544:
+                                // 13.5 us, without 14.9)
     long long wait_limit;
 };
 struct GroupedMaps {

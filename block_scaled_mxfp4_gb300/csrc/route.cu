@@ -33,7 +33,9 @@ constexpr int kRouteThreads = 512;
 // of 8 experts 19.9 us with 256, 26.2 with 128; of 256 experts 24.7 against 25.4.
 constexpr int kRouteRun = 256;
 constexpr int kRunWords = kRouteRun / 32;
-constexpr int kRouteSingle = 64;                 // tokens that one block does alone
+// Tokens that one block does alone, without a workspace (64 tokens of 128 experts:
+// 7.5 us in one launch and in two).
+constexpr int kRouteSingle = 64;
 constexpr int kRouteMaxBlocks = 152;             // a block per SM
 // Shared memory of the placing kernel at most: two partial counts per thread's
 // eight experts, their sums.
@@ -690,6 +692,8 @@ cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream)
     int lanes = 4;
     while (lanes < 32 && (lanes * 32 < a.E || (lanes * 4 < a.E && tokens * lanes * 2 / 32 <= (lanes < 16 ? 32 : 16))))
         lanes *= 2;
+    // (16 tokens of 128 experts 4.8 us by bounding, 6.0 by picking; 32768 of 256 24.3
+    // and 31.3.)
     const bool bound = a.k <= 8, many = lanes < 32 || tokens > 16;
     const cudaError_t picked = many ? (bound ? launch_lanes<true>(a, lanes, stream) : launch_lanes<false>(a, lanes, stream))
                                     : (bound ? launch_warps<true>(a, stream) : launch_warps<false>(a, stream));
