@@ -154,8 +154,10 @@ int run_product(const Product &p, cudaStream_t stream)
         if (a.vec_ok && !encode(&m.D, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.D, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B))
             return MXFP4_ERR_CUDA;
     }
-    if (p.bytes8)
+    if (p.bytes8) {
         a.idesc8 = idesc_mxf8(256, 256, static_cast<uint32_t>(p.fmt_a), static_cast<uint32_t>(p.fmt_b));
+        a.idesc8_solo = idesc_mxf8(128, 256, static_cast<uint32_t>(p.fmt_a), static_cast<uint32_t>(p.fmt_b));
+    }
     a.wait_limit = current_wait_limit();
     return status_of(launch_grouped(a, m, p.bytes8, p.out, stream));
 }

@@ -1,5 +1,5 @@
-// Products grouped by expert with ragged sizes, on CTA pairs (tcgen05
-// cta_group::2, block-scaled FP4 or byte formats):
+// Products grouped by expert with ragged sizes, on CTA pairs or single CTAs
+// (tcgen05 cta_group::2 or ::1, block-scaled FP4 or byte formats):
 //
 //   plain  D[r, n] = alpha * sum_k A[r, k] B[e, n, k]             (bf16)
 //   gated  h[r, f] = silu(alpha * g) * (alpha * u), g and u the products with
@@ -17,9 +17,13 @@
 // 128 h + [64, 128) the up products of the same f, so one thread of the
 // epilogue finds g and u of 64 consecutive f in its own tensor-memory lane:
 // activation, block maxima and rounding need no exchange between threads.
-// The rows of one group are the M side although decoding leaves most of the
-// 256 empty: a stage's MMAs take 512 tensor cycles whatever the rows, less
-// than the ~700 cycles that its 32 KB of weights take to stream from HBM.
+// Where the groups are small (launch_grouped has the rule) a CTA takes a tile of
+// 128 rows x 256 columns by itself, one M = 128, N = 256 MMA, with all of B's rows
+// in its own shared memory: twice as many tiles run together.  "Pair" below is
+// then one CTA, and the leader.
+// The rows of one group are the M side although decoding leaves most of them
+// empty: a stage's MMAs take 512 tensor cycles whatever the rows, less than its
+// 32 KB of weights take to stream from HBM.
 //
 // The grid is persistent: pair i takes tiles i, i + pairs, ... of a list that
 // every CTA derives from `offsets` (prefix sums of the groups' row tiles in
@@ -87,6 +91,47 @@ __device__ __forceinline__ void mma_mxf8_pair_elect(uint32_t d_tmem, uint64_t ad
         : "memory");
 }
 
+// The same by one CTA for its own accumulator.
+__device__ __forceinline__ void mma_mxf8_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_mxf4_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
+template <int SOLO>
+__device__ __forceinline__ void commit_elect(uint64_t *bar, uint16_t mask)
+{
+    if constexpr (SOLO)
+        asm volatile(
+            "{\n\t.reg .pred e;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar))
+            : "memory");
+    else
+        mma_commit_pair_elect(bar, mask);
+}
+
 // Registers move from the warpgroups that load and issue to the epilogue's,
 // which holds a warp's 128 accumulator columns at once.  Their shares, 256
 // threads each, stay within what the block was launched with (128 x 512; the
@@ -117,19 +162,24 @@ constexpr int kOutBoxBytes = 32 * 64;            // one epilogue warp's 32 rows 
 // The plain form's epilogue keeps a 2 KB box per warp beside the ring.  Six
 // stages then leave little room for the tile list, so that more groups than
 // that (WIDE) run with five: 32768 rows, N = 4096, K = 2048: 107 against 113 us.
-template <bool BYTES8, bool GATED, bool WIDE>
+//
+// SOLO: CTAs by themselves, tiles of 128 rows, a stage's B all of the tile's 256.
+// With 32, at most 32 rows exist: a stage's A is those (the MMA's others are what
+// lies behind, and reach only themselves).
+template <bool BYTES8, bool GATED, bool WIDE, int SOLO>
 struct GroupedCfg {
-    static constexpr int STAGES = !GATED && WIDE ? 5 : 6;
-    static constexpr int OUT_BYTES = GATED ? 0 : 8 * kOutBoxBytes;
+    static constexpr int STAGES = SOLO == 128 ? 4 : SOLO || (!GATED && WIDE) ? 5 : 6;
+    static constexpr int ROWS = SOLO ? 128 : 256;
+    static constexpr int OUT_BYTES = GATED ? 0 : (SOLO == 32 ? 2 : 8) * kOutBoxBytes;
     static constexpr int G = BYTES8 ? 1 : 2;
-    static constexpr int A_BYTES = 128 * 128;
-    static constexpr int B_BYTES = 128 * 128;
+    static constexpr int A_BYTES = (SOLO == 32 ? 32 : 128) * 128;
+    static constexpr int B_BYTES = (SOLO ? 256 : 128) * 128;
     static constexpr int SFA_BYTES = G * kSfAtomBytes;
     static constexpr int SFB_BYTES = 2 * G * kSfAtomBytes;
     static constexpr int STAGE_BYTES = (A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES + 1023) / 1024 * 1024;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
     static constexpr int BAR_BYTES = 256;
-    static constexpr int MAX_GROUPS = !GATED && !WIDE ? 80 : kMaxGroups;
+    static constexpr int MAX_GROUPS = GATED || SOLO == 32 ? kMaxGroups : SOLO ? 860 : WIDE ? kMaxGroups : 80;
     static constexpr int TABLE_BYTES = 2 * (MAX_GROUPS + 1) * 4;   // offsets and row-tile prefix sums
     static constexpr int USED_BYTES = RING_BYTES + OUT_BYTES + BAR_BYTES + TABLE_BYTES;
     // The ring wants 1024-byte alignment.  Dynamic shared memory starts on such
@@ -167,6 +217,7 @@ struct Tile {
     bool single;        // the group has no other row tile
 };
 
+template <int ROWS>
 __device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
 {
     // The last group whose first tile is not after i (empty groups share their
@@ -186,15 +237,16 @@ __device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
     r.q = r.single ? local : local / mt;
     const int p = r.single ? 0 : local - r.q * mt;
     r.e = lo;
-    r.row0 = t.off[lo] + p * 256;
+    r.row0 = t.off[lo] + p * ROWS;
     r.end = t.off[lo + 1];
-    r.sfa = static_cast<int>(group_sf_block(t.off[lo], lo)) + 2 * p;
+    r.sfa = static_cast<int>(group_sf_block(t.off[lo], lo)) + ROWS / 128 * p;
     return r;
 }
 
 // Fill the tables: thread t takes groups 2t and 2t + 1 of up to 1024.  Up to 64
 // groups are one warp's work and need no exchange between warps.  warp_sum: 16
 // words of shared memory.  Ends with a block barrier.
+template <int ROWS>
 __device__ __forceinline__ void build_tables(const int *offsets, int groups, int rows, int *off, int *base,
                                              int *warp_sum)
 {
@@ -210,7 +262,7 @@ __device__ __forceinline__ void build_tables(const int *offsets, int groups, int
         int c[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            c[i] = 2 * t + i < groups ? (max(o[i + 1] - o[i], 0) + 255) / 256 : 0;
+            c[i] = 2 * t + i < groups ? (max(o[i + 1] - o[i], 0) + ROWS - 1) / ROWS : 0;
         int sum = c[0] + c[1];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -388,11 +440,11 @@ __device__ __forceinline__ void store_gated(const GroupedArgs &a, int r, int loc
 }
 
 // OUT: -1 plain bf16, else static_cast<int>(QuantFmt) of the gated form.
-template <bool BYTES8, int OUT, bool WIDE>
+template <bool BYTES8, int OUT, bool WIDE, int SOLO>
 __global__ void __launch_bounds__(512, 1)
-    grouped_pair(const __grid_constant__ GroupedArgs a, const __grid_constant__ GroupedMaps maps)
+    grouped_product(const __grid_constant__ GroupedArgs a, const __grid_constant__ GroupedMaps maps)
 {
-    using Cf = GroupedCfg<BYTES8, (OUT >= 0), WIDE>;
+    using Cf = GroupedCfg<BYTES8, (OUT >= 0), WIDE, SOLO>;
     constexpr int G = Cf::G;
     constexpr bool GATED = OUT >= 0;
     constexpr int STAGES = Cf::STAGES;
@@ -420,26 +472,31 @@ __global__ void __launch_bounds__(512, 1)
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank() & 1u;
+    const uint32_t rank = SOLO ? 0u : cluster_ctarank() & 1u;
     const bool leader = rank == 0;
-    const int pair = blockIdx.x / 2;
-    const int pairs = gridDim.x / 2;
+    const int pair = blockIdx.x / (SOLO ? 1 : 2);
+    const int pairs = gridDim.x / (SOLO ? 1 : 2);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 3);          // this CTA's three producers
             mbar_init(&empty[s], 1);         // the pair's MMA commit
-            mbar_init(&sf_ready[s], 8);      // the scale writers of both CTAs
+            mbar_init(&sf_ready[s], SOLO ? 4 : 8);   // the scale writers of both CTAs
         }
         mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 16);            // the epilogue warps of both CTAs
+        mbar_init(acc_empty, SOLO ? 8 : 16); // the epilogue warps of both CTAs
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 5) {
-        tmem_alloc_pair(tmem_slot, Cf::TMEM_COLS);
-        tmem_relinquish_pair();
+        if constexpr (SOLO) {
+            tmem_alloc(tmem_slot, Cf::TMEM_COLS);
+            tmem_relinquish();
+        } else {
+            tmem_alloc_pair(tmem_slot, Cf::TMEM_COLS);
+            tmem_relinquish_pair();
+        }
     }
     if (warp == 4 && lane == 0) {
         prefetch_tensormap(&maps.A);
@@ -449,7 +506,10 @@ __global__ void __launch_bounds__(512, 1)
         prefetch_tensormap(&maps.SB);
     }
     tc_fence_before();
-    cluster_sync();                          // barriers of both CTAs initialised
+    if constexpr (SOLO)
+        __syncthreads();
+    else
+        cluster_sync();                      // barriers of both CTAs initialised
     tc_fence_after();
     const uint64_t keep = l2_policy_evict_last();
     const uint64_t once = l2_policy_evict_first();
@@ -461,7 +521,7 @@ __global__ void __launch_bounds__(512, 1)
     // everything else; with a.early only the rows and their scales do.
     if (!a.early)
         pdl_wait_prerequisites();
-    build_tables(offsets, groups, rows, tab_off, tab_base, warp_sum);
+    build_tables<Cf::ROWS>(offsets, groups, rows, tab_off, tab_base, warp_sum);
     const uint32_t tmem = *tmem_slot;
     const TileTable table{tab_off, tab_base, groups, nt};
     const int tiles = table.tiles();
@@ -477,10 +537,10 @@ __global__ void __launch_bounds__(512, 1)
         const int half = warp >> 3;
         const int row = static_cast<int>(rank) * 128 + quarter * 32 + lane;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
-        const uint32_t lead_empty = map_to_rank(smem_addr(acc_empty), 0);
+        const uint32_t lead_empty = SOLO ? 0u : map_to_rank(smem_addr(acc_empty), 0);
         uint32_t acc_phase = 0;
         for (int t = pair; t < tiles; t += pairs) {
-            const Tile tl = tile_at(table, t);
+            const Tile tl = tile_at<Cf::ROWS>(table, t);
             bool ok = mbar_wait(acc_full, acc_phase, abort_flag, a.wait_limit, &g_status);
             if (!__all_sync(kFull, ok))
                 break;
@@ -518,7 +578,7 @@ __global__ void __launch_bounds__(512, 1)
                     // touch a line each, and 64 KB of them per tile hold up
                     // the MMA warp's barrier polls in the same queue (32768 rows,
                     // N = 4000, K = 2048: 109 us, with those stores 122).
-                    uint8_t *buf = stage_out + (half * 4 + quarter) * kOutBoxBytes;
+                    uint8_t *buf = stage_out + (SOLO == 32 ? half : half * 4 + quarter) * kOutBoxBytes;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         if (n0 + 32 * c >= a.N)
@@ -565,12 +625,12 @@ __global__ void __launch_bounds__(512, 1)
                 int issued = 0;
                 bool stop = false;
                 for (int t = pair; t < tiles && !stop; t += pairs) {
-                    const Tile tl = tile_at(table, t);
+                    const Tile tl = tile_at<Cf::ROWS>(table, t);
                     const int arow = tl.row0 + static_cast<int>(rank) * 128;
                     const bool rows_here = arow < tl.end;
                     // Rows of a decoding step: a quarter of A's box (32 rows in 26
                     // groups, N = K = 4096: 40.4 us, with whole boxes 54.1).
-                    const bool few = tl.end - arow <= 32;
+                    const bool few = SOLO == 32 || tl.end - arow <= 32;
                     // A group of one row tile reads its weights once (same product
                     // with everything kept: 110 us against 109; 26 groups of a
                     // decoding step 41.3 against 40.4).
@@ -597,6 +657,9 @@ __global__ void __launch_bounds__(512, 1)
                             const int n = GATED ? tl.q * 128 + static_cast<int>(rank) * 64
                                                 : tl.q * 256 + static_cast<int>(rank) * 128;
                             tma_load_4d(st + Cf::A_BYTES, &maps.B, &full[stage], kt * 128, n, 0, tl.e, pol_b);
+                            if (SOLO)            // what the peer of a pair would load
+                                tma_load_4d(st + Cf::A_BYTES + 128 * 128, &maps.B, &full[stage], kt * 128,
+                                            n + (GATED ? 64 : 128), 0, tl.e, pol_b);
                         } else {
                             // Plain: two 128-row blocks of the expert.  Gated: the
                             // block of the gate rows and the block of the up rows.
@@ -623,7 +686,7 @@ __global__ void __launch_bounds__(512, 1)
             // the four lane quarters' replicas.
             const int quarter = warp & 3;
             const uint32_t t_q = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + Cf::ACC_COLS;
-            const uint32_t lead_ready = map_to_rank(smem_addr(&sf_ready[0]), 0);
+            const uint32_t lead_ready = SOLO ? 0u : map_to_rank(smem_addr(&sf_ready[0]), 0);
             const int my_tiles = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
             const int total = my_tiles * a.kt;
             int stage = 0;
@@ -682,7 +745,7 @@ __global__ void __launch_bounds__(512, 1)
         } else if (warp == 5) {
             // ------------------------------------------------ MMA (leader) --
             if (leader) {
-                const uint32_t idesc = BYTES8 ? a.idesc8 : idesc_mxf4(256, 256);
+                const uint32_t idesc = BYTES8 ? (SOLO ? a.idesc8_solo : a.idesc8) : idesc_mxf4(SOLO ? 128 : 256, 256);
                 int stage = 0;
                 uint32_t phase = 0, acc_phase = 0;
                 bool stop = false;
@@ -710,26 +773,33 @@ __global__ void __launch_bounds__(512, 1)
                                 break;
                             const uint32_t acc = (kt > 0 || j > 0) ? 1u : 0u;
                             if constexpr (BYTES8) {
-                                mma_mxf8_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_sf_ids(idesc, j, j), sfa, sfb,
-                                                    acc);
+                                const uint32_t id = idesc_sf_ids(idesc, j, j);
+                                if constexpr (SOLO)
+                                    mma_mxf8_elect(tmem, adesc + 2 * j, bdesc + 2 * j, id, sfa, sfb, acc);
+                                else
+                                    mma_mxf8_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, id, sfa, sfb, acc);
                             } else {
-                                const uint32_t id = (j & 1) * 2;
-                                mma_mxf4_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, idesc_sf_ids(idesc, id, id),
-                                                    sfa + (j >> 1) * 4, sfb + (j >> 1) * 8, acc);
+                                const uint32_t id = idesc_sf_ids(idesc, (j & 1) * 2, (j & 1) * 2);
+                                if constexpr (SOLO)
+                                    mma_mxf4_elect(tmem, adesc + 2 * j, bdesc + 2 * j, id, sfa + (j >> 1) * 4,
+                                                   sfb + (j >> 1) * 8, acc);
+                                else
+                                    mma_mxf4_pair_elect(tmem, adesc + 2 * j, bdesc + 2 * j, id, sfa + (j >> 1) * 4,
+                                                        sfb + (j >> 1) * 8, acc);
                             }
                         }
-                        mma_commit_pair_elect(&empty[stage], static_cast<uint16_t>(3u));
+                        commit_elect<SOLO>(&empty[stage], static_cast<uint16_t>(3u));
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
                     if (!stop)
-                        mma_commit_pair_elect(acc_full, static_cast<uint16_t>(3u));
+                        commit_elect<SOLO>(acc_full, static_cast<uint16_t>(3u));
                     acc_phase ^= 1u;
                 }
                 if (*abort_flag) {
-                    mma_commit_pair_elect(drain, static_cast<uint16_t>(1u));
+                    commit_elect<SOLO>(drain, static_cast<uint16_t>(1u));
                     mbar_wait_drain(drain, 0, a.wait_limit);
                 }
             }
@@ -738,18 +808,24 @@ __global__ void __launch_bounds__(512, 1)
 
     tc_fence_before();
     // No CTA leaves while its peer may still signal it.
-    cluster_leave(warp < 4 || (warp >= 8 && warp < 12));
+    if constexpr (SOLO)
+        __syncthreads();
+    else
+        cluster_leave(warp < 4 || (warp >= 8 && warp < 12));
     if (warp == 5) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, Cf::TMEM_COLS);
+        if constexpr (SOLO)
+            tmem_dealloc(tmem, Cf::TMEM_COLS);
+        else
+            tmem_dealloc_pair(tmem, Cf::TMEM_COLS);
     }
 }
 
-template <bool BYTES8, int OUT, bool WIDE>
+template <bool BYTES8, int OUT, bool WIDE, int SOLO>
 cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t stream)
 {
-    using Cf = GroupedCfg<BYTES8, (OUT >= 0), WIDE>;
-    auto kern = grouped_pair<BYTES8, OUT, WIDE>;
+    using Cf = GroupedCfg<BYTES8, (OUT >= 0), WIDE, SOLO>;
+    auto kern = grouped_product<BYTES8, OUT, WIDE, SOLO>;
     static std::atomic<int> max_clusters[64];   // per device; 0 = not yet queried
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -765,7 +841,7 @@ cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t 
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = SOLO ? 0 : 1;
     int limit = dev < 64 ? max_clusters[dev].load() : 0;
     if (limit == 0) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cf::SMEM_BYTES);
@@ -778,9 +854,17 @@ cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t 
             return e;
         if (attributes.numRegs <= 120)
             return cudaErrorInvalidConfiguration;
-        // Persistent: every cluster must be resident at once.
-        cfg.gridDim = dim3(2);
-        e = cudaOccupancyMaxActiveClusters(&limit, kern, &cfg);
+        // Persistent: a CTA, or a pair, for each slot.
+        if (SOLO) {
+            int per_sm = 0;
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, Cf::THREADS, Cf::SMEM_BYTES);
+            if (e == cudaSuccess)
+                e = cudaDeviceGetAttribute(&limit, cudaDevAttrMultiProcessorCount, dev);
+            limit *= per_sm;
+        } else {
+            cfg.gridDim = dim3(2);
+            e = cudaOccupancyMaxActiveClusters(&limit, kern, &cfg);
+        }
         if (e != cudaSuccess)
             return e;
         if (limit <= 0)
@@ -789,31 +873,46 @@ cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t 
             max_clusters[dev] = limit;
     }
     // The host does not know the offsets: at most this many tiles.
-    const int64_t row_tiles = static_cast<int64_t>(a.rows) / 256 + (a.groups < a.rows ? a.groups : a.rows);
+    const int64_t row_tiles = static_cast<int64_t>(a.rows) / Cf::ROWS + (a.groups < a.rows ? a.groups : a.rows);
     const int64_t most = row_tiles * a.nt;
     const int pairs = most < limit ? static_cast<int>(most) : limit;
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.numAttrs = 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(SOLO ? pairs : 2 * pairs));
+    cudaLaunchAttribute &dependent = attr[cfg.numAttrs++];
+    dependent.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    dependent.val.programmaticStreamSerializationAllowed = 1;
     return cudaLaunchKernelEx(&cfg, kern, a, m);
+}
+
+template <bool WIDE, int SOLO>
+cudaError_t launch_form(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, cudaStream_t stream)
+{
+    switch (out) {
+    case -1:
+        return bytes8 ? launch_one<true, -1, WIDE, SOLO>(a, m, stream) : launch_one<false, -1, WIDE, SOLO>(a, m, stream);
+    case 0: return launch_one<false, 0, true, SOLO>(a, m, stream);     // (the gated forms have room for any table)
+    case 1: return launch_one<true, 1, true, SOLO>(a, m, stream);
+    default: return launch_one<true, 2, true, SOLO>(a, m, stream);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool bytes8, int out, cudaStream_t stream)
 {
-    const bool wide = a.groups > GroupedCfg<false, false, false>::MAX_GROUPS;
-    switch (out) {
-    case -1:
-        if (wide)
-            return bytes8 ? launch_one<true, -1, true>(a, m, stream) : launch_one<false, -1, true>(a, m, stream);
-        return bytes8 ? launch_one<true, -1, false>(a, m, stream) : launch_one<false, -1, false>(a, m, stream);
-    case 0: return bytes8 ? cudaErrorInvalidValue : launch_one<false, 0, true>(a, m, stream);
-    case 1: return bytes8 ? launch_one<true, 1, true>(a, m, stream) : cudaErrorInvalidValue;
-    case 2: return bytes8 ? launch_one<true, 2, true>(a, m, stream) : cudaErrorInvalidValue;
-    default: return cudaErrorInvalidValue;
-    }
+    if (out >= 0 && (out == 0) == bytes8)
+        return cudaErrorInvalidValue;
+    // Single CTAs while the groups have 128 rows or fewer on average: twice as many
+    // tiles run together, and a group's last one wastes half as much.  4 tokens x 8
+    // of 64 experts, N = K = 4096: 36.5 us, with pairs 40.3; 256 tokens x 4 of 32,
+    // 2048 x 2048: 15.2 and 18.2; 1024 tokens: 17.6 and 19.1.  Beyond that a pair's
+    // smaller share of B's bytes counts more: 1536 tokens: 22.9 and 19.1.
+    if (a.rows <= 32)                            // (one token x 4 experts: 9.2 us, with 128 rows of A 9.9)
+        return launch_form<true, 32>(a, m, bytes8, out, stream);
+    if (a.rows <= 128 * static_cast<int64_t>(a.groups) &&
+        (out >= 0 || a.groups <= GroupedCfg<false, false, true, 128>::MAX_GROUPS))
+        return launch_form<true, 128>(a, m, bytes8, out, stream);
+    return a.groups > GroupedCfg<false, false, false, 0>::MAX_GROUPS ? launch_form<true, 0>(a, m, bytes8, out, stream)
+                                                                     : launch_form<false, 0>(a, m, bytes8, out, stream);
 }
 
 cudaError_t read_grouped_status(int *status, int reset)

@@ -422,6 +422,26 @@ def test_grouped_gemm_few_tiles_long_k(counts, N, K):
     check_gemm(Grouped(counts, N, K, seed=K, spread=1))
 
 
+# Rows per group on either side of the kernels' forms: at most 32 in all, 128 a
+# group on average (with groups of more among them), above; tables of every size.
+FORMS = {
+    "32 rows": [0, 31, 1], "33 rows": [0, 32, 1], "small groups": [1, 130, 60, 0, 300, 20, 7, 128], "128 a group": [256, 0, 129, 127],
+    "larger": [257, 0, 129, 127], "81 groups": [3] * 80 + [200], "861 groups": [1] * 860 + [300], "861 larger": [0] * 860 + [128 * 861 // 8, 5],
+}
+
+
+@pytest.mark.parametrize("name", sorted(FORMS))
+def test_grouped_products_of_every_form(name):
+    counts, few = FORMS[name], len(FORMS[name]) > 100
+    N, K = (24, 64) if few else (392, 672)
+    capacity = 128 * len(counts) if name == "861 larger" else 0
+    check_gemm(Grouped(counts, N, K, seed=1, capacity=capacity))
+    check_gemm(Grouped(counts, N + 1, K, "e4m3", "e5m2", seed=2, capacity=capacity))
+    for fmt, fmt_h in (("e2m1", "e2m1"), ("e4m3", "e4m3"), ("e5m2", "e5m2")):
+        p = Grouped(counts, 32 if few else 224, K, fmt, halves=2, seed=3, capacity=capacity)
+        check_swiglu(p, fmt_h, 0.01)
+
+
 def test_grouped_gemm_repeats_bit_for_bit_and_shares_a_workspace():
     a = Grouped([5, 0, 130], 520, 4096, seed=1)
     b = Grouped([2, 2], 300, 2048, seed=2)
