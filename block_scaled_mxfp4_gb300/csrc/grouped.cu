@@ -43,14 +43,13 @@
 // own are never used.
 //
 // What bounds it.  Decoding: the weights' bytes (64 groups, 26 of them with
-// rows, N = K = 4096 in FP4: 232 MB in 41 us, 5.6 TB/s, 84 % of a plain copy's
-// rate; the rest is the start and the last of six rounds of tiles).  Prefill: the tensor pipe and its
-// feed.  Groups of whole tiles in FP4: 7.2 PFLOP/s at K = 8192; at K = 2048 a
-// tile is 8 stages, and its hand-overs show (32768 rows in ragged groups,
-// N = 4000: 116 us, 4.6 PFLOP/s, the tensor pipe 61 % busy).  Bytes, gated
-// (16384 rows in ragged groups, F = 2048, K = 4096): 248 us, 2.2 PFLOP/s, the
-// pipe 77 % busy, of which 78 % of the tiles' rows exist; long runs are held at
-// 1.6 to 1.75 GHz by the board's power.
+// rows, N = K = 4096 in FP4: 232 MB in 37 us, 6.3 TB/s, 94 % of a plain copy's
+// rate).  Prefill: the tensor pipe and its feed.  Groups of whole tiles in FP4:
+// 7.2 PFLOP/s at K = 8192; at K = 2048 a tile is 8 stages, and its hand-overs
+// show (32768 rows in ragged groups, N = 4000: 118 us, 4.6 PFLOP/s, the tensor
+// pipe 61 % busy).  Bytes, gated (16384 rows in ragged groups, F = 2048,
+// K = 4096): 250 us, 2.2 PFLOP/s, the pipe 77 % busy, of which 78 % of the tiles'
+// rows exist; long runs are held at 1.6 to 1.75 GHz by the board's power.
 #include <atomic>
 #include <cuda_bf16.h>
 
@@ -901,14 +900,15 @@ cudaError_t launch_grouped(const GroupedArgs &a, const GroupedMaps &m, bool byte
 {
     if (out >= 0 && (out == 0) == bytes8)
         return cudaErrorInvalidValue;
-    // Single CTAs while the groups have 128 rows or fewer on average: twice as many
-    // tiles run together, and a group's last one wastes half as much.  4 tokens x 8
-    // of 64 experts, N = K = 4096: 36.5 us, with pairs 40.3; 256 tokens x 4 of 32,
-    // 2048 x 2048: 15.2 and 18.2; 1024 tokens: 17.6 and 19.1.  Beyond that a pair's
-    // smaller share of B's bytes counts more: 1536 tokens: 22.9 and 19.1.
+    // Single CTAs while nearly all groups have 128 rows or fewer (the host knows
+    // their average alone): twice as many tiles run together, and a group's last
+    // one wastes half as much; a group of more reads B again.  4 tokens x 8 of 64
+    // experts, N = K = 4096: 36.5 us, with pairs 41.3; 32 experts, 2048 x 2048, 64
+    // rows on average: 16.3 and 19.8, 96: 17.8 and 20.3, 128: 21.2 and 20.4; gated
+    // bytes, 16 experts, 96: 15.2 and 17.9, 128: 22.1 and 18.5.
     if (a.rows <= 32)                            // (one token x 4 experts: 9.2 us, with 128 rows of A 9.9)
         return launch_form<true, 32>(a, m, bytes8, out, stream);
-    if (a.rows <= 128 * static_cast<int64_t>(a.groups) &&
+    if (a.rows <= 112 * static_cast<int64_t>(a.groups) &&
         (out >= 0 || a.groups <= GroupedCfg<false, false, true, 128>::MAX_GROUPS))
         return launch_form<true, 128>(a, m, bytes8, out, stream);
     return a.groups > GroupedCfg<false, false, false, 0>::MAX_GROUPS ? launch_form<true, 0>(a, m, bytes8, out, stream)

@@ -422,10 +422,10 @@ def test_grouped_gemm_few_tiles_long_k(counts, N, K):
     check_gemm(Grouped(counts, N, K, seed=K, spread=1))
 
 
-# Rows per group on either side of the kernels' forms: at most 32 in all, 128 a
+# Rows per group on either side of the kernels' forms: at most 32 in all, 112 a
 # group on average (with groups of more among them), above; tables of every size.
 FORMS = {
-    "32 rows": [0, 31, 1], "33 rows": [0, 32, 1], "small groups": [1, 130, 60, 0, 300, 20, 7, 128], "128 a group": [256, 0, 129, 127],
+    "32 rows": [0, 31, 1], "33 rows": [0, 32, 1], "small groups": [1, 130, 60, 0, 300, 20, 7, 128], "112 a group": [256, 0, 65, 127],
     "larger": [257, 0, 129, 127], "81 groups": [3] * 80 + [200], "861 groups": [1] * 860 + [300], "861 larger": [0] * 860 + [128 * 861 // 8, 5],
 }
 
