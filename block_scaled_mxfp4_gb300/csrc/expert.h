@@ -108,7 +108,8 @@ struct GroupedArgs {
     uint8_t *H;                 // gated form: codes [rows, ldh bytes]
     int64_t ldh;
     uint8_t *SH;                // grouped scale layout over N
-    uint32_t idesc8, idesc8_solo;   // byte formats: instruction descriptors, M = 256 and 128
+    // Byte formats, instruction descriptors: M x N = 256 x 256, 128 x 256, 128 x 128.
+    uint32_t idesc8, idesc8_solo, idesc8_half;
     int early;                  // offsets, B and its scales may be read before the preceding
                                 // grid ends: it is a kernel of the same call, which waited
                                 // for the work before the call (one-token block of 3 x 544:

@@ -157,6 +157,7 @@ int run_product(const Product &p, cudaStream_t stream)
     if (p.bytes8) {
         a.idesc8 = idesc_mxf8(256, 256, static_cast<uint32_t>(p.fmt_a), static_cast<uint32_t>(p.fmt_b));
         a.idesc8_solo = idesc_mxf8(128, 256, static_cast<uint32_t>(p.fmt_a), static_cast<uint32_t>(p.fmt_b));
+        a.idesc8_half = idesc_mxf8(128, 128, static_cast<uint32_t>(p.fmt_a), static_cast<uint32_t>(p.fmt_b));
     }
     a.wait_limit = current_wait_limit();
     return status_of(launch_grouped(a, m, p.bytes8, p.out, stream));

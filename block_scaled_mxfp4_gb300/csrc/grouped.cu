@@ -43,7 +43,7 @@
 // own are never used.
 //
 // What bounds it.  Decoding: the weights' bytes (64 groups, 26 of them with
-// rows, N = K = 4096 in FP4: 232 MB in 37 us, 6.3 TB/s, 94 % of a plain copy's
+// rows, N = K = 4096 in FP4: 232 MB in 37 us, 6.2 TB/s, 93 % of a plain copy's
 // rate).  Prefill: the tensor pipe and its feed.  Groups of whole tiles in FP4:
 // 7.2 PFLOP/s at K = 8192; at K = 2048 a tile is 8 stages, and its hand-overs
 // show (32768 rows in ragged groups, N = 4000: 118 us, 4.6 PFLOP/s, the tensor
@@ -522,7 +522,15 @@ __global__ void __launch_bounds__(512, 1)
         pdl_wait_prerequisites();
     build_tables<Cf::ROWS>(offsets, groups, rows, tab_off, tab_base, warp_sum);
     const uint32_t tmem = *tmem_slot;
-    const TileTable table{tab_off, tab_base, groups, nt};
+    TileTable table{tab_off, tab_base, groups, nt};
+    // With single CTAs, tiles that would leave half of them idle are halved (128
+    // accumulator columns; tile_at then counts twice as many), which takes a
+    // stage's MMAs less time to issue: one-token block of 3 experts, 544 x 1504,
+    // 12.3 us, with whole tiles 13.7.  Halving the last of several rounds as well
+    // keeps SMs from the next launch: 32 rows in 25 groups 24.4 against 23.3.
+    const bool halves = SOLO && 2 * table.tiles() <= pairs;
+    if (halves)
+        table.nt *= 2;
     const int tiles = table.tiles();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
@@ -534,6 +542,7 @@ __global__ void __launch_bounds__(512, 1)
             pdl_wait_prerequisites();
         const int quarter = warp & 3;
         const int half = warp >> 3;
+        const bool idle = halves && half != 0;
         const int row = static_cast<int>(rank) * 128 + quarter * 32 + lane;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128;
         const uint32_t lead_empty = SOLO ? 0u : map_to_rank(smem_addr(acc_empty), 0);
@@ -546,7 +555,7 @@ __global__ void __launch_bounds__(512, 1)
             acc_phase ^= 1u;
             tc_fence_after();
             const int r = tl.row0 + row;
-            const bool mine = r < tl.end;
+            const bool mine = r < tl.end && !idle;
             // All 128 columns of the lane to registers, then the accumulator is
             // released: the next tile's MMAs wait for the reads alone.
             uint32_t acc[4][32];
@@ -568,9 +577,9 @@ __global__ void __launch_bounds__(512, 1)
                     mbar_arrive_cluster_relaxed(lead_empty);
             }
             if constexpr (!GATED) {
-                const int n0 = tl.q * 256 + half * 128;
+                const int n0 = tl.q * (halves ? 128 : 256) + half * 128;
                 const int first = r - lane;
-                const int rows_here = min(32, tl.end - first);
+                const int rows_here = idle ? 0 : min(32, tl.end - first);
                 if (rows_here > 0 && (!a.vec_ok || rows_here == 32)) {
                     // Four boxes of 32 rows x 32 columns through shared memory.
                     // Whole ones leave by TMA: a thread's own 32-byte stores
@@ -605,8 +614,9 @@ __global__ void __launch_bounds__(512, 1)
                 }
             } else if (mine) {
                 const int64_t block = static_cast<int64_t>(tl.sfa + row / 128) * (sf_groups(a.N) * kSfAtomBytes);
-                store_gated<static_cast<QuantFmt>(OUT)>(a, r, row & 127, block, tl.q * 128 + half * 64, acc[0], acc[1],
-                                                        acc[2], acc[3]);
+                store_gated<static_cast<QuantFmt>(OUT)>(a, r, row & 127, block,
+                                                        tl.q * (halves ? 64 : 128) + half * 64, acc[0], acc[1], acc[2],
+                                                        acc[3]);
             }
         }
         if (!GATED && lane == 0)
@@ -635,7 +645,7 @@ __global__ void __launch_bounds__(512, 1)
                     // decoding step 41.3 against 40.4).
                     const uint64_t pol_b = tl.single ? once : keep;
                     const uint32_t unit = role == 0   ? (!rows_here ? 0 : (few ? 32 * 128 : Cf::A_BYTES) + Cf::SFA_BYTES)
-                                          : role == 1 ? Cf::B_BYTES
+                                          : role == 1 ? (halves ? Cf::B_BYTES / 2 : Cf::B_BYTES)
                                                       : Cf::SFB_BYTES;
                     for (int kt = 0; kt < a.kt; ++kt) {
                         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_limit, &g_status)) {
@@ -653,17 +663,18 @@ __global__ void __launch_bounds__(512, 1)
                         } else if (role == 1) {
                             // Plain: 128 rows of B.  Gated: 64 gate rows and the
                             // same 64 up rows (the map's third dimension).
-                            const int n = GATED ? tl.q * 128 + static_cast<int>(rank) * 64
-                                                : tl.q * 256 + static_cast<int>(rank) * 128;
+                            const int unit_n = GATED ? 64 : 128;
+                            const int n = (halves ? tl.q : 2 * tl.q + static_cast<int>(rank)) * unit_n;
                             tma_load_4d(st + Cf::A_BYTES, &maps.B, &full[stage], kt * 128, n, 0, tl.e, pol_b);
-                            if (SOLO)            // what the peer of a pair would load
+                            if (SOLO && !halves) // what the peer of a pair would load
                                 tma_load_4d(st + Cf::A_BYTES + 128 * 128, &maps.B, &full[stage], kt * 128,
-                                            n + (GATED ? 64 : 128), 0, tl.e, pol_b);
+                                            n + unit_n, 0, tl.e, pol_b);
                         } else {
                             // Plain: two 128-row blocks of the expert.  Gated: the
                             // block of the gate rows and the block of the up rows.
                             tma_load_4d(sf + Cf::SFA_BYTES, &maps.SB, &full[stage], 0, G * kt,
-                                        GATED ? tl.q : 2 * tl.q, GATED ? 2 * tl.e : tl.e, pol_b);
+                                        GATED == halves ? (GATED ? tl.q / 2 : 2 * tl.q) : tl.q,
+                                        GATED ? 2 * tl.e : tl.e, pol_b);
                         }
                         ++issued;
                         if (++stage == STAGES) {
@@ -688,6 +699,8 @@ __global__ void __launch_bounds__(512, 1)
             const uint32_t lead_ready = SOLO ? 0u : map_to_rank(smem_addr(&sf_ready[0]), 0);
             const int my_tiles = pair < tiles ? (tiles - 1 - pair) / pairs + 1 : 0;
             const int total = my_tiles * a.kt;
+            // The second half of a gated tile has the second half of either block.
+            const bool upper = GATED && halves && total > 0 && (tile_at<Cf::ROWS>(table, pair).q & 1);
             int stage = 0;
             uint32_t phase = 0;
             for (int i = 0; i < total; ++i) {
@@ -718,6 +731,12 @@ __global__ void __launch_bounds__(512, 1)
                     w[5] = GATED ? x.w : y.y;
                     w[6] = y.z;
                     w[7] = y.w;
+                    if (SOLO && GATED && upper) {
+                        w[0] = x.z;
+                        w[1] = x.w;
+                        w[2] = y.z;
+                        w[3] = y.w;
+                    }
                 }
                 const uint32_t slot = t_q + stage * Cf::SF_COLS;
                 if constexpr (G == 2) {
@@ -744,7 +763,8 @@ __global__ void __launch_bounds__(512, 1)
         } else if (warp == 5) {
             // ------------------------------------------------ MMA (leader) --
             if (leader) {
-                const uint32_t idesc = BYTES8 ? (SOLO ? a.idesc8_solo : a.idesc8) : idesc_mxf4(SOLO ? 128 : 256, 256);
+                const uint32_t idesc = BYTES8 ? (!SOLO ? a.idesc8 : halves ? a.idesc8_half : a.idesc8_solo)
+                                              : idesc_mxf4(SOLO ? 128 : 256, halves ? 128 : 256);
                 int stage = 0;
                 uint32_t phase = 0, acc_phase = 0;
                 bool stop = false;
@@ -871,9 +891,12 @@ cudaError_t launch_one(const GroupedArgs &a, const GroupedMaps &m, cudaStream_t 
         if (dev < 64)
             max_clusters[dev] = limit;
     }
-    // The host does not know the offsets: at most this many tiles.
+    // The host does not know the offsets: at most this many tiles.  (SMs beyond
+    // them are left to the next launch, which may start early.)
     const int64_t row_tiles = static_cast<int64_t>(a.rows) / Cf::ROWS + (a.groups < a.rows ? a.groups : a.rows);
-    const int64_t most = row_tiles * a.nt;
+    int64_t most = row_tiles * a.nt;
+    if (SOLO && 2 * most <= limit)
+        most *= 2;                               // as halves
     const int pairs = most < limit ? static_cast<int>(most) : limit;
     cfg.gridDim = dim3(static_cast<unsigned>(SOLO ? pairs : 2 * pairs));
     cudaLaunchAttribute &dependent = attr[cfg.numAttrs++];
