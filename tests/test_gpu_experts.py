@@ -442,6 +442,16 @@ def test_grouped_products_of_every_form(name):
         check_swiglu(p, fmt_h, 0.01)
 
 
+@pytest.mark.parametrize("counts,N", [([40, 130, 7, 0, 64, 1], 3600), ([3, 1, 2, 4, 1, 5], 3601), ([40, 9, 0, 130] * 4, 3400),
+                                      ([2, 0, 3, 1] * 5, 2700)])
+def test_grouped_products_in_rounds_of_small_groups(counts, N):
+    """More tiles than half of the SMs, or than all of them: nothing is halved."""
+    check_gemm(Grouped(counts, N, 416, seed=N))
+    for fmt, fmt_h in (("e2m1", "e2m1"), ("e4m3", "e5m2")):
+        p = Grouped(counts, N // 64 * 32, 416, fmt, halves=2, seed=N)
+        check_swiglu(p, fmt_h, 0.01)
+
+
 def test_grouped_gemm_repeats_bit_for_bit_and_shares_a_workspace():
     a = Grouped([5, 0, 130], 520, 4096, seed=1)
     b = Grouped([2, 2], 300, 2048, seed=2)
