@@ -11,6 +11,7 @@ torch and calls ``mxfp4_gemm``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -496,17 +497,45 @@ def mxfp4_moe_ffn(H, ldh, Nrm, ldn, X, ldx, ids, gates, offsets, slot_row, T, E,
                                       workspace_bytes, _stream(stream)), "mxfp4_moe_ffn")
 
 
+@contextlib.contextmanager
+def _on_stream(stream, inputs, outputs):
+    """Make `stream` (an object, a handle, or None for the current one) torch's
+    current stream, so that what the body allocates, copies and drops belongs to
+    it.  `inputs` are marked as used on it, and what the body puts into the list
+    `outputs` as used on the caller's stream too.  Order between the two streams
+    is the caller's, as for every entry point."""
+    import torch
+    caller = torch.cuda.current_stream() if stream is not None else None
+    if caller is None or _stream(stream) == caller.cuda_stream:
+        yield
+        return
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    try:
+        with torch.cuda.stream(stream):
+            yield
+    finally:
+        for t in inputs:
+            if t is not None:
+                t.record_stream(stream)
+        for t in outputs:
+            t.record_stream(caller)
+
+
 def relaid_expert_scales(S, K, stream=None):
     """Row-major weight scales [..., rows, K / 32] -> one relaid buffer per
     matrix [..., mxfp4_scale_relayout_size(rows, K)], laid out once for the
     grouped products."""
     import torch
     rows = S.shape[-2]
-    flat = S.reshape(-1, rows, K // 32).contiguous()
     size = mxfp4_scale_relayout_size(rows, K)
-    out = torch.empty((flat.shape[0], size), dtype=torch.uint8, device=S.device)
-    for i in range(flat.shape[0]):
-        mxfp4_scale_relayout(out[i], flat[i], rows, K, K // 32, stream)
+    made = []
+    with _on_stream(stream, [S], made):
+        flat = S.reshape(-1, rows, K // 32).contiguous()
+        out = torch.empty((flat.shape[0], size), dtype=torch.uint8, device=S.device)
+        made.append(out)
+        for i in range(flat.shape[0]):
+            mxfp4_scale_relayout(out[i], flat[i], rows, K, K // 32)
     return out.reshape(*S.shape[:-2], size)
 
 
@@ -517,25 +546,29 @@ def moe_block(x, logits, resid, w1, s1, w2, s2, k, w_pre=None, w_post=None, toke
     x bf16 [T, K] (the block's normed input), logits bf16 / fp32 [T, E], resid
     bf16 [T, K], w1 uint8 [E, 2, F, K / 2], w2 uint8 [E, K, F / 2], s1 and s2
     from relaid_expert_scales.  Returns (h, n): the residual stream after the
-    block and its norm, bf16 [T, K].
+    block and its norm, bf16 [T, K].  On another `stream` than the current one
+    the block's own memory belongs to that stream; the caller orders the two.
     """
     import torch
     T, K = x.shape
     E, F = w1.shape[0], w1.shape[2]
-    i32 = dict(dtype=torch.int32, device=x.device)
-    ids, slot_row = torch.empty((T, k), **i32), torch.empty((T, k), **i32)
-    offsets, row_token = torch.empty(E + 1, **i32), torch.empty(T * k, **i32)
-    gates = torch.empty((T, k), dtype=torch.float32, device=x.device)
-    h = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
-    n = torch.empty_like(h)
     need = max(mxfp4_moe_route_workspace_size(T, E), mxfp4_moe_ffn_workspace_size(T, E, k, K, F))
-    ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
     kind = MXFP4_LOGITS_FP32 if logits.dtype == torch.float32 else MXFP4_LOGITS_BF16
-    mxfp4_moe_route(ids, gates, offsets, row_token, slot_row, logits, logits.stride(0), kind,
-                    token_mask, T, E, k, gate_mode, 1.0, ws, ws.numel(), stream)
-    mxfp4_moe_ffn(h, K, n, K, x, x.stride(0), ids, gates, offsets, slot_row, T, E, k, K, F, w1, K,
-                  s1, w2, F, s2, resid, resid.stride(0), w_post, w_pre, float(res_scale),
-                  float(out_scale), float(eps), ws, ws.numel(), stream)
+    made = []
+    with _on_stream(stream, [x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask], made):
+        i32 = dict(dtype=torch.int32, device=x.device)
+        ids, slot_row = torch.empty((T, k), **i32), torch.empty((T, k), **i32)
+        offsets, row_token = torch.empty(E + 1, **i32), torch.empty(T * k, **i32)
+        gates = torch.empty((T, k), dtype=torch.float32, device=x.device)
+        h = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
+        n = torch.empty_like(h)
+        made += [h, n]
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
+        mxfp4_moe_route(ids, gates, offsets, row_token, slot_row, logits, logits.stride(0), kind,
+                        token_mask, T, E, k, gate_mode, 1.0, ws, ws.numel())
+        mxfp4_moe_ffn(h, K, n, K, x, x.stride(0), ids, gates, offsets, slot_row, T, E, k, K, F, w1, K,
+                      s1, w2, F, s2, resid, resid.stride(0), w_post, w_pre, float(res_scale),
+                      float(out_scale), float(eps), ws, ws.numel())
     return h, n
 
 
