@@ -497,20 +497,24 @@ def mxfp4_moe_ffn(H, ldh, Nrm, ldn, X, ldx, ids, gates, offsets, slot_row, T, E,
                                       workspace_bytes, _stream(stream)), "mxfp4_moe_ffn")
 
 
-@contextlib.contextmanager
 def _on_stream(stream, inputs, outputs):
-    """Make `stream` (an object, a handle, or None for the current one) torch's
-    current stream, so that what the body allocates, copies and drops belongs to
-    it.  `inputs` are marked as used on it, and what the body puts into the list
-    `outputs` as used on the caller's stream too.  Order between the two streams
-    is the caller's, as for every entry point."""
+    """A context with `stream` (an object, a handle, or None for the current one)
+    as torch's current stream, so that what the body allocates, copies and drops
+    belongs to it.  `inputs` are marked as used on it, and what the body puts
+    into the list `outputs` as used on the caller's stream too.  Order between
+    the two streams is the caller's, as for every entry point."""
     import torch
-    caller = torch.cuda.current_stream() if stream is not None else None
-    if caller is None or _stream(stream) == caller.cuda_stream:
-        yield
-        return
+    if stream is None or _stream(stream) == torch.cuda.current_stream().cuda_stream:
+        return contextlib.nullcontext()
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return _other_stream(stream, inputs, outputs)
+
+
+@contextlib.contextmanager
+def _other_stream(stream, inputs, outputs):
+    import torch
+    caller = torch.cuda.current_stream()
     try:
         with torch.cuda.stream(stream):
             yield
@@ -581,12 +585,15 @@ def gemm(A, B, SA, SB, alpha=1.0, beta=0.0, C=None, split_k=0, out=None, workspa
     """
     import torch
     M, N, K = A.shape[0], B.shape[0], A.shape[1] * 2
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
     need = mxfp4_gemm_workspace_size(M, N, K, split_k)
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=A.device)
-    mxfp4_gemm(out, out.stride(0), C, 0 if C is None else C.stride(0), A, A.stride(0) * 2,
-               B, B.stride(0) * 2, SA, SA.stride(0), SB, SB.stride(0), float(alpha),
-               float(beta), M, N, K, split_k, workspace, workspace.numel(), stream)
+    made = []
+    with _on_stream(stream, [A, B, SA, SB, C, out, workspace], made):
+        if out is None:
+            out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
+            made.append(out)
+        if workspace is None or workspace.numel() < need:
+            workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=A.device)
+        mxfp4_gemm(out, out.stride(0), C, 0 if C is None else C.stride(0), A, A.stride(0) * 2,
+                   B, B.stride(0) * 2, SA, SA.stride(0), SB, SB.stride(0), float(alpha),
+                   float(beta), M, N, K, split_k, workspace, workspace.numel())
     return out

@@ -72,3 +72,21 @@ def test_relaid_expert_scales_on_another_stream():
     for e in range(E):
         np.testing.assert_array_equal(out[e].cpu().numpy(), ref.relaid(S[e].cpu().numpy(), K))
     del held
+
+
+@pytest.mark.parametrize("M,N,K,split", [(8, 512, 4096, 4), (300, 512, 1024, 0)])
+def test_gemm_on_another_stream(M, N, K, split):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    byte = lambda lo, hi, *shape: torch.randint(lo, hi, shape, dtype=torch.uint8, device="cuda", generator=g)
+    A, B = byte(0, 256, M, K // 2), byte(0, 256, N, K // 2)
+    SA, SB = byte(118, 122, M, K // 32), byte(118, 122, N, K // 32)
+    need = mx.mxfp4_gemm_workspace_size(M, N, K, split)
+    want = mx.gemm(A, B, SA, SB, split_k=split)
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        busy(side)
+        got = mx.gemm(A, B, SA, SB, split_k=split, stream=side)
+        held = churn([M * N * 2, max(need, 256)])
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del held
