@@ -526,11 +526,19 @@ def _other_stream(stream, inputs, outputs):
             t.record_stream(caller)
 
 
+def _require(ok, what, error=ValueError):
+    if not ok:
+        raise error(f"{what} expected")
+
+
 def relaid_expert_scales(S, K, stream=None):
     """Row-major weight scales [..., rows, K / 32] -> one relaid buffer per
     matrix [..., mxfp4_scale_relayout_size(rows, K)], laid out once for the
     grouped products."""
     import torch
+    _require(S.dim() >= 2 and S.shape[-1] * 32 == K, f"relaid_expert_scales: S [..., rows, {K} / 32]")
+    _require(S.element_size() == 1, "relaid_expert_scales: S one byte per scale", TypeError)
+    _require(S.is_cuda, "relaid_expert_scales: S on the GPU")
     rows = S.shape[-2]
     size = mxfp4_scale_relayout_size(rows, K)
     made = []
@@ -543,6 +551,38 @@ def relaid_expert_scales(S, K, stream=None):
     return out.reshape(*S.shape[:-2], size)
 
 
+def _check_block(x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask):
+    """The entries below take pointers; this is where types and layouts are seen."""
+    import torch
+    _require(x.dim() == 2 and w1.dim() == 4 and w1.shape[1] == 2,
+             "moe_block: x [T, K], w1 [E, 2, F, K / 2]")
+    (T, K), E, F = x.shape, w1.shape[0], w1.shape[2]
+    bf16 = (torch.bfloat16,)
+    for name, t, shape, types in (
+            ("x", x, (T, K), bf16), ("resid", resid, (T, K), bf16),
+            ("logits", logits, (T, E), (torch.bfloat16, torch.float32)),
+            ("w_pre", w_pre, (K,), bf16), ("w_post", w_post, (K,), bf16),
+            ("token_mask", token_mask, (T,), (torch.uint8, torch.bool, torch.int8))):
+        if t is None and name in ("w_pre", "w_post", "token_mask"):
+            continue
+        _require(t.dtype in types, f"moe_block: {name} of type {' or '.join(map(str, types))}",
+                 TypeError)
+        _require(tuple(t.shape) == shape, f"moe_block: {name} of shape {shape}")
+        _require(t.numel() == 0 or shape[-1] == 1 or t.stride(-1) == 1,
+                 f"moe_block: {name} with neighbouring elements side by side")
+    size1, size2 = mxfp4_scale_relayout_size(F, K), mxfp4_scale_relayout_size(K, F)
+    for name, t, size, shape in (("w1", w1, E * F * K, (E, 2, F, K // 2)),
+                                 ("w2", w2, E * K * F // 2, (E, K, F // 2)),
+                                 ("s1", s1, 2 * E * size1, None), ("s2", s2, E * size2, None)):
+        _require(t.element_size() == 1, f"moe_block: {name} of bytes", TypeError)
+        _require(t.numel() == size and t.is_contiguous() and (not shape or tuple(t.shape) == shape),
+                 f"moe_block: {name} contiguous, " +
+                 (f"of shape {shape}" if shape else f"from relaid_expert_scales, {size} bytes"))
+    for t in (x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask):
+        _require(t is None or (t.is_cuda and t.device == x.device),
+                 "moe_block: everything on one GPU")
+
+
 def moe_block(x, logits, resid, w1, s1, w2, s2, k, w_pre=None, w_post=None, token_mask=None,
               gate_mode=MXFP4_GATE_TOPK, res_scale=1.0, out_scale=1.0, eps=1e-6, stream=None):
     """A mixture-of-experts block on MXFP4 weights, from the router's logits on.
@@ -552,12 +592,16 @@ def moe_block(x, logits, resid, w1, s1, w2, s2, k, w_pre=None, w_post=None, toke
     from relaid_expert_scales.  Returns (h, n): the residual stream after the
     block and its norm, bf16 [T, K].  On another `stream` than the current one
     the block's own memory belongs to that stream; the caller orders the two.
+    Rows of x, logits and resid may be apart; other types or layouts raise
+    TypeError or ValueError.
     """
     import torch
+    _check_block(x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask)
     T, K = x.shape
     E, F = w1.shape[0], w1.shape[2]
     need = max(mxfp4_moe_route_workspace_size(T, E), mxfp4_moe_ffn_workspace_size(T, E, k, K, F))
     kind = MXFP4_LOGITS_FP32 if logits.dtype == torch.float32 else MXFP4_LOGITS_BF16
+    ld = lambda t: t.stride(0) if T > 1 else t.shape[1]    # (a lone row's stride can be anything)
     made = []
     with _on_stream(stream, [x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask], made):
         i32 = dict(dtype=torch.int32, device=x.device)
@@ -568,10 +612,10 @@ def moe_block(x, logits, resid, w1, s1, w2, s2, k, w_pre=None, w_post=None, toke
         n = torch.empty_like(h)
         made += [h, n]
         ws = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-        mxfp4_moe_route(ids, gates, offsets, row_token, slot_row, logits, logits.stride(0), kind,
+        mxfp4_moe_route(ids, gates, offsets, row_token, slot_row, logits, ld(logits), kind,
                         token_mask, T, E, k, gate_mode, 1.0, ws, ws.numel())
-        mxfp4_moe_ffn(h, K, n, K, x, x.stride(0), ids, gates, offsets, slot_row, T, E, k, K, F, w1, K,
-                      s1, w2, F, s2, resid, resid.stride(0), w_post, w_pre, float(res_scale),
+        mxfp4_moe_ffn(h, K, n, K, x, ld(x), ids, gates, offsets, slot_row, T, E, k, K, F, w1, K,
+                      s1, w2, F, s2, resid, ld(resid), w_post, w_pre, float(res_scale),
                       float(out_scale), float(eps), ws, ws.numel())
     return h, n
 

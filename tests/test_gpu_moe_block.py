@@ -1,0 +1,86 @@
+"""The routed block as a whole: its arguments' layouts, its overlapped steps at
+prefill sizes against a plain 64-bit form, calls back to back.
+
+Bound of the plain form, from the arithmetic: with d the gated product's error
+(as for mxfp4_grouped_swiglu), H's dequantised values lie between the roundings
+of h - d and h + d, under any scale that an amax of that block within d allows;
+that spread, through |B2|, the down product's accumulation (2^-20 sum |a b|) and
+its bf16 rounding bound the rows of Y; the gates (a relative
+(E / 32 + 16) 2^-23) and the join (2^-18 of its terms, one rounding) follow, and
+a change e of the residual row moves its root mean square by rms(e) at most.
+"""
+import numpy as np
+import pytest
+
+import block_scaled_mxfp4_gb300 as mx
+import expert_ref as ref
+from parity_util import bf16_bits_to_f64, d_to_bits, ulp_bf16
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from block_scaled_mxfp4_gb300 import build
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    mx.mxfp4_device_status(reset=True)
+    yield
+    assert mx.mxfp4_device_status() == 0, "a bounded wait timed out during the tests"
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Weights:
+    def __init__(self, E, K, F, seed=0):
+        rng = np.random.default_rng(seed)
+        self.E, self.K, self.F = E, K, F
+        self.q1 = rng.integers(0, 256, size=(E, 2 * F, K // 2), dtype=np.uint8)
+        self.q2 = rng.integers(0, 256, size=(E, K, F // 2), dtype=np.uint8)
+        # Products of a few units, so that the activation sees all of its range.
+        at = 127 - int(round(np.log2(2.9 * np.sqrt(K))))
+        self.c1 = rng.integers(at, at + 2, size=(E, 2 * F, K // 32)).astype(np.uint8)
+        self.c2 = rng.integers(at, at + 2, size=(E, K, F // 32)).astype(np.uint8)
+        self.w1, self.w2 = dev(self.q1.reshape(E, 2, F, K // 2)), dev(self.q2)
+        self.s1 = mx.relaid_expert_scales(dev(self.c1.reshape(E, 2, F, K // 32)), K)
+        self.s2 = mx.relaid_expert_scales(dev(self.c2), F)
+
+    def __call__(self, x, logits, resid, k, **kw):
+        return mx.moe_block(x, logits, resid, self.w1, self.s1, self.w2, self.s2, k, **kw)
+
+
+def inputs(T, E, K, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *shape: torch.randn(shape, device="cuda", generator=g)
+    return rand(T, K).bfloat16(), rand(T, E), rand(T, K).bfloat16()
+
+
+def same(got, want):
+    torch.cuda.synchronize()
+    return all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [1, 37])
+def test_rows_apart_and_masks_of_truth_values(T):
+    w = Weights(4, 256, 96)
+    x, logits, resid = inputs(T, 4, 256, T)
+    mask = torch.arange(T, device="cuda") % 5 != 3
+    want = w(x, logits, resid, 2, token_mask=mask.to(torch.uint8))
+    wide = lambda t, n: torch.cat((t, torch.full((T, n), float("nan"), dtype=t.dtype, device="cuda")), 1)[:, :t.shape[1]]
+    assert same(w(wide(x, 24), wide(logits, 3), wide(resid, 5), 2, token_mask=mask), want)
+    if T == 1:                                             # a lone row's stride says nothing
+        lone = lambda t: t.reshape(-1)[:, None].t()
+        assert lone(x).stride(0) == 1
+        assert same(w(lone(x), lone(logits), lone(resid), 2, token_mask=mask), want)
+
+
+def test_logits_of_other_types_are_refused():
+    w = Weights(4, 256, 96)
+    x, logits, resid = inputs(9, 4, 256, 9)
+    for bad in (logits.half(), logits.double()):
+        with pytest.raises(TypeError):
+            w(x, bad, resid, 2)
