@@ -526,9 +526,8 @@ def _other_stream(stream, inputs, outputs):
             t.record_stream(caller)
 
 
-def _require(ok, what, error=ValueError):
-    if not ok:
-        raise error(f"{what} expected")
+def _refuse(what, error=ValueError):
+    raise error(f"{what} expected")
 
 
 def relaid_expert_scales(S, K, stream=None):
@@ -536,9 +535,12 @@ def relaid_expert_scales(S, K, stream=None):
     matrix [..., mxfp4_scale_relayout_size(rows, K)], laid out once for the
     grouped products."""
     import torch
-    _require(S.dim() >= 2 and S.shape[-1] * 32 == K, f"relaid_expert_scales: S [..., rows, {K} / 32]")
-    _require(S.element_size() == 1, "relaid_expert_scales: S one byte per scale", TypeError)
-    _require(S.is_cuda, "relaid_expert_scales: S on the GPU")
+    if S.dim() < 2 or S.shape[-1] * 32 != K:
+        _refuse(f"relaid_expert_scales: S [..., rows, {K} / 32]")
+    if S.element_size() != 1:
+        _refuse("relaid_expert_scales: S one byte per scale", TypeError)
+    if not S.is_cuda:
+        _refuse("relaid_expert_scales: S on the GPU")
     rows = S.shape[-2]
     size = mxfp4_scale_relayout_size(rows, K)
     made = []
@@ -554,10 +556,10 @@ def relaid_expert_scales(S, K, stream=None):
 def _check_block(x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask):
     """The entries below take pointers; this is where types and layouts are seen."""
     import torch
-    _require(x.dim() == 2 and w1.dim() == 4 and w1.shape[1] == 2,
-             "moe_block: x [T, K], w1 [E, 2, F, K / 2]")
-    (T, K), E, F = x.shape, w1.shape[0], w1.shape[2]
-    bf16 = (torch.bfloat16,)
+    if x.dim() != 2 or w1.dim() != 4 or w1.shape[1] != 2:
+        _refuse("moe_block: x [T, K], w1 [E, 2, F, K / 2]")
+    (T, K), (E, _, F, _) = x.shape, w1.shape
+    bf16, one_gpu = (torch.bfloat16,), x.is_cuda
     for name, t, shape, types in (
             ("x", x, (T, K), bf16), ("resid", resid, (T, K), bf16),
             ("logits", logits, (T, E), (torch.bfloat16, torch.float32)),
@@ -565,22 +567,25 @@ def _check_block(x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask):
             ("token_mask", token_mask, (T,), (torch.uint8, torch.bool, torch.int8))):
         if t is None and name in ("w_pre", "w_post", "token_mask"):
             continue
-        _require(t.dtype in types, f"moe_block: {name} of type {' or '.join(map(str, types))}",
-                 TypeError)
-        _require(tuple(t.shape) == shape, f"moe_block: {name} of shape {shape}")
-        _require(t.numel() == 0 or shape[-1] == 1 or t.stride(-1) == 1,
-                 f"moe_block: {name} with neighbouring elements side by side")
+        if t.dtype not in types:
+            _refuse(f"moe_block: {name} of type {' or '.join(map(str, types))}", TypeError)
+        if t.shape != shape:
+            _refuse(f"moe_block: {name} of shape {shape}")
+        if t.stride(-1) != 1 and shape[-1] != 1 and t.numel():
+            _refuse(f"moe_block: {name} with neighbouring elements side by side")
+        one_gpu = one_gpu and t.device == x.device
     size1, size2 = mxfp4_scale_relayout_size(F, K), mxfp4_scale_relayout_size(K, F)
     for name, t, size, shape in (("w1", w1, E * F * K, (E, 2, F, K // 2)),
                                  ("w2", w2, E * K * F // 2, (E, K, F // 2)),
                                  ("s1", s1, 2 * E * size1, None), ("s2", s2, E * size2, None)):
-        _require(t.element_size() == 1, f"moe_block: {name} of bytes", TypeError)
-        _require(t.numel() == size and t.is_contiguous() and (not shape or tuple(t.shape) == shape),
-                 f"moe_block: {name} contiguous, " +
-                 (f"of shape {shape}" if shape else f"from relaid_expert_scales, {size} bytes"))
-    for t in (x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask):
-        _require(t is None or (t.is_cuda and t.device == x.device),
-                 "moe_block: everything on one GPU")
+        if t.element_size() != 1:
+            _refuse(f"moe_block: {name} of bytes", TypeError)
+        if t.numel() != size or (shape and t.shape != shape) or not t.is_contiguous():
+            _refuse(f"moe_block: {name} contiguous, " +
+                    (f"of shape {shape}" if shape else f"{size} bytes from relaid_expert_scales"))
+        one_gpu = one_gpu and t.device == x.device
+    if not one_gpu:
+        _refuse("moe_block: everything on one GPU")
 
 
 def moe_block(x, logits, resid, w1, s1, w2, s2, k, w_pre=None, w_post=None, token_mask=None,
