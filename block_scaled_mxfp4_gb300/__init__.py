@@ -165,14 +165,18 @@ def _raise(status, where):
     raise Mxfp4Error(status, where)
 
 
+_python_entries = {}        # what _bind_entries replaced
+
+
 def _bind_entries(L):
     """Replace the calls of a decoding step by the extension module's, which
-    take the same arguments and marshal them in C."""
+    take the same arguments, by place or by name, and marshal them in C."""
     from . import _entry
     names = [n for n in dir(_entry) if n.startswith("mxfp")]
     _entry.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _p,
                 _current_stream, _raise)
     for n in names:
+        _python_entries[n] = globals()[n]
         globals()[n] = getattr(_entry, n)
 
 

@@ -2,8 +2,10 @@
 // time to marshal a call's arguments in Python (3 us on the host of a GB300)
 // is a good part of the call.  The module holds no arithmetic and links
 // nothing: each function takes the arguments of the C entry of its name (device
-// pointers as tensors, integers or None; an optional stream), calls it at the
-// address that bind() was given, and raises through the package's own error.
+// pointers as tensors, integers or None; an optional stream), by place or by
+// name like the package's Python function that it stands in for, calls the entry
+// at the address that bind() was given, and raises through the package's own
+// error.  An entry is one list of its arguments' kinds and names.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
@@ -14,7 +16,13 @@ static PyObject *g_pointer;         // the package's pointer conversion, for oth
 static PyObject *g_current_stream;  // -> the current stream's handle
 static PyObject *g_raise;           // (status, name): raises
 
-static void *as_pointer(PyObject *o, int *bad)
+typedef void *ptr;
+typedef int64_t i64;
+typedef int i32;
+typedef float f32;
+typedef size_t size;
+
+static ptr as_ptr(PyObject *o, int *bad)
 {
     if (o == Py_None || *bad)
         return NULL;
@@ -39,7 +47,7 @@ static void *as_pointer(PyObject *o, int *bad)
     return p;
 }
 
-static int64_t as_int64(PyObject *o, int *bad)
+static i64 as_i64(PyObject *o, int *bad)
 {
     if (*bad)
         return 0;
@@ -49,9 +57,9 @@ static int64_t as_int64(PyObject *o, int *bad)
     return v;
 }
 
-static int as_int(PyObject *o, int *bad)
+static i32 as_i32(PyObject *o, int *bad)
 {
-    const int64_t v = as_int64(o, bad);
+    const i64 v = as_i64(o, bad);
     if (!*bad && (v < INT32_MIN || v > INT32_MAX)) {
         PyErr_SetString(PyExc_OverflowError, "argument does not fit a C int");
         *bad = 1;
@@ -59,17 +67,17 @@ static int as_int(PyObject *o, int *bad)
     return (int)v;
 }
 
-static size_t as_size(PyObject *o, int *bad)
+static size as_size(PyObject *o, int *bad)
 {
-    const int64_t v = as_int64(o, bad);
+    const i64 v = as_i64(o, bad);
     if (!*bad && v < 0) {
         PyErr_SetString(PyExc_OverflowError, "a size is negative");
         *bad = 1;
     }
-    return (size_t)v;
+    return (size)v;
 }
 
-static float as_float(PyObject *o, int *bad)
+static f32 as_f32(PyObject *o, int *bad)
 {
     if (*bad)
         return 0.0f;
@@ -97,21 +105,36 @@ static void *as_stream(PyObject *o, int *bad)
     return p;
 }
 
-// The stream is the argument after the entry's own, by place or by name.
-static int stream_argument(const char *name, Py_ssize_t want, PyObject *const *a, Py_ssize_t n, PyObject *kw,
-                           PyObject **stream)
+// The arguments in the order of `names`, whose last is the optional stream (NULL
+// where it is not given).
+static int arrange(const char *entry, const char *const *names, Py_ssize_t count, PyObject *const *a, Py_ssize_t n,
+                   PyObject *kw, PyObject **v)
 {
     const Py_ssize_t named = kw ? PyTuple_GET_SIZE(kw) : 0;
-    if (named == 1 && n == want && PyUnicode_CompareWithASCIIString(PyTuple_GET_ITEM(kw, 0), "stream") == 0) {
-        *stream = a[n];
-        return 1;
+    if (n > count) {
+        PyErr_Format(PyExc_TypeError, "%s() takes at most %zd arguments (%zd given)", entry, count, n);
+        return 0;
     }
-    if (named == 0 && (n == want || n == want + 1)) {
-        *stream = n > want ? a[want] : NULL;
-        return 1;
+    for (Py_ssize_t i = 0; i < count; ++i)
+        v[i] = i < n ? a[i] : NULL;
+    for (Py_ssize_t j = 0; j < named; ++j) {
+        PyObject *name = PyTuple_GET_ITEM(kw, j);
+        Py_ssize_t i = count - 1;                          // the stream first: the usual one
+        while (i >= 0 && PyUnicode_CompareWithASCIIString(name, names[i]) != 0)
+            --i;
+        if (i < 0 || v[i]) {
+            PyErr_Format(PyExc_TypeError, i < 0 ? "%s() got an unexpected keyword argument '%U'"
+                                                : "%s() got multiple values for argument '%U'", entry, name);
+            return 0;
+        }
+        v[i] = a[n + j];
     }
-    PyErr_Format(PyExc_TypeError, "%s takes %zd arguments and an optional stream", name, want);
-    return 0;
+    for (Py_ssize_t i = 0; i < count - 1; ++i)
+        if (!v[i]) {
+            PyErr_Format(PyExc_TypeError, "%s() missing required argument '%s'", entry, names[i]);
+            return 0;
+        }
+    return 1;
 }
 
 static PyObject *finish(int status, const char *name)
@@ -121,379 +144,114 @@ static PyObject *finish(int status, const char *name)
     return PyObject_CallFunction(g_raise, "is", status, name);
 }
 
-static int (*mxfp4_moe_route_at)(void *, void *, void *, void *, void *, void *, int64_t, int, void
-    *, int, int, int, int, float, void *, size_t, void *);
+#define ARGS_mxfp4_moe_route(ARG) \
+    ARG(ptr, ids) ARG(ptr, gates) ARG(ptr, offsets) ARG(ptr, row_token) ARG(ptr, slot_row) ARG(ptr, logits) ARG(i64, ldl) \
+    ARG(i32, logits_type) ARG(ptr, token_mask) ARG(i32, T) ARG(i32, E) ARG(i32, k) ARG(i32, gate_mode) ARG(f32, gate_scale) \
+    ARG(ptr, workspace) ARG(size, workspace_bytes)
+#define DOC_mxfp4_moe_route \
+    "The k largest logits per token, their gates, and the rows' grouping by expert."
 
-static PyObject *call_mxfp4_moe_route(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp4_moe_route", 16, a, n, kw, &so))
-        return NULL;
-    void *ids = as_pointer(a[0], &bad);
-    void *gates = as_pointer(a[1], &bad);
-    void *offsets = as_pointer(a[2], &bad);
-    void *row_token = as_pointer(a[3], &bad);
-    void *slot_row = as_pointer(a[4], &bad);
-    void *logits = as_pointer(a[5], &bad);
-    int64_t ldl = as_int64(a[6], &bad);
-    int logits_type = as_int(a[7], &bad);
-    void *token_mask = as_pointer(a[8], &bad);
-    int T = as_int(a[9], &bad);
-    int E = as_int(a[10], &bad);
-    int k = as_int(a[11], &bad);
-    int gate_mode = as_int(a[12], &bad);
-    float gate_scale = as_float(a[13], &bad);
-    void *workspace = as_pointer(a[14], &bad);
-    size_t workspace_bytes = as_size(a[15], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp4_moe_route_at(ids, gates, offsets, row_token, slot_row, logits, ldl,
-        logits_type, token_mask, T, E, k, gate_mode, gate_scale, workspace, workspace_bytes,
-        stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp4_moe_route");
-}
+#define ARGS_mxfp4_group_quantize(ARG) \
+    ARG(ptr, Q) ARG(i64, ldq) ARG(ptr, S) ARG(ptr, X) ARG(i64, ldx) ARG(i32, T) ARG(i32, K) ARG(ptr, slot_row) ARG(ptr, ids) \
+    ARG(i32, k) ARG(ptr, offsets) ARG(i32, groups) ARG(i32, rows)
+#define DOC_mxfp4_group_quantize \
+    "bf16 rows -> packed E2M1 rows at their places in the grouping, grouped scales."
 
-static int (*mxfp4_group_quantize_at)(void *, int64_t, void *, void *, int64_t, int, int, void *,
-    void *, int, void *, int, int, void *);
+#define ARGS_mxfp8_group_quantize(ARG) \
+    ARG(ptr, Q) ARG(i64, ldq) ARG(ptr, S) ARG(ptr, X) ARG(i64, ldx) ARG(i32, T) ARG(i32, K) ARG(ptr, slot_row) ARG(ptr, ids) \
+    ARG(i32, k) ARG(ptr, offsets) ARG(i32, groups) ARG(i32, rows) ARG(i32, fmt)
+#define DOC_mxfp8_group_quantize \
+    "mxfp4_group_quantize into E4M3 / E5M2 codes, one per byte."
 
-static PyObject *call_mxfp4_group_quantize(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp4_group_quantize", 13, a, n, kw, &so))
-        return NULL;
-    void *Q = as_pointer(a[0], &bad);
-    int64_t ldq = as_int64(a[1], &bad);
-    void *S = as_pointer(a[2], &bad);
-    void *X = as_pointer(a[3], &bad);
-    int64_t ldx = as_int64(a[4], &bad);
-    int T = as_int(a[5], &bad);
-    int K = as_int(a[6], &bad);
-    void *slot_row = as_pointer(a[7], &bad);
-    void *ids = as_pointer(a[8], &bad);
-    int k = as_int(a[9], &bad);
-    void *offsets = as_pointer(a[10], &bad);
-    int groups = as_int(a[11], &bad);
-    int rows = as_int(a[12], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp4_group_quantize_at(Q, ldq, S, X, ldx, T, K, slot_row, ids, k, offsets, groups,
-        rows, stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp4_group_quantize");
-}
+#define ARGS_mxfp4_grouped_gemm(ARG) \
+    ARG(ptr, D) ARG(i64, ldd) ARG(ptr, A) ARG(i64, lda) ARG(ptr, SA) ARG(ptr, B) ARG(i64, ldb) ARG(i64, stride_b) ARG(ptr, SB) \
+    ARG(ptr, offsets) ARG(i32, groups) ARG(i32, rows) ARG(i32, N) ARG(i32, K) ARG(f32, alpha) ARG(ptr, workspace) \
+    ARG(size, workspace_bytes)
+#define DOC_mxfp4_grouped_gemm \
+    "D[r] = alpha * A[r] . B[e]^T for every row r of group e (bf16 out)."
 
-static int (*mxfp8_group_quantize_at)(void *, int64_t, void *, void *, int64_t, int, int, void *,
-    void *, int, void *, int, int, int, void *);
+#define ARGS_mxfp8_grouped_gemm(ARG) \
+    ARG(ptr, D) ARG(i64, ldd) ARG(ptr, A) ARG(i64, lda) ARG(ptr, SA) ARG(ptr, B) ARG(i64, ldb) ARG(i64, stride_b) ARG(ptr, SB) \
+    ARG(ptr, offsets) ARG(i32, groups) ARG(i32, rows) ARG(i32, N) ARG(i32, K) ARG(i32, fmt_a) ARG(i32, fmt_b) ARG(f32, alpha) \
+    ARG(ptr, workspace) ARG(size, workspace_bytes)
+#define DOC_mxfp8_grouped_gemm \
+    "mxfp4_grouped_gemm on the byte formats of mxfp8_gemm."
 
-static PyObject *call_mxfp8_group_quantize(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp8_group_quantize", 14, a, n, kw, &so))
-        return NULL;
-    void *Q = as_pointer(a[0], &bad);
-    int64_t ldq = as_int64(a[1], &bad);
-    void *S = as_pointer(a[2], &bad);
-    void *X = as_pointer(a[3], &bad);
-    int64_t ldx = as_int64(a[4], &bad);
-    int T = as_int(a[5], &bad);
-    int K = as_int(a[6], &bad);
-    void *slot_row = as_pointer(a[7], &bad);
-    void *ids = as_pointer(a[8], &bad);
-    int k = as_int(a[9], &bad);
-    void *offsets = as_pointer(a[10], &bad);
-    int groups = as_int(a[11], &bad);
-    int rows = as_int(a[12], &bad);
-    int fmt = as_int(a[13], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp8_group_quantize_at(Q, ldq, S, X, ldx, T, K, slot_row, ids, k, offsets, groups,
-        rows, fmt, stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp8_group_quantize");
-}
+#define ARGS_mxfp4_grouped_swiglu(ARG) \
+    ARG(ptr, H) ARG(i64, ldh) ARG(ptr, SH) ARG(ptr, A) ARG(i64, lda) ARG(ptr, SA) ARG(ptr, B) ARG(i64, ldb) ARG(i64, stride_b) \
+    ARG(ptr, SB) ARG(ptr, offsets) ARG(i32, groups) ARG(i32, rows) ARG(i32, F) ARG(i32, K) ARG(f32, alpha) ARG(ptr, workspace) \
+    ARG(size, workspace_bytes)
+#define DOC_mxfp4_grouped_swiglu \
+    "H = quantise(silu(A . Bgate^T) * (A . Bup^T)) per group, packed E2M1."
 
-static int (*mxfp4_grouped_gemm_at)(void *, int64_t, void *, int64_t, void *, void *, int64_t,
-    int64_t, void *, void *, int, int, int, int, float, void *, size_t, void *);
+#define ARGS_mxfp8_grouped_swiglu(ARG) \
+    ARG(ptr, H) ARG(i64, ldh) ARG(ptr, SH) ARG(ptr, A) ARG(i64, lda) ARG(ptr, SA) ARG(ptr, B) ARG(i64, ldb) ARG(i64, stride_b) \
+    ARG(ptr, SB) ARG(ptr, offsets) ARG(i32, groups) ARG(i32, rows) ARG(i32, F) ARG(i32, K) ARG(i32, fmt_a) ARG(i32, fmt_b) \
+    ARG(i32, fmt_h) ARG(f32, alpha) ARG(ptr, workspace) ARG(size, workspace_bytes)
+#define DOC_mxfp8_grouped_swiglu \
+    "mxfp4_grouped_swiglu on byte formats, into E4M3 / E5M2 codes."
 
-static PyObject *call_mxfp4_grouped_gemm(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp4_grouped_gemm", 17, a, n, kw, &so))
-        return NULL;
-    void *D = as_pointer(a[0], &bad);
-    int64_t ldd = as_int64(a[1], &bad);
-    void *A = as_pointer(a[2], &bad);
-    int64_t lda = as_int64(a[3], &bad);
-    void *SA = as_pointer(a[4], &bad);
-    void *B = as_pointer(a[5], &bad);
-    int64_t ldb = as_int64(a[6], &bad);
-    int64_t stride_b = as_int64(a[7], &bad);
-    void *SB = as_pointer(a[8], &bad);
-    void *offsets = as_pointer(a[9], &bad);
-    int groups = as_int(a[10], &bad);
-    int rows = as_int(a[11], &bad);
-    int N = as_int(a[12], &bad);
-    int K = as_int(a[13], &bad);
-    float alpha = as_float(a[14], &bad);
-    void *workspace = as_pointer(a[15], &bad);
-    size_t workspace_bytes = as_size(a[16], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp4_grouped_gemm_at(D, ldd, A, lda, SA, B, ldb, stride_b, SB, offsets, groups,
-        rows, N, K, alpha, workspace, workspace_bytes, stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp4_grouped_gemm");
-}
+#define ARGS_mxfp4_moe_combine(ARG) \
+    ARG(ptr, H) ARG(i64, ldh) ARG(ptr, Nrm) ARG(i64, ldn) ARG(ptr, Y) ARG(i64, ldy) ARG(i32, rows) ARG(ptr, slot_row) \
+    ARG(ptr, gates) ARG(i32, k) ARG(ptr, resid) ARG(i64, ldr) ARG(ptr, w_post) ARG(ptr, w_pre) ARG(f32, res_scale) \
+    ARG(f32, out_scale) ARG(f32, eps) ARG(i32, T) ARG(i32, N)
+#define DOC_mxfp4_moe_combine \
+    "Gated sum of a token's rows, its norm, the residual stream and the next block's norm."
 
-static int (*mxfp8_grouped_gemm_at)(void *, int64_t, void *, int64_t, void *, void *, int64_t,
-    int64_t, void *, void *, int, int, int, int, int, int, float, void *, size_t, void *);
+#define ARGS_mxfp4_moe_ffn(ARG) \
+    ARG(ptr, H) ARG(i64, ldh) ARG(ptr, Nrm) ARG(i64, ldn) ARG(ptr, X) ARG(i64, ldx) ARG(ptr, ids) ARG(ptr, gates) \
+    ARG(ptr, offsets) ARG(ptr, slot_row) ARG(i32, T) ARG(i32, E) ARG(i32, k) ARG(i32, K) ARG(i32, F) ARG(ptr, B1) ARG(i64, ldb1) \
+    ARG(ptr, SB1) ARG(ptr, B2) ARG(i64, ldb2) ARG(ptr, SB2) ARG(ptr, resid) ARG(i64, ldr) ARG(ptr, w_post) ARG(ptr, w_pre) \
+    ARG(f32, res_scale) ARG(f32, out_scale) ARG(f32, eps) ARG(ptr, workspace) ARG(size, workspace_bytes)
+#define DOC_mxfp4_moe_ffn \
+    "A routed feed-forward block on MXFP4 weights: quantise, both products, join."
 
-static PyObject *call_mxfp8_grouped_gemm(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp8_grouped_gemm", 19, a, n, kw, &so))
-        return NULL;
-    void *D = as_pointer(a[0], &bad);
-    int64_t ldd = as_int64(a[1], &bad);
-    void *A = as_pointer(a[2], &bad);
-    int64_t lda = as_int64(a[3], &bad);
-    void *SA = as_pointer(a[4], &bad);
-    void *B = as_pointer(a[5], &bad);
-    int64_t ldb = as_int64(a[6], &bad);
-    int64_t stride_b = as_int64(a[7], &bad);
-    void *SB = as_pointer(a[8], &bad);
-    void *offsets = as_pointer(a[9], &bad);
-    int groups = as_int(a[10], &bad);
-    int rows = as_int(a[11], &bad);
-    int N = as_int(a[12], &bad);
-    int K = as_int(a[13], &bad);
-    int fmt_a = as_int(a[14], &bad);
-    int fmt_b = as_int(a[15], &bad);
-    float alpha = as_float(a[16], &bad);
-    void *workspace = as_pointer(a[17], &bad);
-    size_t workspace_bytes = as_size(a[18], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp8_grouped_gemm_at(D, ldd, A, lda, SA, B, ldb, stride_b, SB, offsets, groups,
-        rows, N, K, fmt_a, fmt_b, alpha, workspace, workspace_bytes, stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp8_grouped_gemm");
-}
+#define KIND_OF(kind, name) kind,
+#define NAME_OF(kind, name) #name,
+#define SHOWN(kind, name) #name ", "
+#define CONVERT(kind, name) kind name = as_##kind(v_[at_++], &bad_);
+#define PASS(kind, name) name,
 
-static int (*mxfp4_grouped_swiglu_at)(void *, int64_t, void *, void *, int64_t, void *, void *,
-    int64_t, int64_t, void *, void *, int, int, int, int, float, void *, size_t, void *);
+#define DEFINE(NAME)                                                                                              \
+    static int (*NAME##_at)(ARGS_##NAME(KIND_OF) void *);                                                          \
+    static PyObject *call_##NAME(PyObject *self_, PyObject *const *a_, Py_ssize_t n_, PyObject *kw_)               \
+    {                                                                                                              \
+        (void)self_;                                                                                               \
+        static const char *const names[] = {ARGS_##NAME(NAME_OF) "stream"};                                        \
+        enum { COUNT = sizeof(names) / sizeof(names[0]) };                                                         \
+        PyObject *v_[COUNT];                                                                                       \
+        int bad_ = 0, at_ = 0;                                                                                     \
+        if (!arrange(#NAME, names, COUNT, a_, n_, kw_, v_))                                                        \
+            return NULL;                                                                                           \
+        ARGS_##NAME(CONVERT)                                                                                       \
+        void *stream_ = as_stream(v_[at_], &bad_);                                                                 \
+        if (bad_)                                                                                                  \
+            return NULL;                                                                                           \
+        int status_;                                                                                               \
+        Py_BEGIN_ALLOW_THREADS                                                                                     \
+        status_ = NAME##_at(ARGS_##NAME(PASS) stream_);                                                            \
+        Py_END_ALLOW_THREADS                                                                                       \
+        return finish(status_, #NAME);                                                                             \
+    }
 
-static PyObject *call_mxfp4_grouped_swiglu(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp4_grouped_swiglu", 18, a, n, kw, &so))
-        return NULL;
-    void *H = as_pointer(a[0], &bad);
-    int64_t ldh = as_int64(a[1], &bad);
-    void *SH = as_pointer(a[2], &bad);
-    void *A = as_pointer(a[3], &bad);
-    int64_t lda = as_int64(a[4], &bad);
-    void *SA = as_pointer(a[5], &bad);
-    void *B = as_pointer(a[6], &bad);
-    int64_t ldb = as_int64(a[7], &bad);
-    int64_t stride_b = as_int64(a[8], &bad);
-    void *SB = as_pointer(a[9], &bad);
-    void *offsets = as_pointer(a[10], &bad);
-    int groups = as_int(a[11], &bad);
-    int rows = as_int(a[12], &bad);
-    int F = as_int(a[13], &bad);
-    int K = as_int(a[14], &bad);
-    float alpha = as_float(a[15], &bad);
-    void *workspace = as_pointer(a[16], &bad);
-    size_t workspace_bytes = as_size(a[17], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp4_grouped_swiglu_at(H, ldh, SH, A, lda, SA, B, ldb, stride_b, SB, offsets,
-        groups, rows, F, K, alpha, workspace, workspace_bytes, stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp4_grouped_swiglu");
-}
+#define ENTRIES(DO)                                                                                               \
+    DO(mxfp4_moe_route)                                                                                            \
+    DO(mxfp4_group_quantize)                                                                                       \
+    DO(mxfp8_group_quantize)                                                                                       \
+    DO(mxfp4_grouped_gemm)                                                                                         \
+    DO(mxfp8_grouped_gemm)                                                                                         \
+    DO(mxfp4_grouped_swiglu)                                                                                       \
+    DO(mxfp8_grouped_swiglu)                                                                                       \
+    DO(mxfp4_moe_combine)                                                                                          \
+    DO(mxfp4_moe_ffn)
 
-static int (*mxfp8_grouped_swiglu_at)(void *, int64_t, void *, void *, int64_t, void *, void *,
-    int64_t, int64_t, void *, void *, int, int, int, int, int, int, int, float, void *, size_t, void *);
+ENTRIES(DEFINE)
 
-static PyObject *call_mxfp8_grouped_swiglu(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp8_grouped_swiglu", 21, a, n, kw, &so))
-        return NULL;
-    void *H = as_pointer(a[0], &bad);
-    int64_t ldh = as_int64(a[1], &bad);
-    void *SH = as_pointer(a[2], &bad);
-    void *A = as_pointer(a[3], &bad);
-    int64_t lda = as_int64(a[4], &bad);
-    void *SA = as_pointer(a[5], &bad);
-    void *B = as_pointer(a[6], &bad);
-    int64_t ldb = as_int64(a[7], &bad);
-    int64_t stride_b = as_int64(a[8], &bad);
-    void *SB = as_pointer(a[9], &bad);
-    void *offsets = as_pointer(a[10], &bad);
-    int groups = as_int(a[11], &bad);
-    int rows = as_int(a[12], &bad);
-    int F = as_int(a[13], &bad);
-    int K = as_int(a[14], &bad);
-    int fmt_a = as_int(a[15], &bad);
-    int fmt_b = as_int(a[16], &bad);
-    int fmt_h = as_int(a[17], &bad);
-    float alpha = as_float(a[18], &bad);
-    void *workspace = as_pointer(a[19], &bad);
-    size_t workspace_bytes = as_size(a[20], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp8_grouped_swiglu_at(H, ldh, SH, A, lda, SA, B, ldb, stride_b, SB, offsets,
-        groups, rows, F, K, fmt_a, fmt_b, fmt_h, alpha, workspace, workspace_bytes, stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp8_grouped_swiglu");
-}
-
-static int (*mxfp4_moe_combine_at)(void *, int64_t, void *, int64_t, void *, int64_t, int, void *,
-    void *, int, void *, int64_t, void *, void *, float, float, float, int, int, void *);
-
-static PyObject *call_mxfp4_moe_combine(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp4_moe_combine", 19, a, n, kw, &so))
-        return NULL;
-    void *H = as_pointer(a[0], &bad);
-    int64_t ldh = as_int64(a[1], &bad);
-    void *Nrm = as_pointer(a[2], &bad);
-    int64_t ldn = as_int64(a[3], &bad);
-    void *Y = as_pointer(a[4], &bad);
-    int64_t ldy = as_int64(a[5], &bad);
-    int rows = as_int(a[6], &bad);
-    void *slot_row = as_pointer(a[7], &bad);
-    void *gates = as_pointer(a[8], &bad);
-    int k = as_int(a[9], &bad);
-    void *resid = as_pointer(a[10], &bad);
-    int64_t ldr = as_int64(a[11], &bad);
-    void *w_post = as_pointer(a[12], &bad);
-    void *w_pre = as_pointer(a[13], &bad);
-    float res_scale = as_float(a[14], &bad);
-    float out_scale = as_float(a[15], &bad);
-    float eps = as_float(a[16], &bad);
-    int T = as_int(a[17], &bad);
-    int N = as_int(a[18], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp4_moe_combine_at(H, ldh, Nrm, ldn, Y, ldy, rows, slot_row, gates, k, resid,
-        ldr, w_post, w_pre, res_scale, out_scale, eps, T, N, stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp4_moe_combine");
-}
-
-static int (*mxfp4_moe_ffn_at)(void *, int64_t, void *, int64_t, void *, int64_t, void *, void *,
-    void *, void *, int, int, int, int, int, void *, int64_t, void *, void *, int64_t, void *, void *,
-    int64_t, void *, void *, float, float, float, void *, size_t, void *);
-
-static PyObject *call_mxfp4_moe_ffn(PyObject *self, PyObject *const *a, Py_ssize_t n, PyObject *kw)
-{
-    (void)self;
-    PyObject *so;
-    int bad = 0;
-    if (!stream_argument("mxfp4_moe_ffn", 30, a, n, kw, &so))
-        return NULL;
-    void *H = as_pointer(a[0], &bad);
-    int64_t ldh = as_int64(a[1], &bad);
-    void *Nrm = as_pointer(a[2], &bad);
-    int64_t ldn = as_int64(a[3], &bad);
-    void *X = as_pointer(a[4], &bad);
-    int64_t ldx = as_int64(a[5], &bad);
-    void *ids = as_pointer(a[6], &bad);
-    void *gates = as_pointer(a[7], &bad);
-    void *offsets = as_pointer(a[8], &bad);
-    void *slot_row = as_pointer(a[9], &bad);
-    int T = as_int(a[10], &bad);
-    int E = as_int(a[11], &bad);
-    int k = as_int(a[12], &bad);
-    int K = as_int(a[13], &bad);
-    int F = as_int(a[14], &bad);
-    void *B1 = as_pointer(a[15], &bad);
-    int64_t ldb1 = as_int64(a[16], &bad);
-    void *SB1 = as_pointer(a[17], &bad);
-    void *B2 = as_pointer(a[18], &bad);
-    int64_t ldb2 = as_int64(a[19], &bad);
-    void *SB2 = as_pointer(a[20], &bad);
-    void *resid = as_pointer(a[21], &bad);
-    int64_t ldr = as_int64(a[22], &bad);
-    void *w_post = as_pointer(a[23], &bad);
-    void *w_pre = as_pointer(a[24], &bad);
-    float res_scale = as_float(a[25], &bad);
-    float out_scale = as_float(a[26], &bad);
-    float eps = as_float(a[27], &bad);
-    void *workspace = as_pointer(a[28], &bad);
-    size_t workspace_bytes = as_size(a[29], &bad);
-    void *stream = as_stream(so, &bad);
-    if (bad)
-        return NULL;
-    int status;
-    Py_BEGIN_ALLOW_THREADS
-    status = mxfp4_moe_ffn_at(H, ldh, Nrm, ldn, X, ldx, ids, gates, offsets, slot_row, T, E, k,
-        K, F, B1, ldb1, SB1, B2, ldb2, SB2, resid, ldr, w_post, w_pre, res_scale, out_scale, eps,
-        workspace, workspace_bytes, stream);
-    Py_END_ALLOW_THREADS
-    return finish(status, "mxfp4_moe_ffn");
-}
-
+#define ADDRESS(NAME) {#NAME, (void **)&NAME##_at},
 static struct {
     const char *name;
     void **at;
-} g_entries[] = {
-    {"mxfp4_moe_route", (void **)&mxfp4_moe_route_at},
-    {"mxfp4_group_quantize", (void **)&mxfp4_group_quantize_at},
-    {"mxfp8_group_quantize", (void **)&mxfp8_group_quantize_at},
-    {"mxfp4_grouped_gemm", (void **)&mxfp4_grouped_gemm_at},
-    {"mxfp8_grouped_gemm", (void **)&mxfp8_grouped_gemm_at},
-    {"mxfp4_grouped_swiglu", (void **)&mxfp4_grouped_swiglu_at},
-    {"mxfp8_grouped_swiglu", (void **)&mxfp8_grouped_swiglu_at},
-    {"mxfp4_moe_combine", (void **)&mxfp4_moe_combine_at},
-    {"mxfp4_moe_ffn", (void **)&mxfp4_moe_ffn_at},
-};
+} g_entries[] = {ENTRIES(ADDRESS)};
 
 // bind(addresses: dict, pointer, current_stream, raise_error)
 static PyObject *bind(PyObject *self, PyObject *args)
@@ -518,18 +276,11 @@ static PyObject *bind(PyObject *self, PyObject *args)
     Py_RETURN_NONE;
 }
 
-#define METHOD(NAME) {#NAME, (PyCFunction)(void (*)(void))call_##NAME, METH_FASTCALL | METH_KEYWORDS, NULL}
+#define METHOD(NAME)                                                              \
+    {#NAME, (PyCFunction)(void (*)(void))call_##NAME, METH_FASTCALL | METH_KEYWORDS, \
+     #NAME "($module, " ARGS_##NAME(SHOWN) "stream=None)\n--\n\n" DOC_##NAME},
 static PyMethodDef g_methods[] = {
-    METHOD(mxfp4_moe_route),
-    METHOD(mxfp4_group_quantize),
-    METHOD(mxfp8_group_quantize),
-    METHOD(mxfp4_grouped_gemm),
-    METHOD(mxfp8_grouped_gemm),
-    METHOD(mxfp4_grouped_swiglu),
-    METHOD(mxfp8_grouped_swiglu),
-    METHOD(mxfp4_moe_combine),
-    METHOD(mxfp4_moe_ffn),
-    {"bind", bind, METH_VARARGS, NULL},
+    ENTRIES(METHOD){"bind", bind, METH_VARARGS, NULL},
     {NULL, NULL, 0, NULL},
 };
 
