@@ -15,6 +15,7 @@ import contextlib
 import ctypes
 import os
 import re
+import warnings
 from typing import Optional
 
 __all__ = [
@@ -168,16 +169,32 @@ def _raise(status, where):
 _python_entries = {}        # what _bind_entries replaced
 
 
+def _entry_module():
+    """The extension module built for this interpreter, by its full path: one
+    built for another would be found by its name alone."""
+    import importlib.util
+    from .build import BINDING_LIB
+    spec = importlib.util.spec_from_file_location(__name__ + "._entry", BINDING_LIB)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
 def _bind_entries(L):
     """Replace the calls of a decoding step by the extension module's, which
     take the same arguments, by place or by name, and marshal them in C."""
-    from . import _entry
-    names = [n for n in dir(_entry) if n.startswith("mxfp")]
-    _entry.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _p,
-                _current_stream, _raise)
+    try:
+        entry = _entry_module()
+    except ImportError as e:
+        warnings.warn(f"the Python binding's fast path cannot be loaded ({e}): the expert-layer "
+                      "calls are marshalled in Python, some 2 us slower each")
+        return
+    names = [n for n in dir(entry) if n.startswith("mxfp")]
+    entry.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _p,
+               _current_stream, _raise)
     for n in names:
         _python_entries[n] = globals()[n]
-        globals()[n] = getattr(_entry, n)
+        globals()[n] = getattr(entry, n)
 
 
 def header_functions(path: str = HEADER):

@@ -4,9 +4,11 @@
 
 Each .cu under csrc/ compiles to an object in parallel, then one link makes
 libmxfp4_gb300.so next to this file.  The Python binding's fast path
-(csrc/binding.c) compiles to the extension module _entry.so.  The benchmark's streaming-read helper
-(probe/stream_read.cu, not part of the library) links into libmxfp4_probe.so.
-Rebuilds only when a source or header is newer than its library.
+(csrc/binding.c) compiles to the extension module _entry, named for the
+interpreter that it is built for; without it the package marshals the same calls
+in Python.  The benchmark's streaming-read helper (probe/stream_read.cu, not part
+of the library) links into libmxfp4_probe.so.  Rebuilds only when a source or
+header is newer than its library.
 """
 from __future__ import annotations
 
@@ -18,6 +20,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,7 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmxfp4_gb300.so")
 BINDING_SRC = os.path.join(CSRC, "binding.c")
-BINDING_LIB = os.path.join(PKG, "_entry.so")
+BINDING_LIB = os.path.join(PKG, "_entry" + sysconfig.get_config_var("EXT_SUFFIX"))
 PROBE_SRC = os.path.join(PKG, "probe", "stream_read.cu")
 PROBE_LIB = os.path.join(PKG, "libmxfp4_probe.so")
 OBJDIR = os.path.join(PKG, "_build")
@@ -92,7 +95,15 @@ def build_binding(force: bool = False) -> str:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    build_binding(force)
+    path = build_library(force, verbose_ptxas)
+    try:
+        build_binding(force)
+    except (OSError, RuntimeError) as e:
+        warnings.warn(f"the Python binding's fast path was not built ({e}): its calls are marshalled in Python")
+    return path
+
+
+def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
     if not force and not verbose_ptxas and up_to_date():
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)

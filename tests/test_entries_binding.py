@@ -4,8 +4,12 @@ accepts, the other has to accept.  And every list of an entry's arguments (the C
 header, the ctypes table, the Python function, the extension module) has to say
 the same.  No GPU: every call is refused by the library's checks."""
 import ctypes
+import importlib.machinery
 import inspect
+import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -74,3 +78,53 @@ def test_each_argument_reaches_its_place(name):
     for wrong in names:
         with pytest.raises((TypeError, AttributeError)):
             getattr(mx, name)(**{n: object() if n == wrong else 0 for n in names})
+
+
+WITHOUT = """
+import warnings
+from block_scaled_mxfp4_gb300 import build
+import block_scaled_mxfp4_gb300 as mx
+build.BINDING_LIB = {path!r}
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    mx.lib()
+assert len(seen) == 1 and "marshalled in Python" in str(seen[0].message), seen
+assert mx.mxfp4_version() > 0 and mx.mxfp4_gemm_workspace_size(128, 256, 512) >= 0
+for call, args in ((mx.mxfp4_gemm, [0] * 20), (mx.mxfp4_moe_combine, [0] * 19)):
+    try:
+        call(*args, stream=0)
+    except mx.Mxfp4Error as e:
+        assert e.status == -1
+    else:
+        raise AssertionError
+print("fine")
+"""
+
+
+@pytest.mark.parametrize("content", [None, b"", b"\x7fELF of another machine"])
+def test_the_library_works_without_the_extension(tmp_path, content):
+    path = tmp_path / "_entry.so"
+    if content is not None:
+        path.write_bytes(content)
+    run = subprocess.run([sys.executable, "-c", WITHOUT.format(path=str(path))], cwd=os.path.dirname(os.path.dirname(mx.__file__)),
+                         capture_output=True, text=True)
+    assert run.returncode == 0 and run.stdout == "fine\n", run.stderr
+
+
+def test_build_goes_on_without_the_extension(tmp_path, monkeypatch):
+    monkeypatch.setattr(mxbuild, "BINDING_LIB", str(tmp_path / "_entry.so"))
+    monkeypatch.setenv("PATH", str(tmp_path))              # no compiler
+    with pytest.warns(UserWarning, match="marshalled in Python"):
+        assert mxbuild.build() == mxbuild.LIB
+    monkeypatch.undo()
+    source = tmp_path / "binding.c"
+    source.write_text("#error no headers\n")
+    monkeypatch.setattr(mxbuild, "BINDING_LIB", str(tmp_path / "_entry.so"))
+    monkeypatch.setattr(mxbuild, "BINDING_SRC", str(source))
+    with pytest.warns(UserWarning, match="marshalled in Python"):
+        assert mxbuild.build() == mxbuild.LIB
+
+
+def test_the_extension_is_named_for_its_interpreter():
+    assert any(mxbuild.BINDING_LIB.endswith(s) for s in importlib.machinery.EXTENSION_SUFFIXES if s != ".so")
+    assert mx.mxfp4_moe_ffn.__module__ == "block_scaled_mxfp4_gb300._entry"
