@@ -105,15 +105,18 @@ static void *as_stream(PyObject *o, int *bad)
     return p;
 }
 
-// The arguments in the order of `names`, whose last is the optional stream (NULL
-// where it is not given).
-static int arrange(const char *entry, const char *const *names, Py_ssize_t count, PyObject *const *a, Py_ssize_t n,
-                   PyObject *kw, PyObject **v)
+// The arguments in the order of `names`, whose last is the optional stream: `a`
+// itself where all are given by place, else `v` (NULL for no stream), else NULL
+// with an error.
+static PyObject *const *arrange(const char *entry, const char *const *names, Py_ssize_t count, PyObject *const *a,
+                                Py_ssize_t n, PyObject *kw, PyObject **v)
 {
     const Py_ssize_t named = kw ? PyTuple_GET_SIZE(kw) : 0;
+    if (named == 0 && (n == count - 1 || n == count))
+        return a;
     if (n > count) {
         PyErr_Format(PyExc_TypeError, "%s() takes at most %zd arguments (%zd given)", entry, count, n);
-        return 0;
+        return NULL;
     }
     for (Py_ssize_t i = 0; i < count; ++i)
         v[i] = i < n ? a[i] : NULL;
@@ -125,16 +128,16 @@ static int arrange(const char *entry, const char *const *names, Py_ssize_t count
         if (i < 0 || v[i]) {
             PyErr_Format(PyExc_TypeError, i < 0 ? "%s() got an unexpected keyword argument '%U'"
                                                 : "%s() got multiple values for argument '%U'", entry, name);
-            return 0;
+            return NULL;
         }
         v[i] = a[n + j];
     }
     for (Py_ssize_t i = 0; i < count - 1; ++i)
         if (!v[i]) {
             PyErr_Format(PyExc_TypeError, "%s() missing required argument '%s'", entry, names[i]);
-            return 0;
+            return NULL;
         }
-    return 1;
+    return v;
 }
 
 static PyObject *finish(int status, const char *name)
@@ -219,12 +222,13 @@ static PyObject *finish(int status, const char *name)
         (void)self_;                                                                                               \
         static const char *const names[] = {ARGS_##NAME(NAME_OF) "stream"};                                        \
         enum { COUNT = sizeof(names) / sizeof(names[0]) };                                                         \
-        PyObject *v_[COUNT];                                                                                       \
+        PyObject *arranged_[COUNT];                                                                                \
+        PyObject *const *v_ = arrange(#NAME, names, COUNT, a_, n_, kw_, arranged_);                                \
         int bad_ = 0, at_ = 0;                                                                                     \
-        if (!arrange(#NAME, names, COUNT, a_, n_, kw_, v_))                                                        \
+        if (!v_)                                                                                                   \
             return NULL;                                                                                           \
         ARGS_##NAME(CONVERT)                                                                                       \
-        void *stream_ = as_stream(v_[at_], &bad_);                                                                 \
+        void *stream_ = as_stream(v_ == a_ && n_ < COUNT ? NULL : v_[at_], &bad_);                                 \
         if (bad_)                                                                                                  \
             return NULL;                                                                                           \
         int status_;                                                                                               \
