@@ -517,7 +517,9 @@ __global__ void __launch_bounds__(512, 1)
     const int groups = a.groups, rows = a.rows, nt = a.nt;
     asm volatile("" ::"l"(offsets), "r"(groups), "r"(rows), "r"(nt), "r"(a.kt), "r"(a.N), "l"(a.wait_limit));
     // Offsets and weights may come from the work before this grid, like
-    // everything else; with a.early only the rows and their scales do.
+    // everything else; with a.early only the rows and their scales do.  A role
+    // that those keep waiting first waits for the grid before, which has no
+    // limit: the limit is for this kernel's own work.
     if (!a.early)
         pdl_wait_prerequisites();
     build_tables<Cf::ROWS>(offsets, groups, rows, tab_off, tab_base, warp_sum);
@@ -629,6 +631,8 @@ __global__ void __launch_bounds__(512, 1)
                 const int role = warp == 4 ? 0 : warp - 5;   // 0: A and its scales, 1: B, 2: B's scales
                 if (role == 0 && a.early)
                     pdl_wait_prerequisites();
+                // B's loaders run ahead as far as the ring goes.
+                bool ahead = role != 0 && a.early;
                 int stage = 0;
                 uint32_t phase = 0;
                 int issued = 0;
@@ -648,6 +652,10 @@ __global__ void __launch_bounds__(512, 1)
                                           : role == 1 ? (halves ? Cf::B_BYTES / 2 : Cf::B_BYTES)
                                                       : Cf::SFB_BYTES;
                     for (int kt = 0; kt < a.kt; ++kt) {
+                        if (ahead && issued == STAGES) {
+                            pdl_wait_prerequisites();
+                            ahead = false;
+                        }
                         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_limit, &g_status)) {
                             stop = true;
                             break;
@@ -703,6 +711,8 @@ __global__ void __launch_bounds__(512, 1)
             const bool upper = GATED && halves && total > 0 && (tile_at<Cf::ROWS>(table, pair).q & 1);
             int stage = 0;
             uint32_t phase = 0;
+            if (a.early)
+                pdl_wait_prerequisites();
             for (int i = 0; i < total; ++i) {
                 bool ok = mbar_wait(&full[stage], phase, abort_flag, a.wait_limit, &g_status);
                 if (!__all_sync(kFull, ok))
@@ -768,6 +778,8 @@ __global__ void __launch_bounds__(512, 1)
                 int stage = 0;
                 uint32_t phase = 0, acc_phase = 0;
                 bool stop = false;
+                if (a.early)
+                    pdl_wait_prerequisites();
                 for (int t = pair; t < tiles && !stop; t += pairs) {
                     if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, a.wait_limit, &g_status))
                         break;
