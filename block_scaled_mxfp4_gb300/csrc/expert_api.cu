@@ -412,7 +412,7 @@ int mxfp4_moe_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *
 {
     if (T < 0 || N < 1 || rows < 0 || k < 1 || k > kMaxTopK || (!slot_row && (k != 1 || rows < T)) || !(eps >= 0.0f))
         return MXFP4_ERR_INVALID_ARG;
-    if (T > 0 && ((!H && !Nrm) || !Y || ldy < N || (H && ldh < N) || (Nrm && ldn < N) || (resid && ldr < N)))
+    if (T > 0 && ((!H && !Nrm) || (rows > 0 && (!Y || ldy < N)) || (H && ldh < N) || (Nrm && ldn < N) || (resid && ldr < N)))
         return MXFP4_ERR_INVALID_ARG;
     for (const void *p : {static_cast<const void *>(H), static_cast<const void *>(Nrm), Y, resid, w_post, w_pre})
         if (!aligned(p, 2))

@@ -560,9 +560,10 @@ size_t mxfp4_grouped_workspace_size(int rows, int groups, int N, int K);
  *   h = res_scale * resid[t] + out_scale * b             -> H
  *   n = h / sqrt(mean(h^2) + eps) * w_pre                -> Nrm
  * all in fp32, H and Nrm each rounded once (the norm is of the unrounded h).
- *   Y bf16 [rows, ldy]; resid bf16 [T, ldr] or NULL (0); w_post, w_pre bf16
- *   [N] or NULL (w_pre NULL: ones); H, Nrm bf16 [T, ldh / ldn], either may be
- *   NULL; gates NULL: ones; slot_row NULL (k = 1): row t of Y.
+ *   Y bf16 [rows, ldy] (rows = 0: no slot is taken, Y may be NULL); resid bf16
+ *   [T, ldr] or NULL (0); w_post, w_pre bf16 [N] or NULL (w_pre NULL: ones); H,
+ *   Nrm bf16 [T, ldh / ldn], either may be NULL; gates NULL: ones; slot_row NULL
+ *   (k = 1): row t of Y.
  * H may alias resid (with ldh == ldr).  N <= 32768.  Rows whose pointers and
  * strides allow 16-byte accesses are faster.
  */

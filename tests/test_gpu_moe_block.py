@@ -84,3 +84,19 @@ def test_logits_of_other_types_are_refused():
     for bad in (logits.half(), logits.double()):
         with pytest.raises(TypeError):
             w(x, bad, resid, 2)
+
+
+@pytest.mark.parametrize("T,N", [(5, 512), (5, 515), (700, 2048), (700, 2049)])
+def test_a_join_without_rows(T, N):
+    """No token has an expert and there is no row: the residual stream and its norm, in every form."""
+    rng = np.random.default_rng(N)
+    resid = dev(rng.normal(size=(T, N))).to(torch.bfloat16)
+    Y = torch.empty((0, N), dtype=torch.bfloat16, device="cuda")
+    slots, gates = torch.full((T, 2), -1, dtype=torch.int32, device="cuda"), torch.ones((T, 2), device="cuda")
+    h, n = torch.empty_like(resid), torch.empty_like(resid)
+    mx.mxfp4_moe_combine(h, N, n, N, Y, N, 0, slots, gates, 2, resid, N, None, None, 1.0, 1.0, 1e-6, T, N)
+    torch.cuda.synchronize()
+    assert torch.equal(h, resid)
+    v = resid.double().cpu().numpy()
+    want = v / np.sqrt((v * v).mean(1, keepdims=True) + 1e-6)
+    assert (np.abs(bf16_bits_to_f64(d_to_bits(n)) - want) <= ulp_bf16(want) + 2.0 ** -18 * np.abs(want)).all()
