@@ -11,6 +11,9 @@ using namespace mxfp4;
 namespace {
 
 constexpr size_t kAlign = 256;
+// Row and token counts that the kernels' 32-bit indexes can step over: a tile's
+// rows (256) or a grid's tokens (a few thousand) past the last one.
+constexpr int kMaxRows = 0x7FFFFFFF - (1 << 16);
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -74,6 +77,8 @@ int check_product(const Product &p)
         return MXFP4_ERR_MISALIGNED;
     if (!gated && !aligned(p.D, 2))
         return MXFP4_ERR_MISALIGNED;
+    if (p.rows > kMaxRows)
+        return MXFP4_ERR_UNSUPPORTED_SHAPE;
     const int64_t row_tiles = p.rows / 256 + (p.groups < p.rows ? p.groups : p.rows);
     const int64_t nt = (static_cast<int64_t>(p.N) + (gated ? 127 : 255)) / (gated ? 128 : 256);
     if (row_tiles * nt > 0x3FFFFFFF || group_sf_blocks(p.rows, p.groups) > 0x7FFFFFFF)
@@ -419,7 +424,7 @@ int mxfp4_moe_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *
             return MXFP4_ERR_MISALIGNED;
     if (!aligned(slot_row, 4) || !aligned(gates, 4))
         return MXFP4_ERR_MISALIGNED;
-    if (N > 32768)
+    if (N > 32768 || T > kMaxRows)
         return MXFP4_ERR_UNSUPPORTED_SHAPE;
     int sms = 0;
     const int st = check_current_device(&sms);
@@ -449,7 +454,7 @@ int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, i
     if (T > 0 && (!ids || !gates || !slot_row || !X || ldx < K || (!H && !Nrm) || (H && ldh < K) ||
                   (Nrm && ldn < K) || (resid && ldr < K)))
         return MXFP4_ERR_INVALID_ARG;
-    if (K > 32768)
+    if (K > 32768 || static_cast<int64_t>(T) * k > kMaxRows)
         return MXFP4_ERR_UNSUPPORTED_SHAPE;
     if (T > 0 && (!aligned(H, 2) || !aligned(Nrm, 2) || !aligned(resid, 2) || !aligned(w_post, 2) ||
                   !aligned(w_pre, 2) || !aligned(X, 16) || (ldx % 8) != 0 || !aligned(ids, 4) || !aligned(gates, 4) ||

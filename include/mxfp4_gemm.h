@@ -450,7 +450,8 @@ int mxfp8_quantize(void *Q, int64_t ldq, void *S, int64_t lds, const void *X, in
  *
  * These entry points follow the conventions at the top of this file (caller's
  * memory and stream, arguments checked before anything is enqueued, capture
- * into graphs).  groups <= 1024, k <= 16.  Weights of experts without rows
+ * into graphs).  groups <= 1024, k <= 16; the products, the join and the block
+ * take up to 2^31 - 2^16 rows or tokens.  Weights of experts without rows
  * are not read.
  * ------------------------------------------------------------------------ */
 
