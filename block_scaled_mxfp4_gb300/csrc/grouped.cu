@@ -245,6 +245,11 @@ __device__ __forceinline__ Tile tile_at(const TileTable &t, int i)
 // Fill the tables: thread t takes groups 2t and 2t + 1 of up to 1024.  Up to 64
 // groups are one warp's work and need no exchange between warps.  warp_sum: 16
 // words of shared memory.  Ends with a block barrier.
+//
+// Ascending offsets make at most rows / ROWS + groups row tiles, which the host
+// has checked to fit an int times the column tiles.  Offsets out of order can make
+// up to groups / 2 times rows / ROWS: 32 unsigned bits hold that, and the table is
+// cut off at the bound, so that a tile's number stays one whatever the offsets.
 template <int ROWS>
 __device__ __forceinline__ void build_tables(const int *offsets, int groups, int rows, int *off, int *base,
                                              int *warp_sum)
@@ -258,37 +263,38 @@ __device__ __forceinline__ void build_tables(const int *offsets, int groups, int
             const int e = 2 * t + i;
             o[i] = e <= groups ? min(max(offsets[e], 0), rows) : 0;
         }
-        int c[2];
+        uint32_t c[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            c[i] = 2 * t + i < groups ? (max(o[i + 1] - o[i], 0) + ROWS - 1) / ROWS : 0;
-        int sum = c[0] + c[1];
+            c[i] = 2 * t + i < groups ? static_cast<uint32_t>(max(o[i + 1] - o[i], 0) + ROWS - 1) / ROWS : 0u;
+        uint32_t sum = c[0] + c[1];
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int v = __shfl_up_sync(kFull, sum, d);
+            const uint32_t v = __shfl_up_sync(kFull, sum, d);
             if (lane >= d)
                 sum += v;
         }
-        int before = sum - c[0] - c[1];
+        const uint32_t bound = static_cast<uint32_t>(rows / ROWS) + static_cast<uint32_t>(min(groups, rows));
+        uint32_t before = sum - c[0] - c[1];
         if (!one_warp) {
             if (lane == 31)
-                warp_sum[warp] = sum;
+                warp_sum[warp] = static_cast<int>(sum);
             __syncthreads();
             for (int w = 0; w < warp; ++w)
-                before += warp_sum[w];
+                before += static_cast<uint32_t>(warp_sum[w]);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int e = 2 * t + i;
             if (e <= groups) {
                 off[e] = o[i];
-                base[e] = before;
+                base[e] = static_cast<int>(min(before, bound));
                 before += c[i];
             }
         }
         if (2 * t + 2 == groups) {     // the entry past this thread's pair
             off[groups] = o[2];
-            base[groups] = before;
+            base[groups] = static_cast<int>(min(before, bound));
         }
     }
     __syncthreads();
@@ -530,7 +536,7 @@ __global__ void __launch_bounds__(512, 1)
     // stage's MMAs less time to issue: one-token block of 3 experts, 544 x 1504,
     // 12.3 us, with whole tiles 13.7.  Halving the last of several rounds as well
     // keeps SMs from the next launch: 32 rows in 25 groups 24.4 against 23.3.
-    const bool halves = SOLO && 2 * table.tiles() <= pairs;
+    const bool halves = SOLO && table.tiles() <= pairs / 2;
     if (halves)
         table.nt *= 2;
     const int tiles = table.tiles();

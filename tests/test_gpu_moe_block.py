@@ -14,6 +14,7 @@ import pytest
 
 import block_scaled_mxfp4_gb300 as mx
 import expert_ref as ref
+from test_gpu_experts import Grouped
 from parity_util import bf16_bits_to_f64, d_to_bits, ulp_bf16
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,36 @@ def test_a_join_without_rows(T, N):
     v = resid.double().cpu().numpy()
     want = v / np.sqrt((v * v).mean(1, keepdims=True) + 1e-6)
     assert (np.abs(bf16_bits_to_f64(d_to_bits(n)) - want) <= ulp_bf16(want) + 2.0 ** -18 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("counts", [[10, 10, 10], [40, 0, 60, 20], [300, 250], [3] * 120 + [400]],
+                         ids=["32 rows", "single CTAs", "pairs", "many groups"])
+@pytest.mark.parametrize("gated", [False, True])
+def test_offsets_out_of_order_write_nothing_outside(counts, gated):
+    """Unordered or oversized offsets: values are unspecified, but the arrays' neighbours stay."""
+    p = Grouped(counts, 320, 96, halves=2 if gated else 1)
+    rows, E = p.rows, p.E
+    rng = np.random.default_rng(rows)
+    some = [np.arange(E + 1)[::-1] * rows // E, np.where(np.arange(E + 1) % 2, rows, 0), np.where(np.arange(E + 1) % 2, 0, rows),
+            rng.integers(-rows, 3 * rows, size=E + 1), np.full(E + 1, -(1 << 31)), np.full(E + 1, (1 << 31) - 1),
+            np.where(np.arange(E + 1) % 2, (1 << 31) - 1, -(1 << 31)), rng.permutation(p.offsets)]
+    pad = 4096
+
+    def guarded(n):
+        t = torch.full((n + 2 * pad,), 0xAB, dtype=torch.uint8, device="cuda")
+        return t, t[pad:pad + n]
+
+    for offsets in some:
+        p.dO = dev(offsets.astype(np.int32))
+        if gated:
+            (all_h, H), (all_s, S) = guarded(rows * p.N // 2), guarded(mx.mxfp4_group_scale_size(rows, E, p.N))
+            mx.mxfp4_grouped_swiglu(H, p.N, S, p.dA, p.lda, p.dSA, p.dB, p.ldb, 2 * p.N * p.ldb, p.dSB, p.dO, E, rows, p.N, p.K, 1.0, None, 0)
+            arrays = (all_h, all_s)
+        else:
+            all_d, D = guarded(rows * p.N * 2)
+            mx.mxfp4_grouped_gemm(D, p.N, p.dA, p.lda, p.dSA, p.dB, p.ldb, p.N * p.ldb, p.dSB, p.dO, E, rows, p.N, p.K, 1.0, None, 0)
+            arrays = (all_d,)
+        torch.cuda.synchronize()
+        assert mx.mxfp4_device_status() == 0
+        for t in arrays:
+            assert (t[:pad] == 0xAB).all() and (t[-pad:] == 0xAB).all()
