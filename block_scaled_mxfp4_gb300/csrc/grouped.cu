@@ -637,8 +637,6 @@ __global__ void __launch_bounds__(512, 1)
                 const int role = warp == 4 ? 0 : warp - 5;   // 0: A and its scales, 1: B, 2: B's scales
                 if (role == 0 && a.early)
                     pdl_wait_prerequisites();
-                // B's loaders run ahead as far as the ring goes.
-                bool ahead = role != 0 && a.early;
                 int stage = 0;
                 uint32_t phase = 0;
                 int issued = 0;
@@ -658,13 +656,16 @@ __global__ void __launch_bounds__(512, 1)
                                           : role == 1 ? (halves ? Cf::B_BYTES / 2 : Cf::B_BYTES)
                                                       : Cf::SFB_BYTES;
                     for (int kt = 0; kt < a.kt; ++kt) {
-                        if (ahead && issued == STAGES) {
-                            pdl_wait_prerequisites();
-                            ahead = false;
-                        }
-                        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_limit, &g_status)) {
-                            stop = true;
-                            break;
+                        if (!mbar_try_wait(smem_addr(&empty[stage]), phase ^ 1u)) {
+                            // B's loaders run ahead as far as the ring goes.  (Asked
+                            // only where the slot is not free yet: a test of its own
+                            // on every stage cost the 32768 rows' product 1 %.)
+                            if (a.early)
+                                pdl_wait_prerequisites();
+                            if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.wait_limit, &g_status)) {
+                                stop = true;
+                                break;
+                            }
                         }
                         uint8_t *st = smem + stage * Cf::STAGE_BYTES;
                         uint8_t *sf = st + Cf::A_BYTES + Cf::B_BYTES;
