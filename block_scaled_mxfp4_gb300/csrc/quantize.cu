@@ -21,46 +21,13 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "quant.cuh"
 
 namespace mxfp4 {
 
 namespace {
 
 constexpr int kQuantThreads = 256;
-
-// Largest s with 6 * 2^s <= a for a finite a > 0 (float bits): a = f * 2^e
-// with f in [1, 2) (or a subnormal), and 6 * 2^s = 1.5 * 2^(s + 2), so
-// s = e - 2 when f >= 1.5, else e - 3.
-__device__ __forceinline__ int block_exponent(float amax)
-{
-    if (amax == 0.0f)
-        return 0;
-    const uint32_t bits = __float_as_uint(amax);
-    const int biased = static_cast<int>((bits >> 23) & 0xFFu);
-    int s;
-    if (biased == 0) {
-        s = -127;                                   // below 2^-126: clamps
-    } else {
-        const int e = biased - 127;
-        s = (bits & 0x400000u) ? e - 2 : e - 3;     // f >= 1.5 iff the top significand bit is set
-    }
-    return s < -127 ? -127 : (s > 127 ? 127 : s);
-}
-
-// Two floats -> one byte of two E2M1 codes: `lo` in bits 0-3, `hi` in 4-7.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("{\n\t.reg .b8 t;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\t"
-        "cvt.u32.u8 %0, t;\n\t}"
-        : "=r"(r)
-        : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_kernel(uint8_t *__restrict__ Q, int64_t ldq_bytes, uint8_t *__restrict__ S,
@@ -87,9 +54,7 @@ __global__ void __launch_bounds__(kQuantThreads)
         for (int i = 0; i < 16; ++i)
             amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
         const int s = block_exponent(amax);
-        // 2^-s as a float (s in [-127, 127]: 2^127 is normal, 2^-127 subnormal)
-        const float inv = s == 127 ? __uint_as_float(0x00400000u)
-                                   : __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+        const float inv = exp2_neg(s);
         uint32_t out[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -116,37 +81,6 @@ __global__ void __launch_bounds__(kQuantThreads)
 // converted with cvt.rn.satfinite (nearest, ties to even, saturating at the
 // largest finite value).  One thread per block; its 32 codes leave in two
 // 16-byte stores.
-
-// floor(log2 amax) - emax from amax's float exponent (a subnormal amax is
-// below 2^-126 and clamps).
-__device__ __forceinline__ int block_exponent8(float amax, int emax)
-{
-    if (amax == 0.0f)
-        return 0;
-    const int biased = static_cast<int>((__float_as_uint(amax) >> 23) & 0xFFu);
-    const int s = biased == 0 ? -127 : biased - 127 - emax;
-    return s < -127 ? -127 : (s > 127 ? 127 : s);
-}
-
-// Two floats -> two 8-bit codes: `lo` in bits 0-7, `hi` in bits 8-15.
-template <int FMT>
-__device__ __forceinline__ uint32_t f8x2(float lo, float hi)
-{
-    uint32_t r;
-    if constexpr (FMT == 0)
-        asm("{\n\t.reg .b16 t;\n\t"
-            "cvt.rn.satfinite.e4m3x2.f32 t, %1, %2;\n\t"
-            "cvt.u32.u16 %0, t;\n\t}"
-            : "=r"(r)
-            : "f"(hi), "f"(lo));
-    else
-        asm("{\n\t.reg .b16 t;\n\t"
-            "cvt.rn.satfinite.e5m2x2.f32 t, %1, %2;\n\t"
-            "cvt.u32.u16 %0, t;\n\t}"
-            : "=r"(r)
-            : "f"(hi), "f"(lo));
-    return r;
-}
 
 // Two floats -> two 6-bit codes: `lo` in bits 0-5, `hi` in bits 8-13
 // (FMT 3: E2M3, 4: E3M2).
@@ -211,8 +145,7 @@ __global__ void __launch_bounds__(kQuantThreads)
         for (int i = 0; i < 16; ++i)
             amax = fmaxf(amax, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
         const int s = block_exponent8(amax, kEmax);
-        const float inv = s == 127 ? __uint_as_float(0x00400000u)
-                                   : __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
+        const float inv = exp2_neg(s);
         uint4 *dst = reinterpret_cast<uint4 *>(Q + r * ldq + b * 32);
         if constexpr (FMT <= 1) {
             uint32_t out[8];
