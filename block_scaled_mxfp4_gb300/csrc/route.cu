@@ -682,8 +682,8 @@ cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream)
 {
     if (a.T == 0)
         return launch_dependent(route_empty_kernel, dim3(1), dim3(256), 0, stream, a.offsets, a.E);
-    // Lanes per token: as many as let the block's warps do its tokens (of a run
-    // of 128) in one pass, which has the latency, and at least as many as hold
+    // Lanes per token: as many as let the block's warps do its tokens (128 of
+    // them, if a block has more) in one pass, which has the latency, and at least as many as hold
     // the experts in 32 registers each.  32768 tokens: 64 experts 14.6 us, with
     // the fewest lanes 22; 8 experts 10.8 against 37.  5000 tokens of 256 experts:
     // 11.8 us, with the fewest lanes 12.7, with a warp per token 14.4.  A warp per

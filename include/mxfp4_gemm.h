@@ -430,7 +430,8 @@ int mxfp8_quantize(void *Q, int64_t ldq, void *S, int64_t lds, const void *X, in
  * device memory) is the only description of the groups that the grouped
  * entry points take, so no size travels to the host; groups may be empty, and
  * the total offsets[groups] may be below `rows`, the capacity of the row
- * arrays: rows past it are neither read nor written.  Offsets must ascend
+ * arrays: rows past it are not written, and nothing comes of what they hold (a
+ * tile that the last group does not fill may read them).  Offsets must ascend
  * from 0; out of that order they give unspecified results, but no access
  * outside the arrays.
  *
@@ -510,7 +511,9 @@ int mxfp8_group_quantize(void *Q, int64_t ldq, void *S, const void *X, int64_t l
 
 /*
  * Grouped product: D[r, n] = alpha * sum_k A[r, k] * B[e, n, k] for every row
- * r of group e, accumulated in fp32 and rounded once to bf16.
+ * r of group e, accumulated in the tensor core's fp32 accumulators (whose sums of
+ * a few products at a time are not rounded like single fp32 additions: within
+ * 2^-20 of the sum of magnitudes) and rounded once to bf16.
  *   A    codes [rows, lda], SA its grouped scale layout
  *   B    weights as above, ldb >= K, stride_b >= N * ldb, SB relaid
  *   D    bf16 [rows, ldd], ldd >= N
@@ -534,7 +537,12 @@ int mxfp8_grouped_gemm(void *D, int64_t ldd, const void *A, int64_t lda, const v
  * Gated grouped product, quantised for the next one:
  *   g = alpha * A . Bgate^T, u = alpha * A . Bup^T (fp32),
  *   H = quantise(g / (1 + exp(-g)) * u) in 1x32 blocks along F,
- * by the rules of the grouped quantiser.  Nothing is rounded in between.
+ * by the rules of the grouped quantiser.  Nothing is rounded to fewer bits in
+ * between.  The exponential and the reciprocal are the hardware's approximations
+ * (some units in the last place); gates below -87, whose sigmoid is under the
+ * smallest normal number, give 0.  The products' accumulation can move a code
+ * or a block's scale by one step where the exact value lies beside a rounding's
+ * edge.
  *   B    [groups][2][F, K] (gate rows, up rows), stride_b >= 2 * F * ldb
  *   H    codes [rows, ldh]: packed E2M1 (ldh % 32 == 0), or of fmt_h, one per
  *        byte (MXFP8_E4M3 or MXFP8_E5M2; ldh % 16 == 0); 16-byte aligned
@@ -581,6 +589,10 @@ int mxfp4_moe_combine(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *
  *   B1 [E][2][F, K] rows of ldb1 elements, B2 [E][K, F] rows of ldb2, without
  *   gaps between matrices; SB1, SB2 their relaid scales; the rest as for
  *   mxfp4_moe_combine with N = K.
+ * X and the hidden rows are rounded by mxfp4_quantize's rule, which saturates a
+ * block's values above 6 * 2^s.  Nrm may alias X, H resid.  The steps after the
+ * first start before the one ahead has ended; the wait limit counts their own
+ * work alone.
  * workspace: mxfp4_moe_ffn_workspace_size(T, E, k, K, F) bytes, 256-byte aligned.
  */
 int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, int64_t ldx,
@@ -591,7 +603,8 @@ int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, i
                   void *workspace, size_t workspace_bytes, void *stream);
 size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F);
 
-/* Set the in-kernel wait limit in SM clock cycles (default 2^32, ~2 s). */
+/* Set the in-kernel wait limit in SM clock cycles (default 2^32, ~2 s).  It
+ * bounds waits inside a kernel, not the wait for the work before it. */
 void mxfp4_set_wait_limit(long long cycles);
 
 /* Human-readable name of a status code (never NULL). */
