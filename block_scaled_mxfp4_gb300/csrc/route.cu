@@ -36,7 +36,9 @@ constexpr int kRunWords = kRouteRun / 32;
 // Tokens that one block does alone, without a workspace (64 tokens of 128 experts:
 // 7.5 us in one launch and in two).
 constexpr int kRouteSingle = 64;
-constexpr int kRouteMaxBlocks = 152;             // a block per SM
+// A block per SM of the board that this is for (a constant: the workspace's size is
+// asked for without a device).
+constexpr int kRouteMaxBlocks = 152;
 // Shared memory of the placing kernel at most: two partial counts per thread's
 // eight experts, their sums.
 constexpr int kPlaceSmem = (2 * kRouteThreads * 8 + 2 * kMaxGroups) * 4;
