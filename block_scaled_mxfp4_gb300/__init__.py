@@ -630,10 +630,10 @@ def moe_block(x, logits, resid, w1, s1, w2, s2, k, w_pre=None, w_post=None, toke
     ld = lambda t: t.stride(0) if T > 1 else t.shape[1]    # (a lone row's stride can be anything)
     made = []
     with _on_stream(stream, [x, logits, resid, w1, s1, w2, s2, w_pre, w_post, token_mask], made):
-        i32 = dict(dtype=torch.int32, device=x.device)
-        ids, slot_row = torch.empty((T, k), **i32), torch.empty((T, k), **i32)
-        offsets, row_token = torch.empty(E + 1, **i32), torch.empty(T * k, **i32)
-        gates = torch.empty((T, k), dtype=torch.float32, device=x.device)
+        # ids, gates, row_token and slot_row [T, k] of 4 bytes, offsets [E + 1]: one array.
+        tables = torch.empty(4 * T * k + E + 1, dtype=torch.int32, device=x.device)
+        ids, gates, row_token, slot_row, offsets = (tables.data_ptr() + 4 * T * k * i
+                                                    for i in range(5))
         h = torch.empty((T, K), dtype=torch.bfloat16, device=x.device)
         n = torch.empty_like(h)
         made += [h, n]
