@@ -37,6 +37,10 @@ __all__ = [
     "mxfp4_moe_combine", "mxfp4_moe_ffn", "mxfp4_moe_ffn_workspace_size",
     "MXFP4_LOGITS_BF16", "MXFP4_LOGITS_FP32", "MXFP4_GATE_TOPK", "MXFP4_GATE_ALL",
     "MXFP4_GATE_SIGMOID", "relaid_expert_scales", "moe_block",
+    "mxfp4_gemm_act", "mxfp8_gemm_act", "mxfp8_checkpoint", "mxfp8_checkpoint_workspace_size",
+    "mxfp8_act_backward", "mxfp4_layer_norm", "mxfp4_layer_norm_backward",
+    "mxfp4_layer_norm_workspace_size", "MXFP4_ACT_NONE", "MXFP4_ACT_RELU", "MXFP4_ACT_GELU",
+    "MXFP4_ACT_GELU_TANH", "MXFP4_ACT_SILU", "MXFP4_PARAM_BF16", "MXFP4_PARAM_FP32",
     "gemm", "Plan",
 ]
 
@@ -50,6 +54,8 @@ MXFP4_FLAG_B_STATIC = 1
 MXFP8_E4M3, MXFP8_E5M2, MXFP6_E2M3, MXFP6_E3M2, MXFP4_E2M1_PADDED = 0, 1, 3, 4, 5
 MXFP4_LOGITS_BF16, MXFP4_LOGITS_FP32 = 0, 1
 MXFP4_GATE_TOPK, MXFP4_GATE_ALL, MXFP4_GATE_SIGMOID = 0, 1, 2
+MXFP4_ACT_NONE, MXFP4_ACT_RELU, MXFP4_ACT_GELU, MXFP4_ACT_GELU_TANH, MXFP4_ACT_SILU = range(5)
+MXFP4_PARAM_BF16, MXFP4_PARAM_FP32 = 0, 1
 STATUS_NAMES = {0: "MXFP4_OK", -1: "MXFP4_ERR_INVALID_ARG", -2: "MXFP4_ERR_UNSUPPORTED_SHAPE",
                 -3: "MXFP4_ERR_MISALIGNED", -4: "MXFP4_ERR_WORKSPACE", -5: "MXFP4_ERR_CUDA",
                 -6: "MXFP4_ERR_TIMEOUT", -7: "MXFP4_ERR_ARCH"}
@@ -147,6 +153,19 @@ def lib() -> ctypes.CDLL:
                                     i32, vp, i64, vp, vp, i64, vp, vp, i64, vp, vp, f32, f32, f32,
                                     vp, sz, vp]),
             "mxfp4_moe_ffn_workspace_size": (sz, [i32, i32, i32, i32, i32]),
+            "mxfp4_gemm_act": (i32, [vp, i64] * 9 + [i32, f32, vp, i32, i32, vp, i64, f32, i32, i32,
+                                                     i32, i32, ctypes.c_uint, vp, sz, vp]),
+            "mxfp8_gemm_act": (i32, [vp, i64] * 9 + [i32, i32, i32, i32, f32, vp, i32, i32, vp, i64,
+                                                     f32, i32, i32, i32, i32, ctypes.c_uint, vp, sz,
+                                                     vp]),
+            "mxfp8_checkpoint": (i32, [vp, i64] * 4 + [vp, vp, i64, i32, i32, i32, vp, sz, vp]),
+            "mxfp8_checkpoint_workspace_size": (sz, [i32, i32]),
+            "mxfp8_act_backward": (i32, [vp, i64] * 7 + [vp] + [vp, i64] * 3 +
+                                   [i32, i32, i32, i32, i32, i32, vp, sz, vp]),
+            "mxfp4_layer_norm": (i32, [vp, i64, vp, vp, vp, i64, vp, vp, i32, f32, i32, i32, vp]),
+            "mxfp4_layer_norm_backward": (i32, [vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, vp, i32,
+                                                vp, i64, i32, i32, vp, sz, vp]),
+            "mxfp4_layer_norm_workspace_size": (sz, [i32, i32]),
             "mxfp4_device_status": (i32, [ctypes.POINTER(ctypes.c_int), i32]),
             "mxfp4_wait_timeout_probe": (i32, [ctypes.c_longlong, vp]),
             "mxfp4_set_wait_limit": (None, [ctypes.c_longlong]),
@@ -516,6 +535,74 @@ def mxfp4_moe_ffn(H, ldh, Nrm, ldn, X, ldx, ids, gates, offsets, slot_row, T, E,
                                       _p(SB1), _p(B2), ldb2, _p(SB2), _p(resid), ldr, _p(w_post),
                                       _p(w_pre), res_scale, out_scale, eps, _p(workspace),
                                       workspace_bytes, _stream(stream)), "mxfp4_moe_ffn")
+
+
+def mxfp4_gemm_act(D, ldd, H, ldh, SH, ld_sh, Z, ldz, SZ, ld_sz, A, lda, B, ldb, scaleA, ld_sa,
+                   scaleB, ld_sb, fmt_z, alpha, bias, bias_type, act, R, ldr, res_scale, M, N, K,
+                   split_k, flags, workspace, workspace_bytes, stream=None):
+    """z = alpha * A . B^T + bias kept in 8 bits, act(z) + res_scale * R as bf16 and packed E2M1."""
+    return _check(lib().mxfp4_gemm_act(_p(D), ldd, _p(H), ldh, _p(SH), ld_sh, _p(Z), ldz, _p(SZ),
+                                       ld_sz, _p(A), lda, _p(B), ldb, _p(scaleA), ld_sa,
+                                       _p(scaleB), ld_sb, fmt_z, alpha, _p(bias), bias_type, act,
+                                       _p(R), ldr, res_scale, M, N, K, split_k, flags,
+                                       _p(workspace), workspace_bytes, _stream(stream)),
+                  "mxfp4_gemm_act")
+
+
+def mxfp8_gemm_act(D, ldd, H, ldh, SH, ld_sh, Z, ldz, SZ, ld_sz, A, lda, B, ldb, scaleA, ld_sa,
+                   scaleB, ld_sb, fmt_a, fmt_b, fmt_h, fmt_z, alpha, bias, bias_type, act, R, ldr,
+                   res_scale, M, N, K, split_k, flags, workspace, workspace_bytes, stream=None):
+    """mxfp4_gemm_act on the byte formats of mxfp8_gemm, into E4M3 / E5M2 codes."""
+    return _check(lib().mxfp8_gemm_act(_p(D), ldd, _p(H), ldh, _p(SH), ld_sh, _p(Z), ldz, _p(SZ),
+                                       ld_sz, _p(A), lda, _p(B), ldb, _p(scaleA), ld_sa,
+                                       _p(scaleB), ld_sb, fmt_a, fmt_b, fmt_h, fmt_z, alpha,
+                                       _p(bias), bias_type, act, _p(R), ldr, res_scale, M, N, K,
+                                       split_k, flags, _p(workspace), workspace_bytes,
+                                       _stream(stream)), "mxfp8_gemm_act")
+
+
+def mxfp8_checkpoint(Q, ldq, S, lds, QT, ldqt, ST, ldst, col_sums, X, ldx, rows, cols, fmt,
+                     workspace, workspace_bytes, stream=None):
+    """bf16 rows -> MXFP8 blocks along the rows and along the columns, and the column sums."""
+    return _check(lib().mxfp8_checkpoint(_p(Q), ldq, _p(S), lds, _p(QT), ldqt, _p(ST), ldst,
+                                         _p(col_sums), _p(X), ldx, rows, cols, fmt, _p(workspace),
+                                         workspace_bytes, _stream(stream)), "mxfp8_checkpoint")
+
+
+def mxfp8_checkpoint_workspace_size(rows, cols) -> int:
+    return lib().mxfp8_checkpoint_workspace_size(rows, cols)
+
+
+def mxfp8_act_backward(dZ, lddz, Q, ldq, S, lds, QT, ldqt, ST, ldst, HT, ldht, SHT, ld_sht, dbias,
+                       dH, lddh, Z, ldz, SZ, ld_sz, fmt_z, act, rows, cols, fmt, fmt_h, workspace,
+                       workspace_bytes, stream=None):
+    """dz = dH * act'(z) from an 8-bit z in both orientations, its column sums, and act(z)^T."""
+    return _check(lib().mxfp8_act_backward(_p(dZ), lddz, _p(Q), ldq, _p(S), lds, _p(QT), ldqt,
+                                           _p(ST), ldst, _p(HT), ldht, _p(SHT), ld_sht, _p(dbias),
+                                           _p(dH), lddh, _p(Z), ldz, _p(SZ), ld_sz, fmt_z, act,
+                                           rows, cols, fmt, fmt_h, _p(workspace), workspace_bytes,
+                                           _stream(stream)), "mxfp8_act_backward")
+
+
+def mxfp4_layer_norm(Y, ldy, mean, rstd, X, ldx, w, b, param_type, eps, T, N, stream=None):
+    """Layer norm of bf16 rows, and the rows' statistics."""
+    return _check(lib().mxfp4_layer_norm(_p(Y), ldy, _p(mean), _p(rstd), _p(X), ldx, _p(w), _p(b),
+                                         param_type, eps, T, N, _stream(stream)),
+                  "mxfp4_layer_norm")
+
+
+def mxfp4_layer_norm_backward(dX, lddx, dw, db, dY, lddy, X, ldx, mean, rstd, w, param_type, dres,
+                              ldr, T, N, workspace, workspace_bytes, stream=None):
+    """Layer norm's gradients: dx plus the residual stream's, dw, db."""
+    return _check(lib().mxfp4_layer_norm_backward(_p(dX), lddx, _p(dw), _p(db), _p(dY), lddy, _p(X),
+                                                  ldx, _p(mean), _p(rstd), _p(w), param_type,
+                                                  _p(dres), ldr, T, N, _p(workspace),
+                                                  workspace_bytes, _stream(stream)),
+                  "mxfp4_layer_norm_backward")
+
+
+def mxfp4_layer_norm_workspace_size(T, N) -> int:
+    return lib().mxfp4_layer_norm_workspace_size(T, N)
 
 
 def _on_stream(stream, inputs, outputs):

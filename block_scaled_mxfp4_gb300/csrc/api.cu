@@ -375,12 +375,13 @@ uint32_t next_epoch()
 }
 
 // ws: workspace base (split-K counters and partials), or nullptr when the
-// plan needs none.  flags: MXFP4_FLAG_* of the call.
+// plan needs none.  flags: MXFP4_FLAG_* of the call.  epi: the arguments beyond
+// GemmArgs of a product with bias, activation and residual.
 int run_gemm(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A, int64_t lda,
              const void *B, int64_t ldb, const Scales &sc, float alpha, float beta, int M, int N,
              int K, const mxfp4_plan &plan, const GemmShape &shape, uint8_t *ws,
              cudaStream_t stream, bool after_relayout = false, int fmt_a = 0, int fmt_b = 0,
-             unsigned flags = 0, bool nv = false)
+             unsigned flags = 0, bool nv = false, const ActGemmArgs *epi = nullptr)
 {
     if (shape.pair) {
         if (sc.rowmajor)
@@ -412,10 +413,15 @@ int run_gemm(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A, in
         a.ab_early = after_relayout ? 1 : 0;
         a.wait_limit = g_wait_limit.load();
         const int tiles_p = (M + 255) / 256, tiles_q = (N + 255) / 256;
-        if (launch_gemm_pair(a, tiles_p, tiles_q, shape.pair_ctas, tmA, tmB, tmSA, tmSB, nv,
-                             stream) != cudaSuccess)
-            return MXFP4_ERR_CUDA;
-        return MXFP4_OK;
+        cudaError_t e;
+        if (epi) {
+            ActGemmArgs x = *epi;
+            static_cast<GemmArgs &>(x) = a;
+            e = launch_gemm_act_pair(x, tiles_p, tiles_q, shape.pair_ctas, tmA, tmB, tmSA, tmSB, stream);
+        } else {
+            e = launch_gemm_pair(a, tiles_p, tiles_q, shape.pair_ctas, tmA, tmB, tmSA, tmSB, nv, stream);
+        }
+        return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
     }
     const bool swap = shape.swap != 0;
     CUtensorMap tmP, tmQ;
@@ -494,9 +500,15 @@ int run_gemm(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A, in
     a.wait_limit = g_wait_limit.load();
 
     dim3 grid(plan.grid_x, plan.grid_y, plan.grid_z);
-    if (launch_gemm(a, tmP, tmQ, tmSP, tmSQ, shape, grid, stream) != cudaSuccess)
-        return MXFP4_ERR_CUDA;
-    return MXFP4_OK;
+    cudaError_t e;
+    if (epi) {
+        ActGemmArgs x = *epi;
+        static_cast<GemmArgs &>(x) = a;
+        e = launch_gemm_act(x, tmP, tmQ, tmSP, tmSQ, shape, grid, stream);
+    } else {
+        e = launch_gemm(a, tmP, tmQ, tmSP, tmSQ, shape, grid, stream);
+    }
+    return e == cudaSuccess ? MXFP4_OK : MXFP4_ERR_CUDA;
 }
 
 }  // namespace
@@ -670,12 +682,15 @@ static int gemm_rowmajor(void *D, int64_t ldd, const void *C, int64_t ldc, const
                          int64_t lda, const void *B, int64_t ldb, const void *scaleA,
                          int64_t ld_sa, const void *scaleB, int64_t ld_sb, float alpha, float beta,
                          int M, int N, int K, int split_k, void *workspace, size_t workspace_bytes,
-                         void *stream, bool fp8, int fmt_a, int fmt_b, unsigned flags = 0)
+                         void *stream, bool fp8, int fmt_a, int fmt_b, unsigned flags = 0,
+                         const ActGemmArgs *epi = nullptr)
 {
     const int kx = fp8 ? 2 : 1;
     if (fp8 && (K > (1 << 29) || lda > (INT64_MAX / 4) || ldb > (INT64_MAX / 4)))
         return MXFP4_ERR_INVALID_ARG;
-    int st = check_common(D, ldd, C, ldc, A, lda * kx, B, ldb * kx, beta, M, N, K * kx, split_k);
+    const bool no_d = epi && !D;                     // other outputs are wanted instead
+    int st = check_common(no_d ? A : D, no_d ? N : ldd, C, ldc, A, lda * kx, B, ldb * kx, beta, M, N,
+                          K * kx, split_k);
     if (st != MXFP4_OK)
         return st;
     if (K < 32 || (K % 32) != 0)
@@ -715,7 +730,80 @@ static int gemm_rowmajor(void *D, int64_t ldd, const void *C, int64_t ldc, const
     }
     return run_gemm(D, ldd, C, ldc, A, lda, B, ldb, sc, alpha, beta, M, N, K, plan, shape,
                     plan.workspace_bytes ? ws : nullptr, s, plan.relayout_pass != 0, fmt_a,
-                    fmt_b, flags);
+                    fmt_b, flags, false, epi);
+}
+
+// Codes of a product's epilogue: null, or rows of whole blocks on 16-byte
+// boundaries and their scales.  packed: E2M1, strides in elements.
+static int check_act_codes(const void *q, int64_t ldq, const void *s, int64_t lds, int N, bool packed, int fmt)
+{
+    if (!q)
+        return s ? MXFP4_ERR_INVALID_ARG : MXFP4_OK;
+    const int64_t whole = (static_cast<int64_t>(N) + 31) / 32 * 32;
+    if (!s || ldq < whole || lds < whole / 32 || (!packed && fmt != MXFP8_E4M3 && fmt != MXFP8_E5M2))
+        return MXFP4_ERR_INVALID_ARG;
+    return !aligned(q, 16) || (ldq % (packed ? 32 : 16)) != 0 ? MXFP4_ERR_MISALIGNED : MXFP4_OK;
+}
+
+// mxfp4_gemm_act and mxfp8_gemm_act.
+static int gemm_act(void *D, int64_t ldd, void *H, int64_t ldh, void *SH, int64_t ld_sh, void *Z, int64_t ldz,
+                    void *SZ, int64_t ld_sz, const void *A, int64_t lda, const void *B, int64_t ldb,
+                    const void *scaleA, int64_t ld_sa, const void *scaleB, int64_t ld_sb, int fmt_a, int fmt_b,
+                    int fmt_h, int fmt_z, float alpha, const void *bias, int bias_type, int act, const void *R,
+                    int64_t ldr, float res_scale, int M, int N, int K, int split_k, unsigned flags,
+                    void *workspace, size_t workspace_bytes, void *stream, bool fp8)
+{
+    if ((!D && !H && !Z) || N < 1 || (H && (N % 32) != 0) || act < MXFP4_ACT_NONE || act > MXFP4_ACT_SILU ||
+        (bias_type != MXFP4_PARAM_BF16 && bias_type != MXFP4_PARAM_FP32) || (R && ldr < N) ||
+        (flags & ~static_cast<unsigned>(MXFP4_FLAG_B_STATIC)) != 0)
+        return MXFP4_ERR_INVALID_ARG;
+    int st = check_act_codes(H, ldh, SH, ld_sh, N, !fp8, fmt_h);
+    if (st == MXFP4_OK)
+        st = check_act_codes(Z, ldz, SZ, ld_sz, N, false, fmt_z);
+    if (st != MXFP4_OK)
+        return st;
+    const bool fp32 = bias_type == MXFP4_PARAM_FP32;
+    if (!aligned(D, 2) || !aligned(R, 2) || !aligned(bias, fp32 ? 4 : 2))
+        return MXFP4_ERR_MISALIGNED;
+    ActGemmArgs e;
+    std::memset(&e, 0, sizeof(e));
+    e.bias = bias;
+    e.bias_fp32 = fp32 ? 1 : 0;
+    e.bias_vec = aligned(bias, 16) ? 1 : 0;
+    e.act = act;
+    e.R = static_cast<const uint16_t *>(R);
+    e.ldr = ldr;
+    e.res_scale = res_scale;
+    e.r_vec = aligned(R, 16) && (ldr % 8) == 0 ? 1 : 0;
+    e.H = ActCodes{static_cast<uint8_t *>(H), fp8 ? ldh : ldh / 2, static_cast<uint8_t *>(SH), ld_sh,
+                   !fp8 ? 2 : fmt_h == MXFP8_E5M2 ? 1 : 0};
+    e.Z = ActCodes{static_cast<uint8_t *>(Z), ldz, static_cast<uint8_t *>(SZ), ld_sz, fmt_z == MXFP8_E5M2 ? 1 : 0};
+    return gemm_rowmajor(D, ldd, nullptr, 0, A, lda, B, ldb, scaleA, ld_sa, scaleB, ld_sb, alpha, 0.0f, M, N, K,
+                         split_k, workspace, workspace_bytes, stream, fp8, fmt_a, fmt_b, flags, &e);
+}
+
+int mxfp4_gemm_act(void *D, int64_t ldd, void *H, int64_t ldh, void *SH, int64_t ld_sh, void *Z, int64_t ldz,
+                   void *SZ, int64_t ld_sz, const void *A, int64_t lda, const void *B, int64_t ldb,
+                   const void *scaleA, int64_t ld_sa, const void *scaleB, int64_t ld_sb, int fmt_z, float alpha,
+                   const void *bias, int bias_type, int act, const void *R, int64_t ldr, float res_scale, int M,
+                   int N, int K, int split_k, unsigned flags, void *workspace, size_t workspace_bytes,
+                   void *stream)
+{
+    return gemm_act(D, ldd, H, ldh, SH, ld_sh, Z, ldz, SZ, ld_sz, A, lda, B, ldb, scaleA, ld_sa, scaleB, ld_sb, 0,
+                    0, 0, fmt_z, alpha, bias, bias_type, act, R, ldr, res_scale, M, N, K, split_k, flags,
+                    workspace, workspace_bytes, stream, false);
+}
+
+int mxfp8_gemm_act(void *D, int64_t ldd, void *H, int64_t ldh, void *SH, int64_t ld_sh, void *Z, int64_t ldz,
+                   void *SZ, int64_t ld_sz, const void *A, int64_t lda, const void *B, int64_t ldb,
+                   const void *scaleA, int64_t ld_sa, const void *scaleB, int64_t ld_sb, int fmt_a, int fmt_b,
+                   int fmt_h, int fmt_z, float alpha, const void *bias, int bias_type, int act, const void *R,
+                   int64_t ldr, float res_scale, int M, int N, int K, int split_k, unsigned flags,
+                   void *workspace, size_t workspace_bytes, void *stream)
+{
+    return gemm_act(D, ldd, H, ldh, SH, ld_sh, Z, ldz, SZ, ld_sz, A, lda, B, ldb, scaleA, ld_sa, scaleB, ld_sb,
+                    fmt_a, fmt_b, fmt_h, fmt_z, alpha, bias, bias_type, act, R, ldr, res_scale, M, N, K, split_k,
+                    flags, workspace, workspace_bytes, stream, true);
 }
 
 int mxfp4_gemm(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A, int64_t lda,

@@ -1,4 +1,4 @@
-// Fast path of the Python binding for the calls of a decoding step, where the
+// Fast path of the Python binding for the calls of a decoding or training step, where the
 // time to marshal a call's arguments in Python (3 us on the host of a GB300)
 // is a good part of the call.  The module holds no arithmetic and links
 // nothing: each function takes the arguments of the C entry of its name (device
@@ -19,6 +19,7 @@ static PyObject *g_raise;           // (status, name): raises
 typedef void *ptr;
 typedef int64_t i64;
 typedef int i32;
+typedef unsigned u32;
 typedef float f32;
 typedef size_t size;
 
@@ -65,6 +66,16 @@ static i32 as_i32(PyObject *o, int *bad)
         *bad = 1;
     }
     return (int)v;
+}
+
+static u32 as_u32(PyObject *o, int *bad)
+{
+    const i64 v = as_i64(o, bad);
+    if (!*bad && (v < 0 || v > UINT32_MAX)) {
+        PyErr_SetString(PyExc_OverflowError, "argument does not fit an unsigned C int");
+        *bad = 1;
+    }
+    return (u32)v;
 }
 
 static size as_size(PyObject *o, int *bad)
@@ -209,6 +220,52 @@ static PyObject *finish(int status, const char *name)
 #define DOC_mxfp4_moe_ffn \
     "A routed feed-forward block on MXFP4 weights: quantise, both products, join."
 
+#define ARGS_mxfp4_gemm_act(ARG) \
+    ARG(ptr, D) ARG(i64, ldd) ARG(ptr, H) ARG(i64, ldh) ARG(ptr, SH) ARG(i64, ld_sh) ARG(ptr, Z) ARG(i64, ldz) \
+    ARG(ptr, SZ) ARG(i64, ld_sz) ARG(ptr, A) ARG(i64, lda) ARG(ptr, B) ARG(i64, ldb) ARG(ptr, scaleA) ARG(i64, ld_sa) \
+    ARG(ptr, scaleB) ARG(i64, ld_sb) ARG(i32, fmt_z) ARG(f32, alpha) ARG(ptr, bias) ARG(i32, bias_type) ARG(i32, act) \
+    ARG(ptr, R) ARG(i64, ldr) ARG(f32, res_scale) ARG(i32, M) ARG(i32, N) ARG(i32, K) ARG(i32, split_k) \
+    ARG(u32, flags) ARG(ptr, workspace) ARG(size, workspace_bytes)
+#define DOC_mxfp4_gemm_act \
+    "z = alpha * A . B^T + bias kept in 8 bits, act(z) + res_scale * R as bf16 and packed E2M1."
+
+#define ARGS_mxfp8_gemm_act(ARG) \
+    ARG(ptr, D) ARG(i64, ldd) ARG(ptr, H) ARG(i64, ldh) ARG(ptr, SH) ARG(i64, ld_sh) ARG(ptr, Z) ARG(i64, ldz) \
+    ARG(ptr, SZ) ARG(i64, ld_sz) ARG(ptr, A) ARG(i64, lda) ARG(ptr, B) ARG(i64, ldb) ARG(ptr, scaleA) ARG(i64, ld_sa) \
+    ARG(ptr, scaleB) ARG(i64, ld_sb) ARG(i32, fmt_a) ARG(i32, fmt_b) ARG(i32, fmt_h) ARG(i32, fmt_z) ARG(f32, alpha) \
+    ARG(ptr, bias) ARG(i32, bias_type) ARG(i32, act) ARG(ptr, R) ARG(i64, ldr) ARG(f32, res_scale) ARG(i32, M) \
+    ARG(i32, N) ARG(i32, K) ARG(i32, split_k) ARG(u32, flags) ARG(ptr, workspace) ARG(size, workspace_bytes)
+#define DOC_mxfp8_gemm_act \
+    "mxfp4_gemm_act on the byte formats of mxfp8_gemm, into E4M3 / E5M2 codes."
+
+#define ARGS_mxfp8_checkpoint(ARG) \
+    ARG(ptr, Q) ARG(i64, ldq) ARG(ptr, S) ARG(i64, lds) ARG(ptr, QT) ARG(i64, ldqt) ARG(ptr, ST) ARG(i64, ldst) \
+    ARG(ptr, col_sums) ARG(ptr, X) ARG(i64, ldx) ARG(i32, rows) ARG(i32, cols) ARG(i32, fmt) ARG(ptr, workspace) \
+    ARG(size, workspace_bytes)
+#define DOC_mxfp8_checkpoint \
+    "bf16 rows -> MXFP8 blocks along the rows and along the columns, and the column sums."
+
+#define ARGS_mxfp8_act_backward(ARG) \
+    ARG(ptr, dZ) ARG(i64, lddz) ARG(ptr, Q) ARG(i64, ldq) ARG(ptr, S) ARG(i64, lds) ARG(ptr, QT) ARG(i64, ldqt) \
+    ARG(ptr, ST) ARG(i64, ldst) ARG(ptr, HT) ARG(i64, ldht) ARG(ptr, SHT) ARG(i64, ld_sht) ARG(ptr, dbias) \
+    ARG(ptr, dH) ARG(i64, lddh) ARG(ptr, Z) ARG(i64, ldz) ARG(ptr, SZ) ARG(i64, ld_sz) ARG(i32, fmt_z) ARG(i32, act) \
+    ARG(i32, rows) ARG(i32, cols) ARG(i32, fmt) ARG(i32, fmt_h) ARG(ptr, workspace) ARG(size, workspace_bytes)
+#define DOC_mxfp8_act_backward \
+    "dz = dH * act'(z) from an 8-bit z in both orientations, its column sums, and act(z)^T."
+
+#define ARGS_mxfp4_layer_norm(ARG) \
+    ARG(ptr, Y) ARG(i64, ldy) ARG(ptr, mean) ARG(ptr, rstd) ARG(ptr, X) ARG(i64, ldx) ARG(ptr, w) ARG(ptr, b) \
+    ARG(i32, param_type) ARG(f32, eps) ARG(i32, T) ARG(i32, N)
+#define DOC_mxfp4_layer_norm \
+    "Layer norm of bf16 rows, and the rows' statistics."
+
+#define ARGS_mxfp4_layer_norm_backward(ARG) \
+    ARG(ptr, dX) ARG(i64, lddx) ARG(ptr, dw) ARG(ptr, db) ARG(ptr, dY) ARG(i64, lddy) ARG(ptr, X) ARG(i64, ldx) \
+    ARG(ptr, mean) ARG(ptr, rstd) ARG(ptr, w) ARG(i32, param_type) ARG(ptr, dres) ARG(i64, ldr) ARG(i32, T) \
+    ARG(i32, N) ARG(ptr, workspace) ARG(size, workspace_bytes)
+#define DOC_mxfp4_layer_norm_backward \
+    "Layer norm's gradients: dx plus the residual stream's, dw, db."
+
 #define KIND_OF(kind, name) kind,
 #define NAME_OF(kind, name) #name,
 #define SHOWN(kind, name) #name ", "
@@ -247,7 +304,13 @@ static PyObject *finish(int status, const char *name)
     DO(mxfp4_grouped_swiglu)                                                                                       \
     DO(mxfp8_grouped_swiglu)                                                                                       \
     DO(mxfp4_moe_combine)                                                                                          \
-    DO(mxfp4_moe_ffn)
+    DO(mxfp4_moe_ffn)                                                                                              \
+    DO(mxfp4_gemm_act)                                                                                             \
+    DO(mxfp8_gemm_act)                                                                                             \
+    DO(mxfp8_checkpoint)                                                                                           \
+    DO(mxfp8_act_backward)                                                                                         \
+    DO(mxfp4_layer_norm)                                                                                           \
+    DO(mxfp4_layer_norm_backward)
 
 ENTRIES(DEFINE)
 

@@ -1,0 +1,75 @@
+// Internal launchers of the dense layer's operators: checkpoints in 8 bits, the
+// activation's backward pass, layer norm and its gradients.  Arguments are
+// checked in dense_api.cu; the ABI is in include/mxfp4_gemm.h.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace mxfp4 {
+
+// One output of the transposing quantiser: codes (one per byte) and scales, both
+// row-major; codes null: not wanted.
+struct CodesOut {
+    uint8_t *q;
+    int64_t ldq;
+    uint8_t *s;
+    int64_t lds;
+    int fmt;                    // 0: E4M3, 1: E5M2
+};
+
+struct CheckpointArgs {
+    CodesOut by_row;            // [rows, cols], blocks along the row
+    CodesOut by_col;            // [cols, rows], blocks along the column
+    CodesOut act_by_col;        // backward: act(z), [cols, rows]
+    uint16_t *dz;               // backward: bf16 [rows, lddz] or null
+    int64_t lddz;
+    float *sums;                // [cols] or null
+    float *partials;            // [strips][cols], where strips > 1 and sums
+    const uint16_t *x;          // bf16 [rows, ldx]: the rows, or dh
+    int64_t ldx;
+    const uint8_t *z, *sz;      // backward: 8-bit checkpoint of z
+    int64_t ldz, ld_sz;
+    int fmt_z;
+    int rows, cols;
+    int strips;                 // row strips, one block each per column tile
+    int act;
+    int vec_dz;                 // dz's rows allow 16-byte stores
+};
+// Row strips of a call: by its sizes alone, so that the sums' order is too.
+int checkpoint_strips(int rows, int cols, bool backward);
+cudaError_t launch_checkpoint(const CheckpointArgs &a, bool backward, cudaStream_t stream);
+
+// a[c] and b[c]: sums over the strips of partials[strip][na + nb], in a fixed order; zeros for
+// no strips.  Either array may be null.
+cudaError_t launch_sum_partials(float *a, int64_t na, float *b, int64_t nb, const float *partials, int strips, cudaStream_t stream);
+
+struct NormArgs {
+    const uint16_t *x;          // bf16 [T, ldx]
+    int64_t ldx;
+    const void *w, *b;          // [N] or null, bf16 or fp32
+    int fp32;                   // type of w and b
+    uint16_t *y;                // forward: bf16 [T, ldy]
+    int64_t ldy;
+    float *mean, *rstd;         // forward: [T] or null; backward: inputs
+    float eps;
+    const uint16_t *dy;         // backward
+    int64_t lddy;
+    const uint16_t *dres;       // backward: [T, ldr] or null
+    int64_t ldr;
+    uint16_t *dx;               // backward
+    int64_t lddx;
+    float *dw, *db;             // backward: [N], either may be null
+    float *partials;            // backward: [blocks][2][N]
+    int blocks;                 // backward: blocks that share the rows
+    int T, N;
+    int width;                  // elements of the widest access that every row allows: 8, 4, 2, 1
+};
+cudaError_t launch_layer_norm(const NormArgs &a, int sms, cudaStream_t stream);
+int norm_backward_blocks(int T, int N);
+cudaError_t launch_layer_norm_backward(const NormArgs &a, cudaStream_t stream);
+
+}  // namespace mxfp4

@@ -1,0 +1,351 @@
+// Epilogue of the products with bias, activation and residual (included by
+// gemm_sm103.cu).
+//
+//   z = alpha * acc + bias[n]                       -> Z, 1x32 blocks along n
+//   d = act(z) + res_scale * R[m, n]                -> D (bf16), H (1x32 blocks along n)
+//
+// in fp32, each output rounded once.  A block of 32 columns is a thread's
+// (row-wise forms), eight neighbouring lanes' (cluster reduction), or a warp's
+// (swapped forms, where a lane holds one n).  The activation is a uniform
+// branch on its code, around 32 values at a time: one kernel per tile shape
+// and not five.
+#pragma once
+
+#include "act.cuh"
+#include "quant.cuh"
+
+namespace mxfp4 {
+
+template <int N>
+__device__ __forceinline__ void act_apply(int act, float (&v)[N])
+{
+    auto each = [&](auto tag) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = act_value<decltype(tag)::value>(v[i]);
+    };
+    switch (act) {
+    case 1: each(ActTag<Act::kRelu>{}); break;
+    case 2: each(ActTag<Act::kGelu>{}); break;
+    case 3: each(ActTag<Act::kGeluTanh>{}); break;
+    case 4: each(ActTag<Act::kSilu>{}); break;
+    default: break;
+    }
+}
+
+__device__ __forceinline__ float act_bias(const ActGemmArgs &a, int n)
+{
+    return a.bias_fp32 ? __ldg(static_cast<const float *>(a.bias) + n)
+                       : bf16_bits_to_float(__ldg(static_cast<const uint16_t *>(a.bias) + n));
+}
+
+// bias[n0 .. n0 + 31], zeros past N and for no bias.
+__device__ __forceinline__ void act_bias_chunk(const ActGemmArgs &a, int n0, float (&b)[32])
+{
+    if (a.bias && a.bias_vec && n0 + 32 <= a.N) {
+        if (a.bias_fp32) {
+            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.bias) + n0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float4 v = __ldg(p + i);
+                b[4 * i] = v.x;
+                b[4 * i + 1] = v.y;
+                b[4 * i + 2] = v.z;
+                b[4 * i + 3] = v.w;
+            }
+        } else {
+            const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.bias) + n0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = __ldg(p + i);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    b[8 * i + 2 * j] = bf16_lo(w[j]);
+                    b[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            b[i] = a.bias && n0 + i < a.N ? act_bias(a, n0 + i) : 0.0f;
+    }
+}
+
+// One block in a thread: codes and scale of row m, columns n0 ..+31.
+template <QuantFmt Q>
+__device__ __forceinline__ void act_put_block(const ActCodes &o, int m, int n0, const float (&v)[32])
+{
+    constexpr int W = QuantTraits<Q>::kWords;
+    uint32_t w[W];
+    const uint32_t code = quantize_block<Q>(v, w);
+    uint4 *q = reinterpret_cast<uint4 *>(o.q + m * o.ldq + (Q == QuantFmt::kE2M1 ? n0 / 2 : n0));
+    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (W == 8)
+        q[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    o.s[m * o.lds + n0 / 32] = static_cast<uint8_t>(code);
+}
+
+__device__ __forceinline__ void act_put_codes(const ActCodes &o, int m, int n0, const float (&v)[32])
+{
+    if (o.fmt == 0)
+        act_put_block<QuantFmt::kE4M3>(o, m, n0, v);
+    else if (o.fmt == 1)
+        act_put_block<QuantFmt::kE5M2>(o, m, n0, v);
+    else
+        act_put_block<QuantFmt::kE2M1>(o, m, n0, v);
+}
+
+// Row m < M, columns n0 .. n0 + 31 (n0 < N): v holds the accumulators.
+__device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m, int n0, float (&v)[32])
+{
+    {
+        float b[32];
+        act_bias_chunk(a, n0, b);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = fmaf(a.alpha, v[i], b[i]);
+    }
+    const bool full = n0 + 32 <= a.N;
+    if (a.Z.q) {
+        if (!full) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (n0 + i >= a.N)
+                    v[i] = 0.0f;                         // the block's end: zeros, not counted
+        }
+        act_put_codes(a.Z, m, n0, v);
+    }
+    act_apply(a.act, v);
+    if (a.R) {
+        const uint16_t *r = a.R + m * a.ldr + n0;
+        if (a.r_vec && full) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                const uint4 w = *reinterpret_cast<const uint4 *>(r + i);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[i + 2 * j] = fmaf(a.res_scale, bf16_lo(ww[j]), v[i + 2 * j]);
+                    v[i + 2 * j + 1] = fmaf(a.res_scale, bf16_hi(ww[j]), v[i + 2 * j + 1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (n0 + i < a.N)
+                    v[i] = fmaf(a.res_scale, bf16_bits_to_float(r[i]), v[i]);
+        }
+    }
+    if (a.D)
+        put_d_row(a, m, n0, v);
+    if (a.H.q)
+        act_put_codes(a.H, m, n0, v);
+}
+
+// A block across a warp: lane's value of column n (0 where there is none), row m.
+// Every lane of the warp calls it; `in`: n is below the row's whole blocks.
+__device__ __forceinline__ void act_put_lane(const ActCodes &o, int m, int n, bool in, float v)
+{
+    const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7FFFFFFFu);
+    const bool finite = top < 0x7F800000u;               // not for infinities and NaN
+    const float amax = finite ? __uint_as_float(top) : 0.0f;
+    const int s = o.fmt == 2 ? block_exponent(amax) : block_exponent8(amax, o.fmt == 0 ? 8 : 15);
+    const float y = v * exp2_neg(s);
+    const uint32_t code = finite ? static_cast<uint32_t>(s + 127) : 0xFFu;
+    if (o.fmt == 2) {
+        const uint32_t two = e2m1x2(y, __shfl_down_sync(0xffffffffu, y, 1));
+        if (in && (n & 1) == 0)
+            o.q[m * o.ldq + n / 2] = static_cast<uint8_t>(two);
+    } else if (in) {
+        o.q[m * o.ldq + n] = static_cast<uint8_t>(o.fmt == 0 ? f8x2<0>(y, 0.0f) : f8x2<1>(y, 0.0f));
+    }
+    if (in && (n & 31) == 0)
+        o.s[m * o.lds + n / 32] = static_cast<uint8_t>(code);
+}
+
+// Swapped forms: lane's column n, rows m0 .. m0 + COUNT - 1; v holds the
+// accumulators.  The 32 lanes hold the columns of one block; every lane calls it.
+template <int COUNT>
+__device__ __forceinline__ void act_col_chunk(const ActGemmArgs &a, int m0, int n, float (&v)[COUNT])
+{
+    const int mcount = min(COUNT, a.M - m0);
+    const bool real = n < a.N, in = n - (n & 31) < a.N;
+    const float b = real && a.bias ? act_bias(a, n) : 0.0f;
+    uint16_t r[COUNT];
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)                      // before any store: R may alias D
+        r[i] = a.R && real && i < mcount ? a.R[(m0 + i) * a.ldr + n] : uint16_t(0);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+        v[i] = real ? fmaf(a.alpha, v[i], b) : 0.0f;
+    if (a.Z.q) {
+#pragma unroll
+        for (int i = 0; i < COUNT; ++i)
+            if (i < mcount)
+                act_put_lane(a.Z, m0 + i, n, in, v[i]);
+    }
+    act_apply(a.act, v);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+        if (i < mcount) {
+            if (a.R)
+                v[i] = fmaf(a.res_scale, bf16_bits_to_float(r[i]), v[i]);
+            if (a.D && real) {
+                const __nv_bfloat16 d = __float2bfloat16_rn(v[i]);
+                a.D[(m0 + i) * a.ldd + n] = *reinterpret_cast<const uint16_t *>(&d);
+            }
+            if (a.H.q)
+                act_put_lane(a.H, m0 + i, n, in, v[i]);
+        }
+}
+
+// Four columns n .. n + 3 of row m, the block's other values in the seven
+// lanes beside (all 32 lanes call it).  `in`: n is below the row's whole blocks.
+__device__ __forceinline__ void act_put_four(const ActCodes &o, int m, int n, bool in, const float (&v)[4])
+{
+    float amax = max_abs3(max_abs3(0.0f, v[0], v[1]), v[2], v[3]);
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1)
+        amax = max_abs3(0.0f, amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    const bool finite = amax <= 3.402823466e38f;
+    if (!finite)
+        amax = 0.0f;
+    const int s = o.fmt == 2 ? block_exponent(amax) : block_exponent8(amax, o.fmt == 0 ? 8 : 15);
+    const float inv = exp2_neg(s);
+    if (!in)
+        return;
+    if (o.fmt == 2) {
+        *reinterpret_cast<uint16_t *>(o.q + m * o.ldq + n / 2) =
+            static_cast<uint16_t>(e2m1x2(v[0] * inv, v[1] * inv) | (e2m1x2(v[2] * inv, v[3] * inv) << 8));
+    } else {
+        const uint32_t w = o.fmt == 0 ? f8x2<0>(v[0] * inv, v[1] * inv) | (f8x2<0>(v[2] * inv, v[3] * inv) << 16)
+                                      : f8x2<1>(v[0] * inv, v[1] * inv) | (f8x2<1>(v[2] * inv, v[3] * inv) << 16);
+        *reinterpret_cast<uint32_t *>(o.q + m * o.ldq + n) = w;
+    }
+    if ((n & 31) == 0)
+        o.s[m * o.lds + n / 32] = static_cast<uint8_t>(finite ? s + 127 : 0xFF);
+}
+
+// Rows of a tile that one rank of a cluster of `split` sums: whole 32-blocks
+// where the rows are n.
+template <bool SWAP>
+__device__ __forceinline__ int act_rank_rows(int split)
+{
+    const int rows = (kTileM + split - 1) / split;
+    return SWAP ? (rows + 31) / 32 * 32 : rows;
+}
+
+// reduce_tile_cluster with this epilogue: the partials are summed in split
+// order, four columns of a tile row at a time.
+template <bool SWAP>
+__device__ __forceinline__ void act_reduce_cluster(const ActGemmArgs &a, uint32_t part_smem, int stride, int p0, int q0, int t)
+{
+    const int S = a.split_k;
+    const int R = act_rank_rows<SWAP>(S);
+    const int r0 = min(kTileM, static_cast<int>(cluster_ctarank()) * R);
+    const int r1 = min(kTileM, r0 + R);
+    const int warp = t >> 5, lane = t & 31;
+    const int qvalid = min(a.part_cols, (SWAP ? a.M : a.N) - q0);
+    auto sum4 = [&](int row, int ch, float (&x)[4]) {
+        const uint32_t off = part_smem + static_cast<uint32_t>((row * stride + 4 * ch) * 4);
+        float4 v[8];
+#pragma unroll
+        for (int z = 0; z < 8; ++z)
+            if (z < S)
+                v[z] = ld_dsmem_v4(map_to_rank(off, static_cast<uint32_t>(z)));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[j] = 0.0f;
+#pragma unroll
+        for (int z = 0; z < 8; ++z)
+            if (z < S) {
+                x[0] += v[z].x;
+                x[1] += v[z].y;
+                x[2] += v[z].z;
+                x[3] += v[z].w;
+            }
+    };
+    if constexpr (SWAP) {
+        const int nch = (qvalid + 3) / 4;
+        const int units = (r1 - r0) / 32 * nch;
+        for (int u = warp; u < units; u += kGemmThreadsC / 32) {
+            const int row = r0 + u / nch * 32 + lane, ch = u % nch;
+            if (p0 + row - lane >= a.N)
+                continue;                                // a whole block past the last column
+            float x[4];
+            sum4(row, ch, x);
+            act_col_chunk<4>(a, q0 + 4 * ch, p0 + row, x);
+        }
+    } else {
+        const int nrows = max(0, min(r1, a.M - p0) - r0);
+        const int nch = (qvalid + 31) / 32 * 8;          // whole blocks of eight lanes
+        const int items = nrows * nch;
+        for (int base = warp * 32; base < items; base += kGemmThreadsC) {
+            const int it = base + lane;
+            const bool in = it < items;
+            const int row = r0 + (in ? it / nch : 0), ch = in ? it % nch : 0;
+            const int m = p0 + row, n = q0 + 4 * ch;
+            const int cnt = in ? max(0, min(4, qvalid - 4 * ch)) : 0;
+            float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (cnt > 0)
+                sum4(row, ch, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                x[j] = j < cnt ? fmaf(a.alpha, x[j], a.bias ? act_bias(a, n + j) : 0.0f) : 0.0f;
+            if (a.Z.q)
+                act_put_four(a.Z, m, n, in, x);
+            act_apply(a.act, x);
+            if (a.R) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < cnt)
+                        x[j] = fmaf(a.res_scale, bf16_bits_to_float(a.R[m * a.ldr + n + j]), x[j]);
+            }
+            if (a.D) {
+                if (a.vec_ok && cnt == 4) {
+                    *reinterpret_cast<uint2 *>(a.D + m * a.ldd + n) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (j < cnt) {
+                            const __nv_bfloat16 d = __float2bfloat16_rn(x[j]);
+                            a.D[m * a.ldd + n + j] = *reinterpret_cast<const uint16_t *>(&d);
+                        }
+                }
+            }
+            if (a.H.q)
+                act_put_four(a.H, m, n, in, x);
+        }
+    }
+}
+
+// Bring the lines of R that this CTA's share of the cluster reduction reads
+// into L2 (called while the CTA waits for its peers).
+template <bool SWAP>
+__device__ __forceinline__ void act_prefetch_share(const ActGemmArgs &a, int p0, int q0, int t)
+{
+    const int R = act_rank_rows<SWAP>(a.split_k);
+    const int r0 = min(kTileM, static_cast<int>(cluster_ctarank()) * R);
+    const int nrows = max(0, min(min(kTileM, r0 + R), (SWAP ? a.N : a.M) - p0) - r0);
+    const int qvalid = min(a.part_cols, (SWAP ? a.M : a.N) - q0);
+    if (nrows <= 0 || qvalid <= 0)
+        return;
+    if (SWAP) {
+        for (int i = t; i < qvalid; i += kGemmThreadsC) {
+            const uint16_t *row = a.R + (q0 + i) * a.ldr + p0 + r0;
+            prefetch_l2(row);
+            prefetch_l2(row + nrows - 1);
+        }
+    } else {
+        for (int i = t; i < nrows; i += kGemmThreadsC) {
+            const uint16_t *row = a.R + (p0 + r0 + i) * a.ldr + q0;
+            for (int c = 0; c < qvalid; c += 64)
+                prefetch_l2(row + c);
+            prefetch_l2(row + qvalid - 1);
+        }
+    }
+}
+
+}  // namespace mxfp4

@@ -183,13 +183,14 @@ __device__ __forceinline__ void pair_round_chunk(const GemmArgs &a, int m, int n
         out[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
 }
 
-template <int STAGES, bool NV>
+template <int STAGES, bool NV, class ARGS>
 __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
-    gemm_mxf4_pair(const __grid_constant__ GemmArgs a, const __grid_constant__ PairSched ps,
+    gemm_mxf4_pair(const __grid_constant__ ARGS a, const __grid_constant__ PairSched ps,
                    const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB)
 {
     using PC = PairCfg<STAGES, NV>;
+    constexpr bool EPI = !std::is_same_v<ARGS, GemmArgs>;
     constexpr int BN = PC::BN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -445,35 +446,69 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
             const int m = pt * 256 + static_cast<int>(rank) * kTileM + row;
             const int n0 = qt * BN + half * PC::HALF;
             const uint32_t t_row = t_lane;
-            uint32_t out[PC::HALF / 2];
-            // Columns 0-63 are read and rounded; 64-127 are read, the
-            // accumulator released, and only then rounded: the next tile's
-            // MMAs wait for the reads alone, not the arithmetic.  Once this
-            // warp's accumulator cells are read (tcgen05.wait::ld has
-            // returned, so no TMEM read is outstanding) they are released to
-            // the leader.  No memory fence is needed for that, and a
-            // cluster-scope release arrive costs ~1000 cycles, so the leader's
-            // warps arrive locally and the peer's with a relaxed remote arrive.
-            uint32_t r0[32], r1[32];
-            tmem_ld_32x32b_x32(t_row, r0);
-            tmem_ld_32x32b_x32(t_row + 32, r1);
-            tmem_ld_wait(r0, r1);
-            pair_round_chunk<32>(a, m, n0, r0, out);
-            pair_round_chunk<32>(a, m, n0 + 32, r1, out + 16);
-            tmem_ld_32x32b_x32(t_row + 64, r0);
-            tmem_ld_32x32b_x32(t_row + 96, r1);
-            tmem_ld_wait(r0, r1);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (leader)
-                    mbar_arrive(acc_empty);
-                else
-                    mbar_arrive_cluster_relaxed(map_to_rank(smem_addr(acc_empty), lead));
+            if constexpr (EPI) {
+                // 64 columns at a time; the accumulator is released once the
+                // second 64 are read.
+#pragma unroll
+                for (int c0 = 0; c0 < PC::HALF; c0 += 64) {
+                    uint32_t r0[32], r1[32];
+                    tmem_ld_32x32b_x32(t_row + c0, r0);
+                    tmem_ld_32x32b_x32(t_row + c0 + 32, r1);
+                    tmem_ld_wait(r0, r1);
+                    if (c0 + 64 == PC::HALF) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            if (leader)
+                                mbar_arrive(acc_empty);
+                            else
+                                mbar_arrive_cluster_relaxed(map_to_rank(smem_addr(acc_empty), lead));
+                        }
+                    }
+                    auto put = [&](int n, const uint32_t (&r)[32]) {
+                        if (m >= a.M || n >= a.N)
+                            return;
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = __uint_as_float(r[i]);
+                        act_row_chunk(a, m, n, v);
+                    };
+                    put(n0 + c0, r0);
+                    put(n0 + c0 + 32, r1);
+                    __syncwarp();
+                }
+            } else {
+                uint32_t out[PC::HALF / 2];
+                // Columns 0-63 are read and rounded; 64-127 are read, the
+                // accumulator released, and only then rounded: the next tile's
+                // MMAs wait for the reads alone, not the arithmetic.  Once this
+                // warp's accumulator cells are read (tcgen05.wait::ld has
+                // returned, so no TMEM read is outstanding) they are released to
+                // the leader.  No memory fence is needed for that, and a
+                // cluster-scope release arrive costs ~1000 cycles, so the leader's
+                // warps arrive locally and the peer's with a relaxed remote arrive.
+                uint32_t r0[32], r1[32];
+                tmem_ld_32x32b_x32(t_row, r0);
+                tmem_ld_32x32b_x32(t_row + 32, r1);
+                tmem_ld_wait(r0, r1);
+                pair_round_chunk<32>(a, m, n0, r0, out);
+                pair_round_chunk<32>(a, m, n0 + 32, r1, out + 16);
+                tmem_ld_32x32b_x32(t_row + 64, r0);
+                tmem_ld_32x32b_x32(t_row + 96, r1);
+                tmem_ld_wait(r0, r1);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(acc_empty);
+                    else
+                        mbar_arrive_cluster_relaxed(map_to_rank(smem_addr(acc_empty), lead));
+                }
+                pair_round_chunk<32>(a, m, n0 + 64, r0, out + 32);
+                pair_round_chunk<32>(a, m, n0 + 96, r1, out + 48);
+                pair_store_row<PC::HALF>(a, m, n0, out);
             }
-            pair_round_chunk<32>(a, m, n0 + 64, r0, out + 32);
-            pair_round_chunk<32>(a, m, n0 + 96, r1, out + 48);
-            pair_store_row<PC::HALF>(a, m, n0, out);
         }
     }
 

@@ -53,6 +53,7 @@
 // stage's full barrier completed again, which needs the producers to have
 // seen the stage's previous MMAs commit, so no write overtakes a read.
 #include <atomic>
+#include <type_traits>
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -125,32 +126,11 @@ __device__ __forceinline__ float bf16_bits_to_float(uint16_t b)
     return __uint_as_float(static_cast<uint32_t>(b) << 16);
 }
 
-// D[m][n0 .. n0+31] = bf16(alpha * v + beta * C), vector stores when the
-// whole chunk is inside the row and the pointers allow it.
-__device__ __forceinline__ void store_d_row(const GemmArgs &a, int m, int n0, float (&v)[32])
+// D[m][n0 .. n0+31] = bf16(v), vector stores when the whole chunk is inside
+// the row and the pointers allow it.
+__device__ __forceinline__ void put_d_row(const GemmArgs &a, int m, int n0, const float (&v)[32])
 {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] *= a.alpha;
     const bool full = n0 + 32 <= a.N;
-    if (a.beta != 0.0f) {
-        const uint16_t *c = a.C + static_cast<int64_t>(m) * a.ldc + n0;
-        if (a.vec_ok && full) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                uint4 w = *reinterpret_cast<const uint4 *>(c + i);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[i + 2 * j] = fmaf(a.beta, bf16_bits_to_float(ww[j] & 0xFFFF), v[i + 2 * j]);
-                    v[i + 2 * j + 1] = fmaf(a.beta, bf16_bits_to_float(ww[j] >> 16), v[i + 2 * j + 1]);
-                }
-            }
-        } else {
-            for (int i = 0; i < 32 && n0 + i < a.N; ++i)
-                v[i] = fmaf(a.beta, bf16_bits_to_float(c[i]), v[i]);
-        }
-    }
     uint16_t *d = a.D + static_cast<int64_t>(m) * a.ldd + n0;
     if (a.vec32_ok && full) {
         // 32-byte stores: half the store instructions of 16-byte ones.  D is
@@ -176,6 +156,34 @@ __device__ __forceinline__ void store_d_row(const GemmArgs &a, int m, int n0, fl
             d[i] = *reinterpret_cast<uint16_t *>(&b);
         }
     }
+}
+
+// D[m][n0 .. n0+31] = bf16(alpha * v + beta * C).
+__device__ __forceinline__ void store_d_row(const GemmArgs &a, int m, int n0, float (&v)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] *= a.alpha;
+    const bool full = n0 + 32 <= a.N;
+    if (a.beta != 0.0f) {
+        const uint16_t *c = a.C + static_cast<int64_t>(m) * a.ldc + n0;
+        if (a.vec_ok && full) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                uint4 w = *reinterpret_cast<const uint4 *>(c + i);
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[i + 2 * j] = fmaf(a.beta, bf16_bits_to_float(ww[j] & 0xFFFF), v[i + 2 * j]);
+                    v[i + 2 * j + 1] = fmaf(a.beta, bf16_bits_to_float(ww[j] >> 16), v[i + 2 * j + 1]);
+                }
+            }
+        } else {
+            for (int i = 0; i < 32 && n0 + i < a.N; ++i)
+                v[i] = fmaf(a.beta, bf16_bits_to_float(c[i]), v[i]);
+        }
+    }
+    put_d_row(a, m, n0, v);
 }
 
 // D[m0 + i][n] = bf16(alpha * v[i] + beta * C) for the valid i (swap: one n
@@ -280,12 +288,13 @@ __device__ __forceinline__ bool tile_count_done(unsigned long long *word, uint32
 // half of the columns (t >> 7), over the tile's split partials in the fixed
 // order z = 0, 1, ..., split-1, then applies alpha / beta with C and rounds
 // once to bf16 (swap: the row is n, the columns are m).
-template <bool SWAP>
-__device__ __forceinline__ void reduce_tile(const GemmArgs &a, int64_t tile, int p0, int q0, int t)
+// ALL_LANES: `put` needs whole warps (rows past the last come too, without a value).
+template <bool SWAP, bool ALL_LANES, typename PUT>
+__device__ __forceinline__ void reduce_tile(const GemmArgs &a, int64_t tile, int p0, int q0, int t, PUT put)
 {
     const int row = t & (kTileM - 1);
     const int prows = SWAP ? a.N : a.M;
-    if (p0 + row >= prows)
+    if (p0 + (ALL_LANES ? row & ~31 : row) >= prows)
         return;
     const int qvalid = min(a.part_cols, (SWAP ? a.M : a.N) - q0);
     // Halves on 32-column boundaries: a chunk's stores (bounded by M and N
@@ -334,10 +343,7 @@ __device__ __forceinline__ void reduce_tile(const GemmArgs &a, int64_t tile, int
                 }
             }
         }
-        if (!SWAP)
-            store_d_row(a, p0 + row, q0 + cg, acc);
-        else
-            store_d_col(a, q0 + cg, p0 + row, acc);
+        put(p0 + row, q0 + cg, acc);
     }
 }
 
@@ -624,16 +630,24 @@ __device__ __forceinline__ void write_stage_scales(uint8_t *smem, uint64_t *full
 
 constexpr int kGemmThreads = kGemmThreadsC;
 
+}  // namespace mxfp4
+
+#include "gemm_act.cuh"
+
+namespace mxfp4 {
+
 // FMT 0: fp4 (E2M1) elements, kind::mxf4; FMT 1: one byte per element
 // (E4M3 / E5M2 / padded E2M3, E3M2, E2M1), kind::mxf8f6f4 with the element
 // types in a.idesc8.  MINB: CTAs per SM the configuration is planned for.
-template <int BN, int STAGES, bool SWAP, int FMT, int MINB>
+// ARGS: GemmArgs, or ActGemmArgs for the epilogue of gemm_act.cuh.
+template <int BN, int STAGES, bool SWAP, int FMT, int MINB, class ARGS>
 __global__ void __launch_bounds__(kGemmThreads, MINB)
-    gemm_mxf4_kernel(const __grid_constant__ GemmArgs a, const __grid_constant__ CUtensorMap tmP,
+    gemm_mxf4_kernel(const __grid_constant__ ARGS a, const __grid_constant__ CUtensorMap tmP,
                      const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmSP,
                      const __grid_constant__ CUtensorMap tmSQ)
 {
     using Cf = CfgFor<BN, STAGES, FMT>;
+    constexpr bool EPI = !std::is_same_v<ARGS, GemmArgs>;
     constexpr int G = Cf::GROUPS;
     extern __shared__ uint8_t smem_raw[];
     // 1024-byte alignment of the ring (128-byte swizzle atoms).
@@ -999,7 +1013,7 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
                     park_partial_chunk(a, slot, row, c0, r);
                 }
                 __threadfence();
-            } else {
+            } else if constexpr (!EPI) {
 #pragma unroll 1
                 for (int c0 = 0; c0 < BN; c0 += 32) {
                     if (SWAP && q0 + c0 >= a.M)
@@ -1021,16 +1035,63 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
 
     tc_fence_before();
     __syncthreads();
+    if constexpr (EPI) {
+        // One split: the epilogue's arithmetic is as long as a good part of the
+        // main loop, so all eight warps share it, two per lane quarter with half
+        // of the columns each.
+        if (a.split_k == 1) {
+            bool ok = nkt > 0 && mbar_wait(acc_full, 0, abort_flag, a.wait_limit, &g_device_status);
+            ok = __all_sync(0xffffffffu, ok);
+            pdl_wait_prerequisites();
+            if (ok) {
+                tc_fence_after();
+                const int quarter = warp & 3;
+                const int row = quarter * 32 + lane;
+                const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+                const int c_begin = (warp >> 2) * (BN / 2);
+#pragma unroll 1
+                for (int c0 = c_begin; c0 < c_begin + BN / 2; c0 += 32) {
+                    if (q0 + c0 >= (SWAP ? a.M : a.N))
+                        break;
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(t_row + c0, r);
+                    tmem_ld_wait(r);
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __uint_as_float(r[i]);
+                    if constexpr (SWAP) {
+                        if (p0 + quarter * 32 < a.N)
+                            act_col_chunk<32>(a, q0 + c0, p0 + row, v);
+                    } else {
+                        if (p0 + row < a.M)
+                            act_row_chunk(a, p0 + row, q0 + c0, v);
+                        __syncwarp();
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncthreads();
+        }
+    }
     if (a.split_k > 1 && a.cluster_reduce) {
         // Every partial of the tile is in its CTA's shared memory once the
         // cluster barrier completes; the second barrier keeps this CTA's
         // partial alive until its peers have read it.
         pdl_wait_prerequisites();
-        if (a.beta != 0.0f)
+        if constexpr (EPI) {
+            if (a.R)
+                act_prefetch_share<SWAP>(a, p0, q0, threadIdx.x);
+        } else if (a.beta != 0.0f) {
             prefetch_c_share<SWAP>(a, p0, q0, threadIdx.x);
+        }
         cluster_sync();
-        reduce_tile_cluster<SWAP>(a, smem_addr(smem), cluster_part_stride(a.part_cols), p0, q0,
-                                  threadIdx.x);
+        if constexpr (EPI)
+            act_reduce_cluster<SWAP>(a, smem_addr(smem), cluster_part_stride(a.part_cols), p0, q0,
+                                     threadIdx.x);
+        else
+            reduce_tile_cluster<SWAP>(a, smem_addr(smem), cluster_part_stride(a.part_cols), p0, q0,
+                                      threadIdx.x);
         cluster_sync();
     } else if (a.split_k > 1 && nkt > 0) {
         // Count this CTA into its tile (its partial rows are written and
@@ -1047,7 +1108,20 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
         if (*last_flag) {
             __threadfence();
             pdl_wait_prerequisites();
-            reduce_tile<SWAP>(a, tile, p0, q0, threadIdx.x);
+            if constexpr (EPI)
+                reduce_tile<SWAP, SWAP>(a, tile, p0, q0, threadIdx.x, [&](int p, int q, float (&acc)[32]) {
+                    if constexpr (SWAP)
+                        act_col_chunk<32>(a, q, p, acc);
+                    else
+                        act_row_chunk(a, p, q, acc);
+                });
+            else
+                reduce_tile<SWAP, false>(a, tile, p0, q0, threadIdx.x, [&](int p, int q, float (&acc)[32]) {
+                    if constexpr (SWAP)
+                        store_d_col(a, q, p, acc);
+                    else
+                        store_d_row(a, p, q, acc);
+                });
         }
     }
     if (warp == 5) {
@@ -1064,13 +1138,13 @@ namespace mxfp4 {
 
 // ----------------------------------------------------------- host side --
 
-template <int BN, int STAGES, bool SWAP, int FMT, int MINB>
-static cudaError_t launch_cfg(const GemmArgs &a, const CUtensorMap &tmP, const CUtensorMap &tmQ,
+template <int BN, int STAGES, bool SWAP, int FMT, int MINB, class ARGS>
+static cudaError_t launch_cfg(const ARGS &a, const CUtensorMap &tmP, const CUtensorMap &tmQ,
                               const CUtensorMap &tmSP, const CUtensorMap &tmSQ, dim3 grid,
                               cudaStream_t stream)
 {
     using Cf = CfgFor<BN, STAGES, FMT>;
-    auto kern = gemm_mxf4_kernel<BN, STAGES, SWAP, FMT, MINB>;
+    auto kern = gemm_mxf4_kernel<BN, STAGES, SWAP, FMT, MINB, ARGS>;
     // Opt in to the large dynamic shared memory once per device.
     static std::atomic<int> configured[64];
     int dev = 0;
@@ -1129,8 +1203,8 @@ bool gemm_config_exists(const GemmShape &s)
     return s.tile_n == 64 && s.stages == 4;
 }
 
-template <int FMT>
-static cudaError_t launch_gemm_fmt(const GemmArgs &a, const CUtensorMap &tmP, const CUtensorMap &tmQ,
+template <int FMT, class ARGS>
+static cudaError_t launch_gemm_fmt(const ARGS &a, const CUtensorMap &tmP, const CUtensorMap &tmQ,
                                    const CUtensorMap &tmSP, const CUtensorMap &tmSQ,
                                    const GemmShape &s, dim3 grid, cudaStream_t stream)
 {
@@ -1149,6 +1223,22 @@ static cudaError_t launch_gemm_fmt(const GemmArgs &a, const CUtensorMap &tmP, co
     return cudaErrorInvalidConfiguration;
 }
 
+// The byte formats' kernels, after their element codes' check.
+template <class ARGS>
+static cudaError_t launch_gemm_bytes(const ARGS &a, const CUtensorMap &tmP, const CUtensorMap &tmQ,
+                                     const CUtensorMap &tmSP, const CUtensorMap &tmSQ,
+                                     const GemmShape &s, dim3 grid, cudaStream_t stream)
+{
+    // kind::mxf8f6f4 element codes: E4M3 0, E5M2 1, E2M3 3, E3M2 4, E2M1 5.
+    auto known = [](int f) { return f == 0 || f == 1 || (f >= 3 && f <= 5); };
+    if (!known(a.fmt_p) || !known(a.fmt_q))
+        return cudaErrorInvalidValue;
+    ARGS b = a;
+    b.idesc8 = idesc_mxf8(kTileM, s.tile_n, static_cast<uint32_t>(a.fmt_p),
+                          static_cast<uint32_t>(a.fmt_q));
+    return launch_gemm_fmt<1>(b, tmP, tmQ, tmSP, tmSQ, s, grid, stream);
+}
+
 cudaError_t launch_gemm(const GemmArgs &a, const CUtensorMap &tmP, const CUtensorMap &tmQ,
                         const CUtensorMap &tmSP, const CUtensorMap &tmSQ, const GemmShape &s,
                         dim3 grid, cudaStream_t stream)
@@ -1162,14 +1252,16 @@ cudaError_t launch_gemm(const GemmArgs &a, const CUtensorMap &tmP, const CUtenso
     }
     if (!s.fp8)
         return launch_gemm_fmt<0>(a, tmP, tmQ, tmSP, tmSQ, s, grid, stream);
-    // kind::mxf8f6f4 element codes: E4M3 0, E5M2 1, E2M3 3, E3M2 4, E2M1 5.
-    auto known = [](int f) { return f == 0 || f == 1 || (f >= 3 && f <= 5); };
-    if (!known(a.fmt_p) || !known(a.fmt_q))
-        return cudaErrorInvalidValue;
-    GemmArgs b = a;
-    b.idesc8 = idesc_mxf8(kTileM, s.tile_n, static_cast<uint32_t>(a.fmt_p),
-                          static_cast<uint32_t>(a.fmt_q));
-    return launch_gemm_fmt<1>(b, tmP, tmQ, tmSP, tmSQ, s, grid, stream);
+    return launch_gemm_bytes(a, tmP, tmQ, tmSP, tmSQ, s, grid, stream);
+}
+
+cudaError_t launch_gemm_act(const ActGemmArgs &a, const CUtensorMap &tmP, const CUtensorMap &tmQ,
+                            const CUtensorMap &tmSP, const CUtensorMap &tmSQ, const GemmShape &s,
+                            dim3 grid, cudaStream_t stream)
+{
+    if (!s.fp8)
+        return launch_gemm_fmt<0>(a, tmP, tmQ, tmSP, tmSQ, s, grid, stream);
+    return launch_gemm_bytes(a, tmP, tmQ, tmSP, tmSQ, s, grid, stream);
 }
 
 // The compiled pair configurations: MXFP4 with 6 stages of 256 K, NVFP4 with
@@ -1179,14 +1271,14 @@ constexpr int kPairStagesNv = 5;
 
 size_t gemm_pair_smem_bytes() { return PairCfg<kPairStages, false>::SMEM_BYTES; }
 
-template <int STAGES, bool NV>
-static cudaError_t launch_pair_kernel(const GemmArgs &a, int tiles_p, int tiles_q, int ctas,
+template <int STAGES, bool NV, class ARGS>
+static cudaError_t launch_pair_kernel(const ARGS &a, int tiles_p, int tiles_q, int ctas,
                                       const CUtensorMap &tmA, const CUtensorMap &tmB,
                                       const CUtensorMap &tmSA, const CUtensorMap &tmSB,
                                       cudaStream_t stream)
 {
     using PC = PairCfg<STAGES, NV>;
-    auto kern = gemm_mxf4_pair<STAGES, NV>;
+    auto kern = gemm_mxf4_pair<STAGES, NV, ARGS>;
     static std::atomic<int> max_clusters[64];   // per device; 0 = not yet queried
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1247,6 +1339,15 @@ cudaError_t launch_gemm_pair(const GemmArgs &a, int tiles_p, int tiles_q, int ct
     if (nv)
         return launch_pair_kernel<kPairStagesNv, true>(a, tiles_p, tiles_q, ctas, tmA, tmB, tmSA,
                                                        tmSB, stream);
+    return launch_pair_kernel<kPairStages, false>(a, tiles_p, tiles_q, ctas, tmA, tmB, tmSA, tmSB,
+                                                  stream);
+}
+
+cudaError_t launch_gemm_act_pair(const ActGemmArgs &a, int tiles_p, int tiles_q, int ctas,
+                                 const CUtensorMap &tmA, const CUtensorMap &tmB,
+                                 const CUtensorMap &tmSA, const CUtensorMap &tmSB,
+                                 cudaStream_t stream)
+{
     return launch_pair_kernel<kPairStages, false>(a, tiles_p, tiles_q, ctas, tmA, tmB, tmSA, tmSB,
                                                   stream);
 }

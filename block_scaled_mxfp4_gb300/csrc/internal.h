@@ -75,6 +75,26 @@ struct GemmArgs {
     int fmt_p, fmt_q;       // fp8: element types of P and Q (kind::mxf8f6f4 codes)
 };
 
+// Arguments of a product with bias, activation and residual (gemm_act.cuh).
+struct ActCodes {               // quantised output [M, N], 1x32 blocks along N; q null: not wanted
+    uint8_t *q;
+    int64_t ldq;                // bytes
+    uint8_t *s;
+    int64_t lds;
+    int fmt;                    // 0: E4M3, 1: E5M2, 2: packed E2M1
+};
+struct ActGemmArgs : GemmArgs { // D may be null; beta and C are not used
+    const void *bias;           // [N] or null
+    int bias_fp32;              // fp32, else bf16
+    int bias_vec;               // 16-byte aligned
+    int act;                    // MXFP4_ACT_*
+    const uint16_t *R;          // bf16 [M, ldr] or null
+    int64_t ldr;
+    float res_scale;
+    int r_vec;                  // R's rows allow 16-byte loads
+    ActCodes H, Z;
+};
+
 struct GemmShape {
     int tile_n;
     int stages;
@@ -101,6 +121,10 @@ cudaError_t launch_gemm(const GemmArgs &a, const CUtensorMap &tmP, const CUtenso
                         const CUtensorMap &tmSP, const CUtensorMap &tmSQ, const GemmShape &s,
                         dim3 grid, cudaStream_t stream);
 
+cudaError_t launch_gemm_act(const ActGemmArgs &a, const CUtensorMap &tmP, const CUtensorMap &tmQ,
+                            const CUtensorMap &tmSP, const CUtensorMap &tmSQ, const GemmShape &s,
+                            dim3 grid, cudaStream_t stream);
+
 // CTA-pair kernel (relaid scales): grid of up to `ctas` CTAs in clusters of
 // two (clamped to the clusters the GPU holds at once), persistent over 256 x
 // 256 tiles, launched as a programmatic dependent of the preceding work.
@@ -112,6 +136,11 @@ cudaError_t launch_gemm_pair(const GemmArgs &a, int tiles_p, int tiles_q, int ct
                              const CUtensorMap &tmA, const CUtensorMap &tmB,
                              const CUtensorMap &tmSA, const CUtensorMap &tmSB, bool nv,
                              cudaStream_t stream);
+
+cudaError_t launch_gemm_act_pair(const ActGemmArgs &a, int tiles_p, int tiles_q, int ctas,
+                                 const CUtensorMap &tmA, const CUtensorMap &tmB,
+                                 const CUtensorMap &tmSA, const CUtensorMap &tmSB,
+                                 cudaStream_t stream);
 
 cudaError_t launch_scale_relayout(uint8_t *dst, const uint8_t *src, int rows, int K, int64_t ld,
                                   cudaStream_t stream);

@@ -603,6 +603,136 @@ int mxfp4_moe_ffn(void *H, int64_t ldh, void *Nrm, int64_t ldn, const void *X, i
                   void *workspace, size_t workspace_bytes, void *stream);
 size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F);
 
+/* ------------------------------------------------------------------------
+ * A dense layer in training and serving: products with bias, activation and
+ * residual, what the forward pass keeps in 8 bits, the activation's backward
+ * pass, layer norm.
+ *
+ * The operands of these are the library's: the backward pass's products are
+ * mxfp8_gemm on the forms below (with z = x W^T + b, dx = dz W on W's transposed
+ * form, dW = dz^T x on the transposed forms of dz and x, K the tokens rounded up
+ * to 32).  They follow the conventions at the top of this file (caller's memory
+ * and stream, arguments checked before anything is enqueued, capture into
+ * graphs); each is launched as a programmatic dependent of the work before it.
+ * All arithmetic is fp32, rounded once where an output has fewer bits.
+ *
+ * MXFP8 form of [rows, cols] here: codes of E4M3 or E5M2, one per byte, rows of
+ * whole 32-blocks (ld >= cols rounded up to 32, ld % 16 == 0, 16-byte aligned),
+ * and row-major E8M0 scales (ld >= cols / 32 rounded up).  Columns past the last
+ * one of its block are written as zeros and do not count in the block's scale.
+ * Codes and scales by the rule of mxfp8_quantize; a block that holds an infinity
+ * or a NaN gets the scale 0xFF (NaN), and reads as NaN.
+ *
+ * Activations: none, max(z, 0), GELU z Phi(z), GELU's tanh form, SiLU.
+ * Exponentials and reciprocals are the hardware's approximations; GELU's Phi is a
+ * polynomial of this library's own with a relative error of 5e-7 in the lower
+ * tail.  Values are within 2^-20 (1 + z^2) of themselves.
+ * ------------------------------------------------------------------------ */
+
+enum { MXFP4_ACT_NONE = 0, MXFP4_ACT_RELU = 1, MXFP4_ACT_GELU = 2, MXFP4_ACT_GELU_TANH = 3, MXFP4_ACT_SILU = 4 };
+enum { MXFP4_PARAM_BF16 = 0, MXFP4_PARAM_FP32 = 1 };
+
+/*
+ * mxfp4_gemm with an epilogue:
+ *   z = alpha * A . B^T + bias                    -> Z, the 8-bit checkpoint (MXFP8 form, fmt_z)
+ *   d = act(z) + res_scale * R                    -> D (bf16), H (quantised for the next product)
+ *   D     bf16 [M, ldd] or NULL
+ *   H     [M, ldh] and SH [M, ld_sh] or both NULL: packed E2M1 by the rule of
+ *         mxfp4_quantize (ldh in elements, ldh % 32 == 0); for mxfp8_gemm_act the
+ *         MXFP8 form in fmt_h.  Needs N % 32 == 0
+ *   Z     [M, ldz] and SZ [M, ld_sz] or both NULL, in fmt_z (MXFP8_E4M3 / MXFP8_E5M2)
+ *   bias  [N], bf16 or fp32 (bias_type), or NULL
+ *   R     bf16 [M, ldr] or NULL; may alias D with ldr == ldd
+ * At least one of D, H, Z.  A, B, scales, alpha, M, N, K, split_k, flags, workspace:
+ * as for mxfp4_gemm_ex, with the same plan and workspace (mxfp4_gemm_workspace_size).
+ * Without bias, activation and R, D is mxfp4_gemm's bit for bit.  The product's
+ * accumulation is mxfp4_gemm's: it can move a code or a block's scale by one
+ * step where the exact value lies beside a rounding's edge.
+ */
+int mxfp4_gemm_act(void *D, int64_t ldd, void *H, int64_t ldh, void *SH, int64_t ld_sh, void *Z,
+                   int64_t ldz, void *SZ, int64_t ld_sz, const void *A, int64_t lda, const void *B,
+                   int64_t ldb, const void *scaleA, int64_t ld_sa, const void *scaleB, int64_t ld_sb,
+                   int fmt_z, float alpha, const void *bias, int bias_type, int act, const void *R,
+                   int64_t ldr, float res_scale, int M, int N, int K, int split_k, unsigned flags,
+                   void *workspace, size_t workspace_bytes, void *stream);
+/* The same on the byte formats and with the plan of mxfp8_gemm (mxfp8_gemm_workspace_size). */
+int mxfp8_gemm_act(void *D, int64_t ldd, void *H, int64_t ldh, void *SH, int64_t ld_sh, void *Z,
+                   int64_t ldz, void *SZ, int64_t ld_sz, const void *A, int64_t lda, const void *B,
+                   int64_t ldb, const void *scaleA, int64_t ld_sa, const void *scaleB, int64_t ld_sb,
+                   int fmt_a, int fmt_b, int fmt_h, int fmt_z, float alpha, const void *bias,
+                   int bias_type, int act, const void *R, int64_t ldr, float res_scale, int M, int N,
+                   int K, int split_k, unsigned flags, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/*
+ * bf16 rows to MXFP8 in both orientations, read once.
+ *   X         bf16 [rows, ldx], 16-byte aligned rows (ldx % 8 == 0, ldx >= cols)
+ *   Q, S      MXFP8 form of X [rows, cols], as mxfp8_quantize writes it: an operand
+ *             of the product over cols
+ *   QT, ST    MXFP8 form of X^T [cols, rows]: an operand of the product over rows
+ *             (a weight's gradient), kept from the forward pass for the backward one
+ *   col_sums  fp32 [cols]: the sum of each column (a bias's gradient), in an order
+ *             that depends on rows and cols alone
+ * Q, QT and col_sums may each be NULL (with its scales), not all of them.  cols
+ * need not be a multiple of 32.  rows, cols >= 1.
+ * workspace: mxfp8_checkpoint_workspace_size(rows, cols) bytes, 256-byte aligned,
+ * contents arbitrary; used for col_sums alone (else NULL will do).
+ */
+int mxfp8_checkpoint(void *Q, int64_t ldq, void *S, int64_t lds, void *QT, int64_t ldqt, void *ST,
+                     int64_t ldst, float *col_sums, const void *X, int64_t ldx, int rows, int cols,
+                     int fmt, void *workspace, size_t workspace_bytes, void *stream);
+size_t mxfp8_checkpoint_workspace_size(int rows, int cols);
+
+/*
+ * The activation's backward pass from an 8-bit checkpoint of z:
+ *   dz = dH * act'(z)     -> dZ (bf16), Q, S and QT, ST (MXFP8 forms of dz and dz^T, fmt)
+ *   dbias = column sums of dz (fp32, before any rounding)
+ *   h = act(z)            -> HT, SHT (MXFP8 form of h^T, fmt_h): h is not kept from the
+ *                            forward pass, the checkpoint gives it again
+ *   dH  bf16 [rows, lddh], 16-byte aligned rows
+ *   Z   MXFP8 form [rows, cols] in fmt_z, SZ its scales (as mxfp4_gemm_act and
+ *       mxfp8_gemm_act write them)
+ * Every output may be NULL (with its scales), not all of them.  dZ may alias dH
+ * (with lddz == lddh).  act'(0) of max(z, 0) is 0.  Sizes and workspace as for mxfp8_checkpoint.
+ */
+int mxfp8_act_backward(void *dZ, int64_t lddz, void *Q, int64_t ldq, void *S, int64_t lds, void *QT,
+                       int64_t ldqt, void *ST, int64_t ldst, void *HT, int64_t ldht, void *SHT,
+                       int64_t ld_sht, float *dbias, const void *dH, int64_t lddh, const void *Z,
+                       int64_t ldz, const void *SZ, int64_t ld_sz, int fmt_z, int act, int rows,
+                       int cols, int fmt, int fmt_h, void *workspace, size_t workspace_bytes,
+                       void *stream);
+
+/*
+ * Layer norm of rows:
+ *   mean = sum x / N, rstd = 1 / sqrt(sum (x - mean)^2 / N + eps), y = (x - mean) * rstd * w + b
+ *   X, Y       bf16 [T, ldx / ldy]; Y may alias X (with ldy == ldx)
+ *   mean, rstd fp32 [T], for the backward pass; either may be NULL
+ *   w, b       [N], bf16 or fp32 (param_type), or NULL (ones, zeros)
+ * T >= 0, 1 <= N <= 32768, eps >= 0.  Rows of any alignment; those whose pointers and
+ * strides allow 16-byte accesses are faster.
+ */
+int mxfp4_layer_norm(void *Y, int64_t ldy, float *mean, float *rstd, const void *X, int64_t ldx,
+                     const void *w, const void *b, int param_type, float eps, int T, int N,
+                     void *stream);
+
+/*
+ * Its gradients, with xhat = (x - mean) * rstd and g = dy * w:
+ *   dx = rstd * (g - mean(g) - xhat * mean(g * xhat)) + dres     -> dX (bf16)
+ *   dw = sum of dy * xhat, db = sum of dy over the rows          (fp32 [N])
+ *   dres  bf16 [T, ldr] or NULL: the gradient that passes the norm by (the
+ *         residual stream's), added before the one rounding
+ *   dw, db may be NULL.  dX may alias dY, X or dres (with the same stride).
+ * The sums' order depends on T and N alone.  T = 0 writes zeros to dw and db.
+ * workspace: mxfp4_layer_norm_workspace_size(T, N) bytes, 256-byte aligned,
+ * contents arbitrary; used for dw and db alone.
+ */
+int mxfp4_layer_norm_backward(void *dX, int64_t lddx, float *dw, float *db, const void *dY,
+                              int64_t lddy, const void *X, int64_t ldx, const float *mean,
+                              const float *rstd, const void *w, int param_type, const void *dres,
+                              int64_t ldr, int T, int N, void *workspace, size_t workspace_bytes,
+                              void *stream);
+size_t mxfp4_layer_norm_workspace_size(int T, int N);
+
 /* Set the in-kernel wait limit in SM clock cycles (default 2^32, ~2 s).  It
  * bounds waits inside a kernel, not the wait for the work before it. */
 void mxfp4_set_wait_limit(long long cycles);
