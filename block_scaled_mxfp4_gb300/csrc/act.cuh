@@ -22,8 +22,56 @@ __device__ __forceinline__ float ex2_approx(float x)
     return r;
 }
 
+// Two fp32 values in a register pair: one instruction rounds both.
+struct F2 {
+    uint64_t v;
+};
+
+__device__ __forceinline__ F2 f2(float lo, float hi)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
+__device__ __forceinline__ float2 parts(F2 a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 rcp2(F2 a)
+{
+    const float2 p = parts(a);
+    return f2(rcp_approx(p.x), rcp_approx(p.y));
+}
+__device__ __forceinline__ F2 ex2_2(F2 a)
+{
+    const float2 p = parts(a);
+    return f2(ex2_approx(p.x), ex2_approx(p.y));
+}
+
 // sigmoid(u) = 1 / (1 + exp(-u)); 0 where exp(-u) passes the largest number.
-__device__ __forceinline__ float sigmoid_approx(float u) { return rcp_approx(1.0f + ex2_approx(-1.44269504f * u)); }
+// u log2(e) is given.
+__device__ __forceinline__ F2 sigmoid2(F2 u_log2e) { return rcp2(f2(1.0f) + ex2_2(f2(-1.0f) * u_log2e)); }
 
 // The normal distribution: phi(z) = exp(-z^2 / 2) / sqrt(2 pi) and Phi(z).
 // With x = |z|, Phi(-x) exp(x^2 / 2) is smooth and falls like 1 / x, so it is
@@ -32,69 +80,62 @@ __device__ __forceinline__ float sigmoid_approx(float u) { return rcp_approx(1.0
 // (2.2e-7; 5.1e-7 with P's own rounding).  The lower tail comes out of it to that relative
 // precision, without a subtraction, and both phi and Phi from one exponential and
 // one reciprocal.
-__device__ __forceinline__ void normal_approx(float z, float &below, float &density)
+__device__ __forceinline__ void normal2(F2 z, F2 &below, F2 &density)
 {
-    const float x = fabsf(z);
-    const float t = rcp_approx(fmaf(0.375f, x, 1.0f));
-    const float e = ex2_approx(-0.72134752f * z * z);
-    float p = -0.032911055f;
-    p = fmaf(p, t, 0.136879951f);
-    p = fmaf(p, t, -0.186521217f);
-    p = fmaf(p, t, 0.0506323874f);
-    p = fmaf(p, t, 0.0156279318f);
-    p = fmaf(p, t, 0.0886382312f);
-    p = fmaf(p, t, 0.12844570f);
-    p = fmaf(p, t, 0.149604589f);
-    p = fmaf(p, t, 0.149603382f);
-    const float tail = e * (t * p);
-    below = z < 0.0f ? tail : 1.0f - tail;
-    density = 0.39894228f * e;
+    const float2 zs = parts(z);
+    const F2 t = rcp2(fma2(f2(0.375f), f2(fabsf(zs.x), fabsf(zs.y)), f2(1.0f)));
+    const F2 e = ex2_2(f2(-0.72134752f) * (z * z));
+    F2 p = f2(-0.032911055f);
+    p = fma2(p, t, f2(0.136879951f));
+    p = fma2(p, t, f2(-0.186521217f));
+    p = fma2(p, t, f2(0.0506323874f));
+    p = fma2(p, t, f2(0.0156279318f));
+    p = fma2(p, t, f2(0.0886382312f));
+    p = fma2(p, t, f2(0.12844570f));
+    p = fma2(p, t, f2(0.149604589f));
+    p = fma2(p, t, f2(0.149603382f));
+    const F2 tail = e * (t * p);
+    const float2 low = parts(tail), high = parts(fma2(tail, f2(-1.0f), f2(1.0f)));
+    below = f2(zs.x < 0.0f ? low.x : high.x, zs.y < 0.0f ? low.y : high.y);
+    density = f2(0.39894228f) * e;
 }
 
-// act(z).  GELU's tanh form is z sigmoid(2 u), u = sqrt(2 / pi) (z + 0.044715 z^3),
-// as (1 + tanh u) / 2 = sigmoid(2 u).  NaN stays NaN.
+// act(z) and act'(z) of two values.  GELU's tanh form is z sigmoid(2 u), u = sqrt(2 / pi)
+// (z + 0.044715 z^3), as (1 + tanh u) / 2 = sigmoid(2 u).  NaN stays NaN in act(z).
 template <Act A>
-__device__ __forceinline__ float act_value(float z)
+__device__ __forceinline__ void act_and_slope2(F2 z, F2 &h, F2 &slope)
 {
     if constexpr (A == Act::kRelu) {
-        return z < 0.0f ? 0.0f : z;
+        const float2 p = parts(z);
+        h = f2(p.x < 0.0f ? 0.0f : p.x, p.y < 0.0f ? 0.0f : p.y);
+        slope = f2(p.x <= 0.0f ? 0.0f : 1.0f, p.y <= 0.0f ? 0.0f : 1.0f);
     } else if constexpr (A == Act::kGelu) {
-        float below, density;
-        normal_approx(z, below, density);
-        return z * below;
-    } else if constexpr (A == Act::kGeluTanh) {
-        return z * sigmoid_approx(z * fmaf(0.0713548163f, z * z, 1.59576912f));
-    } else if constexpr (A == Act::kSilu) {
-        return z * sigmoid_approx(z);
-    } else {
-        return z;
-    }
-}
-
-// act(z) and act'(z).
-template <Act A>
-__device__ __forceinline__ void act_and_slope(float z, float &h, float &slope)
-{
-    if constexpr (A == Act::kRelu) {
-        h = z < 0.0f ? 0.0f : z;
-        slope = z <= 0.0f ? 0.0f : 1.0f;
-    } else if constexpr (A == Act::kGelu) {
-        float below, density;
-        normal_approx(z, below, density);
+        F2 below, density;
+        normal2(z, below, density);
         h = z * below;
-        slope = fmaf(z, density, below);
+        slope = fma2(z, density, below);
     } else if constexpr (A == Act::kGeluTanh) {
-        const float g = sigmoid_approx(z * fmaf(0.0713548163f, z * z, 1.59576912f));
+        // 2 u log2(e) = z (2.302208 + 0.10294324 z^2)
+        const F2 zz = z * z;
+        const F2 g = sigmoid2(z * fma2(f2(0.10294324f), zz, f2(2.3022082f)));
         h = z * g;
-        slope = fmaf(h * (1.0f - g), fmaf(0.214064449f, z * z, 1.59576912f), g);
+        slope = fma2(h * fma2(g, f2(-1.0f), f2(1.0f)), fma2(f2(0.214064449f), zz, f2(1.59576912f)), g);
     } else if constexpr (A == Act::kSilu) {
-        const float g = sigmoid_approx(z);
+        const F2 g = sigmoid2(f2(1.44269504f) * z);
         h = z * g;
-        slope = fmaf(h, 1.0f - g, g);
+        slope = fma2(h, fma2(g, f2(-1.0f), f2(1.0f)), g);
     } else {
         h = z;
-        slope = 1.0f;
+        slope = f2(1.0f);
     }
+}
+
+template <Act A>
+__device__ __forceinline__ F2 act_value2(F2 z)
+{
+    F2 h, slope;
+    act_and_slope2<A>(z, h, slope);
+    return h;
 }
 
 // Calls f(std::integral_constant-like tag) for the runtime code of an activation.

@@ -35,13 +35,15 @@ struct CheckpointArgs {
     int64_t ldz, ld_sz;
     int fmt_z;
     int rows, cols;
-    int strips;                 // row strips, one block each per column tile
+    int64_t strips, col_blocks; // blocks along the rows and along the columns
+    int steps;                  // tiles of a warp along the rows
     int act;
     int vec_dz;                 // dz's rows allow 16-byte stores
+    int wide_x, wide_z, wide_q, wide_qt, wide_ht;   // rows allow 32-byte accesses (set at launch)
 };
-// Row strips of a call: by its sizes alone, so that the sums' order is too.
-int checkpoint_strips(int rows, int cols, bool backward);
-cudaError_t launch_checkpoint(const CheckpointArgs &a, bool backward, cudaStream_t stream);
+// Row strips of a call and the tiles of a warp in each: by its sizes alone, so that the sums' order is too.
+int64_t checkpoint_strips(int rows, int cols, int *steps);
+cudaError_t launch_checkpoint(CheckpointArgs &a, bool backward, cudaStream_t stream);
 
 // a[c] and b[c]: sums over the strips of partials[strip][na + nb], in a fixed order; zeros for
 // no strips.  Either array may be null.

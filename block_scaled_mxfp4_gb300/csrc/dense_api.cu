@@ -36,7 +36,7 @@ CodesOut codes_out(void *q, int64_t ldq, void *s, int64_t lds, int fmt)
     return CodesOut{static_cast<uint8_t *>(q), ldq, static_cast<uint8_t *>(s), lds, fmt == MXFP8_E5M2 ? 1 : 0};
 }
 
-size_t partial_bytes(int strips, int64_t cols)
+size_t partial_bytes(int64_t strips, int64_t cols)
 {
     return strips > 1 ? align_up(static_cast<size_t>(strips) * static_cast<size_t>(cols) * sizeof(float)) : 0;
 }
@@ -52,7 +52,9 @@ int check_workspace(size_t need, const void *workspace, size_t bytes)
 
 int run_checkpoint(CheckpointArgs &a, bool backward, const void *workspace, size_t workspace_bytes, cudaStream_t stream)
 {
-    a.strips = checkpoint_strips(a.rows, a.cols, backward);
+    a.strips = checkpoint_strips(a.rows, a.cols, &a.steps);
+    if (a.strips * ((static_cast<int64_t>(a.cols) + 31) / 32) > 0x7FFFFFFF)
+        return MXFP4_ERR_UNSUPPORTED_SHAPE;              // more blocks than a grid has
     int st = check_workspace(a.sums ? partial_bytes(a.strips, a.cols) : 0, workspace, workspace_bytes);
     if (st != MXFP4_OK)
         return st;
@@ -105,9 +107,8 @@ size_t mxfp8_checkpoint_workspace_size(int rows, int cols)
 {
     if (rows < 1 || cols < 1 || rows > kMaxCount || cols > kMaxCount)
         return 0;
-    const size_t a = partial_bytes(checkpoint_strips(rows, cols, false), cols);
-    const size_t b = partial_bytes(checkpoint_strips(rows, cols, true), cols);
-    return a > b ? a : b;
+    int steps = 0;
+    return partial_bytes(checkpoint_strips(rows, cols, &steps), cols);
 }
 
 int mxfp8_checkpoint(void *Q, int64_t ldq, void *S, int64_t lds, void *QT, int64_t ldqt, void *ST, int64_t ldst, float *col_sums,

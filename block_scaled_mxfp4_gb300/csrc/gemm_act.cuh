@@ -21,8 +21,11 @@ __device__ __forceinline__ void act_apply(int act, float (&v)[N])
 {
     auto each = [&](auto tag) {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = act_value<decltype(tag)::value>(v[i]);
+        for (int i = 0; i < N; i += 2) {
+            const float2 h = parts(act_value2<decltype(tag)::value>(f2(v[i], v[i + 1])));
+            v[i] = h.x;
+            v[i + 1] = h.y;
+        }
     };
     switch (act) {
     case 1: each(ActTag<Act::kRelu>{}); break;
