@@ -22,26 +22,55 @@ namespace {
 // checkpoint (and then also act(z), blocks of 32 rows).  Values stay fp32 from
 // the load to the one rounding of each orientation.
 //
-// A warp takes 32 x 32 values at a time, a lane one row of them: the block along
-// the row is then one lane's, and its input and codes are whole 32-byte sectors.
-// The values go through the warp's piece of shared memory, and a lane takes one
-// column: that block is one lane's too, no orientation needs a shuffle, and
-// the codes leave as sectors again.  A warp does kAcross such tiles side by side
-// and `steps` below one another, a block kDown warps on top of each other and two
-// beside.
+// A block of 256 threads takes tiles of 128 rows, one below the other, by 128
+// columns (64 in the backward pass), copied to shared memory asynchronously while
+// the tile before is worked on.  A lane then takes 32 values of a row, and 32 of a
+// column: a block of either orientation is one lane's, and nothing needs a
+// shuffle.  Lanes are dealt so that a warp's accesses fall into whole
+// lines (128 bytes of codes are four lanes') and on different banks.  In the
+// backward pass the computed values go through shared memory as fp32, act(z) and
+// dz in turn.
+//
+// Why not straight from global memory, a row or column per lane: each such
+// access touches 32 lines, and the L1's tag stage, one line a cycle, was 80 %
+// busy at half of HBM's rate.
 
-constexpr int kWarps = 8;
-constexpr int kDown = 4;                         // warps of a block along the rows
-constexpr int kBeside = kWarps / kDown;
-constexpr int kAcross = 2;                       // tiles of a warp along the columns
-constexpr int kBlockCols = 32 * kAcross * kBeside;
-constexpr int kPitch = 36;                       // floats between rows in shared memory: no bank conflict either way
+constexpr int kThreads = 256;
+constexpr int kTileRows = 128;
 
-__device__ __forceinline__ void ld_sector(const void *p, uint32_t *w)
+template <bool BACKWARD>
+struct Tile {
+    static constexpr int kCols = BACKWARD ? 64 : 128;
+    static constexpr int kPitch = 2 * kCols + 16;        // bytes between x's rows: 4 words past a multiple of 32
+    static constexpr int kSkew = 32;                     // more before each 32 rows: lanes 32 rows apart meet no bank twice
+    static constexpr int kXBytes = kTileRows * kPitch + 4 * kSkew;
+    static constexpr int kZPitch = 80;
+    static constexpr int kZBytes = BACKWARD ? kTileRows * kZPitch : 0;
+    static constexpr int kStage = kXBytes + kZBytes;
+    static constexpr int kFPitch = 68;                   // floats between rows of computed values
+    static constexpr int kFBytes = BACKWARD ? (kTileRows * kFPitch + 32) * 4 : 0;
+    static constexpr int kBytes = 2 * kStage + kFBytes;
+    static constexpr int kUnits = kTileRows * kCols / 32 / kThreads;   // row blocks of a thread
+
+    static __device__ __forceinline__ int x_at(int row) { return row * kPitch + row / 32 * kSkew; }
+    static __device__ __forceinline__ int f_at(int row) { return row * kFPitch + row / 32 * 8; }
+    // Row and 32-column block of a thread's unit k: eight neighbouring rows to eight neighbouring lanes.
+    static __device__ __forceinline__ void unit(int warp, int lane, int k, int &row, int &b)
+    {
+        if (BACKWARD) {
+            row = warp * 16 + (lane & 7) + 8 * (lane >> 4);
+            b = (lane >> 3) & 1;
+        } else {
+            row = (k * 8 + warp) * 8 + (lane & 7);
+            b = lane >> 3;
+        }
+    }
+};
+
+// 16 bytes, the first `have` of them from src and the rest zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int have)
 {
-    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
-                 : "l"(p));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have) : "memory");
 }
 
 __device__ __forceinline__ void st_sector(void *p, const uint32_t (&w)[8], bool wide)
@@ -84,205 +113,231 @@ __device__ __forceinline__ float e8m0_value(uint32_t code)
     return code == 0u ? __uint_as_float(0x00400000u) : code == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(code << 23);
 }
 
-// 32 bf16 values of a row from column col0 on, zeros past the last one.
-__device__ __forceinline__ void load_row(const CheckpointArgs &a, int64_t row, int64_t col0, uint32_t (&w)[16])
+// Start the copies of one tile; what lies past the last row or column becomes zeros.
+template <bool BACKWARD>
+__device__ __forceinline__ void load_tile(const CheckpointArgs &a, uint32_t stage, int64_t row0, int64_t col0, int t)
 {
-    const uint16_t *src = a.x + row * a.ldx + col0;
-    if (col0 + 32 <= a.cols) {
-        if (a.wide_x) {
-            ld_sector(src, w);
-            ld_sector(src + 16, w + 8);
-        } else {
+    using T = Tile<BACKWARD>;
+    constexpr int kChunks = T::kCols / 8;                // 16-byte pieces of a row
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(src) + i);
-                w[4 * i] = v.x;
-                w[4 * i + 1] = v.y;
-                w[4 * i + 2] = v.z;
-                w[4 * i + 3] = v.w;
-            }
-        }
-    } else {
+    for (int i = 0; i < kTileRows * kChunks / kThreads; ++i) {
+        const int at = i * kThreads + t, r = at / kChunks, c = at % kChunks * 8;
+        const int64_t left = row0 + r < a.rows ? a.cols - (col0 + c) : 0;
+        const int have = left >= 8 ? 16 : left > 0 ? static_cast<int>(left) * 2 : 0;
+        copy16(stage + T::x_at(r) + 2 * c, have ? a.x + (row0 + r) * a.ldx + col0 + c : a.x, have);
+    }
+    if constexpr (BACKWARD) {
+        constexpr int kZChunks = T::kCols / 16;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t lo = col0 + 2 * i < a.cols ? src[2 * i] : 0u, hi = col0 + 2 * i + 1 < a.cols ? src[2 * i + 1] : 0u;
-            w[i] = lo | hi << 16;
+        for (int i = 0; i < kTileRows * kZChunks / kThreads; ++i) {
+            const int at = i * kThreads + t, r = at / kZChunks, c = at % kZChunks * 16;
+            const int64_t left = row0 + r < a.rows ? a.cols - (col0 + c) : 0;
+            const int have = left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0;
+            copy16(stage + T::kXBytes + r * T::kZPitch + c, have ? a.z + (row0 + r) * a.ldz + col0 + c : a.z, have);
         }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
-// act(z) to the lane's row of the tile, v *= act'(z).
+// act(z) to h, v *= act'(z).
 template <Act ACT, int FMT>
-__device__ __forceinline__ void back_row(const uint32_t (&zw)[8], float scale, int count, float *tile, float (&v)[32])
+__device__ __forceinline__ void back_row(const uint32_t (&zw)[8], float scale, float *h, float (&v)[32])
 {
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
-        float h[4];
+        float x[4];
 #pragma unroll
         for (int j = 0; j < 4; j += 2) {
-            F2 z = values_of<FMT>((zw[i / 4] >> (8 * j)) & 0xFFFFu) * f2(scale);
-            if (count < 32) {                            // codes past the last column count as zeros
-                const float2 p = parts(z);
-                z = f2(i + j < count ? p.x : 0.0f, i + j + 1 < count ? p.y : 0.0f);
-            }
+            const F2 z = values_of<FMT>((zw[i / 4] >> (8 * j)) & 0xFFFFu) * f2(scale);
             F2 act, slope;
             act_and_slope2<ACT>(z, act, slope);
             const float2 p = parts(f2(v[i + j], v[i + j + 1]) * slope), q = parts(act);
             v[i + j] = p.x;
             v[i + j + 1] = p.y;
-            h[j] = q.x;
-            h[j + 1] = q.y;
+            x[j] = q.x;
+            x[j + 1] = q.y;
         }
-        *reinterpret_cast<float4 *>(tile + i) = make_float4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<float4 *>(h + i) = make_float4(x[0], x[1], x[2], x[3]);
     }
 }
 
-// The lane's column of the tile.
-__device__ __forceinline__ void read_col(const float *tile, int lane, float (&v)[32])
+// dz of one row block as bf16.
+__device__ __forceinline__ void put_dz(const CheckpointArgs &a, int64_t row, int64_t col0, const float (&v)[32])
 {
+    uint16_t *dst = a.dz + row * a.lddz + col0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] = tile[i * kPitch + lane];
+    for (int i = 0; i < 32; i += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 p = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+        if (a.vec_dz && col0 + i + 8 <= a.cols) {
+            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (col0 + i + j < a.cols)
+                    dst[i + j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+        }
+    }
+}
+
+// One column block's codes and scale.
+__device__ __forceinline__ void put_col(const CodesOut &o, bool wide, int64_t col, int64_t row0, const float (&v)[32])
+{
+    const uint32_t code = put_block(v, o.fmt, o.q + col * o.ldq + row0, wide, true);
+    o.s[col * o.lds + row0 / 32] = static_cast<uint8_t>(code);
 }
 
 template <bool BACKWARD, Act ACT>
-__global__ void __launch_bounds__(kWarps * 32, BACKWARD ? 2 : 3) checkpoint_kernel(const __grid_constant__ CheckpointArgs a)
+__global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(const __grid_constant__ CheckpointArgs a)
 {
-    __shared__ __align__(16) float tiles[kWarps][32 * kPitch];
+    using T = Tile<BACKWARD>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    float *computed = reinterpret_cast<float *>(smem + 2 * T::kStage);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    float *tile = tiles[warp];
-    const int64_t strip = blockIdx.x / a.col_blocks, col_block = blockIdx.x % a.col_blocks;
-    const int64_t row_first = (strip * kDown + warp % kDown) * 32 * a.steps;
-    const int64_t col_first = col_block * kBlockCols + warp / kDown * 32 * kAcross;
-    float sum[kAcross];
+    const int64_t strip = blockIdx.x / a.col_blocks;
+    const int64_t col_first = blockIdx.x % a.col_blocks * T::kCols;
+    const int64_t row_first = strip * a.steps * kTileRows;
+    const int64_t left = (a.rows - row_first + kTileRows - 1) / kTileRows;
+    const int steps = static_cast<int>(left < a.steps ? left : a.steps);
+    // The thread's column block: eight neighbouring (pairs of) columns to eight lanes, the four row
+    // blocks of a column to lanes eight apart.
+    const int rb = lane >> 3, cl = warp * 8 + (lane & 7);
+    constexpr int kSums = BACKWARD ? 1 : 2;
+    float sum[kSums];
 #pragma unroll
-    for (int k = 0; k < kAcross; ++k)
+    for (int k = 0; k < kSums; ++k)
         sum[k] = 0.0f;
     pdl_wait_prerequisites();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
-    for (int step = 0; step < a.steps; ++step) {
-        const int64_t row0 = row_first + 32 * step, row = row0 + lane;
-        if (row0 >= a.rows)
-            break;
-        const bool have = row < a.rows;
+    load_tile<BACKWARD>(a, smem_addr(smem), row_first, col_first, threadIdx.x);
+    for (int step = 0; step < steps; ++step) {
+        const int64_t row0 = row_first + static_cast<int64_t>(step) * kTileRows;
+        const uint8_t *stage = smem + (step & 1) * T::kStage;
+        uint32_t zs[T::kUnits];
+        if constexpr (BACKWARD) {
 #pragma unroll
-        for (int k = 0; k < kAcross; ++k) {
-            const int64_t col0 = col_first + 32 * k, col = col0 + lane;
-            if (col0 >= a.cols)
-                break;
-            float v[32];
-            {
-                uint32_t w[16];
+            for (int k = 0; k < T::kUnits; ++k) {
+                int r, b;
+                T::unit(warp, lane, k, r, b);
+                const int64_t row = row0 + r, col0 = col_first + 32 * b;
+                zs[k] = row < a.rows && col0 < a.cols ? a.sz[row * a.ld_sz + col0 / 32] : 127u;
+            }
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        // Every thread is past the tile before, whose memory the next one takes.
+        if (step + 1 < steps)
+            load_tile<BACKWARD>(a, smem_addr(smem + ((step + 1) & 1) * T::kStage), row0 + kTileRows, col_first, threadIdx.x);
+        if (BACKWARD || a.by_row.q) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    w[i] = 0u;
-                uint32_t zw[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-                uint32_t zs = 127u;
-                if (have) {
-                    load_row(a, row, col0, w);
-                    if constexpr (BACKWARD) {
-                        const uint8_t *z = a.z + row * a.ldz + col0;
-                        if (a.wide_z) {
-                            ld_sector(z, zw);
-                        } else {
+            for (int k = 0; k < T::kUnits; ++k) {
+                int r, b;
+                T::unit(warp, lane, k, r, b);
+                const int64_t row = row0 + r, col0 = col_first + 32 * b;
+                const bool have = row < a.rows && col0 < a.cols;
+                float v[32];
+                const uint4 *x = reinterpret_cast<const uint4 *>(stage + T::x_at(r) + 64 * b);
 #pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(z) + i);
-                                zw[4 * i] = q.x;
-                                zw[4 * i + 1] = q.y;
-                                zw[4 * i + 2] = q.z;
-                                zw[4 * i + 3] = q.w;
-                            }
-                        }
-                        zs = a.sz[row * a.ld_sz + col0 / 32];
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 q = x[i];
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        v[8 * i + 2 * j] = bf16_lo(w[j]);
+                        v[8 * i + 2 * j + 1] = bf16_hi(w[j]);
                     }
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[2 * i] = bf16_lo(w[i]);
-                    v[2 * i + 1] = bf16_hi(w[i]);
                 }
                 if constexpr (BACKWARD) {
-                    const int count = static_cast<int>(col0 + 32 <= a.cols ? 32 : a.cols - col0);
+                    float *mine = computed + T::f_at(r) + 32 * b;
+                    const uint4 *z = reinterpret_cast<const uint4 *>(stage + T::kXBytes + r * T::kZPitch + 32 * b);
+                    const uint4 lo = z[0], hi = z[1];
+                    const uint32_t zw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     if (a.fmt_z == 0)
-                        back_row<ACT, 0>(zw, e8m0_value(zs), count, tile + lane * kPitch, v);
+                        back_row<ACT, 0>(zw, e8m0_value(zs[k]), mine, v);
                     else
-                        back_row<ACT, 1>(zw, e8m0_value(zs), count, tile + lane * kPitch, v);
-                }
-            }
-            if constexpr (BACKWARD) {
-                __syncwarp();
-                if (a.act_by_col.q) {
-                    float h[32];
-                    read_col(tile, lane, h);
-                    const uint32_t code = put_block(h, a.act_by_col.fmt, a.act_by_col.q + col * a.act_by_col.ldq + row0, a.wide_ht, col < a.cols);
-                    if (col < a.cols)
-                        a.act_by_col.s[col * a.act_by_col.lds + row0 / 32] = static_cast<uint8_t>(code);
-                }
-                __syncwarp();
-                if (a.dz && have) {
-                    uint16_t *dst = a.dz + row * a.lddz + col0;
+                        back_row<ACT, 1>(zw, e8m0_value(zs[k]), mine, v);
+                    const int64_t col = col_first + cl, block0 = row0 + 32 * rb;
+                    const bool have_col = col < a.cols && block0 < a.rows;
+                    float u[32];
+                    if (a.act_by_col.q) {
+                        __syncthreads();
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const __nv_bfloat162 p = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
-                            w[j] = *reinterpret_cast<const uint32_t *>(&p);
-                        }
-                        if (a.vec_dz && col0 + i + 8 <= a.cols) {
-                            *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[0], w[1], w[2], w[3]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                if (col0 + i + j < a.cols)
-                                    dst[i + j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
-                        }
+                        for (int i = 0; i < 32; ++i)
+                            u[i] = computed[T::f_at(32 * rb) + i * T::kFPitch + cl];
+                        if (have_col)
+                            put_col(a.act_by_col, a.wide_ht, col, block0, u);
                     }
+                    __syncthreads();
+                    if (a.by_col.q || a.sums) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<float4 *>(mine + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    }
+                    if (a.dz && have)
+                        put_dz(a, row, col0, v);
+                    if (a.by_row.q && have) {
+                        const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q, true);
+                        a.by_row.s[row * a.by_row.lds + col0 / 32] = static_cast<uint8_t>(code);
+                    }
+                    if (a.by_col.q || a.sums) {
+                        __syncthreads();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            u[i] = computed[T::f_at(32 * rb) + i * T::kFPitch + cl];
+                        if (a.sums) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                sum[0] += u[i];
+                        }
+                        if (a.by_col.q && have_col)
+                            put_col(a.by_col, a.wide_qt, col, block0, u);
+                    }
+                } else if (have) {
+                    const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q, true);
+                    a.by_row.s[row * a.by_row.lds + col0 / 32] = static_cast<uint8_t>(code);
                 }
             }
+        }
+        if constexpr (!BACKWARD) {
             if (a.by_col.q || a.sums) {
+                uint32_t w[32];
+                const uint8_t *x = stage + T::x_at(32 * rb) + 4 * cl;
 #pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    *reinterpret_cast<float4 *>(tile + lane * kPitch + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            }
-            if (a.by_row.q) {
-                const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q, have);
-                if (have)
-                    a.by_row.s[row * a.by_row.lds + col0 / 32] = static_cast<uint8_t>(code);
-            }
-            if (a.by_col.q || a.sums) {
-                __syncwarp();
-                read_col(tile, lane, v);
-                if (a.sums) {
+                for (int i = 0; i < 32; ++i)
+                    w[i] = *reinterpret_cast<const uint32_t *>(x + i * T::kPitch);
+                const int64_t block0 = row0 + 32 * rb;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int64_t col = col_first + 2 * cl + k;
+                    float v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        sum[k] += v[i];
+                        v[i] = k ? bf16_hi(w[i]) : bf16_lo(w[i]);
+                    if (a.sums) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            sum[k] += v[i];
+                    }
+                    if (a.by_col.q && col < a.cols && block0 < a.rows)
+                        put_col(a.by_col, a.wide_qt, col, block0, v);
                 }
-                if (a.by_col.q) {
-                    const uint32_t code = put_block(v, a.by_col.fmt, a.by_col.q + col * a.by_col.ldq + row0, a.wide_qt, col < a.cols);
-                    if (col < a.cols)
-                        a.by_col.s[col * a.by_col.lds + row0 / 32] = static_cast<uint8_t>(code);
-                }
-                __syncwarp();
             }
         }
     }
     if (!a.sums)
         return;
 #pragma unroll
-    for (int k = 0; k < kAcross; ++k)
-        tile[32 * k + lane] = sum[k];
-    __syncthreads();
-    const int64_t col = col_block * kBlockCols + threadIdx.x;
-    if (threadIdx.x < kBlockCols && col < a.cols) {
-        const int beside = threadIdx.x / (32 * kAcross), at = threadIdx.x % (32 * kAcross);
-        float s = 0.0f;
-#pragma unroll
-        for (int d = 0; d < kDown; ++d)
-            s += tiles[beside * kDown + d][at];
-        (a.strips > 1 ? a.partials + strip * a.cols : a.sums)[col] = s;
+    for (int k = 0; k < kSums; ++k) {
+        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 8);
+        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 16);
+        const int64_t col = col_first + kSums * cl + k;
+        if (rb == 0 && col < a.cols)
+            (a.strips > 1 ? a.partials + strip * a.cols : a.sums)[col] = sum[k];
     }
 }
 
@@ -317,13 +372,16 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(float *a, int64_t na
 
 }  // namespace
 
-int64_t checkpoint_strips(int rows, int cols, int *steps)
+int64_t checkpoint_strips(int rows, int cols, bool backward, int *steps)
 {
-    const int64_t across = (static_cast<int64_t>(cols) + kBlockCols - 1) / kBlockCols;
-    auto strips = [&](int n) { return (static_cast<int64_t>(rows) + 32 * kDown * n - 1) / (32 * kDown * n); };
-    // Four tiles down a warp where that still fills a GB300's 152 SMs three times, else one.
-    *steps = strips(4) * across >= 3 * 152 ? 4 : 1;
-    return strips(*steps);
+    const int wide = backward ? Tile<true>::kCols : Tile<false>::kCols;
+    const int64_t down = (static_cast<int64_t>(rows) + kTileRows - 1) / kTileRows;
+    const int64_t tiles = down * ((static_cast<int64_t>(cols) + wide - 1) / wide);
+    // Resident blocks on a GB300's 152 SMs; tiles below one another in a block as long as that
+    // leaves several rounds of blocks.
+    const int64_t resident = 152 * (backward ? 2 : 3);
+    *steps = tiles >= 16 * resident ? 4 : tiles >= 4 * resident ? 2 : 1;
+    return (down + *steps - 1) / *steps;
 }
 
 cudaError_t launch_sum_partials(float *a, int64_t na, float *b, int64_t nb, const float *partials, int strips, cudaStream_t stream)
@@ -332,23 +390,27 @@ cudaError_t launch_sum_partials(float *a, int64_t na, float *b, int64_t nb, cons
                             partials, strips);
 }
 
+template <bool BACKWARD, Act ACT>
+static cudaError_t start_checkpoint(const CheckpointArgs &a, cudaStream_t stream)
+{
+    constexpr int kBytes = Tile<BACKWARD>::kBytes;
+    const cudaError_t e = opt_in<checkpoint_kernel<BACKWARD, ACT>>(kBytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_dependent(checkpoint_kernel<BACKWARD, ACT>, dim3(static_cast<unsigned>(a.strips * a.col_blocks)), dim3(kThreads), kBytes,
+                            stream, a);
+}
+
 cudaError_t launch_checkpoint(CheckpointArgs &a, bool backward, cudaStream_t stream)
 {
-    a.col_blocks = (static_cast<int64_t>(a.cols) + kBlockCols - 1) / kBlockCols;
+    const int wide_cols = backward ? Tile<true>::kCols : Tile<false>::kCols;
+    a.col_blocks = (static_cast<int64_t>(a.cols) + wide_cols - 1) / wide_cols;
     auto wide = [](const void *p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % 32 == 0 && bytes % 32 == 0; };
-    a.wide_x = wide(a.x, 2 * a.ldx);
-    a.wide_z = wide(a.z, a.ldz);
     a.wide_q = wide(a.by_row.q, a.by_row.ldq);
     a.wide_qt = wide(a.by_col.q, a.by_col.ldq);
     a.wide_ht = wide(a.act_by_col.q, a.act_by_col.ldq);
-    const dim3 grid(static_cast<unsigned>(a.strips * a.col_blocks));
-    cudaError_t e;
-    if (!backward)
-        e = launch_dependent(checkpoint_kernel<false, Act::kNone>, grid, dim3(kWarps * 32), 0, stream, a);
-    else
-        e = with_act(a.act, [&](auto tag) {
-            return launch_dependent(checkpoint_kernel<true, decltype(tag)::value>, grid, dim3(kWarps * 32), 0, stream, a);
-        });
+    cudaError_t e = backward ? with_act(a.act, [&](auto tag) { return start_checkpoint<true, decltype(tag)::value>(a, stream); })
+                             : start_checkpoint<false, Act::kNone>(a, stream);
     if (e == cudaSuccess && a.sums && a.strips > 1)
         e = launch_sum_partials(a.sums, a.cols, nullptr, 0, a.partials, static_cast<int>(a.strips), stream);
     return e;

@@ -39,10 +39,10 @@ struct CheckpointArgs {
     int steps;                  // tiles of a warp along the rows
     int act;
     int vec_dz;                 // dz's rows allow 16-byte stores
-    int wide_x, wide_z, wide_q, wide_qt, wide_ht;   // rows allow 32-byte accesses (set at launch)
+    int wide_q, wide_qt, wide_ht;   // rows allow 32-byte stores (set at launch)
 };
 // Row strips of a call and the tiles of a warp in each: by its sizes alone, so that the sums' order is too.
-int64_t checkpoint_strips(int rows, int cols, int *steps);
+int64_t checkpoint_strips(int rows, int cols, bool backward, int *steps);
 cudaError_t launch_checkpoint(CheckpointArgs &a, bool backward, cudaStream_t stream);
 
 // a[c] and b[c]: sums over the strips of partials[strip][na + nb], in a fixed order; zeros for

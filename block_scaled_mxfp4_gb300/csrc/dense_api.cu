@@ -52,7 +52,7 @@ int check_workspace(size_t need, const void *workspace, size_t bytes)
 
 int run_checkpoint(CheckpointArgs &a, bool backward, const void *workspace, size_t workspace_bytes, cudaStream_t stream)
 {
-    a.strips = checkpoint_strips(a.rows, a.cols, &a.steps);
+    a.strips = checkpoint_strips(a.rows, a.cols, backward, &a.steps);
     if (a.strips * ((static_cast<int64_t>(a.cols) + 31) / 32) > 0x7FFFFFFF)
         return MXFP4_ERR_UNSUPPORTED_SHAPE;              // more blocks than a grid has
     int st = check_workspace(a.sums ? partial_bytes(a.strips, a.cols) : 0, workspace, workspace_bytes);
@@ -108,7 +108,9 @@ size_t mxfp8_checkpoint_workspace_size(int rows, int cols)
     if (rows < 1 || cols < 1 || rows > kMaxCount || cols > kMaxCount)
         return 0;
     int steps = 0;
-    return partial_bytes(checkpoint_strips(rows, cols, &steps), cols);
+    const size_t a = partial_bytes(checkpoint_strips(rows, cols, false, &steps), cols);
+    const size_t b = partial_bytes(checkpoint_strips(rows, cols, true, &steps), cols);
+    return a > b ? a : b;
 }
 
 int mxfp8_checkpoint(void *Q, int64_t ldq, void *S, int64_t lds, void *QT, int64_t ldqt, void *ST, int64_t ldst, float *col_sums,
