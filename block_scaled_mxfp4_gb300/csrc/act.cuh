@@ -3,6 +3,8 @@
 
 #include <cstdint>
 
+#include "pairs.cuh"
+
 namespace mxfp4 {
 
 // The ABI's MXFP4_ACT_* codes.
@@ -22,42 +24,6 @@ __device__ __forceinline__ float ex2_approx(float x)
     return r;
 }
 
-// Two fp32 values in a register pair: one instruction rounds both.
-struct F2 {
-    uint64_t v;
-};
-
-__device__ __forceinline__ F2 f2(float lo, float hi)
-{
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ F2 f2(float both) { return f2(both, both); }
-__device__ __forceinline__ float2 parts(F2 a)
-{
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator*(F2 a, F2 b)
-{
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 operator+(F2 a, F2 b)
-{
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
-{
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
 __device__ __forceinline__ F2 rcp2(F2 a)
 {
     const float2 p = parts(a);

@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "../../include/mxfp4_gemm.h"
+#include "dense.h"
 #include "expert.h"
 #include "internal.h"
 
@@ -1241,12 +1242,12 @@ int mxfp4_device_status(int *status, int reset)
     int st = check_device();
     if (st != MXFP4_OK)
         return st;
-    int grouped = 0, expert = 0;
+    int grouped = 0, expert = 0, checkpoint = 0;
     if (read_device_status(status, reset) != cudaSuccess || read_grouped_status(&grouped, reset) != cudaSuccess ||
-        read_expert_status(&expert, reset) != cudaSuccess)
+        read_expert_status(&expert, reset) != cudaSuccess || read_checkpoint_status(&checkpoint, reset) != cudaSuccess)
         return MXFP4_ERR_CUDA;
     if (*status == MXFP4_OK)
-        *status = grouped != MXFP4_OK ? grouped : expert;
+        *status = grouped != MXFP4_OK ? grouped : expert != MXFP4_OK ? expert : checkpoint;
     return MXFP4_OK;
 }
 

@@ -23,17 +23,19 @@ namespace {
 // the load to the one rounding of each orientation.
 //
 // A block of 256 threads takes tiles of 128 rows, one below the other, by 128
-// columns (64 in the backward pass), copied to shared memory asynchronously while
-// the tile before is worked on.  A lane then takes 32 values of a row, and 32 of a
+// columns (64 in the backward pass), copied to shared memory by TMA while the tile
+// before is worked on.  A lane then takes 32 values of a row, and 32 of a
 // column: a block of either orientation is one lane's, and nothing needs a
-// shuffle.  Lanes are dealt so that a warp's accesses fall into whole
-// lines (128 bytes of codes are four lanes') and on different banks.  In the
-// backward pass the computed values go through shared memory as fp32, act(z) and
-// dz in turn.
+// shuffle.  Lanes are dealt so that a warp's stores fall into whole lines (128
+// bytes of codes are four lanes') and its shared-memory reads on different banks:
+// TMA's swizzle moves 16-byte pieces by the row, and lanes 32 rows apart read
+// their column's rows in orders of their own (put_col).  In the backward pass the
+// computed values go through shared memory as fp32, act(z) and dz in turn.
 //
 // Why not straight from global memory, a row or column per lane: each such
 // access touches 32 lines, and the L1's tag stage, one line a cycle, was 80 %
-// busy at half of HBM's rate.
+// busy at half of HBM's rate.  Copies by cp.async instead of TMA took as many of
+// its cycles as all stores together.
 
 constexpr int kThreads = 256;
 constexpr int kTileRows = 128;
@@ -41,18 +43,16 @@ constexpr int kTileRows = 128;
 template <bool BACKWARD>
 struct Tile {
     static constexpr int kCols = BACKWARD ? 64 : 128;
-    static constexpr int kPitch = 2 * kCols + 16;        // bytes between x's rows: 4 words past a multiple of 32
-    static constexpr int kSkew = 32;                     // more before each 32 rows: lanes 32 rows apart meet no bank twice
-    static constexpr int kXBytes = kTileRows * kPitch + 4 * kSkew;
-    static constexpr int kZPitch = 80;
-    static constexpr int kZBytes = BACKWARD ? kTileRows * kZPitch : 0;
+    static constexpr int kBox = kTileRows * 128;         // 64 columns of x: 128-byte rows, 128-byte swizzle
+    static constexpr int kXBytes = kCols / 64 * kBox;
+    static constexpr int kZBytes = BACKWARD ? kTileRows * 64 : 0;   // 64-byte rows, 64-byte swizzle
     static constexpr int kStage = kXBytes + kZBytes;
     static constexpr int kFPitch = 68;                   // floats between rows of computed values
     static constexpr int kFBytes = BACKWARD ? (kTileRows * kFPitch + 32) * 4 : 0;
-    static constexpr int kBytes = 2 * kStage + kFBytes;
+    static constexpr int kBytes = 2 * kStage + kFBytes + 1024;      // with the alignment that the swizzle asks for
     static constexpr int kUnits = kTileRows * kCols / 32 / kThreads;   // row blocks of a thread
 
-    static __device__ __forceinline__ int x_at(int row) { return row * kPitch + row / 32 * kSkew; }
+    // Eight floats more before each 32 rows: lanes 32 rows apart meet no bank twice.
     static __device__ __forceinline__ int f_at(int row) { return row * kFPitch + row / 32 * 8; }
     // Row and 32-column block of a thread's unit k: eight neighbouring rows to eight neighbouring lanes.
     static __device__ __forceinline__ void unit(int warp, int lane, int k, int &row, int &b)
@@ -67,11 +67,7 @@ struct Tile {
     }
 };
 
-// 16 bytes, the first `have` of them from src and the rest zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int have)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have) : "memory");
-}
+__device__ int g_status = 0;                     // bounded waits that ran out
 
 __device__ __forceinline__ void st_sector(void *p, const uint32_t (&w)[8], bool wide)
 {
@@ -84,12 +80,11 @@ __device__ __forceinline__ void st_sector(void *p, const uint32_t (&w)[8], bool 
 }
 
 // One block of a lane: its codes to q; the scale code.
-__device__ __forceinline__ uint32_t put_block(const float (&v)[32], int fmt, uint8_t *q, bool wide, bool store)
+__device__ __forceinline__ uint32_t put_block(const float (&v)[32], int fmt, uint8_t *q, bool wide)
 {
     uint32_t w[8];
-    const uint32_t code = fmt == 0 ? quantize_block<QuantFmt::kE4M3>(v, w) : quantize_block<QuantFmt::kE5M2>(v, w);
-    if (store)
-        st_sector(q, w, wide);
+    const uint32_t code = fmt == 0 ? quantize_block_pairs<QuantFmt::kE4M3>(v, w) : quantize_block_pairs<QuantFmt::kE5M2>(v, w);
+    st_sector(q, w, wide);
     return code;
 }
 
@@ -113,30 +108,18 @@ __device__ __forceinline__ float e8m0_value(uint32_t code)
     return code == 0u ? __uint_as_float(0x00400000u) : code == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(code << 23);
 }
 
-// Start the copies of one tile; what lies past the last row or column becomes zeros.
+// Start the copies of one tile; what lies past the last row or column arrives as zeros.
 template <bool BACKWARD>
-__device__ __forceinline__ void load_tile(const CheckpointArgs &a, uint32_t stage, int64_t row0, int64_t col0, int t)
+__device__ __forceinline__ void load_tile(const CUtensorMap *x, const CUtensorMap *z, uint8_t *stage, uint64_t *full, int64_t row0, int64_t col0)
 {
     using T = Tile<BACKWARD>;
-    constexpr int kChunks = T::kCols / 8;                // 16-byte pieces of a row
+    const uint64_t policy = l2_policy_evict_first();
+    mbar_arrive_expect_tx(full, T::kStage);
 #pragma unroll
-    for (int i = 0; i < kTileRows * kChunks / kThreads; ++i) {
-        const int at = i * kThreads + t, r = at / kChunks, c = at % kChunks * 8;
-        const int64_t left = row0 + r < a.rows ? a.cols - (col0 + c) : 0;
-        const int have = left >= 8 ? 16 : left > 0 ? static_cast<int>(left) * 2 : 0;
-        copy16(stage + T::x_at(r) + 2 * c, have ? a.x + (row0 + r) * a.ldx + col0 + c : a.x, have);
-    }
-    if constexpr (BACKWARD) {
-        constexpr int kZChunks = T::kCols / 16;
-#pragma unroll
-        for (int i = 0; i < kTileRows * kZChunks / kThreads; ++i) {
-            const int at = i * kThreads + t, r = at / kZChunks, c = at % kZChunks * 16;
-            const int64_t left = row0 + r < a.rows ? a.cols - (col0 + c) : 0;
-            const int have = left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0;
-            copy16(stage + T::kXBytes + r * T::kZPitch + c, have ? a.z + (row0 + r) * a.ldz + col0 + c : a.z, have);
-        }
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (int k = 0; k < T::kCols / 64; ++k)
+        tma_load_2d(stage + k * T::kBox, x, full, static_cast<int>(col0) + 64 * k, static_cast<int>(row0), policy);
+    if constexpr (BACKWARD)
+        tma_load_2d(stage + T::kXBytes, z, full, static_cast<int>(col0), static_cast<int>(row0), policy);
 }
 
 // act(z) to h, v *= act'(z).
@@ -184,18 +167,35 @@ __device__ __forceinline__ void put_dz(const CheckpointArgs &a, int64_t row, int
     }
 }
 
-// One column block's codes and scale.
-__device__ __forceinline__ void put_col(const CodesOut &o, bool wide, int64_t col, int64_t row0, const float (&v)[32])
+// One column block's codes and scale.  v[i] is row i ^ ROWS of the block (0, 2, 4 or 6): the codes
+// change places accordingly, in units of two.
+template <bool PERMUTED>
+__device__ __forceinline__ void put_col(const CodesOut &o, bool wide, int64_t col, int64_t row0, int rows, const float (&v)[32])
 {
-    const uint32_t code = put_block(v, o.fmt, o.q + col * o.ldq + row0, wide, true);
+    uint32_t w[8];
+    const uint32_t code = o.fmt == 0 ? quantize_block_pairs<QuantFmt::kE4M3>(v, w) : quantize_block_pairs<QuantFmt::kE5M2>(v, w);
+    if constexpr (PERMUTED) {
+        const uint32_t order = rows & 2 ? 0x1032u : 0x3210u;
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const uint32_t lo = __byte_perm(w[i], 0u, order), hi = __byte_perm(w[i + 1], 0u, order);
+            w[i] = rows & 4 ? hi : lo;
+            w[i + 1] = rows & 4 ? lo : hi;
+        }
+    }
+    st_sector(o.q + col * o.ldq + row0, w, wide);
     o.s[col * o.lds + row0 / 32] = static_cast<uint8_t>(code);
 }
 
 template <bool BACKWARD, Act ACT>
-__global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(const __grid_constant__ CheckpointArgs a)
+__global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3)
+    checkpoint_kernel(const __grid_constant__ CheckpointArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mz)
 {
     using T = Tile<BACKWARD>;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint64_t full[2];
+    __shared__ int abort_flag;
+    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     float *computed = reinterpret_cast<float *>(smem + 2 * T::kStage);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t strip = blockIdx.x / a.col_blocks;
@@ -207,17 +207,23 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(
     // blocks of a column to lanes eight apart.
     const int rb = lane >> 3, cl = warp * 8 + (lane & 7);
     constexpr int kSums = BACKWARD ? 1 : 2;
-    float sum[kSums];
-#pragma unroll
-    for (int k = 0; k < kSums; ++k)
-        sum[k] = 0.0f;
+    F2 sum = f2(0.0f);                                   // of two columns, or of one column's rows two by two
+    if (threadIdx.x == 0) {
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
     pdl_wait_prerequisites();
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0) {
         pdl_launch_dependents();
-    load_tile<BACKWARD>(a, smem_addr(smem), row_first, col_first, threadIdx.x);
+        load_tile<BACKWARD>(&mx, &mz, smem, &full[0], row_first, col_first);
+    }
     for (int step = 0; step < steps; ++step) {
         const int64_t row0 = row_first + static_cast<int64_t>(step) * kTileRows;
-        const uint8_t *stage = smem + (step & 1) * T::kStage;
+        const int at = step & 1;
+        const uint8_t *stage = smem + at * T::kStage;
         uint32_t zs[T::kUnits];
         if constexpr (BACKWARD) {
 #pragma unroll
@@ -228,11 +234,15 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(
                 zs[k] = row < a.rows && col0 < a.cols ? a.sz[row * a.ld_sz + col0 / 32] : 127u;
             }
         }
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();
+        const bool ok = mbar_wait(&full[at], (step >> 1) & 1, &abort_flag, a.wait_limit, &g_status);
+        if (__syncthreads_or(!ok)) {
+            if (threadIdx.x == 0)
+                mbar_wait_drain(&full[at], (step >> 1) & 1, a.wait_limit);   // its copies land before the block leaves
+            return;
+        }
         // Every thread is past the tile before, whose memory the next one takes.
-        if (step + 1 < steps)
-            load_tile<BACKWARD>(a, smem_addr(smem + ((step + 1) & 1) * T::kStage), row0 + kTileRows, col_first, threadIdx.x);
+        if (step + 1 < steps && threadIdx.x == 0)
+            load_tile<BACKWARD>(&mx, &mz, smem + (at ^ 1) * T::kStage, &full[at ^ 1], row0 + kTileRows, col_first);
         if (BACKWARD || a.by_row.q) {
 #pragma unroll
             for (int k = 0; k < T::kUnits; ++k) {
@@ -241,10 +251,10 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(
                 const int64_t row = row0 + r, col0 = col_first + 32 * b;
                 const bool have = row < a.rows && col0 < a.cols;
                 float v[32];
-                const uint4 *x = reinterpret_cast<const uint4 *>(stage + T::x_at(r) + 64 * b);
+                const uint8_t *x = stage + (b >> 1) * T::kBox + r * 128;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint4 q = x[i];
+                    const uint4 q = *reinterpret_cast<const uint4 *>(x + (((b & 1) * 4 + i) ^ (r & 7)) * 16);
                     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -254,8 +264,9 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(
                 }
                 if constexpr (BACKWARD) {
                     float *mine = computed + T::f_at(r) + 32 * b;
-                    const uint4 *z = reinterpret_cast<const uint4 *>(stage + T::kXBytes + r * T::kZPitch + 32 * b);
-                    const uint4 lo = z[0], hi = z[1];
+                    const uint8_t *z = stage + T::kXBytes + r * 64;
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(z + ((2 * b) ^ ((r >> 1) & 3)) * 16);
+                    const uint4 hi = *reinterpret_cast<const uint4 *>(z + ((2 * b + 1) ^ ((r >> 1) & 3)) * 16);
                     const uint32_t zw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     if (a.fmt_z == 0)
                         back_row<ACT, 0>(zw, e8m0_value(zs[k]), mine, v);
@@ -270,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(
                         for (int i = 0; i < 32; ++i)
                             u[i] = computed[T::f_at(32 * rb) + i * T::kFPitch + cl];
                         if (have_col)
-                            put_col(a.act_by_col, a.wide_ht, col, block0, u);
+                            put_col<false>(a.act_by_col, a.wide_ht, col, block0, 0, u);
                     }
                     __syncthreads();
                     if (a.by_col.q || a.sums) {
@@ -281,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(
                     if (a.dz && have)
                         put_dz(a, row, col0, v);
                     if (a.by_row.q && have) {
-                        const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q, true);
+                        const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q);
                         a.by_row.s[row * a.by_row.lds + col0 / 32] = static_cast<uint8_t>(code);
                     }
                     if (a.by_col.q || a.sums) {
@@ -291,53 +302,60 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3) checkpoint_kernel(
                             u[i] = computed[T::f_at(32 * rb) + i * T::kFPitch + cl];
                         if (a.sums) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                sum[0] += u[i];
+                            for (int i = 0; i < 32; i += 2)
+                                sum = sum + f2(u[i], u[i + 1]);
                         }
                         if (a.by_col.q && have_col)
-                            put_col(a.by_col, a.wide_qt, col, block0, u);
+                            put_col<false>(a.by_col, a.wide_qt, col, block0, 0, u);
                     }
                 } else if (have) {
-                    const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q, true);
+                    const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q);
                     a.by_row.s[row * a.by_row.lds + col0 / 32] = static_cast<uint8_t>(code);
                 }
             }
         }
         if constexpr (!BACKWARD) {
             if (a.by_col.q || a.sums) {
+                // Word cl of the tile's rows (two columns): piece (cl % 32) / 4 of box cl / 32.
                 uint32_t w[32];
-                const uint8_t *x = stage + T::x_at(32 * rb) + 4 * cl;
+                const uint8_t *x = stage + (cl >> 5) * T::kBox + 32 * rb * 128 + 4 * (cl & 3);
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    w[i] = *reinterpret_cast<const uint32_t *>(x + i * T::kPitch);
+                for (int i = 0; i < 32; ++i) {
+                    const int r = i ^ (2 * rb);
+                    w[i] = *reinterpret_cast<const uint32_t *>(x + r * 128 + (((cl & 31) >> 2) ^ (r & 7)) * 16);
+                }
                 const int64_t block0 = row0 + 32 * rb;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int64_t col = col_first + 2 * cl + k;
-                    float v[32];
+                if (a.sums) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        v[i] = k ? bf16_hi(w[i]) : bf16_lo(w[i]);
-                    if (a.sums) {
+                        sum = sum + f2(bf16_lo(w[i]), bf16_hi(w[i]));
+                }
+                if (a.by_col.q) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int64_t col = col_first + 2 * cl + k;
+                        float v[32];
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            sum[k] += v[i];
+                            v[i] = k ? bf16_hi(w[i]) : bf16_lo(w[i]);
+                        if (col < a.cols && block0 < a.rows)
+                            put_col<true>(a.by_col, a.wide_qt, col, block0, 2 * rb, v);
                     }
-                    if (a.by_col.q && col < a.cols && block0 < a.rows)
-                        put_col(a.by_col, a.wide_qt, col, block0, v);
                 }
             }
         }
     }
     if (!a.sums)
         return;
+    const float2 two = parts(sum);
+    float total[2] = {BACKWARD ? two.x + two.y : two.x, two.y};
 #pragma unroll
     for (int k = 0; k < kSums; ++k) {
-        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 8);
-        sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], 16);
+        total[k] += __shfl_xor_sync(0xffffffffu, total[k], 8);
+        total[k] += __shfl_xor_sync(0xffffffffu, total[k], 16);
         const int64_t col = col_first + kSums * cl + k;
         if (rb == 0 && col < a.cols)
-            (a.strips > 1 ? a.partials + strip * a.cols : a.sums)[col] = sum[k];
+            (a.strips > 1 ? a.partials + strip * a.cols : a.sums)[col] = total[k];
     }
 }
 
@@ -391,17 +409,17 @@ cudaError_t launch_sum_partials(float *a, int64_t na, float *b, int64_t nb, cons
 }
 
 template <bool BACKWARD, Act ACT>
-static cudaError_t start_checkpoint(const CheckpointArgs &a, cudaStream_t stream)
+static cudaError_t start_checkpoint(const CheckpointArgs &a, const CUtensorMap &mx, const CUtensorMap &mz, cudaStream_t stream)
 {
     constexpr int kBytes = Tile<BACKWARD>::kBytes;
     const cudaError_t e = opt_in<checkpoint_kernel<BACKWARD, ACT>>(kBytes);
     if (e != cudaSuccess)
         return e;
     return launch_dependent(checkpoint_kernel<BACKWARD, ACT>, dim3(static_cast<unsigned>(a.strips * a.col_blocks)), dim3(kThreads), kBytes,
-                            stream, a);
+                            stream, a, mx, mz);
 }
 
-cudaError_t launch_checkpoint(CheckpointArgs &a, bool backward, cudaStream_t stream)
+cudaError_t launch_checkpoint(CheckpointArgs &a, const CUtensorMap &mx, const CUtensorMap &mz, bool backward, cudaStream_t stream)
 {
     const int wide_cols = backward ? Tile<true>::kCols : Tile<false>::kCols;
     a.col_blocks = (static_cast<int64_t>(a.cols) + wide_cols - 1) / wide_cols;
@@ -409,11 +427,20 @@ cudaError_t launch_checkpoint(CheckpointArgs &a, bool backward, cudaStream_t str
     a.wide_q = wide(a.by_row.q, a.by_row.ldq);
     a.wide_qt = wide(a.by_col.q, a.by_col.ldq);
     a.wide_ht = wide(a.act_by_col.q, a.act_by_col.ldq);
-    cudaError_t e = backward ? with_act(a.act, [&](auto tag) { return start_checkpoint<true, decltype(tag)::value>(a, stream); })
-                             : start_checkpoint<false, Act::kNone>(a, stream);
+    cudaError_t e = backward ? with_act(a.act, [&](auto tag) { return start_checkpoint<true, decltype(tag)::value>(a, mx, mz, stream); })
+                             : start_checkpoint<false, Act::kNone>(a, mx, mz, stream);
     if (e == cudaSuccess && a.sums && a.strips > 1)
         e = launch_sum_partials(a.sums, a.cols, nullptr, 0, a.partials, static_cast<int>(a.strips), stream);
     return e;
+}
+
+cudaError_t read_checkpoint_status(int *status, int reset)
+{
+    const cudaError_t e = cudaMemcpyFromSymbol(status, g_status, sizeof(int));
+    if (e != cudaSuccess || !reset)
+        return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
 }
 
 }  // namespace mxfp4

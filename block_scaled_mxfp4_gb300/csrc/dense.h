@@ -5,6 +5,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -40,10 +41,13 @@ struct CheckpointArgs {
     int act;
     int vec_dz;                 // dz's rows allow 16-byte stores
     int wide_q, wide_qt, wide_ht;   // rows allow 32-byte stores (set at launch)
+    long long wait_limit;
 };
 // Row strips of a call and the tiles of a warp in each: by its sizes alone, so that the sums' order is too.
 int64_t checkpoint_strips(int rows, int cols, bool backward, int *steps);
-cudaError_t launch_checkpoint(CheckpointArgs &a, bool backward, cudaStream_t stream);
+// mx: x in boxes of 64 columns x 128 rows, 128-byte swizzle; mz (backward): z likewise, 64-byte swizzle.
+cudaError_t launch_checkpoint(CheckpointArgs &a, const CUtensorMap &mx, const CUtensorMap &mz, bool backward, cudaStream_t stream);
+cudaError_t read_checkpoint_status(int *status, int reset);
 
 // a[c] and b[c]: sums over the strips of partials[strip][na + nb], in a fixed order; zeros for
 // no strips.  Either array may be null.

@@ -50,6 +50,21 @@ int check_workspace(size_t need, const void *workspace, size_t bytes)
     return aligned(workspace, kAlign) ? MXFP4_OK : MXFP4_ERR_MISALIGNED;
 }
 
+// Rows of `size`-byte elements in boxes of 64 columns x 128 rows, zeros past the last ones.
+bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, int rows, int cols, int64_t ld, int size, CUtensorMapSwizzle swizzle)
+{
+    auto enc = tensor_map_encode_fn();
+    if (!enc)
+        return false;
+    if (rows == 1)
+        ld = (static_cast<int64_t>(cols) + 15) / 16 * 16;    // a lone row's stride can be anything
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(size)};
+    const cuuint32_t box[2] = {64, 128}, ones[2] = {1, 1};
+    return enc(map, type, 2, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int run_checkpoint(CheckpointArgs &a, bool backward, const void *workspace, size_t workspace_bytes, cudaStream_t stream)
 {
     a.strips = checkpoint_strips(a.rows, a.cols, backward, &a.steps);
@@ -63,7 +78,13 @@ int run_checkpoint(CheckpointArgs &a, bool backward, const void *workspace, size
     if (st != MXFP4_OK)
         return st;
     a.partials = static_cast<float *>(const_cast<void *>(workspace));
-    return status_of(launch_checkpoint(a, backward, stream));
+    a.wait_limit = current_wait_limit();
+    CUtensorMap mx, mz;
+    std::memset(&mz, 0, sizeof(mz));
+    if (!encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.rows, a.cols, a.ldx, 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        (backward && !encode(&mz, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.z, a.rows, a.cols, a.ldz, 1, CU_TENSOR_MAP_SWIZZLE_64B)))
+        return MXFP4_ERR_CUDA;
+    return status_of(launch_checkpoint(a, mx, mz, backward, stream));
 }
 
 // Rows of 16-bit values as the checkpoint kernels read them.

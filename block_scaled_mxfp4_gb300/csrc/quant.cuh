@@ -6,6 +6,8 @@
 
 #include <cstdint>
 
+#include "pairs.cuh"
+
 namespace mxfp4 {
 
 // Largest s with 6 * 2^s <= a for a finite a > 0 (float bits): a = f * 2^e
@@ -122,6 +124,28 @@ __device__ __forceinline__ uint32_t quantize_block(const float (&x)[32], uint32_
             out[w] = f8x2<kF>(x[4 * w] * inv, x[4 * w + 1] * inv) |
                      (f8x2<kF>(x[4 * w + 2] * inv, x[4 * w + 3] * inv) << 16);
         }
+    }
+    return finite ? static_cast<uint32_t>(s + 127) : 0xFFu;
+}
+
+// quantize_block for a byte format, scaled two values at a time (the same codes).
+template <QuantFmt Q>
+__device__ __forceinline__ uint32_t quantize_block_pairs(const float (&x)[32], uint32_t (&out)[8])
+{
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        amax = max_abs3(amax, x[i], x[i + 1]);
+    const bool finite = amax <= 3.402823466e38f;     // not for infinities and NaN
+    if (!finite)
+        amax = 0.0f;
+    const int s = block_exponent8(amax, Q == QuantFmt::kE4M3 ? 8 : 15);
+    const F2 inv = f2(exp2_neg(s));
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        constexpr int kF = Q == QuantFmt::kE4M3 ? 0 : 1;
+        const float2 lo = parts(f2(x[4 * w], x[4 * w + 1]) * inv), hi = parts(f2(x[4 * w + 2], x[4 * w + 3]) * inv);
+        out[w] = f8x2<kF>(lo.x, lo.y) | (f8x2<kF>(hi.x, hi.y) << 16);
     }
     return finite ? static_cast<uint32_t>(s + 127) : 0xFFu;
 }
