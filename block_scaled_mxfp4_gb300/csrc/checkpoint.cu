@@ -30,7 +30,7 @@ namespace {
 // bytes of codes are four lanes') and its shared-memory reads on different banks:
 // TMA's swizzle moves 16-byte pieces by the row, and lanes 32 rows apart read
 // their column's rows in orders of their own (put_col).  In the backward pass the
-// computed values go through shared memory as fp32, act(z) and dz in turn.
+// computed values go through shared memory as fp32.
 //
 // Why not straight from global memory, a row or column per lane: each such
 // access touches 32 lines, and the L1's tag stage, one line a cycle, was 80 %
@@ -47,9 +47,11 @@ struct Tile {
     static constexpr int kXBytes = kCols / 64 * kBox;
     static constexpr int kZBytes = BACKWARD ? kTileRows * 64 : 0;   // 64-byte rows, 64-byte swizzle
     static constexpr int kStage = kXBytes + kZBytes;
+    // The backward pass has one stage: the row pass empties it, and it fills again under the column passes.
+    static constexpr int kStages = BACKWARD ? 1 : 2;
     static constexpr int kFPitch = 68;                   // floats between rows of computed values
-    static constexpr int kFBytes = BACKWARD ? (kTileRows * kFPitch + 32) * 4 : 0;
-    static constexpr int kBytes = 2 * kStage + kFBytes + 1024;      // with the alignment that the swizzle asks for
+    static constexpr int kF = BACKWARD ? kTileRows * kFPitch + 32 : 0;     // floats of act(z), and of dz
+    static constexpr int kBytes = kStages * kStage + 2 * kF * 4 + 1024;    // with the alignment that the swizzle asks for
     static constexpr int kUnits = kTileRows * kCols / 32 / kThreads;   // row blocks of a thread
 
     // Eight floats more before each 32 rows: lanes 32 rows apart meet no bank twice.
@@ -196,7 +198,6 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3)
     __shared__ uint64_t full[2];
     __shared__ int abort_flag;
     uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    float *computed = reinterpret_cast<float *>(smem + 2 * T::kStage);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t strip = blockIdx.x / a.col_blocks;
     const int64_t col_first = blockIdx.x % a.col_blocks * T::kCols;
@@ -220,28 +221,29 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3)
         pdl_launch_dependents();
         load_tile<BACKWARD>(&mx, &mz, smem, &full[0], row_first, col_first);
     }
+    // The scale of the thread's row block of z, in the tile that starts at row0.
+    auto z_scale = [&](int64_t row0) -> uint32_t {
+        int r, b;
+        T::unit(warp, lane, 0, r, b);
+        const int64_t row = row0 + r, col0 = col_first + 32 * b;
+        return row < a.rows && col0 < a.cols ? a.sz[row * a.ld_sz + col0 / 32] : 127u;
+    };
+    uint32_t zs = 127u;
+    if constexpr (BACKWARD)
+        zs = z_scale(row_first);
     for (int step = 0; step < steps; ++step) {
         const int64_t row0 = row_first + static_cast<int64_t>(step) * kTileRows;
-        const int at = step & 1;
+        const int at = step % T::kStages;
+        const uint32_t phase = step / T::kStages & 1;
         const uint8_t *stage = smem + at * T::kStage;
-        uint32_t zs[T::kUnits];
-        if constexpr (BACKWARD) {
-#pragma unroll
-            for (int k = 0; k < T::kUnits; ++k) {
-                int r, b;
-                T::unit(warp, lane, k, r, b);
-                const int64_t row = row0 + r, col0 = col_first + 32 * b;
-                zs[k] = row < a.rows && col0 < a.cols ? a.sz[row * a.ld_sz + col0 / 32] : 127u;
-            }
-        }
-        const bool ok = mbar_wait(&full[at], (step >> 1) & 1, &abort_flag, a.wait_limit, &g_status);
+        const bool ok = mbar_wait(&full[at], phase, &abort_flag, a.wait_limit, &g_status);
         if (__syncthreads_or(!ok)) {
             if (threadIdx.x == 0)
-                mbar_wait_drain(&full[at], (step >> 1) & 1, a.wait_limit);   // its copies land before the block leaves
+                mbar_wait_drain(&full[at], phase, a.wait_limit);     // its copies land before the block leaves
             return;
         }
-        // Every thread is past the tile before, whose memory the next one takes.
-        if (step + 1 < steps && threadIdx.x == 0)
+        // Every thread is past the tile before.
+        if (!BACKWARD && step + 1 < steps && threadIdx.x == 0)
             load_tile<BACKWARD>(&mx, &mz, smem + (at ^ 1) * T::kStage, &full[at ^ 1], row0 + kTileRows, col_first);
         if (BACKWARD || a.by_row.q) {
 #pragma unroll
@@ -263,84 +265,83 @@ __global__ void __launch_bounds__(kThreads, BACKWARD ? 2 : 3)
                     }
                 }
                 if constexpr (BACKWARD) {
-                    float *mine = computed + T::f_at(r) + 32 * b;
+                    float *h = reinterpret_cast<float *>(smem + T::kStage) + T::f_at(r) + 32 * b;
                     const uint8_t *z = stage + T::kXBytes + r * 64;
                     const uint4 lo = *reinterpret_cast<const uint4 *>(z + ((2 * b) ^ ((r >> 1) & 3)) * 16);
                     const uint4 hi = *reinterpret_cast<const uint4 *>(z + ((2 * b + 1) ^ ((r >> 1) & 3)) * 16);
                     const uint32_t zw[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                     if (a.fmt_z == 0)
-                        back_row<ACT, 0>(zw, e8m0_value(zs[k]), mine, v);
+                        back_row<ACT, 0>(zw, e8m0_value(zs), h, v);
                     else
-                        back_row<ACT, 1>(zw, e8m0_value(zs[k]), mine, v);
-                    const int64_t col = col_first + cl, block0 = row0 + 32 * rb;
-                    const bool have_col = col < a.cols && block0 < a.rows;
-                    float u[32];
-                    if (a.act_by_col.q) {
-                        __syncthreads();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            u[i] = computed[T::f_at(32 * rb) + i * T::kFPitch + cl];
-                        if (have_col)
-                            put_col<false>(a.act_by_col, a.wide_ht, col, block0, 0, u);
-                    }
-                    __syncthreads();
+                        back_row<ACT, 1>(zw, e8m0_value(zs), h, v);
+                    if (step + 1 < steps)
+                        zs = z_scale(row0 + kTileRows);
                     if (a.by_col.q || a.sums) {
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(mine + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                            *reinterpret_cast<float4 *>(h + T::kF + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                     }
                     if (a.dz && have)
                         put_dz(a, row, col0, v);
-                    if (a.by_row.q && have) {
-                        const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q);
-                        a.by_row.s[row * a.by_row.lds + col0 / 32] = static_cast<uint8_t>(code);
-                    }
-                    if (a.by_col.q || a.sums) {
-                        __syncthreads();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            u[i] = computed[T::f_at(32 * rb) + i * T::kFPitch + cl];
-                        if (a.sums) {
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2)
-                                sum = sum + f2(u[i], u[i + 1]);
-                        }
-                        if (a.by_col.q && have_col)
-                            put_col<false>(a.by_col, a.wide_qt, col, block0, 0, u);
-                    }
-                } else if (have) {
+                }
+                if (a.by_row.q && have) {
                     const uint32_t code = put_block(v, a.by_row.fmt, a.by_row.q + row * a.by_row.ldq + col0, a.wide_q);
                     a.by_row.s[row * a.by_row.lds + col0 / 32] = static_cast<uint8_t>(code);
                 }
             }
         }
-        if constexpr (!BACKWARD) {
-            if (a.by_col.q || a.sums) {
-                // Word cl of the tile's rows (two columns): piece (cl % 32) / 4 of box cl / 32.
-                uint32_t w[32];
-                const uint8_t *x = stage + (cl >> 5) * T::kBox + 32 * rb * 128 + 4 * (cl & 3);
+        const int64_t block0 = row0 + 32 * rb;
+        if constexpr (BACKWARD) {
+            __syncthreads();
+            if (step + 1 < steps && threadIdx.x == 0)
+                load_tile<BACKWARD>(&mx, &mz, smem, &full[0], row0 + kTileRows, col_first);
+            const int64_t col = col_first + cl;
+            const bool have = col < a.cols && block0 < a.rows;
+            const float *h = reinterpret_cast<const float *>(smem + T::kStage) + T::f_at(32 * rb) + cl;
+            float u[32];
+            if (a.act_by_col.q) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int r = i ^ (2 * rb);
-                    w[i] = *reinterpret_cast<const uint32_t *>(x + r * 128 + (((cl & 31) >> 2) ^ (r & 7)) * 16);
-                }
-                const int64_t block0 = row0 + 32 * rb;
+                for (int i = 0; i < 32; ++i)
+                    u[i] = h[i * T::kFPitch];
+                if (have)
+                    put_col<false>(a.act_by_col, a.wide_ht, col, block0, 0, u);
+            }
+            if (a.by_col.q || a.sums) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    u[i] = h[T::kF + i * T::kFPitch];
                 if (a.sums) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        sum = sum + f2(bf16_lo(w[i]), bf16_hi(w[i]));
+                    for (int i = 0; i < 32; i += 2)
+                        sum = sum + f2(u[i], u[i + 1]);
                 }
-                if (a.by_col.q) {
+                if (a.by_col.q && have)
+                    put_col<false>(a.by_col, a.wide_qt, col, block0, 0, u);
+            }
+        } else if (a.by_col.q || a.sums) {
+            // Word cl of the tile's rows (two columns): piece (cl % 32) / 4 of box cl / 32.
+            uint32_t w[32];
+            const uint8_t *x = stage + (cl >> 5) * T::kBox + 32 * rb * 128 + 4 * (cl & 3);
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int64_t col = col_first + 2 * cl + k;
-                        float v[32];
+            for (int i = 0; i < 32; ++i) {
+                const int r = i ^ (2 * rb);
+                w[i] = *reinterpret_cast<const uint32_t *>(x + r * 128 + (((cl & 31) >> 2) ^ (r & 7)) * 16);
+            }
+            if (a.sums) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = k ? bf16_hi(w[i]) : bf16_lo(w[i]);
-                        if (col < a.cols && block0 < a.rows)
-                            put_col<true>(a.by_col, a.wide_qt, col, block0, 2 * rb, v);
-                    }
+                for (int i = 0; i < 32; ++i)
+                    sum = sum + f2(bf16_lo(w[i]), bf16_hi(w[i]));
+            }
+            if (a.by_col.q) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int64_t col = col_first + 2 * cl + k;
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = k ? bf16_hi(w[i]) : bf16_lo(w[i]);
+                    if (col < a.cols && block0 < a.rows)
+                        put_col<true>(a.by_col, a.wide_qt, col, block0, 2 * rb, v);
                 }
             }
         }
