@@ -1242,12 +1242,17 @@ int mxfp4_device_status(int *status, int reset)
     int st = check_device();
     if (st != MXFP4_OK)
         return st;
-    int grouped = 0, expert = 0, checkpoint = 0;
-    if (read_device_status(status, reset) != cudaSuccess || read_grouped_status(&grouped, reset) != cudaSuccess ||
-        read_expert_status(&expert, reset) != cudaSuccess || read_checkpoint_status(&checkpoint, reset) != cudaSuccess)
-        return MXFP4_ERR_CUDA;
-    if (*status == MXFP4_OK)
-        *status = grouped != MXFP4_OK ? grouped : expert != MXFP4_OK ? expert : checkpoint;
+    // Each translation unit's kernels have a word of their own; the first that is set counts.
+    cudaError_t (*const words[])(int *, int) = {read_device_status, read_grouped_status, read_expert_status, read_checkpoint_status,
+                                                read_norm_status};
+    *status = MXFP4_OK;
+    for (auto read : words) {
+        int one = MXFP4_OK;
+        if (read(&one, reset) != cudaSuccess)
+            return MXFP4_ERR_CUDA;
+        if (*status == MXFP4_OK)
+            *status = one;
+    }
     return MXFP4_OK;
 }
 

@@ -73,9 +73,11 @@ struct NormArgs {
     int blocks;                 // backward: blocks that share the rows
     int T, N;
     int width;                  // elements of the widest access that every row allows: 8, 4, 2, 1
+    long long wait_limit;
 };
 cudaError_t launch_layer_norm(const NormArgs &a, int sms, cudaStream_t stream);
 int norm_backward_blocks(int T, int N);
-cudaError_t launch_layer_norm_backward(const NormArgs &a, cudaStream_t stream);
+cudaError_t launch_layer_norm_backward(NormArgs &a, cudaStream_t stream);
+cudaError_t read_norm_status(int *status, int reset);
 
 }  // namespace mxfp4

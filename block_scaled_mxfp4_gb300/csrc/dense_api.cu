@@ -292,6 +292,7 @@ int mxfp4_layer_norm_backward(void *dX, int64_t lddx, float *dw, float *db, cons
     a.dw = dw;
     a.db = db;
     a.partials = static_cast<float *>(workspace);
+    a.wait_limit = current_wait_limit();
     a.T = T;
     a.N = N;
     a.width = 8;

@@ -327,6 +327,199 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : PARAMS ? 512 : 1024) n
     }
 }
 
+// The gradients of many aligned rows: the same sums, with the rows streamed through
+// shared memory.  A ring of stages, each the x, dy and dres of as many rows as
+// 512 threads with 16 elements each hold, is filled by bulk copies; the
+// threads take a stage into registers, add to dw and db and reduce, and the
+// reduction's barrier is also what frees the stage for the next copy.  One block
+// to an SM, 150 KB of reads in flight in each: bound by HBM.
+constexpr int kRing = 8;                         // most stages
+constexpr int kRingBytes = 200 << 10;
+constexpr int kStreamThreads = 512;
+constexpr int kStreamRow = 8192;                 // longest row: 16 elements a thread
+
+struct StreamShape {
+    int tpr;                    // threads of a row, whole warps
+    int rows;                   // rows of a stage
+    int row_bytes;
+    int arrays;                 // 2, or 3 with dres
+    int depth;                  // stages
+};
+
+__device__ int g_status = 0;                     // bounded waits that ran out
+
+__global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel(const __grid_constant__ NormArgs a, const StreamShape sh)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint64_t full[kRing];
+    __shared__ float2 slots[2][kStreamThreads / 32];
+    __shared__ int abort_flag;
+    const int stage_bytes = sh.rows * sh.arrays * sh.row_bytes;
+    const int mine = static_cast<int>(threadIdx.x) / sh.tpr;         // the thread's row of a stage
+    const int at = static_cast<int>(threadIdx.x) - mine * sh.tpr;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool works = mine < sh.rows;
+    const float inv_n = 1.0f / static_cast<float>(a.N);
+    const int64_t groups = (static_cast<int64_t>(a.T) + sh.rows - 1) / sh.rows;
+    const int64_t mygroups = groups > blockIdx.x ? (groups - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < sh.depth; ++s)
+            mbar_init(&full[s], static_cast<uint32_t>(sh.rows));
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait_prerequisites();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    // The first thread of each row copies that row of group k to stage s; rows past the last arrive empty.
+    auto fill = [&](int64_t k, int s) {
+        if (at != 0 || !works || k >= mygroups)
+            return;
+        const int64_t t = (blockIdx.x + k * gridDim.x) * sh.rows + mine;
+        if (t >= a.T) {
+            mbar_arrive(&full[s]);
+            return;
+        }
+        const uint64_t policy = l2_policy_evict_first();
+        uint8_t *dst = ring + s * stage_bytes + mine * sh.arrays * sh.row_bytes;
+        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(sh.arrays * sh.row_bytes));
+        bulk_load(dst, a.x + t * a.ldx, static_cast<uint32_t>(sh.row_bytes), &full[s], policy);
+        bulk_load(dst + sh.row_bytes, a.dy + t * a.lddy, static_cast<uint32_t>(sh.row_bytes), &full[s], policy);
+        if (a.dres)
+            bulk_load(dst + 2 * sh.row_bytes, a.dres + t * a.ldr, static_cast<uint32_t>(sh.row_bytes), &full[s], policy);
+    };
+    for (int k = 0; k < sh.depth; ++k)
+        fill(k, k);
+    const int n0 = at * 8, n1 = (sh.tpr + at) * 8;       // the thread's two units of a row
+    const bool on0 = works && n0 < a.N, on1 = works && n1 < a.N;
+    float w[16], dw[16], db[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        w[i] = dw[i] = db[i] = 0.0f;
+    {
+        float u[8];
+        if (on0) {
+            load_param<8>(a.w, a.fp32, n0, 1.0f, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = u[i];
+        }
+        if (on1) {
+            load_param<8>(a.w, a.fp32, n1, 1.0f, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[8 + i] = u[i];
+        }
+    }
+    float mean = 0.0f, rstd = 0.0f;
+    auto statistics = [&](int64_t k) {
+        const int64_t t = (blockIdx.x + k * gridDim.x) * sh.rows + mine;
+        if (works && k < mygroups && t < a.T) {
+            mean = a.mean[t];
+            rstd = a.rstd[t];
+        }
+    };
+    statistics(0);
+    int s = 0;
+    uint32_t phase = 0;
+    for (int64_t k = 0; k < mygroups; ++k) {
+        const bool ok = mbar_wait(&full[s], phase, &abort_flag, a.wait_limit, &g_status);
+        const int64_t t = (blockIdx.x + k * gridDim.x) * sh.rows + mine;
+        const bool row = ok && t < a.T;
+        const uint8_t *src = ring + s * stage_bytes + mine * sh.arrays * sh.row_bytes;
+        uint4 x[2], dy[2], res[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            x[v] = dy[v] = res[v] = make_uint4(0u, 0u, 0u, 0u);
+            if (row && (v ? on1 : on0)) {
+                const uint8_t *p = src + 2 * (v ? n1 : n0);
+                x[v] = *reinterpret_cast<const uint4 *>(p);
+                dy[v] = *reinterpret_cast<const uint4 *>(p + sh.row_bytes);
+                if (a.dres)
+                    res[v] = *reinterpret_cast<const uint4 *>(p + 2 * sh.row_bytes);
+            }
+        }
+        const float mu = mean, r = row ? rstd : 0.0f;
+        statistics(k + 1);
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float xhat = (pick<8>(x[v], i) - mu) * r, d = pick<8>(dy[v], i), g = d * w[8 * v + i];
+                sum.x += g;
+                sum.y = fmaf(g, xhat, sum.y);
+                dw[8 * v + i] = fmaf(d, xhat, dw[8 * v + i]);
+                db[8 * v + i] += d;
+            }
+        sum.x = warp_sum(sum.x);
+        sum.y = warp_sum(sum.y);
+        if (lane == 0)
+            slots[k & 1][warp] = sum;
+        // Every thread has taken the stage into registers: it fills again.
+        if (__syncthreads_or(!ok)) {
+            if (threadIdx.x == 0)                        // copies land before the block leaves
+                for (int64_t j = k; j < k + sh.depth && j < mygroups; ++j) {
+                    mbar_wait_drain(&full[s], phase, a.wait_limit);
+                    if (++s == sh.depth) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            return;
+        }
+        fill(k + sh.depth, s);
+        if (++s == sh.depth) {
+            s = 0;
+            phase ^= 1u;
+        }
+        const int first = mine * sh.tpr / 32, warps = sh.tpr / 32;
+        sum = lane < warps && works ? slots[k & 1][first + lane] : make_float2(0.0f, 0.0f);
+        sum.x = warp_sum(sum.x) * inv_n;
+        sum.y = warp_sum(sum.y) * inv_n;
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            if (row && (v ? on1 : on0)) {
+                float y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float xhat = (pick<8>(x[v], i) - mu) * r;
+                    y[i] = r * (fmaf(pick<8>(dy[v], i), w[8 * v + i], -sum.x) - xhat * sum.y) + pick<8>(res[v], i);
+                }
+                store_unit<8>(a.dx + t * a.lddx + (v ? n1 : n0), y);
+            }
+    }
+    if (!a.dw && !a.db)
+        return;
+    // The stage's rows of a block add up in the ring's memory, in their order.
+    float *joint = reinterpret_cast<float *>(ring);
+    float *out[2] = {a.dw, a.db};
+    if (gridDim.x > 1) {
+        out[0] = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
+        out[1] = out[0] + a.N;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        __syncthreads();
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            if (v ? on1 : on0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    joint[mine * a.N + (v ? n1 : n0) + i] = q ? db[8 * v + i] : dw[8 * v + i];
+            }
+        __syncthreads();
+        for (int n = threadIdx.x; n < a.N; n += kStreamThreads) {
+            float s = 0.0f;
+            for (int g = 0; g < sh.rows; ++g)
+                s += joint[g * a.N + n];
+            if (out[q])
+                out[q][n] = s;
+        }
+    }
+}
+
 // dw and db of rows too long for a block's registers: a block takes 32 W columns
 // and rows gridDim.y apart, a warp every eighth of them.
 template <int W>
@@ -377,6 +570,7 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant_
 }
 
 constexpr int kWarpRow = 1024;                   // longest row of one warp: 32 elements a lane
+constexpr int kStreamBlocks = 152;               // one to each SM of a GB300
 constexpr int kBlockRow = 16384;                 // longest row whose dw and db fit a block's registers
 
 // Elements a thread and threads a row, in whole warps.
@@ -395,9 +589,12 @@ cudaError_t start_norm(const NormArgs &a, int sms, cudaStream_t stream)
 template <int W>
 cudaError_t start_norm_width(const NormArgs &a, int sms, cudaStream_t stream)
 {
-    if (a.N <= kWarpRow && a.T > 2 * sms)
+    // Many rows: 32 elements a thread, so that many rows are in flight on an SM.  Few: eight, the shortest
+    // time for one row.
+    const bool many = a.T > 2 * sms;
+    if (a.N <= kWarpRow && many)
         return a.N <= 256 ? start_norm<W, 8, true>(a, sms, stream) : start_norm<W, 32, true>(a, sms, stream);
-    if (a.N <= 8192)
+    if (a.N <= 8192 && !many)
         return start_norm<W, 8, false>(a, sms, stream);
     return start_norm<W, 32, false>(a, sms, stream);
 }
@@ -408,6 +605,29 @@ cudaError_t start_backward(const NormArgs &a, cudaStream_t stream)
     const int threads = WARP ? kRowWarps * 32 : threads_for(a.N, EPT);
     return launch_dependent(norm_backward_kernel<W, EPT, WARP, PARAMS>, dim3(static_cast<unsigned>(a.blocks)),
                             dim3(static_cast<unsigned>(threads)), 0, stream, a);
+}
+
+// Whether a call's rows are streamed: 16-byte rows of a fair length, enough of them to fill the ring.
+bool streams(const NormArgs &a)
+{
+    return a.width == 8 && a.N > kWarpRow && a.N <= kStreamRow && a.T >= 8 * kStreamBlocks;
+}
+
+cudaError_t start_stream(const NormArgs &a, cudaStream_t stream)
+{
+    StreamShape sh;
+    sh.tpr = threads_for(a.N, 16);
+    sh.rows = kStreamThreads / sh.tpr;
+    sh.row_bytes = 2 * a.N;
+    sh.arrays = a.dres ? 3 : 2;
+    const int stage = sh.rows * sh.arrays * sh.row_bytes;
+    sh.depth = kRingBytes / stage < kRing ? kRingBytes / stage : kRing;
+    const int bytes = sh.depth * stage;
+    const cudaError_t e = opt_in<norm_backward_stream_kernel>(bytes);
+    if (e != cudaSuccess)
+        return e;
+    return launch_dependent(norm_backward_stream_kernel, dim3(static_cast<unsigned>(a.blocks)), dim3(kStreamThreads),
+                            static_cast<size_t>(bytes), stream, a, sh);
 }
 
 template <int W>
@@ -450,11 +670,14 @@ int norm_backward_blocks(int T, int N)
     return static_cast<int>(need < 1 ? 1 : need < most ? need : most);
 }
 
-cudaError_t launch_layer_norm_backward(const NormArgs &a, cudaStream_t stream)
+cudaError_t launch_layer_norm_backward(NormArgs &a, cudaStream_t stream)
 {
     cudaError_t e;
+    const bool stream_rows = streams(a);
+    if (stream_rows)
+        a.blocks = kStreamBlocks;                        // (fewer than norm_backward_blocks)
     switch (a.width) {
-    case 8: e = start_backward_width<8>(a, stream); break;
+    case 8: e = stream_rows ? start_stream(a, stream) : start_backward_width<8>(a, stream); break;
     case 4: e = start_backward_width<4>(a, stream); break;
     case 2: e = start_backward_width<2>(a, stream); break;
     default: e = start_backward_width<1>(a, stream); break;
@@ -462,6 +685,15 @@ cudaError_t launch_layer_norm_backward(const NormArgs &a, cudaStream_t stream)
     if (e == cudaSuccess && a.blocks > 1 && (a.dw || a.db))
         e = launch_sum_partials(a.dw, a.N, a.db, a.N, a.partials, a.blocks, stream);
     return e;
+}
+
+cudaError_t read_norm_status(int *status, int reset)
+{
+    const cudaError_t e = cudaMemcpyFromSymbol(status, g_status, sizeof(int));
+    if (e != cudaSuccess || !reset)
+        return e;
+    const int zero = 0;
+    return cudaMemcpyToSymbol(g_status, &zero, sizeof(int));
 }
 
 }  // namespace mxfp4
