@@ -232,6 +232,7 @@ int mxfp4_layer_norm(void *Y, int64_t ldy, float *mean, float *rstd, const void 
     a.mean = mean;
     a.rstd = rstd;
     a.eps = eps;
+    a.wait_limit = current_wait_limit();
     a.T = T;
     a.N = N;
     a.width = 8;

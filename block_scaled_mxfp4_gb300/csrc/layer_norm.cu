@@ -327,41 +327,214 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : PARAMS ? 512 : 1024) n
     }
 }
 
-// The gradients of many aligned rows: the same sums, with the rows streamed through
-// shared memory.  A ring of stages, each the x, dy and dres of as many rows as
-// 512 threads with 16 elements each hold, is filled by bulk copies; the
-// threads take a stage into registers, add to dw and db and reduce, and the
-// reduction's barrier is also what frees the stage for the next copy.  One block
-// to an SM, 150 KB of reads in flight in each: bound by HBM.
+// ------------------------------------------------------------ many rows --
+//
+// The same sums with the rows streamed through shared memory.  A ring of stages,
+// each the arrays' rows of as many row numbers as 512 threads with 16 elements
+// each hold, is filled by bulk copies; the threads take a stage into registers and
+// reduce, and the reduction's barrier is also what frees the stage for the next
+// copy.  Bound by HBM.
+//
+// Bulk copies want 16-byte boundaries.  Rows off them are copied from the boundary
+// before to the one after, which lie in the array except at its two ends: the
+// first and the last row are read straight from memory instead.
+
 constexpr int kRing = 8;                         // most stages
-constexpr int kRingBytes = 200 << 10;
 constexpr int kStreamThreads = 512;
 constexpr int kStreamRow = 8192;                 // longest row: 16 elements a thread
 
 struct StreamShape {
     int tpr;                    // threads of a row, whole warps
     int rows;                   // rows of a stage
-    int row_bytes;
-    int arrays;                 // 2, or 3 with dres
+    int slot;                   // bytes of a row in the ring
+    int arrays;
     int depth;                  // stages
 };
 
 __device__ int g_status = 0;                     // bounded waits that ran out
 
+// Element i of a thread's 16: whole units of eight, or (W = 1) neighbours to neighbouring lanes.
+template <int W>
+__device__ __forceinline__ int element(int tpr, int at, int i)
+{
+    return W == 8 ? (i / 8 * tpr + at) * 8 + i % 8 : i * tpr + at;
+}
+
+// Two elements, as they lie in a word.
+__device__ __forceinline__ F2 pair_of(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
+
+// A thread's 16 elements of a row at p (shared or global memory), zeros past the end.
+template <int W>
+__device__ __forceinline__ void take(const uint16_t *p, int tpr, int at, int N, bool row, uint32_t (&w)[8])
+{
+    if constexpr (W == 8) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (row && element<8>(tpr, at, 8 * v) < N)
+                q = *reinterpret_cast<const uint4 *>(p + element<8>(tpr, at, 8 * v));
+            w[4 * v] = q.x;
+            w[4 * v + 1] = q.y;
+            w[4 * v + 2] = q.z;
+            w[4 * v + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int lo = element<1>(tpr, at, 2 * i), hi = element<1>(tpr, at, 2 * i + 1);
+            w[i] = (row && lo < N ? static_cast<uint32_t>(p[lo]) : 0u) | (row && hi < N ? static_cast<uint32_t>(p[hi]) << 16 : 0u);
+        }
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void give(uint16_t *p, int tpr, int at, int N, const F2 (&y)[8])
+{
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 v = parts(y[i]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    if constexpr (W == 8) {
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            if (element<8>(tpr, at, 8 * v) < N)
+                *reinterpret_cast<uint4 *>(p + element<8>(tpr, at, 8 * v)) = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (element<1>(tpr, at, i) < N)
+                p[element<1>(tpr, at, i)] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// A thread's 16 parameters, zeros past the end.
+template <int W>
+__device__ __forceinline__ void take_params(const void *p, int fp32, float missing, int tpr, int at, int N, F2 (&w)[8])
+{
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; i += W) {
+        float u[W];
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            u[j] = 0.0f;
+        if (element<W>(tpr, at, i) < N)
+            load_param<W>(p, fp32, element<W>(tpr, at, i), missing, u);
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+            v[i + j] = u[j];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i] = f2(v[2 * i], v[2 * i + 1]);
+}
+
+// x - m of two elements, zero past the row's end (where x is 0 and m need not be a number).
+template <int W>
+__device__ __forceinline__ F2 centred(uint32_t word, F2 minus_m, int tpr, int at, int N, int i)
+{
+    const F2 d = pair_of(word) + minus_m;
+    if (W == 8)
+        return element<8>(tpr, at, 2 * i) < N ? d : f2(0.0f);
+    const float2 v = parts(d);
+    return f2(element<1>(tpr, at, 2 * i) < N ? v.x : 0.0f, element<1>(tpr, at, 2 * i + 1) < N ? v.y : 0.0f);
+}
+
+// The ring of one block.  Group k of the block is its rows first + k * step .. + rows - 1; stage
+// k % depth holds it.  (Row numbers past the last stay below 2^31: T does by more than a step.)
+template <int W, int ARRAYS>
+struct Ring {
+    const uint16_t *array[ARRAYS];
+    int64_t ld[ARRAYS];
+    uint8_t *memory;            // of the thread's row in stage 0
+    uint64_t *full;
+    StreamShape sh;
+    int T, bytes;               // bytes of a row
+    int t;                      // the row that is filled next: the thread's
+    int step, last;             // last: no group starts behind it
+    int mine;
+    int s = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ int stage_bytes() const { return sh.rows * sh.arrays * sh.slot; }
+    // Rows that are not copied: W = 1, the arrays' ends.
+    __device__ __forceinline__ bool direct(int row) const { return W == 1 && (row == 0 || row == T - 1); }
+    __device__ __forceinline__ static uint32_t ahead(const uint16_t *p) { return W == 1 ? reinterpret_cast<uintptr_t>(p) & 15u : 0u; }
+
+    // By the first thread of each row: copy that row of the next group to stage `stage`; rows past the
+    // last, and those that are read from memory, arrive empty.
+    __device__ __forceinline__ void fill(int stage)
+    {
+        const int row = t;
+        if (row - mine > last)
+            return;
+        t += step;
+        if (row >= T || direct(row)) {
+            mbar_arrive(&full[stage]);
+            return;
+        }
+        const uint64_t policy = l2_policy_evict_first();
+        const uint16_t *p[ARRAYS];
+        uint32_t size[ARRAYS], total = 0;
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i)
+            if (i < sh.arrays) {
+                p[i] = array[i] + row * ld[i];
+                size[i] = W == 8 ? bytes : (ahead(p[i]) + bytes + 15u) / 16u * 16u;
+                total += size[i];
+            }
+        mbar_arrive_expect_tx(&full[stage], total);
+#pragma unroll
+        for (int i = 0; i < ARRAYS; ++i)
+            if (i < sh.arrays)
+                bulk_load(memory + stage * stage_bytes() + i * sh.slot, reinterpret_cast<const uint8_t *>(p[i]) - ahead(p[i]), size[i],
+                          &full[stage], policy);
+    }
+    // Array i's row `row` of the present stage.
+    __device__ __forceinline__ const uint16_t *at_row(int row, int i) const
+    {
+        const uint8_t *here = memory + s * stage_bytes() + i * sh.slot;
+        if (W == 8)
+            return reinterpret_cast<const uint16_t *>(here);
+        const uint16_t *p = array[i] + row * ld[i];
+        return direct(row) ? p : reinterpret_cast<const uint16_t *>(here + ahead(p));
+    }
+    __device__ __forceinline__ void next()
+    {
+        if (++s == sh.depth) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+    // After a wait that ran out: the copies of the stages from this one on land before the block leaves.
+    __device__ __forceinline__ void drain(int first, long long limit)
+    {
+        for (int j = 0; j < sh.depth && first <= last; ++j, first += step) {
+            mbar_wait_drain(&full[s], phase, limit);
+            next();
+        }
+    }
+};
+
+// One block to an SM.
+template <int W>
 __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel(const __grid_constant__ NormArgs a, const StreamShape sh)
 {
-    extern __shared__ __align__(128) uint8_t ring[];
+    extern __shared__ __align__(128) uint8_t memory[];
     __shared__ uint64_t full[kRing];
     __shared__ float2 slots[2][kStreamThreads / 32];
     __shared__ int abort_flag;
-    const int stage_bytes = sh.rows * sh.arrays * sh.row_bytes;
     const int mine = static_cast<int>(threadIdx.x) / sh.tpr;         // the thread's row of a stage
     const int at = static_cast<int>(threadIdx.x) - mine * sh.tpr;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool works = mine < sh.rows;
+    const bool works = mine < sh.rows, fills = works && at == 0;
     const float inv_n = 1.0f / static_cast<float>(a.N);
-    const int64_t groups = (static_cast<int64_t>(a.T) + sh.rows - 1) / sh.rows;
-    const int64_t mygroups = groups > blockIdx.x ? (groups - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+    const int first = static_cast<int>(blockIdx.x) * sh.rows, step = static_cast<int>(gridDim.x) * sh.rows;
+    Ring<W, 3> ring{{a.x, a.dy, a.dres}, {a.ldx, a.lddy, a.ldr}, memory + mine * sh.arrays * sh.slot, full, sh, a.T, 2 * a.N, first + mine, step,
+                    a.T - 1, mine};
     if (threadIdx.x == 0) {
         for (int s = 0; s < sh.depth; ++s)
             mbar_init(&full[s], static_cast<uint32_t>(sh.rows));
@@ -372,150 +545,197 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel
     pdl_wait_prerequisites();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
-    // The first thread of each row copies that row of group k to stage s; rows past the last arrive empty.
-    auto fill = [&](int64_t k, int s) {
-        if (at != 0 || !works || k >= mygroups)
-            return;
-        const int64_t t = (blockIdx.x + k * gridDim.x) * sh.rows + mine;
-        if (t >= a.T) {
-            mbar_arrive(&full[s]);
-            return;
-        }
-        const uint64_t policy = l2_policy_evict_first();
-        uint8_t *dst = ring + s * stage_bytes + mine * sh.arrays * sh.row_bytes;
-        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(sh.arrays * sh.row_bytes));
-        bulk_load(dst, a.x + t * a.ldx, static_cast<uint32_t>(sh.row_bytes), &full[s], policy);
-        bulk_load(dst + sh.row_bytes, a.dy + t * a.lddy, static_cast<uint32_t>(sh.row_bytes), &full[s], policy);
-        if (a.dres)
-            bulk_load(dst + 2 * sh.row_bytes, a.dres + t * a.ldr, static_cast<uint32_t>(sh.row_bytes), &full[s], policy);
-    };
-    for (int k = 0; k < sh.depth; ++k)
-        fill(k, k);
-    const int n0 = at * 8, n1 = (sh.tpr + at) * 8;       // the thread's two units of a row
-    const bool on0 = works && n0 < a.N, on1 = works && n1 < a.N;
-    float w[16], dw[16], db[16];
+    if (fills)
+        for (int k = 0; k < sh.depth; ++k)
+            ring.fill(k);
+    F2 w[8], dw[8], db[8];
+    take_params<W>(a.w, a.fp32, 1.0f, sh.tpr, at, a.N, w);
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        w[i] = dw[i] = db[i] = 0.0f;
-    {
-        float u[8];
-        if (on0) {
-            load_param<8>(a.w, a.fp32, n0, 1.0f, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i] = u[i];
-        }
-        if (on1) {
-            load_param<8>(a.w, a.fp32, n1, 1.0f, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[8 + i] = u[i];
-        }
-    }
+    for (int i = 0; i < 8; ++i)
+        dw[i] = db[i] = f2(0.0f);
+    const int warp0 = mine * sh.tpr / 32, warps = sh.tpr / 32;
     float mean = 0.0f, rstd = 0.0f;
-    auto statistics = [&](int64_t k) {
-        const int64_t t = (blockIdx.x + k * gridDim.x) * sh.rows + mine;
-        if (works && k < mygroups && t < a.T) {
-            mean = a.mean[t];
-            rstd = a.rstd[t];
+    if (works && first + mine < a.T) {
+        mean = a.mean[first + mine];
+        rstd = a.rstd[first + mine];
+    }
+    uint16_t *out = a.dx + (first + mine) * a.lddx;
+    int parity = 0;
+    for (int t0 = first; t0 < a.T; t0 += step, parity ^= 1, out += step * a.lddx) {
+        const bool ok = mbar_wait(&full[ring.s], ring.phase, &abort_flag, a.wait_limit, &g_status);
+        const int t = t0 + mine;
+        const bool row = ok && works && t < a.T;
+        uint32_t x[8], dy[8], res[8];
+        take<W>(ring.at_row(t, 0), sh.tpr, at, a.N, row, x);
+        take<W>(ring.at_row(t, 1), sh.tpr, at, a.N, row, dy);
+        if (a.dres)
+            take<W>(ring.at_row(t, 2), sh.tpr, at, a.N, row, res);
+        const F2 minus_m = f2(row ? -mean : 0.0f), r = f2(row ? rstd : 0.0f);
+        if (works && t + step < a.T) {
+            mean = a.mean[t + step];
+            rstd = a.rstd[t + step];
         }
-    };
-    statistics(0);
-    int s = 0;
-    uint32_t phase = 0;
-    for (int64_t k = 0; k < mygroups; ++k) {
-        const bool ok = mbar_wait(&full[s], phase, &abort_flag, a.wait_limit, &g_status);
-        const int64_t t = (blockIdx.x + k * gridDim.x) * sh.rows + mine;
-        const bool row = ok && t < a.T;
-        const uint8_t *src = ring + s * stage_bytes + mine * sh.arrays * sh.row_bytes;
-        uint4 x[2], dy[2], res[2];
+        F2 s1 = f2(0.0f), s2 = f2(0.0f);
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            x[v] = dy[v] = res[v] = make_uint4(0u, 0u, 0u, 0u);
-            if (row && (v ? on1 : on0)) {
-                const uint8_t *p = src + 2 * (v ? n1 : n0);
-                x[v] = *reinterpret_cast<const uint4 *>(p);
-                dy[v] = *reinterpret_cast<const uint4 *>(p + sh.row_bytes);
-                if (a.dres)
-                    res[v] = *reinterpret_cast<const uint4 *>(p + 2 * sh.row_bytes);
-            }
+        for (int i = 0; i < 8; ++i) {
+            const F2 xhat = centred<W>(x[i], minus_m, sh.tpr, at, a.N, i) * r, d = pair_of(dy[i]), g = d * w[i];
+            s1 = s1 + g;
+            s2 = fma2(g, xhat, s2);
+            dw[i] = fma2(d, xhat, dw[i]);
+            db[i] = db[i] + d;
         }
-        const float mu = mean, r = row ? rstd : 0.0f;
-        statistics(k + 1);
-        float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float xhat = (pick<8>(x[v], i) - mu) * r, d = pick<8>(dy[v], i), g = d * w[8 * v + i];
-                sum.x += g;
-                sum.y = fmaf(g, xhat, sum.y);
-                dw[8 * v + i] = fmaf(d, xhat, dw[8 * v + i]);
-                db[8 * v + i] += d;
-            }
-        sum.x = warp_sum(sum.x);
-        sum.y = warp_sum(sum.y);
+        const float2 p1 = parts(s1), p2 = parts(s2);
+        float2 sum = make_float2(warp_sum(p1.x + p1.y), warp_sum(p2.x + p2.y));
         if (lane == 0)
-            slots[k & 1][warp] = sum;
+            slots[parity][warp] = sum;
         // Every thread has taken the stage into registers: it fills again.
         if (__syncthreads_or(!ok)) {
-            if (threadIdx.x == 0)                        // copies land before the block leaves
-                for (int64_t j = k; j < k + sh.depth && j < mygroups; ++j) {
-                    mbar_wait_drain(&full[s], phase, a.wait_limit);
-                    if (++s == sh.depth) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
-                }
+            if (threadIdx.x == 0)
+                ring.drain(t0, a.wait_limit);
             return;
         }
-        fill(k + sh.depth, s);
-        if (++s == sh.depth) {
-            s = 0;
-            phase ^= 1u;
-        }
-        const int first = mine * sh.tpr / 32, warps = sh.tpr / 32;
-        sum = lane < warps && works ? slots[k & 1][first + lane] : make_float2(0.0f, 0.0f);
-        sum.x = warp_sum(sum.x) * inv_n;
-        sum.y = warp_sum(sum.y) * inv_n;
+        if (fills)
+            ring.fill(ring.s);
+        ring.next();
+        sum = lane < warps && works ? slots[parity][warp0 + lane] : make_float2(0.0f, 0.0f);
+        const F2 m1 = f2(-warp_sum(sum.x) * inv_n), m2 = f2(-warp_sum(sum.y) * inv_n);
+        if (row) {
+            F2 y[8];
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-            if (row && (v ? on1 : on0)) {
-                float y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float xhat = (pick<8>(x[v], i) - mu) * r;
-                    y[i] = r * (fmaf(pick<8>(dy[v], i), w[8 * v + i], -sum.x) - xhat * sum.y) + pick<8>(res[v], i);
-                }
-                store_unit<8>(a.dx + t * a.lddx + (v ? n1 : n0), y);
+            for (int i = 0; i < 8; ++i) {
+                const F2 xhat = (pair_of(x[i]) + minus_m) * r;
+                y[i] = r * fma2(xhat, m2, fma2(pair_of(dy[i]), w[i], m1));
+                if (a.dres)
+                    y[i] = y[i] + pair_of(res[i]);
             }
+            give<W>(out, sh.tpr, at, a.N, y);
+        }
     }
     if (!a.dw && !a.db)
         return;
     // The stage's rows of a block add up in the ring's memory, in their order.
-    float *joint = reinterpret_cast<float *>(ring);
-    float *out[2] = {a.dw, a.db};
+    float *joint = reinterpret_cast<float *>(memory);
+    float *sums[2] = {a.dw, a.db};
     if (gridDim.x > 1) {
-        out[0] = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
-        out[1] = out[0] + a.N;
+        sums[0] = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
+        sums[1] = sums[0] + a.N;
     }
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         __syncthreads();
+        if (works) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v)
-            if (v ? on1 : on0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    joint[mine * a.N + (v ? n1 : n0) + i] = q ? db[8 * v + i] : dw[8 * v + i];
+            for (int i = 0; i < 16; ++i) {
+                const float2 v = parts(q ? db[i / 2] : dw[i / 2]);
+                if (element<W>(sh.tpr, at, i) < a.N)
+                    joint[mine * a.N + element<W>(sh.tpr, at, i)] = i & 1 ? v.y : v.x;
             }
+        }
         __syncthreads();
         for (int n = threadIdx.x; n < a.N; n += kStreamThreads) {
             float s = 0.0f;
             for (int g = 0; g < sh.rows; ++g)
                 s += joint[g * a.N + n];
-            if (out[q])
-                out[q][n] = s;
+            if (sums[q])
+                sums[q][n] = s;
+        }
+    }
+}
+
+// The norm itself: two blocks to an SM, half of the ring each.  One barrier a
+// stage: a warp takes the mean of its elements and the squares of their
+// differences from that, and the row's follow from the warps' as
+//   m = sum n_i m_i / N,  sum (x - m)^2 = sum [q_i + n_i (m_i - m)^2],
+// sums of positive terms throughout.
+template <int W>
+__global__ void __launch_bounds__(kStreamThreads, 2) norm_stream_kernel(const __grid_constant__ NormArgs a, const StreamShape sh)
+{
+    extern __shared__ __align__(128) uint8_t memory[];
+    __shared__ uint64_t full[kRing];
+    __shared__ float2 slots[2][kStreamThreads / 32];
+    __shared__ int abort_flag;
+    const int mine = static_cast<int>(threadIdx.x) / sh.tpr;
+    const int at = static_cast<int>(threadIdx.x) - mine * sh.tpr;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool works = mine < sh.rows, fills = works && at == 0;
+    const float inv_n = 1.0f / static_cast<float>(a.N);
+    const int first = static_cast<int>(blockIdx.x) * sh.rows, step = static_cast<int>(gridDim.x) * sh.rows;
+    Ring<W, 1> ring{{a.x}, {a.ldx}, memory + mine * sh.slot, full, sh, a.T, 2 * a.N, first + mine, step, a.T - 1, mine};
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < sh.depth; ++s)
+            mbar_init(&full[s], static_cast<uint32_t>(sh.rows));
+        abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_wait_prerequisites();
+    if (threadIdx.x == 0)
+        pdl_launch_dependents();
+    if (fills)
+        for (int k = 0; k < sh.depth; ++k)
+            ring.fill(k);
+    F2 w[8], b[8];
+    take_params<W>(a.w, a.fp32, 1.0f, sh.tpr, at, a.N, w);
+    take_params<W>(a.b, a.fp32, 0.0f, sh.tpr, at, a.N, b);
+    // Elements of the row's warp number i.
+    auto count = [&](int i) {
+        int n = 0;
+        for (int j = 0; j < 16; j += W)
+            n += max(0, min(32 * W, a.N - element<W>(sh.tpr, 32 * i, j)));
+        return static_cast<float>(n);
+    };
+    const int warp0 = mine * sh.tpr / 32, warps = sh.tpr / 32;
+    const float own = count(warp - warp0), theirs = lane < warps ? count(lane) : 0.0f;
+    const float inv_own = own > 0.0f ? 1.0f / own : 0.0f;
+    uint16_t *out = a.y + (first + mine) * a.ldy;
+    int parity = 0;
+    for (int t0 = first; t0 < a.T; t0 += step, parity ^= 1, out += step * a.ldy) {
+        const bool ok = mbar_wait(&full[ring.s], ring.phase, &abort_flag, a.wait_limit, &g_status);
+        const int t = t0 + mine;
+        const bool row = ok && works && t < a.T;
+        uint32_t x[8];
+        take<W>(ring.at_row(t, 0), sh.tpr, at, a.N, row, x);
+        F2 total = pair_of(x[0]);
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            total = total + pair_of(x[i]);
+        const float2 p = parts(total);
+        const float m = warp_sum(p.x + p.y) * inv_own;
+        F2 squares = f2(0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const F2 d = centred<W>(x[i], f2(-m), sh.tpr, at, a.N, i);
+            squares = fma2(d, d, squares);
+        }
+        const float2 q = parts(squares);
+        const float q_warp = warp_sum(q.x + q.y);
+        if (lane == 0)
+            slots[parity][warp] = make_float2(m, q_warp);
+        // Every thread has taken the stage into registers: it fills again.
+        if (__syncthreads_or(!ok)) {
+            if (threadIdx.x == 0)
+                ring.drain(t0, a.wait_limit);
+            return;
+        }
+        if (fills)
+            ring.fill(ring.s);
+        ring.next();
+        const float2 part = lane < warps && works ? slots[parity][warp0 + lane] : make_float2(0.0f, 0.0f);
+        const float mean = warp_sum(theirs * part.x) * inv_n;
+        const float d = part.x - mean;
+        const float rstd = rsqrtf(warp_sum(theirs > 0.0f ? fmaf(theirs * d, d, part.y) : 0.0f) * inv_n + a.eps);
+        if (row) {
+            if (at == 0) {
+                if (a.mean)
+                    a.mean[t] = mean;
+                if (a.rstd)
+                    a.rstd[t] = rstd;
+            }
+            F2 y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y[i] = fma2((pair_of(x[i]) + f2(-mean)) * f2(rstd), w[i], b[i]);
+            give<W>(out, sh.tpr, at, a.N, y);
         }
     }
 }
@@ -571,10 +791,26 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant_
 
 constexpr int kWarpRow = 1024;                   // longest row of one warp: 32 elements a lane
 constexpr int kStreamBlocks = 152;               // one to each SM of a GB300
+constexpr int kRingBytes = 200 << 10;            // of an SM
+constexpr int kStreamLeast = 256;                // shorter rows are a warp's
 constexpr int kBlockRow = 16384;                 // longest row whose dw and db fit a block's registers
 
 // Elements a thread and threads a row, in whole warps.
 int threads_for(int N, int ept) { return ((N + ept - 1) / ept + 31) / 32 * 32; }
+
+// The ring of a call, if its rows are streamed: of a fair length, and enough of them for every block.
+bool stream_shape(const NormArgs &a, int arrays, int blocks, int ring_bytes, StreamShape &sh)
+{
+    if (a.N <= kStreamLeast || a.N > kStreamRow)
+        return false;
+    sh.tpr = threads_for(a.N, 16);
+    sh.rows = kStreamThreads / sh.tpr;
+    sh.slot = a.width == 8 ? 2 * a.N : (2 * a.N + 14 + 15) / 16 * 16;
+    sh.arrays = arrays;
+    const int stage = sh.rows * arrays * sh.slot;
+    sh.depth = ring_bytes / stage < kRing ? ring_bytes / stage : kRing;
+    return sh.depth >= 2 && a.T >= sh.rows * blocks;
+}
 
 template <int W, int EPT, bool WARP>
 cudaError_t start_norm(const NormArgs &a, int sms, cudaStream_t stream)
@@ -592,6 +828,16 @@ cudaError_t start_norm_width(const NormArgs &a, int sms, cudaStream_t stream)
     // Many rows: 32 elements a thread, so that many rows are in flight on an SM.  Few: eight, the shortest
     // time for one row.
     const bool many = a.T > 2 * sms;
+    StreamShape sh;
+    if (stream_shape(a, 1, 2 * kStreamBlocks, kRingBytes / 2, sh)) {
+        const int bytes = sh.depth * sh.rows * sh.slot;
+        auto kernel = norm_stream_kernel<W == 8 ? 8 : 1>;
+        const cudaError_t e = opt_in<norm_stream_kernel<W == 8 ? 8 : 1>>(bytes);
+        if (e != cudaSuccess)
+            return e;
+        return launch_dependent(kernel, dim3(2 * kStreamBlocks), dim3(kStreamThreads), static_cast<size_t>(bytes),
+                                stream, a, sh);
+    }
     if (a.N <= kWarpRow && many)
         return a.N <= 256 ? start_norm<W, 8, true>(a, sms, stream) : start_norm<W, 32, true>(a, sms, stream);
     if (a.N <= 8192 && !many)
@@ -607,32 +853,21 @@ cudaError_t start_backward(const NormArgs &a, cudaStream_t stream)
                             dim3(static_cast<unsigned>(threads)), 0, stream, a);
 }
 
-// Whether a call's rows are streamed: 16-byte rows of a fair length, enough of them to fill the ring.
-bool streams(const NormArgs &a)
-{
-    return a.width == 8 && a.N > kWarpRow && a.N <= kStreamRow && a.T >= 8 * kStreamBlocks;
-}
-
-cudaError_t start_stream(const NormArgs &a, cudaStream_t stream)
+template <int W>
+cudaError_t start_backward_width(NormArgs &a, cudaStream_t stream)
 {
     StreamShape sh;
-    sh.tpr = threads_for(a.N, 16);
-    sh.rows = kStreamThreads / sh.tpr;
-    sh.row_bytes = 2 * a.N;
-    sh.arrays = a.dres ? 3 : 2;
-    const int stage = sh.rows * sh.arrays * sh.row_bytes;
-    sh.depth = kRingBytes / stage < kRing ? kRingBytes / stage : kRing;
-    const int bytes = sh.depth * stage;
-    const cudaError_t e = opt_in<norm_backward_stream_kernel>(bytes);
-    if (e != cudaSuccess)
-        return e;
-    return launch_dependent(norm_backward_stream_kernel, dim3(static_cast<unsigned>(a.blocks)), dim3(kStreamThreads),
-                            static_cast<size_t>(bytes), stream, a, sh);
-}
-
-template <int W>
-cudaError_t start_backward_width(const NormArgs &a, cudaStream_t stream)
-{
+    if (stream_shape(a, a.dres ? 3 : 2, kStreamBlocks, kRingBytes, sh)) {
+        a.blocks = kStreamBlocks;                        // (never more than norm_backward_blocks)
+        const int ring = sh.depth * sh.rows * sh.arrays * sh.slot, joint = sh.rows * a.N * 4;
+        const int bytes = ring > joint ? ring : joint;
+        auto kernel = norm_backward_stream_kernel<W == 8 ? 8 : 1>;
+        const cudaError_t e = opt_in<norm_backward_stream_kernel<W == 8 ? 8 : 1>>(bytes);
+        if (e != cudaSuccess)
+            return e;
+        return launch_dependent(kernel, dim3(kStreamBlocks), dim3(kStreamThreads),
+                                static_cast<size_t>(bytes), stream, a, sh);
+    }
     if (a.N <= 256)
         return start_backward<W, 8, true, true>(a, stream);
     if (a.N <= kWarpRow)
@@ -673,11 +908,8 @@ int norm_backward_blocks(int T, int N)
 cudaError_t launch_layer_norm_backward(NormArgs &a, cudaStream_t stream)
 {
     cudaError_t e;
-    const bool stream_rows = streams(a);
-    if (stream_rows)
-        a.blocks = kStreamBlocks;                        // (fewer than norm_backward_blocks)
     switch (a.width) {
-    case 8: e = stream_rows ? start_stream(a, stream) : start_backward_width<8>(a, stream); break;
+    case 8: e = start_backward_width<8>(a, stream); break;
     case 4: e = start_backward_width<4>(a, stream); break;
     case 2: e = start_backward_width<2>(a, stream); break;
     default: e = start_backward_width<1>(a, stream); break;

@@ -540,9 +540,36 @@ def test_norm_layouts(T, N):
     check_norm(T, N, "fp32", w=False, b=False, eps=1.0)
 
 
+# Enough rows for the streamed forms: 16-byte rows and others, one and several rows of a stage.
+STREAMED = [(2500, 2056), (1300, 4104), (1250, 8192), (1300, 8190), (1280, 5001), (6500, 1032), (10000, 264), (10000, 513), (20000, 257)]
+
+
+@pytest.mark.parametrize("T,N", STREAMED)
+def test_norm_of_many_rows(T, N):
+    check_norm(T, N, "fp32")
+    check_norm(T, N, "bf16", ld=N + 1, shift=3, b=False)
+    check_norm(T, N, w=False, in_place=True, stats=False, ld=N + 8 - N % 8)
+    X, x = bf16(np.random.default_rng(0).normal(size=(T, N)))
+    X[3, 5], X[T // 2, N - 1], X[T - 1, 0] = float("nan"), float("inf"), float("nan")
+    Y = torch.empty_like(X)
+    mx.mxfp4_layer_norm(Y, N, None, None, X, N, None, None, 0, 1e-5, T, N)
+    bad = torch.isnan(Y)
+    assert bad[[3, T // 2, T - 1]].all() and int(bad.sum()) == 3 * N
+
+
+@pytest.mark.parametrize("T,N", STREAMED)
+def test_norm_backward_of_many_rows(T, N):
+    check_norm_backward(T, N, "fp32")
+    check_norm_backward(T, N, "bf16", resid=False, ld=N + 1, shift=3)
+    check_norm_backward(T, N, w=False, ld=N + 8 - N % 8, alias="x", params=(True, False))
+    check_norm_backward(T, N, alias="dy", params=(False, True))
+    check_norm_backward(T, N, alias="res")
+
+
 def test_norm_rows_far_from_zero():
     """The variance is of differences from the mean, so a large mean costs no more than its own rounding."""
     check_norm(50, 4096, mean=1000.0)
+    check_norm(1300, 4096, mean=1000.0)
     X, x = bf16(np.full((3, 777), 1.0) * [[2.5], [0.0], [-300.0]])
     Y, r = torch.empty_like(X), torch.empty(3, device="cuda")
     mx.mxfp4_layer_norm(Y, 777, None, r, X, 777, None, None, 0, 1e-5, 3, 777)
