@@ -329,19 +329,22 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : PARAMS ? 512 : 1024) n
 
 // ------------------------------------------------------------ many rows --
 //
-// The same sums with the rows streamed through shared memory.  A ring of stages,
-// each the arrays' rows of as many row numbers as 512 threads with 16 elements
-// each hold, is filled by bulk copies; the threads take a stage into registers and
-// reduce, and the reduction's barrier is also what frees the stage for the next
-// copy.  Bound by HBM.
+// The same sums with the rows streamed through shared memory: rings of stages that
+// bulk copies fill, as far ahead as shared memory reaches; a row's threads take
+// a stage into registers and reduce, and the reduction's barrier is also what frees
+// the stage for the next copy.  Bound by HBM.
 //
-// Bulk copies want 16-byte boundaries.  Rows off them are copied from the boundary
-// before to the one after, which lie in the array except at its two ends: the
-// first and the last row are read straight from memory instead.
+// A thread holds units of eight elements, a warp's side by side (a lane's next
+// unit is 32 on), so that accesses are of 16 bytes.  Bulk copies want 16-byte
+// boundaries too.  Rows off them (ALIGNED false) are copied from the boundary before to
+// the one after, which lie in the array except at its two ends: the first and the
+// last row are read straight from memory instead.  A unit is then cut out of two
+// neighbouring 16-byte words in shared memory, and stores take the end of the
+// lane before's unit and the start of the own, so that they lie on boundaries again.
 
 constexpr int kRing = 8;                         // most stages
 constexpr int kStreamThreads = 512;
-constexpr int kStreamRow = 8192;                 // longest row: 16 elements a thread
+constexpr int kStreamRow = 8192;                 // longest row
 
 struct StreamShape {
     int tpr;                    // threads of a row, whole warps
@@ -353,99 +356,154 @@ struct StreamShape {
 
 __device__ int g_status = 0;                     // bounded waits that ran out
 
-// Element i of a thread's 16: whole units of eight, or (W = 1) neighbours to neighbouring lanes.
-template <int W>
-__device__ __forceinline__ int element(int tpr, int at, int i)
+// First element of a thread's unit v of UNITS.
+template <int UNITS>
+__device__ __forceinline__ int unit_at(int at, int v)
 {
-    return W == 8 ? (i / 8 * tpr + at) * 8 + i % 8 : i * tpr + at;
+    return ((at >> 5) * UNITS * 32 + v * 32 + (at & 31)) * 8;
 }
 
 // Two elements, as they lie in a word.
 __device__ __forceinline__ F2 pair_of(uint32_t w) { return f2(bf16_lo(w), bf16_hi(w)); }
 
-// A thread's 16 elements of a row at p (shared or global memory), zeros past the end.
-template <int W>
-__device__ __forceinline__ void take(const uint16_t *p, int tpr, int at, int N, bool row, uint32_t (&w)[8])
+__device__ __forceinline__ uint32_t word_of(F2 v)
 {
-    if constexpr (W == 8) {
+    const float2 p = parts(v);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+// Words k .. k + 3 of eight, half a word on if shift is 16.
+__device__ __forceinline__ void cut(const uint32_t (&w)[8], int k, uint32_t shift, uint32_t (&out)[4])
+{
+    switch (k) {                                         // uniform
+    case 0:
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (row && element<8>(tpr, at, 8 * v) < N)
-                q = *reinterpret_cast<const uint4 *>(p + element<8>(tpr, at, 8 * v));
-            w[4 * v] = q.x;
-            w[4 * v + 1] = q.y;
-            w[4 * v + 2] = q.z;
-            w[4 * v + 3] = q.w;
+        for (int i = 0; i < 4; ++i)
+            out[i] = __funnelshift_r(w[i], w[i + 1], shift);
+        break;
+    case 1:
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            out[i] = __funnelshift_r(w[i + 1], w[i + 2], shift);
+        break;
+    case 2:
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            out[i] = __funnelshift_r(w[i + 2], w[i + 3], shift);
+        break;
+    default:
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            out[i] = __funnelshift_r(w[i + 3], w[i + 4], shift);
+        break;
+    }
+}
+
+// A thread's units of a row, zeros past its end.  The row's first element is number `ahead` of the
+// 16-byte word at p in shared memory, or the row is at `direct` in memory.
+template <bool ALIGNED, int UNITS>
+__device__ __forceinline__ void take(const uint8_t *p, uint32_t ahead, const uint16_t *direct, int at, int N, uint32_t (&w)[4 * UNITS])
+{
+#pragma unroll
+    for (int v = 0; v < UNITS; ++v) {
+        const int n = unit_at<UNITS>(at, v);
+        uint32_t out[4] = {0u, 0u, 0u, 0u};
+        if (n < N) {
+            if (!ALIGNED && direct) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (n + i < N)
+                        out[i / 2] |= static_cast<uint32_t>(direct[n + i]) << (16 * (i & 1));
+            } else {
+                const uint4 lo = *reinterpret_cast<const uint4 *>(p + 2 * n);
+                if (ALIGNED || ahead == 0u) {
+                    out[0] = lo.x;
+                    out[1] = lo.y;
+                    out[2] = lo.z;
+                    out[3] = lo.w;
+                } else {
+                    const uint4 hi = *reinterpret_cast<const uint4 *>(p + 2 * n + 16);
+                    const uint32_t both[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    cut(both, static_cast<int>(ahead >> 1), 16u * (ahead & 1u), out);
+                }
+                if (!ALIGNED && n + 8 > N) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        out[i] = n + 2 * i >= N ? 0u : n + 2 * i + 1 >= N ? out[i] & 0xFFFFu : out[i];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[4 * v + i] = out[i];
+    }
+}
+
+// A thread's units to a row off 16-byte boundaries, or one that ends inside a unit.
+template <int UNITS>
+__device__ __forceinline__ void give_anywhere(uint16_t *p, int at, int N, const uint32_t (&w)[4 * UNITS])
+{
+    const int lane = at & 31;
+    const uint32_t ahead = (reinterpret_cast<uintptr_t>(p) & 15u) / 2u;
+    // The lane's 16-byte word of memory starts `ahead` elements before its unit: in the unit before,
+    // which is the lane before's, or for the first lane the last one's of the v before.
+#pragma unroll
+    for (int v = 0; v < UNITS; ++v) {
+        const int n = unit_at<UNITS>(at, v), e0 = n - static_cast<int>(ahead);
+        uint32_t both[8], out[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            both[4 + i] = w[4 * v + i];
+            const uint32_t sent = v > 0 && lane == 31 ? w[v > 0 ? 4 * v - 4 + i : 0] : w[4 * v + i];
+            both[i] = __shfl_sync(kFull, sent, (lane + 31) & 31);
+        }
+        if (ahead == 0u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                out[i] = both[4 + i];
+        } else {
+            cut(both, static_cast<int>((8u - ahead) >> 1), 16u * (ahead & 1u), out);
+        }
+        const int begin = v == 0 && lane == 0 ? n : e0;  // what comes before a warp's first unit is the warp before's
+        if (begin == e0 && e0 + 8 <= N) {
+            *reinterpret_cast<uint4 *>(p + e0) = make_uint4(out[0], out[1], out[2], out[3]);
+        } else if (begin < N) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (e0 + i >= begin && e0 + i < N)
+                    p[e0 + i] = static_cast<uint16_t>(out[i / 2] >> (16 * (i & 1)));
+        }
+    }
+    // And the end of its last unit, behind the last lane's word.
+    const int n = unit_at<UNITS>(at, UNITS - 1);
+    if (lane == 31 && n + 8 - static_cast<int>(ahead) < N) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i >= 8 - static_cast<int>(ahead) && n + i < N)
+                p[n + i] = static_cast<uint16_t>(w[4 * (UNITS - 1) + i / 2] >> (16 * (i & 1)));
+    }
+}
+
+// A thread's units to a row; all lanes of a warp call it.
+template <bool ALIGNED, int UNITS>
+__device__ __forceinline__ void give(uint16_t *p, int at, int N, const uint32_t (&w)[4 * UNITS])
+{
+    if constexpr (ALIGNED) {
+#pragma unroll
+        for (int v = 0; v < UNITS; ++v) {
+            const int n = unit_at<UNITS>(at, v);
+            if (n < N)
+                *reinterpret_cast<uint4 *>(p + n) = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int lo = element<1>(tpr, at, 2 * i), hi = element<1>(tpr, at, 2 * i + 1);
-            w[i] = (row && lo < N ? static_cast<uint32_t>(p[lo]) : 0u) | (row && hi < N ? static_cast<uint32_t>(p[hi]) << 16 : 0u);
-        }
+        give_anywhere<UNITS>(p, at, N, w);
     }
 }
 
-template <int W>
-__device__ __forceinline__ void give(uint16_t *p, int tpr, int at, int N, const F2 (&y)[8])
-{
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 v = parts(y[i]);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
-    }
-    if constexpr (W == 8) {
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-            if (element<8>(tpr, at, 8 * v) < N)
-                *reinterpret_cast<uint4 *>(p + element<8>(tpr, at, 8 * v)) = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (element<1>(tpr, at, i) < N)
-                p[element<1>(tpr, at, i)] = static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1)));
-    }
-}
-
-// A thread's 16 parameters, zeros past the end.
-template <int W>
-__device__ __forceinline__ void take_params(const void *p, int fp32, float missing, int tpr, int at, int N, F2 (&w)[8])
-{
-    float v[16];
-#pragma unroll
-    for (int i = 0; i < 16; i += W) {
-        float u[W];
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            u[j] = 0.0f;
-        if (element<W>(tpr, at, i) < N)
-            load_param<W>(p, fp32, element<W>(tpr, at, i), missing, u);
-#pragma unroll
-        for (int j = 0; j < W; ++j)
-            v[i + j] = u[j];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i] = f2(v[2 * i], v[2 * i + 1]);
-}
-
-// x - m of two elements, zero past the row's end (where x is 0 and m need not be a number).
-template <int W>
-__device__ __forceinline__ F2 centred(uint32_t word, F2 minus_m, int tpr, int at, int N, int i)
-{
-    const F2 d = pair_of(word) + minus_m;
-    if (W == 8)
-        return element<8>(tpr, at, 2 * i) < N ? d : f2(0.0f);
-    const float2 v = parts(d);
-    return f2(element<1>(tpr, at, 2 * i) < N ? v.x : 0.0f, element<1>(tpr, at, 2 * i + 1) < N ? v.y : 0.0f);
-}
-
-// The ring of one block.  Group k of the block is its rows first + k * step .. + rows - 1; stage
-// k % depth holds it.  (Row numbers past the last stay below 2^31: T does by more than a step.)
-template <int W, int ARRAYS>
+// The ring of one block, or of one team of it.  Group k is the rows first + k * step .. + rows - 1;
+// stage k % depth holds it.  (Row numbers past the last stay below 2^31: T does by more than a step.)
+template <bool ALIGNED, int ARRAYS>
 struct Ring {
     const uint16_t *array[ARRAYS];
     int64_t ld[ARRAYS];
@@ -455,14 +513,13 @@ struct Ring {
     int T, bytes;               // bytes of a row
     int t;                      // the row that is filled next: the thread's
     int step, last;             // last: no group starts behind it
-    int mine;
+    int mine;                   // the thread's row of a stage
     int s = 0;
     uint32_t phase = 0;
 
     __device__ __forceinline__ int stage_bytes() const { return sh.rows * sh.arrays * sh.slot; }
-    // Rows that are not copied: W = 1, the arrays' ends.
-    __device__ __forceinline__ bool direct(int row) const { return W == 1 && (row == 0 || row == T - 1); }
-    __device__ __forceinline__ static uint32_t ahead(const uint16_t *p) { return W == 1 ? reinterpret_cast<uintptr_t>(p) & 15u : 0u; }
+    __device__ __forceinline__ bool direct(int row) const { return !ALIGNED && (row == 0 || row == T - 1); }
+    __device__ __forceinline__ static uint32_t ahead(const uint16_t *p) { return ALIGNED ? 0u : reinterpret_cast<uintptr_t>(p) & 15u; }
 
     // By the first thread of each row: copy that row of the next group to stage `stage`; rows past the
     // last, and those that are read from memory, arrive empty.
@@ -483,7 +540,7 @@ struct Ring {
         for (int i = 0; i < ARRAYS; ++i)
             if (i < sh.arrays) {
                 p[i] = array[i] + row * ld[i];
-                size[i] = W == 8 ? bytes : (ahead(p[i]) + bytes + 15u) / 16u * 16u;
+                size[i] = ALIGNED ? bytes : (ahead(p[i]) + bytes + 15u) / 16u * 16u;
                 total += size[i];
             }
         mbar_arrive_expect_tx(&full[stage], total);
@@ -493,14 +550,12 @@ struct Ring {
                 bulk_load(memory + stage * stage_bytes() + i * sh.slot, reinterpret_cast<const uint8_t *>(p[i]) - ahead(p[i]), size[i],
                           &full[stage], policy);
     }
-    // Array i's row `row` of the present stage.
-    __device__ __forceinline__ const uint16_t *at_row(int row, int i) const
+    // The thread's units of array i's row `row`, which the present stage holds.
+    template <int UNITS>
+    __device__ __forceinline__ void read(int row, int i, int at, int N, uint32_t (&w)[4 * UNITS]) const
     {
-        const uint8_t *here = memory + s * stage_bytes() + i * sh.slot;
-        if (W == 8)
-            return reinterpret_cast<const uint16_t *>(here);
         const uint16_t *p = array[i] + row * ld[i];
-        return direct(row) ? p : reinterpret_cast<const uint16_t *>(here + ahead(p));
+        take<ALIGNED, UNITS>(memory + s * stage_bytes() + i * sh.slot, ahead(p) / 2u, direct(row) ? p : nullptr, at, N, w);
     }
     __device__ __forceinline__ void next()
     {
@@ -519,8 +574,9 @@ struct Ring {
     }
 };
 
-// One block to an SM.
-template <int W>
+// The gradients: one block of 512 threads to an SM, as many rows a stage as they
+// hold with two units each, all of a block's in step.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel(const __grid_constant__ NormArgs a, const StreamShape sh)
 {
     extern __shared__ __align__(128) uint8_t memory[];
@@ -533,8 +589,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel
     const bool works = mine < sh.rows, fills = works && at == 0;
     const float inv_n = 1.0f / static_cast<float>(a.N);
     const int first = static_cast<int>(blockIdx.x) * sh.rows, step = static_cast<int>(gridDim.x) * sh.rows;
-    Ring<W, 3> ring{{a.x, a.dy, a.dres}, {a.ldx, a.lddy, a.ldr}, memory + mine * sh.arrays * sh.slot, full, sh, a.T, 2 * a.N, first + mine, step,
-                    a.T - 1, mine};
+    Ring<ALIGNED, 3> ring{{a.x, a.dy, a.dres}, {a.ldx, a.lddy, a.ldr}, memory + mine * sh.arrays * sh.slot, full, sh, a.T, 2 * a.N,
+                          first + mine, step, a.T - 1, mine};
     if (threadIdx.x == 0) {
         for (int s = 0; s < sh.depth; ++s)
             mbar_init(&full[s], static_cast<uint32_t>(sh.rows));
@@ -549,10 +605,17 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel
         for (int k = 0; k < sh.depth; ++k)
             ring.fill(k);
     F2 w[8], dw[8], db[8];
-    take_params<W>(a.w, a.fp32, 1.0f, sh.tpr, at, a.N, w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+        const int n = unit_at<2>(at, i / 4) + 2 * (i % 4);
+        float lo[1] = {0.0f}, hi[1] = {0.0f};
+        if (n < a.N)
+            load_param<1>(a.w, a.fp32, n, 1.0f, lo);
+        if (n + 1 < a.N)
+            load_param<1>(a.w, a.fp32, n + 1, 1.0f, hi);
+        w[i] = f2(lo[0], hi[0]);
         dw[i] = db[i] = f2(0.0f);
+    }
     const int warp0 = mine * sh.tpr / 32, warps = sh.tpr / 32;
     float mean = 0.0f, rstd = 0.0f;
     if (works && first + mine < a.T) {
@@ -564,21 +627,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel
     for (int t0 = first; t0 < a.T; t0 += step, parity ^= 1, out += step * a.lddx) {
         const bool ok = mbar_wait(&full[ring.s], ring.phase, &abort_flag, a.wait_limit, &g_status);
         const int t = t0 + mine;
-        const bool row = ok && works && t < a.T;
+        const bool row = works && t < a.T;               // (of whole warps)
         uint32_t x[8], dy[8], res[8];
-        take<W>(ring.at_row(t, 0), sh.tpr, at, a.N, row, x);
-        take<W>(ring.at_row(t, 1), sh.tpr, at, a.N, row, dy);
-        if (a.dres)
-            take<W>(ring.at_row(t, 2), sh.tpr, at, a.N, row, res);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            x[i] = dy[i] = res[i] = 0u;
+        if (row) {
+            ring.template read<2>(t, 0, at, a.N, x);
+            ring.template read<2>(t, 1, at, a.N, dy);
+            if (a.dres)
+                ring.template read<2>(t, 2, at, a.N, res);
+        }
         const F2 minus_m = f2(row ? -mean : 0.0f), r = f2(row ? rstd : 0.0f);
         if (works && t + step < a.T) {
             mean = a.mean[t + step];
             rstd = a.rstd[t + step];
         }
+        // (Past the row's end dy is 0.)
         F2 s1 = f2(0.0f), s2 = f2(0.0f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const F2 xhat = centred<W>(x[i], minus_m, sh.tpr, at, a.N, i) * r, d = pair_of(dy[i]), g = d * w[i];
+            const F2 xhat = (pair_of(x[i]) + minus_m) * r, d = pair_of(dy[i]), g = d * w[i];
             s1 = s1 + g;
             s2 = fma2(g, xhat, s2);
             dw[i] = fma2(d, xhat, dw[i]);
@@ -600,15 +669,16 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel
         sum = lane < warps && works ? slots[parity][warp0 + lane] : make_float2(0.0f, 0.0f);
         const F2 m1 = f2(-warp_sum(sum.x) * inv_n), m2 = f2(-warp_sum(sum.y) * inv_n);
         if (row) {
-            F2 y[8];
+            uint32_t y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const F2 xhat = (pair_of(x[i]) + minus_m) * r;
-                y[i] = r * fma2(xhat, m2, fma2(pair_of(dy[i]), w[i], m1));
+                F2 v = r * fma2(xhat, m2, fma2(pair_of(dy[i]), w[i], m1));
                 if (a.dres)
-                    y[i] = y[i] + pair_of(res[i]);
+                    v = v + pair_of(res[i]);
+                y[i] = word_of(v);
             }
-            give<W>(out, sh.tpr, at, a.N, y);
+            give<ALIGNED, 2>(out, at, a.N, y);
         }
     }
     if (!a.dw && !a.db)
@@ -627,8 +697,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float2 v = parts(q ? db[i / 2] : dw[i / 2]);
-                if (element<W>(sh.tpr, at, i) < a.N)
-                    joint[mine * a.N + element<W>(sh.tpr, at, i)] = i & 1 ? v.y : v.x;
+                const int n = unit_at<2>(at, i / 8) + i % 8;
+                if (n < a.N)
+                    joint[mine * a.N + n] = i & 1 ? v.y : v.x;
             }
         }
         __syncthreads();
@@ -642,101 +713,175 @@ __global__ void __launch_bounds__(kStreamThreads, 1) norm_backward_stream_kernel
     }
 }
 
-// The norm itself: two blocks to an SM, half of the ring each.  One barrier a
-// stage: a warp takes the mean of its elements and the squares of their
-// differences from that, and the row's follow from the warps' as
+// The norm itself: four units a thread, teams of a row's threads that go round
+// rings of their own and meet at barriers of their own; the parameters are in shared
+// memory as fp32.  One barrier a row: a warp takes the mean of its elements and
+// the squares of their differences from that, and the row's follow from the warps' as
 //   m = sum n_i m_i / N,  sum (x - m)^2 = sum [q_i + n_i (m_i - m)^2],
 // sums of positive terms throughout.
-template <int W>
-__global__ void __launch_bounds__(kStreamThreads, 2) norm_stream_kernel(const __grid_constant__ NormArgs a, const StreamShape sh)
+constexpr int kNormThreads = 768;
+constexpr int kTeams = kNormThreads / 32;
+
+// Whether any of a team's threads says so, and a barrier for them.
+__device__ __forceinline__ bool team_any(bool yes, int team, int threads)
+{
+    int any;
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
+                 "setp.ne.s32 p, %1, 0;\n\t"
+                 "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+                 "selp.s32 %0, 1, 0, q;\n\t}"
+                 : "=r"(any)
+                 : "r"(static_cast<int>(yes)), "r"(team + 1), "r"(threads)
+                 : "memory");
+    return any != 0;
+}
+
+template <bool ALIGNED>
+__global__ void __launch_bounds__(kNormThreads, 1) norm_stream_kernel(const __grid_constant__ NormArgs a, const StreamShape sh)
 {
     extern __shared__ __align__(128) uint8_t memory[];
-    __shared__ uint64_t full[kRing];
-    __shared__ float2 slots[2][kStreamThreads / 32];
-    __shared__ int abort_flag;
-    const int mine = static_cast<int>(threadIdx.x) / sh.tpr;
-    const int at = static_cast<int>(threadIdx.x) - mine * sh.tpr;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool works = mine < sh.rows, fills = works && at == 0;
+    __shared__ uint64_t full[kTeams][kRing];
+    __shared__ float2 slots[kTeams][2][8];
+    __shared__ int abort_flag[kTeams];
+    const int teams = sh.rows;
+    const int team = static_cast<int>(threadIdx.x) / sh.tpr;
+    const int at = static_cast<int>(threadIdx.x) - team * sh.tpr;
+    const int lane = threadIdx.x & 31, warp = at >> 5, warps = sh.tpr >> 5;
+    const int units = (a.N + 7) / 8;
+    // w, then b: the first four of every unit, then the other four, so that neighbouring lanes' reads are neighbours.
+    float *params = reinterpret_cast<float *>(memory);
     const float inv_n = 1.0f / static_cast<float>(a.N);
-    const int first = static_cast<int>(blockIdx.x) * sh.rows, step = static_cast<int>(gridDim.x) * sh.rows;
-    Ring<W, 1> ring{{a.x}, {a.ldx}, memory + mine * sh.slot, full, sh, a.T, 2 * a.N, first + mine, step, a.T - 1, mine};
-    if (threadIdx.x == 0) {
+    if (team < teams && at == 0) {
         for (int s = 0; s < sh.depth; ++s)
-            mbar_init(&full[s], static_cast<uint32_t>(sh.rows));
-        abort_flag = 0;
+            mbar_init(&full[team][s], 1);
+        abort_flag[team] = 0;
         fence_mbar_init();
     }
-    __syncthreads();
     pdl_wait_prerequisites();
     if (threadIdx.x == 0)
         pdl_launch_dependents();
-    if (fills)
+    for (int n = threadIdx.x; n < 8 * units; n += kNormThreads) {
+        float w[1] = {0.0f}, b[1] = {0.0f};
+        if (n < a.N) {
+            load_param<1>(a.w, a.fp32, n, 1.0f, w);
+            load_param<1>(a.b, a.fp32, n, 0.0f, b);
+        }
+        const int to = ((n >> 2 & 1) * units + (n >> 3)) * 4 + (n & 3);
+        params[to] = w[0];
+        params[8 * units + to] = b[0];
+    }
+    __syncthreads();
+    if (team >= teams)
+        return;
+    // A team is a block of its own in the ring's terms: one row a stage.
+    StreamShape mine = sh;
+    mine.rows = 1;
+    const int step = static_cast<int>(gridDim.x) * teams, first = static_cast<int>(blockIdx.x) * teams + team;
+    Ring<ALIGNED, 1> ring{{a.x}, {a.ldx}, memory + 64 * units + team * sh.depth * sh.slot, full[team], mine, a.T, 2 * a.N, first, step,
+                          a.T - 1, 0};
+    if (at == 0)
         for (int k = 0; k < sh.depth; ++k)
             ring.fill(k);
-    F2 w[8], b[8];
-    take_params<W>(a.w, a.fp32, 1.0f, sh.tpr, at, a.N, w);
-    take_params<W>(a.b, a.fp32, 0.0f, sh.tpr, at, a.N, b);
     // Elements of the row's warp number i.
-    auto count = [&](int i) {
-        int n = 0;
-        for (int j = 0; j < 16; j += W)
-            n += max(0, min(32 * W, a.N - element<W>(sh.tpr, 32 * i, j)));
-        return static_cast<float>(n);
-    };
-    const int warp0 = mine * sh.tpr / 32, warps = sh.tpr / 32;
-    const float own = count(warp - warp0), theirs = lane < warps ? count(lane) : 0.0f;
+    auto count = [&](int i) { return static_cast<float>(max(0, min(1024, a.N - 1024 * i))); };
+    const float own = count(warp), theirs = (lane & 7) < warps ? count(lane & 7) : 0.0f;
     const float inv_own = own > 0.0f ? 1.0f / own : 0.0f;
-    uint16_t *out = a.y + (first + mine) * a.ldy;
+    uint16_t *out = a.y + first * a.ldy;
     int parity = 0;
-    for (int t0 = first; t0 < a.T; t0 += step, parity ^= 1, out += step * a.ldy) {
-        const bool ok = mbar_wait(&full[ring.s], ring.phase, &abort_flag, a.wait_limit, &g_status);
-        const int t = t0 + mine;
-        const bool row = ok && works && t < a.T;
-        uint32_t x[8];
-        take<W>(ring.at_row(t, 0), sh.tpr, at, a.N, row, x);
-        F2 total = pair_of(x[0]);
+    for (int t = first; t < a.T; t += step, parity ^= 1, out += step * a.ldy) {
+        const bool ok = mbar_wait(&full[team][ring.s], ring.phase, &abort_flag[team], a.wait_limit, &g_status);
+        F2 x[16];
+        {
+            uint32_t words[16];
+            ring.template read<4>(t, 0, at, a.N, words);
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
-            total = total + pair_of(x[i]);
+            for (int i = 0; i < 16; ++i)
+                x[i] = pair_of(words[i]);
+        }
+        F2 total = x[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i)
+            total = total + x[i];
         const float2 p = parts(total);
         const float m = warp_sum(p.x + p.y) * inv_own;
+        const F2 minus_m = f2(-m);
         F2 squares = f2(0.0f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const F2 d = centred<W>(x[i], f2(-m), sh.tpr, at, a.N, i);
-            squares = fma2(d, d, squares);
+        for (int v = 0; v < 4; ++v) {
+            const int n = unit_at<4>(at, v);
+            if (n + 8 <= a.N) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const F2 d = x[4 * v + i] + minus_m;
+                    squares = fma2(d, d, squares);
+                }
+            } else if (!ALIGNED && n < a.N) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 d = parts(x[4 * v + i] + minus_m);
+                    const F2 e = f2(n + 2 * i < a.N ? d.x : 0.0f, n + 2 * i + 1 < a.N ? d.y : 0.0f);
+                    squares = fma2(e, e, squares);
+                }
+            }
         }
         const float2 q = parts(squares);
-        const float q_warp = warp_sum(q.x + q.y);
-        if (lane == 0)
-            slots[parity][warp] = make_float2(m, q_warp);
-        // Every thread has taken the stage into registers: it fills again.
-        if (__syncthreads_or(!ok)) {
-            if (threadIdx.x == 0)
-                ring.drain(t0, a.wait_limit);
+        float2 part = make_float2(m, warp_sum(q.x + q.y));
+        if (warps > 1) {
+            if (lane == 0)
+                slots[team][parity][warp] = part;
+            // Every thread has taken the stage into registers: it fills again.
+            if (team_any(!ok, team, sh.tpr)) {
+                if (at == 0)
+                    ring.drain(t, a.wait_limit);
+                return;
+            }
+            part = (lane & 7) < warps ? slots[team][parity][lane & 7] : make_float2(0.0f, 0.0f);
+        } else if (__any_sync(kFull, !ok)) {
+            if (at == 0)
+                ring.drain(t, a.wait_limit);
             return;
         }
-        if (fills)
+        if (at == 0)
             ring.fill(ring.s);
         ring.next();
-        const float2 part = lane < warps && works ? slots[parity][warp0 + lane] : make_float2(0.0f, 0.0f);
-        const float mean = warp_sum(theirs * part.x) * inv_n;
-        const float d = part.x - mean;
-        const float rstd = rsqrtf(warp_sum(theirs > 0.0f ? fmaf(theirs * d, d, part.y) : 0.0f) * inv_n + a.eps);
-        if (row) {
-            if (at == 0) {
-                if (a.mean)
-                    a.mean[t] = mean;
-                if (a.rstd)
-                    a.rstd[t] = rstd;
-            }
-            F2 y[8];
+        float mean = part.x, var = part.y * inv_n;
+        if (warps > 1) {
+            mean = theirs * part.x;
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                y[i] = fma2((pair_of(x[i]) + f2(-mean)) * f2(rstd), w[i], b[i]);
-            give<W>(out, sh.tpr, at, a.N, y);
+            for (int d = 1; d < 8; d <<= 1)
+                mean += __shfl_xor_sync(kFull, mean, d);
+            mean *= inv_n;
+            const float d = part.x - mean;
+            var = theirs > 0.0f ? fmaf(theirs * d, d, part.y) : 0.0f;
+#pragma unroll
+            for (int d = 1; d < 8; d <<= 1)
+                var += __shfl_xor_sync(kFull, var, d);
+            var *= inv_n;
         }
+        const float rstd = rsqrtf(var + a.eps);
+        if (at == 0) {
+            if (a.mean)
+                a.mean[t] = mean;
+            if (a.rstd)
+                a.rstd[t] = rstd;
+        }
+        const F2 centre = f2(-mean), r = f2(rstd);
+        uint32_t y[16];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+            const int unit = unit_at<4>(at, v) / 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f), b = w;
+                if (unit < units) {
+                    w = *reinterpret_cast<const float4 *>(params + (h * units + unit) * 4);
+                    b = *reinterpret_cast<const float4 *>(params + 8 * units + (h * units + unit) * 4);
+                }
+                y[4 * v + 2 * h] = word_of(fma2((x[4 * v + 2 * h] + centre) * r, f2(w.x, w.y), f2(b.x, b.y)));
+                y[4 * v + 2 * h + 1] = word_of(fma2((x[4 * v + 2 * h + 1] + centre) * r, f2(w.z, w.w), f2(b.z, b.w)));
+            }
+        }
+        give<ALIGNED, 4>(out, at, a.N, y);
     }
 }
 
@@ -791,7 +936,7 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant_
 
 constexpr int kWarpRow = 1024;                   // longest row of one warp: 32 elements a lane
 constexpr int kStreamBlocks = 152;               // one to each SM of a GB300
-constexpr int kRingBytes = 200 << 10;            // of an SM
+constexpr int kRingBytes = 216 << 10;            // of an SM
 constexpr int kStreamLeast = 256;                // shorter rows are a warp's
 constexpr int kBlockRow = 16384;                 // longest row whose dw and db fit a block's registers
 
@@ -799,17 +944,18 @@ constexpr int kBlockRow = 16384;                 // longest row whose dw and db 
 int threads_for(int N, int ept) { return ((N + ept - 1) / ept + 31) / 32 * 32; }
 
 // The ring of a call, if its rows are streamed: of a fair length, and enough of them for every block.
-bool stream_shape(const NormArgs &a, int arrays, int blocks, int ring_bytes, StreamShape &sh)
+bool stream_shape(const NormArgs &a, bool backward, StreamShape &sh)
 {
     if (a.N <= kStreamLeast || a.N > kStreamRow)
         return false;
-    sh.tpr = threads_for(a.N, 16);
-    sh.rows = kStreamThreads / sh.tpr;
-    sh.slot = a.width == 8 ? 2 * a.N : (2 * a.N + 14 + 15) / 16 * 16;
-    sh.arrays = arrays;
-    const int stage = sh.rows * arrays * sh.slot;
-    sh.depth = ring_bytes / stage < kRing ? ring_bytes / stage : kRing;
-    return sh.depth >= 2 && a.T >= sh.rows * blocks;
+    sh.tpr = threads_for(a.N, backward ? 16 : 32);
+    sh.rows = (backward ? kStreamThreads : kNormThreads) / sh.tpr;
+    sh.slot = a.width == 8 ? 2 * a.N : (2 * a.N + 14 + 15) / 16 * 16 + 16;   // (the last unit's second word)
+    sh.arrays = !backward ? 1 : a.dres ? 3 : 2;
+    const int stage = sh.rows * sh.arrays * sh.slot;
+    const int room = kRingBytes - (backward ? 0 : (a.N + 7) / 8 * 64);
+    sh.depth = room / stage < kRing ? room / stage : kRing;
+    return sh.depth >= 2 && a.T >= sh.rows * kStreamBlocks * (backward ? 1 : 4);
 }
 
 template <int W, int EPT, bool WARP>
@@ -829,14 +975,14 @@ cudaError_t start_norm_width(const NormArgs &a, int sms, cudaStream_t stream)
     // time for one row.
     const bool many = a.T > 2 * sms;
     StreamShape sh;
-    if (stream_shape(a, 1, 2 * kStreamBlocks, kRingBytes / 2, sh)) {
-        const int bytes = sh.depth * sh.rows * sh.slot;
-        auto kernel = norm_stream_kernel<W == 8 ? 8 : 1>;
-        const cudaError_t e = opt_in<norm_stream_kernel<W == 8 ? 8 : 1>>(bytes);
+    if (stream_shape(a, false, sh)) {
+        const int bytes = sh.depth * sh.rows * sh.slot + (a.N + 7) / 8 * 64;
+        auto kernel = norm_stream_kernel<W == 8>;
+        const cudaError_t e = opt_in<norm_stream_kernel<W == 8>>(bytes);
         if (e != cudaSuccess)
             return e;
-        return launch_dependent(kernel, dim3(2 * kStreamBlocks), dim3(kStreamThreads), static_cast<size_t>(bytes),
-                                stream, a, sh);
+        return launch_dependent(kernel, dim3(kStreamBlocks), dim3(kNormThreads), static_cast<size_t>(bytes), stream, a,
+                                sh);
     }
     if (a.N <= kWarpRow && many)
         return a.N <= 256 ? start_norm<W, 8, true>(a, sms, stream) : start_norm<W, 32, true>(a, sms, stream);
@@ -857,12 +1003,12 @@ template <int W>
 cudaError_t start_backward_width(NormArgs &a, cudaStream_t stream)
 {
     StreamShape sh;
-    if (stream_shape(a, a.dres ? 3 : 2, kStreamBlocks, kRingBytes, sh)) {
+    if (stream_shape(a, true, sh)) {
         a.blocks = kStreamBlocks;                        // (never more than norm_backward_blocks)
         const int ring = sh.depth * sh.rows * sh.arrays * sh.slot, joint = sh.rows * a.N * 4;
         const int bytes = ring > joint ? ring : joint;
-        auto kernel = norm_backward_stream_kernel<W == 8 ? 8 : 1>;
-        const cudaError_t e = opt_in<norm_backward_stream_kernel<W == 8 ? 8 : 1>>(bytes);
+        auto kernel = norm_backward_stream_kernel<W == 8>;
+        const cudaError_t e = opt_in<norm_backward_stream_kernel<W == 8>>(bytes);
         if (e != cudaSuccess)
             return e;
         return launch_dependent(kernel, dim3(kStreamBlocks), dim3(kStreamThreads),
