@@ -387,12 +387,14 @@ int run_gemm(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A, in
     if (shape.pair) {
         if (sc.rowmajor)
             return MXFP4_ERR_INVALID_ARG;            // the pair kernel reads relaid atoms
-        // Atoms per stage and 128-row block: 2 (128 K each), or 4 for NVFP4.
-        const int per_stage = nv ? 4 : 2;
+        // Atoms per stage and 128-row block: 2 (128 K each), or 4 for NVFP4; a
+        // stage of a byte format is 128 K.
+        const int per_stage = nv ? 4 : shape.fp8 ? 1 : 2;
+        const int kx = shape.fp8 ? 2 : 1;
         const int64_t groups = nv ? sf_groups_nv(K) : sf_groups(K);
         CUtensorMap tmA, tmB, tmSA, tmSB;
-        if (!encode_operand(&tmA, A, M, K, lda, kTileM) ||
-            !encode_operand(&tmB, B, N, K, ldb, 128) ||
+        if (!encode_operand(&tmA, A, M, K * kx, lda * kx, kTileM) ||
+            !encode_operand(&tmB, B, N, K * kx, ldb * kx, 128) ||
             !encode_atoms(&tmSA, sc.a, M, groups, per_stage) ||
             !encode_atoms_3d(&tmSB, sc.b, N, groups, 2, per_stage))
             return MXFP4_ERR_CUDA;
@@ -401,7 +403,9 @@ int run_gemm(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A, in
         a.M = M;
         a.N = N;
         a.K = K;
-        a.kt_total = (K + kTileK - 1) / kTileK;
+        a.kt_total = (K * kx + kTileK - 1) / kTileK;
+        a.fmt_p = fmt_a;
+        a.fmt_q = fmt_b;
         a.alpha = alpha;
         a.beta = beta;
         a.C = static_cast<const uint16_t *>(beta != 0.0f ? C : nullptr);
@@ -418,7 +422,8 @@ int run_gemm(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A, in
         if (epi) {
             ActGemmArgs x = *epi;
             static_cast<GemmArgs &>(x) = a;
-            e = launch_gemm_act_pair(x, tiles_p, tiles_q, shape.pair_ctas, tmA, tmB, tmSA, tmSB, stream);
+            e = launch_gemm_act_pair(x, tiles_p, tiles_q, shape.pair_ctas, tmA, tmB, tmSA, tmSB,
+                                     shape.fp8 != 0, stream);
         } else {
             e = launch_gemm_pair(a, tiles_p, tiles_q, shape.pair_ctas, tmA, tmB, tmSA, tmSB, nv, stream);
         }
@@ -679,6 +684,21 @@ static bool byte_format_ok(int fmt)
            fmt == MXFP4_E2M1_PADDED;
 }
 
+// Byte formats with an epilogue of their own run the CTA-pair kernel where MXFP4
+// does, provided that the plan relays the scales (whose workspace the caller has
+// sized by it): its epilogue runs under the next tile's MMAs, the one-tile
+// kernel's after its own (8192 x 8192 x 4096 with GELU and two outputs in 8
+// bits: 298 us there).
+static void pair_for_bytes(mxfp4_plan *plan, GemmShape *shape, int M, int N, int sms)
+{
+    const int64_t tiles = ((static_cast<int64_t>(M) + 255) / 256) * ((static_cast<int64_t>(N) + 255) / 256);
+    const int64_t pairs = sms / 2;
+    if (!plan->relayout_pass || shape->swap || M < 256 || N < 256 || tiles < pairs)
+        return;
+    shape->pair = 1;
+    shape->pair_ctas = 2 * static_cast<int>(tiles < pairs ? tiles : pairs);
+}
+
 static int gemm_rowmajor(void *D, int64_t ldd, const void *C, int64_t ldc, const void *A,
                          int64_t lda, const void *B, int64_t ldb, const void *scaleA,
                          int64_t ld_sa, const void *scaleB, int64_t ld_sb, float alpha, float beta,
@@ -708,6 +728,8 @@ static int gemm_rowmajor(void *D, int64_t ldd, const void *C, int64_t ldc, const
     st = make_plan(M, N, K * kx, split_k, sms, &plan, &shape, fp8);
     if (st != MXFP4_OK)
         return st;
+    if (epi && fp8 && split_k == 0)
+        pair_for_bytes(&plan, &shape, M, N, sms);
     const size_t sfa_bytes = plan.relayout_pass ? align_up(sf_relaid_bytes(M, K)) : 0;
     const size_t sfb_bytes = plan.relayout_pass ? align_up(sf_relaid_bytes(N, K)) : 0;
     // Layout: [split-K counters + partials (plan.workspace_bytes)][relaid A][relaid B].

@@ -45,7 +45,11 @@ __device__ __forceinline__ float act_bias(const ActGemmArgs &a, int n)
 // bias[n0 .. n0 + 31], zeros past N and for no bias.
 __device__ __forceinline__ void act_bias_chunk(const ActGemmArgs &a, int n0, float (&b)[32])
 {
-    if (a.bias && a.bias_vec && n0 + 32 <= a.N) {
+    if (!a.bias) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            b[i] = 0.0f;
+    } else if (a.bias_vec && n0 + 32 <= a.N) {
         if (a.bias_fp32) {
             const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.bias) + n0);
 #pragma unroll
@@ -72,7 +76,7 @@ __device__ __forceinline__ void act_bias_chunk(const ActGemmArgs &a, int n0, flo
     } else {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            b[i] = a.bias && n0 + i < a.N ? act_bias(a, n0 + i) : 0.0f;
+            b[i] = n0 + i < a.N ? act_bias(a, n0 + i) : 0.0f;
     }
 }
 
@@ -81,8 +85,11 @@ template <QuantFmt Q>
 __device__ __forceinline__ void act_put_block(const ActCodes &o, int m, int n0, const float (&v)[32])
 {
     constexpr int W = QuantTraits<Q>::kWords;
-    uint32_t w[W];
-    const uint32_t code = quantize_block<Q>(v, w);
+    uint32_t w[W], code;
+    if constexpr (Q == QuantFmt::kE2M1)
+        code = quantize_block<Q>(v, w);
+    else
+        code = quantize_block_pairs<Q>(v, w);
     uint4 *q = reinterpret_cast<uint4 *>(o.q + m * o.ldq + (Q == QuantFmt::kE2M1 ? n0 / 2 : n0));
     q[0] = make_uint4(w[0], w[1], w[2], w[3]);
     if constexpr (W == 8)
@@ -100,17 +107,81 @@ __device__ __forceinline__ void act_put_codes(const ActCodes &o, int m, int n0, 
         act_put_block<QuantFmt::kE2M1>(o, m, n0, v);
 }
 
-// Row m < M, columns n0 .. n0 + 31 (n0 < N): v holds the accumulators.
-__device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m, int n0, float (&v)[32])
+// Rows of D and R off 16-byte boundaries, and the last columns of others: 16
+// columns of the warp's 32 rows go through a piece of shared memory, so that lanes
+// move neighbouring elements of a row.  (One lane a row instead, 32 rows apart in
+// every access of two bytes: a product of 2048 x 4010 x 1024 took 87 us where
+// 4096 columns take 14.)  Rows are 9 words apart: no bank conflicts either way.
+constexpr int kActPitch = 18;                    // 16-bit elements
+constexpr int kActPieceBytes = 32 * kActPitch * 2;
+
+// Rows m0 .. + 31 and columns n0 + 16 h .. + 15 of R, the lane's row into r as packed pairs.
+__device__ __forceinline__ void act_fetch_piece(const uint16_t *src, int64_t ld, int M, int N, int m0, int n, int lane, uint16_t *piece,
+                                                uint32_t (&r)[8])
 {
+    const int c = lane & 15;
+    uint16_t x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int m = m0 + 2 * i + (lane >> 4);
+        x[i] = m < M && n + c < N ? src[m * ld + n + c] : uint16_t(0);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        piece[(2 * i + (lane >> 4)) * kActPitch + c] = x[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        r[i] = *reinterpret_cast<const uint32_t *>(piece + lane * kActPitch + 2 * i);
+    __syncwarp();
+}
+
+__device__ __forceinline__ void act_put_piece(uint16_t *dst, int64_t ld, int M, int N, int m0, int n, int lane, uint16_t *piece,
+                                              const uint32_t (&d)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<uint32_t *>(piece + lane * kActPitch + 2 * i) = d[i];
+    __syncwarp();
+    const int c = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int m = m0 + 2 * i + (lane >> 4);
+        const uint16_t x = piece[(2 * i + (lane >> 4)) * kActPitch + c];
+        if (m < M && n + c < N)
+            dst[m * ld + n + c] = x;
+    }
+    __syncwarp();
+}
+
+// The L2 lines of R's row m from column n on.
+__device__ __forceinline__ void act_prefetch_row(const ActGemmArgs &a, int m, int n, int count)
+{
+    if (!a.R || m >= a.M || n >= a.N)
+        return;
+    const uint16_t *r = a.R + m * a.ldr + n;
+    const int have = min(count, a.N - n);
+    for (int c = 0; c < have; c += 64)
+        prefetch_l2(r + c);
+    prefetch_l2(r + have - 1);
+}
+
+// Rows m0 .. m0 + 31 (m0 < M), one a lane, columns n0 .. n0 + 31 (n0 < N): v holds
+// the accumulators.  All lanes call it; `piece`: kActPieceBytes of the warp's own.
+__device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m0, int n0, int lane, float (&v)[32], uint16_t *piece)
+{
+    const int m = m0 + lane;
+    const bool real = m < a.M, full = n0 + 32 <= a.N;
     {
         float b[32];
         act_bias_chunk(a, n0, b);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i] = fmaf(a.alpha, v[i], b[i]);
+        for (int i = 0; i < 32; i += 2) {
+            const float2 z = parts(fma2(f2(a.alpha), f2(v[i], v[i + 1]), f2(b[i], b[i + 1])));
+            v[i] = z.x;
+            v[i + 1] = z.y;
+        }
     }
-    const bool full = n0 + 32 <= a.N;
     if (a.Z.q) {
         if (!full) {
 #pragma unroll
@@ -118,32 +189,53 @@ __device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m, int n
                 if (n0 + i >= a.N)
                     v[i] = 0.0f;                         // the block's end: zeros, not counted
         }
-        act_put_codes(a.Z, m, n0, v);
+        if (real)
+            act_put_codes(a.Z, m, n0, v);
     }
     act_apply(a.act, v);
     if (a.R) {
-        const uint16_t *r = a.R + m * a.ldr + n0;
-        if (a.r_vec && full) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(r + i);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int h = 0; h < 2; ++h) {
+            uint32_t r[8];
+            if (a.r_vec && full) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    v[i + 2 * j] = fmaf(a.res_scale, bf16_lo(ww[j]), v[i + 2 * j]);
-                    v[i + 2 * j + 1] = fmaf(a.res_scale, bf16_hi(ww[j]), v[i + 2 * j + 1]);
+                for (int i = 0; i < 2; ++i) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (real)
+                        w = *reinterpret_cast<const uint4 *>(a.R + m * a.ldr + n0 + 16 * h + 8 * i);
+                    r[4 * i] = w.x;
+                    r[4 * i + 1] = w.y;
+                    r[4 * i + 2] = w.z;
+                    r[4 * i + 3] = w.w;
                 }
+            } else {
+                act_fetch_piece(a.R, a.ldr, a.M, a.N, m0, n0 + 16 * h, lane, piece, r);
             }
-        } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (n0 + i < a.N)
-                    v[i] = fmaf(a.res_scale, bf16_bits_to_float(r[i]), v[i]);
+            for (int i = 0; i < 8; ++i) {
+                const int k = 16 * h + 2 * i;
+                const float2 y = parts(fma2(f2(a.res_scale), f2(bf16_lo(r[i]), bf16_hi(r[i])), f2(v[k], v[k + 1])));
+                v[k] = y.x;
+                v[k + 1] = y.y;
+            }
         }
     }
-    if (a.D)
-        put_d_row(a, m, n0, v);
-    if (a.H.q)
+    if (a.D) {
+        if (a.vec_ok && full) {
+            if (real)
+                put_d_row(a, m, n0, v);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t d[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    d[i] = pack_bf16x2(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
+                act_put_piece(a.D, a.ldd, a.M, a.N, m0, n0 + 16 * h, lane, piece, d);
+            }
+        }
+    }
+    if (a.H.q && real)
         act_put_codes(a.H, m, n0, v);
 }
 

@@ -17,6 +17,14 @@
 // instead of two (each atom spans 64 K), a scale slot takes 48 columns, and
 // five stages fit the tensor memory (256 + 5 x 48 = 496 columns).
 //
+// BYTES8 = true: byte formats (kind::mxf8f6f4), a stage of 128 K with one scale
+// atom per 128-row block, a scale slot of 12 columns.
+//
+// With ARGS = ActGemmArgs the epilogue is gemm_act.cuh's.  Its arithmetic takes up
+// to a third of a tile's MMAs, so that the accumulator has to be free before it:
+// registers move from the loading and issuing warpgroups to the epilogue's, whose
+// warps take their 128 columns at once and release them.
+//
 // Roles (512 threads = 16 warps per CTA):
 //   warps 4, 6, 7 (each CTA)  TMA producers: A half, B half, and the scale
 //                      atoms (this CTA's 128 rows of scale-A; all BN rows of
@@ -60,21 +68,22 @@
 
 namespace mxfp4 {
 
-template <int STAGES, bool NV>
+template <int STAGES, bool NV, bool BYTES8 = false, bool EPI = false>
 struct PairCfg {
     static constexpr int BN = 256;                        // tile N
     static constexpr int B_ROWS = BN / 2;                 // this CTA's rows of the B tile
-    static constexpr int GROUPS = NV ? 4 : 2;             // scale atoms per stage and row block
+    static constexpr int GROUPS = NV ? 4 : BYTES8 ? 1 : 2;   // scale atoms per stage and row block
     static constexpr int A_BYTES = kTileM * 128;          // 128 rows x 128 bytes (256 K)
     static constexpr int B_BYTES = B_ROWS * 128;
     static constexpr int SFB_RB = 2;                      // 128-row scale blocks a tile can touch
     static constexpr int SFA_BYTES = GROUPS * kSfAtomBytes;           // 128 rows
     static constexpr int SFB_BYTES = SFB_RB * GROUPS * kSfAtomBytes;
     static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;
-    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SF_BYTES;
+    static constexpr int STAGE_BYTES = (A_BYTES + B_BYTES + SF_BYTES + 1023) / 1024 * 1024;
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
     static constexpr int BAR_BYTES = 512;
-    static constexpr int SMEM_BYTES = RING_BYTES + BAR_BYTES + 1024;
+    static constexpr int PIECE_BYTES = EPI ? 8 * kActPieceBytes : 0;   // gemm_act.cuh's, one an epilogue warp
+    static constexpr int SMEM_BYTES = RING_BYTES + BAR_BYTES + PIECE_BYTES + 1024;
     static constexpr int SF_COLS_A = 4 * GROUPS;          // 4 columns per k-group
     static constexpr int SF_COLS_B = 4 * GROUPS * SFB_RB; // and per 128-row block
     static constexpr int SF_COLS = SF_COLS_A + SF_COLS_B; // one scale slot per stage
@@ -183,14 +192,19 @@ __device__ __forceinline__ void pair_round_chunk(const GemmArgs &a, int m, int n
         out[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
 }
 
-template <int STAGES, bool NV, class ARGS>
+// Registers a thread, 256 threads each: together what the block was launched with
+// (512 x 128, which the launcher checks), so that neither side waits for the other's.
+constexpr int kPairEpilogueRegs = 192, kPairOtherRegs = 64;
+static_assert((kPairEpilogueRegs + kPairOtherRegs) * 256 <= 128 * 512, "register split");
+
+template <int STAGES, bool NV, class ARGS, bool BYTES8>
 __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
     gemm_mxf4_pair(const __grid_constant__ ARGS a, const __grid_constant__ PairSched ps,
                    const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB)
 {
-    using PC = PairCfg<STAGES, NV>;
     constexpr bool EPI = !std::is_same_v<ARGS, GemmArgs>;
+    using PC = PairCfg<STAGES, NV, BYTES8, EPI>;
     constexpr int BN = PC::BN;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_addr(smem_raw);
@@ -247,7 +261,10 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
     // grid before touching anything this grid writes.
     if (threadIdx.x == 0)
         pdl_launch_dependents();
-
+    if (warp & 4) {
+    // Warpgroups 4-7 and 12-15.
+    if constexpr (EPI)
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairOtherRegs));
     if (warp == 4 || warp == 6 || warp == 7) {
         // ------------------------------------------------------ producers --
         if (lane == 0) {
@@ -339,6 +356,9 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
             if constexpr (NV) {
                 tmem_st_32x32b_x16(slot, wa);
                 tmem_st_32x32b_x32(slot + PC::SF_COLS_A, wb);
+            } else if constexpr (BYTES8) {
+                tmem_st_32x32b_x4(slot, wa);
+                tmem_st_32x32b_x8(slot + PC::SF_COLS_A, wb);
             } else {
                 tmem_st_32x32b_x8(slot, wa);
                 tmem_st_32x32b_x16(slot + PC::SF_COLS_A, wb);
@@ -362,7 +382,7 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
         // The whole warp runs the loop (warp-uniform descriptors and
         // barrier polls); one elected lane issues each MMA and commit.
         if (leader) {
-            const uint32_t idesc = NV ? idesc_nvf4(256, BN) : idesc_mxf4(256, BN);
+            const uint32_t idesc = NV ? idesc_nvf4(256, BN) : BYTES8 ? a.idesc8 : idesc_mxf4(256, BN);
             const uint32_t t_sf = tmem + BN;
             int stage = 0;
             uint32_t phase = 0;
@@ -400,6 +420,11 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
                             mma_nvf4_pair_elect(d_tmem, adesc + 2 * j, bdesc + 2 * j, idesc,
                                                 sfa_t + j * 4, sfb_t + j * 4 * PC::SFB_RB,
                                                 (kt > 0 || j > 0) ? 1u : 0u);
+                        } else if constexpr (BYTES8) {
+                            // K=32: byte j of the stage's single k-group.
+                            mma_mxf8_pair_elect(d_tmem, adesc + 2 * j, bdesc + 2 * j,
+                                                idesc_sf_ids(idesc, j, j), sfa_t, sfb_t,
+                                                (kt > 0 || j > 0) ? 1u : 0u);
                         } else {
                             const uint32_t sf_id = (j & 1) * 2;
                             const int g = j >> 1;                    // scale k-group
@@ -424,17 +449,28 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
                 mbar_wait_drain(&drain[0], 0, a.wait_limit);
             }
         }
+    }
     } else {
         // ------------------------------------------------------ epilogue --
         // warps 0-3: columns [0, HALF), warps 8-11: columns [HALF, BN).
+        if constexpr (EPI)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairEpilogueRegs));
         // C and D may belong to the work before this grid.
         pdl_wait_prerequisites();
         const int quarter = warp & 3;
         const int half = warp >> 3;
         const int row = quarter * 32 + lane;
+        [[maybe_unused]] uint16_t *piece =
+            reinterpret_cast<uint16_t *>(smem + PC::RING_BYTES + PC::BAR_BYTES + (half * 4 + quarter) * kActPieceBytes);
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * PC::HALF;
         uint32_t acc_phase = 0;
         for (int t = cl; t < tiles; t += ncl) {
+            if constexpr (EPI) {
+                // R's lines come while the tile's MMAs run.
+                int pt, qt;
+                pair_tile_coords(ps, t, pt, qt);
+                act_prefetch_row(a, pt * 256 + static_cast<int>(rank) * kTileM + row, qt * BN + half * PC::HALF, PC::HALF);
+            }
             bool ok = mbar_wait(acc_full, acc_phase, abort_flag, a.wait_limit, &g_device_status);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
@@ -447,37 +483,34 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
             const int n0 = qt * BN + half * PC::HALF;
             const uint32_t t_row = t_lane;
             if constexpr (EPI) {
-                // 64 columns at a time; the accumulator is released once the
-                // second 64 are read.
-#pragma unroll
-                for (int c0 = 0; c0 < PC::HALF; c0 += 64) {
-                    uint32_t r0[32], r1[32];
-                    tmem_ld_32x32b_x32(t_row + c0, r0);
-                    tmem_ld_32x32b_x32(t_row + c0 + 32, r1);
-                    tmem_ld_wait(r0, r1);
-                    if (c0 + 64 == PC::HALF) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (leader)
-                                mbar_arrive(acc_empty);
-                            else
-                                mbar_arrive_cluster_relaxed(map_to_rank(smem_addr(acc_empty), lead));
-                        }
-                    }
-                    auto put = [&](int n, const uint32_t (&r)[32]) {
-                        if (m >= a.M || n >= a.N)
-                            return;
-                        float v[32];
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[i] = __uint_as_float(r[i]);
-                        act_row_chunk(a, m, n, v);
-                    };
-                    put(n0 + c0, r0);
-                    put(n0 + c0 + 32, r1);
-                    __syncwarp();
+                uint32_t r0[32], r1[32], r2[32], r3[32];
+                tmem_ld_32x32b_x32(t_row, r0);
+                tmem_ld_32x32b_x32(t_row + 32, r1);
+                tmem_ld_32x32b_x32(t_row + 64, r2);
+                tmem_ld_32x32b_x32(t_row + 96, r3);
+                tmem_ld_wait(r0, r1);
+                tmem_ld_wait(r2, r3);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(acc_empty);
+                    else
+                        mbar_arrive_cluster_relaxed(map_to_rank(smem_addr(acc_empty), lead));
                 }
+                auto put = [&](int n, const uint32_t (&r)[32]) {
+                    if (m - lane >= a.M || n >= a.N)         // (the warp's)
+                        return;
+                    float v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        v[i] = __uint_as_float(r[i]);
+                    act_row_chunk(a, m - lane, n, lane, v, piece);
+                };
+                put(n0, r0);
+                put(n0 + 32, r1);
+                put(n0 + 64, r2);
+                put(n0 + 96, r3);
             } else {
                 uint32_t out[PC::HALF / 2];
                 // Columns 0-63 are read and rounded; 64-127 are read, the

@@ -636,6 +636,13 @@ constexpr int kGemmThreads = kGemmThreadsC;
 
 namespace mxfp4 {
 
+// A warp's piece of the ring for the epilogue: every stage's copies have landed
+// and been read once the accumulator is complete.
+__device__ __forceinline__ uint16_t *act_piece(uint8_t *smem, int warp)
+{
+    return reinterpret_cast<uint16_t *>(smem + warp * kActPieceBytes);
+}
+
 // FMT 0: fp4 (E2M1) elements, kind::mxf4; FMT 1: one byte per element
 // (E4M3 / E5M2 / padded E2M3, E3M2, E2M1), kind::mxf8f6f4 with the element
 // types in a.idesc8.  MINB: CTAs per SM the configuration is planned for.
@@ -1040,9 +1047,11 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
         // main loop, so all eight warps share it, two per lane quarter with half
         // of the columns each.
         if (a.split_k == 1) {
+            pdl_wait_prerequisites();
+            if constexpr (!SWAP)                         // R's lines come while the last MMAs run
+                act_prefetch_row(a, p0 + (warp & 3) * 32 + lane, q0 + (warp >> 2) * (BN / 2), BN / 2);
             bool ok = nkt > 0 && mbar_wait(acc_full, 0, abort_flag, a.wait_limit, &g_device_status);
             ok = __all_sync(0xffffffffu, ok);
-            pdl_wait_prerequisites();
             if (ok) {
                 tc_fence_after();
                 const int quarter = warp & 3;
@@ -1063,10 +1072,8 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
                     if constexpr (SWAP) {
                         if (p0 + quarter * 32 < a.N)
                             act_col_chunk<32>(a, q0 + c0, p0 + row, v);
-                    } else {
-                        if (p0 + row < a.M)
-                            act_row_chunk(a, p0 + row, q0 + c0, v);
-                        __syncwarp();
+                    } else if (p0 + quarter * 32 < a.M) {
+                        act_row_chunk(a, p0 + quarter * 32, q0 + c0, lane, v, act_piece(smem, warp));
                     }
                 }
             }
@@ -1109,11 +1116,11 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
             __threadfence();
             pdl_wait_prerequisites();
             if constexpr (EPI)
-                reduce_tile<SWAP, SWAP>(a, tile, p0, q0, threadIdx.x, [&](int p, int q, float (&acc)[32]) {
+                reduce_tile<SWAP, true>(a, tile, p0, q0, threadIdx.x, [&](int p, int q, float (&acc)[32]) {
                     if constexpr (SWAP)
                         act_col_chunk<32>(a, q, p, acc);
                     else
-                        act_row_chunk(a, p, q, acc);
+                        act_row_chunk(a, p - lane, q, lane, acc, act_piece(smem, warp));
                 });
             else
                 reduce_tile<SWAP, false>(a, tile, p0, q0, threadIdx.x, [&](int p, int q, float (&acc)[32]) {
@@ -1271,14 +1278,15 @@ constexpr int kPairStagesNv = 5;
 
 size_t gemm_pair_smem_bytes() { return PairCfg<kPairStages, false>::SMEM_BYTES; }
 
-template <int STAGES, bool NV, class ARGS>
+template <int STAGES, bool NV, bool BYTES8 = false, class ARGS>
 static cudaError_t launch_pair_kernel(const ARGS &a, int tiles_p, int tiles_q, int ctas,
                                       const CUtensorMap &tmA, const CUtensorMap &tmB,
                                       const CUtensorMap &tmSA, const CUtensorMap &tmSB,
                                       cudaStream_t stream)
 {
-    using PC = PairCfg<STAGES, NV>;
-    auto kern = gemm_mxf4_pair<STAGES, NV, ARGS>;
+    constexpr bool EPI = !std::is_same_v<ARGS, GemmArgs>;
+    using PC = PairCfg<STAGES, NV, BYTES8, EPI>;
+    auto kern = gemm_mxf4_pair<STAGES, NV, ARGS, BYTES8>;
     static std::atomic<int> max_clusters[64];   // per device; 0 = not yet queried
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1297,6 +1305,15 @@ static cudaError_t launch_pair_kernel(const ARGS &a, int tiles_p, int tiles_q, i
     cfg.numAttrs = 1;
     int limit = dev < 64 ? max_clusters[dev].load() : 0;
     if (limit == 0) {
+        if (EPI) {
+            // The epilogue's registers come out of what the block was launched with.
+            cudaFuncAttributes fa;
+            e = cudaFuncGetAttributes(&fa, kern);
+            if (e != cudaSuccess)
+                return e;
+            if (fa.numRegs * PC::THREADS < (kPairEpilogueRegs + kPairOtherRegs) * 256)
+                return cudaErrorInvalidConfiguration;
+        }
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PC::SMEM_BYTES);
         if (e != cudaSuccess)
             return e;
@@ -1346,10 +1363,15 @@ cudaError_t launch_gemm_pair(const GemmArgs &a, int tiles_p, int tiles_q, int ct
 cudaError_t launch_gemm_act_pair(const ActGemmArgs &a, int tiles_p, int tiles_q, int ctas,
                                  const CUtensorMap &tmA, const CUtensorMap &tmB,
                                  const CUtensorMap &tmSA, const CUtensorMap &tmSB,
-                                 cudaStream_t stream)
+                                 bool bytes8, cudaStream_t stream)
 {
-    return launch_pair_kernel<kPairStages, false>(a, tiles_p, tiles_q, ctas, tmA, tmB, tmSA, tmSB,
-                                                  stream);
+    if (!bytes8)
+        return launch_pair_kernel<kPairStages, false>(a, tiles_p, tiles_q, ctas, tmA, tmB, tmSA, tmSB,
+                                                      stream);
+    ActGemmArgs b = a;
+    b.idesc8 = idesc_mxf8(256, 256, static_cast<uint32_t>(a.fmt_p), static_cast<uint32_t>(a.fmt_q));
+    return launch_pair_kernel<kPairStages, false, true>(b, tiles_p, tiles_q, ctas, tmA, tmB, tmSA, tmSB,
+                                                        stream);
 }
 
 // Test hook: one wait on an mbarrier nobody arrives at.

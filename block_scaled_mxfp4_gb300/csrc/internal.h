@@ -140,7 +140,7 @@ cudaError_t launch_gemm_pair(const GemmArgs &a, int tiles_p, int tiles_q, int ct
 cudaError_t launch_gemm_act_pair(const ActGemmArgs &a, int tiles_p, int tiles_q, int ctas,
                                  const CUtensorMap &tmA, const CUtensorMap &tmB,
                                  const CUtensorMap &tmSA, const CUtensorMap &tmSB,
-                                 cudaStream_t stream);
+                                 bool bytes8, cudaStream_t stream);
 
 cudaError_t launch_scale_relayout(uint8_t *dst, const uint8_t *src, int rows, int K, int64_t ld,
                                   cudaStream_t stream);

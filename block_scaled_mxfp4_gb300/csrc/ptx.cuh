@@ -571,6 +571,22 @@ __device__ __forceinline__ void mma_nvf4_pair_elect(uint32_t d_tmem, uint64_t ad
         : "memory");
 }
 
+// Byte-format form of mma_mxf4_pair_elect: kind::mxf8f6f4, K = 32 and one
+// E8M0 scale per row of an instruction (scale_vec::1X).
+__device__ __forceinline__ void mma_mxf8_pair_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                    uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                                    uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
 // mma_commit_pair issued by one elected lane of the warp.
 __device__ __forceinline__ void mma_commit_pair_elect(uint64_t *bar, uint16_t mask)
 {

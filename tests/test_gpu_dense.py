@@ -137,7 +137,8 @@ PLANS = [("mxfp4", 2560, 2304, 512, 0), ("mxfp4", 2309, 2500, 288, 0), ("mxfp8",
          ("mxfp4", 200, 40, 320, 0), ("mxfp4", 1, 256, 512, 0), ("mxfp8", 5, 1000, 2048, 0), ("mxfp8", 64, 333, 4096, 0),
          ("mxfp4", 33, 160, 8192, 0), ("mxfp4", 300, 500, 4096, 4), ("mxfp8", 130, 290, 2048, 5), ("mxfp8", 257, 129, 1024, 8),
          ("mxfp4", 7, 97, 8192, 3), ("mxfp8", 40, 64, 2048, 7), ("mxfp8", 140, 200, 4096, 11), ("mxfp4", 9, 200, 8192, 16),
-         ("mixed", 1, 1, 32, 0), ("mixed", 65, 3, 64, 0), ("mixed", 3, 2, 32, 0), ("mxfp8", 128, 256, 128, 0)]
+         ("mixed", 1, 1, 32, 0), ("mixed", 65, 3, 64, 0), ("mixed", 3, 2, 32, 0), ("mxfp8", 128, 256, 128, 0),
+         ("mxfp8", 2560, 2304, 512, 0), ("mixed", 2309, 2501, 416, 0), ("mxfp8", 1000, 4999, 64, 0)]
 assert all(M != 3072 and N != 3072 and K != 3072 for _, M, N, K, _ in PLANS)
 
 
@@ -184,7 +185,7 @@ def test_product_forms_of_one_call_agree(products):
     assert torch.equal(D, D1) and torch.equal(Z, Z1)
 
 
-@pytest.mark.parametrize("form,M,N,K,split", [PLANS[i] for i in (0, 2, 5, 7, 8, 9, 11, 14, 15)])
+@pytest.mark.parametrize("form,M,N,K,split", [PLANS[i] for i in (0, 2, 5, 7, 8, 9, 11, 14, 15, 20, 21)])
 def test_product_without_epilogue_is_the_gemm(products, form, M, N, K, split):
     p = products(form, M, N, K)
     got = p.run(split_k=split)[0]
@@ -200,7 +201,7 @@ def test_product_without_epilogue_is_the_gemm(products, form, M, N, K, split):
     assert torch.equal(got, want)
 
 
-@pytest.mark.parametrize("form,M,N,K,split", [PLANS[i] for i in (0, 1, 2, 5, 7, 9, 10, 14, 15)])
+@pytest.mark.parametrize("form,M,N,K,split", [PLANS[i] for i in (0, 1, 2, 5, 7, 9, 10, 14, 15, 20, 21)])
 def test_product_strides_and_residual_in_place(products, form, M, N, K, split):
     p = products(form, M, N, K)
     x = np.random.default_rng(1).normal(size=(M, N))
