@@ -46,11 +46,9 @@ __device__ __forceinline__ F2 sigmoid2(F2 u_log2e) { return rcp2(f2(1.0f) + ex2_
 // (2.2e-7; 5.1e-7 with P's own rounding).  The lower tail comes out of it to that relative
 // precision, without a subtraction, and both phi and Phi from one exponential and
 // one reciprocal.
-__device__ __forceinline__ void normal2(F2 z, F2 &below, F2 &density)
+__device__ __forceinline__ F2 normal_tail2(F2 minus_abs, F2 e)
 {
-    const float2 zs = parts(z);
-    const F2 t = rcp2(fma2(f2(0.375f), f2(fabsf(zs.x), fabsf(zs.y)), f2(1.0f)));
-    const F2 e = ex2_2(f2(-0.72134752f) * (z * z));
+    const F2 t = rcp2(fma2(f2(-0.375f), minus_abs, f2(1.0f)));
     F2 p = f2(-0.032911055f);
     p = fma2(p, t, f2(0.136879951f));
     p = fma2(p, t, f2(-0.186521217f));
@@ -60,7 +58,16 @@ __device__ __forceinline__ void normal2(F2 z, F2 &below, F2 &density)
     p = fma2(p, t, f2(0.12844570f));
     p = fma2(p, t, f2(0.149604589f));
     p = fma2(p, t, f2(0.149603382f));
-    const F2 tail = e * (t * p);
+    return e * (t * p);
+}
+
+// exp(-z^2 / 2)
+__device__ __forceinline__ F2 bell2(F2 z) { return ex2_2(f2(-0.72134752f) * (z * z)); }
+
+__device__ __forceinline__ void normal2(F2 z, F2 &below, F2 &density)
+{
+    const float2 zs = parts(z);
+    const F2 e = bell2(z), tail = normal_tail2(f2(-fabsf(zs.x), -fabsf(zs.y)), e);
     const float2 low = parts(tail), high = parts(fma2(tail, f2(-1.0f), f2(1.0f)));
     below = f2(zs.x < 0.0f ? low.x : high.x, zs.y < 0.0f ? low.y : high.y);
     density = f2(0.39894228f) * e;
@@ -99,6 +106,12 @@ __device__ __forceinline__ void act_and_slope2(F2 z, F2 &h, F2 &slope)
 template <Act A>
 __device__ __forceinline__ F2 act_value2(F2 z)
 {
+    if constexpr (A == Act::kGelu) {
+        // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
+        const float2 p = parts(z);
+        const F2 minus = f2(-fabsf(p.x), -fabsf(p.y)), above = f2(p.x < 0.0f ? 0.0f : p.x, p.y < 0.0f ? 0.0f : p.y);
+        return fma2(minus, normal_tail2(minus, bell2(z)), above);
+    }
     F2 h, slope;
     act_and_slope2<A>(z, h, slope);
     return h;

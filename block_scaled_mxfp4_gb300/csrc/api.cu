@@ -798,9 +798,12 @@ static int gemm_act(void *D, int64_t ldd, void *H, int64_t ldh, void *SH, int64_
     e.ldr = ldr;
     e.res_scale = res_scale;
     e.r_vec = aligned(R, 16) && (ldr % 8) == 0 ? 1 : 0;
-    e.H = ActCodes{static_cast<uint8_t *>(H), fp8 ? ldh : ldh / 2, static_cast<uint8_t *>(SH), ld_sh,
-                   !fp8 ? 2 : fmt_h == MXFP8_E5M2 ? 1 : 0};
-    e.Z = ActCodes{static_cast<uint8_t *>(Z), ldz, static_cast<uint8_t *>(SZ), ld_sz, fmt_z == MXFP8_E5M2 ? 1 : 0};
+    auto codes = [](void *q, int64_t ld, void *s, int64_t lds, int fmt) {
+        return ActCodes{static_cast<uint8_t *>(q), ld, static_cast<uint8_t *>(s), lds, fmt,
+                        aligned(q, 32) && (ld % 32) == 0, aligned(s, 4) && (lds % 4) == 0};
+    };
+    e.H = codes(H, fp8 ? ldh : ldh / 2, SH, ld_sh, !fp8 ? 2 : fmt_h == MXFP8_E5M2 ? 1 : 0);
+    e.Z = codes(Z, ldz, SZ, ld_sz, fmt_z == MXFP8_E5M2 ? 1 : 0);
     return gemm_rowmajor(D, ldd, nullptr, 0, A, lda, B, ldb, scaleA, ld_sa, scaleB, ld_sb, alpha, 0.0f, M, N, K,
                          split_k, workspace, workspace_bytes, stream, fp8, fmt_a, fmt_b, flags, &e);
 }

@@ -80,9 +80,9 @@ __device__ __forceinline__ void act_bias_chunk(const ActGemmArgs &a, int n0, flo
     }
 }
 
-// One block in a thread: codes and scale of row m, columns n0 ..+31.
+// One block in a thread: codes of row m, columns n0 ..+31; the scale code.
 template <QuantFmt Q>
-__device__ __forceinline__ void act_put_block(const ActCodes &o, int m, int n0, const float (&v)[32])
+__device__ __forceinline__ uint32_t act_put_block(const ActCodes &o, int m, int n0, const float (&v)[32])
 {
     constexpr int W = QuantTraits<Q>::kWords;
     uint32_t w[W], code;
@@ -90,22 +90,47 @@ __device__ __forceinline__ void act_put_block(const ActCodes &o, int m, int n0, 
         code = quantize_block<Q>(v, w);
     else
         code = quantize_block_pairs<Q>(v, w);
-    uint4 *q = reinterpret_cast<uint4 *>(o.q + m * o.ldq + (Q == QuantFmt::kE2M1 ? n0 / 2 : n0));
-    q[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    if constexpr (W == 8)
-        q[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    o.s[m * o.lds + n0 / 32] = static_cast<uint8_t>(code);
+    uint8_t *q = o.q + m * o.ldq + (Q == QuantFmt::kE2M1 ? n0 / 2 : n0);
+    if constexpr (W == 8) {
+        if (o.wide) {
+            st_global_v8_hint(q, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7], l2_policy_evict_first());
+            return code;
+        }
+        reinterpret_cast<uint4 *>(q)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+    reinterpret_cast<uint4 *>(q)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    return code;
 }
 
-__device__ __forceinline__ void act_put_codes(const ActCodes &o, int m, int n0, const float (&v)[32])
+__device__ __forceinline__ uint32_t act_put_codes(const ActCodes &o, int m, int n0, const float (&v)[32])
 {
     if (o.fmt == 0)
-        act_put_block<QuantFmt::kE4M3>(o, m, n0, v);
-    else if (o.fmt == 1)
-        act_put_block<QuantFmt::kE5M2>(o, m, n0, v);
-    else
-        act_put_block<QuantFmt::kE2M1>(o, m, n0, v);
+        return act_put_block<QuantFmt::kE4M3>(o, m, n0, v);
+    if (o.fmt == 1)
+        return act_put_block<QuantFmt::kE5M2>(o, m, n0, v);
+    return act_put_block<QuantFmt::kE2M1>(o, m, n0, v);
 }
+
+// Scale codes of up to four neighbouring blocks of row m, the first of column n0,
+// in the bytes of `codes`.  One store where it may be: the rows of a warp's lanes are
+// apart, and every store of them costs as many lines as it has lanes.
+__device__ __forceinline__ void act_put_scales(const ActCodes &o, int m, int n0, int N, int count, uint32_t codes)
+{
+    uint8_t *s = o.s + m * o.lds + n0 / 32;
+    if (count == 4 && o.pack && n0 + 128 <= N) {
+        *reinterpret_cast<uint32_t *>(s) = codes;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < count && n0 + 32 * i < N)
+            s[i] = static_cast<uint8_t>(codes >> (8 * i));
+}
+
+// The scales of a run of chunks, as they come.
+struct ActScales {
+    uint32_t z = 0, h = 0;
+};
 
 // Rows of D and R off 16-byte boundaries, and the last columns of others: 16
 // columns of the warp's 32 rows go through a piece of shared memory, so that lanes
@@ -166,9 +191,23 @@ __device__ __forceinline__ void act_prefetch_row(const ActGemmArgs &a, int m, in
     prefetch_l2(r + have - 1);
 }
 
+// Columns n0 .. + 31 of R's row m for act_row_chunk, a chunk or more ahead of it: a
+// load's 32 rows are 32 lines, which take long under the operands' traffic (fetched
+// where they are used, they made an 8192^3 product of MXFP4 181 us, not @@).
+__device__ __forceinline__ void act_fetch_row(const ActGemmArgs &a, int m, int n0, uint4 (&r4)[4])
+{
+    if (!a.R || !a.r_vec || m >= a.M || n0 + 32 > a.N)
+        return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r4[i] = *reinterpret_cast<const uint4 *>(a.R + m * a.ldr + n0 + 8 * i);
+}
+
 // Rows m0 .. m0 + 31 (m0 < M), one a lane, columns n0 .. n0 + 31 (n0 < N): v holds
 // the accumulators.  All lanes call it; `piece`: kActPieceBytes of the warp's own.
-__device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m0, int n0, int lane, float (&v)[32], uint16_t *piece)
+// The blocks' scale codes go to byte `at` of `scales`; `r4`: what act_fetch_row left.
+__device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m0, int n0, int lane, float (&v)[32], const uint4 (&r4)[4],
+                                              uint16_t *piece, int at, ActScales &scales)
 {
     const int m = m0 + lane;
     const bool real = m < a.M, full = n0 + 32 <= a.N;
@@ -190,7 +229,7 @@ __device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m0, int 
                     v[i] = 0.0f;                         // the block's end: zeros, not counted
         }
         if (real)
-            act_put_codes(a.Z, m, n0, v);
+            scales.z |= act_put_codes(a.Z, m, n0, v) << (8 * at);
     }
     act_apply(a.act, v);
     if (a.R) {
@@ -200,9 +239,7 @@ __device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m0, int 
             if (a.r_vec && full) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (real)
-                        w = *reinterpret_cast<const uint4 *>(a.R + m * a.ldr + n0 + 16 * h + 8 * i);
+                    const uint4 w = r4[2 * h + i];
                     r[4 * i] = w.x;
                     r[4 * i + 1] = w.y;
                     r[4 * i + 2] = w.z;
@@ -236,7 +273,18 @@ __device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m0, int 
         }
     }
     if (a.H.q && real)
-        act_put_codes(a.H, m, n0, v);
+        scales.h |= act_put_codes(a.H, m, n0, v) << (8 * at);
+}
+
+// After `count` chunks from column n0 on.
+__device__ __forceinline__ void act_row_scales(const ActGemmArgs &a, int m, int n0, int count, const ActScales &scales)
+{
+    if (m >= a.M)
+        return;
+    if (a.Z.q)
+        act_put_scales(a.Z, m, n0, a.N, count, scales.z);
+    if (a.H.q)
+        act_put_scales(a.H, m, n0, a.N, count, scales.h);
 }
 
 // A block across a warp: lane's value of column n (0 where there is none), row m.

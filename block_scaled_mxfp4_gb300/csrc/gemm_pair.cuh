@@ -88,7 +88,8 @@ struct PairCfg {
     static constexpr int SF_COLS_B = 4 * GROUPS * SFB_RB; // and per 128-row block
     static constexpr int SF_COLS = SF_COLS_A + SF_COLS_B; // one scale slot per stage
     static constexpr int HALF = BN / 2;                   // columns per epilogue warp
-    static constexpr int TMEM_USED = BN + STAGES * SF_COLS;
+    static constexpr int SET_ASIDE = BN + STAGES * SF_COLS;   // the epilogue's, 32 columns a half
+    static constexpr int TMEM_USED = SET_ASIDE + (EPI ? 64 : 0);
     static constexpr int TMEM_COLS = TMEM_USED <= 256 ? 256 : 512;
     static constexpr int THREADS = 512;
     static constexpr int EPI_WARPS = 8;                   // per CTA
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
         uint32_t acc_phase = 0;
         for (int t = cl; t < tiles; t += ncl) {
             if constexpr (EPI) {
-                // R's lines come while the tile's MMAs run.
+                // R's lines come to L2 while the tile's MMAs run.
                 int pt, qt;
                 pair_tile_coords(ps, t, pt, qt);
                 act_prefetch_row(a, pt * 256 + static_cast<int>(rank) * kTileM + row, qt * BN + half * PC::HALF, PC::HALF);
@@ -483,13 +484,24 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
             const int n0 = qt * BN + half * PC::HALF;
             const uint32_t t_row = t_lane;
             if constexpr (EPI) {
-                uint32_t r0[32], r1[32], r2[32], r3[32];
-                tmem_ld_32x32b_x32(t_row, r0);
-                tmem_ld_32x32b_x32(t_row + 32, r1);
-                tmem_ld_32x32b_x32(t_row + 64, r2);
-                tmem_ld_32x32b_x32(t_row + 96, r3);
-                tmem_ld_wait(r0, r1);
-                tmem_ld_wait(r2, r3);
+                // One copy of the code for the four chunks of columns, which move up
+                // (four do not stay in the instruction cache).  Three wait in
+                // registers, the last in spare columns of tensor memory, so that the
+                // accumulator is free at once: four leave too few registers, and what spills
+                // comes back from L2, as shared memory takes the L1's place.
+                const uint32_t aside = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + PC::SET_ASIDE + half * 32;
+                uint32_t r0[32], r1[32], r2[32];
+                {
+                    uint32_t r3[32];
+                    tmem_ld_32x32b_x32(t_row + 96, r3);
+                    tmem_ld_32x32b_x32(t_row, r0);
+                    tmem_ld_32x32b_x32(t_row + 32, r1);
+                    tmem_ld_32x32b_x32(t_row + 64, r2);
+                    tmem_ld_wait(r0, r1);
+                    tmem_ld_wait(r2, r3);
+                    tmem_st_32x32b_x32(aside, r3);
+                    tmem_st_wait();
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -498,19 +510,29 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
                     else
                         mbar_arrive_cluster_relaxed(map_to_rank(smem_addr(acc_empty), lead));
                 }
-                auto put = [&](int n, const uint32_t (&r)[32]) {
-                    if (m - lane >= a.M || n >= a.N)         // (the warp's)
-                        return;
+                ActScales scales;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    const int n = n0 + 32 * c;
                     float v[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        v[i] = __uint_as_float(r[i]);
-                    act_row_chunk(a, m - lane, n, lane, v, piece);
-                };
-                put(n0, r0);
-                put(n0 + 32, r1);
-                put(n0 + 64, r2);
-                put(n0 + 96, r3);
+                    for (int i = 0; i < 32; ++i) {
+                        v[i] = __uint_as_float(r0[i]);
+                        r0[i] = r1[i];
+                        r1[i] = r2[i];
+                    }
+                    if (m - lane < a.M && n < a.N) {         // (the warp's)
+                        uint4 r4[4];
+                        act_fetch_row(a, m, n, r4);
+                        act_row_chunk(a, m - lane, n, lane, v, r4, piece, c, scales);
+                    }
+                    if (c == 0) {
+                        __syncwarp();
+                        tmem_ld_32x32b_x32(aside, r2);
+                        tmem_ld_wait(r2);
+                    }
+                }
+                act_row_scales(a, m, n0, 4, scales);
             } else {
                 uint32_t out[PC::HALF / 2];
                 // Columns 0-63 are read and rounded; 64-127 are read, the

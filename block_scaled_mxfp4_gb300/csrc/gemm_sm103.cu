@@ -1048,8 +1048,12 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
         // of the columns each.
         if (a.split_k == 1) {
             pdl_wait_prerequisites();
-            if constexpr (!SWAP)                         // R's lines come while the last MMAs run
-                act_prefetch_row(a, p0 + (warp & 3) * 32 + lane, q0 + (warp >> 2) * (BN / 2), BN / 2);
+            [[maybe_unused]] uint4 r4[4];
+            if constexpr (!SWAP) {                       // R comes while the last MMAs run
+                const int m = p0 + (warp & 3) * 32 + lane, n = q0 + (warp >> 2) * (BN / 2);
+                act_fetch_row(a, m, n, r4);
+                act_prefetch_row(a, m, n, BN / 2);
+            }
             bool ok = nkt > 0 && mbar_wait(acc_full, 0, abort_flag, a.wait_limit, &g_device_status);
             ok = __all_sync(0xffffffffu, ok);
             if (ok) {
@@ -1058,6 +1062,7 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
                 const int row = quarter * 32 + lane;
                 const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
                 const int c_begin = (warp >> 2) * (BN / 2);
+                [[maybe_unused]] ActScales scales;
 #pragma unroll 1
                 for (int c0 = c_begin; c0 < c_begin + BN / 2; c0 += 32) {
                     if (q0 + c0 >= (SWAP ? a.M : a.N))
@@ -1073,9 +1078,18 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
                         if (p0 + quarter * 32 < a.N)
                             act_col_chunk<32>(a, q0 + c0, p0 + row, v);
                     } else if (p0 + quarter * 32 < a.M) {
-                        act_row_chunk(a, p0 + quarter * 32, q0 + c0, lane, v, act_piece(smem, warp));
+                        uint4 here[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            here[i] = r4[i];
+                        if (c0 + 32 < c_begin + BN / 2)
+                            act_fetch_row(a, p0 + row, q0 + c0 + 32, r4);
+                        act_row_chunk(a, p0 + quarter * 32, q0 + c0, lane, v, here, act_piece(smem, warp),
+                                      (c0 - c_begin) / 32, scales);
                     }
                 }
+                if constexpr (!SWAP)
+                    act_row_scales(a, p0 + row, q0 + c_begin, BN / 64, scales);
             }
             tc_fence_before();
             __syncthreads();
@@ -1117,10 +1131,15 @@ __global__ void __launch_bounds__(kGemmThreads, MINB)
             pdl_wait_prerequisites();
             if constexpr (EPI)
                 reduce_tile<SWAP, true>(a, tile, p0, q0, threadIdx.x, [&](int p, int q, float (&acc)[32]) {
-                    if constexpr (SWAP)
+                    if constexpr (SWAP) {
                         act_col_chunk<32>(a, q, p, acc);
-                    else
-                        act_row_chunk(a, p - lane, q, lane, acc, act_piece(smem, warp));
+                    } else {
+                        ActScales scales;
+                        uint4 r4[4];
+                        act_fetch_row(a, p, q, r4);
+                        act_row_chunk(a, p - lane, q, lane, acc, r4, act_piece(smem, warp), 0, scales);
+                        act_row_scales(a, p, q, 1, scales);
+                    }
                 });
             else
                 reduce_tile<SWAP, false>(a, tile, p0, q0, threadIdx.x, [&](int p, int q, float (&acc)[32]) {

@@ -82,6 +82,8 @@ struct ActCodes {               // quantised output [M, N], 1x32 blocks along N;
     uint8_t *s;
     int64_t lds;
     int fmt;                    // 0: E4M3, 1: E5M2, 2: packed E2M1
+    int wide;                   // byte formats: rows allow 32-byte stores
+    int pack;                   // rows of scales allow 4-byte stores
 };
 struct ActGemmArgs : GemmArgs { // D may be null; beta and C are not used
     const void *bias;           // [N] or null
