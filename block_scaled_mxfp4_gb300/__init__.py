@@ -7,7 +7,8 @@ tensors or raw integer pointers -> void*, the current torch stream by
 default); every step of the computation runs in the library's CUDA kernels.
 There is no CPU fallback: if the compiled library is missing, loading fails.
 ``gemm`` is a convenience wrapper that allocates D and the workspace with
-torch and calls ``mxfp4_gemm``.
+torch and calls ``mxfp4_gemm``; ``moe_block``, ``dense_block`` and
+``dense_block_backward`` do the same for whole layers.
 """
 from __future__ import annotations
 
@@ -41,6 +42,7 @@ __all__ = [
     "mxfp8_act_backward", "mxfp4_layer_norm", "mxfp4_layer_norm_backward",
     "mxfp4_layer_norm_workspace_size", "MXFP4_ACT_NONE", "MXFP4_ACT_RELU", "MXFP4_ACT_GELU",
     "MXFP4_ACT_GELU_TANH", "MXFP4_ACT_SILU", "MXFP4_PARAM_BF16", "MXFP4_PARAM_FP32",
+    "mxfp8_forms", "dense_block", "dense_block_backward", "Mxfp8Forms", "DenseKept", "DenseGrads",
     "gemm", "Plan",
 ]
 
@@ -754,3 +756,7 @@ def gemm(A, B, SA, SB, alpha=1.0, beta=0.0, C=None, split_k=0, out=None, workspa
                    B, B.stride(0) * 2, SA, SA.stride(0), SB, SB.stride(0), float(alpha),
                    float(beta), M, N, K, split_k, workspace, workspace.numel())
     return out
+
+
+from .dense import (DenseGrads, DenseKept, Mxfp8Forms, dense_block, dense_block_backward,  # noqa: E402
+                    mxfp8_forms)

@@ -191,9 +191,8 @@ __device__ __forceinline__ void act_prefetch_row(const ActGemmArgs &a, int m, in
     prefetch_l2(r + have - 1);
 }
 
-// Columns n0 .. + 31 of R's row m for act_row_chunk, a chunk or more ahead of it: a
-// load's 32 rows are 32 lines, which take long under the operands' traffic (fetched
-// where they are used, they made an 8192^3 product of MXFP4 181 us, not @@).
+// Columns n0 .. + 31 of R's row m for act_row_chunk, issued ahead of it: a load's 32
+// rows are 32 lines, which take long under the operands' traffic.
 __device__ __forceinline__ void act_fetch_row(const ActGemmArgs &a, int m, int n0, uint4 (&r4)[4])
 {
     if (!a.R || !a.r_vec || m >= a.M || n0 + 32 > a.N)

@@ -626,7 +626,9 @@ size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F);
  * Activations: none, max(z, 0), GELU z Phi(z), GELU's tanh form, SiLU.
  * Exponentials and reciprocals are the hardware's approximations; GELU's Phi is a
  * polynomial of this library's own with a relative error of 5e-7 in the lower
- * tail.  Values are within 2^-20 (1 + z^2) of themselves.
+ * tail.  Relative to an activation's value its error stays within 2^-19 + |u| 2^-21,
+ * u the exponential's argument (z^2 / 2 for GELU, sqrt(8 / pi) (z + 0.044715 z^3) for
+ * its tanh form, z for SiLU); a value under the smallest normal number may be 0.
  * ------------------------------------------------------------------------ */
 
 enum { MXFP4_ACT_NONE = 0, MXFP4_ACT_RELU = 1, MXFP4_ACT_GELU = 2, MXFP4_ACT_GELU_TANH = 3, MXFP4_ACT_SILU = 4 };

@@ -1,0 +1,123 @@
+"""What dense_block, dense_block_backward and mxfp8_forms refuse.  No GPU: tensors on
+the CPU, whose place is looked at last."""
+import pytest
+
+import block_scaled_mxfp4_gb300 as mx
+from block_scaled_mxfp4_gb300 import build as mxbuild
+
+torch = pytest.importorskip("torch")
+
+T, K, F = 10, 64, 96
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    mxbuild.build()
+
+
+def u8(*shape):
+    return torch.zeros(shape, dtype=torch.uint8)
+
+
+def bf16(*shape):
+    return torch.zeros(shape, dtype=torch.bfloat16)
+
+
+def forward_args(packed=False):
+    per = 2 if packed else 1
+    return dict(x=bf16(T, K), w1=u8(F, K // per), s1=u8(F, K // 32), w2=u8(K, F // per), s2=u8(K, F // 32), b1=bf16(F), b2=bf16(K),
+                norm_w=torch.zeros(K), norm_b=torch.zeros(K))
+
+
+def backward_args():
+    kept = mx.DenseKept(bf16(T, K), torch.zeros(K), torch.zeros(T), torch.zeros(T), u8(K, 32), u8(K, 1), u8(T, F), u8(T, F // 32),
+                        mx.MXFP4_ACT_SILU, mx.MXFP8_E4M3)
+    return dict(dout=bf16(T, K), kept=kept, w1t=u8(K, F), s1t=u8(K, F // 32), w2t=u8(F, K), s2t=u8(F, K // 32))
+
+
+def refusal(call, args, **changes):
+    for name, change in changes.items():
+        args[name] = change(args[name]) if callable(change) else change
+    with pytest.raises((TypeError, ValueError)) as e:
+        call(**args)
+    return e.type, str(e.value)
+
+
+def apart(t):
+    wide = torch.zeros((*t.shape, 2), dtype=t.dtype)
+    wide[..., 0] = t
+    return wide[..., 0]
+
+
+HERE = "everything on one GPU expected"
+
+
+def test_right_arguments_are_refused_for_their_place_alone():
+    for packed in (False, True):
+        good = lambda **c: refusal(mx.dense_block, forward_args(packed), **c)
+        assert good() == (ValueError, "dense_block: " + HERE)
+        assert good(b1=None, b2=None, norm_w=None, norm_b=None) == (ValueError, "dense_block: " + HERE)
+        assert good(b1=lambda t: t.float(), norm_w=lambda t: t.bfloat16(), norm_b=lambda t: t.bfloat16()) == (ValueError, "dense_block: " + HERE)
+        assert good(x=bf16(T, K + 5)[:, :K]) == (ValueError, "dense_block: " + HERE)      # rows may be apart
+        assert good(x=bf16(0, K)) == (ValueError, "dense_block: " + HERE)
+        assert good(x=torch.empty_strided((1, K), (1, 1), dtype=torch.bfloat16)) == (ValueError, "dense_block: " + HERE)
+    assert refusal(mx.dense_block_backward, backward_args()) == (ValueError, "dense_block_backward: " + HERE)
+    assert refusal(mx.mxfp8_forms, dict(x=bf16(3, 8))) == (ValueError, "mxfp8_forms: " + HERE)
+
+
+@pytest.mark.parametrize("name,bad", [("x", torch.float16), ("x", torch.float32), ("w1", torch.bfloat16), ("s1", torch.int32),
+                                      ("w2", torch.float32), ("s2", torch.int16), ("b1", torch.float16), ("b2", torch.float64),
+                                      ("norm_w", torch.float64), ("norm_b", torch.bfloat16), ("norm_b", torch.int32)])
+def test_types(name, bad):
+    kind, text = refusal(mx.dense_block, forward_args(), **{name: lambda t: t.to(bad)})
+    assert kind is TypeError and name in text
+
+
+@pytest.mark.parametrize("name", ["x", "w1", "s1", "w2", "s2", "b1", "b2", "norm_w", "norm_b"])
+def test_layouts(name):
+    kind, text = refusal(mx.dense_block, forward_args(), **{name: apart})
+    assert kind is ValueError and name in text
+
+
+@pytest.mark.parametrize("name,cut", [("x", lambda t: t[:, :32]), ("x", lambda t: t[0]), ("x", lambda t: t[:1].expand(T, K)),
+                                      ("w1", lambda t: t[:, :48]), ("w1", lambda t: t.t()), ("w2", lambda t: t[:, :64]),
+                                      ("w2", lambda t: t[:48]), ("s1", lambda t: t[:, :1]), ("s2", lambda t: t[:, :2]),
+                                      ("b1", lambda t: t[:95]), ("b2", lambda t: t[:, None]), ("norm_w", lambda t: t[:63]),
+                                      ("norm_b", lambda t: t[None])])
+def test_shapes(name, cut):
+    kind, text = refusal(mx.dense_block, forward_args(), **{name: cut})
+    assert kind is ValueError and (name in text or "w1" in text)
+
+
+def test_sizes_and_codes():
+    for K_, F_ in ((48, 96), (64, 80)):
+        args = dict(forward_args(), x=bf16(T, K_), w1=u8(F_, K_), s1=u8(F_, K_ // 32), w2=u8(K_, F_), s2=u8(K_, F_ // 32), b1=None, b2=None,
+                    norm_w=None, norm_b=None)
+        assert refusal(mx.dense_block, args) == (ValueError, "dense_block: K and F multiples of 32 expected")
+    for bad in (-1, 5, 99):
+        assert "act" in refusal(mx.dense_block, forward_args(), act=bad)[1]
+    for bad in (-1, 2, mx.MXFP6_E2M3, mx.MXFP4_E2M1_PADDED):
+        assert "formats" in refusal(mx.dense_block, forward_args(), fmt=bad)[1]
+        assert "formats" in refusal(mx.dense_block_backward, backward_args(), fmt_grad=bad)[1]
+        assert "formats" in refusal(mx.mxfp8_forms, dict(x=bf16(3, 8)), fmt=bad)[1]
+    assert "keep" in refusal(mx.dense_block, forward_args(packed=True), keep=True)[1]
+
+
+@pytest.mark.parametrize("name,bad,kind", [("dout", lambda t: t.float(), TypeError), ("dout", lambda t: t[:9], ValueError),
+                                           ("dout", apart, ValueError), ("dout", bf16(T, K + 4)[:, :K], ValueError),
+                                           ("dout", bf16(T, K + 8)[:, 4:K + 4], ValueError),
+                                           ("w1t", lambda t: t.t(), ValueError), ("w2t", lambda t: t.bfloat16(), TypeError),
+                                           ("s1t", lambda t: t[:, :1], ValueError), ("s2t", lambda t: t[:90], ValueError)])
+def test_gradients_arguments(name, bad, kind):
+    got, text = refusal(mx.dense_block_backward, backward_args(), **{name: bad})
+    assert got is kind and name in text
+
+
+def test_forms_arguments():
+    for bad, kind in ((bf16(3, 8).float(), TypeError), (bf16(8), ValueError), (bf16(3, 12)[:, :8], ValueError), (bf16(0, 8), ValueError),
+                      (bf16(8, 8).t(), ValueError), (bf16(3, 20)[:, 4:12], ValueError)):
+        with pytest.raises(kind) as e:
+            mx.mxfp8_forms(bad)
+        assert "GPU" not in str(e.value)
+    with pytest.raises(ValueError, match="at least one form"):
+        mx.mxfp8_forms(bf16(3, 8), rows=False, columns=False)
