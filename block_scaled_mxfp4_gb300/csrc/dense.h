@@ -36,17 +36,24 @@ struct CheckpointArgs {
     int64_t ldz, ld_sz;
     int fmt_z;
     int rows, cols;
-    int64_t strips, col_blocks; // blocks along the rows and along the columns
-    int steps;                  // tiles of a warp along the rows
+    int64_t strips, across;     // blocks below one another and side by side (checkpoint_shape)
+    int steps;                  // tiles of a block
     int act;
     int vec_dz;                 // dz's rows allow 16-byte stores
-    int wide_q, wide_qt, wide_ht;   // rows allow 32-byte stores (set at launch)
+    int wide_q, wide_qt;        // rows allow 32-byte stores (set at launch)
     long long wait_limit;
 };
-// Row strips of a call and the tiles of a warp in each: by its sizes alone, so that the sums' order is too.
-int64_t checkpoint_strips(int rows, int cols, bool backward, int *steps);
-// mx: x in boxes of 64 columns x 128 rows, 128-byte swizzle; mz (backward): z likewise, 64-byte swizzle.
-cudaError_t launch_checkpoint(CheckpointArgs &a, const CUtensorMap &mx, const CUtensorMap &mz, bool backward, cudaStream_t stream);
+// A call's tiles, from rows and cols alone, so that the sums' order is too.
+void checkpoint_shape(CheckpointArgs &a, bool backward);
+// x in boxes of 64 columns x 128 rows, 128-byte swizzle.
+cudaError_t launch_checkpoint(CheckpointArgs &a, const CUtensorMap &x, cudaStream_t stream);
+// The backward pass's arrays: x and z in boxes of 64 columns x 128 rows, 128- and 64-byte swizzle; the
+// codes along the rows like z, those along the columns in boxes of 128 rows' codes x 64 columns, 128-byte
+// swizzle (those of an output that is not wanted: zeros).
+struct BackwardMaps {
+    CUtensorMap x, z, by_row, by_col, act_by_col;
+};
+cudaError_t launch_act_backward(const CheckpointArgs &a, const BackwardMaps &maps, cudaStream_t stream);
 cudaError_t read_checkpoint_status(int *status, int reset);
 
 // a[c] and b[c]: sums over the strips of partials[strip][na + nb], in a fixed order; zeros for

@@ -50,25 +50,32 @@ int check_workspace(size_t need, const void *workspace, size_t bytes)
     return aligned(workspace, kAlign) ? MXFP4_OK : MXFP4_ERR_MISALIGNED;
 }
 
-// Rows of `size`-byte elements in boxes of 64 columns x 128 rows, zeros past the last ones.
-bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, int rows, int cols, int64_t ld, int size, CUtensorMapSwizzle swizzle)
+// Rows of `size`-byte elements in boxes of `wide` columns x `tall` rows, zeros past the last ones.
+bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t rows, int64_t cols, int64_t ld, int size, int wide, int tall,
+            CUtensorMapSwizzle swizzle)
 {
     auto enc = tensor_map_encode_fn();
     if (!enc)
         return false;
     if (rows == 1)
-        ld = (static_cast<int64_t>(cols) + 15) / 16 * 16;    // a lone row's stride can be anything
+        ld = (cols + 15) / 16 * 16;                      // a lone row's stride can be anything
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * static_cast<cuuint64_t>(size)};
-    const cuuint32_t box[2] = {64, 128}, ones[2] = {1, 1};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(wide), static_cast<cuuint32_t>(tall)}, ones[2] = {1, 1};
     return enc(map, type, 2, const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same of an output's codes [rows, cols], whole blocks of 32 in each row; true too where it is not wanted.
+bool encode_codes(CUtensorMap *map, const CodesOut &o, int64_t rows, int64_t cols, int wide, int tall, CUtensorMapSwizzle swizzle)
+{
+    return !o.q || encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.q, rows, (cols + 31) / 32 * 32, o.ldq, 1, wide, tall, swizzle);
+}
+
 int run_checkpoint(CheckpointArgs &a, bool backward, const void *workspace, size_t workspace_bytes, cudaStream_t stream)
 {
-    a.strips = checkpoint_strips(a.rows, a.cols, backward, &a.steps);
-    if (a.strips * ((static_cast<int64_t>(a.cols) + 31) / 32) > 0x7FFFFFFF)
+    checkpoint_shape(a, backward);
+    if (a.strips * a.across > 0x7FFFFFFF)
         return MXFP4_ERR_UNSUPPORTED_SHAPE;              // more blocks than a grid has
     int st = check_workspace(a.sums ? partial_bytes(a.strips, a.cols) : 0, workspace, workspace_bytes);
     if (st != MXFP4_OK)
@@ -79,12 +86,18 @@ int run_checkpoint(CheckpointArgs &a, bool backward, const void *workspace, size
         return st;
     a.partials = static_cast<float *>(const_cast<void *>(workspace));
     a.wait_limit = current_wait_limit();
-    CUtensorMap mx, mz;
-    std::memset(&mz, 0, sizeof(mz));
-    if (!encode(&mx, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.rows, a.cols, a.ldx, 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        (backward && !encode(&mz, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.z, a.rows, a.cols, a.ldz, 1, CU_TENSOR_MAP_SWIZZLE_64B)))
+    BackwardMaps m;
+    std::memset(&m, 0, sizeof(m));
+    if (!encode(&m.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.rows, a.cols, a.ldx, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
         return MXFP4_ERR_CUDA;
-    return status_of(launch_checkpoint(a, mx, mz, backward, stream));
+    if (!backward)
+        return status_of(launch_checkpoint(a, m.x, stream));
+    if (!encode(&m.z, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.z, a.rows, a.cols, a.ldz, 1, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_codes(&m.by_row, a.by_row, a.rows, a.cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_codes(&m.by_col, a.by_col, a.cols, a.rows, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_codes(&m.act_by_col, a.act_by_col, a.cols, a.rows, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+        return MXFP4_ERR_CUDA;
+    return status_of(launch_act_backward(a, m, stream));
 }
 
 // Rows of 16-bit values as the checkpoint kernels read them.
@@ -128,10 +141,16 @@ size_t mxfp8_checkpoint_workspace_size(int rows, int cols)
 {
     if (rows < 1 || cols < 1 || rows > kMaxCount || cols > kMaxCount)
         return 0;
-    int steps = 0;
-    const size_t a = partial_bytes(checkpoint_strips(rows, cols, false, &steps), cols);
-    const size_t b = partial_bytes(checkpoint_strips(rows, cols, true, &steps), cols);
-    return a > b ? a : b;
+    size_t need = 0;
+    for (const bool backward : {false, true}) {
+        CheckpointArgs a{};
+        a.rows = rows;
+        a.cols = cols;
+        checkpoint_shape(a, backward);
+        const size_t bytes = partial_bytes(a.strips, cols);
+        need = need > bytes ? need : bytes;
+    }
+    return need;
 }
 
 int mxfp8_checkpoint(void *Q, int64_t ldq, void *S, int64_t lds, void *QT, int64_t ldqt, void *ST, int64_t ldst, float *col_sums,

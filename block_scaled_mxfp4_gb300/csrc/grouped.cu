@@ -296,21 +296,6 @@ __device__ __forceinline__ void cluster_leave(bool stored)
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// 2-D tiled bulk-tensor store from shared memory (x innermost), in this
-// thread's current bulk group.
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(smem_addr(src)), "r"(x), "r"(y)
-                 : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-// The group's shared memory has been read / its writes are done.
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-
 // 32 columns: alpha, one rounding, bf16 pairs.
 __device__ __forceinline__ void round_bf16(const GroupedArgs &a, const uint32_t (&x)[32], uint32_t (&out)[16])
 {

@@ -55,6 +55,27 @@ __device__ __forceinline__ int block_exponent8(float amax, int emax)
     return s < -127 ? -127 : (s > 127 ? 127 : s);
 }
 
+// Output formats of the quantising kernels: packed E2M1, or one E4M3 / E5M2
+// code per byte (the ABI's MXFP8_E4M3 and MXFP8_E5M2).
+enum class QuantFmt { kE2M1, kE4M3, kE5M2 };
+
+// The scale code of a block for a byte format (its E8M0 byte; 0xFF for an infinity or a NaN among
+// its values) and the factor 2^-s, from the largest magnitude.  The code is the float's own biased
+// exponent less emax: at most 254 - emax, so 2^-s is a normal number.
+template <QuantFmt Q>
+__device__ __forceinline__ uint32_t block_scale8(float amax, float &inv)
+{
+    constexpr int kEmax = Q == QuantFmt::kE4M3 ? 8 : 15;
+    const uint32_t bits = __float_as_uint(amax);
+    int code = static_cast<int>(bits >> 23) - kEmax;
+    code = code < 0 ? 0 : code;
+    const bool finite = bits < 0x7F800000u;
+    if (bits == 0u || !finite)
+        code = 127;
+    inv = __uint_as_float(static_cast<uint32_t>(254 - code) << 23);
+    return finite ? static_cast<uint32_t>(code) : 0xFFu;
+}
+
 // Two floats -> two 8-bit codes: `lo` in bits 0-7, `hi` in bits 8-15.
 template <int FMT>
 __device__ __forceinline__ uint32_t f8x2(float lo, float hi)
@@ -80,10 +101,6 @@ __device__ __forceinline__ float exp2_neg(int s)
 {
     return s == 127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(127 - s) << 23);
 }
-
-// Output formats of the quantising kernels: packed E2M1, or one E4M3 / E5M2
-// code per byte (the ABI's MXFP8_E4M3 and MXFP8_E5M2).
-enum class QuantFmt { kE2M1, kE4M3, kE5M2 };
 
 template <QuantFmt Q>
 struct QuantTraits {
@@ -136,18 +153,16 @@ __device__ __forceinline__ uint32_t quantize_block_pairs(const float (&x)[32], u
 #pragma unroll
     for (int i = 0; i < 32; i += 2)
         amax = max_abs3(amax, x[i], x[i + 1]);
-    const bool finite = amax <= 3.402823466e38f;     // not for infinities and NaN
-    if (!finite)
-        amax = 0.0f;
-    const int s = block_exponent8(amax, Q == QuantFmt::kE4M3 ? 8 : 15);
-    const F2 inv = f2(exp2_neg(s));
+    float factor;
+    const uint32_t code = block_scale8<Q>(amax, factor);
+    const F2 inv = f2(factor);
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
         constexpr int kF = Q == QuantFmt::kE4M3 ? 0 : 1;
         const float2 lo = parts(f2(x[4 * w], x[4 * w + 1]) * inv), hi = parts(f2(x[4 * w + 2], x[4 * w + 3]) * inv);
         out[w] = f8x2<kF>(lo.x, lo.y) | (f8x2<kF>(hi.x, hi.y) << 16);
     }
-    return finite ? static_cast<uint32_t>(s + 127) : 0xFFu;
+    return code;
 }
 
 }  // namespace mxfp4
