@@ -42,14 +42,10 @@ __device__ __forceinline__ float act_bias(const ActGemmArgs &a, int n)
                        : bf16_bits_to_float(__ldg(static_cast<const uint16_t *>(a.bias) + n));
 }
 
-// bias[n0 .. n0 + 31], zeros past N and for no bias.
+// bias[n0 .. n0 + 31], zeros past N.
 __device__ __forceinline__ void act_bias_chunk(const ActGemmArgs &a, int n0, float (&b)[32])
 {
-    if (!a.bias) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            b[i] = 0.0f;
-    } else if (a.bias_vec && n0 + 32 <= a.N) {
+    if (a.bias_vec && n0 + 32 <= a.N) {
         if (a.bias_fp32) {
             const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.bias) + n0);
 #pragma unroll
@@ -210,15 +206,16 @@ __device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m0, int 
 {
     const int m = m0 + lane;
     const bool real = m < a.M, full = n0 + 32 <= a.N;
-    {
+    if (a.bias) {
         float b[32];
         act_bias_chunk(a, n0, b);
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const float2 z = parts(fma2(f2(a.alpha), f2(v[i], v[i + 1]), f2(b[i], b[i + 1])));
-            v[i] = z.x;
-            v[i + 1] = z.y;
-        }
+        for (int i = 0; i < 32; ++i)
+            v[i] = fmaf(a.alpha, v[i], b[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] *= a.alpha;
     }
     if (a.Z.q) {
         if (!full) {
