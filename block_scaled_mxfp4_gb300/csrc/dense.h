@@ -77,13 +77,13 @@ struct NormArgs {
     int64_t lddx;
     float *dw, *db;             // backward: [N], either may be null
     float *partials;            // backward: [blocks][2][N]
-    int blocks;                 // backward: blocks that share the rows
+    int blocks;                 // backward: blocks that share the rows (at most, until it is launched)
     int T, N;
     int width;                  // elements of the widest access that every row allows: 8, 4, 2, 1
     long long wait_limit;
 };
 cudaError_t launch_layer_norm(const NormArgs &a, int sms, cudaStream_t stream);
-int norm_backward_blocks(int T, int N);
+int norm_backward_blocks(int T, int N);              // at most, by the sizes
 cudaError_t launch_layer_norm_backward(NormArgs &a, cudaStream_t stream);
 cudaError_t read_norm_status(int *status, int reset);
 

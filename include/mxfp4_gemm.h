@@ -724,7 +724,8 @@ int mxfp4_layer_norm(void *Y, int64_t ldy, float *mean, float *rstd, const void 
  *   dres  bf16 [T, ldr] or NULL: the gradient that passes the norm by (the
  *         residual stream's), added before the one rounding
  *   dw, db may be NULL.  dX may alias dY, X or dres (with the same stride).
- * The sums' order depends on T and N alone.  T = 0 writes zeros to dw and db.
+ * The sums' order depends on T, N and the rows' alignment alone.  T = 0 writes zeros to
+ * dw and db.
  * workspace: mxfp4_layer_norm_workspace_size(T, N) bytes, 256-byte aligned,
  * contents arbitrary; used for dw and db alone.
  */
