@@ -688,7 +688,7 @@ static bool byte_format_ok(int fmt)
 // does, provided that the plan relays the scales (whose workspace the caller has
 // sized by it): its epilogue runs under the next tile's MMAs, the one-tile
 // kernel's after its own (8192 x 8192 x 4096 with GELU and two outputs in 8
-// bits: 298 us there).
+// bits: 298 us there, 185 to 215 on pairs).
 static void pair_for_bytes(mxfp4_plan *plan, GemmShape *shape, int M, int N, int sms)
 {
     const int64_t tiles = ((static_cast<int64_t>(M) + 255) / 256) * ((static_cast<int64_t>(N) + 255) / 256);
