@@ -290,6 +290,8 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : PARAMS ? 512 : 1024) n
         }
     }
     if constexpr (PARAMS) {
+        if (!a.dw && !a.db)
+            return;                                      // (and perhaps no workspace)
         float *out[2] = {a.dw, a.db};
         if (gridDim.x > 1) {
             out[0] = a.partials + static_cast<int64_t>(blockIdx.x) * 2 * a.N;
