@@ -109,7 +109,9 @@ __device__ __forceinline__ F2 act_value2(F2 z)
     if constexpr (A == Act::kGelu) {
         // z Phi(z) = max(z, 0) - |z| Phi(-|z|)
         const float2 p = parts(z);
-        const F2 minus = f2(-fabsf(p.x), -fabsf(p.y)), above = f2(p.x < 0.0f ? 0.0f : p.x, p.y < 0.0f ? 0.0f : p.y);
+        // (bounded, as Phi is 0 long before and infinity times 0 is NaN; a NaN comes through `above`)
+        const F2 minus = f2(fmaxf(-fabsf(p.x), -1e30f), fmaxf(-fabsf(p.y), -1e30f)),
+                 above = f2(p.x < 0.0f ? 0.0f : p.x, p.y < 0.0f ? 0.0f : p.y);
         return fma2(minus, normal_tail2(minus, bell2(z)), above);
     }
     F2 h, slope;

@@ -629,6 +629,8 @@ size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F);
  * tail.  Relative to an activation's value its error stays within 2^-19 + |u| 2^-21,
  * u the exponential's argument (z^2 / 2 for GELU, sqrt(8 / pi) (z + 0.044715 z^3) for
  * its tanh form, z for SiLU); a value under the smallest normal number may be 0.
+ * In a product's epilogue z = infinity gives infinity, and minus infinity 0 (ReLU, GELU)
+ * or NaN (its tanh form, SiLU).
  * ------------------------------------------------------------------------ */
 
 enum { MXFP4_ACT_NONE = 0, MXFP4_ACT_RELU = 1, MXFP4_ACT_GELU = 2, MXFP4_ACT_GELU_TANH = 3, MXFP4_ACT_SILU = 4 };

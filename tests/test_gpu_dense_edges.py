@@ -198,3 +198,21 @@ def test_norm_gradient_without_sums_or_workspace(T, N):
     mx.mxfp4_layer_norm_backward(got, N, None, None, dy, N, x, N, m, r, None, 0, None, 0, T, N, None, 0)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("form,M,N,K", [("mxfp8", 2560, 2304, 512), ("mxfp8", 300, 96, 160), ("mxfp4", 3, 97, 8192), ("mxfp4", 130, 290, 2048)])
+@pytest.mark.parametrize("act", dr.ACTS)
+def test_infinite_and_missing_biases_stay_in_their_columns(form, M, N, K, act):
+    p = Product(form, M, N, K, 4)
+    bias = torch.randn(N, device="cuda")
+    want = p.run(act, bias, "fp32")[0]
+    odd = bias.clone()
+    odd[1], odd[40], odd[65] = float("inf"), float("-inf"), float("nan")
+    got = p.run(act, odd, "fp32")[0]
+    torch.cuda.synchronize()
+    assert (got[:, 1] == float("inf")).all() and got[:, 65].isnan().all()
+    low = got[:, 40]
+    assert {"none": low == float("-inf"), "relu": low == 0, "gelu": low == 0}.get(act, low.isnan()).all()
+    keep = torch.ones(N, dtype=torch.bool, device="cuda")
+    keep[[1, 40, 65]] = False
+    assert torch.equal(got[:, keep], want[:, keep])
