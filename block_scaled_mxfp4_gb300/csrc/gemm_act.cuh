@@ -201,13 +201,23 @@ __device__ __forceinline__ void act_fetch_row(const ActGemmArgs &a, int m, int n
 
 // Rows m0 .. m0 + 31 (m0 < M), one a lane, columns n0 .. n0 + 31 (n0 < N): v holds
 // the accumulators.  All lanes call it; `piece`: kActPieceBytes of the warp's own.
-// The blocks' scale codes go to byte `at` of `scales`; `r4`: what act_fetch_row left.
+// The blocks' scale codes go to byte `at` of `scales`; `r4`: what act_fetch_row left; `bias`: the 32
+// columns' in shared memory, or null.
 __device__ __forceinline__ void act_row_chunk(const ActGemmArgs &a, int m0, int n0, int lane, float (&v)[32], const uint4 (&r4)[4],
-                                              uint16_t *piece, int at, ActScales &scales)
+                                              uint16_t *piece, int at, ActScales &scales, const float *bias = nullptr)
 {
     const int m = m0 + lane;
     const bool real = m < a.M, full = n0 + 32 <= a.N;
-    if (a.bias) {
+    if (a.bias && bias) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            const float4 b = *reinterpret_cast<const float4 *>(bias + i);
+            v[i] = fmaf(a.alpha, v[i], b.x);
+            v[i + 1] = fmaf(a.alpha, v[i + 1], b.y);
+            v[i + 2] = fmaf(a.alpha, v[i + 2], b.z);
+            v[i + 3] = fmaf(a.alpha, v[i + 3], b.w);
+        }
+    } else if (a.bias) {
         float b[32];
         act_bias_chunk(a, n0, b);
 #pragma unroll

@@ -83,7 +83,8 @@ struct PairCfg {
     static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
     static constexpr int BAR_BYTES = 512;
     static constexpr int PIECE_BYTES = EPI ? 8 * kActPieceBytes : 0;   // gemm_act.cuh's, one an epilogue warp
-    static constexpr int SMEM_BYTES = RING_BYTES + BAR_BYTES + PIECE_BYTES + 1024;
+    static constexpr int BIAS_BYTES = EPI ? 8 * 128 * 4 : 0;           // fp32, of an epilogue warp's columns
+    static constexpr int SMEM_BYTES = RING_BYTES + BAR_BYTES + PIECE_BYTES + BIAS_BYTES + 1024;
     static constexpr int SF_COLS_A = 4 * GROUPS;          // 4 columns per k-group
     static constexpr int SF_COLS_B = 4 * GROUPS * SFB_RB; // and per 128-row block
     static constexpr int SF_COLS = SF_COLS_A + SF_COLS_B; // one scale slot per stage
@@ -463,14 +464,26 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
         const int row = quarter * 32 + lane;
         [[maybe_unused]] uint16_t *piece =
             reinterpret_cast<uint16_t *>(smem + PC::RING_BYTES + PC::BAR_BYTES + (half * 4 + quarter) * kActPieceBytes);
+        [[maybe_unused]] float *bias =
+            reinterpret_cast<float *>(smem + PC::RING_BYTES + PC::BAR_BYTES + PC::PIECE_BYTES) + (half * 4 + quarter) * 128;
         const uint32_t t_lane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + half * PC::HALF;
         uint32_t acc_phase = 0;
         for (int t = cl; t < tiles; t += ncl) {
             if constexpr (EPI) {
-                // R's lines come to L2 while the tile's MMAs run.
+                // While the tile's MMAs run R's lines come to L2, the bias to shared memory (from L2 for
+                // each piece, 8192 x 8192 x 2048 MXFP8 with bias, GELU and residual took 183 us for 166).
                 int pt, qt;
                 pair_tile_coords(ps, t, pt, qt);
                 act_prefetch_row(a, pt * 256 + static_cast<int>(rank) * kTileM + row, qt * BN + half * PC::HALF, PC::HALF);
+                if (a.bias) {
+                    __syncwarp();
+#pragma unroll
+                    for (int i = lane; i < PC::HALF; i += 32) {
+                        const int n = qt * BN + half * PC::HALF + i;
+                        bias[i] = n < a.N ? act_bias(a, n) : 0.0f;
+                    }
+                    __syncwarp();
+                }
             }
             bool ok = mbar_wait(acc_full, acc_phase, abort_flag, a.wait_limit, &g_device_status);
             ok = __all_sync(0xffffffffu, ok);
@@ -524,7 +537,7 @@ __global__ void __launch_bounds__(PairCfg<STAGES, NV>::THREADS, 1)
                     if (m - lane < a.M && n < a.N) {         // (the warp's)
                         uint4 r4[4];
                         act_fetch_row(a, m, n, r4);
-                        act_row_chunk(a, m - lane, n, lane, v, r4, piece, c, scales);
+                        act_row_chunk(a, m - lane, n, lane, v, r4, piece, c, scales, bias + 32 * c);
                     }
                     if (c == 0) {
                         __syncwarp();
