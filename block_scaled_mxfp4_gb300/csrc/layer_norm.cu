@@ -957,7 +957,13 @@ bool stream_shape(const NormArgs &a, bool backward, StreamShape &sh)
     const int stage = sh.rows * sh.arrays * sh.slot;
     const int room = kRingBytes - (backward ? 0 : (a.N + 7) / 8 * 64);
     sh.depth = room / stage < kRing ? room / stage : kRing;
-    return sh.depth >= 2 && a.T >= sh.rows * kStreamBlocks * (backward ? 1 : 4);
+    // Against the kernels above: aligned rows of the norm gain from four full rounds of stages on (2432 x 2048:
+    // 6.2 us there, 7.8 here); others, which those take element by element, soon (608 x 1501: 10.1 there,
+    // 6.4 here); its gradients of more than 1024 soon too, as each of its blocks writes one partial
+    // sum for all its rows (304 x 2048: 14.2 there, 9.7 here; 1216 x 701: 10.7 and 10.5).
+    const int full = sh.rows * kStreamBlocks;            // every block's first stage
+    const int least = backward ? (a.N > kWarpRow ? full / 4 : full) : a.width == 8 ? 4 * full : full / 4;
+    return sh.depth >= 2 && a.T >= least;
 }
 
 template <int W, int EPT, bool WARP>
@@ -974,10 +980,11 @@ template <int W>
 cudaError_t start_norm_width(const NormArgs &a, int sms, cudaStream_t stream)
 {
     // Many rows: 32 elements a thread, so that many rows are in flight on an SM.  Few: eight, the shortest
-    // time for one row.
-    const bool many = a.T > 2 * sms;
+    // time for one row; with narrow accesses up to more rows, whose code for 32 is long (608 x 701: 8.1 us
+    // with 32, 4.8 with eight).
+    const bool many = a.T > (W < 8 ? 8 : 2) * sms;
     StreamShape sh;
-    if (stream_shape(a, false, sh)) {
+    if (a.T > 2 * sms && stream_shape(a, false, sh)) {
         const int bytes = sh.depth * sh.rows * sh.slot + (a.N + 7) / 8 * 64;
         auto kernel = norm_stream_kernel<W == 8>;
         const cudaError_t e = opt_in<norm_stream_kernel<W == 8>>(bytes);
@@ -1012,15 +1019,19 @@ template <int W>
 cudaError_t start_backward_width(NormArgs &a, cudaStream_t stream)
 {
     StreamShape sh;
-    if (stream_shape(a, true, sh)) {
-        a.blocks = kStreamBlocks;                        // (never more than norm_backward_blocks)
+    // A few rows of middling length: eight elements a thread, a block each, while their partial sums are
+    // small (152 x 2048: 8.6 us, streamed 10.0; 304 x 2048: 11.9 and 9.8).
+    const bool few_long = a.N > kWarpRow && a.N <= 4096 && static_cast<int64_t>(a.T) * a.N <= 3 << 17;
+    if (!few_long && stream_shape(a, true, sh)) {
+        const int stages = (a.T + sh.rows - 1) / sh.rows;
+        a.blocks = stages < kStreamBlocks ? stages : kStreamBlocks;      // (never more than norm_backward_blocks)
         const int ring = sh.depth * sh.rows * sh.arrays * sh.slot, joint = sh.rows * a.N * 4;
         const int bytes = ring > joint ? ring : joint;
         auto kernel = norm_backward_stream_kernel<W == 8>;
         const cudaError_t e = opt_in<norm_backward_stream_kernel<W == 8>>(bytes);
         if (e != cudaSuccess)
             return e;
-        return launch_dependent(kernel, dim3(kStreamBlocks), dim3(kStreamThreads),
+        return launch_dependent(kernel, dim3(static_cast<unsigned>(a.blocks)), dim3(kStreamThreads),
                                 static_cast<size_t>(bytes), stream, a, sh);
     }
     // A row of up to 1024 is a warp's where there are many: fewer partial sums.  Few are a block's each,
@@ -1034,6 +1045,8 @@ cudaError_t start_backward_width(NormArgs &a, cudaStream_t stream)
         a.blocks = backward_blocks(a.T, kRowWarps);
         return a.N <= 256 ? start_backward<W, 8, true, true>(a, stream) : start_backward<W, 32, true, true>(a, stream);
     }
+    if (few_long)
+        return start_backward<W, 8, false, true>(a, stream);
     if (a.N <= 8192)
         return start_backward<W, 16, false, true>(a, stream);
     if (a.N <= kBlockRow)

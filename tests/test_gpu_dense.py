@@ -602,6 +602,7 @@ def check_norm_backward(T, N, kind="bf16", w=True, resid=True, ld=None, shift=0,
     dw, db = (torch.full((N,), float("nan"), device="cuda") if p else None for p in params)
     need = mx.mxfp4_layer_norm_workspace_size(T, N)
     ws = workspace(need)
+    torch.cuda.synchronize()                                # (arrays are filled on the current stream)
     mx.mxfp4_layer_norm_backward(dX, dX.stride(0), dw, db, dY, dY.stride(0), X, X.stride(0), m, r, dw_, KIND[kind], R,
                                  R.stride(0) if resid else 0, T, N, ws, need, stream=stream)
     wx, ww, wb, ex, ew, eb = dr.norm_backward(x, dy, mean, rstd, w, res)

@@ -7,7 +7,7 @@ import pytest
 import block_scaled_mxfp4_gb300 as mx
 import dense_ref as dr
 from block_scaled_mxfp4_gb300 import inputs
-from test_gpu_dense import KIND, Product, bf16, check_norm_backward, checkpoint_of, dev, host, run_backward, run_checkpoint, workspace
+from test_gpu_dense import KIND, Product, bf16, check_norm, check_norm_backward, checkpoint_of, dev, host, run_backward, run_checkpoint, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -216,3 +216,18 @@ def test_infinite_and_missing_biases_stay_in_their_columns(form, M, N, K, act):
     keep = torch.ones(N, dtype=torch.bool, device="cuda")
     keep[[1, 40, 65]] = False
     assert torch.equal(got[:, keep], want[:, keep])
+
+
+@pytest.mark.parametrize("T,N", [(305, 6001), (305, 8191), (460, 1501), (609, 3001), (913, 301), (1217, 701), (1300, 258), (39, 8191), (38, 8192), (77, 4097),
+                                 (76, 4104), (97, 4096), (263, 1500), (300, 1501), (192, 2048), (193, 2048), (200, 1030)])
+def test_norms_between_few_and_many_rows(T, N):
+    check_norm(T, N, "fp32")
+    check_norm_backward(T, N, "bf16")
+    need = mx.mxfp4_layer_norm_workspace_size(T, N)          # nothing behind the workspace is written
+    ws = workspace(need + (1 << 20))
+    x, dy = (torch.randn((T, N), device="cuda").bfloat16() for _ in range(2))
+    m, r = torch.zeros(T, device="cuda"), torch.ones(T, device="cuda")
+    dx, dw, db = torch.empty_like(x), torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+    mx.mxfp4_layer_norm_backward(dx, N, dw, db, dy, N, x, N, m, r, None, 0, None, 0, T, N, ws, need)
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0xAB).all()
