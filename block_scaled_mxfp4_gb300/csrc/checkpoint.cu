@@ -23,31 +23,31 @@ namespace {
 // the load to the one rounding of each orientation.
 //
 // A block of 256 threads takes tiles of 128 rows, one below the other, by 128 columns
-// (64 in the backward pass), copied to shared memory by TMA while the tile before is
-// worked on.
+// (128 threads, 64 by 64 in the backward pass), copied to shared memory by TMA while the
+// tile before is worked on.
 //
 // Why not straight from global memory, a row or column per lane: each such
 // access touches 32 lines, and the L1's tag stage, one line a cycle, was 80 %
 // busy at half of HBM's rate.  Copies by cp.async instead of TMA took as many of
 // its cycles as all stores together.
 
-constexpr int kThreads = 256;
-constexpr int kTileRows = 128;
 constexpr int kSms = 152;
 
 template <bool BACKWARD>
 struct Tile {
+    static constexpr int kThreads = BACKWARD ? 128 : 256;
+    static constexpr int kRows = BACKWARD ? 64 : 128;
     static constexpr int kCols = BACKWARD ? 64 : 128;
-    static constexpr int kBox = kTileRows * 128;         // 64 columns of x: 128-byte rows, 128-byte swizzle
+    static constexpr int kBox = kRows * 128;             // 64 columns of x: 128-byte rows, 128-byte swizzle
     static constexpr int kXBytes = kCols / 64 * kBox;
-    static constexpr int kZBytes = BACKWARD ? kTileRows * 64 : 0;   // 64-byte rows, 64-byte swizzle
+    static constexpr int kZBytes = BACKWARD ? kRows * 64 : 0;       // 64-byte rows, 64-byte swizzle
     static constexpr int kStage = kXBytes + kZBytes;
-    static constexpr int kDz = BACKWARD ? kTileRows * 256 : 0;      // dz, fp32
-    static constexpr int kScales = BACKWARD ? 2 * kThreads * 8 : 0; // z's scales of two tiles, each twice
-    static constexpr int kCodes = BACKWARD ? kTileRows * kCols : 0; // of one output of a tile
-    static constexpr int kAlign = BACKWARD ? 2048 : 1024; // the swizzle's, and that of dz's rows
-    static constexpr int kBytes = 2 * kStage + kDz + 3 * kCodes + kScales + kAlign;
-    static constexpr int kResident = BACKWARD ? 2 : 3;
+    static constexpr int kDz = BACKWARD ? kRows * 256 : 0;          // dz, fp32
+    static constexpr int kCodes = BACKWARD ? kRows * kCols : 0;     // of one output of a tile
+    static constexpr int kScales = BACKWARD ? 2 * kThreads * 4 : 0; // z's scales of two tiles
+    static constexpr int kAlign = BACKWARD ? 2048 : 1024;           // the swizzle's, and that of dz's rows
+    static constexpr int kBytes = 2 * kStage + kDz + 3 * kCodes + kScales + kAlign - 1024;   // (the base is on 1024)
+    static constexpr int kResident = BACKWARD ? 4 : 3;
 };
 
 __device__ int g_status = 0;                     // bounded waits that ran out
@@ -133,18 +133,18 @@ __device__ __forceinline__ void put_col(const CodesOut &o, bool wide, int64_t co
 // that a warp's stores fall into whole lines (128 bytes of codes are four lanes') and
 // its shared-memory reads on different banks: TMA's swizzle moves 16-byte pieces by the
 // row, and lanes 32 rows apart read their column's rows in orders of their own.
-__global__ void __launch_bounds__(kThreads, Tile<false>::kResident)
+__global__ void __launch_bounds__(Tile<false>::kThreads, Tile<false>::kResident)
     checkpoint_kernel(const __grid_constant__ CheckpointArgs a, const __grid_constant__ CUtensorMap mx)
 {
     using T = Tile<false>;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t full[2];
     __shared__ int abort_flag;
-    uint8_t *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    uint8_t *smem = smem_raw;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t strip = blockIdx.x / a.across, col_first = blockIdx.x % a.across * static_cast<int64_t>(T::kCols);
-    const int64_t row_first = strip * a.steps * kTileRows;
-    const int tiles = static_cast<int>(min((a.rows - row_first + kTileRows - 1) / kTileRows, static_cast<int64_t>(a.steps)));
+    const int64_t row_first = strip * a.steps * T::kRows;
+    const int tiles = static_cast<int>(min((a.rows - row_first + T::kRows - 1) / T::kRows, static_cast<int64_t>(a.steps)));
     // The thread's column block: eight neighbouring pairs of columns to eight lanes, the four row
     // blocks of a column to lanes eight apart.
     const int rb = lane >> 3, cl = warp * 8 + (lane & 7);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kThreads, Tile<false>::kResident)
         load_tile<false>(&mx, nullptr, smem, &full[0], row_first, col_first);
     }
     for (int n = 0; n < tiles; ++n) {
-        const int64_t row0 = row_first + static_cast<int64_t>(n) * kTileRows;
+        const int64_t row0 = row_first + static_cast<int64_t>(n) * T::kRows;
         const uint32_t phase = n / 2 & 1;
         const uint8_t *stage = smem + (n & 1) * T::kStage;
         const bool ok = mbar_wait(&full[n & 1], phase, &abort_flag, a.wait_limit, &g_status);
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, Tile<false>::kResident)
         }
         // Every thread is past the tile before.
         if (n + 1 < tiles && threadIdx.x == 0)
-            load_tile<false>(&mx, nullptr, smem + (~n & 1) * T::kStage, &full[~n & 1], row0 + kTileRows, col_first);
+            load_tile<false>(&mx, nullptr, smem + (~n & 1) * T::kStage, &full[~n & 1], row0 + T::kRows, col_first);
         if (a.by_row.q) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -252,20 +252,21 @@ __global__ void __launch_bounds__(kThreads, Tile<false>::kResident)
 // shared memory too and leave it as whole boxes by TMA: stored by the lanes, each 32-byte
 // sector took the L1's data stage most of a cycle, a third of all its work.
 //
-// 8192 x 16384 with GELU, all outputs but dz itself: 233 us, 3.5 TB/s, of 121 that its
-// bytes need (245 computing along the rows, 239 with the lanes' own stores); 201 with
-// SiLU, 191 with none.  What bounds it is issue: 41 instructions per value, 14 of them
-// GELU's, on 16 warps an SM, which h and dz of 32 values in registers allow.
+// 8192 x 16384 with GELU, all outputs but dz itself: 205 us, 4.0 TB/s, of 121 that its
+// bytes need; 187 with SiLU, 185 with none.  (Computing along the rows 245, with the
+// lanes' own stores 239 of then 233, in blocks of 256 threads and tiles of 128 rows, whose
+// passes overlap less, 233.)  What bounds it is issue: 41 instructions per value, 14 of
+// them GELU's, on 16 warps an SM, which act(z) and dz of 32 values in registers allow.
 //
-// A warp has 8 columns and all 128 rows: a column's 128 codes are one row of its
-// box.  Its eight groups of 16 rows take them in orders of their own, row
-// i ^ key: each step's eight rows differ modulo 8, and TMA's swizzle (the row's low bits
-// move a 16-byte piece) spreads them over all banks.  dz is laid out by the same rule in
-// rows of 256 bytes; a half-warp's keys, 0, 2, 4 and 6 or 1, 3, 5 and 7, spread its 32-byte
-// pieces too.  Offsets of row i ^ key are the key's with i's bits flipped.
+// A warp has 16 columns and all 64 rows: a column's 64 codes are one row of its
+// box.  Its four groups of 16 rows take them in orders of their own, row i ^ key with the
+// keys 0, 4, 2 and 6, and TMA's swizzle (the row's low bits move a 16-byte piece) spreads
+// each step's four rows, two pieces of x each, over all banks.  dz is laid out by the
+// same rule in rows of 256 bytes; a half-warp's keys, four apart, spread its four pieces of
+// either row too.  Offsets of row i ^ key are the key's with i's bits flipped.
 
 // Two columns' values in the lane's 16 rows: their codes to shared memory (the first column's row of
-// them at `codes`, 16 rows' codes at `at`, moved by the column's low bits), and the scales of the first
+// them at `codes`, in its 16-byte piece `at`, moved by the column's bits), and the scales of the first
 // `have` of them.
 template <QuantFmt Q>
 __device__ __forceinline__ void put_two_columns(const CodesOut &o, uint8_t *codes, int have, int64_t col, int64_t row, int key, int half, const float2 (&v)[16])
@@ -280,7 +281,7 @@ __device__ __forceinline__ void put_two_columns(const CodesOut &o, uint8_t *code
     float inv[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const float other = __shfl_xor_sync(0xffffffffu, amax[k], 4);      // the block's other 16 rows
+        const float other = __shfl_xor_sync(0xffffffffu, amax[k], 8);      // the block's other 16 rows
         code[k] = block_scale8<Q>(max_abs3(amax[k], other, other), inv[k]);
     }
     constexpr int kF = Q == QuantFmt::kE4M3 ? 0 : 1;
@@ -294,14 +295,14 @@ __device__ __forceinline__ void put_two_columns(const CodesOut &o, uint8_t *code
     // Row i ^ key to place i: bytes within a word by the key's low bits, words in pairs by its third.
     const uint32_t order = 0x3210u ^ (0x1111u * (key & 3));
     const bool swap = key & 4;
-    const int at = static_cast<int>(row / 16) & 7, move = static_cast<int>(col) & 7;
+    const int at = (static_cast<int>(row / 16) & 3) ^ (static_cast<int>(col / 2) & 3);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             u[i] = __byte_perm(w[k][i], 0u, order);
-        *reinterpret_cast<uint4 *>(codes + 128 * k + (at ^ (move + k)) * 16) =
+        *reinterpret_cast<uint4 *>(codes + 64 * k + at * 16) =
             make_uint4(swap ? u[1] : u[0], swap ? u[0] : u[1], swap ? u[3] : u[2], swap ? u[2] : u[3]);
     }
     // One of the block's two lanes stores the one column's scale, one the other's.
@@ -327,12 +328,12 @@ __device__ __forceinline__ void back_columns(uint32_t xa, uint32_t za, uint32_t 
         const int lo = i & 7, hi = i >> 3;
         uint32_t x;
         uint16_t z;
-        F2 s;
+        float s;
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"((xa ^ (lo * 144)) + hi * 1024));
         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(z) : "r"((za ^ (lo * 64 + (lo >> 1) * 16)) + hi * 512));
-        asm volatile("ld.shared.b64 %0, [%1];" : "=l"(s.v) : "r"((sa ^ (lo * 8)) + hi * 64));
+        asm volatile("ld.shared.f32 %0, [%1];" : "=f"(s) : "r"((sa ^ (lo * 4)) + hi * 32));
         F2 act, slope;
-        act_and_slope2<ACT>(values_of<FMT>(z) * s, act, slope);
+        act_and_slope2<ACT>(values_of<FMT>(z) * f2(s), act, slope);
         h[i] = parts(act);
         d[i] = parts(f2(bf16_lo(x), bf16_hi(x)) * slope);
     }
@@ -366,11 +367,11 @@ __device__ __forceinline__ void put_dz(const CheckpointArgs &a, int64_t row, int
 }
 
 template <Act ACT>
-__global__ void __launch_bounds__(kThreads, Tile<true>::kResident)
+__global__ void __launch_bounds__(Tile<true>::kThreads, Tile<true>::kResident)
     act_backward_kernel(const __grid_constant__ CheckpointArgs a, const __grid_constant__ BackwardMaps maps)
 {
     using T = Tile<true>;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ uint64_t full[2];
     __shared__ int abort_flag;
     uint8_t *smem = smem_raw + ((T::kAlign - smem_addr(smem_raw) % T::kAlign) % T::kAlign);
@@ -378,15 +379,15 @@ __global__ void __launch_bounds__(kThreads, Tile<true>::kResident)
             *scales = row_codes + T::kCodes;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int64_t strip = blockIdx.x / a.across, col_first = blockIdx.x % a.across * static_cast<int64_t>(T::kCols);
-    const int64_t row_first = strip * a.steps * kTileRows;
-    const int tiles = static_cast<int>(min((a.rows - row_first + kTileRows - 1) / kTileRows, static_cast<int64_t>(a.steps)));
+    const int64_t row_first = strip * a.steps * T::kRows;
+    const int tiles = static_cast<int>(min((a.rows - row_first + T::kRows - 1) / T::kRows, static_cast<int64_t>(a.steps)));
     // The column pass: pair of columns, group of rows, and the offsets of the group's row `key`.
-    const int pair = lane & 3, group = lane >> 2, key = (group & 3) << 1 | group >> 2;
+    const int pair = lane & 7, group = lane >> 3, key = (group & 1) << 2 | (group & 2);
     const int top = 16 * group + key;
-    const uint32_t xo = top * 128 + (warp ^ key) * 16 + 4 * pair;
-    const uint32_t zo = top * 64 + ((warp >> 1) ^ (key >> 1)) * 16 + 8 * (warp & 1) + 2 * pair;
-    const uint32_t so = (warp >> 2) * (8 * kTileRows) + top * 8;
-    const uint32_t po = top * 256 + ((2 * warp + (pair >> 1)) ^ key) * 16 + 8 * (pair & 1);
+    const uint32_t xo = top * 128 + ((2 * warp + (pair >> 2)) ^ key) * 16 + 4 * (pair & 3);
+    const uint32_t zo = top * 64 + (warp ^ (key >> 1)) * 16 + 2 * pair;
+    const uint32_t so = (warp >> 1) * (4 * T::kRows) + top * 4;
+    const uint32_t po = top * 256 + ((4 * warp + (pair >> 1)) ^ key) * 16 + 8 * (pair & 1);
     float2 sum = make_float2(0.0f, 0.0f);                // of two columns
     // The row pass: eight neighbouring rows to eight neighbouring lanes, the two blocks of a row to lanes eight apart.
     const int rr = warp * 16 + (lane & 7) + 8 * (lane >> 4), rb = (lane >> 3) & 1;
@@ -403,22 +404,21 @@ __global__ void __launch_bounds__(kThreads, Tile<true>::kResident)
     };
     // The scale of z in the tile's row threadIdx % 128, block threadIdx / 128.
     auto z_scale = [&](int64_t row0) -> uint32_t {
-        const int64_t row = row0 + threadIdx.x % kTileRows, col0 = col_first + threadIdx.x / kTileRows * 32;
+        const int64_t row = row0 + threadIdx.x % T::kRows, col0 = col_first + threadIdx.x / T::kRows * 32;
         return row < a.rows && col0 < a.cols ? a.sz[row * a.ld_sz + col0 / 32] : 127u;
     };
     auto put_scale = [&](int n, uint32_t code) {
-        const float s = e8m0_value(code);
-        *reinterpret_cast<float2 *>(scales + (n & 1) * (8 * kThreads) + 8 * threadIdx.x) = make_float2(s, s);
+        *reinterpret_cast<float *>(scales + (n & 1) * (4 * T::kThreads) + 4 * threadIdx.x) = e8m0_value(code);
     };
     if (threadIdx.x == 0) {
         pdl_launch_dependents();
         load(0, row_first);
         if (tiles > 1)
-            load(1, row_first + kTileRows);
+            load(1, row_first + T::kRows);
     }
     put_scale(0, z_scale(row_first));
     for (int n = 0; n < tiles; ++n) {
-        const int64_t row0 = row_first + static_cast<int64_t>(n) * kTileRows;
+        const int64_t row0 = row_first + static_cast<int64_t>(n) * T::kRows;
         const uint32_t phase = n / 2 & 1;
         const uint8_t *stage = smem + (n & 1) * T::kStage;
         const bool ok = mbar_wait(&full[n & 1], phase, &abort_flag, a.wait_limit, &g_status);
@@ -435,23 +435,23 @@ __global__ void __launch_bounds__(kThreads, Tile<true>::kResident)
         }
         // Every thread is past the tile before, its codes and the scales are in place.
         if (n > 0 && a.by_row.q && threadIdx.x == 0) {
-            tma_store_2d(&maps.by_row, row_codes, static_cast<int>(col_first), static_cast<int>(row0) - kTileRows);
+            tma_store_2d(&maps.by_row, row_codes, static_cast<int>(col_first), static_cast<int>(row0) - T::kRows);
             bulk_commit();
         }
-        const uint32_t code = n + 1 < tiles ? z_scale(row0 + kTileRows) : 0u;
+        const uint32_t code = n + 1 < tiles ? z_scale(row0 + T::kRows) : 0u;
         const bool rows_too = a.by_row.q || a.dz;
         {
             float2 h[16], d[16];
             const uint32_t xa = smem_addr(stage) + xo, za = smem_addr(stage) + T::kXBytes + zo,
-                           sa = smem_addr(scales) + (n & 1) * (8 * kThreads) + so, pa = smem_addr(dz) + po;
+                           sa = smem_addr(scales) + (n & 1) * (4 * T::kThreads) + so, pa = smem_addr(dz) + po;
             if (a.fmt_z == 0)
                 back_columns<ACT, 0>(xa, za, sa, pa, h, d);
             else
                 back_columns<ACT, 1>(xa, za, sa, pa, h, d);
-            const int64_t col = col_first + 8 * warp + 2 * pair, row = row0 + 16 * group;
+            const int64_t col = col_first + 16 * warp + 2 * pair, row = row0 + 16 * group;
             const int have = (row & ~int64_t{31}) >= a.rows ? 0 : static_cast<int>(min(a.cols - col, int64_t{2}));
             if (a.act_by_col.q)
-                put_two_columns(a.act_by_col, h_codes + (8 * warp + 2 * pair) * 128, have, col, row, key, group & 1, h);
+                put_two_columns(a.act_by_col, h_codes + (16 * warp + 2 * pair) * 64, have, col, row, key, group & 1, h);
             if (a.sums) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, Tile<true>::kResident)
                 }
             }
             if (a.by_col.q)
-                put_two_columns(a.by_col, dz_codes + (8 * warp + 2 * pair) * 128, have, col, row, key, group & 1, d);
+                put_two_columns(a.by_col, dz_codes + (16 * warp + 2 * pair) * 64, have, col, row, key, group & 1, d);
         }
         if (n + 1 < tiles)
             put_scale(n + 1, code);
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Tile<true>::kResident)
         __syncthreads();
         if (threadIdx.x == 0) {
             if (n + 2 < tiles)
-                load(n & 1, row0 + 2 * kTileRows);
+                load(n & 1, row0 + 2 * T::kRows);
             if (a.act_by_col.q)
                 tma_store_2d(&maps.act_by_col, h_codes, static_cast<int>(row0), static_cast<int>(col_first));
             if (a.by_col.q)
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, Tile<true>::kResident)
     __syncthreads();
     if (threadIdx.x == 0) {
         if (a.by_row.q) {
-            tma_store_2d(&maps.by_row, row_codes, static_cast<int>(col_first), static_cast<int>(row_first) + (tiles - 1) * kTileRows);
+            tma_store_2d(&maps.by_row, row_codes, static_cast<int>(col_first), static_cast<int>(row_first) + (tiles - 1) * T::kRows);
             bulk_commit();
         }
         bulk_wait();
@@ -515,9 +515,9 @@ __global__ void __launch_bounds__(kThreads, Tile<true>::kResident)
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
 #pragma unroll
-        for (int m = 4; m < 32; m *= 2)
+        for (int m = 8; m < 32; m *= 2)
             total[k] += __shfl_xor_sync(0xffffffffu, total[k], m);
-        const int64_t col = col_first + 8 * warp + 2 * pair + k;
+        const int64_t col = col_first + 16 * warp + 2 * pair + k;
         if (group == 0 && col < a.cols)
             put_sum(a, strip, col, total[k]);
     }
@@ -557,11 +557,12 @@ __global__ void __launch_bounds__(1024) sum_partials_kernel(float *a, int64_t na
 void checkpoint_shape(CheckpointArgs &a, bool backward)
 {
     const int wide = backward ? Tile<true>::kCols : Tile<false>::kCols;
-    const int64_t down = (static_cast<int64_t>(a.rows) + kTileRows - 1) / kTileRows;
+    const int tall = backward ? Tile<true>::kRows : Tile<false>::kRows;
+    const int64_t down = (static_cast<int64_t>(a.rows) + tall - 1) / tall;
     a.across = (static_cast<int64_t>(a.cols) + wide - 1) / wide;
     // Tiles below one another in a block as long as that leaves several rounds of blocks.  16384 x 8192
     // in both forms with sums took 104 us with 4 of them, 106 with 2, 111 with 8, and 115 shared out among
-    // resident blocks beforehand; the backward pass of 8192 x 16384 241, 250, 240 and 242.
+    // resident blocks beforehand; the backward pass of 8192 x 16384 205 with 4, 220 with 2, 204 with 8.
     const int64_t resident = kSms * (backward ? Tile<true>::kResident : Tile<false>::kResident), tiles = down * a.across;
     a.steps = tiles >= 16 * resident ? 4 : tiles >= 4 * resident ? 2 : 1;
     a.strips = (down + a.steps - 1) / a.steps;
@@ -580,7 +581,7 @@ static cudaError_t start_backward(const CheckpointArgs &a, const BackwardMaps &m
     const cudaError_t e = opt_in<act_backward_kernel<ACT>>(kBytes);
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(act_backward_kernel<ACT>, dim3(static_cast<unsigned>(a.strips * a.across)), dim3(kThreads), kBytes, stream, a, maps);
+    return launch_dependent(act_backward_kernel<ACT>, dim3(static_cast<unsigned>(a.strips * a.across)), dim3(Tile<true>::kThreads), kBytes, stream, a, maps);
 }
 
 static cudaError_t finish_sums(const CheckpointArgs &a, cudaStream_t stream)
@@ -596,7 +597,7 @@ cudaError_t launch_checkpoint(CheckpointArgs &a, const CUtensorMap &mx, cudaStre
     constexpr int kBytes = Tile<false>::kBytes;
     cudaError_t e = opt_in<checkpoint_kernel>(kBytes);
     if (e == cudaSuccess)
-        e = launch_dependent(checkpoint_kernel, dim3(static_cast<unsigned>(a.strips * a.across)), dim3(kThreads), kBytes, stream, a, mx);
+        e = launch_dependent(checkpoint_kernel, dim3(static_cast<unsigned>(a.strips * a.across)), dim3(Tile<false>::kThreads), kBytes, stream, a, mx);
     return e == cudaSuccess ? finish_sums(a, stream) : e;
 }
 

@@ -47,9 +47,8 @@ struct CheckpointArgs {
 void checkpoint_shape(CheckpointArgs &a, bool backward);
 // x in boxes of 64 columns x 128 rows, 128-byte swizzle.
 cudaError_t launch_checkpoint(CheckpointArgs &a, const CUtensorMap &x, cudaStream_t stream);
-// The backward pass's arrays: x and z in boxes of 64 columns x 128 rows, 128- and 64-byte swizzle; the
-// codes along the rows like z, those along the columns in boxes of 128 rows' codes x 64 columns, 128-byte
-// swizzle (those of an output that is not wanted: zeros).
+// The backward pass's arrays, all in boxes of 64 x 64 with a 64-byte swizzle but x, whose is of 128
+// bytes (those of an output that is not wanted: zeros).
 struct BackwardMaps {
     CUtensorMap x, z, by_row, by_col, act_by_col;
 };

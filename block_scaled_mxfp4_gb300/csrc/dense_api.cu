@@ -88,14 +88,14 @@ int run_checkpoint(CheckpointArgs &a, bool backward, const void *workspace, size
     a.wait_limit = current_wait_limit();
     BackwardMaps m;
     std::memset(&m, 0, sizeof(m));
-    if (!encode(&m.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.rows, a.cols, a.ldx, 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode(&m.x, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.x, a.rows, a.cols, a.ldx, 2, 64, backward ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B))
         return MXFP4_ERR_CUDA;
     if (!backward)
         return status_of(launch_checkpoint(a, m.x, stream));
-    if (!encode(&m.z, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.z, a.rows, a.cols, a.ldz, 1, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode_codes(&m.by_row, a.by_row, a.rows, a.cols, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode_codes(&m.by_col, a.by_col, a.cols, a.rows, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !encode_codes(&m.act_by_col, a.act_by_col, a.cols, a.rows, 128, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!encode(&m.z, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.z, a.rows, a.cols, a.ldz, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_codes(&m.by_row, a.by_row, a.rows, a.cols, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_codes(&m.by_col, a.by_col, a.cols, a.rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode_codes(&m.act_by_col, a.act_by_col, a.cols, a.rows, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B))
         return MXFP4_ERR_CUDA;
     return status_of(launch_act_backward(a, m, stream));
 }
