@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(Tile<true>::kThreads, Tile<true>::kResident)
     auto load = [&](int stage, int64_t row0) {
         load_tile<true>(&maps.x, &maps.z, smem + stage * T::kStage, &full[stage], row0, col_first);
     };
-    // The scale of z in the tile's row threadIdx % 128, block threadIdx / 128.
+    // The scale of z in the tile's row threadIdx % 64, block threadIdx / 64.
     auto z_scale = [&](int64_t row0) -> uint32_t {
         const int64_t row = row0 + threadIdx.x % T::kRows, col0 = col_first + threadIdx.x / T::kRows * 32;
         return row < a.rows && col0 < a.cols ? a.sz[row * a.ld_sz + col0 / 32] : 127u;
