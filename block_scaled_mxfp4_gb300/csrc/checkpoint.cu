@@ -578,7 +578,7 @@ template <Act ACT>
 static cudaError_t start_backward(const CheckpointArgs &a, const BackwardMaps &maps, cudaStream_t stream)
 {
     constexpr int kBytes = Tile<true>::kBytes;
-    const cudaError_t e = opt_in<act_backward_kernel<ACT>>(kBytes);
+    const cudaError_t e = opt_in<act_backward_kernel<ACT>, kBytes>();
     if (e != cudaSuccess)
         return e;
     return launch_dependent(act_backward_kernel<ACT>, dim3(static_cast<unsigned>(a.strips * a.across)), dim3(Tile<true>::kThreads), kBytes, stream, a, maps);
@@ -595,7 +595,7 @@ cudaError_t launch_checkpoint(CheckpointArgs &a, const CUtensorMap &mx, cudaStre
     a.wide_q = wide(a.by_row.q, a.by_row.ldq);
     a.wide_qt = wide(a.by_col.q, a.by_col.ldq);
     constexpr int kBytes = Tile<false>::kBytes;
-    cudaError_t e = opt_in<checkpoint_kernel>(kBytes);
+    cudaError_t e = opt_in<checkpoint_kernel, kBytes>();
     if (e == cudaSuccess)
         e = launch_dependent(checkpoint_kernel, dim3(static_cast<unsigned>(a.strips * a.across)), dim3(Tile<false>::kThreads), kBytes, stream, a, mx);
     return e == cudaSuccess ? finish_sums(a, stream) : e;

@@ -697,7 +697,7 @@ template <int W, int E, int THREADS, int BLOCKS, int LOADERS>
 cudaError_t launch_ring_as(const CombineArgs &a, int sms, cudaStream_t stream)
 {
     constexpr auto kern = combine_ring_kernel<W, E / W, THREADS, BLOCKS, LOADERS>;
-    const cudaError_t e = opt_in<kern>(kRingBytes / BLOCKS);
+    const cudaError_t e = opt_in<kern, kRingBytes / BLOCKS>();
     if (e != cudaSuccess)
         return e;
     const int pitch = static_cast<int>(ring_pitch(a.N, W));

@@ -7,18 +7,20 @@
 
 namespace mxfp4 {
 
-// Let kernel `Kern` use up to `bytes` of dynamic shared memory, once per device.
-template <auto Kern>
-cudaError_t opt_in(int bytes)
+// Let kernel `Kern` use up to `Bytes` of dynamic shared memory, once per device.  `Bytes` is the most that
+// any of its launches asks for, and not a launch's own: host threads that come here at
+// once then all set the same limit, so that none takes another's away.
+template <auto Kern, int Bytes>
+cudaError_t opt_in()
 {
-    static std::atomic<int> done[64];
+    static std::atomic<bool> done[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed) >= bytes))
+    if (e != cudaSuccess || (dev < 64 && done[dev].load(std::memory_order_relaxed)))
         return e;
-    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Bytes);
     if (e == cudaSuccess && dev < 64)
-        done[dev].store(bytes, std::memory_order_relaxed);
+        done[dev].store(true, std::memory_order_relaxed);
     return e;
 }
 

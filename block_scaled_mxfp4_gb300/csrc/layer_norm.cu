@@ -938,7 +938,7 @@ __global__ void __launch_bounds__(256) norm_params_kernel(const __grid_constant_
 
 constexpr int kWarpRow = 1024;                   // longest row of one warp: 32 elements a lane
 constexpr int kStreamBlocks = 152;               // one to each SM of a GB300
-constexpr int kRingBytes = 216 << 10;            // of an SM
+constexpr int kRingBytes = 216 << 10;            // of an SM: the most dynamic shared memory of a streamed launch
 constexpr int kStreamLeast = 256;                // shorter rows are a warp's
 constexpr int kBlockRow = 16384;                 // longest row whose dw and db fit a block's registers
 
@@ -987,7 +987,7 @@ cudaError_t start_norm_width(const NormArgs &a, int sms, cudaStream_t stream)
     if (a.T > 2 * sms && stream_shape(a, false, sh)) {
         const int bytes = sh.depth * sh.rows * sh.slot + (a.N + 7) / 8 * 64;
         auto kernel = norm_stream_kernel<W == 8>;
-        const cudaError_t e = opt_in<norm_stream_kernel<W == 8>>(bytes);
+        const cudaError_t e = opt_in<norm_stream_kernel<W == 8>, kRingBytes>();
         if (e != cudaSuccess)
             return e;
         return launch_dependent(kernel, dim3(kStreamBlocks), dim3(kNormThreads), static_cast<size_t>(bytes), stream, a,
@@ -1028,7 +1028,7 @@ cudaError_t start_backward_width(NormArgs &a, cudaStream_t stream)
         const int ring = sh.depth * sh.rows * sh.arrays * sh.slot, joint = sh.rows * a.N * 4;
         const int bytes = ring > joint ? ring : joint;
         auto kernel = norm_backward_stream_kernel<W == 8>;
-        const cudaError_t e = opt_in<norm_backward_stream_kernel<W == 8>>(bytes);
+        const cudaError_t e = opt_in<norm_backward_stream_kernel<W == 8>, kRingBytes>();
         if (e != cudaSuccess)
             return e;
         return launch_dependent(kernel, dim3(static_cast<unsigned>(a.blocks)), dim3(kStreamThreads),

@@ -623,12 +623,12 @@ template <int THREADS, int BLOCKS, int LANES, int CH, bool BOUND>
 cudaError_t launch_pick(const RouteArgs &a, cudaStream_t stream)
 {
     constexpr auto kern = route_pick_kernel<THREADS, BLOCKS, LANES, CH, BOUND>;
-    auto bytes = [](int k, int E) {
+    constexpr auto bytes = [](int k, int E) {
         return THREADS * CH * 16 + THREADS / LANES * (k + (BOUND ? kCandidates<LANES> : 0)) * 8 +
                (kRunWords + 1) * E * 4 + kRouteRun * k * 4;
     };
     // The most that any E and k need of this instance.
-    const cudaError_t e = opt_in<kern>(bytes(BOUND ? 8 : kMaxTopK, LANES * CH * 4));
+    const cudaError_t e = opt_in<kern, bytes(BOUND ? 8 : kMaxTopK, LANES * CH * 4)>();
     if (e != cudaSuccess)
         return e;
     return launch_dependent(kern, dim3(a.blocks), dim3(THREADS), static_cast<size_t>(bytes(a.k, a.E)), stream, a);
@@ -703,7 +703,7 @@ cudaError_t launch_route(const RouteArgs &a, int sms, cudaStream_t stream)
         return picked;
     const int ep = (a.E + 7) / 8 * 8;
     const size_t smem = static_cast<size_t>(2 * place_at_once(ep) + 2) * ep * 4;
-    const cudaError_t e = opt_in<route_place_kernel>(kPlaceSmem);
+    const cudaError_t e = opt_in<route_place_kernel, kPlaceSmem>();
     if (e != cudaSuccess)
         return e;
     return launch_dependent(route_place_kernel, dim3(a.blocks), dim3(kRouteThreads), smem, stream, a);
