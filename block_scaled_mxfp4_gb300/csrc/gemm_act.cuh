@@ -42,6 +42,9 @@ __device__ __forceinline__ float act_bias(const ActGemmArgs &a, int n)
                        : bf16_bits_to_float(__ldg(static_cast<const uint16_t *>(a.bias) + n));
 }
 
+// What to add where there is no bias: x + -0 is x for every x, where x + 0 makes 0 of -0.
+constexpr float kNoBias = -0.0f;
+
 // bias[n0 .. n0 + 31], zeros past N.
 __device__ __forceinline__ void act_bias_chunk(const ActGemmArgs &a, int n0, float (&b)[32])
 {
@@ -322,7 +325,7 @@ __device__ __forceinline__ void act_col_chunk(const ActGemmArgs &a, int m0, int 
 {
     const int mcount = min(COUNT, a.M - m0);
     const bool real = n < a.N, in = n - (n & 31) < a.N;
-    const float b = real && a.bias ? act_bias(a, n) : 0.0f;
+    const float b = a.bias ? (real ? act_bias(a, n) : 0.0f) : kNoBias;
     uint16_t r[COUNT];
 #pragma unroll
     for (int i = 0; i < COUNT; ++i)                      // before any store: R may alias D
@@ -465,7 +468,7 @@ __device__ __forceinline__ void act_reduce_cluster(const ActGemmArgs &a, uint32_
                 sum4(row, ch, x);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                x[j] = j < cnt ? fmaf(a.alpha, x[j], a.bias ? act_bias(a, n + j) : 0.0f) : 0.0f;
+                x[j] = j < cnt ? fmaf(a.alpha, x[j], a.bias ? act_bias(a, n + j) : kNoBias) : 0.0f;
             if (a.Z.q)
                 act_put_four(a.Z, m, n, in, x);
             act_apply(a.act, x);
