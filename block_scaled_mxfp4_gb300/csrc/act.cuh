@@ -92,7 +92,9 @@ __device__ __forceinline__ void act_and_slope2(F2 z, F2 &h, F2 &slope)
         const F2 zz = z * z;
         const F2 g = sigmoid2(z * fma2(f2(0.10294324f), zz, f2(2.3022082f)));
         h = z * g;
-        slope = fma2(h * fma2(g, f2(-1.0f), f2(1.0f)), fma2(f2(0.214064449f), zz, f2(1.59576912f)), g);
+        // The slope's factor stays finite where z^2 does not: h (1 - g) is 0 long before, and 0 times infinity is NaN.
+        const float2 p = parts(zz);
+        slope = fma2(h * fma2(g, f2(-1.0f), f2(1.0f)), fma2(f2(0.214064449f), f2(fminf(p.x, 1e30f), fminf(p.y, 1e30f)), f2(1.59576912f)), g);
     } else if constexpr (A == Act::kSilu) {
         const F2 g = sigmoid2(f2(1.44269504f) * z);
         h = z * g;

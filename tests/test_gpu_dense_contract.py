@@ -1,8 +1,11 @@
 """What the header says of the dense layer's operators at the far ends of their arguments."""
+import numpy as np
 import pytest
 
 import block_scaled_mxfp4_gb300 as mx
-from test_gpu_dense import Product, workspace
+import dense_ref as dr
+import expert_ref as ref
+from test_gpu_dense import Product, bf16, dev, host, run_backward, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +49,31 @@ def test_product_without_epilogue_has_the_gemms_zeros(form, M, N, K, split):
         torch.cuda.synchronize()
         assert (want == 0).any()
         assert torch.equal(got.view(torch.int16), want.view(torch.int16)), alpha
+
+
+@pytest.mark.parametrize("act", dr.ACTS)
+@pytest.mark.parametrize("fmt_z", ["e4m3", "e5m2"])
+def test_slopes_of_large_z(fmt_z, act):
+    """z from 2^13 up to the largest fp32 numbers, which 8 bits with a scale hold: there every slope is 1 above
+    zero, and 0 below (1 with no activation), to far more digits than fp32 has, and so dz is dh or 0."""
+    emax, mantissas = {"e4m3": (8, 7), "e5m2": (15, 4)}[fmt_z]
+    scales = np.arange(127 + 13 - emax, 255 - emax)          # of z from 2^13 to under 2^128
+    rows, cols = len(scales), 96
+    rng = np.random.default_rng(8)
+    codes = 0x78 + rng.integers(0, mantissas, size=(rows, cols)) + 0x80 * rng.integers(0, 2, size=(rows, cols))
+    codes[:, 5:9] = 0                                        # and zeros among them
+    codes, s = codes.astype(np.uint8), np.repeat(scales[:, None], 3, axis=1).astype(np.uint8)
+    z = ref.values(codes, s, fmt_z)
+    assert np.abs(z).max() < 2.0 ** 128 and (np.abs(z[z != 0]) >= 2.0 ** 13).all()
+    dh, g = bf16(rng.normal(size=(rows, cols)))
+    dZ, Q, S, QT, ST, HT, SHT, db = map(host, run_backward(dh, dev(codes), dev(s), fmt_z, act, cols))
+    one, zero = 1.0, (1.0 if act == "none" else 0.0)
+    slope = np.where(z == 0, {"none": 1.0, "relu": 0.0}.get(act, 0.5), np.where(z > 0, one, zero))
+    h, v = z if act == "none" else np.maximum(z, 0), g * slope
+    e = np.where(z == 0, 2.0 ** -19 * np.abs(g), 0.0)        # exp, 1 / x and the polynomial, at 0
+    dr.check_bf16(dZ, v, e, "dZ")
+    dr.check_codes(Q, S, v, e, "e4m3", "rows")
+    dr.check_codes(QT, ST, v.T.copy(), e.T.copy(), "e4m3", "columns")
+    dr.check_codes(HT, SHT, h.T.copy(), 0, "e4m3", "h")
+    # (chains of fp32 additions: a lane's rows, then lanes, warps and strips)
+    assert (np.abs(db - v.sum(0)) <= (rows / 32 + 64) * dr.EPS24 * np.abs(v).sum(0) + e.sum(0)).all()
