@@ -628,7 +628,9 @@ size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F);
  * polynomial of this library's own with a relative error of 5e-7 in the lower
  * tail.  Relative to an activation's value its error stays within 2^-19 + |u| 2^-21,
  * u the exponential's argument (z^2 / 2 for GELU, sqrt(8 / pi) (z + 0.044715 z^3) for
- * its tanh form, z for SiLU); a value under the smallest normal number may be 0.
+ * its tanh form, z for SiLU); a value under the smallest normal number may be 0, and so
+ * may one of SiLU or of GELU's tanh form whose sigmoid is under 2^-125: a value of up to
+ * |z| 2^-125 (SiLU of -88 is -5.3e-37, and -0 here).
  * In a product's epilogue z = infinity gives infinity, and minus infinity 0 (ReLU, GELU)
  * or NaN (its tanh form, SiLU).
  * ------------------------------------------------------------------------ */

@@ -77,3 +77,31 @@ def test_slopes_of_large_z(fmt_z, act):
     dr.check_codes(HT, SHT, h.T.copy(), 0, "e4m3", "h")
     # (chains of fp32 additions: a lane's rows, then lanes, warps and strips)
     assert (np.abs(db - v.sum(0)) <= (rows / 32 + 64) * dr.EPS24 * np.abs(v).sum(0) + e.sum(0)).all()
+
+
+@pytest.mark.parametrize("act,lo,hi", [("silu", -130.0, 20.0), ("gelu_tanh", -14.0, 6.0), ("gelu", -15.0, 6.0), ("relu", -3.0, 3.0)])
+def test_activations_down_to_the_smallest_numbers(act, lo, hi):
+    """Every activation within the header's bound of its value, with nothing but what the header allows
+    for small ones: 0 under the smallest normal number, or for SiLU and GELU's tanh form where the
+    sigmoid is under 2^-125.  z is the bias: the product's sums are 0."""
+    N = 1 << 15
+    p = Product("mxfp8", 2, N, 32, 12)
+    p.dA.zero_()
+    z = np.linspace(lo, hi, N).astype(np.float32)
+    D = host(p.run(act, dev(z), "fp32")[0])
+    z = z.astype(np.float64)
+    if act == "silu":
+        u = z
+    elif act == "gelu_tanh":
+        u = np.sqrt(8 / np.pi) * (z + 0.044715 * z ** 3)
+    else:
+        u = z * z / 2 if act == "gelu" else 0.0 * z
+    if act in ("silu", "gelu_tanh"):
+        g = np.exp(u - np.logaddexp(0, u))
+        h, zero = z * g, np.where(g < 2.0 ** -125, np.abs(z) * g, 0.0)
+    else:
+        h = dr.act(z, act)[0]
+        zero = np.where(np.abs(h) < 2.0 ** -126, np.abs(h), 0.0)
+    e = np.abs(h) * (2.0 ** -19 + np.abs(u) * 2.0 ** -21) if act != "relu" else 0.0
+    for row in D:
+        dr.check_bf16(row, h, np.maximum(e, zero), act)
