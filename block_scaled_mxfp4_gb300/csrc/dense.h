@@ -78,7 +78,9 @@ struct NormArgs {
     float *partials;            // backward: [blocks][2][N]
     int blocks;                 // backward: blocks that share the rows (at most, until it is launched)
     int T, N;
-    int width;                  // elements of the widest access that every row allows: 8, 4, 2, 1
+    int width;                  // elements of the widest access that every row allows (forward: and every
+                                // parameter): 8, 4, 2, 1
+    int single_w;               // backward: w does not allow accesses of that many
     long long wait_limit;
 };
 cudaError_t launch_layer_norm(const NormArgs &a, int sms, cudaStream_t stream);

@@ -320,9 +320,12 @@ int mxfp4_layer_norm_backward(void *dX, int64_t lddx, float *dw, float *db, cons
     allow_rows(a.width, dY, T > 1 ? lddy : 0);
     allow_rows(a.width, dX, T > 1 ? lddx : 0);
     allow_rows(a.width, dres, T > 1 ? ldr : 0);
-    allow_param(a.width, w, a.fp32 != 0);
     while (N % a.width != 0)
         a.width /= 2;
+    // (w changes how it is read, and not the order of the sums)
+    int width = a.width;
+    allow_param(width, w, a.fp32 != 0);
+    a.single_w = width < a.width ? 1 : 0;
     return status_of(launch_layer_norm_backward(a, s));
 }
 

@@ -87,10 +87,20 @@ __device__ __forceinline__ void store_unit(uint16_t *p, const float (&x)[W])
     }
 }
 
-// W parameters from element n on, `missing` where there is no array.
-template <int W>
+// W parameters from element n on, `missing` where there is no array.  SINGLE: the array does not allow
+// accesses of W elements.
+template <int W, bool SINGLE = false>
 __device__ __forceinline__ void load_param(const void *p, int fp32, int n, float missing, float (&x)[W])
 {
+    if constexpr (SINGLE) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            float one[1];
+            load_param<1>(p, fp32, n + i, missing, one);
+            x[i] = one[0];
+        }
+        return;
+    }
     if (!p) {
 #pragma unroll
         for (int i = 0; i < W; ++i)
@@ -216,7 +226,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : 1024) norm_kernel(cons
 // all in fp32; dx is rounded once.  x and dy are read once: a block takes rows
 // gridDim apart, keeps its share of dw and db in registers and leaves it in
 // partials, which a second kernel adds in a fixed order.
-template <int W, int EPT, bool WARP, bool PARAMS>
+template <int W, int EPT, bool WARP, bool PARAMS, bool SINGLE>
 __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : PARAMS ? 512 : 1024) norm_backward_kernel(const __grid_constant__ NormArgs a)
 {
     constexpr int VPT = EPT / W;
@@ -252,7 +262,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : PARAMS ? 512 : 1024) n
             const int n = (v * tpr + at) * W;
             if (n < a.N) {
                 float w[W];
-                load_param<W>(a.w, a.fp32, n, 1.0f, w);
+                load_param<W, SINGLE>(a.w, a.fp32, n, 1.0f, w);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     const float xhat = (pick<W>(x[v], i) - mean) * rstd, d = pick<W>(dy[v], i), g = d * w[i];
@@ -273,7 +283,7 @@ __global__ void __launch_bounds__(WARP ? kRowWarps * 32 : PARAMS ? 512 : 1024) n
             const int n = (v * tpr + at) * W;
             if (n < a.N) {
                 float w[W], y[W];
-                load_param<W>(a.w, a.fp32, n, 1.0f, w);
+                load_param<W, SINGLE>(a.w, a.fp32, n, 1.0f, w);
 #pragma unroll
                 for (int i = 0; i < W; ++i) {
                     const float xhat = (pick<W>(x[v], i) - mean) * rstd;
@@ -1011,8 +1021,15 @@ template <int W, int EPT, bool WARP, bool PARAMS>
 cudaError_t start_backward(const NormArgs &a, cudaStream_t stream)
 {
     const int threads = WARP ? kRowWarps * 32 : threads_for(a.N, EPT);
-    return launch_dependent(norm_backward_kernel<W, EPT, WARP, PARAMS>, dim3(static_cast<unsigned>(a.blocks)),
-                            dim3(static_cast<unsigned>(threads)), 0, stream, a);
+    // (a kernel of its own for each way to read w: both in one take up to 38 registers more, and from the
+    // blocks of an SM)
+    auto start = [&](auto kernel) {
+        return launch_dependent(kernel, dim3(static_cast<unsigned>(a.blocks)), dim3(static_cast<unsigned>(threads)), 0, stream, a);
+    };
+    if constexpr (W > 1)
+        if (a.single_w)
+            return start(norm_backward_kernel<W, EPT, WARP, PARAMS, true>);
+    return start(norm_backward_kernel<W, EPT, WARP, PARAMS, false>);
 }
 
 template <int W>

@@ -5,7 +5,7 @@ import pytest
 import block_scaled_mxfp4_gb300 as mx
 import dense_ref as dr
 import expert_ref as ref
-from test_gpu_dense import Product, bf16, dev, host, run_backward, workspace
+from test_gpu_dense import KIND, Product, bf16, dev, host, run_backward, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +105,25 @@ def test_activations_down_to_the_smallest_numbers(act, lo, hi):
     e = np.abs(h) * (2.0 ** -19 + np.abs(u) * 2.0 ** -21) if act != "relu" else 0.0
     for row in D:
         dr.check_bf16(row, h, np.maximum(e, zero), act)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp32"])
+@pytest.mark.parametrize("T,N", [(5, 200), (300, 200), (20, 512), (76, 1024), (77, 1024), (300, 1024), (1300, 1024), (20, 2048), (300, 2048), (3000, 1024),
+                                 (40, 4096), (100, 4104), (700, 9000), (400, 17000), (33, 1022), (33, 1001)])
+def test_order_of_a_norm_gradients_sums(T, N, kind):
+    """Sizes and the rows' alignment decide it, not the weight's."""
+    x, dy = (torch.randn((T, N), device="cuda").bfloat16() for _ in range(2))
+    m, r = x.float().mean(1), 1 + torch.rand(T, device="cuda")
+    base = torch.randn(N, device="cuda").to(torch.bfloat16 if kind == "bf16" else torch.float32)
+    ws = workspace(mx.mxfp4_layer_norm_workspace_size(T, N))
+    outs = []
+    for off in (0, 1, 2, 4):
+        w = torch.zeros(N + 8, dtype=base.dtype, device="cuda")
+        w[off:off + N] = base
+        dx, dw, db = torch.empty_like(x), torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+        mx.mxfp4_layer_norm_backward(dx, N, dw, db, dy, N, x, N, m, r, w[off:off + N], KIND[kind], None, 0, T, N, ws, ws.numel())
+        outs.append((dx, dw, db))
+    torch.cuda.synchronize()
+    for one in outs[1:]:
+        for a, b in zip(outs[0], one):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
