@@ -220,15 +220,29 @@ def dense_block_backward(dout, kept, w1t, s1t, w2t, s2t, fmt_grad=mx.MXFP8_E4M3,
     """
     import torch
     where = "dense_block_backward"
+    _check_rows(where, "kept.x", kept.x, None)
     T, K = kept.x.shape
+    if kept.z.dim() != 2:
+        mx._refuse(f"{where}: kept.z of two dimensions")
     F = kept.z.shape[1]
+    if K % 32 or F % 32 or not K or not F:
+        mx._refuse(f"{where}: K and F multiples of 32")
+    T32 = _up32(T)
+    for name, shape in (("yt", (K, T32)), ("syt", (K, T32 // 32)), ("z", (T, F)), ("sz", (T, F // 32))):
+        _check_bytes(where, "kept." + name, getattr(kept, name), shape)
+    for name in ("mean", "rstd"):
+        t = getattr(kept, name)
+        if t.dtype != torch.float32:
+            mx._refuse(f"{where}: kept.{name} of type torch.float32", TypeError)
+        if tuple(t.shape) != (T,) or not t.is_contiguous():
+            mx._refuse(f"{where}: kept.{name} contiguous, of shape ({T},)")
     _check_rows(where, "dout", dout, (T, K), aligned=True)
     for name, t, shape in (("w1t", w1t, (K, F)), ("w2t", w2t, (F, K)), ("s1t", s1t, (K, F // 32)),
                            ("s2t", s2t, (F, K // 32))):
         _check_bytes(where, name, t, shape)
     _check_codes(where, kept.act, kept.fmt, fmt_grad)
     x, norm_w, mean, rstd, yt, syt, z, sz, act, fmt = kept
-    norm = _check_params(where, [("norm_w", norm_w, K)])
+    norm = _check_params(where, [("kept.norm_w", norm_w, K)])
     inputs = [dout, w1t, s1t, w2t, s2t, *kept[:8]]
     _check_place(where, *inputs)
     made = []
@@ -241,7 +255,6 @@ def dense_block_backward(dout, kept, w1t, s1t, w2t, s2t, fmt_grad=mx.MXFP8_E4M3,
         g = DenseGrads(bf16(T, K), bf16(F, K), bf16(K, F), f32(F), f32(K), f32(K), f32(K))
         made += g
         if T:
-            T32 = _up32(T)
             size = mx.mxfp8_gemm_workspace_size
             need = max(size(T, F, K, 0), size(T, K, F, 0), size(K, F, T32, 0), size(F, K, T32, 0),
                        mx.mxfp8_checkpoint_workspace_size(T, K), mx.mxfp8_checkpoint_workspace_size(T, F),

@@ -121,3 +121,31 @@ def test_forms_arguments():
         assert "GPU" not in str(e.value)
     with pytest.raises(ValueError, match="at least one form"):
         mx.mxfp8_forms(bf16(3, 8), rows=False, columns=False)
+
+
+KEPT = [("x", lambda t: t.float(), TypeError), ("x", lambda t: t[0], ValueError), ("x", apart, ValueError), ("x", lambda t: t[:9], ValueError),
+        ("x", lambda t: bf16(T, K + 32), ValueError), ("x", lambda t: bf16(T, 48), ValueError), ("x", lambda t: bf16(T, 0), ValueError),
+        ("norm_w", lambda t: t[:63], ValueError), ("norm_w", lambda t: t.double(), TypeError),
+        ("mean", lambda t: t[:9], ValueError), ("mean", lambda t: t.bfloat16(), TypeError), ("mean", apart, ValueError),
+        ("rstd", lambda t: t[:, None], ValueError), ("rstd", lambda t: t.double(), TypeError), ("rstd", lambda t: t[:0], ValueError),
+        ("yt", lambda t: t[:, :16], ValueError), ("yt", lambda t: t[:63], ValueError), ("yt", lambda t: t.to(torch.int16), TypeError),
+        ("yt", lambda t: t.t(), ValueError), ("syt", lambda t: t[:1], ValueError), ("syt", apart, ValueError),
+        ("z", lambda t: t[:9], ValueError), ("z", lambda t: t[0], ValueError), ("z", lambda t: t[:, :64], ValueError),
+        ("z", lambda t: t[:, :95], ValueError), ("z", lambda t: t.float(), TypeError), ("z", lambda t: t[:, :0], ValueError),
+        ("sz", lambda t: t[:, :2], ValueError), ("sz", lambda t: t[:9], ValueError), ("sz", lambda t: t.int(), TypeError)]
+
+
+@pytest.mark.parametrize("name,change,kind", KEPT)
+def test_what_the_forward_pass_kept(name, change, kind):
+    """The kernels take each array's size from the others': one that is too short would be read past its end."""
+    args = backward_args()
+    args["kept"] = args["kept"]._replace(**{name: change(getattr(args["kept"], name))})
+    got, text = refusal(mx.dense_block_backward, args)
+    assert got is kind and HERE not in text and text.startswith("dense_block_backward: ")
+
+
+def test_what_the_forward_pass_kept_with_other_codes():
+    for field, bad in (("act", -1), ("act", 5), ("fmt", 2), ("fmt", mx.MXFP4_E2M1_PADDED)):
+        args = backward_args()
+        args["kept"] = args["kept"]._replace(**{field: bad})
+        assert HERE not in refusal(mx.dense_block_backward, args)[1]
