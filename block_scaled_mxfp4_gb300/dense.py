@@ -12,6 +12,9 @@ from typing import NamedTuple, Optional
 
 import block_scaled_mxfp4_gb300 as mx
 
+# The types that the codes and scales of a form stand for.
+_CODES = {mx.MXFP8_E4M3: "torch.float8_e4m3fn", mx.MXFP8_E5M2: "torch.float8_e5m2"}
+_PACKED, _SCALES = "torch.float4_e2m1fn_x2", "torch.float8_e8m0fnu"
 _PARAMS = {"torch.bfloat16": mx.MXFP4_PARAM_BF16, "torch.float32": mx.MXFP4_PARAM_FP32}
 
 
@@ -73,9 +76,10 @@ def _check_rows(where, name, t, shape, aligned=False):
         mx._refuse(f"{where}: {name} of 16-byte aligned rows")
 
 
-def _check_bytes(where, name, t, shape):
-    if t.element_size() != 1:
-        mx._refuse(f"{where}: {name} of bytes", TypeError)
+def _check_bytes(where, name, t, shape, means):
+    """`means`: the type of 8 or 4 bits whose codes these are; other such types are refused, bytes are not."""
+    if t.element_size() != 1 or t.dtype.is_floating_point and str(t.dtype) != means:
+        mx._refuse(f"{where}: {name} of bytes or type {means}", TypeError)
     if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         mx._refuse(f"{where}: {name} contiguous, of shape {tuple(shape)}")
 
@@ -143,6 +147,8 @@ def dense_block(x, w1, s1, w2, s2, b1=None, b2=None, norm_w=None, norm_b=None, a
     x bf16 [T, K].  MXFP4: w1 uint8 [F, K / 2], w2 uint8 [K, F / 2] as
     mxfp4_quantize writes them; MXFP8 (codes of `fmt`): w1 [F, K], w2 [K, F] as in
     mxfp8_forms; s1 [F, K / 32], s2 [K, F / 32] either way, K and F multiples of 32.
+    Codes and scales are bytes, or of torch's own types for them (float8_e4m3fn for
+    MXFP8_E4M3 and so on; another format's are refused).
     What the products read is quantised in the weights' form.  b1 [F] and b2 [K],
     norm_w and norm_b [K]: bf16 or fp32, each pair of one type, None for none.
 
@@ -160,13 +166,13 @@ def dense_block(x, w1, s1, w2, s2, b1=None, b2=None, norm_w=None, norm_b=None, a
     F, packed = w1.shape[0], w1.shape[1] * 2 == K
     if K % 32 or F % 32 or not K or not F:
         mx._refuse(f"{where}: K and F multiples of 32")
-    per = 2 if packed else 1
-    for name, t, shape in (("w1", w1, (F, K // per)), ("w2", w2, (K, F // per)), ("s1", s1, (F, K // 32)),
-                           ("s2", s2, (K, F // 32))):
-        _check_bytes(where, name, t, shape)
+    _check_codes(where, act, fmt)
+    per, codes = (2, _PACKED) if packed else (1, _CODES[fmt])
+    for name, t, shape, means in (("w1", w1, (F, K // per), codes), ("w2", w2, (K, F // per), codes),
+                                  ("s1", s1, (F, K // 32), _SCALES), ("s2", s2, (K, F // 32), _SCALES)):
+        _check_bytes(where, name, t, shape, means)
     bias1, bias2 = _check_params(where, [("b1", b1, F)]), _check_params(where, [("b2", b2, K)])
     norm = _check_params(where, [("norm_w", norm_w, K), ("norm_b", norm_b, K)])
-    _check_codes(where, act, fmt)
     if keep and packed:
         mx._refuse(f"{where}: MXFP8 weights with keep=True")
     inputs = [x, w1, s1, w2, s2, b1, b2, norm_w, norm_b]
@@ -228,8 +234,11 @@ def dense_block_backward(dout, kept, w1t, s1t, w2t, s2t, fmt_grad=mx.MXFP8_E4M3,
     if K % 32 or F % 32 or not K or not F:
         mx._refuse(f"{where}: K and F multiples of 32")
     T32 = _up32(T)
-    for name, shape in (("yt", (K, T32)), ("syt", (K, T32 // 32)), ("z", (T, F)), ("sz", (T, F // 32))):
-        _check_bytes(where, "kept." + name, getattr(kept, name), shape)
+    _check_codes(where, kept.act, kept.fmt, fmt_grad)
+    codes = _CODES[kept.fmt]
+    for name, shape, means in (("yt", (K, T32), codes), ("syt", (K, T32 // 32), _SCALES), ("z", (T, F), codes),
+                               ("sz", (T, F // 32), _SCALES)):
+        _check_bytes(where, "kept." + name, getattr(kept, name), shape, means)
     for name in ("mean", "rstd"):
         t = getattr(kept, name)
         if t.dtype != torch.float32:
@@ -237,10 +246,9 @@ def dense_block_backward(dout, kept, w1t, s1t, w2t, s2t, fmt_grad=mx.MXFP8_E4M3,
         if tuple(t.shape) != (T,) or not t.is_contiguous():
             mx._refuse(f"{where}: kept.{name} contiguous, of shape ({T},)")
     _check_rows(where, "dout", dout, (T, K), aligned=True)
-    for name, t, shape in (("w1t", w1t, (K, F)), ("w2t", w2t, (F, K)), ("s1t", s1t, (K, F // 32)),
-                           ("s2t", s2t, (F, K // 32))):
-        _check_bytes(where, name, t, shape)
-    _check_codes(where, kept.act, kept.fmt, fmt_grad)
+    for name, t, shape, means in (("w1t", w1t, (K, F), codes), ("w2t", w2t, (F, K), codes), ("s1t", s1t, (K, F // 32), _SCALES),
+                                  ("s2t", s2t, (F, K // 32), _SCALES)):
+        _check_bytes(where, name, t, shape, means)
     x, norm_w, mean, rstd, yt, syt, z, sz, act, fmt = kept
     norm = _check_params(where, [("kept.norm_w", norm_w, K)])
     inputs = [dout, w1t, s1t, w2t, s2t, *kept[:8]]

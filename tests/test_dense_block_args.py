@@ -149,3 +149,41 @@ def test_what_the_forward_pass_kept_with_other_codes():
         args = backward_args()
         args["kept"] = args["kept"]._replace(**{field: bad})
         assert HERE not in refusal(mx.dense_block_backward, args)[1]
+
+
+E4M3, E5M2, E8M0 = torch.float8_e4m3fn, torch.float8_e5m2, torch.float8_e8m0fnu
+
+
+@pytest.mark.parametrize("fmt,right,wrong", [(mx.MXFP8_E4M3, E4M3, E5M2), (mx.MXFP8_E5M2, E5M2, E4M3)])
+def test_codes_of_a_type_are_those_of_the_format(fmt, right, wrong):
+    """Weights that say what their codes are: read as the other format's they would give other numbers."""
+    args = dict(forward_args(), fmt=fmt)
+    for name in ("w1", "w2"):
+        assert refusal(mx.dense_block, dict(args), **{name: lambda t: t.view(right)})[1] == "dense_block: " + HERE
+        for bad in (wrong, E8M0, torch.float8_e4m3fnuz):
+            kind, text = refusal(mx.dense_block, dict(args), **{name: lambda t: t.view(bad)})
+            assert kind is TypeError and name in text
+    for name in ("s1", "s2"):
+        assert refusal(mx.dense_block, dict(args), **{name: lambda t: t.view(E8M0)})[1] == "dense_block: " + HERE
+        for bad in (E4M3, E5M2):
+            kind, text = refusal(mx.dense_block, dict(args), **{name: lambda t: t.view(bad)})
+            assert kind is TypeError and name in text
+    args = dict(backward_args())
+    args["kept"] = args["kept"]._replace(fmt=fmt)
+    for name in ("w1t", "w2t"):
+        assert refusal(mx.dense_block_backward, dict(args), **{name: lambda t: t.view(right)})[1] == "dense_block_backward: " + HERE
+        kind, text = refusal(mx.dense_block_backward, dict(args), **{name: lambda t: t.view(wrong)})
+        assert kind is TypeError and name in text
+    for name, good, bad in (("yt", right, wrong), ("z", right, wrong), ("syt", E8M0, right), ("sz", E8M0, right)):
+        put = lambda to: dict(args, kept=args["kept"]._replace(**{name: getattr(args["kept"], name).view(to)}))
+        assert refusal(mx.dense_block_backward, put(good))[1] == "dense_block_backward: " + HERE
+        kind, text = refusal(mx.dense_block_backward, put(bad))
+        assert kind is TypeError and "kept." + name in text
+
+
+def test_packed_codes_of_a_type():
+    for name in ("w1", "w2"):
+        assert refusal(mx.dense_block, forward_args(packed=True), **{name: lambda t: t.view(torch.float4_e2m1fn_x2)})[1] == "dense_block: " + HERE
+        for bad in (E4M3, E5M2, E8M0):
+            kind, text = refusal(mx.dense_block, forward_args(packed=True), **{name: lambda t: t.view(bad)})
+            assert kind is TypeError and name in text
