@@ -15,6 +15,7 @@ import block_scaled_mxfp4_gb300 as mx
 # The types that the codes and scales of a form stand for.
 _CODES = {mx.MXFP8_E4M3: "torch.float8_e4m3fn", mx.MXFP8_E5M2: "torch.float8_e5m2"}
 _PACKED, _SCALES = "torch.float4_e2m1fn_x2", "torch.float8_e8m0fnu"
+_MAX_NORM = 32768                                        # the layer norm's longest row
 _PARAMS = {"torch.bfloat16": mx.MXFP4_PARAM_BF16, "torch.float32": mx.MXFP4_PARAM_FP32}
 
 
@@ -146,7 +147,7 @@ def dense_block(x, w1, s1, w2, s2, b1=None, b2=None, norm_w=None, norm_b=None, a
 
     x bf16 [T, K].  MXFP4: w1 uint8 [F, K / 2], w2 uint8 [K, F / 2] as
     mxfp4_quantize writes them; MXFP8 (codes of `fmt`): w1 [F, K], w2 [K, F] as in
-    mxfp8_forms; s1 [F, K / 32], s2 [K, F / 32] either way, K and F multiples of 32.
+    mxfp8_forms; s1 [F, K / 32], s2 [K, F / 32] either way, K and F multiples of 32, K up to 32768.
     Codes and scales are bytes, or of torch's own types for them (float8_e4m3fn for
     MXFP8_E4M3 and so on; another format's are refused).
     What the products read is quantised in the weights' form.  b1 [F] and b2 [K],
@@ -166,6 +167,10 @@ def dense_block(x, w1, s1, w2, s2, b1=None, b2=None, norm_w=None, norm_b=None, a
     F, packed = w1.shape[0], w1.shape[1] * 2 == K
     if K % 32 or F % 32 or not K or not F:
         mx._refuse(f"{where}: K and F multiples of 32")
+    if K > _MAX_NORM:
+        mx._refuse(f"{where}: K of at most {_MAX_NORM}")
+    if not eps >= 0:
+        mx._refuse(f"{where}: eps of at least 0")
     _check_codes(where, act, fmt)
     per, codes = (2, _PACKED) if packed else (1, _CODES[fmt])
     for name, t, shape, means in (("w1", w1, (F, K // per), codes), ("w2", w2, (K, F // per), codes),
@@ -233,6 +238,8 @@ def dense_block_backward(dout, kept, w1t, s1t, w2t, s2t, fmt_grad=mx.MXFP8_E4M3,
     F = kept.z.shape[1]
     if K % 32 or F % 32 or not K or not F:
         mx._refuse(f"{where}: K and F multiples of 32")
+    if K > _MAX_NORM:
+        mx._refuse(f"{where}: K of at most {_MAX_NORM}")
     T32 = _up32(T)
     _check_codes(where, kept.act, kept.fmt, fmt_grad)
     codes = _CODES[kept.fmt]

@@ -187,3 +187,19 @@ def test_packed_codes_of_a_type():
         for bad in (E4M3, E5M2, E8M0):
             kind, text = refusal(mx.dense_block, forward_args(packed=True), **{name: lambda t: t.view(bad)})
             assert kind is TypeError and name in text
+
+
+def test_rows_longer_than_the_norms():
+    for K_, text in ((32768, HERE), (32800, "K of at most 32768 expected")):
+        args = dict(forward_args(), x=bf16(2, K_), w1=u8(32, K_), s1=u8(32, K_ // 32), w2=u8(K_, 32), s2=u8(K_, 1), b1=None, b2=None,
+                    norm_w=None, norm_b=None)
+        assert refusal(mx.dense_block, args) == (ValueError, "dense_block: " + text)
+        kept = mx.DenseKept(bf16(2, K_), None, torch.zeros(2), torch.zeros(2), u8(K_, 32), u8(K_, 1), u8(2, 32), u8(2, 1), 0, 0)
+        args = dict(dout=bf16(2, K_), kept=kept, w1t=u8(K_, 32), s1t=u8(K_, 1), w2t=u8(32, K_), s2t=u8(32, K_ // 32))
+        assert refusal(mx.dense_block_backward, args) == (ValueError, "dense_block_backward: " + text)
+
+
+def test_eps():
+    assert refusal(mx.dense_block, forward_args(), eps=0)[1] == "dense_block: " + HERE
+    for bad in (-1e-9, float("nan")):
+        assert refusal(mx.dense_block, forward_args(), eps=bad) == (ValueError, "dense_block: eps of at least 0 expected")
