@@ -488,6 +488,13 @@ __global__ void __launch_bounds__(Tile<true>::kThreads, Tile<true>::kResident)
                 v[4 * i + 2] = p.z;
                 v[4 * i + 3] = p.w;
             }
+            if (col0 + 32 > a.cols) {
+                // Behind the last column z is 0 times the block's scale: NaN where that is.
+#pragma unroll
+                for (int i = 1; i < 32; ++i)
+                    if (col0 + i >= a.cols)
+                        v[i] = 0.0f;
+            }
             if (a.dz)
                 put_dz(a, row, col0, v);
             if (a.by_row.q) {
