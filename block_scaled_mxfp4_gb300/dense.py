@@ -108,9 +108,17 @@ def _check_codes(where, act, *fmts):
         mx._refuse(f"{where}: formats MXFP8_E4M3 or MXFP8_E5M2")
 
 
-def _check_place(where, x, *others):
+def _check_place(where, stream, x, *others):
+    """One GPU, and the one that the kernels are launched on: that of a stream other than the current one
+    (as _on_stream takes it), or else the current one."""
+    import torch
     if not x.is_cuda or any(t is not None and t.device != x.device for t in others):
         mx._refuse(f"{where}: everything on one GPU")
+    device = torch.cuda.current_device()
+    if isinstance(stream, torch.cuda.Stream) and stream.cuda_stream != torch.cuda.current_stream().cuda_stream:
+        device = stream.device.index
+    if x.device.index != device:
+        mx._refuse(f"{where}: tensors on the device of the current stream, or of the one given,")
 
 
 def mxfp8_forms(x, fmt=mx.MXFP8_E4M3, rows=True, columns=True, sums=False, stream=None) -> Mxfp8Forms:
@@ -126,7 +134,7 @@ def mxfp8_forms(x, fmt=mx.MXFP8_E4M3, rows=True, columns=True, sums=False, strea
         mx._refuse(f"{where}: x of at least one element")
     if not (rows or columns or sums):
         mx._refuse(f"{where}: at least one form")
-    _check_place(where, x)
+    _check_place(where, stream, x)
     made = []
     with mx._on_stream(stream, [x], made):
         u8 = lambda want, *shape: torch.empty(shape, dtype=torch.uint8, device=x.device) if want else None
@@ -181,7 +189,7 @@ def dense_block(x, w1, s1, w2, s2, b1=None, b2=None, norm_w=None, norm_b=None, a
     if keep and packed:
         mx._refuse(f"{where}: MXFP8 weights with keep=True")
     inputs = [x, w1, s1, w2, s2, b1, b2, norm_w, norm_b]
-    _check_place(where, *inputs)
+    _check_place(where, stream, *inputs)
     made = []
     with mx._on_stream(stream, inputs, made):
         u8 = lambda *shape: torch.empty(shape, dtype=torch.uint8, device=x.device)
@@ -259,7 +267,7 @@ def dense_block_backward(dout, kept, w1t, s1t, w2t, s2t, fmt_grad=mx.MXFP8_E4M3,
     x, norm_w, mean, rstd, yt, syt, z, sz, act, fmt = kept
     norm = _check_params(where, [("kept.norm_w", norm_w, K)])
     inputs = [dout, w1t, s1t, w2t, s2t, *kept[:8]]
-    _check_place(where, *inputs)
+    _check_place(where, stream, *inputs)
     made = []
     with mx._on_stream(stream, inputs, made):
         u8 = lambda *shape: torch.empty(shape, dtype=torch.uint8, device=x.device)

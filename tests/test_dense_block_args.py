@@ -203,3 +203,32 @@ def test_eps():
     assert refusal(mx.dense_block, forward_args(), eps=0)[1] == "dense_block: " + HERE
     for bad in (-1e-9, float("nan")):
         assert refusal(mx.dense_block, forward_args(), eps=bad) == (ValueError, "dense_block: eps of at least 0 expected")
+
+
+def test_another_device_than_the_launches(monkeypatch):
+    """Pointers to one GPU's memory are no other's to read.  No GPU: devices by name."""
+    from types import SimpleNamespace
+
+    from block_scaled_mxfp4_gb300 import dense
+
+    class Stream:
+        def __init__(self, index, handle):
+            self.device, self.cuda_stream = torch.device("cuda", index), handle
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream(0, 0))
+    on = [SimpleNamespace(is_cuda=True, device=torch.device("cuda", i)) for i in (0, 1)]
+
+    def refused(stream, *tensors):
+        try:
+            dense._check_place("here", stream, *tensors)
+        except ValueError as e:
+            return str(e)
+
+    assert refused(None, on[0], on[0], None) is None and refused(77, on[0]) is None
+    assert refused(Stream(0, 5), on[0]) is None and refused(Stream(1, 5), on[1], on[1]) is None
+    assert refused(None, on[0], on[1]) == "here: " + HERE
+    # (a default stream's handle is the same on every device: nothing switches to its device)
+    for stream, tensor in ((None, 1), (77, 1), (Stream(0, 5), 1), (Stream(1, 5), 0), (Stream(1, 0), 1)):
+        assert "device of the current stream" in refused(stream, on[tensor])
