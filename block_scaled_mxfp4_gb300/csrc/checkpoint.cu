@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(Tile<false>::kThreads, Tile<false>::kResident)
 // shared memory too and leave it as whole boxes by TMA: stored by the lanes, each 32-byte
 // sector took the L1's data stage most of a cycle, a third of all its work.
 //
-// 8192 x 16384 with GELU, all outputs but dz itself: 205 us, 4.0 TB/s, of 121 that its
-// bytes need; 187 with SiLU, 185 with none.  (Computing along the rows 245, with the
+// 8192 x 16384 with GELU, all outputs but dz itself: 207 us, 4.0 TB/s, of 121 that its
+// bytes need; 191 with its tanh form, 190 with SiLU, 188 with none.  (Computing along the rows 245, with the
 // lanes' own stores 239 of then 233, in blocks of 256 threads and tiles of 128 rows, whose
 // passes overlap less, 233.)  What bounds it is issue: 41 instructions per value, 14 of
 // them GELU's, on 16 warps an SM, which act(z) and dz of 32 values in registers allow.

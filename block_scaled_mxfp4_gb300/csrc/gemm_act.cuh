@@ -434,7 +434,8 @@ __device__ __forceinline__ void act_reduce_cluster(const ActGemmArgs &a, uint32_
         // Two passes: sums, a row's neighbouring pieces to neighbouring lanes, to this rank's own part
         // (only this thread reads that place); then a block's 32 columns to a warp's lanes.  Peers' memory
         // read in the second order, 16 bytes from each row, made the product of 64 x 8192 x 4096 MXFP8
-        // 17.4 us, of 16 rows 11.5; so they take 14.7 and 11.1, the plain products 14.6 and 10.5.
+        // 17.4 us, of 16 rows 11.5; so they take 14.7 and 10.8, the plain products 14.7 and 10.3 (15.8 and
+        // 11.1 with bias and GELU).
         const int items = max(0, min(r1, a.N - p0) - r0) * nch;
 #pragma unroll 1
         for (int it = t; it < items; it += kGemmThreadsC) {

@@ -1,4 +1,4 @@
-// Launch helpers of the expert-layer kernels.
+// Launch helpers of the expert-layer and dense-layer kernels.
 #pragma once
 
 #include <atomic>

@@ -1,7 +1,8 @@
 // Block scaling and rounding of 1x32 blocks: the rules of mxfp4_quantize and
-// mxfp8_quantize (quantize.cu).  The expert-layer kernels round whole blocks with
-// quantize_block; there, beyond those rules, a block that holds an infinity or a
-// NaN gets the scale code 0xFF (NaN), so that the rows computed from it show it.
+// mxfp8_quantize (quantize.cu).  The expert-layer and dense-layer kernels round whole
+// blocks with quantize_block and quantize_block_pairs; there, beyond those rules, a block
+// that holds an infinity or a NaN gets the scale code 0xFF (NaN), so that the rows
+// computed from it show it.
 #pragma once
 
 #include <cstdint>

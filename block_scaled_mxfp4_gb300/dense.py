@@ -155,10 +155,12 @@ def dense_block(x, w1, s1, w2, s2, b1=None, b2=None, norm_w=None, norm_b=None, a
 
     x bf16 [T, K].  MXFP4: w1 uint8 [F, K / 2], w2 uint8 [K, F / 2] as
     mxfp4_quantize writes them; MXFP8 (codes of `fmt`): w1 [F, K], w2 [K, F] as in
-    mxfp8_forms; s1 [F, K / 32], s2 [K, F / 32] either way, K and F multiples of 32, K up to 32768.
+    mxfp8_forms; s1 [F, K / 32], s2 [K, F / 32] either way, K and F multiples of 32,
+    K up to 32768.
     Codes and scales are bytes, or of torch's own types for them (float8_e4m3fn for
     MXFP8_E4M3 and so on; another format's are refused).
-    What the products read is quantised in the weights' form.  b1 [F] and b2 [K],
+    What the products read is quantised in the weights' form: the normed rows, which the
+    norm rounds to bf16 first, and h, from fp32.  b1 [F] and b2 [K],
     norm_w and norm_b [K]: bf16 or fp32, each pair of one type, None for none.
 
     Returns out bf16 [T, K], or with keep=True (MXFP8 weights) (out, DenseKept).
@@ -235,7 +237,8 @@ def dense_block_backward(dout, kept, w1t, s1t, w2t, s2t, fmt_grad=mx.MXFP8_E4M3,
     [F, K], s2t [F, K / 32]: the weights' transposed forms (qt, st of mxfp8_forms), in
     the forward pass's format.  Gradients are products' operands in `fmt_grad`.  The
     gradients are those of the arithmetic that ran: from z as it was kept, with every
-    rounding's slope taken as one.
+    rounding's slope taken as one.  dh and the gradient behind the norm pass through
+    bf16; dz and h are rounded to their forms from fp32.
     """
     import torch
     where = "dense_block_backward"

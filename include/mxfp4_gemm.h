@@ -632,7 +632,9 @@ size_t mxfp4_moe_ffn_workspace_size(int T, int E, int k, int K, int F);
  * may one of SiLU or of GELU's tanh form whose sigmoid is under 2^-125: a value of up to
  * |z| 2^-125 (SiLU of -88 is -5.3e-37, and -0 here).
  * In a product's epilogue z = infinity gives infinity, and minus infinity 0 (ReLU, GELU)
- * or NaN (its tanh form, SiLU).
+ * or NaN (its tanh form, SiLU).  In the backward pass a z beyond fp32 (an infinity of E5M2, or a
+ * code times its scale of 2^128 or more, none of which this library writes) has the slope NaN
+ * with GELU, its tanh form and SiLU.
  * ------------------------------------------------------------------------ */
 
 enum { MXFP4_ACT_NONE = 0, MXFP4_ACT_RELU = 1, MXFP4_ACT_GELU = 2, MXFP4_ACT_GELU_TANH = 3, MXFP4_ACT_SILU = 4 };
@@ -661,7 +663,10 @@ int mxfp4_gemm_act(void *D, int64_t ldd, void *H, int64_t ldh, void *SH, int64_t
                    int fmt_z, float alpha, const void *bias, int bias_type, int act, const void *R,
                    int64_t ldr, float res_scale, int M, int N, int K, int split_k, unsigned flags,
                    void *workspace, size_t workspace_bytes, void *stream);
-/* The same on the byte formats and with the plan of mxfp8_gemm (mxfp8_gemm_workspace_size). */
+/* The same on the byte formats, in the workspace of mxfp8_gemm (mxfp8_gemm_workspace_size).  Its plan
+ * too (mxfp8_plan_gemm), but where split_k is 0, the plan relays the scales without swapping the
+ * operands, M and N are at least 256, and there is a tile of 256 x 256 for every two SMs: those calls
+ * run on CTA pairs, which mxfp8_gemm's never do and no plan shows.  D's bits are the same. */
 int mxfp8_gemm_act(void *D, int64_t ldd, void *H, int64_t ldh, void *SH, int64_t ld_sh, void *Z,
                    int64_t ldz, void *SZ, int64_t ld_sz, const void *A, int64_t lda, const void *B,
                    int64_t ldb, const void *scaleA, int64_t ld_sa, const void *scaleB, int64_t ld_sb,

@@ -142,3 +142,22 @@ def test_columns_behind_a_block_that_is_not_finite(act):
     assert (Q[:, cols:96] == 0).all()
     if act not in ("none", "relu"):
         assert ((S[:, :3] == 255) == (s == 255)).all()
+
+
+@pytest.mark.parametrize("act", dr.ACTS)
+def test_slopes_of_infinite_z(act):
+    rows, cols = 32, 64
+    codes, s = np.full((rows, cols), 0x3C, np.uint8), np.full((rows, 2), 127, np.uint8)      # ones
+    codes[3, 5], codes[7, 40] = 0x7C, 0xFC
+    codes[9, 32:] = 0x7B                                     # 57344 2^127
+    s[9, 1] = 254
+    dh, g = bf16(np.random.default_rng(10).normal(size=(rows, cols)))
+    dZ = host(run_backward(dh, dev(codes), dev(s), "e5m2", act, cols)[0])
+    odd = np.zeros((rows, cols), bool)
+    odd[3, 5] = odd[7, 40] = odd[9, 32:] = True
+    if act in ("none", "relu"):
+        want = g.copy()
+        want[7, 40] *= act == "none"
+        assert (dZ == want).all()
+    else:
+        assert (np.isnan(dZ) == odd).all()
